@@ -19,7 +19,8 @@ LIB_PATH = os.path.join(PKG, "libspecfold.so")
 HEADER = os.path.join(os.path.dirname(PKG), "include", "specfold.h")
 
 OK, EINVAL, EALIGN, ECAPACITY, EUNSUPPORTED, ECUDA, EDEVICE = 0, -1, -2, -3, -4, -5, -6
-DEV_TIMEOUT, DEV_BAD_PARENT, DEV_BAD_PAGE = 1, 2, 4
+DEV_TIMEOUT, DEV_BAD_PARENT, DEV_BAD_PAGE, DEV_BAD_SEQ = 1, 2, 4, 8
+MAX_SEQS, MAX_TREE, TREE_PAD = 1024, 256, -2
 DEV_SITE_SHIFT = 8  # with DEV_TIMEOUT: bit DEV_SITE_SHIFT + site names the wait that ran out
 DEV_SITES = ("attention loader: Q buffer free", "attention loader: K/V stage free", "attention softmax: S ready",
              "attention softmax: P V before a rescale", "attention softmax: P V before the last P",
@@ -63,6 +64,18 @@ class specfold_kv_view(ctypes.Structure):
                 ("block_table", ctypes.c_void_p), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32)]
 
 
+class specfold_head_rows(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64)]
+
+
+class specfold_paged_cache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+                ("k_token_stride", ctypes.c_int64), ("k_head_stride", ctypes.c_int64),
+                ("v_token_stride", ctypes.c_int64), ("v_head_stride", ctypes.c_int64),
+                ("block_table", ctypes.c_void_p), ("table_stride", ctypes.c_int64),
+                ("table_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32)]
+
+
 class specfold_ws_layout(ctypes.Structure):
     _fields_ = [(k, ctypes.c_size_t) for k in
                 ("status", "n_packed", "fold", "rel", "src", "packed_idx", "slot_of_row", "dep_rng", "dep_rows", "sync", "x1", "q",
@@ -90,6 +103,13 @@ _SIG = {
     "specfold_ffn": (_I, [_P, _P, _P, _P, _P, _P, _P, _P, _I, _I, _P, _P, ctypes.c_size_t, _P]),
     "specfold_layer_forward": (_I, [_P, _P, _P, _P, _I, _I, specfold_kv_view, specfold_kv_view, _I,
                                     ctypes.c_float, _P, _P, ctypes.c_size_t, _P, _P]),
+    "specfold_qk_norm_rope": (_I, [_I, _I, _I, _I, _I, specfold_head_rows, specfold_head_rows, specfold_head_rows,
+                                   specfold_head_rows, _P, _P, ctypes.c_float, _P, ctypes.c_float, _P]),
+    "specfold_kv_append": (_I, [_I, _I, _I, _I, specfold_head_rows, specfold_head_rows, _I, _P, _P, ctypes.c_float, _P,
+                                ctypes.c_float, _P, _P, _P, _I, _P, _P]),
+    "specfold_tree_attention": (_I, [_I, _I, _I, _I, _I, _I, specfold_head_rows, _P, _P, _P, _P, _I, ctypes.c_float,
+                                     specfold_head_rows, _P, ctypes.c_size_t, _P]),
+    "specfold_tree_attention_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
     "specfold_linear": (_I, [_I, _P, _P, _I, _I, _I, _P, _P, ctypes.c_size_t, _P]),
     "specfold_linear_noalloc": (_I, [_I, _P, _P, _I, _I, _I, _P, _P]),
     "specfold_workspace_size": (ctypes.c_size_t, [_P, _I, _I]),
@@ -294,6 +314,162 @@ def specfold_layer_forward(dims, weights, H_in, parent, prefK, prefV, P, tau, H_
     _check(lib().specfold_layer_forward(ctypes.byref(dims), ctypes.byref(weights), _ptr(H_in), _ptr(parent), B, L,
                                         kv_view(prefK), kv_view(prefV), P, float(tau), _ptr(H_out), _ptr(ws),
                                         ws.numel(), ev, _stream(stream)), "specfold_layer_forward")
+
+
+# ---- a decoder's paged cache ----
+
+class PagedCache:
+    """Page pools of a layer's keys and values and the sequences' block tables
+    (specfold_paged_cache).  `k_pool`, `v_pool`: [num_pages * page_size, n_kv,
+    hd] with unit last stride (slices of a fused pool and head-major pools
+    are fine); `block_table`: int32 [n_seqs, pages per sequence] on the same
+    device.  The tensors are kept; a table changed in place is seen by the
+    next call."""
+
+    def __init__(self, k_pool: torch.Tensor, v_pool: torch.Tensor, block_table: torch.Tensor, page_size: int):
+        if k_pool.dim() != 3 or k_pool.shape != v_pool.shape or k_pool.dtype != v_pool.dtype:
+            raise ValueError("k_pool and v_pool are [tokens, n_kv, hd] of one shape and dtype")
+        if k_pool.stride(2) != 1 or v_pool.stride(2) != 1:
+            raise ValueError("pools need unit last stride")
+        if page_size <= 0 or k_pool.shape[0] % page_size:
+            raise ValueError("the pool holds whole pages")
+        if block_table.dim() != 2 or block_table.dtype != torch.int32 or block_table.stride(1) != 1:
+            raise ValueError("block_table is int32 [n_seqs, pages] with unit last stride")
+        if not (k_pool.is_cuda and k_pool.device == v_pool.device == block_table.device):
+            raise ValueError("pools and table are on one CUDA device")
+        self.k_pool, self.v_pool, self.block_table, self.page_size = k_pool, v_pool, block_table, int(page_size)
+        self.n_seqs, self.n_kv, self.head_dim = block_table.shape[0], k_pool.shape[1], k_pool.shape[2]
+        self.dtype, self.device = k_pool.dtype, k_pool.device
+        self.struct = specfold_paged_cache(
+            k_pool.data_ptr(), v_pool.data_ptr(), k_pool.stride(0), k_pool.stride(1), v_pool.stride(0),
+            v_pool.stride(1), block_table.data_ptr(), block_table.stride(0), block_table.shape[1], self.page_size,
+            k_pool.shape[0] // self.page_size)
+        self.ref = ctypes.byref(self.struct)
+
+
+def _head_rows(t: torch.Tensor, heads: int, hd: int, like: torch.Tensor, what: str) -> specfold_head_rows:
+    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != hd or t.stride(2) != 1:
+        raise ValueError(f"{what} must be [rows, {heads}, {hd}] with unit last stride")
+    if t.dtype != like.dtype or t.device != like.device:
+        raise ValueError(f"{what} must have the dtype and device of the other tensors")
+    return specfold_head_rows(t.data_ptr(), t.stride(0), t.stride(1))
+
+
+def _vec(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, like: torch.Tensor, what: str):
+    """Pointer of a contiguous vector of at least n entries (None: NULL)."""
+    if t is None:
+        return None
+    if t.dim() != 1 or t.dtype != dtype or t.device != like.device or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
+        raise ValueError(f"{what} must be a contiguous {dtype} vector of {n} entries on the same device")
+    return t.data_ptr()
+
+
+class _on_device:
+    """Makes the tensors' device current for a call (a no-op where it is)."""
+
+    def __init__(self, t: torch.Tensor):
+        if not t.is_cuda:
+            raise ValueError("the operators take CUDA tensors")
+        self.dev = t.device.index
+
+    def __enter__(self):
+        self.prev = torch.cuda.current_device()
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.dev)
+
+    def __exit__(self, *exc):
+        if self.prev != self.dev:
+            torch.cuda.set_device(self.prev)
+
+
+def specfold_qk_norm_rope(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], Q_out: Optional[torch.Tensor],
+                          K_out: Optional[torch.Tensor], gq: Optional[torch.Tensor] = None,
+                          gk: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                          positions: Optional[torch.Tensor] = None, rope_theta: float = 0.0, stream=None):
+    """Norm of every query and key head (gains gq, gk [hd]; None: not normed)
+    and the rotation by positions (int32 [T]; rope_theta 0: none).  Q, Q_out
+    [T, n_q, hd] and K, K_out [T, n_kv, hd], strided views allowed, an output
+    may be its input; Q or K may be None."""
+    like = Q if Q is not None else K
+    if like is None:
+        raise ValueError("Q or K must be given")
+    T, _, hd = like.shape
+    none = specfold_head_rows(None, 0, 0)
+    n_q = n_kv = 0
+    q = qo = k = ko = none
+    if Q is not None:
+        n_q = Q.shape[1]
+        q, qo = _head_rows(Q, n_q, hd, like, "Q"), _head_rows(Q_out, n_q, hd, like, "Q_out")
+    if K is not None:
+        n_kv = K.shape[1]
+        k, ko = _head_rows(K, n_kv, hd, like, "K"), _head_rows(K_out, n_kv, hd, like, "K_out")
+    for t in (Q, K, Q_out, K_out):
+        if t is not None and t.shape[0] != T:
+            raise ValueError("Q, K and their outputs have the same rows")
+    if rope_theta and positions is None:
+        raise ValueError("a rotation needs positions")
+    with _on_device(like):
+        _check(lib().specfold_qk_norm_rope(dtype_code(like.dtype), T, n_q, n_kv, hd, q, k, qo, ko,
+                                           _vec(gq, hd, like.dtype, like, "gq"), _vec(gk, hd, like.dtype, like, "gk"),
+                                           eps, _vec(positions, T, torch.int32, like, "positions"), rope_theta,
+                                           _stream(stream)), "specfold_qk_norm_rope")
+
+
+def specfold_kv_append(K: torch.Tensor, V: torch.Tensor, cache: PagedCache, row_start: torch.Tensor,
+                       ctx_len: torch.Tensor, gk: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                       positions: Optional[torch.Tensor] = None, rope_theta: float = 0.0,
+                       rows: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """Appends the batch's keys and values to the cache: row i of sequence s
+    (batch rows row_start[s] .. row_start[s+1]-1, int32 [n_seqs + 1]) becomes
+    token ctx_len[s] + i.  K, V [n_src, n_kv, hd]; `rows` (int32) picks their
+    rows, one per batch row; `positions` (int32, per batch row) defaults to
+    the tokens' own indices.  `status`: an optional int32/uint32 word for the
+    device status bits (read it with specfold_get_status)."""
+    n_seqs = ctx_len.shape[0]
+    T = K.shape[0] if rows is None else rows.shape[0]
+    if V.shape[0] != K.shape[0] or n_seqs > cache.n_seqs:
+        raise ValueError("K and V have the same rows, the cache a table for every sequence")
+    if status is not None and (status.element_size() != 4 or status.device != K.device):
+        raise ValueError("status is one 32-bit word on the same device")
+    k = _head_rows(K, cache.n_kv, cache.head_dim, cache.k_pool, "K")
+    v = _head_rows(V, cache.n_kv, cache.head_dim, cache.k_pool, "V")
+    with _on_device(K):
+        _check(lib().specfold_kv_append(dtype_code(K.dtype), T, cache.n_kv, cache.head_dim, k, v, K.shape[0],
+                                        _vec(rows, T, torch.int32, K, "rows"),
+                                        _vec(gk, cache.head_dim, K.dtype, K, "gk"), eps,
+                                        _vec(positions, T, torch.int32, K, "positions"), rope_theta, cache.ref,
+                                        _vec(row_start, n_seqs + 1, torch.int32, K, "row_start"),
+                                        _vec(ctx_len, n_seqs, torch.int32, K, "ctx_len"), n_seqs,
+                                        None if status is None else status.data_ptr(), _stream(stream)),
+               "specfold_kv_append")
+
+
+def tree_attention_workspace_size(dtype: int, n_q: int, n_kv: int, hd: int, max_nodes: int) -> int:
+    return int(lib().specfold_tree_attention_workspace_size(dtype, n_q, n_kv, hd, max_nodes))
+
+
+def specfold_tree_attention(Q: torch.Tensor, cache: PagedCache, parent: Optional[torch.Tensor],
+                            row_start: torch.Tensor, ctx_len: torch.Tensor, max_nodes: int, O: torch.Tensor,
+                            ws: torch.Tensor, scale: float = 0.0, stream=None):
+    """Attention of the batch's rows over their sequence's cache and their own
+    ancestors (their keys and values already appended).  Q, O [T, n_q, hd];
+    parent int32 [T], the parent's index within its sequence, -1 for the last
+    cached token, TREE_PAD for a padding row, None for a chain; max_nodes: at
+    least every sequence's rows; ws: tree_attention_workspace_size bytes."""
+    T, n_q, hd = Q.shape
+    n_seqs = ctx_len.shape[0]
+    if hd != cache.head_dim or O.shape[0] != T or n_seqs > cache.n_seqs:
+        raise ValueError("Q and O have the same rows and the cache's head size, the cache a table for every sequence")
+    if ws.device != Q.device or ws.element_size() != 1 or ws.stride(0) != 1:
+        raise ValueError("ws is a byte workspace on the same device")
+    q = _head_rows(Q, n_q, hd, cache.k_pool, "Q")
+    o = _head_rows(O, n_q, hd, cache.k_pool, "O")
+    with _on_device(Q):
+        _check(lib().specfold_tree_attention(dtype_code(Q.dtype), T, max_nodes, n_q, cache.n_kv, hd, q, cache.ref,
+                                             _vec(parent, T, torch.int32, Q, "parent"),
+                                             _vec(row_start, n_seqs + 1, torch.int32, Q, "row_start"),
+                                             _vec(ctx_len, n_seqs, torch.int32, Q, "ctx_len"), n_seqs, scale, o,
+                                             ws.data_ptr(), ws.numel(), _stream(stream)), "specfold_tree_attention")
 
 
 def stack_workspace_size(dims: specfold_dims, B: int, L: int) -> int:

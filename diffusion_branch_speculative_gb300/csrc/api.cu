@@ -183,6 +183,46 @@ static int check_views(const specfold_kv_view& k, const specfold_kv_view& v, int
 
 
 
+// ---- a decoder's paged cache ----
+static bool stride8_ok(int64_t x) { return x > 0 && x % 8 == 0; }
+
+static int check_head_rows(const specfold_head_rows& v) {
+  if (!v.ptr || v.row_stride <= 0 || v.head_stride <= 0) return SPECFOLD_EINVAL;
+  if (!a16(v.ptr) || v.row_stride % 8 || v.head_stride % 8) return SPECFOLD_EALIGN;
+  return SPECFOLD_OK;
+}
+
+static int check_norm_rope(int dtype, int T, int hd, float eps, float theta) {
+  if (!dtype_ok(dtype) || T < 0) return SPECFOLD_EINVAL;
+  if (!(eps >= 0.f) || std::isinf(eps) || !(theta >= 0.f) || std::isinf(theta)) return SPECFOLD_EINVAL;
+  return hd == 64 || hd == 128 ? SPECFOLD_OK : SPECFOLD_EUNSUPPORTED;
+}
+
+static int check_paged_cache(const specfold_paged_cache* c) {
+  if (!c || !c->k || !c->v || !c->block_table) return SPECFOLD_EINVAL;
+  if (c->table_pages <= 0 || c->table_stride < 0 || c->page_size <= 0 || c->num_pages <= 0) return SPECFOLD_EINVAL;
+  if (c->k_token_stride <= 0 || c->k_head_stride <= 0 || c->v_token_stride <= 0 || c->v_head_stride <= 0)
+    return SPECFOLD_EINVAL;
+  if (!a16(c->k) || !a16(c->v) || !stride8_ok(c->k_token_stride) || !stride8_ok(c->k_head_stride) ||
+      !stride8_ok(c->v_token_stride) || !stride8_ok(c->v_head_stride))
+    return SPECFOLD_EALIGN;
+  if (c->page_size % 8) return SPECFOLD_EUNSUPPORTED;
+  if (static_cast<long long>(c->num_pages) * c->page_size > 0x7fffffffLL) return SPECFOLD_ECAPACITY;
+  return SPECFOLD_OK;
+}
+
+static int check_batch(const int32_t* row_start, const int32_t* ctx_len, int n_seqs) {
+  if (!row_start || !ctx_len || n_seqs < 1) return SPECFOLD_EINVAL;
+  return n_seqs <= SPECFOLD_MAX_SEQS ? SPECFOLD_OK : SPECFOLD_ECAPACITY;
+}
+
+static int check_tree_shape(int dtype, int n_q, int n_kv, int hd, int max_nodes) {
+  if (!dtype_ok(dtype) || n_q <= 0 || n_kv <= 0 || max_nodes <= 0) return SPECFOLD_EINVAL;
+  if (hd != 64 && hd != 128) return SPECFOLD_EUNSUPPORTED;
+  if (n_q % n_kv || n_q / n_kv > 128) return SPECFOLD_EUNSUPPORTED;
+  return max_nodes <= SPECFOLD_MAX_TREE ? SPECFOLD_OK : SPECFOLD_ECAPACITY;
+}
+
 // ------------------------------------------------------ workspace layout --
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -624,6 +664,68 @@ int specfold_workspace_layout(const specfold_dims* dims, int B, int L, specfold_
   SF_TRY(check_rows(B, L));
   layout(dims, B, L, out);
   return SPECFOLD_OK;
+}
+
+int specfold_qk_norm_rope(int dtype, int T, int n_q, int n_kv, int head_dim, specfold_head_rows q_in,
+                          specfold_head_rows k_in, specfold_head_rows q_out, specfold_head_rows k_out,
+                          const void* gq, const void* gk, float eps, const int32_t* positions, float rope_theta,
+                          void* stream) {
+  SF_TRY(check_norm_rope(dtype, T, head_dim, eps, rope_theta));
+  if (n_q < 0 || n_kv < 0) return SPECFOLD_EINVAL;
+  if (T == 0 || n_q + n_kv == 0) return SPECFOLD_OK;
+  if (rope_theta > 0.f && !positions) return SPECFOLD_EINVAL;
+  if (n_q > 0) {
+    SF_TRY(check_head_rows(q_in));
+    SF_TRY(check_head_rows(q_out));
+  }
+  if (n_kv > 0) {
+    SF_TRY(check_head_rows(k_in));
+    SF_TRY(check_head_rows(k_out));
+  }
+  QkNormRopeCall c{dtype, T, n_q, n_kv, head_dim, q_in, k_in, q_out, k_out, gq, gk, eps, positions, rope_theta};
+  return launch_qk_norm_rope(c, static_cast<cudaStream_t>(stream));
+}
+
+int specfold_kv_append(int dtype, int T, int n_kv, int head_dim, specfold_head_rows k, specfold_head_rows v, int n_src,
+                       const int32_t* rows, const void* gk, float eps, const int32_t* positions, float rope_theta,
+                       const specfold_paged_cache* cache, const int32_t* row_start, const int32_t* ctx_len, int n_seqs,
+                       uint32_t* status, void* stream) {
+  SF_TRY(check_norm_rope(dtype, T, head_dim, eps, rope_theta));
+  if (n_kv <= 0 || n_src < 0) return SPECFOLD_EINVAL;
+  SF_TRY(check_paged_cache(cache));
+  SF_TRY(check_batch(row_start, ctx_len, n_seqs));
+  if (!rows && n_src < T) return SPECFOLD_EINVAL;
+  if (T == 0) return SPECFOLD_OK;
+  if (n_src > 0) {
+    SF_TRY(check_head_rows(k));
+    SF_TRY(check_head_rows(v));
+  }
+  KvAppendCall c{dtype, n_kv, head_dim, k, v, n_src, rows, gk, eps, positions, rope_theta, *cache,
+                 {row_start, ctx_len, n_seqs, T}, status};
+  return launch_kv_append(c, static_cast<cudaStream_t>(stream));
+}
+
+size_t specfold_tree_attention_workspace_size(int dtype, int n_q, int n_kv, int head_dim, int max_nodes) {
+  if (check_tree_shape(dtype, n_q, n_kv, head_dim, max_nodes)) return 0;
+  return tree_attn_ws_bytes(dtype, n_q, n_kv, head_dim, max_nodes);
+}
+
+int specfold_tree_attention(int dtype, int T, int max_nodes, int n_q, int n_kv, int head_dim, specfold_head_rows q,
+                            const specfold_paged_cache* cache, const int32_t* parent, const int32_t* row_start,
+                            const int32_t* ctx_len, int n_seqs, float scale, specfold_head_rows o, void* ws,
+                            size_t ws_bytes, void* stream) {
+  SF_TRY(check_tree_shape(dtype, n_q, n_kv, head_dim, max_nodes));
+  if (T < 0 || !(scale >= 0.f) || std::isinf(scale)) return SPECFOLD_EINVAL;
+  SF_TRY(check_paged_cache(cache));
+  SF_TRY(check_batch(row_start, ctx_len, n_seqs));
+  if (!ws) return SPECFOLD_EINVAL;
+  if (!a16(ws)) return SPECFOLD_EALIGN;
+  if (ws_bytes < tree_attn_ws_bytes(dtype, n_q, n_kv, head_dim, max_nodes)) return SPECFOLD_ECAPACITY;
+  if (T == 0) return SPECFOLD_OK;
+  SF_TRY(check_head_rows(q));
+  SF_TRY(check_head_rows(o));
+  TreeAttnCall c{dtype, n_q, n_kv, head_dim, max_nodes, q, o, *cache, parent, {row_start, ctx_len, n_seqs, T}, scale, ws};
+  return launch_tree_attention(c, static_cast<cudaStream_t>(stream));
 }
 
 size_t specfold_linear_workspace_size(int M, int N) {

@@ -161,6 +161,53 @@ size_t attn_partial_bytes(int R, int g, int n_kv, int hd);
 int launch_attention(const AttnCall& c, cudaStream_t st);
 int launch_attention_f32(const AttnCall& c, cudaStream_t st);  // fp32 Q/K/V/O (simt_f32.cu)
 
+// ---- a decoder's paged cache (cache_ops.cu, tree_attn.cu) ----
+struct QkNormRopeCall {
+  int dtype, T, n_q, n_kv, hd;
+  specfold_head_rows q_in, k_in, q_out, k_out;
+  const void* gq;  // gains, null: not normed
+  const void* gk;
+  float eps;
+  const int32_t* positions;
+  float theta;  // 0: not rotated
+};
+int launch_qk_norm_rope(const QkNormRopeCall& c, cudaStream_t st);
+
+// Rows of a batch: sequence s owns rows row_start[s] .. row_start[s+1]-1,
+// behind ctx_len[s] cached tokens.
+struct SeqBatch {
+  const int32_t* row_start;
+  const int32_t* ctx_len;
+  int n_seqs;
+  int T;
+};
+struct KvAppendCall {
+  int dtype, n_kv, hd;
+  specfold_head_rows k, v;
+  int n_src;
+  const int32_t* rows;  // null: row t takes k and v row t
+  const void* gk;
+  float eps;
+  const int32_t* positions;  // null: the token's own index
+  float theta;
+  specfold_paged_cache cache;
+  SeqBatch batch;
+  uint32_t* status;  // may be null
+};
+int launch_kv_append(const KvAppendCall& c, cudaStream_t st);
+
+struct TreeAttnCall {
+  int dtype, n_q, n_kv, hd, max_nodes;
+  specfold_head_rows q, o;
+  specfold_paged_cache cache;
+  const int32_t* parent;  // null: a chain
+  SeqBatch batch;
+  float scale;
+  void* ws;  // tree_attn_ws_bytes
+};
+size_t tree_attn_ws_bytes(int dtype, int n_q, int n_kv, int hd, int max_nodes);
+int launch_tree_attention(const TreeAttnCall& c, cudaStream_t st);
+
 // ---- TMA descriptors (api.cu) ----
 // 2-D bf16 map over a row-major [rows, cols] matrix with a {64, box_rows}
 // box and 128-byte swizzle.

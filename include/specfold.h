@@ -70,7 +70,9 @@ extern "C" {
 /* ---- device status bits (specfold_get_status) ---- */
 #define SPECFOLD_DEV_TIMEOUT    1u  /* a bounded wait inside a kernel ran out; outputs invalid */
 #define SPECFOLD_DEV_BAD_PARENT 2u  /* parent[b] outside [0, b) for b > 0, or parent[0] != -1 */
-#define SPECFOLD_DEV_BAD_PAGE   4u  /* a paged prefix view's block table names a page outside the pool */
+#define SPECFOLD_DEV_BAD_PAGE   4u  /* a block table names a page outside the pool, or a token lies past
+                                       the table */
+#define SPECFOLD_DEV_BAD_SEQ    8u  /* a batch's row_start, ctx_len or rows entry is invalid (see specfold_kv_append) */
 /* With SPECFOLD_DEV_TIMEOUT, bit (SPECFOLD_DEV_SITE_SHIFT + site) names the
  * wait that ran out (the other waits of that kernel then give up without a
  * bit of their own), for a report:
@@ -88,6 +90,9 @@ extern "C" {
 #define SPECFOLD_DEV_SITE_SHIFT 8
 
 #define SPECFOLD_MAX_ROWS 16384     /* largest B*L */
+#define SPECFOLD_MAX_SEQS 1024      /* sequences of one batch (specfold_kv_append, specfold_tree_attention) */
+#define SPECFOLD_MAX_TREE 256       /* drafted rows of one sequence (specfold_tree_attention) */
+#define SPECFOLD_TREE_PAD -2        /* parent of a padding row (specfold_tree_attention) */
 
 typedef enum { SPECFOLD_BF16 = 0, SPECFOLD_F32 = 1 } specfold_dtype;
 
@@ -397,6 +402,126 @@ int specfold_stack_graph_create(const specfold_dims* dims, int n_layers, const s
                                 const specfold_kv_view* prefK, const specfold_kv_view* prefV, int P,
                                 float tau, void* H_out, const specfold_stack_trace* trace,
                                 void* ws, size_t ws_bytes, specfold_graph* graph);
+
+/* ---- a decoder's paged cache -------------------------------------- */
+/* Drafts of an autoregressive decoder: a batch of sequences, each with its
+ * own pages of one key/value cache and a tree of drafted tokens behind it.
+ * A step of a layer norms and rotates queries and keys
+ * (specfold_qk_norm_rope), writes the rows' keys and values into the cache
+ * (specfold_kv_append) and lets every drafted row attend to its sequence's
+ * cache and to its own ancestors (specfold_tree_attention).  The pages that
+ * this layer's sources leave open (how a cache comes to hold the prefix) are
+ * filled by these calls: specfold_attention reads one sequence's pages of
+ * the same pool through a paged specfold_kv_view. */
+
+/* Rows of heads: element (row t, head h, dim j) is
+ * ptr[t*row_stride + h*head_stride + j].  Any slice of a fused projection's
+ * output, or a head-major buffer, is such a view.  Strides are positive
+ * multiples of 8 elements, ptr 16-byte aligned. */
+typedef struct {
+  void* ptr;
+  int64_t row_stride;
+  int64_t head_stride;
+} specfold_head_rows;
+
+/* Page pools of a layer's keys and values and the sequences' block tables.
+ * Token t of sequence s is pool token
+ *   block_table[s*table_stride + t / page_size] * page_size + t % page_size,
+ * head h of pool token p at k[p*k_token_stride + h*k_head_stride].  Every row
+ * of the table has table_pages entries, so a sequence holds at most
+ * table_pages * page_size tokens; entries past its length are not read.
+ * page_size is a multiple of 8, num_pages * page_size < 2^31; strides are
+ * positive multiples of 8 elements. */
+typedef struct {
+  void* k;
+  void* v;
+  int64_t k_token_stride, k_head_stride;
+  int64_t v_token_stride, v_head_stride;
+  const int32_t* block_table;  /* device int32 */
+  int64_t table_stride;        /* entries from one sequence's table to the next */
+  int32_t table_pages;         /* entries of one sequence's table */
+  int32_t page_size;           /* tokens per page */
+  int32_t num_pages;           /* pages in the pool */
+} specfold_paged_cache;
+
+/* Norm of every query and key head and the rotation by the rows' positions,
+ * in one pass.  For row t and head h, x = in[t, h, :] in 32 bits:
+ *   y = x / sqrt(mean(x^2) + eps) * gain       (a NULL gain: y = x)
+ *   out[j]        = y[j] cos a_j - y[j + hd/2] sin a_j
+ *   out[j + hd/2] = y[j + hd/2] cos a_j + y[j] sin a_j
+ * with a_j = positions[t] * rope_theta^(-2j/hd) reduced exactly to one turn
+ * (rope_theta 0: no rotation, positions may be NULL), rounded once to dtype.
+ * gq and gk [head_dim] are the queries' and the keys' gains.
+ *   q_in, q_out [T, n_q, hd], k_in, k_out [T, n_kv, hd]; n_q or n_kv may be 0
+ * (that side's views are not read).  An output may be its input (the same
+ * pointer and strides), and may not overlap it in any other way.
+ * head_dim 64 or 128; eps >= 0; T >= 0. */
+int specfold_qk_norm_rope(int dtype, int T, int n_q, int n_kv, int head_dim, specfold_head_rows q_in,
+                          specfold_head_rows k_in, specfold_head_rows q_out, specfold_head_rows k_out,
+                          const void* gq, const void* gk, float eps, const int32_t* positions,
+                          float rope_theta, void* stream);
+
+/* Appends keys and values to a paged cache.  The batch: sequence s owns the
+ * rows row_start[s] .. row_start[s+1]-1 (device int32 [n_seqs + 1],
+ * ascending; a sequence may have none), and its cache holds ctx_len[s]
+ * tokens (device int32).  Its row i goes to the cache's token
+ * ctx_len[s] + i: the key normed with gk (NULL: not normed) and rotated to
+ * positions[t] (NULL: to the token's own index; rope_theta 0: not rotated)
+ * as in specfold_qk_norm_rope, the value as it is.
+ *   k, v     views of n_src rows of n_kv heads, 0 <= n_src
+ *   rows     device int32 [T] or NULL: the row of k and v that row t of the
+ *            batch takes (a step's accepted rows are committed this way:
+ *            appended again, at their final places).  NULL: row t itself,
+ *            n_src >= T.
+ *   status   device uint32 or NULL
+ * T is the capacity of the row lists (T >= row_start[n_seqs]); positions has
+ * T entries.  Nothing but the rows' own tokens is written; rows behind
+ * row_start[n_seqs] are not touched.  Two rows that name the same pool token
+ * (tables that share a page there) leave either one's values.  A page
+ * outside the pool or a token past the table drops the row and sets
+ * SPECFOLD_DEV_BAD_PAGE; a row_start entry that descends, is negative or
+ * above T, a negative ctx_len or a `rows` entry outside [0, n_src) drops that
+ * sequence's (that) row and sets SPECFOLD_DEV_BAD_SEQ.
+ * head_dim 64 or 128; n_seqs <= SPECFOLD_MAX_SEQS (SPECFOLD_ECAPACITY). */
+int specfold_kv_append(int dtype, int T, int n_kv, int head_dim, specfold_head_rows k, specfold_head_rows v,
+                       int n_src, const int32_t* rows, const void* gk, float eps, const int32_t* positions,
+                       float rope_theta, const specfold_paged_cache* cache, const int32_t* row_start,
+                       const int32_t* ctx_len, int n_seqs, uint32_t* status, void* stream);
+
+/* Attention of drafted rows over cache and tree.  The batch is
+ * specfold_kv_append's, its rows' keys and values already appended.  Row i of
+ * sequence s sees the cache's tokens 0 .. ctx_len[s]-1 and, of its own
+ * sequence's rows, itself and its ancestors (token ctx_len[s] + j for row j):
+ *   o[t, h] = softmax over visible tokens of (q[t, h] . k * scale), times v,
+ * key/value head h / (n_q / n_kv).  scale 0 means 1/sqrt(head_dim).
+ *   parent   device int32 [T], the parent's index within its sequence, less
+ *            than the row's own; -1: the last cached token.  NULL: every row
+ *            follows the one before it (one token, or a chunk of a prompt).
+ *            SPECFOLD_TREE_PAD: a padding row, which sees nothing and gets
+ *            zeros.  Any other value, or a padding row as parent, counts as
+ *            -1 and sets SPECFOLD_DEV_BAD_PARENT.
+ *   max_nodes  1 .. SPECFOLD_MAX_TREE, no less than any sequence's rows
+ *   q, o     views of T rows of n_q heads; o may be q
+ * Tokens that a row does not see change nothing in its output, whatever
+ * their pages hold (infinities and NaN included).  Rows of o that belong to
+ * no sequence stay as they were, as do those of a sequence whose row_start,
+ * ctx_len or row count is invalid (SPECFOLD_DEV_BAD_SEQ); a page outside the
+ * pool or a token past the table reads as zeros (SPECFOLD_DEV_BAD_PAGE).
+ * bf16 runs on the tensor cores: products of bf16 values summed in 32 bits,
+ * softmax in 32 bits, the probabilities rounded to bf16 for their product
+ * with the values.  fp32 keeps 32 bits throughout.
+ * head_dim 64 or 128; n_q / n_kv at most 128.  ws: workspace of
+ * specfold_tree_attention_workspace_size bytes, zero-filled once, its status
+ * word read with specfold_get_status.  It depends on the shape and on
+ * max_nodes only; calls that may overlap need one each. */
+int specfold_tree_attention(int dtype, int T, int max_nodes, int n_q, int n_kv, int head_dim,
+                            specfold_head_rows q, const specfold_paged_cache* cache, const int32_t* parent,
+                            const int32_t* row_start, const int32_t* ctx_len, int n_seqs, float scale,
+                            specfold_head_rows o, void* ws, size_t ws_bytes, void* stream);
+
+/* Workspace bytes of specfold_tree_attention (host only, no GPU needed).  0
+ * if the shape is invalid. */
+size_t specfold_tree_attention_workspace_size(int dtype, int n_q, int n_kv, int head_dim, int max_nodes);
 
 /* Enqueue one replay on `stream`. */
 int specfold_graph_launch(specfold_graph graph, void* stream);
