@@ -32,6 +32,47 @@ SF_DEV float merge_weight(float m, float M) { return m == M ? 1.f : ex2(m - M); 
 // The output of a row with sum l: zeros where nothing was seen.
 SF_DEV float merge_scale(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
+// The four warps' (o [RT][HD], {m, l} [RT]), `stride` bytes apart, into the
+// output of the current piece's rows, or into its partial slot.
+template <typename T, int HD, int RT>
+SF_DEV void merge_warps(const TreeArgs& p, const TreeWalk& w, bool first, const uint8_t* smem, int stride) {
+  const int h = w.head(), m0 = tree_m0(p, w), rows = tree_tile_rows(p, w);
+  const bool whole = w.whole();
+  const size_t ps = static_cast<size_t>(tree_slot(first)) * p.tile_rows;
+  const float* mw = reinterpret_cast<const float*>(smem);
+  const int ws = stride / 4;
+  for (int i = threadIdx.x; i < rows * (HD / 4); i += kThreads) {
+    const int r = i / (HD / 4), d = (i % (HD / 4)) * 4;
+    float M = -INFINITY, L = 0.f;
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) M = fmaxf(M, mw[k * ws + RT * HD + 2 * r]);
+    float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+    for (int k = 0; k < kWarps; ++k) {
+      const float wk = merge_weight(mw[k * ws + RT * HD + 2 * r], M);
+      const float4 v = load4(mw + k * ws + r * HD + d);
+      L = fmaf(wk, mw[k * ws + RT * HD + 2 * r + 1], L);
+      a.x = fmaf(wk, v.x, a.x);
+      a.y = fmaf(wk, v.y, a.y);
+      a.z = fmaf(wk, v.z, a.z);
+      a.w = fmaf(wk, v.w, a.w);
+    }
+    if (whole) {
+      const int m = m0 + r;
+      const float sc = merge_scale(L);
+      if (L == 0.f) a = make_float4(0.f, 0.f, 0.f, 0.f);
+      store4(static_cast<T*>(p.o) + (w.q.row0 + m / p.g) * p.o_rs + (h * p.g + m % p.g) * p.o_hs + d,
+             make_float4(a.x * sc, a.y * sc, a.z * sc, a.w * sc));
+    } else {
+      store4(p.part_o + (ps + r) * HD + d, a);
+      if (d == 0) {
+        p.part_ml[(ps + r) * 2] = M;
+        p.part_ml[(ps + r) * 2 + 1] = L;
+      }
+    }
+  }
+}
+
 // ------------------------------------------------------------ CUDA cores --
 // Tiles of RT rows (row m = node m / g, head m % g of the group).  Every warp
 // streams its own chunks of 16 keys through a private ring of asynchronous
@@ -78,7 +119,6 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const __grid_c
   float* s_q = reinterpret_cast<float*>(smem + C::OFF_Q);
   float* s_p = reinterpret_cast<float*>(smem + C::OFF_P) + warp * kChunk * RT;
   const T* qp = static_cast<const T*>(p.q);
-  T* op = static_cast<T*>(p.o);
 
   for (bool first = true; w.left > 0; first = false, w.next(p)) {
     const int h = w.head(), m0 = tree_m0(p, w), rows = tree_tile_rows(p, w);
@@ -239,40 +279,329 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const __grid_c
       }
     }
     __syncthreads();
-    const bool whole = w.whole();
-    const size_t ps = static_cast<size_t>(tree_slot(first)) * p.tile_rows;
-    constexpr int WSTEP = (C::RING > C::MERGE ? C::RING : C::MERGE) / 4;
-    const float* mw = reinterpret_cast<const float*>(smem);
-    for (int i = threadIdx.x; i < rows * (HD / 4); i += kThreads) {
-      const int r = i / (HD / 4), d = (i % (HD / 4)) * 4;
-      float M = -INFINITY, L = 0.f;
+    merge_warps<T, HD, RT>(p, w, first, smem, C::RING > C::MERGE ? C::RING : C::MERGE);
+  }
+}
+
+// ---------------------------------------------------- few rows, bf16: mma --
+// Up to RT = 16 MT rows of a head group (a whole sequence's nodes times the
+// group): decoding and small trees.  Such a unit does at most 32 operations a
+// byte of cache, so the memory bounds it and warp-level matrix instructions,
+// whose rows fit, are enough; what counts is bytes in flight and no barrier
+// between them.  So, as above, each of the four warps streams its own 16-key
+// chunks through a private ring of asynchronous copies:
+//   S [rows x 16 keys] = Q K^T, keys as the B operand straight from their rows;
+//   O [rows x HD] += P V, P from S's registers (rounded to bf16, the tensor
+//   cores' operand: off by half a step of each weight), V's rows transposed
+//   by the load.
+// 64 KB in flight an SM would cover the latency at full bandwidth; two CTAs of
+// 96 KB keep it covered while one of them merges.
+template <int HD, int MT>
+struct Few {
+  static constexpr int RT = 16 * MT;
+  static constexpr int STAGES = 3;
+  static constexpr int ROW = HD * 2;
+  static constexpr int CPR = ROW / 16;
+  static constexpr int STAGE = 2 * kChunk * ROW;
+  static constexpr int RING = STAGES * STAGE;
+  static constexpr int MERGE = RT * (HD + 2) * 4;
+  static_assert(MERGE <= RING, "the merge goes over the ring");
+  static constexpr int OFF_Q = kWarps * RING;
+  static constexpr int SMEM = OFF_Q + RT * ROW;
+  static constexpr int CTAS = HD == 128 ? 2 : 4;  // per SM
+  static constexpr bool Q_IN_REGS = MT == 1;      // two row tiles' queries would not fit beside their outputs
+};
+
+SF_DEV void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+SF_DEV void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
+  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+               : "r"(addr)
+               : "memory");
+}
+// c [16 x 8] += a [16 x 16] b [16 x 8], bf16 in, fp32 accumulate.
+SF_DEV void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+SF_DEV bool bf16_not_finite(uint32_t x) {  // either half
+  return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
+}
+
+template <int HD, int MT>
+__global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_kernel(const __grid_constant__ TreeArgs p) {
+  using C = Few<HD, MT>;
+  using T = __nv_bfloat16;
+  constexpr int RT = C::RT, KS = HD / 16;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ TreeLocate loc;
+  pdl_wait();
+  pdl_trigger();
+  TreeWalk w;
+  if (!tree_locate<kThreads>(p, loc, w)) {
+    if (threadIdx.x == 0) tree_describe_none(p);
+    return;
+  }
+  if (threadIdx.x == 0) tree_describe(p, w, loc.per, loc.lo);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* ring = smem + warp * C::RING;
+  uint8_t* s_q = smem + C::OFF_Q;
+  // a stored row's 16-byte piece c lies at c ^ (row & 7): the eight rows of a
+  // matrix load then never share a bank
+  auto q_addr = [&](int mt, int ks) {
+    const int r = mt * 16 + (lane & 15);
+    return smem_u32(s_q + r * C::ROW + (((ks * 2 + (lane >> 4)) ^ (r & 7)) << 4));
+  };
+
+  for (bool first = true; w.left > 0; first = false, w.next(p)) {
+    const int h = w.head(), rows = w.q.n * p.g;
+    const int len = w.q.ctx + w.q.n, key_lo = w.b0 * p.kb;
+    const int key_hi = min(static_cast<long long>(len), static_cast<long long>(w.b0 + w.blocks()) * p.kb);
+    __syncthreads();  // the previous piece's shared memory is free
+
+    // this warp's chunks: key_lo + 16 * (warp + 4 i)
+    const int chunks = (key_hi - key_lo + kChunk - 1) / kChunk;
+    const int mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
+    auto key_of = [&](int i) { return key_lo + kChunk * (warp + kWarps * i); };
+    auto slot_of = [&](int i) {  // lanes 0..15: pool tokens of chunk i's keys
+      const int tok = key_of(i) + (lane & (kChunk - 1));
+      return i < mine && tok < key_hi ? tree_pool_token(p, w.s, tok) : -1;
+    };
+    const T* kbase = static_cast<const T*>(p.cache.k) + h * p.cache.k_head_stride;
+    const T* vbase = static_cast<const T*>(p.cache.v) + h * p.cache.v_head_stride;
+    auto load = [&](int i, int slot) {
+      if (i < mine) {
+        const uint32_t st = smem_u32(ring + (i % C::STAGES) * C::STAGE);
+        constexpr int KEYS = 32 / C::CPR;  // keys of one step of the warp's lanes
+        const int c = lane % C::CPR;
 #pragma unroll
-      for (int k = 0; k < kWarps; ++k) M = fmaxf(M, mw[k * WSTEP + RT * HD + 2 * r]);
-      float4 a = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-      for (int k = 0; k < kWarps; ++k) {
-        const float wk = merge_weight(mw[k * WSTEP + RT * HD + 2 * r], M);
-        const float4 v = load4(mw + k * WSTEP + r * HD + d);
-        L = fmaf(wk, mw[k * WSTEP + RT * HD + 2 * r + 1], L);
-        a.x = fmaf(wk, v.x, a.x);
-        a.y = fmaf(wk, v.y, a.y);
-        a.z = fmaf(wk, v.z, a.z);
-        a.w = fmaf(wk, v.w, a.w);
+        for (int it = 0; it < kChunk / KEYS; ++it) {
+          const int key = it * KEYS + lane / C::CPR;
+          const int tk = __shfl_sync(0xffffffffu, slot, key);
+          const uint32_t n = tk < 0 ? 0u : 16u, at = st + key * C::ROW + ((c ^ (key & 7)) << 4);
+          const long long tz = tk < 0 ? 0 : tk;  // any valid address when nothing is read
+          cp_async16(at, kbase + tz * p.cache.k_token_stride + c * 8, n);
+          cp_async16(at + kChunk * C::ROW, vbase + tz * p.cache.v_token_stride + c * 8, n);
+        }
       }
-      if (whole) {
-        const int m = m0 + r;
-        const float sc = merge_scale(L);
-        if (L == 0.f) a = make_float4(0.f, 0.f, 0.f, 0.f);
-        store4(op + (w.q.row0 + m / p.g) * p.o_rs + (h * p.g + m % p.g) * p.o_hs + d,
-               make_float4(a.x * sc, a.y * sc, a.z * sc, a.w * sc));
-      } else {
-        store4(p.part_o + (ps + r) * HD + d, a);
-        if (d == 0) {
-          p.part_ml[(ps + r) * 2] = M;
-          p.part_ml[(ps + r) * 2 + 1] = L;
+      cp_async_commit();
+    };
+    int slot = slot_of(0);
+#pragma unroll
+    for (int i = 0; i < C::STAGES - 1; ++i) {
+      load(i, slot);
+      slot = slot_of(i + 1);
+    }
+
+    // queries: row m = node m / g, head m % g of the group
+    for (int i = threadIdx.x; i < RT * C::CPR; i += kThreads) {
+      const int r = i / C::CPR, c = i % C::CPR;
+      uint4 v = make_uint4(0u, 0u, 0u, 0u);
+      if (r < rows)
+        v = *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + (w.q.row0 + r / p.g) * p.q_rs +
+                                            (h * p.g + r % p.g) * p.q_hs + c * 8);
+      *reinterpret_cast<uint4*>(s_q + r * C::ROW + ((c ^ (r & 7)) << 4)) = v;
+    }
+    // ancestors: lane i has node i's, by doubling its jump towards the root
+    uint32_t sees = 0u;
+    {
+      const bool live = lane < w.q.n;
+      const int raw = !live ? SPECFOLD_TREE_PAD : p.parent ? p.parent[w.q.row0 + lane] : lane - 1;
+      int jump = raw;
+      const int up = __shfl_sync(0xffffffffu, raw, raw >= 0 ? raw & 31 : 0);
+      if (live && raw != SPECFOLD_TREE_PAD &&
+          (raw < -1 || raw >= lane || (raw >= 0 && up == SPECFOLD_TREE_PAD))) {
+        jump = -1;
+        if (warp == 0) atomicOr(p.status, SPECFOLD_DEV_BAD_PARENT);
+      }
+      if (raw != SPECFOLD_TREE_PAD) sees = 1u << lane;
+#pragma unroll
+      for (int k = 0; k < 5; ++k) {
+        const int from = max(jump, 0);
+        const uint32_t more = __shfl_sync(0xffffffffu, sees, from);
+        const int next = __shfl_sync(0xffffffffu, jump, from);
+        if (jump >= 0) {
+          sees |= more;
+          jump = next;
         }
       }
     }
+    uint32_t vis[MT][2];  // what this thread's rows see of the tree; 0: nothing at all
+#pragma unroll
+    for (int q = 0; q < 2 * MT; ++q) {
+      const int r = (q >> 1) * 16 + (q & 1) * 8 + (lane >> 2);
+      const uint32_t v = __shfl_sync(0xffffffffu, sees, r < rows ? r / p.g : 0);
+      vis[q >> 1][q & 1] = r < rows ? v : 0u;
+    }
+    __syncthreads();
+    uint32_t qf[C::Q_IN_REGS ? KS : 1][4];
+    if constexpr (C::Q_IN_REGS) {
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) ldsm4(q_addr(0, ks), qf[ks]);
+    }
+
+    float mx[MT][2], l[MT][2], o[MT][HD / 8][4];
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt) {
+      mx[mt][0] = mx[mt][1] = -INFINITY;
+      l[mt][0] = l[mt][1] = 0.f;
+#pragma unroll
+      for (int j = 0; j < HD / 8; ++j) o[mt][j][0] = o[mt][j][1] = o[mt][j][2] = o[mt][j][3] = 0.f;
+    }
+    for (int i = 0; i < mine; ++i) {
+      load(i + C::STAGES - 1, slot);
+      slot = slot_of(i + C::STAGES);
+      cp_async_wait<C::STAGES - 1>();
+      __syncwarp();
+      uint8_t* stg = ring + (i % C::STAGES) * C::STAGE;
+      uint8_t* sv = stg + kChunk * C::ROW;
+      float s[MT][2][4] = {};
+      {
+        const int key = (lane & 7) + ((lane >> 4) << 3);
+        const uint32_t base = smem_u32(stg + key * C::ROW);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t b[4];
+          ldsm4(base + (((ks * 2 + ((lane >> 3) & 1)) ^ (key & 7)) << 4), b);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            if constexpr (C::Q_IN_REGS) {
+              mma16816(s[mt][0], qf[ks], b[0], b[1]);
+              mma16816(s[mt][1], qf[ks], b[2], b[3]);
+            } else {
+              uint32_t a[4];
+              ldsm4(q_addr(mt, ks), a);
+              mma16816(s[mt][0], a, b[0], b[1]);
+              mma16816(s[mt][1], a, b[2], b[3]);
+            }
+          }
+        }
+      }
+      const int e0 = key_of(i) - w.q.ctx;
+      const bool tail = e0 + kChunk > 0;  // holds tokens that not every row sees
+      if (tail) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int x = 0; x < 8; ++x) {
+            const int e = e0 + (x >> 2) * 8 + (lane & 3) * 2 + (x & 1);
+            const bool see = e < 0 || (e < 32 && (vis[mt][(x >> 1) & 1] >> (e & 31) & 1u));
+            if (!see) s[mt][x >> 2][x & 3] = -INFINITY;
+          }
+      }
+      uint32_t pf[MT][4];
+      bool grew = false;
+      float alpha[MT][2];
+#pragma unroll
+      for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+        for (int hr = 0; hr < 2; ++hr) {
+          float m = fmaxf(fmaxf(s[mt][0][2 * hr], s[mt][0][2 * hr + 1]), fmaxf(s[mt][1][2 * hr], s[mt][1][2 * hr + 1]));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
+          m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
+          m = fmaxf(m * p.sl2, mx[mt][hr]);
+          const float base = m == -INFINITY ? 0.f : m;
+          alpha[mt][hr] = mx[mt][hr] == m ? 1.f : ex2(mx[mt][hr] - base);
+          grew = grew || mx[mt][hr] != m;
+          mx[mt][hr] = m;
+          float pr[4];
+#pragma unroll
+          for (int x = 0; x < 4; ++x) pr[x] = ex2(fmaf(s[mt][x >> 1][2 * hr + (x & 1)], p.sl2, -base));
+          l[mt][hr] = l[mt][hr] * alpha[mt][hr] + ((pr[0] + pr[1]) + (pr[2] + pr[3]));
+          pf[mt][hr] = pack_bf16x2(pr[0], pr[1]);
+          pf[mt][2 + hr] = pack_bf16x2(pr[2], pr[3]);
+        }
+      if (__any_sync(0xffffffffu, grew)) {
+#pragma unroll
+        for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+          for (int j = 0; j < HD / 8; ++j) {
+            o[mt][j][0] *= alpha[mt][0];
+            o[mt][j][1] *= alpha[mt][0];
+            o[mt][j][2] *= alpha[mt][1];
+            o[mt][j][3] *= alpha[mt][1];
+          }
+      }
+      if (tail) {
+        // a weight of zero does not silence an infinite value or a NaN in a
+        // product, so such values of the tree's rows are added by hand to the
+        // rows that see them and then taken out
+        bool odd = false;
+        for (int x = lane; x < kChunk * C::CPR; x += 32) {
+          const uint4 u = *reinterpret_cast<const uint4*>(sv + x * 16);
+          odd = odd || bf16_not_finite(u.x) || bf16_not_finite(u.y) || bf16_not_finite(u.z) || bf16_not_finite(u.w);
+        }
+        if (__any_sync(0xffffffffu, odd)) {
+          for (int k = 0; k < kChunk; ++k) {
+            const int e = e0 + k;
+#pragma unroll
+            for (int j = 0; j < HD / 8; ++j) {
+              const uint32_t u = *reinterpret_cast<const uint32_t*>(sv + k * C::ROW + ((j ^ (k & 7)) << 4) + (lane & 3) * 4);
+#pragma unroll
+              for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+                for (int x = 0; x < 4; ++x) {
+                  const bool see = e < 0 || (e < 32 && (vis[mt][x >> 1] >> (e & 31) & 1u));
+                  const float v = (x & 1) ? bf16hi(u) : bf16lo(u);
+                  if (see && !isfinite(v)) o[mt][j][x] += v;
+                }
+            }
+          }
+          __syncwarp();
+          for (int x = lane; x < kChunk * C::CPR * 8; x += 32) {
+            uint16_t* v = reinterpret_cast<uint16_t*>(sv) + x;
+            if ((*v & 0x7f80u) == 0x7f80u) *v = 0;
+          }
+          __syncwarp();
+        }
+      }
+      {
+        const int key = (lane & 7) + ((lane >> 3) & 1) * 8;
+        const uint32_t base = smem_u32(sv + key * C::ROW);
+#pragma unroll
+        for (int j = 0; j < HD / 16; ++j) {
+          uint32_t b[4];
+          ldsm4t(base + (((j * 2 + (lane >> 4)) ^ (key & 7)) << 4), b);
+#pragma unroll
+          for (int mt = 0; mt < MT; ++mt) {
+            mma16816(o[mt][2 * j], pf[mt], b[0], b[1]);
+            mma16816(o[mt][2 * j + 1], pf[mt], b[2], b[3]);
+          }
+        }
+      }
+      __syncwarp();  // the stage may be overwritten
+    }
+    cp_async_wait<0>();
+    __syncwarp();
+
+    float* mo = reinterpret_cast<float*>(ring);
+#pragma unroll
+    for (int mt = 0; mt < MT; ++mt)
+#pragma unroll
+      for (int hr = 0; hr < 2; ++hr) {
+        const int r = mt * 16 + hr * 8 + (lane >> 2);
+        const bool dead = vis[mt][hr] == 0u;
+        float ls = l[mt][hr];
+        ls += __shfl_xor_sync(0xffffffffu, ls, 1);
+        ls += __shfl_xor_sync(0xffffffffu, ls, 2);
+#pragma unroll
+        for (int j = 0; j < HD / 8; ++j)
+          *reinterpret_cast<float2*>(mo + r * HD + j * 8 + (lane & 3) * 2) =
+              dead ? make_float2(0.f, 0.f) : make_float2(o[mt][j][2 * hr], o[mt][j][2 * hr + 1]);
+        if ((lane & 3) == 0) {
+          mo[RT * HD + 2 * r] = dead ? -INFINITY : mx[mt][hr];
+          mo[RT * HD + 2 * r + 1] = dead ? 0.f : ls;
+        }
+      }
+    __syncthreads();
+    merge_warps<T, HD, RT>(p, w, first, smem, C::RING);
   }
 }
 
@@ -346,10 +675,19 @@ struct Plan {
 };
 
 Plan plan_of(int dtype, int g, int hd, int max_nodes) {
-  (void)dtype;
-  (void)hd;
-  (void)max_nodes;
+  const int rows = max_nodes * g;
+  if (dtype == SPECFOLD_BF16 && rows <= 32) {
+    const int rt = rows <= 16 ? 16 : 32;
+    return {hd == 128 ? Few<128, 1>::CTAS : Few<64, 1>::CTAS, g, rt, rt, 4 * kChunk};
+  }
   return {1, g, 8, 8, 4 * kChunk};
+}
+
+int tree_start(void (*kernel)(TreeArgs), int smem, const TreeArgs& a, int grid, cudaStream_t st) {
+  if (const int rc = smem_limit_once(kernel, smem)) return rc;
+  launch_k(kernel, dim3(grid), dim3(kThreads), smem, st, a);
+  count_launch();
+  return check_launch();
 }
 
 template <typename T, int HD>
@@ -380,11 +718,15 @@ int tree_go(const TreeAttnCall& c, const Plan& pl, cudaStream_t st) {
   a.part_ml = reinterpret_cast<float*>(a.desc + slots);
   a.part_o = a.part_ml + static_cast<size_t>(slots) * pl.tile_rows * 2;
   const int grid = std::min(num_sms(), kSmBudget) * pl.ctas_per_sm;
-  using C = Simt<T, HD>;
-  if (const int rc = smem_limit_once(tree_attn_simt_kernel<T, HD>, C::SMEM)) return rc;
-  launch_k(tree_attn_simt_kernel<T, HD>, dim3(grid), dim3(kThreads), C::SMEM, st, a);
-  count_launch();
-  if (const int rc = check_launch()) return rc;
+  int rc;
+  if constexpr (sizeof(T) == 2) {
+    rc = pl.tile_rows == 16   ? tree_start(tree_attn_few_kernel<HD, 1>, Few<HD, 1>::SMEM, a, grid, st)
+         : pl.tile_rows == 32 ? tree_start(tree_attn_few_kernel<HD, 2>, Few<HD, 2>::SMEM, a, grid, st)
+                              : tree_start(tree_attn_simt_kernel<T, HD>, Simt<T, HD>::SMEM, a, grid, st);
+  } else {
+    rc = tree_start(tree_attn_simt_kernel<T, HD>, Simt<T, HD>::SMEM, a, grid, st);
+  }
+  if (rc) return rc;
   if (grid == 1) return SPECFOLD_OK;
   launch_k(tree_combine_kernel<T, HD>, dim3(grid - 1, (pl.tile_rows + kCombineRows - 1) / kCombineRows),
            dim3(kCombineRows * 32), 0, st, a);
