@@ -1,6 +1,7 @@
 // Attention of drafted rows over a paged cache and their tree
-// (specfold_tree_attention): the kernel on the CUDA cores and the merge of
-// split units.  tree_sched.cuh has the decomposition.
+// (specfold_tree_attention): the fp32 kernel, the bf16 kernel for few rows a head
+// group, and the merge of split units.  tree_sched.cuh has the decomposition,
+// tree_attn_tc.cu the bf16 kernel for many rows.
 #include "tree_sched.cuh"
 
 #include <algorithm>
@@ -24,13 +25,6 @@ SF_DEV void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 SF_DEV void store4(__nv_bfloat16* p, float4 v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
 }
-
-// Weight of a partial with maximum m in a merge with maximum M: 1 where they
-// are equal, -inf included (a partial that saw nothing holds zeros, and one
-// whose scores are NaN keeps its NaN).
-SF_DEV float merge_weight(float m, float M) { return m == M ? 1.f : ex2(m - M); }
-// The output of a row with sum l: zeros where nothing was seen.
-SF_DEV float merge_scale(float l) { return l == 0.f ? 0.f : 1.f / l; }
 
 // The four warps' (o [RT][HD], {m, l} [RT]), `stride` bytes apart, into the
 // output of the current piece's rows, or into its partial slot.
@@ -73,7 +67,7 @@ SF_DEV void merge_warps(const TreeArgs& p, const TreeWalk& w, bool first, const 
   }
 }
 
-// ------------------------------------------------------------ CUDA cores --
+// ------------------------------------------------------ fp32: CUDA cores --
 // Tiles of RT rows (row m = node m / g, head m % g of the group).  Every warp
 // streams its own chunks of 16 keys through a private ring of asynchronous
 // copies, with its own running maximum and sum, so the loop has no block-wide
@@ -83,8 +77,9 @@ SF_DEV void merge_warps(const TreeArgs& p, const TreeWalk& w, bool first, const 
 //   output: lane = dimensions, the probabilities broadcast.
 // A chunk's 16-byte pieces are stored with their index xored with the row's low
 // three bits, so that eight rows read at one place never share a bank.
-template <typename T, int HD>
+template <int HD>
 struct Simt {
+  using T = float;
   static constexpr int RT = 8;
   static constexpr int STAGES = 2;
   static constexpr int ROW = HD * sizeof(T);        // bytes of a key
@@ -97,9 +92,10 @@ struct Simt {
   static constexpr int SMEM = OFF_P + kWarps * kChunk * RT * 4;
 };
 
-template <typename T, int HD>
+template <int HD>
 __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const __grid_constant__ TreeArgs p) {
-  using C = Simt<T, HD>;
+  using C = Simt<HD>;
+  using T = float;
   constexpr int RT = C::RT, DPL = HD / 32;  // dimensions of the output a lane holds
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ TreeLocate loc;
@@ -671,16 +667,17 @@ __global__ void __launch_bounds__(kCombineRows * 32) tree_combine_kernel(const _
 // --------------------------------------------------------------- launches --
 // A kernel's geometry: CTAs per SM, rows of a tile, keys of a block.
 struct Plan {
-  int ctas_per_sm, tile_mul, tile_per, tile_rows, kb;
+  int ctas_per_sm, tile_rows, kb;
 };
 
 Plan plan_of(int dtype, int g, int hd, int max_nodes) {
   const int rows = max_nodes * g;
-  if (dtype == SPECFOLD_BF16 && rows <= 32) {
+  if (dtype == SPECFOLD_BF16) {
+    if (rows > 32) return {1, kTreeTcRows, kTreeTcKeys};
     const int rt = rows <= 16 ? 16 : 32;
-    return {hd == 128 ? Few<128, 1>::CTAS : Few<64, 1>::CTAS, g, rt, rt, 4 * kChunk};
+    return {hd == 128 ? Few<128, 1>::CTAS : Few<64, 1>::CTAS, rt, 4 * kChunk};
   }
-  return {1, g, 8, 8, 4 * kChunk};
+  return {1, 8, 4 * kChunk};
 }
 
 int tree_start(void (*kernel)(TreeArgs), int smem, const TreeArgs& a, int grid, cudaStream_t st) {
@@ -706,8 +703,6 @@ int tree_go(const TreeAttnCall& c, const Plan& pl, cudaStream_t st) {
   a.max_nodes = c.max_nodes;
   a.n_kv = c.n_kv;
   a.g = c.n_q / c.n_kv;
-  a.tile_mul = pl.tile_mul;
-  a.tile_per = pl.tile_per;
   a.tile_rows = pl.tile_rows;
   a.kb = pl.kb;
   a.sl2 = static_cast<float>(1.4426950408889634 * (c.scale > 0.f ? c.scale : 1.0 / std::sqrt(static_cast<double>(HD))));
@@ -722,9 +717,9 @@ int tree_go(const TreeAttnCall& c, const Plan& pl, cudaStream_t st) {
   if constexpr (sizeof(T) == 2) {
     rc = pl.tile_rows == 16   ? tree_start(tree_attn_few_kernel<HD, 1>, Few<HD, 1>::SMEM, a, grid, st)
          : pl.tile_rows == 32 ? tree_start(tree_attn_few_kernel<HD, 2>, Few<HD, 2>::SMEM, a, grid, st)
-                              : tree_start(tree_attn_simt_kernel<T, HD>, Simt<T, HD>::SMEM, a, grid, st);
+                              : launch_tree_tc(a, HD, grid, st);
   } else {
-    rc = tree_start(tree_attn_simt_kernel<T, HD>, Simt<T, HD>::SMEM, a, grid, st);
+    rc = tree_start(tree_attn_simt_kernel<HD>, Simt<HD>::SMEM, a, grid, st);
   }
   if (rc) return rc;
   if (grid == 1) return SPECFOLD_OK;

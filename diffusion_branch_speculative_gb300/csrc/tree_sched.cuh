@@ -24,9 +24,8 @@ struct TreeArgs {
   const int32_t* parent;
   SeqBatch batch;
   int max_nodes, n_kv, g;
-  int tile_mul, tile_per;  // tiles of a sequence of n rows: ceil(n * tile_mul / tile_per)
-  int tile_rows;           // rows of a partial slot
-  int kb;                  // keys per block
+  int tile_rows;  // query rows of a tile: row m is node m / g, head m % g of the group
+  int kb;         // keys per block
   float sl2;               // scale * log2(e)
   uint32_t* status;
   int4* desc;              // [2 * grid]: the unit cut at CTA c's start, see tree_describe
@@ -42,6 +41,13 @@ struct TreeSeq {
   SF_DEV long long items(int n_kv) const { return static_cast<long long>(nb) * tiles * n_kv; }
 };
 
+// Weight of a partial with maximum m in a merge with maximum M: 1 where they
+// are equal, -inf included (a partial that saw nothing holds zeros, and one
+// whose scores are NaN keeps its NaN).
+SF_DEV float merge_weight(float m, float M) { return m == M ? 1.f : ex2(m - M); }
+// The factor of a row with sum l: zeros where nothing was seen.
+SF_DEV float merge_scale(float l) { return l == 0.f ? 0.f : 1.f / l; }
+
 SF_DEV TreeSeq tree_seq(const TreeArgs& p, int s) {
   TreeSeq q;
   q.row0 = p.batch.row_start[s];
@@ -51,7 +57,7 @@ SF_DEV TreeSeq tree_seq(const TreeArgs& p, int s) {
           q.ctx > 0x7fffffff - 2 * SPECFOLD_MAX_TREE;
   q.n = q.bad ? 0 : end - q.row0;
   q.nb = q.n > 0 ? (q.ctx + q.n - 1) / p.kb + 1 : 0;
-  q.tiles = (q.n * p.tile_mul + p.tile_per - 1) / p.tile_per;
+  q.tiles = (q.n * p.g + p.tile_rows - 1) / p.tile_rows;
   return q;
 }
 
@@ -156,14 +162,10 @@ SF_DEV bool tree_locate(const TreeArgs& p, TreeLocate& sh, TreeWalk& w) {
 // The partial slot of a run's piece.
 SF_DEV int tree_slot(bool first) { return 2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1); }
 
-// Rows of the current unit's tile: the first one m0 (row m is node m / g, head
-// m % g of the group) and how many.
-SF_DEV int tree_m0(const TreeArgs& p, const TreeWalk& w) {
-  return w.tile() * p.tile_per * (p.tile_mul == 1 ? p.g : 1);
-}
+// Rows of the current unit's tile: the first one and how many.
+SF_DEV int tree_m0(const TreeArgs& p, const TreeWalk& w) { return w.tile() * p.tile_rows; }
 SF_DEV int tree_tile_rows(const TreeArgs& p, const TreeWalk& w) {
-  const int m0 = tree_m0(p, w), most = p.tile_per * (p.tile_mul == 1 ? p.g : 1);
-  return min(most, w.q.n * p.g - m0);
+  return min(p.tile_rows, w.q.n * p.g - tree_m0(p, w));
 }
 
 // By one thread of every CTA: the unit that this CTA's start cuts, if this is
@@ -203,5 +205,11 @@ template <int N>
 SF_DEV void cp_async_wait() {
   asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
+
+// ---- host ----
+// Many rows a head group, bf16 (tree_attn_tc.cu): tiles of 128 rows, blocks of
+// 128 keys, one CTA per SM.
+constexpr int kTreeTcRows = 128, kTreeTcKeys = 128;
+int launch_tree_tc(const TreeArgs& a, int hd, int grid, cudaStream_t st);
 
 }  // namespace sf
