@@ -207,9 +207,9 @@ SF_DEV void cp_async_wait() {
 }
 
 // ---- host ----
-// Many rows a head group, bf16 (tree_attn_tc.cu): tiles of 128 rows, blocks of
+// Many rows a head group, bf16 (tree_attn_tc.cu): tiles of 256 rows, blocks of
 // 128 keys, one CTA per SM.
-constexpr int kTreeTcRows = 128, kTreeTcKeys = 128;
+constexpr int kTreeTcRows = 256, kTreeTcKeys = 128;
 int launch_tree_tc(const TreeArgs& a, int hd, int grid, cudaStream_t st);
 
 }  // namespace sf
