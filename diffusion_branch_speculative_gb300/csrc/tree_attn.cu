@@ -98,18 +98,16 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const __grid_c
   using T = float;
   constexpr int RT = C::RT, DPL = HD / 32;  // dimensions of the output a lane holds
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ TreeLocate loc;
   __shared__ int16_t s_parent[SPECFOLD_MAX_TREE];
   __shared__ uint32_t s_sees[RT][SPECFOLD_MAX_TREE / 32];  // a tile row's ancestors and itself
   __shared__ int s_dead[RT];                               // padding rows
   pdl_wait();
   pdl_trigger();
   TreeWalk w;
-  if (!tree_locate<kThreads>(p, loc, w)) {
-    if (threadIdx.x == 0) tree_describe_none(p);
-    return;
-  }
-  if (threadIdx.x == 0) tree_describe(p, w, loc.per, loc.lo);
+  long long lo, per;
+  const bool work = tree_locate(p, w, lo, per);
+  if (threadIdx.x == 0) tree_describe(p, w, work, lo, per);
+  if (!work) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = smem + warp * (C::RING > C::MERGE ? C::RING : C::MERGE);
   float* s_q = reinterpret_cast<float*>(smem + C::OFF_Q);
@@ -337,15 +335,13 @@ __global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_ker
   using T = __nv_bfloat16;
   constexpr int RT = C::RT, KS = HD / 16;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ TreeLocate loc;
   pdl_wait();
   pdl_trigger();
   TreeWalk w;
-  if (!tree_locate<kThreads>(p, loc, w)) {
-    if (threadIdx.x == 0) tree_describe_none(p);
-    return;
-  }
-  if (threadIdx.x == 0) tree_describe(p, w, loc.per, loc.lo);
+  long long lo, per;
+  const bool work = tree_locate(p, w, lo, per);
+  if (threadIdx.x == 0) tree_describe(p, w, work, lo, per);
+  if (!work) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = smem + warp * C::RING;
   uint8_t* s_q = smem + C::OFF_Q;
@@ -664,6 +660,46 @@ __global__ void __launch_bounds__(kCombineRows * 32) tree_combine_kernel(const _
   }
 }
 
+// The same for partials stored [quad of columns][row]: a warp has 32 rows and
+// one quad, so that every load is 512 bytes side by side; block (c, rows, quads).
+constexpr int kCombineQuads = 8;
+
+template <int HD>
+__global__ void __launch_bounds__(kCombineQuads * 32) tree_combine_quads_kernel(const __grid_constant__ TreeArgs p) {
+  pdl_wait();
+  pdl_trigger();
+  const int c = blockIdx.x + 1;
+  const int4 a = p.desc[2 * c], b = p.desc[2 * c + 1];
+  const int lane = threadIdx.x & 31;
+  if (static_cast<int>(blockIdx.y) * 32 >= a.x) return;
+  const int r = min(static_cast<int>(blockIdx.y) * 32 + lane, a.x - 1);
+  const int quad = blockIdx.z * kCombineQuads + (threadIdx.x >> 5);
+  const int n = b.y - b.x + 1;
+  auto slot = [&](int z) { return static_cast<size_t>(z == 0 ? b.z : 2 * (b.x + z)) * p.tile_rows; };
+  float M = -INFINITY;
+#pragma unroll 8
+  for (int z = 0; z < n; ++z) M = fmaxf(M, p.part_ml[(slot(z) + r) * 2]);
+  float L = 0.f;
+  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 8
+  for (int z = 0; z < n; ++z) {
+    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot(z) + r) * 2);
+    const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(z) * HD + (quad * p.tile_rows + r) * 4);
+    const float wz = merge_weight(ml.x, M);
+    L = fmaf(wz, ml.y, L);
+    acc.x = fmaf(wz, v.x, acc.x);
+    acc.y = fmaf(wz, v.y, acc.y);
+    acc.z = fmaf(wz, v.z, acc.z);
+    acc.w = fmaf(wz, v.w, acc.w);
+  }
+  if (static_cast<int>(blockIdx.y) * 32 + lane >= a.x) return;
+  const float sc = merge_scale(L);
+  if (L == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+  const int m = a.z + r;
+  store4(static_cast<__nv_bfloat16*>(p.o) + (a.y + m / p.g) * p.o_rs + (a.w * p.g + m % p.g) * p.o_hs + quad * 4,
+         make_float4(acc.x * sc, acc.y * sc, acc.z * sc, acc.w * sc));
+}
+
 // --------------------------------------------------------------- launches --
 // A kernel's geometry: CTAs per SM, rows of a tile, keys of a block.
 struct Plan {
@@ -723,8 +759,12 @@ int tree_go(const TreeAttnCall& c, const Plan& pl, cudaStream_t st) {
   }
   if (rc) return rc;
   if (grid == 1) return SPECFOLD_OK;
-  launch_k(tree_combine_kernel<T, HD>, dim3(grid - 1, (pl.tile_rows + kCombineRows - 1) / kCombineRows),
-           dim3(kCombineRows * 32), 0, st, a);
+  if (sizeof(T) == 2 && pl.tile_rows == kTreeTcRows)
+    launch_k(tree_combine_quads_kernel<HD>, dim3(grid - 1, kTreeTcRows / 32, HD / 4 / kCombineQuads),
+             dim3(kCombineQuads * 32), 0, st, a);
+  else
+    launch_k(tree_combine_kernel<T, HD>, dim3(grid - 1, (pl.tile_rows + kCombineRows - 1) / kCombineRows),
+             dim3(kCombineRows * 32), 0, st, a);
   count_launch();
   return check_launch();
 }

@@ -16,15 +16,17 @@
 // a block and pair of lanes (a lane's P through shared memory and half-width
 // products took 1.35 us a block and lane, above the memory's own time).
 //
-// Roles (384 threads): warps 0-1 load, warps 2 and 3 issue lane 0's and lane 1's
-// products (warp 3 owns the TMEM allocation), warps 4-7 and 8-11 are the lanes'
-// softmax.  K and V tiles go through one ring, K then V of every block, each
-// released by both lanes.  Blocks of cached tokens alone come by TMA, one box
-// per run of tokens inside a page (page_size's power of two, 8 to 64), the boxes
-// issued by the loaders' threads side by side; blocks that hold the tree's
-// tokens, or end the sequence, are gathered row by row, zero-filled past the
-// end.  Which of them a row sees is 64 bits at a time, found by walking up its
-// ancestors when such a block is met.
+// Roles (384 threads): warps 0-1 load, warp 2 issues all products, warp 3 owns
+// the TMEM allocation, warps 4-7 and 8-11 are the lanes' softmax.  One issuer, so
+// that a lane's P V and next Q K^T run in one go and the lanes fall into
+// alternation (an issuer per lane interleaved their products: both lanes' S came
+// at once and the tensor cores idled through both softmaxes, 5050 cycles a block
+// against 2900).  K and V tiles go through one ring in the order of their use.
+// They come by TMA, one box per run of tokens inside a page (page_size's power
+// of two, 8 to 64), the boxes issued by the loaders' threads side by side; boxes
+// past the sequence read zeros, and a block that holds the tree's tokens, or
+// ends the sequence, has its values mended before they are handed on.  Which of
+// its tokens a row sees is 64 bits at a time, found by walking up its ancestors.
 #include "tree_sched.cuh"
 
 namespace sf {
@@ -74,6 +76,29 @@ SF_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
       : "memory");
 }
 
+// Pairs of 32-bit operations in one instruction, and the maximum of three.
+SF_DEV float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y, z;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+      "fma.rn.f32x2 x, x, y, z;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+SF_DEV float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 x, y;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+      "add.rn.f32x2 x, x, y;\n\tmov.b64 {%0, %1}, x;\n\t}\n"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+SF_DEV float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
+  return d;
+}
+
 // The ancestors (and itself) of node i among nodes [e0, e0 + 64), as bits, for
 // a node that is no padding row.  par: the sequence's parents, null: a chain.
 SF_DEV uint64_t sees_window(const int32_t* par, int i, int e0, uint32_t* status) {
@@ -104,60 +129,65 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
   const TreeArgs& p = ta.t;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) uint64_t bars[2 * C::RING + 11];
+  __shared__ __align__(8) uint64_t bars[2 * C::RING + 11];  // 10 more barriers behind the ring's
   __shared__ uint32_t tmem_slot_s;
   __shared__ volatile int abort_s;
   __shared__ volatile int okflag[C::RING];
   __shared__ volatile int okq;
   __shared__ float2 xch[128];
-  __shared__ TreeLocate loc;
   // nodes whose values are not all finite, by unit (see the loaders)
   __shared__ uint32_t odd[kOddBufs][SPECFOLD_MAX_TREE / 32];
   uint64_t* full = bars;                // [RING]
-  uint64_t* empty = bars + C::RING;     // [RING]: one arrival per lane
+  uint64_t* empty = bars + C::RING;     // [RING]
   uint64_t* q_full = bars + 2 * C::RING;
   uint64_t* q_empty = q_full + 1;       // both lanes' S products of a unit are done: Q may be replaced
   uint64_t* s_full = q_full + 2;        // [lane]: one completion per block of the lane
   uint64_t* p_full = q_full + 4;        // [lane]
   uint64_t* o_full = q_full + 6;        // [lane]
   uint64_t* o_empty = q_full + 8;       // the softmax warps have read a unit's outputs
-  uint64_t* drain = q_full + 9;         // [lane]
+  uint64_t* landed = q_full + 9;        // a value tile that is mended before it is handed on
+  uint64_t* drain = q_full + 10;
   volatile int* abort_flag = &abort_s;
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  pdl_wait();
-  pdl_trigger();
-  TreeWalk w;
-  if (!tree_locate<kTcThreads>(p, loc, w)) {
-    if (threadIdx.x == 0) tree_describe_none(p);
-    return;
-  }
   if (threadIdx.x == 0) {
-    tree_describe(p, w, loc.per, loc.lo);
     mbar_init(smem_u32(q_full), 1);
-    mbar_init(smem_u32(q_empty), 2);
+    mbar_init(smem_u32(q_empty), 1);
     for (int i = 0; i < C::RING; ++i) {
       mbar_init(smem_u32(&full[i]), 1);
-      mbar_init(smem_u32(&empty[i]), 2);
+      mbar_init(smem_u32(&empty[i]), 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(smem_u32(&s_full[x]), 1);
-      mbar_init(smem_u32(&p_full[x]), 128);
+      mbar_init(smem_u32(&p_full[x]), 4);  // one arrival a warp: 128 would queue at the barrier's word
       mbar_init(smem_u32(&o_full[x]), 1);
-      mbar_init(smem_u32(&drain[x]), 1);
     }
-    mbar_init(smem_u32(o_empty), 256);
+    mbar_init(smem_u32(o_empty), 8);
+    mbar_init(smem_u32(landed), 1);
+    mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
     fence_mbar_init();
+    prefetch_tmap(&ta.mapK);
+    prefetch_tmap(&ta.mapV);
   }
   if (warp == 3) {
     tmem_alloc(smem_u32(&tmem_slot_s), C::TMEM_COLS);
     tmem_relinquish();
   }
+  pdl_wait();
+  pdl_trigger();
+  TreeWalk w;
+  long long lo, per;
+  const bool work = tree_locate(p, w, lo, per);
+  if (threadIdx.x == 0) tree_describe(p, w, work, lo, per);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot_s;
+  if (!work) {
+    if (warp == 3) tmem_dealloc(tmem, C::TMEM_COLS);
+    return;
+  }
   const int g = p.g;
 
   // Every role walks the same pieces in the same order; j counts them, it the
@@ -170,26 +200,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
   if (warp < 2) {
     // ------------------------------------------------------------ loaders --
     const int lt = threadIdx.x;
-    int it = 0, j = 0, issued = -1;
+    int it = 0, j = 0, issued = -1, fixes = 0;
     bool ok = true;
-    if (lt == 0) {
-      prefetch_tmap(&ta.mapK);
-      prefetch_tmap(&ta.mapV);
-    }
     const int boxes = kTreeTcKeys / ta.box;
     const int pool = p.cache.num_pages * p.cache.page_size;
     for (; w.left > 0 && ok; w.next(p), ++j) {
       const int h = w.head(), m0 = tree_m0(p, w), rows = tree_tile_rows(p, w), ctx = w.q.ctx, len = ctx + w.q.n;
       const int nt = w.blocks();
-      const bool pair = rows > 128;
-      // pool token of this lane's box of block b; read one block ahead of its use
-      auto box_token = [&](int b) {
-        const int tok = b * kTreeTcKeys + lane * ta.box;
-        if (lane >= boxes || b >= w.b0 + nt || (b + 1) * kTreeTcKeys > ctx) return 0;
-        const int at = tree_pool_token(p, w.s, tok);
-        return at < 0 ? pool : at;  // wholly past the pool: the box reads zeros
+      const int lead = rows > 128 ? 1 : 2;  // key tiles ahead of the first value tile
+      // this thread's box of a block: the table's entry is read a tile ahead of
+      // its use and looked at only then; kNoBox past the sequence
+      constexpr int kNoBox = -0x7fffffff;
+      auto box_page = [&](int t) {
+        const long long tok = static_cast<long long>(w.b0 + t) * kTreeTcKeys + lane * ta.box;
+        if (lane >= boxes || t >= nt || tok >= len) return kNoBox;
+        const unsigned pg = static_cast<unsigned>(tok) / static_cast<unsigned>(p.cache.page_size);
+        return pg < static_cast<unsigned>(p.cache.table_pages) ? p.cache.block_table[w.s * p.cache.table_stride + pg] : -1;
       };
-      int z = box_token(w.b0);
+      auto box_token = [&](int t, int page) {
+        if (page >= 0 && page < p.cache.num_pages)
+          return page * p.cache.page_size +
+                 static_cast<int>(static_cast<unsigned>((w.b0 + t) * kTreeTcKeys + lane * ta.box) %
+                                  static_cast<unsigned>(p.cache.page_size));
+        if (page != kNoBox) atomicOr(p.status, SPECFOLD_DEV_BAD_PAGE);
+        return pool;  // wholly past the pool: the box reads zeros
+      };
+      int zk = box_page(0), zv = zk;
       // the previous unit's S products must be done with the Q buffers
       if (lt == 0)
         okq = j == 0 || mbar_wait(smem_u32(q_empty), (j - 1) & 1, abort_flag, p.status, kWaitLimitNs, kSiteAttnQEmpty);
@@ -199,113 +235,101 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
         break;
       }
       if (lt < SPECFOLD_MAX_TREE / 32) odd[j % kOddBufs][lt] = 0u;
-      for (int r = lt; r < (pair ? 256 : 128); r += kLoaders) {
-        const int m = m0 + r;
-        const uint32_t n = r < rows ? 16u : 0u;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q);
-        if (r < rows) src += (w.q.row0 + m / g) * p.q_rs + (h * g + m % g) * p.q_hs;
-        uint8_t* dst = smem + (r >> 7) * C::Q_BYTES + (r & 127) * 128;
-#pragma unroll
-        for (int c = 0; c < HD / 8; ++c)
-          cp_async16(smem_u32(dst + (c >> 3) * kAtom + (((c & 7) ^ (r & 7)) << 4)), src + c * 8, n);
-      }
-      for (int t = 0; t < nt && ok; ++t) {
-        const int b = w.b0 + t;
-        const bool whole = (b + 1) * kTreeTcKeys <= ctx;  // cached tokens alone
-        constexpr int RPT = 128 / kLoaders;
-        int at[RPT];
-        if (!whole) {
-#pragma unroll
-          for (int q = 0; q < RPT; ++q) {
-            const int tok = b * kTreeTcKeys + lt + q * kLoaders;
-            at[q] = tok < len ? tree_pool_token(p, w.s, tok) : -1;
-          }
+      // the order of use: `lead` key tiles, then V of block t and K of t + lead
+      for (int i = 0; i < 2 * nt; ++i, ++it) {
+        const int heads_k = min(lead, nt), past = nt - heads_k;  // leading keys, and those behind them
+        const bool lead_k = i < heads_k, paired = !lead_k && i < heads_k + 2 * past;
+        const bool is_v = !lead_k && (!paired || (i - heads_k) % 2 == 0);
+        const int t = lead_k ? i : paired ? (i - heads_k) / 2 + (is_v ? 0 : lead) : i - nt;
+        const bool mend = is_v && static_cast<long long>(w.b0 + t + 1) * kTreeTcKeys > ctx;
+        const int st = it % C::RING;
+        const uint32_t fb = smem_u32(mend ? landed : &full[st]);
+        if (lt == 0) {
+          const bool free = mbar_wait(smem_u32(&empty[st]), ((it / C::RING) & 1) ^ 1, abort_flag, p.status,
+                                      kWaitLimitNs, kSiteAttnKvEmpty);
+          if (free) mbar_arrive_expect_tx(fb, C::TILE);
+          if (free && !mend) issued = it;
+          okflag[st] = free;
         }
-#pragma unroll
-        for (int is_v = 0; is_v < 2; ++is_v, ++it) {
-          const int st = it % C::RING;
-          const uint32_t fb = smem_u32(&full[st]);
-          if (lt == 0) {
-            const bool free = mbar_wait(smem_u32(&empty[st]), ((it / C::RING) & 1) ^ 1, abort_flag, p.status,
-                                        kWaitLimitNs, kSiteAttnKvEmpty);
-            if (free && whole) {
-              mbar_arrive_expect_tx(fb, C::TILE);
-              issued = it;
-            }
-            okflag[st] = free;
+        named_bar_sync(1, kLoaders);
+        if (!okflag[st]) {
+          ok = false;
+          break;
+        }
+        uint8_t* tile = smem + C::OFF_RING + st * C::TILE;
+        if (lane < boxes && warp < C::NATOM)
+          tma_load_3d(smem_u32(tile + warp * kAtom + lane * ta.box * 128), is_v ? &ta.mapV : &ta.mapK, fb, warp * 64, h,
+                      box_token(t, is_v ? zv : zk));
+        if (is_v)
+          zv = box_page(t + 1);
+        else
+          zk = box_page(t + 1);
+        if (i == 0) {  // the queries, behind the first keys' load
+          constexpr int RSTEP = kLoaders / (HD / 8);  // rows of one step; the row's node and head follow by steps
+          const int c = lt % (HD / 8), dn = RSTEP / g, dh = RSTEP % g;
+          int r = lt / (HD / 8), node = (m0 + r) / g, hd = (m0 + r) % g;
+          const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(p.q) + w.q.row0 * p.q_rs + h * g * p.q_hs + c * 8;
+          const uint32_t q0 = smem_u32(smem) + (c >> 3) * kAtom;
+          const int most = lead == 1 ? 256 : 128;
+#pragma unroll 4
+          for (; r < most; r += RSTEP) {
+            const bool there = r < rows;
+            cp_async16(q0 + (r >> 7) * C::Q_BYTES + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
+                       there ? qb + node * p.q_rs + hd * p.q_hs : qb, there ? 16u : 0u);
+            node += dn;
+            hd += dh;
+            if (hd >= g) hd -= g, ++node;
           }
+          cp_async_commit();
+          cp_async_wait<0>();
+          fence_proxy_async_smem();
           named_bar_sync(1, kLoaders);
-          if (!okflag[st]) {
-            ok = false;
-            break;
-          }
-          uint8_t* tile = smem + C::OFF_RING + st * C::TILE;
-          if (whole) {
-            if (lane < boxes && warp < C::NATOM)
-              tma_load_3d(smem_u32(tile + warp * kAtom + lane * ta.box * 128), is_v ? &ta.mapV : &ta.mapK, fb, warp * 64,
-                          h, z);
-          } else {
-            // gathered rows: 16-byte pieces straight to their swizzled places
-            const __nv_bfloat16* base =
-                is_v ? static_cast<const __nv_bfloat16*>(p.cache.v) + h * p.cache.v_head_stride
-                     : static_cast<const __nv_bfloat16*>(p.cache.k) + h * p.cache.k_head_stride;
-            const long long ts = is_v ? p.cache.v_token_stride : p.cache.k_token_stride;
-#pragma unroll
-            for (int q = 0; q < RPT; ++q) {
-              const int kr = lt + q * kLoaders;
-              const __nv_bfloat16* src = base + max(at[q], 0) * ts;  // any valid address when nothing is read
-#pragma unroll
-              for (int c = 0; c < HD / 8; ++c)
-                cp_async16(smem_u32(tile + (c >> 3) * kAtom + kr * 128 + (((c & 7) ^ (kr & 7)) << 4)), src + c * 8,
-                           at[q] < 0 ? 0u : 16u);
-            }
-            cp_async_commit();
-            cp_async_wait<0>();
-            // A weight of zero does not silence an infinite value or a NaN in
-            // a product: such values of the tree's tokens are taken out here,
-            // noted, and added at the end to the rows that see them.
-            if (is_v) {
-#pragma unroll
-              for (int q = 0; q < RPT; ++q) {
-                const int kr = lt + q * kLoaders, e = b * kTreeTcKeys + kr - ctx;
-                if (e < 0 || at[q] < 0) continue;
-                bool note = false;
-#pragma unroll
-                for (int c = 0; c < HD / 8; ++c) {
-                  uint4* v = reinterpret_cast<uint4*>(tile + (c >> 3) * kAtom + kr * 128 + (((c & 7) ^ (kr & 7)) << 4));
-                  const uint4 u = *v;
-                  uint32_t x[4] = {u.x, u.y, u.z, u.w};
-                  bool mine = false;
-#pragma unroll
-                  for (int k = 0; k < 4; ++k) {
-                    if ((x[k] & 0x7f80u) == 0x7f80u) x[k] &= 0xffff0000u, mine = true;
-                    if ((x[k] & 0x7f800000u) == 0x7f800000u) x[k] &= 0xffffu, mine = true;
-                  }
-                  if (mine) *v = make_uint4(x[0], x[1], x[2], x[3]);
-                  note = note || mine;
-                }
-                if (note) atomicOr(&odd[j % kOddBufs][e >> 5], 1u << (e & 31));
-              }
-            }
-            fence_proxy_async_smem();
-            named_bar_sync(1, kLoaders);
-            if (lt == 0) mbar_arrive(fb);
-          }
-          if (t == 0 && is_v == 0) {  // the queries, behind the first keys' loads
-            cp_async_commit();
-            cp_async_wait<0>();
-            fence_proxy_async_smem();
-            named_bar_sync(1, kLoaders);
-            if (lt == 0) mbar_arrive(smem_u32(q_full));
-          }
+          if (lt == 0) mbar_arrive(smem_u32(q_full));
         }
-        z = box_token(b + 1);
+        if (mend) {
+          // Tokens past the end may hold anything, and a weight of zero does not
+          // silence an infinite value or a NaN in a product: values past the
+          // end become zeros; such values of the tree's tokens are taken out,
+          // noted, and added at the end to the rows that see them.
+          const bool there = mbar_wait(smem_u32(landed), fixes & 1, abort_flag, p.status, kWaitLimitNs, kSiteAttnKvFull);
+          ++fixes;
+          const long long tok0 = static_cast<long long>(w.b0 + t) * kTreeTcKeys;
+          if (there) {
+#pragma unroll 1
+            for (int k = lt; k < 128 * (HD / 8); k += kLoaders) {
+              const int kr = k / (HD / 8), c = k % (HD / 8);
+              const int e = static_cast<int>(tok0 + kr - ctx);
+              if (e < 0) continue;
+              uint4* v = reinterpret_cast<uint4*>(tile + (c >> 3) * kAtom + kr * 128 + (((c & 7) ^ (kr & 7)) << 4));
+              const uint4 u = *v;
+              uint32_t y[4] = {u.x, u.y, u.z, u.w};
+              bool change = false;
+              if (e >= w.q.n) {
+                change = (u.x | u.y | u.z | u.w) != 0u;
+                y[0] = y[1] = y[2] = y[3] = 0u;
+              } else {
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                  if ((y[q] & 0x7f80u) == 0x7f80u) y[q] &= 0xffff0000u, change = true;
+                  if ((y[q] & 0x7f800000u) == 0x7f800000u) y[q] &= 0xffffu, change = true;
+                }
+                if (change) atomicOr(&odd[j % kOddBufs][e >> 5], 1u << (e & 31));
+              }
+              if (change) *v = make_uint4(y[0], y[1], y[2], y[3]);
+            }
+          }
+          fence_proxy_async_smem();
+          named_bar_sync(1, kLoaders);
+          if (lt == 0) mbar_arrive(smem_u32(&full[st]));
+        }
       }
     }
-    if (lt == 0 && *abort_flag && issued >= 0) {
+    if (lt == 0 && *abort_flag) {
       // let the copies already issued land before the CTA exits
       int never = 0;
-      mbar_wait(smem_u32(&full[issued % C::RING]), (issued / C::RING) & 1, &never, nullptr, 10000000ull);
+      if (issued >= 0)
+        mbar_wait(smem_u32(&full[issued % C::RING]), (issued / C::RING) & 1, &never, nullptr, 10000000ull);
+      if (fixes > 0) mbar_wait(smem_u32(landed), (fixes - 1) & 1, &never, nullptr, 10000000ull);
     }
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax --
@@ -370,15 +394,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
             for (int e = 0; e < 32; ++e)
               if (!((km[c >> 1] >> (32 * (c & 1) + e)) & 1u)) sv[c][e] = 0xff800000u;  // -inf
         }
-        float mx8[8];
-#pragma unroll
-        for (int q = 0; q < 8; ++q) mx8[q] = -INFINITY;
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
 #pragma unroll
         for (int c = 0; c < 4; ++c)
 #pragma unroll
-          for (int e = 0; e < 32; ++e) mx8[e & 7] = fmaxf(mx8[e & 7], __uint_as_float(sv[c][e]));
-        const float mx = fmaxf(fmaxf(fmaxf(mx8[0], mx8[1]), fmaxf(mx8[2], mx8[3])),
-                               fmaxf(fmaxf(mx8[4], mx8[5]), fmaxf(mx8[6], mx8[7])));
+          for (int e = 0; e < 32; e += 2)
+            mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
+        const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
         const float m_new = fmaxf(m_ref, mx * p.sl2);
         float alpha = 1.f;
         bool rescale = false;
@@ -403,23 +425,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
         }
         began = true;
         const float base = m_ref == -INFINITY ? 0.f : m_ref;
-        float ls[4] = {0.f, 0.f, 0.f, 0.f};
+        const float2 scale2 = make_float2(p.sl2, p.sl2), base2 = make_float2(-base, -base);
+        float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
 #pragma unroll
         for (int c = 0; c < 4; ++c) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
-            const float x0 = ex2(fmaf(__uint_as_float(sv[c][e]), p.sl2, -base));
-            const float x1 = ex2(fmaf(__uint_as_float(sv[c][e + 1]), p.sl2, -base));
-            ls[(e >> 1) & 3] += x0 + x1;
-            pk[e / 2] = pack_bf16x2(x0, x1);
+            float2 y = fma2(make_float2(__uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1])), scale2, base2);
+            y = make_float2(ex2(y.x), ex2(y.y));
+            ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], y);
+            pk[e / 2] = pack_bf16x2(y.x, y.y);
           }
           tmem_st16(tS + c * 16, pk);
         }
-        l += (ls[0] + ls[1]) + (ls[2] + ls[3]);
+        l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         tmem_st_wait();
         tc_fence_before();
-        mbar_arrive(smem_u32(&p_full[x]));
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&p_full[x]));
       }
       // this lane's last P V (a lane without blocks has none to wait for)
       const bool oku = ok && (!began || mbar_wait(smem_u32(&o_full[x]), (cnt - 1) & 1, abort_flag, p.status,
@@ -460,7 +484,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
       uint32_t any_odd = 0u;
 #pragma unroll
       for (int k = 0; k < SPECFOLD_MAX_TREE / 32; ++k) any_odd |= odd[j % kOddBufs][k];
-      const size_t pr = static_cast<size_t>(tree_slot(first)) * p.tile_rows + r;
+      const size_t ps = static_cast<size_t>(tree_slot(first)) * p.tile_rows;
       __nv_bfloat16* dst =
           static_cast<__nv_bfloat16*>(p.o) + (w.q.row0 + node) * p.o_rs + (h * g + m % g) * p.o_hs;
       // columns this thread writes: all of its lane's, or half of the shared rows'
@@ -510,91 +534,103 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
                            pack_bf16x2(o[8 * q8 + 4], o[8 * q8 + 5]), pack_bf16x2(o[8 * q8 + 6], o[8 * q8 + 7]));
         } else if (valid) {
 #pragma unroll
-          for (int q4 = 0; q4 < 8; ++q4)
-            reinterpret_cast<float4*>(p.part_o + pr * HD + c * 32)[q4] =
+          for (int q4 = 0; q4 < 8; ++q4)  // [quad of columns][row]: a warp's rows side by side
+            reinterpret_cast<float4*>(p.part_o + ps * HD)[(c * 8 + q4) * p.tile_rows + r] =
                 make_float4(o[4 * q4], o[4 * q4 + 1], o[4 * q4 + 2], o[4 * q4 + 3]);
         }
         __syncwarp();  // the next load of TMEM is the whole warp's
       }
       if (!whole && valid && (pair || x == 0)) {
-        p.part_ml[pr * 2] = dead ? -INFINITY : M;
-        p.part_ml[pr * 2 + 1] = dead ? 0.f : lrow;
+        p.part_ml[(ps + r) * 2] = dead ? -INFINITY : M;
+        p.part_ml[(ps + r) * 2 + 1] = dead ? 0.f : lrow;
       }
       // the accumulators are free for the next unit's first P V products
       tc_fence_before();
-      mbar_arrive(smem_u32(o_empty));
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(o_empty));
     }
-  } else {
+  } else if (warp == 2) {
     // ---------------------------------------------------------------- MMA --
-    const int x = warp - 2;
     if (lane == 0) {
       constexpr uint32_t idS = idesc_bf16_f32(128, 128, false);
       constexpr uint32_t idPV = idesc_bf16_f32(128, HD, true);
-      const uint32_t tS = tmem + x * 128, tO = tmem + C::COL_O + x * HD;
-      int it = 0, cnt = 0, j = 0;
+      int it = 0, j = 0;
+      int cnt[2] = {0, 0};  // the lanes' blocks so far
       bool ok = true;
       auto wait = [&](uint64_t* bar, int parity, int site) {
         ok = ok && mbar_wait(smem_u32(bar), parity & 1, abort_flag, p.status, kWaitLimitNs, site);
         return ok;
       };
+      // S = Q K^T of lane x with the keys of ring tile `i`, which is there
+      auto issue_s = [&](int x, int i, uint32_t aQ) {
+        const uint32_t aK = smem_u32(smem + C::OFF_RING + (i % C::RING) * C::TILE);
+#pragma unroll
+        for (int kk = 0; kk < HD / 16; ++kk)
+          tc_mma_f16(tmem + x * 128, sdesc_sw128(aQ + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024),
+                     sdesc_sw128(aK + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024), idS, kk > 0 ? 1u : 0u);
+        tc_commit(smem_u32(&s_full[x]));
+      };
+      auto issue_pv = [&](int x, int i, bool first) {
+        const uint32_t aV = smem_u32(smem + C::OFF_RING + (i % C::RING) * C::TILE);
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          tc_mma_f16_ta(tmem + C::COL_O + x * HD, tmem + x * 128 + kk * 8, sdesc_sw128(aV + kk * 2048, kAtom, 1024),
+                        idPV, (!first || kk > 0) ? 1u : 0u);
+        tc_commit(smem_u32(&o_full[x]));
+      };
+      auto release = [&](int i) { tc_commit(smem_u32(&empty[i % C::RING])); };
       for (; w.left > 0 && ok; w.next(p), ++j) {
         const int nt = w.blocks();
         const bool pair = tree_tile_rows(p, w) > 128;
-        const uint32_t aQ = smem_u32(smem) + (pair ? x * C::Q_BYTES : 0);
-        const int t_first = pair ? 0 : x, t_last = pair ? nt - 1 : nt - 1 - ((nt - 1 - x) & 1);  // this lane's
+        const int lead = pair ? 1 : 2;
+        const uint32_t aQ0 = smem_u32(smem), aQ1 = aQ0 + (pair ? C::Q_BYTES : 0);
         if (!wait(q_full, j, kSiteAttnQFull)) break;
-        if (t_first >= nt) mbar_arrive(smem_u32(q_empty));  // no block of this unit
+        // the first S of each lane; P V of its last block (the unit before) has
+        // read P from S's place
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (!pair && x >= nt) break;
+          const int i = it + (pair ? 0 : x);
+          if (!wait(&full[i % C::RING], i / C::RING, kSiteAttnKvFull)) break;
+          if (cnt[x] > 0 && !wait(&o_full[x], cnt[x] - 1, kSiteAttnSFree)) break;
+          tc_fence_after();
+          issue_s(x, i, x ? aQ1 : aQ0);
+          if (!pair || x == 1) release(i);
+        }
+        if (!ok) break;
+        it += min(lead, nt);
+        if (nt <= lead) tc_commit(smem_u32(q_empty));  // Q is read by no later product of this unit
         for (int t = 0; t < nt && ok; ++t) {
-          const bool mine = pair || (t & 1) == x;
-          // Both lanes follow every tile of the ring, a lane that has no use
-          // for one releasing it when it is full: so neither a full nor an empty
-          // barrier can run two phases ahead of, or behind, a wait.
-          {  // K: S = Q K^T, once P V of the lane's previous block has read P from S's place
-            const int st = it % C::RING;
-            if (!wait(&full[st], it / C::RING, kSiteAttnKvFull)) break;
-            if (mine) {
-              if (cnt > 0 && !wait(&o_full[x], cnt - 1, kSiteAttnSFree)) break;
+          const int iv = it, ik = it + 1;               // V of block t, K of block t + lead
+          const bool more = t + lead < nt;
+          for (int q = 0; q < (pair ? 2 : 1); ++q) {
+            const int x = pair ? q : t & 1;
+            // The accumulator's first product of a unit overwrites it: the
+            // softmax warps have read the previous unit's outputs.
+            const bool first = pair ? t == 0 : t < 2;
+            if (q == 0 && !wait(&full[iv % C::RING], iv / C::RING, kSiteAttnKvFull)) break;
+            if (!wait(&p_full[x], cnt[x], kSiteAttnPFull)) break;
+            if (first && j > 0 && !wait(o_empty, j - 1, kSiteAttnOEmpty)) break;
+            tc_fence_after();
+            issue_pv(x, iv, first);
+            if (!pair || q == 1) release(iv);
+            ++cnt[x];
+            if (more) {
+              if (q == 0 && !wait(&full[ik % C::RING], ik / C::RING, kSiteAttnKvFull)) break;
+              if (!wait(&o_full[x], cnt[x] - 1, kSiteAttnSFree)) break;  // P has been read: S may be overwritten
               tc_fence_after();
-              const uint32_t aK = smem_u32(smem + C::OFF_RING + st * C::TILE);
-#pragma unroll
-              for (int kk = 0; kk < HD / 16; ++kk)
-                tc_mma_f16(tS, sdesc_sw128(aQ + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024),
-                           sdesc_sw128(aK + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024), idS, kk > 0 ? 1u : 0u);
-              tc_commit(smem_u32(&s_full[x]));
-              tc_commit(smem_u32(&empty[st]));
-              if (t == t_last) tc_commit(smem_u32(q_empty));  // Q is read by no later product of this unit
-            } else {
-              mbar_arrive(smem_u32(&empty[st]));
+              issue_s(x, ik, x ? aQ1 : aQ0);
+              if (!pair || q == 1) {
+                release(ik);
+                if (t + lead == nt - 1) tc_commit(smem_u32(q_empty));
+              }
             }
-            ++it;
           }
-          {  // V: O += P V
-            const int st = it % C::RING;
-            if (!wait(&full[st], it / C::RING, kSiteAttnKvFull)) break;
-            if (mine) {
-              if (!wait(&p_full[x], cnt, kSiteAttnPFull)) break;
-              // the unit's first product overwrites O: the softmax warps have
-              // read the previous unit's
-              if (t == t_first && j > 0 && !wait(o_empty, j - 1, kSiteAttnOEmpty)) break;
-              tc_fence_after();
-              const uint32_t aV = smem_u32(smem + C::OFF_RING + st * C::TILE);
-#pragma unroll
-              for (int kk = 0; kk < 8; ++kk)
-                tc_mma_f16_ta(tO, tS + kk * 8, sdesc_sw128(aV + kk * 2048, kAtom, 1024), idPV,
-                              (t != t_first || kk > 0) ? 1u : 0u);
-              tc_commit(smem_u32(&o_full[x]));
-              tc_commit(smem_u32(&empty[st]));
-              ++cnt;
-            } else {
-              mbar_arrive(smem_u32(&empty[st]));
-            }
-            ++it;
-          }
+          it += more ? 2 : 1;
         }
       }
-      tc_commit(smem_u32(&drain[x]));
+      tc_commit(smem_u32(drain));
       int never = 0;
-      mbar_wait(smem_u32(&drain[x]), 0, &never, nullptr, 10000000ull);
+      mbar_wait(smem_u32(drain), 0, &never, nullptr, 10000000ull);
     }
     __syncwarp();
   }

@@ -29,7 +29,7 @@ struct TreeArgs {
   float sl2;               // scale * log2(e)
   uint32_t* status;
   int4* desc;              // [2 * grid]: the unit cut at CTA c's start, see tree_describe
-  float* part_o;           // [2 * grid][tile_rows][hd]
+  float* part_o;           // [2 * grid][tile_rows][hd], or [2 * grid][hd / 4][tile_rows][4] (tree_attn_tc.cu)
   float* part_ml;          // [2 * grid][tile_rows][2]
 };
 
@@ -90,72 +90,68 @@ struct TreeWalk {
   }
 };
 
-// Scratch of tree_locate in shared memory.
-struct TreeLocate {
-  long long warp_sum[32];
-  long long per, lo, hi, off;
-  int s;
-};
+// Quotient of numbers that hardly ever need more than 32 bits.
+SF_DEV long long div_ll(long long a, unsigned b) {
+  return a >> 32 ? a / b : static_cast<long long>(static_cast<unsigned>(a) / b);
+}
 
-// This CTA's run: every thread counts a contiguous share of the sequences, a
-// block-wide scan gives the total and finds the sequence that holds the run's
-// first block.  Called by all THREADS threads; `w` is the same in all of them.
-// Returns false for a CTA without work.
-template <int THREADS>
-SF_DEV bool tree_locate(const TreeArgs& p, TreeLocate& sh, TreeWalk& w) {
-  const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-  constexpr int W = THREADS / 32;
-  const int share = (p.batch.n_seqs + THREADS - 1) / THREADS;
-  const int s_lo = min(tid * share, p.batch.n_seqs), s_hi = min(s_lo + share, p.batch.n_seqs);
-  long long mine = 0;
-  bool bad = false;
-  for (int s = s_lo; s < s_hi; ++s) {
-    const TreeSeq q = tree_seq(p, s);
-    mine += q.items(p.n_kv);
-    bad = bad || q.bad;
-  }
-  if (bad && blockIdx.x == 0) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
-  long long inc = mine;
+SF_DEV TreeSeq tree_seq_or_none(const TreeArgs& p, int s) {
+  if (s < p.batch.n_seqs) return tree_seq(p, s);
+  TreeSeq q;
+  q.row0 = q.n = q.ctx = q.nb = q.tiles = 0;
+  q.bad = false;
+  return q;
+}
+
+SF_DEV long long warp_prefix(long long v, int lane) {
 #pragma unroll
   for (int o = 1; o < 32; o <<= 1) {
-    const long long v = __shfl_up_sync(0xffffffffu, inc, o);
-    if (lane >= o) inc += v;
+    const long long u = __shfl_up_sync(0xffffffffu, v, o);
+    if (lane >= o) v += u;
   }
-  if (lane == 31) sh.warp_sum[warp] = inc;
-  __syncthreads();
-  long long before = 0, total = 0;
-#pragma unroll
-  for (int i = 0; i < W; ++i) {
-    const long long v = sh.warp_sum[i];
-    if (i < warp) before += v;
-    total += v;
+  return v;
+}
+
+// This CTA's run, found by every warp on its own (a lane a sequence, 32 at a
+// time: no block-wide barrier, one round trip for up to 32 sequences).  lo: the
+// run's first block, per: the blocks of a run.  Returns false for a CTA without
+// work; the walk is the same in all threads.
+SF_DEV bool tree_locate(const TreeArgs& p, TreeWalk& w, long long& lo, long long& per) {
+  const int lane = threadIdx.x & 31, n = p.batch.n_seqs;
+  TreeSeq q = tree_seq_or_none(p, lane);
+  bool bad = q.bad;
+  long long inc = warp_prefix(q.items(p.n_kv), lane);
+  long long total = __shfl_sync(0xffffffffu, inc, 31);
+  for (int c = 32; c < n; c += 32) {
+    const TreeSeq r = tree_seq_or_none(p, c + lane);
+    bad = bad || r.bad;
+    total += __shfl_sync(0xffffffffu, warp_prefix(r.items(p.n_kv), lane), 31);
   }
-  const long long per = (total + gridDim.x - 1) / gridDim.x;
-  const long long lo = per * blockIdx.x;
+  if (bad && blockIdx.x == 0 && threadIdx.x < 32) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
+  per = div_ll(total + gridDim.x - 1, gridDim.x);
+  lo = per * blockIdx.x;
   const long long hi = min(lo + per, total);
-  if (lo >= hi) return false;  // the same in every thread
-  long long at = before + inc - mine;
-  if (lo >= at && lo < at + mine) {
-    for (int s = s_lo; s < s_hi; ++s) {
-      const long long it = tree_seq(p, s).items(p.n_kv);
-      if (lo < at + it) {
-        sh.s = s;
-        sh.off = lo - at;
-        break;
-      }
-      at += it;
-    }
+  if (lo >= hi) return false;
+  long long base = 0;
+  int c = 0;
+  while (lo >= base + __shfl_sync(0xffffffffu, inc, 31)) {
+    base += __shfl_sync(0xffffffffu, inc, 31);
+    c += 32;
+    q = tree_seq_or_none(p, c + lane);
+    inc = warp_prefix(q.items(p.n_kv), lane);
   }
-  __syncthreads();
-  w.s = sh.s;
-  w.q = tree_seq(p, w.s);
-  w.u = static_cast<int>(sh.off / w.q.nb);
-  w.b0 = static_cast<int>(sh.off % w.q.nb);
+  const int src = __ffs(__ballot_sync(0xffffffffu, lo < base + inc)) - 1;
+  const long long off = lo - base - __shfl_sync(0xffffffffu, inc - q.items(p.n_kv), src);
+  w.s = c + src;
+  w.q.row0 = __shfl_sync(0xffffffffu, q.row0, src);
+  w.q.n = __shfl_sync(0xffffffffu, q.n, src);
+  w.q.ctx = __shfl_sync(0xffffffffu, q.ctx, src);
+  w.q.nb = __shfl_sync(0xffffffffu, q.nb, src);
+  w.q.tiles = __shfl_sync(0xffffffffu, q.tiles, src);
+  w.q.bad = false;
+  w.u = static_cast<int>(div_ll(off, w.q.nb));
+  w.b0 = static_cast<int>(off - static_cast<long long>(w.u) * w.q.nb);
   w.left = hi - lo;
-  if (tid == 0) {
-    sh.per = per;
-    sh.lo = lo;
-  }
   return true;
 }
 
@@ -171,16 +167,19 @@ SF_DEV int tree_tile_rows(const TreeArgs& p, const TreeWalk& w) {
 // By one thread of every CTA: the unit that this CTA's start cuts, if this is
 // the first cut in it, for the combine kernel: {rows, row0, m0, head},
 // {first CTA, last CTA, the first CTA's slot, 0}; rows 0: nothing to merge.
-SF_DEV void tree_describe_none(const TreeArgs& p) { p.desc[2 * blockIdx.x] = make_int4(0, 0, 0, 0); }
-SF_DEV void tree_describe(const TreeArgs& p, const TreeWalk& w, long long per, long long lo) {
+SF_DEV void tree_describe(const TreeArgs& p, const TreeWalk& w, bool work, long long lo, long long per) {
   const int c = blockIdx.x;
-  const long long beg = lo - w.b0, end = beg + w.q.nb;
-  if (w.b0 == 0 || beg < lo - per) {
-    tree_describe_none(p);
-    return;
+  int4 a = make_int4(0, 0, 0, 0);
+  if (work && w.b0 > 0) {
+    const long long beg = lo - w.b0, end = beg + w.q.nb;
+    if (beg >= lo - per) {
+      a = make_int4(tree_tile_rows(p, w), w.q.row0, tree_m0(p, w), w.head());
+      // per < 2^32: a run of more 64-key blocks than that is no cache's
+      p.desc[2 * c + 1] = make_int4(c - 1, static_cast<int>(div_ll(end - 1, static_cast<unsigned>(per))),
+                                    2 * (c - 1) + (beg == lo - per ? 0 : 1), 0);
+    }
   }
-  p.desc[2 * c] = make_int4(tree_tile_rows(p, w), w.q.row0, tree_m0(p, w), w.head());
-  p.desc[2 * c + 1] = make_int4(c - 1, static_cast<int>((end - 1) / per), 2 * (c - 1) + (beg == lo - per ? 0 : 1), 0);
+  p.desc[2 * c] = a;
 }
 
 // Pool token of a sequence's token, or -1 (flagged) where the table has none.
