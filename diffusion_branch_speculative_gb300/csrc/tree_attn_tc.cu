@@ -51,9 +51,10 @@ struct Tc {
   static constexpr int RING = HD == 128 ? 5 : 10;   // tiles
   static constexpr int OFF_RING = 2 * Q_BYTES;
   static constexpr int SMEM = OFF_RING + RING * TILE + 1024;  // and the base's alignment
-  // TMEM: S (then P over its first 64 columns) of lane x at 128 x, O at COL_O + HD x
+  // TMEM: S of lane x at 128 x (then P over its columns from COL_P on), O at COL_O + HD x
   static constexpr uint32_t TMEM_COLS = 512;
   static constexpr uint32_t COL_O = 256;
+  static constexpr uint32_t COL_P = 64;
 };
 
 // D[tmem] (+)= A[tmem] * B[smem]^T: as tc_mma_f16, A's row r in lane r, two bf16
@@ -192,11 +193,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
 
   // Every role walks the same pieces in the same order; j counts them, it the
   // ring's tiles.  In a piece of at most 128 rows lane x has blocks x, x + 2, ...
-  if (warp < 4) {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-  } else {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
-  }
   if (warp < 2) {
     // ------------------------------------------------------------ loaders --
     const int lt = threadIdx.x;
@@ -382,24 +378,31 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
           break;
         }
         tc_fence_after();
-        uint32_t sv[4][32];
+        // Two passes of 64 columns: the maximum over the first half, which is
+        // read again after the second's weights (128 scores a thread would not
+        // fit its registers beside the rest).
+        uint32_t sv[2][32];
+        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+        auto mask = [&](int half) {
 #pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld32(tS + c * 32, sv[c]);
-#pragma unroll
-        for (int c = 0; c < 4; ++c) tmem_ld_wait(sv[c]);
-        if (!allv) {
-#pragma unroll
-          for (int c = 0; c < 4; ++c)
+          for (int c = 0; c < 2; ++c)
 #pragma unroll
             for (int e = 0; e < 32; ++e)
-              if (!((km[c >> 1] >> (32 * (c & 1) + e)) & 1u)) sv[c][e] = 0xff800000u;  // -inf
+              if (!((km[half] >> (32 * c + e)) & 1u)) sv[c][e] = 0xff800000u;  // -inf
+        };
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+          tmem_ld32(tS + half * 64, sv[0]);
+          tmem_ld32(tS + half * 64 + 32, sv[1]);
+          tmem_ld_wait(sv[0]);
+          tmem_ld_wait(sv[1]);
+          if (!allv) mask(half);
+#pragma unroll
+          for (int c = 0; c < 2; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; e += 2)
+              mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
         }
-        float mx4[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
-#pragma unroll
-        for (int c = 0; c < 4; ++c)
-#pragma unroll
-          for (int e = 0; e < 32; e += 2)
-            mx4[(e >> 1) & 3] = max3(mx4[(e >> 1) & 3], __uint_as_float(sv[c][e]), __uint_as_float(sv[c][e + 1]));
         const float mx = fmaxf(max3(mx4[0], mx4[1], mx4[2]), mx4[3]);
         const float m_new = fmaxf(m_ref, mx * p.sl2);
         float alpha = 1.f;
@@ -427,8 +430,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
         const float base = m_ref == -INFINITY ? 0.f : m_ref;
         const float2 scale2 = make_float2(p.sl2, p.sl2), base2 = make_float2(-base, -base);
         float2 ls[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll
-        for (int c = 0; c < 4; ++c) {
+        // the second half's weights from the registers into P's upper columns,
+        // then the first half's, read again, into its lower ones (over scores
+        // that have been used)
+        auto weights = [&](int c, int column) {
           uint32_t pk[16];
 #pragma unroll
           for (int e = 0; e < 32; e += 2) {
@@ -437,8 +442,17 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
             ls[(e >> 1) & 1] = add2(ls[(e >> 1) & 1], y);
             pk[e / 2] = pack_bf16x2(y.x, y.y);
           }
-          tmem_st16(tS + c * 16, pk);
-        }
+          tmem_st16(tS + C::COL_P + column, pk);
+        };
+        weights(0, 32);
+        tmem_ld32(tS, sv[0]);
+        weights(1, 48);
+        tmem_ld32(tS + 32, sv[1]);
+        tmem_ld_wait(sv[0]);
+        tmem_ld_wait(sv[1]);
+        if (!allv) mask(0);
+        weights(0, 0);
+        weights(1, 16);
         l += (ls[0].x + ls[0].y) + (ls[1].x + ls[1].y);
         tmem_st_wait();
         tc_fence_before();
@@ -574,7 +588,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
         const uint32_t aV = smem_u32(smem + C::OFF_RING + (i % C::RING) * C::TILE);
 #pragma unroll
         for (int kk = 0; kk < 8; ++kk)
-          tc_mma_f16_ta(tmem + C::COL_O + x * HD, tmem + x * 128 + kk * 8, sdesc_sw128(aV + kk * 2048, kAtom, 1024),
+          tc_mma_f16_ta(tmem + C::COL_O + x * HD, tmem + x * 128 + C::COL_P + kk * 8, sdesc_sw128(aV + kk * 2048, kAtom, 1024),
                         idPV, (!first || kk > 0) ? 1u : 0u);
         tc_commit(smem_u32(&o_full[x]));
       };
