@@ -11,29 +11,31 @@
 //   S = Q K^T (128 x 128 x HD), softmax with one thread per row, P as bf16 (the
 //   tensor cores' operand: each weight off by half a step) back over S in TMEM,
 //   O += P V with P read from TMEM.
-// Shared memory's 128 bytes a cycle are what such products run short of: P in
-// TMEM and full-width products leave Q K^T 64 KB, V 32 KB and the copies 64 KB
-// a block and pair of lanes (a lane's P through shared memory and half-width
-// products took 1.35 us a block and lane, above the memory's own time).
+// P in TMEM keeps it out of shared memory, whose 128 bytes a cycle are what such
+// products run short of.  A lane's chain of S, softmax and P V is what bounds
+// a block: the products alone take 2050 cycles for both lanes.
 //
-// Roles (384 threads): warps 0-1 load, warp 2 issues all products, warp 3 owns
-// the TMEM allocation, warps 4-7 and 8-11 are the lanes' softmax.  One issuer, so
-// that a lane's P V and next Q K^T run in one go and the lanes fall into
-// alternation (an issuer per lane interleaved their products: both lanes' S came
-// at once and the tensor cores idled through both softmaxes, 5050 cycles a block
-// against 2900).  K and V tiles go through one ring in the order of their use.
+// Roles (384 threads): warp 0 loads keys, warp 1 values, both the queries; warp 2
+// issues all products (warp 3 owns the TMEM allocation), warps 4-7 and 8-11 are
+// the lanes' softmax.  One issuer, so that a lane's P V and next Q K^T go out in
+// one run and the lanes fall into alternation (with an issuer each, both lanes'
+// products interleaved, both S came at once and the tensor cores idled through
+// both softmaxes: 4700-5000 cycles a block against 3950).  A run of products is
+// followed by one commit alone, since a second one waits for the products: tiles
+// are released by the softmax (which has seen S) and by the issuer (which has
+// seen P V).
+// K and V tiles (128 keys) go through a ring each.
 // They come by TMA, one box per run of tokens inside a page (page_size's power
-// of two, 8 to 64), the boxes issued by the loaders' threads side by side; boxes
+// of two, 8 to 64), the boxes issued by a warp's threads side by side; boxes
 // past the sequence read zeros, and a block that holds the tree's tokens, or
 // ends the sequence, has its values mended before they are handed on.  Which of
-// its tokens a row sees is 64 bits at a time, found by walking up its ancestors.
+// its tokens a row sees is 64 bits a step, found by walking up its ancestors.
 #include "tree_sched.cuh"
 
 namespace sf {
 namespace {
 
 constexpr int kTcThreads = 384;
-constexpr int kLoaders = 64;
 constexpr int kAtom = 128 * 128;  // one 128-row x 128-byte swizzle block
 constexpr int kOddBufs = 4;       // units whose odd-value notes may be alive at once
 
@@ -48,7 +50,8 @@ struct Tc {
   static constexpr int NATOM = HD / 64;
   static constexpr int Q_BYTES = kAtom * NATOM;     // of one lane
   static constexpr int TILE = kAtom * NATOM;        // 128 keys' K or V
-  static constexpr int RING = HD == 128 ? 5 : 10;   // tiles
+  // tiles in flight; a value tile waits longer for its use
+  static constexpr int KRING = HD == 128 ? 2 : 5, VRING = HD == 128 ? 3 : 5, RING = KRING + VRING;
   static constexpr int OFF_RING = 2 * Q_BYTES;
   static constexpr int SMEM = OFF_RING + RING * TILE + 1024;  // and the base's alignment
   // TMEM: S of lane x at 128 x (then P over its columns from COL_P on), O at COL_O + HD x
@@ -130,16 +133,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
   const TreeArgs& p = ta.t;
   extern __shared__ uint8_t smem_raw[];
   uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
-  __shared__ __align__(8) uint64_t bars[2 * C::RING + 11];  // 10 more barriers behind the ring's
+  __shared__ __align__(8) uint64_t bars[2 * C::RING + 11];
   __shared__ uint32_t tmem_slot_s;
   __shared__ volatile int abort_s;
-  __shared__ volatile int okflag[C::RING];
-  __shared__ volatile int okq;
   __shared__ float2 xch[128];
   // nodes whose values are not all finite, by unit (see the loaders)
   __shared__ uint32_t odd[kOddBufs][SPECFOLD_MAX_TREE / 32];
-  uint64_t* full = bars;                // [RING]
-  uint64_t* empty = bars + C::RING;     // [RING]
+  uint64_t* full = bars;                // [RING]: the keys' tiles, then the values'
+  uint64_t* empty = bars + C::RING;     // [RING]: a key tile's two arrivals (the lanes'), a value tile's one
   uint64_t* q_full = bars + 2 * C::RING;
   uint64_t* q_empty = q_full + 1;       // both lanes' S products of a unit are done: Q may be replaced
   uint64_t* s_full = q_full + 2;        // [lane]: one completion per block of the lane
@@ -152,11 +153,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
 
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(q_full), 1);
-    mbar_init(smem_u32(q_empty), 1);
+    mbar_init(smem_u32(q_full), 2);  // the two loading warps
+    mbar_init(smem_u32(q_empty), 2);
     for (int i = 0; i < C::RING; ++i) {
       mbar_init(smem_u32(&full[i]), 1);
-      mbar_init(smem_u32(&empty[i]), 1);
+      mbar_init(smem_u32(&empty[i]), i < C::KRING ? 2 : 1);
     }
     for (int x = 0; x < 2; ++x) {
       mbar_init(smem_u32(&s_full[x]), 1);
@@ -192,110 +193,120 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
   const int g = p.g;
 
   // Every role walks the same pieces in the same order; j counts them, it the
-  // ring's tiles.  In a piece of at most 128 rows lane x has blocks x, x + 2, ...
+  // blocks (tiles of each ring).  The lanes use K of block t + lead after V of
+  // block t: lead 1, or 2 where they take alternate blocks.
   if (warp < 2) {
     // ------------------------------------------------------------ loaders --
-    const int lt = threadIdx.x;
+    const bool is_v = warp == 1;
+    const CUtensorMap* map = is_v ? &ta.mapV : &ta.mapK;
     int it = 0, j = 0, issued = -1, fixes = 0;
     bool ok = true;
-    const int boxes = kTreeTcKeys / ta.box;
-    const int pool = p.cache.num_pages * p.cache.page_size;
+    const int boxes = kTreeTcKeys / ta.box, ps = p.cache.page_size;
+    const int pool = p.cache.num_pages * ps;
+    const int box = lane & 15, atom = lane >> 4;  // what this thread issues of a tile
+    const bool issues = box < boxes && atom < C::NATOM;
     for (; w.left > 0 && ok; w.next(p), ++j) {
-      const int h = w.head(), m0 = tree_m0(p, w), rows = tree_tile_rows(p, w), ctx = w.q.ctx, len = ctx + w.q.n;
-      const int nt = w.blocks();
-      const int lead = rows > 128 ? 1 : 2;  // key tiles ahead of the first value tile
-      // this thread's box of a block: the table's entry is read a tile ahead of
-      // its use and looked at only then; kNoBox past the sequence
-      constexpr int kNoBox = -0x7fffffff;
-      auto box_page = [&](int t) {
-        const long long tok = static_cast<long long>(w.b0 + t) * kTreeTcKeys + lane * ta.box;
-        if (lane >= boxes || t >= nt || tok >= len) return kNoBox;
-        const unsigned pg = static_cast<unsigned>(tok) / static_cast<unsigned>(p.cache.page_size);
-        return pg < static_cast<unsigned>(p.cache.table_pages) ? p.cache.block_table[w.s * p.cache.table_stride + pg] : -1;
+      const int h = w.head(), rows = tree_tile_rows(p, w), ctx = w.q.ctx, len = ctx + w.q.n;
+      const int nt = w.blocks(), lead = rows > 128 ? 1 : 2;
+      // queries, by both warps: the previous unit's S products must be done with
+      // their place
+      auto load_queries = [&]() {
+        const int qt = threadIdx.x;
+        bool free = true;
+        if (lane == 0 && j > 0)
+          free = mbar_wait(smem_u32(q_empty), (j - 1) & 1, abort_flag, p.status, kWaitLimitNs, kSiteAttnQEmpty);
+        if (!__shfl_sync(0xffffffffu, free, 0)) return false;
+        constexpr int RSTEP = 64 / (HD / 8);  // rows of one step; a row's node and head follow by steps
+        const int c = qt % (HD / 8), dn = RSTEP / g, dh = RSTEP % g, m = tree_m0(p, w) + qt / (HD / 8);
+        int hd = m % g;
+        const long long d_node = p.q_rs - g * p.q_hs, d_step = dn * p.q_rs + dh * p.q_hs;
+        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (w.q.row0 + m / g) * p.q_rs +
+                                   (h * g + hd) * p.q_hs + c * 8;
+        const int most = lead == 1 ? 256 : 128;
+        const uint32_t q0 = smem_u32(smem) + (c >> 3) * kAtom;
+#pragma unroll 4
+        for (int r = qt / (HD / 8); r < most; r += RSTEP) {
+          const bool there = r < rows;
+          cp_async16(q0 + (r >> 7) * C::Q_BYTES + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
+                     there ? src : static_cast<const __nv_bfloat16*>(p.q), there ? 16u : 0u);
+          src += d_step;
+          hd += dh;
+          if (hd >= g) {
+            hd -= g;
+            src += d_node;
+          }
+        }
+        cp_async_commit();
+        cp_async_wait<0>();
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(q_full));
+        return true;
       };
-      auto box_token = [&](int t, int page) {
-        if (page >= 0 && page < p.cache.num_pages)
-          return page * p.cache.page_size +
-                 static_cast<int>(static_cast<unsigned>((w.b0 + t) * kTreeTcKeys + lane * ta.box) %
-                                  static_cast<unsigned>(p.cache.page_size));
-        if (page != kNoBox) atomicOr(p.status, SPECFOLD_DEV_BAD_PAGE);
-        return pool;  // wholly past the pool: the box reads zeros
-      };
-      int zk = box_page(0), zv = zk;
-      // the previous unit's S products must be done with the Q buffers
-      if (lt == 0)
-        okq = j == 0 || mbar_wait(smem_u32(q_empty), (j - 1) & 1, abort_flag, p.status, kWaitLimitNs, kSiteAttnQEmpty);
-      named_bar_sync(1, kLoaders);
-      if (!okq) {
+      const int heads_k = min(lead, nt);
+      if (is_v && !load_queries()) {
         ok = false;
         break;
       }
-      if (lt < SPECFOLD_MAX_TREE / 32) odd[j % kOddBufs][lt] = 0u;
-      // the order of use: `lead` key tiles, then V of block t and K of t + lead
-      for (int i = 0; i < 2 * nt; ++i, ++it) {
-        const int heads_k = min(lead, nt), past = nt - heads_k;  // leading keys, and those behind them
-        const bool lead_k = i < heads_k, paired = !lead_k && i < heads_k + 2 * past;
-        const bool is_v = !lead_k && (!paired || (i - heads_k) % 2 == 0);
-        const int t = lead_k ? i : paired ? (i - heads_k) / 2 + (is_v ? 0 : lead) : i - nt;
-        const bool mend = is_v && static_cast<long long>(w.b0 + t + 1) * kTreeTcKeys > ctx;
-        const int st = it % C::RING;
-        const uint32_t fb = smem_u32(mend ? landed : &full[st]);
-        if (lt == 0) {
-          const bool free = mbar_wait(smem_u32(&empty[st]), ((it / C::RING) & 1) ^ 1, abort_flag, p.status,
-                                      kWaitLimitNs, kSiteAttnKvEmpty);
-          if (free) mbar_arrive_expect_tx(fb, C::TILE);
-          if (free && !mend) issued = it;
-          okflag[st] = free;
-        }
-        named_bar_sync(1, kLoaders);
-        if (!okflag[st]) {
+      // this thread's box of the next tile: the table's entry is read a tile
+      // ahead of its use and looked at only then
+      const unsigned tok0 = static_cast<unsigned>(w.b0) * kTreeTcKeys + box * ta.box;
+      int pg = tok0 / static_cast<unsigned>(ps), off = tok0 - pg * ps;
+      const int dpg = kTreeTcKeys / ps, doff = kTreeTcKeys - dpg * ps;
+      const int32_t* table = p.cache.block_table + w.s * p.cache.table_stride;
+      long long left = static_cast<long long>(len) - tok0;  // tokens from the box's first on
+      auto entry = [&](int t) {
+        return issues && t < nt && left > 0 && pg < p.cache.table_pages ? table[pg] : -1;
+      };
+      int page = entry(0);
+      if (is_v && lane < SPECFOLD_MAX_TREE / 32) odd[j % kOddBufs][lane] = 0u;
+      for (int t = 0; t < nt; ++t) {
+        if (!is_v && t == heads_k && !load_queries()) {  // behind the first keys' loads
           ok = false;
           break;
         }
-        uint8_t* tile = smem + C::OFF_RING + st * C::TILE;
-        if (lane < boxes && warp < C::NATOM)
-          tma_load_3d(smem_u32(tile + warp * kAtom + lane * ta.box * 128), is_v ? &ta.mapV : &ta.mapK, fb, warp * 64, h,
-                      box_token(t, is_v ? zv : zk));
-        if (is_v)
-          zv = box_page(t + 1);
-        else
-          zk = box_page(t + 1);
-        if (i == 0) {  // the queries, behind the first keys' load
-          constexpr int RSTEP = kLoaders / (HD / 8);  // rows of one step; the row's node and head follow by steps
-          const int c = lt % (HD / 8), dn = RSTEP / g, dh = RSTEP % g;
-          int r = lt / (HD / 8), node = (m0 + r) / g, hd = (m0 + r) % g;
-          const __nv_bfloat16* qb = static_cast<const __nv_bfloat16*>(p.q) + w.q.row0 * p.q_rs + h * g * p.q_hs + c * 8;
-          const uint32_t q0 = smem_u32(smem) + (c >> 3) * kAtom;
-          const int most = lead == 1 ? 256 : 128;
-#pragma unroll 4
-          for (; r < most; r += RSTEP) {
-            const bool there = r < rows;
-            cp_async16(q0 + (r >> 7) * C::Q_BYTES + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
-                       there ? qb + node * p.q_rs + hd * p.q_hs : qb, there ? 16u : 0u);
-            node += dn;
-            hd += dh;
-            if (hd >= g) hd -= g, ++node;
-          }
-          cp_async_commit();
-          cp_async_wait<0>();
-          fence_proxy_async_smem();
-          named_bar_sync(1, kLoaders);
-          if (lt == 0) mbar_arrive(smem_u32(q_full));
+        const int i = it + t, turn = i / (is_v ? C::VRING : C::KRING);
+        const int st = is_v ? C::KRING + i % C::VRING : i % C::KRING;
+        const bool mend = is_v && static_cast<long long>(w.b0 + t + 1) * kTreeTcKeys > ctx;
+        const uint32_t fb = smem_u32(mend ? landed : &full[st]);
+        if (lane == 0) {
+          ok = mbar_wait(smem_u32(&empty[st]), (turn & 1) ^ 1, abort_flag, p.status, kWaitLimitNs,
+                         kSiteAttnKvEmpty);
+          if (ok) mbar_arrive_expect_tx(fb, C::TILE);
         }
+        ok = __shfl_sync(0xffffffffu, ok, 0);
+        if (!ok) break;
+        if (!mend) issued = i;
+        uint8_t* tile = smem + C::OFF_RING + st * C::TILE;
+        if (issues) {
+          const bool there = page >= 0 && page < p.cache.num_pages;
+          if (!there && left > 0) atomicOr(p.status, SPECFOLD_DEV_BAD_PAGE);
+          // a box without a page lies wholly past the pool: it reads zeros
+          tma_load_3d(smem_u32(tile + atom * kAtom + box * ta.box * 128), map, fb, atom * 64, h,
+                      there && left > 0 ? page * ps + off : pool);
+        }
+        left -= kTreeTcKeys;
+        pg += dpg;
+        off += doff;
+        if (off >= ps) {
+          off -= ps;
+          ++pg;
+        }
+        page = entry(t + 1);
         if (mend) {
-          // Tokens past the end may hold anything, and a weight of zero does not
-          // silence an infinite value or a NaN in a product: values past the
-          // end become zeros; such values of the tree's tokens are taken out,
-          // noted, and added at the end to the rows that see them.
+          // Tokens past the end may hold anything, and a weight of zero does
+          // not silence an infinite value or a NaN in a product: values past
+          // the end become zeros; such values of the tree's tokens are taken
+          // out, noted, and added at the end to the rows that see them.
           const bool there = mbar_wait(smem_u32(landed), fixes & 1, abort_flag, p.status, kWaitLimitNs, kSiteAttnKvFull);
           ++fixes;
-          const long long tok0 = static_cast<long long>(w.b0 + t) * kTreeTcKeys;
+          const long long t0 = static_cast<long long>(w.b0 + t) * kTreeTcKeys;
+          const int r0 = t0 >= ctx ? 0 : static_cast<int>(ctx - t0);  // the tree's first row of the tile
           if (there) {
 #pragma unroll 1
-            for (int k = lt; k < 128 * (HD / 8); k += kLoaders) {
+            for (int k = r0 * (HD / 8) + lane; k < 128 * (HD / 8); k += 32) {
               const int kr = k / (HD / 8), c = k % (HD / 8);
-              const int e = static_cast<int>(tok0 + kr - ctx);
-              if (e < 0) continue;
+              const int e = static_cast<int>(t0 + kr - ctx);
               uint4* v = reinterpret_cast<uint4*>(tile + (c >> 3) * kAtom + kr * 128 + (((c & 7) ^ (kr & 7)) << 4));
               const uint4 u = *v;
               uint32_t y[4] = {u.x, u.y, u.z, u.w};
@@ -315,18 +326,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
             }
           }
           fence_proxy_async_smem();
-          named_bar_sync(1, kLoaders);
-          if (lt == 0) mbar_arrive(smem_u32(&full[st]));
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(&full[st]));
         }
       }
+      if (ok && !is_v && nt == heads_k) ok = load_queries();
+      it += nt;
     }
-    if (lt == 0 && *abort_flag) {
+    if (lane == 0 && *abort_flag) {
       // let the copies already issued land before the CTA exits
       int never = 0;
-      if (issued >= 0)
-        mbar_wait(smem_u32(&full[issued % C::RING]), (issued / C::RING) & 1, &never, nullptr, 10000000ull);
+      if (issued >= 0) {
+        const int ring = is_v ? C::VRING : C::KRING;
+        mbar_wait(smem_u32(&full[(is_v ? C::KRING : 0) + issued % ring]), (issued / ring) & 1, &never, nullptr, 10000000ull);
+      }
       if (fixes > 0) mbar_wait(smem_u32(landed), (fixes - 1) & 1, &never, nullptr, 10000000ull);
     }
+    __syncwarp();
   } else if (warp >= 4) {
     // ------------------------------------------------------------ softmax --
     // A row's thread raises its reference maximum m, and rescales O in place,
@@ -340,7 +356,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
     const uint32_t tS = tmem + lane_off + x * 128;
     const uint32_t tO = tmem + lane_off + C::COL_O;  // lane 0's; lane 1's HD columns on
     const int pair_bar = 2 + (warp & 3);  // named barrier of the two warps of these rows
-    int cnt = 0, j = 0;  // blocks of this lane so far
+    int cnt = 0, j = 0, it = 0;  // blocks of this lane so far
+    const bool leader = (warp & 3) == 0 && lane == 0;
     bool ok = true;
     for (bool first = true; w.left > 0 && ok; first = false, w.next(p), ++j) {
       const int h = w.head(), ctx = w.q.ctx, nt = w.blocks(), rows = tree_tile_rows(p, w);
@@ -353,6 +370,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
       float m_ref = -INFINITY, l = 0.f;
       const int t_step = pair ? 1 : 2;
       bool began = false;
+      if (leader && !pair && x >= nt) mbar_arrive(smem_u32(q_empty));  // no block of this unit
       for (int t = pair ? 0 : x; t < nt; t += t_step, ++cnt) {
         const int key0 = (w.b0 + t) * kTreeTcKeys;
         const bool allv = key0 + kTreeTcKeys <= ctx;
@@ -378,6 +396,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
           break;
         }
         tc_fence_after();
+        if (leader) {  // S is there: its keys are done with, and after the last one the queries
+          const uint32_t eb = smem_u32(&empty[(it + t) % C::KRING]);
+          mbar_arrive(eb);
+          if (!pair) mbar_arrive(eb);
+          if (t + t_step >= nt) mbar_arrive(smem_u32(q_empty));
+        }
         // Two passes of 64 columns: the maximum over the first half, which is
         // read again after the second's weights (128 scores a thread would not
         // fit its registers beside the rest).
@@ -562,6 +586,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
       tc_fence_before();
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(o_empty));
+      it += nt;
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------------- MMA --
@@ -569,78 +594,67 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
       constexpr uint32_t idS = idesc_bf16_f32(128, 128, false);
       constexpr uint32_t idPV = idesc_bf16_f32(128, HD, true);
       int it = 0, j = 0;
-      int cnt[2] = {0, 0};  // the lanes' blocks so far
+      int cnt[2] = {0, 0};  // the lanes' P V products so far
       bool ok = true;
       auto wait = [&](uint64_t* bar, int parity, int site) {
         ok = ok && mbar_wait(smem_u32(bar), parity & 1, abort_flag, p.status, kWaitLimitNs, site);
         return ok;
       };
-      // S = Q K^T of lane x with the keys of ring tile `i`, which is there
+      auto v_at = [&](int i) { return C::KRING + i % C::VRING; };
+      auto k_there = [&](int i) { return wait(&full[i % C::KRING], i / C::KRING, kSiteAttnKvFull); };
+      // S = Q K^T of lane x with the keys of block i, once the lane's last P V
+      // has read P from S's place
       auto issue_s = [&](int x, int i, uint32_t aQ) {
-        const uint32_t aK = smem_u32(smem + C::OFF_RING + (i % C::RING) * C::TILE);
+        tc_fence_after();
+        const uint32_t aK = smem_u32(smem + C::OFF_RING + (i % C::KRING) * C::TILE);
 #pragma unroll
         for (int kk = 0; kk < HD / 16; ++kk)
           tc_mma_f16(tmem + x * 128, sdesc_sw128(aQ + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024),
                      sdesc_sw128(aK + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024), idS, kk > 0 ? 1u : 0u);
         tc_commit(smem_u32(&s_full[x]));
       };
-      auto issue_pv = [&](int x, int i, bool first) {
-        const uint32_t aV = smem_u32(smem + C::OFF_RING + (i % C::RING) * C::TILE);
-#pragma unroll
-        for (int kk = 0; kk < 8; ++kk)
-          tc_mma_f16_ta(tmem + C::COL_O + x * HD, tmem + x * 128 + C::COL_P + kk * 8, sdesc_sw128(aV + kk * 2048, kAtom, 1024),
-                        idPV, (!first || kk > 0) ? 1u : 0u);
-        tc_commit(smem_u32(&o_full[x]));
-      };
-      auto release = [&](int i) { tc_commit(smem_u32(&empty[i % C::RING])); };
       for (; w.left > 0 && ok; w.next(p), ++j) {
         const int nt = w.blocks();
         const bool pair = tree_tile_rows(p, w) > 128;
         const int lead = pair ? 1 : 2;
         const uint32_t aQ0 = smem_u32(smem), aQ1 = aQ0 + (pair ? C::Q_BYTES : 0);
         if (!wait(q_full, j, kSiteAttnQFull)) break;
-        // the first S of each lane; P V of its last block (the unit before) has
-        // read P from S's place
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (!pair && x >= nt) break;
+        for (int x = 0; x < 2 && (pair || x < nt); ++x) {  // the lanes' first S
           const int i = it + (pair ? 0 : x);
-          if (!wait(&full[i % C::RING], i / C::RING, kSiteAttnKvFull)) break;
-          if (cnt[x] > 0 && !wait(&o_full[x], cnt[x] - 1, kSiteAttnSFree)) break;
-          tc_fence_after();
+          if (!k_there(i) || (cnt[x] > 0 && !wait(&o_full[x], cnt[x] - 1, kSiteAttnSFree))) break;
           issue_s(x, i, x ? aQ1 : aQ0);
-          if (!pair || x == 1) release(i);
         }
-        if (!ok) break;
-        it += min(lead, nt);
-        if (nt <= lead) tc_commit(smem_u32(q_empty));  // Q is read by no later product of this unit
         for (int t = 0; t < nt && ok; ++t) {
-          const int iv = it, ik = it + 1;               // V of block t, K of block t + lead
+          const int iv = it + t, ik = it + t + lead;
           const bool more = t + lead < nt;
-          for (int q = 0; q < (pair ? 2 : 1); ++q) {
+          const int turns = pair ? 2 : 1;
+          if (!wait(&full[v_at(iv)], iv / C::VRING, kSiteAttnKvFull)) break;
+          for (int q = 0; q < turns; ++q) {
             const int x = pair ? q : t & 1;
-            // The accumulator's first product of a unit overwrites it: the
-            // softmax warps have read the previous unit's outputs.
+            // the accumulator's first product of a unit overwrites it: the
+            // softmax warps have read the previous unit's outputs
             const bool first = pair ? t == 0 : t < 2;
-            if (q == 0 && !wait(&full[iv % C::RING], iv / C::RING, kSiteAttnKvFull)) break;
             if (!wait(&p_full[x], cnt[x], kSiteAttnPFull)) break;
             if (first && j > 0 && !wait(o_empty, j - 1, kSiteAttnOEmpty)) break;
             tc_fence_after();
-            issue_pv(x, iv, first);
-            if (!pair || q == 1) release(iv);
+            const uint32_t aV = smem_u32(smem + C::OFF_RING + v_at(iv) * C::TILE);
+            const uint32_t tO = tmem + C::COL_O + x * HD, tP = tmem + x * 128 + C::COL_P;
+#pragma unroll
+            for (int kk = 0; kk < 8; ++kk)
+              tc_mma_f16_ta(tO, tP + kk * 8, sdesc_sw128(aV + kk * 2048, kAtom, 1024), idPV, (!first || kk > 0) ? 1u : 0u);
+            tc_commit(smem_u32(&o_full[x]));
+            const bool last = q == turns - 1;
             ++cnt[x];
-            if (more) {
-              if (q == 0 && !wait(&full[ik % C::RING], ik / C::RING, kSiteAttnKvFull)) break;
-              if (!wait(&o_full[x], cnt[x] - 1, kSiteAttnSFree)) break;  // P has been read: S may be overwritten
-              tc_fence_after();
-              issue_s(x, ik, x ? aQ1 : aQ0);
-              if (!pair || q == 1) {
-                release(ik);
-                if (t + lead == nt - 1) tc_commit(smem_u32(q_empty));
-              }
+            if (!more) {
+              if (last) tc_commit(smem_u32(&empty[v_at(iv)]));
+              continue;
             }
+            if ((q == 0 && !k_there(ik)) || !wait(&o_full[x], cnt[x] - 1, kSiteAttnSFree)) break;
+            if (last) mbar_arrive(smem_u32(&empty[v_at(iv)]));
+            issue_s(x, ik, x ? aQ1 : aQ0);
           }
-          it += more ? 2 : 1;
         }
+        it += nt;
       }
       tc_commit(smem_u32(drain));
       int never = 0;
