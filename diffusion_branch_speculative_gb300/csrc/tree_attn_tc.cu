@@ -60,14 +60,37 @@ struct Tc {
   static constexpr uint32_t COL_P = 64;
 };
 
-// D[tmem] (+)= A[tmem] * B[smem]^T: as tc_mma_f16, A's row r in lane r, two bf16
-// of consecutive k a column.
-SF_DEV void tc_mma_f16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+// The products and commits of a warp that runs as one, issued by the thread with
+// `me` set: with the whole warp converged the descriptors stay in uniform
+// registers (a single thread's branch moves each there first: 80 cycles a
+// product, above its 64 of execution).
+// D[tmem] (+)= A[smem] * B[smem]^T
+SF_DEV void warp_mma(bool me, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
   asm volatile(
-      "{\n\t.reg .pred p;\n\t"
+      "{\n\t.reg .pred p, q;\n\t"
       "setp.ne.b32 p, %4, 0;\n\t"
-      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(me))
+      : "memory");
+}
+// D[tmem] (+)= A[tmem] * B[smem]^T: A's row r in TMEM lane r, two bf16 of
+// consecutive k a column.
+SF_DEV void warp_mma_ta(bool me, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p, q;\n\t"
+      "setp.ne.b32 p, %4, 0;\n\t"
+      "setp.ne.b32 q, %5, 0;\n\t"
+      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
+      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(me))
+      : "memory");
+}
+SF_DEV void warp_commit(bool me, uint32_t bar) {
+  asm volatile(
+      "{\n\t.reg .pred q;\n\t"
+      "setp.ne.b32 q, %1, 0;\n\t"
+      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar),
+      "r"(static_cast<uint32_t>(me))
       : "memory");
 }
 // Store 16 consecutive 32-bit columns of this thread's TMEM lane.
@@ -151,7 +174,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
   uint64_t* drain = q_full + 10;
   volatile int* abort_flag = &abort_s;
 
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // lane 0's copy: the compiler then knows that a warp's role is one
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
     mbar_init(smem_u32(q_full), 2);  // the two loading warps
     mbar_init(smem_u32(q_empty), 2);
@@ -590,76 +614,83 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
     }
   } else if (warp == 2) {
     // ---------------------------------------------------------------- MMA --
-    if (lane == 0) {
-      constexpr uint32_t idS = idesc_bf16_f32(128, 128, false);
-      constexpr uint32_t idPV = idesc_bf16_f32(128, HD, true);
-      int it = 0, j = 0;
-      int cnt[2] = {0, 0};  // the lanes' P V products so far
-      bool ok = true;
-      auto wait = [&](uint64_t* bar, int parity, int site) {
-        ok = ok && mbar_wait(smem_u32(bar), parity & 1, abort_flag, p.status, kWaitLimitNs, site);
-        return ok;
-      };
-      auto v_at = [&](int i) { return C::KRING + i % C::VRING; };
-      auto k_there = [&](int i) { return wait(&full[i % C::KRING], i / C::KRING, kSiteAttnKvFull); };
-      // S = Q K^T of lane x with the keys of block i, once the lane's last P V
-      // has read P from S's place
-      auto issue_s = [&](int x, int i, uint32_t aQ) {
-        tc_fence_after();
-        const uint32_t aK = smem_u32(smem + C::OFF_RING + (i % C::KRING) * C::TILE);
+    // The whole warp runs this, lane 0 issues; values that all lanes have alike
+    // are taken from lane 0 where the compiler could not know it.
+    constexpr uint32_t idS = idesc_bf16_f32(128, 128, false);
+    constexpr uint32_t idPV = idesc_bf16_f32(128, HD, true);
+    const bool me = lane == 0;
+    int it = 0, j = 0;
+    int cnt0 = 0, cnt1 = 0;  // the lanes' P V products so far
+    bool ok = true;
+    auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    auto wait = [&](uint64_t* bar, int parity, int site) {
+      ok = __all_sync(0xffffffffu,
+                      ok && mbar_wait(smem_u32(bar), parity & 1, abort_flag, p.status, kWaitLimitNs, site));
+      return ok;
+    };
+    auto v_at = [&](int i) { return C::KRING + i % C::VRING; };
+    auto k_there = [&](int i) { return wait(&full[i % C::KRING], i / C::KRING, kSiteAttnKvFull); };
+    const uint32_t base = uniform(smem_u32(smem)), tm = uniform(tmem);
+    // S = Q K^T of lane x with the keys of block i, once the lane's last P V
+    // has read P from S's place
+    auto issue_s = [&](int x, int i, uint32_t aQ) {
+      tc_fence_after();
+      const uint32_t aK = base + C::OFF_RING + (i % C::KRING) * C::TILE;
 #pragma unroll
-        for (int kk = 0; kk < HD / 16; ++kk)
-          tc_mma_f16(tmem + x * 128, sdesc_sw128(aQ + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024),
-                     sdesc_sw128(aK + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024), idS, kk > 0 ? 1u : 0u);
-        tc_commit(smem_u32(&s_full[x]));
-      };
-      for (; w.left > 0 && ok; w.next(p), ++j) {
-        const int nt = w.blocks();
-        const bool pair = tree_tile_rows(p, w) > 128;
-        const int lead = pair ? 1 : 2;
-        const uint32_t aQ0 = smem_u32(smem), aQ1 = aQ0 + (pair ? C::Q_BYTES : 0);
-        if (!wait(q_full, j, kSiteAttnQFull)) break;
-        for (int x = 0; x < 2 && (pair || x < nt); ++x) {  // the lanes' first S
-          const int i = it + (pair ? 0 : x);
-          if (!k_there(i) || (cnt[x] > 0 && !wait(&o_full[x], cnt[x] - 1, kSiteAttnSFree))) break;
-          issue_s(x, i, x ? aQ1 : aQ0);
-        }
-        for (int t = 0; t < nt && ok; ++t) {
-          const int iv = it + t, ik = it + t + lead;
-          const bool more = t + lead < nt;
-          const int turns = pair ? 2 : 1;
-          if (!wait(&full[v_at(iv)], iv / C::VRING, kSiteAttnKvFull)) break;
-          for (int q = 0; q < turns; ++q) {
-            const int x = pair ? q : t & 1;
-            // the accumulator's first product of a unit overwrites it: the
-            // softmax warps have read the previous unit's outputs
-            const bool first = pair ? t == 0 : t < 2;
-            if (!wait(&p_full[x], cnt[x], kSiteAttnPFull)) break;
-            if (first && j > 0 && !wait(o_empty, j - 1, kSiteAttnOEmpty)) break;
-            tc_fence_after();
-            const uint32_t aV = smem_u32(smem + C::OFF_RING + v_at(iv) * C::TILE);
-            const uint32_t tO = tmem + C::COL_O + x * HD, tP = tmem + x * 128 + C::COL_P;
-#pragma unroll
-            for (int kk = 0; kk < 8; ++kk)
-              tc_mma_f16_ta(tO, tP + kk * 8, sdesc_sw128(aV + kk * 2048, kAtom, 1024), idPV, (!first || kk > 0) ? 1u : 0u);
-            tc_commit(smem_u32(&o_full[x]));
-            const bool last = q == turns - 1;
-            ++cnt[x];
-            if (!more) {
-              if (last) tc_commit(smem_u32(&empty[v_at(iv)]));
-              continue;
-            }
-            if ((q == 0 && !k_there(ik)) || !wait(&o_full[x], cnt[x] - 1, kSiteAttnSFree)) break;
-            if (last) mbar_arrive(smem_u32(&empty[v_at(iv)]));
-            issue_s(x, ik, x ? aQ1 : aQ0);
-          }
-        }
-        it += nt;
+      for (int kk = 0; kk < HD / 16; ++kk)
+        warp_mma(me, tm + x * 128, sdesc_sw128(aQ + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024),
+                 sdesc_sw128(aK + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024), idS, kk > 0 ? 1u : 0u);
+      warp_commit(me, smem_u32(&s_full[x]));
+    };
+    for (; uniform(w.left > 0) && ok; w.next(p), ++j) {
+      const int nt = uniform(w.blocks());
+      const bool pair = uniform(tree_tile_rows(p, w) > 128);
+      const int lead = pair ? 1 : 2;
+      const uint32_t aQ1 = base + (pair ? C::Q_BYTES : 0);
+      if (!wait(q_full, j, kSiteAttnQFull)) break;
+      for (int x = 0; x < 2 && (pair || x < nt); ++x) {  // the lanes' first S
+        const int i = it + (pair ? 0 : x), c = x ? cnt1 : cnt0;
+        if (!k_there(i) || (c > 0 && !wait(&o_full[x], c - 1, kSiteAttnSFree))) break;
+        issue_s(x, i, x ? aQ1 : base);
       }
-      tc_commit(smem_u32(drain));
-      int never = 0;
-      mbar_wait(smem_u32(drain), 0, &never, nullptr, 10000000ull);
+      for (int t = 0; t < nt && ok; ++t) {
+        const int iv = it + t, ik = it + t + lead;
+        const bool more = t + lead < nt;
+        const int turns = pair ? 2 : 1;
+        if (!wait(&full[v_at(iv)], iv / C::VRING, kSiteAttnKvFull)) break;
+        for (int q = 0; q < turns; ++q) {
+          const int x = pair ? q : t & 1, c = x ? cnt1 : cnt0;
+          // the accumulator's first product of a unit overwrites it: the
+          // softmax warps have read the previous unit's outputs
+          const bool first = pair ? t == 0 : t < 2;
+          if (!wait(&p_full[x], c, kSiteAttnPFull)) break;
+          if (first && j > 0 && !wait(o_empty, j - 1, kSiteAttnOEmpty)) break;
+          tc_fence_after();
+          const uint32_t aV = base + C::OFF_RING + v_at(iv) * C::TILE;
+          const uint32_t tO = tm + C::COL_O + x * HD, tP = tm + x * 128 + C::COL_P;
+#pragma unroll
+          for (int kk = 0; kk < 8; ++kk)
+            warp_mma_ta(me, tO, tP + kk * 8, sdesc_sw128(aV + kk * 2048, kAtom, 1024), idPV, (!first || kk > 0) ? 1u : 0u);
+          warp_commit(me, smem_u32(&o_full[x]));
+          const bool last = q == turns - 1;
+          if (x)
+            ++cnt1;
+          else
+            ++cnt0;
+          if (!more) {
+            if (last) warp_commit(me, smem_u32(&empty[v_at(iv)]));
+            continue;
+          }
+          if ((q == 0 && !k_there(ik)) || !wait(&o_full[x], c, kSiteAttnSFree)) break;
+          if (last && me) mbar_arrive(smem_u32(&empty[v_at(iv)]));
+          issue_s(x, ik, x ? aQ1 : base);
+        }
+      }
+      it += nt;
     }
+    warp_commit(me, smem_u32(drain));
+    int never = 0;
+    mbar_wait(smem_u32(drain), 0, &never, nullptr, 10000000ull);
     __syncwarp();
   }
 
