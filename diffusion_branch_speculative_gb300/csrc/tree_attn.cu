@@ -703,17 +703,17 @@ __global__ void __launch_bounds__(kCombineQuads * 32) tree_combine_quads_kernel(
 // --------------------------------------------------------------- launches --
 // A kernel's geometry: CTAs per SM, rows of a tile, keys of a block.
 struct Plan {
-  int ctas_per_sm, tile_rows, kb;
+  int ctas_per_sm, tile_rows, kb, unit_cost;
 };
 
 Plan plan_of(int dtype, int g, int hd, int max_nodes) {
   const int rows = max_nodes * g;
   if (dtype == SPECFOLD_BF16) {
-    if (rows > 32) return {1, kTreeTcRows, kTreeTcKeys};
+    if (rows > 32) return {1, kTreeTcRows, kTreeTcKeys, 3};
     const int rt = rows <= 16 ? 16 : 32;
-    return {hd == 128 ? Few<128, 1>::CTAS : Few<64, 1>::CTAS, rt, 4 * kChunk};
+    return {hd == 128 ? Few<128, 1>::CTAS : Few<64, 1>::CTAS, rt, 4 * kChunk, 2};
   }
-  return {1, 8, 4 * kChunk};
+  return {1, 8, 4 * kChunk, 1};
 }
 
 int tree_start(void (*kernel)(TreeArgs), int smem, const TreeArgs& a, int grid, cudaStream_t st) {
@@ -741,6 +741,7 @@ int tree_go(const TreeAttnCall& c, const Plan& pl, cudaStream_t st) {
   a.g = c.n_q / c.n_kv;
   a.tile_rows = pl.tile_rows;
   a.kb = pl.kb;
+  a.unit_cost = pl.unit_cost;
   a.sl2 = static_cast<float>(1.4426950408889634 * (c.scale > 0.f ? c.scale : 1.0 / std::sqrt(static_cast<double>(HD))));
   uint8_t* ws = static_cast<uint8_t*>(c.ws);
   a.status = reinterpret_cast<uint32_t*>(ws);

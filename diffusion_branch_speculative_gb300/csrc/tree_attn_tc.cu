@@ -150,6 +150,36 @@ SF_DEV uint64_t sees_window(const int32_t* par, int i, int e0, uint32_t* status)
   return bits;
 }
 
+// A tile's queries into the lanes' places, by THREADS threads (thread tid); rows
+// past the tile's become zeros.  Returns with this thread's part visible to the
+// tensor cores.
+template <int HD, int THREADS>
+SF_DEV void gather_queries(const TreeArgs& p, const TreeWalk& w, uint8_t* smem, int tid) {
+  constexpr int RSTEP = THREADS / (HD / 8);  // rows of one step; a row's node and head follow by steps
+  const int g = p.g, rows = tree_tile_rows(p, w), most = rows > 128 ? 256 : 128;
+  const int c = tid % (HD / 8), dn = RSTEP / g, dh = RSTEP % g, m = tree_m0(p, w) + tid / (HD / 8);
+  int hd = m % g;
+  const long long d_node = p.q_rs - g * p.q_hs, d_step = dn * p.q_rs + dh * p.q_hs;
+  const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (w.q.row0 + m / g) * p.q_rs +
+                             (w.head() * g + hd) * p.q_hs + c * 8;
+  const uint32_t q0 = smem_u32(smem) + (c >> 3) * kAtom;
+#pragma unroll 4
+  for (int r = tid / (HD / 8); r < most; r += RSTEP) {
+    const bool there = r < rows;
+    cp_async16(q0 + (r >> 7) * Tc<HD>::Q_BYTES + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
+               there ? src : static_cast<const __nv_bfloat16*>(p.q), there ? 16u : 0u);
+    src += d_step;
+    hd += dh;
+    if (hd >= g) {
+      hd -= g;
+      src += d_node;
+    }
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  fence_proxy_async_smem();
+}
+
 template <int HD>
 __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __grid_constant__ TcArgs ta) {
   using C = Tc<HD>;
@@ -177,7 +207,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
   // lane 0's copy: the compiler then knows that a warp's role is one
   const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
   if (threadIdx.x == 0) {
-    mbar_init(smem_u32(q_full), 2);  // the two loading warps
+    mbar_init(smem_u32(q_full), 2);  // the two loading warps, or the lanes' softmax
     mbar_init(smem_u32(q_empty), 2);
     for (int i = 0; i < C::RING; ++i) {
       mbar_init(smem_u32(&full[i]), 1);
@@ -233,36 +263,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
       const int h = w.head(), rows = tree_tile_rows(p, w), ctx = w.q.ctx, len = ctx + w.q.n;
       const int nt = w.blocks(), lead = rows > 128 ? 1 : 2;
       // queries, by both warps: the previous unit's S products must be done with
-      // their place
+      // their place (the first unit's come from the softmax warps, idle then)
       auto load_queries = [&]() {
-        const int qt = threadIdx.x;
-        bool free = true;
-        if (lane == 0 && j > 0)
-          free = mbar_wait(smem_u32(q_empty), (j - 1) & 1, abort_flag, p.status, kWaitLimitNs, kSiteAttnQEmpty);
+        if (j == 0) return true;
+        const bool free = lane == 0 ? mbar_wait(smem_u32(q_empty), (j - 1) & 1, abort_flag, p.status, kWaitLimitNs,
+                                                kSiteAttnQEmpty)
+                                    : true;
         if (!__shfl_sync(0xffffffffu, free, 0)) return false;
-        constexpr int RSTEP = 64 / (HD / 8);  // rows of one step; a row's node and head follow by steps
-        const int c = qt % (HD / 8), dn = RSTEP / g, dh = RSTEP % g, m = tree_m0(p, w) + qt / (HD / 8);
-        int hd = m % g;
-        const long long d_node = p.q_rs - g * p.q_hs, d_step = dn * p.q_rs + dh * p.q_hs;
-        const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (w.q.row0 + m / g) * p.q_rs +
-                                   (h * g + hd) * p.q_hs + c * 8;
-        const int most = lead == 1 ? 256 : 128;
-        const uint32_t q0 = smem_u32(smem) + (c >> 3) * kAtom;
-#pragma unroll 4
-        for (int r = qt / (HD / 8); r < most; r += RSTEP) {
-          const bool there = r < rows;
-          cp_async16(q0 + (r >> 7) * C::Q_BYTES + (r & 127) * 128 + (((c & 7) ^ (r & 7)) << 4),
-                     there ? src : static_cast<const __nv_bfloat16*>(p.q), there ? 16u : 0u);
-          src += d_step;
-          hd += dh;
-          if (hd >= g) {
-            hd -= g;
-            src += d_node;
-          }
-        }
-        cp_async_commit();
-        cp_async_wait<0>();
-        fence_proxy_async_smem();
+        gather_queries<HD, 64>(p, w, smem, threadIdx.x);
         __syncwarp();
         if (lane == 0) mbar_arrive(smem_u32(q_full));
         return true;
@@ -382,6 +390,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
     const int pair_bar = 2 + (warp & 3);  // named barrier of the two warps of these rows
     int cnt = 0, j = 0, it = 0;  // blocks of this lane so far
     const bool leader = (warp & 3) == 0 && lane == 0;
+    gather_queries<HD, 256>(p, w, smem, threadIdx.x - 128);
+    named_bar_sync(1, 256);
+    if (leader) mbar_arrive(smem_u32(q_full));
     bool ok = true;
     for (bool first = true; w.left > 0 && ok; first = false, w.next(p), ++j) {
       const int h = w.head(), ctx = w.q.ctx, nt = w.blocks(), rows = tree_tile_rows(p, w);

@@ -4,7 +4,10 @@
 // blocks of kb keys of that sequence.  All units' blocks in one line, sequence
 // by sequence, head by head, tile by tile, are cut into equal runs, one per CTA:
 // the lengths are known on the device only, and one rule serves a single long
-// sequence and a ragged batch of short ones.  A run's piece that covers its
+// sequence and a ragged batch of short ones.  Starting a unit costs a CTA as
+// much as some blocks (its queries, an output to write): a unit counts unit_cost
+// places more than its blocks, in front of them, so that a CTA that starts more
+// units gets fewer blocks.  A cut inside these places is one at the unit's start.  A run's piece that covers its
 // whole unit writes the output; any other writes an unnormalised partial (o,
 // running max m in log2 units, sum l), at most the run's first and last piece
 // (slots 2c and 2c + 1 of CTA c), which the combine kernel merges in order, so
@@ -26,6 +29,7 @@ struct TreeArgs {
   int max_nodes, n_kv, g;
   int tile_rows;  // query rows of a tile: row m is node m / g, head m % g of the group
   int kb;         // keys per block
+  int unit_cost;  // a unit's start, in blocks
   float sl2;               // scale * log2(e)
   uint32_t* status;
   int4* desc;              // [2 * grid]: the unit cut at CTA c's start, see tree_describe
@@ -38,7 +42,9 @@ struct TreeArgs {
 struct TreeSeq {
   int row0, n, ctx, nb, tiles;
   bool bad;
-  SF_DEV long long items(int n_kv) const { return static_cast<long long>(nb) * tiles * n_kv; }
+  SF_DEV long long items(const TreeArgs& p) const {  // its places in the line
+    return static_cast<long long>(nb + (n > 0 ? p.unit_cost : 0)) * tiles * p.n_kv;
+  }
 };
 
 // Weight of a partial with maximum m in a merge with maximum M: 1 where they
@@ -62,7 +68,8 @@ SF_DEV TreeSeq tree_seq(const TreeArgs& p, int s) {
 }
 
 // A CTA's walk along its run: the current unit u (head u / tiles, tile u %
-// tiles) of sequence s from block b0 on, `left` blocks to go.
+// tiles) of sequence s from block b0 on, `left` places to go (the unit's start
+// not counted when b0 > 0).
 struct TreeWalk {
   int s, u, b0;
   long long left;
@@ -74,19 +81,26 @@ struct TreeWalk {
     return static_cast<int>(rest < left ? rest : left);
   }
   SF_DEV bool whole() const { return b0 == 0 && blocks() == q.nb; }
+  // Enter the current unit at its start: its places are paid for, or, where the
+  // run ends among them, it is left to the next CTA.
+  SF_DEV void enter(const TreeArgs& p) {
+    b0 = 0;
+    left = left > p.unit_cost ? left - p.unit_cost : 0;
+  }
   SF_DEV void next(const TreeArgs& p) {
     left -= blocks();
-    b0 = 0;
-    if (++u < q.tiles * p.n_kv) return;
-    u = 0;
-    while (left > 0) {
-      if (++s >= p.batch.n_seqs) {  // lengths that changed under the call
-        left = 0;
-        break;
+    if (++u >= q.tiles * p.n_kv) {
+      u = 0;
+      while (left > 0) {
+        if (++s >= p.batch.n_seqs) {  // lengths that changed under the call
+          left = 0;
+          break;
+        }
+        q = tree_seq(p, s);
+        if (q.n > 0) break;
       }
-      q = tree_seq(p, s);
-      if (q.n > 0) break;
     }
+    enter(p);
   }
 };
 
@@ -120,12 +134,12 @@ SF_DEV bool tree_locate(const TreeArgs& p, TreeWalk& w, long long& lo, long long
   const int lane = threadIdx.x & 31, n = p.batch.n_seqs;
   TreeSeq q = tree_seq_or_none(p, lane);
   bool bad = q.bad;
-  long long inc = warp_prefix(q.items(p.n_kv), lane);
+  long long inc = warp_prefix(q.items(p), lane);
   long long total = __shfl_sync(0xffffffffu, inc, 31);
   for (int c = 32; c < n; c += 32) {
     const TreeSeq r = tree_seq_or_none(p, c + lane);
     bad = bad || r.bad;
-    total += __shfl_sync(0xffffffffu, warp_prefix(r.items(p.n_kv), lane), 31);
+    total += __shfl_sync(0xffffffffu, warp_prefix(r.items(p), lane), 31);
   }
   if (bad && blockIdx.x == 0 && threadIdx.x < 32) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
   per = div_ll(total + gridDim.x - 1, gridDim.x);
@@ -138,10 +152,10 @@ SF_DEV bool tree_locate(const TreeArgs& p, TreeWalk& w, long long& lo, long long
     base += __shfl_sync(0xffffffffu, inc, 31);
     c += 32;
     q = tree_seq_or_none(p, c + lane);
-    inc = warp_prefix(q.items(p.n_kv), lane);
+    inc = warp_prefix(q.items(p), lane);
   }
   const int src = __ffs(__ballot_sync(0xffffffffu, lo < base + inc)) - 1;
-  const long long off = lo - base - __shfl_sync(0xffffffffu, inc - q.items(p.n_kv), src);
+  const long long off = lo - base - __shfl_sync(0xffffffffu, inc - q.items(p), src);
   w.s = c + src;
   w.q.row0 = __shfl_sync(0xffffffffu, q.row0, src);
   w.q.n = __shfl_sync(0xffffffffu, q.n, src);
@@ -149,10 +163,17 @@ SF_DEV bool tree_locate(const TreeArgs& p, TreeWalk& w, long long& lo, long long
   w.q.nb = __shfl_sync(0xffffffffu, q.nb, src);
   w.q.tiles = __shfl_sync(0xffffffffu, q.tiles, src);
   w.q.bad = false;
-  w.u = static_cast<int>(div_ll(off, w.q.nb));
-  w.b0 = static_cast<int>(off - static_cast<long long>(w.u) * w.q.nb);
+  const int places = w.q.nb + p.unit_cost;
+  w.u = static_cast<int>(div_ll(off, places));
+  const int at = static_cast<int>(off - static_cast<long long>(w.u) * places);
   w.left = hi - lo;
-  return true;
+  if (at <= p.unit_cost) {  // at the unit's start
+    w.left += at;
+    w.enter(p);
+  } else {
+    w.b0 = at - p.unit_cost;
+  }
+  return w.left > 0;
 }
 
 // The partial slot of a run's piece.
@@ -171,12 +192,13 @@ SF_DEV void tree_describe(const TreeArgs& p, const TreeWalk& w, bool work, long 
   const int c = blockIdx.x;
   int4 a = make_int4(0, 0, 0, 0);
   if (work && w.b0 > 0) {
-    const long long beg = lo - w.b0, end = beg + w.q.nb;
-    if (beg >= lo - per) {
+    // the unit's places are [beg, end), its first block's place beg + unit_cost
+    const long long beg = lo - w.b0 - p.unit_cost, end = beg + p.unit_cost + w.q.nb, before = lo - per;
+    if (beg + p.unit_cost >= before) {  // CTA c - 1 has the first block
       a = make_int4(tree_tile_rows(p, w), w.q.row0, tree_m0(p, w), w.head());
       // per < 2^32: a run of more 64-key blocks than that is no cache's
       p.desc[2 * c + 1] = make_int4(c - 1, static_cast<int>(div_ll(end - 1, static_cast<unsigned>(per))),
-                                    2 * (c - 1) + (beg == lo - per ? 0 : 1), 0);
+                                    2 * (c - 1) + (beg <= before ? 0 : 1), 0);
     }
   }
   p.desc[2 * c] = a;
