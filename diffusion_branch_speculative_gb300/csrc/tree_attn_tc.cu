@@ -333,28 +333,33 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
           const bool there = mbar_wait(smem_u32(landed), fixes & 1, abort_flag, p.status, kWaitLimitNs, kSiteAttnKvFull);
           ++fixes;
           const long long t0 = static_cast<long long>(w.b0 + t) * kTreeTcKeys;
-          const int r0 = t0 >= ctx ? 0 : static_cast<int>(ctx - t0);  // the tree's first row of the tile
+          // rows of the tile: the tree's from r0 on, past the end from r1 on
+          const int r0 = t0 >= ctx ? 0 : static_cast<int>(ctx - t0);
+          const int r1 = len - t0 >= 128 ? 128 : static_cast<int>(len - t0);
+          constexpr int RSTEP = 32 / (HD / 8);
+          const int c = lane % (HD / 8), rl = lane / (HD / 8);
+          uint8_t* col = tile + (c >> 3) * kAtom;
+          auto piece = [&](int r) { return reinterpret_cast<uint4*>(col + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
           if (there) {
-#pragma unroll 1
-            for (int k = r0 * (HD / 8) + lane; k < 128 * (HD / 8); k += 32) {
-              const int kr = k / (HD / 8), c = k % (HD / 8);
-              const int e = static_cast<int>(t0 + kr - ctx);
-              uint4* v = reinterpret_cast<uint4*>(tile + (c >> 3) * kAtom + kr * 128 + (((c & 7) ^ (kr & 7)) << 4));
-              const uint4 u = *v;
-              uint32_t y[4] = {u.x, u.y, u.z, u.w};
-              bool change = false;
-              if (e >= w.q.n) {
-                change = (u.x | u.y | u.z | u.w) != 0u;
-                y[0] = y[1] = y[2] = y[3] = 0u;
-              } else {
+            for (int r = r1 + rl; r < 128; r += RSTEP) *piece(r) = make_uint4(0u, 0u, 0u, 0u);
+#pragma unroll 8
+            for (int r = r0 + rl; r < r1; r += RSTEP) {
+              const uint4 u = *piece(r);
+              // an exponent of ones carries into the place above it
+              const uint32_t not_finite = (((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
+                                           ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u)) &
+                                          0x80008000u;
+              if (not_finite) {
+                uint32_t y[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                  if ((y[q] & 0x7f80u) == 0x7f80u) y[q] &= 0xffff0000u, change = true;
-                  if ((y[q] & 0x7f800000u) == 0x7f800000u) y[q] &= 0xffffu, change = true;
+                  if ((y[q] & 0x7f80u) == 0x7f80u) y[q] &= 0xffff0000u;
+                  if ((y[q] & 0x7f800000u) == 0x7f800000u) y[q] &= 0xffffu;
                 }
-                if (change) atomicOr(&odd[j % kOddBufs][e >> 5], 1u << (e & 31));
+                *piece(r) = make_uint4(y[0], y[1], y[2], y[3]);
+                const int e = static_cast<int>(t0 - ctx) + r;
+                atomicOr(&odd[j % kOddBufs][e >> 5], 1u << (e & 31));
               }
-              if (change) *v = make_uint4(y[0], y[1], y[2], y[3]);
             }
           }
           fence_proxy_async_smem();
@@ -639,6 +644,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
                       ok && mbar_wait(smem_u32(bar), parity & 1, abort_flag, p.status, kWaitLimitNs, site));
       return ok;
     };
+    // two waits, both asked at once (each takes a good hundred cycles)
+    auto wait2 = [&](uint64_t* a, int pa, int sa, uint64_t* b, int pb, int sb) {
+      const bool ra = mbar_try_wait(smem_u32(a), pa & 1), rb = mbar_try_wait(smem_u32(b), pb & 1);
+      if (__all_sync(0xffffffffu, ra && rb && ok)) return true;
+      return wait(a, pa, sa) && wait(b, pb, sb);
+    };
     auto v_at = [&](int i) { return C::KRING + i % C::VRING; };
     auto k_there = [&](int i) { return wait(&full[i % C::KRING], i / C::KRING, kSiteAttnKvFull); };
     const uint32_t base = uniform(smem_u32(smem)), tm = uniform(tmem);
@@ -664,38 +675,41 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
         if (!k_there(i) || (c > 0 && !wait(&o_full[x], c - 1, kSiteAttnSFree))) break;
         issue_s(x, i, x ? aQ1 : base);
       }
+      // P V of lane x's next block with the values of block i; first: the unit's
+      // first, which overwrites O (read by then, see its wait)
+      auto issue_pv = [&](int x, int i, bool first) {
+        if (first && j > 0 && !wait(o_empty, j - 1, kSiteAttnOEmpty)) return;
+        tc_fence_after();
+        const uint32_t aV = base + C::OFF_RING + v_at(i) * C::TILE;
+#pragma unroll
+        for (int kk = 0; kk < 8; ++kk)
+          warp_mma_ta(me, tm + C::COL_O + x * HD, tm + x * 128 + C::COL_P + kk * 8, sdesc_sw128(aV + kk * 2048, kAtom, 1024),
+                      idPV, (!first || kk > 0) ? 1u : 0u);
+        warp_commit(me, smem_u32(&o_full[x]));
+      };
       for (int t = 0; t < nt && ok; ++t) {
         const int iv = it + t, ik = it + t + lead;
         const bool more = t + lead < nt;
-        const int turns = pair ? 2 : 1;
-        if (!wait(&full[v_at(iv)], iv / C::VRING, kSiteAttnKvFull)) break;
-        for (int q = 0; q < turns; ++q) {
-          const int x = pair ? q : t & 1, c = x ? cnt1 : cnt0;
-          // the accumulator's first product of a unit overwrites it: the
-          // softmax warps have read the previous unit's outputs
-          const bool first = pair ? t == 0 : t < 2;
-          if (!wait(&p_full[x], c, kSiteAttnPFull)) break;
-          if (first && j > 0 && !wait(o_empty, j - 1, kSiteAttnOEmpty)) break;
-          tc_fence_after();
-          const uint32_t aV = base + C::OFF_RING + v_at(iv) * C::TILE;
-          const uint32_t tO = tm + C::COL_O + x * HD, tP = tm + x * 128 + C::COL_P;
-#pragma unroll
-          for (int kk = 0; kk < 8; ++kk)
-            warp_mma_ta(me, tO, tP + kk * 8, sdesc_sw128(aV + kk * 2048, kAtom, 1024), idPV, (!first || kk > 0) ? 1u : 0u);
-          warp_commit(me, smem_u32(&o_full[x]));
-          const bool last = q == turns - 1;
-          if (x)
-            ++cnt1;
-          else
-            ++cnt0;
-          if (!more) {
-            if (last) warp_commit(me, smem_u32(&empty[v_at(iv)]));
-            continue;
-          }
-          if ((q == 0 && !k_there(ik)) || !wait(&o_full[x], c, kSiteAttnSFree)) break;
-          if (last && me) mbar_arrive(smem_u32(&empty[v_at(iv)]));
+        uint64_t *vf = &full[v_at(iv)], *kf = &full[ik % C::KRING], *ve = &empty[v_at(iv)];
+        // lane 0, or the only lane of this block
+        const int x = pair ? 0 : t & 1;
+        if (!wait2(vf, iv / C::VRING, kSiteAttnKvFull, &p_full[x], x ? cnt1 : cnt0, kSiteAttnPFull)) break;
+        issue_pv(x, iv, pair ? t == 0 : t < 2);
+        x ? ++cnt1 : ++cnt0;
+        if (more && wait2(kf, ik / C::KRING, kSiteAttnKvFull, &o_full[x], (x ? cnt1 : cnt0) - 1, kSiteAttnSFree)) {
+          if (!pair && me) mbar_arrive(smem_u32(ve));  // the values are done with
           issue_s(x, ik, x ? aQ1 : base);
         }
+        if (pair && ok) {  // lane 1
+          if (!wait(&p_full[1], cnt1, kSiteAttnPFull)) break;
+          issue_pv(1, iv, t == 0);
+          ++cnt1;
+          if (more && wait(&o_full[1], cnt1 - 1, kSiteAttnSFree)) {
+            if (me) mbar_arrive(smem_u32(ve));
+            issue_s(1, ik, aQ1);
+          }
+        }
+        if (!more) warp_commit(me, smem_u32(ve));
       }
       it += nt;
     }
