@@ -126,17 +126,26 @@ SF_DEV float max3(float a, float b, float c) {
   return d;
 }
 
-// The ancestors (and itself) of node i among nodes [e0, e0 + 64), as bits, for
+// Which of the 128 tokens e0, e0 + 1, ... behind the cached ones (negative: still
+// cached) node i sees, as bits: the cached ones, itself and its ancestors.  For
 // a node that is no padding row.  par: the sequence's parents, null: a chain.
-SF_DEV uint64_t sees_window(const int32_t* par, int i, int e0, uint32_t* status) {
+SF_DEV void sees_window(const int32_t* par, int i, int e0, uint32_t* status, uint64_t (&bits)[2]) {
+  // tokens [0, n) of the window
+  auto below = [](int n) { return n <= 0 ? 0ull : n >= 64 ? ~0ull : (1ull << n) - 1ull; };
   if (!par) {
-    const int hi = min(i - e0, 63);
-    return hi < 0 ? 0ull : (~0ull >> (63 - hi)) & (e0 < 0 ? ~0ull << min(-e0, 63) : ~0ull);
+    bits[0] = below(i + 1 - e0);
+    bits[1] = below(i + 1 - e0 - 64);
+    return;
   }
-  uint64_t bits = 0ull;
+  bits[0] = below(-e0);
+  bits[1] = below(-e0 - 64);
   int a = i, up = par[i];
   while (a >= e0) {
-    if (a < e0 + 64) bits |= 1ull << (a - e0);
+    const int at = a - e0;
+    if (at < 64)
+      bits[0] |= 1ull << at;
+    else if (at < 128)
+      bits[1] |= 1ull << (at - 64);
     if (up == -1) break;
     int above = SPECFOLD_TREE_PAD;
     if (up >= 0 && up < a) above = par[up];
@@ -147,7 +156,6 @@ SF_DEV uint64_t sees_window(const int32_t* par, int i, int e0, uint32_t* status)
     a = up;
     up = above;
   }
-  return bits;
 }
 
 // A tile's queries into the lanes' places, by THREADS threads (thread tid); rows
@@ -342,24 +350,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
           auto piece = [&](int r) { return reinterpret_cast<uint4*>(col + r * 128 + (((c & 7) ^ (r & 7)) << 4)); };
           if (there) {
             for (int r = r1 + rl; r < 128; r += RSTEP) *piece(r) = make_uint4(0u, 0u, 0u, 0u);
-#pragma unroll 8
-            for (int r = r0 + rl; r < r1; r += RSTEP) {
-              const uint4 u = *piece(r);
-              // an exponent of ones carries into the place above it
-              const uint32_t not_finite = (((u.x & 0x7f807f80u) + 0x00800080u) | ((u.y & 0x7f807f80u) + 0x00800080u) |
-                                           ((u.z & 0x7f807f80u) + 0x00800080u) | ((u.w & 0x7f807f80u) + 0x00800080u)) &
-                                          0x80008000u;
-              if (not_finite) {
-                uint32_t y[4] = {u.x, u.y, u.z, u.w};
+            // an exponent of ones carries into the place above it
+            auto odd_of = [](uint32_t v) { return ((v & 0x7f807f80u) + 0x00800080u) & 0x80008000u; };
+            for (int rb = r0; rb < r1; rb += 8 * RSTEP) {
+              uint4 u[8];  // all read before any is looked at
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                  if ((y[q] & 0x7f80u) == 0x7f80u) y[q] &= 0xffff0000u;
-                  if ((y[q] & 0x7f800000u) == 0x7f800000u) y[q] &= 0xffffu;
+              for (int k = 0; k < 8; ++k) u[k] = *piece(min(rb + rl + k * RSTEP, r1 - 1));
+              uint32_t any = 0u;
+#pragma unroll
+              for (int k = 0; k < 8; ++k) any |= odd_of(u[k].x) | odd_of(u[k].y) | odd_of(u[k].z) | odd_of(u[k].w);
+              if (any) {
+#pragma unroll 1
+                for (int r = rb + rl; r < min(rb + 8 * RSTEP, r1); r += RSTEP) {
+                  const uint4 v = *piece(r);
+                  uint32_t y[4] = {v.x, v.y, v.z, v.w};
+                  if (!(odd_of(v.x) | odd_of(v.y) | odd_of(v.z) | odd_of(v.w))) continue;
+#pragma unroll
+                  for (int q = 0; q < 4; ++q) {
+                    if ((y[q] & 0x7f80u) == 0x7f80u) y[q] &= 0xffff0000u;
+                    if ((y[q] & 0x7f800000u) == 0x7f800000u) y[q] &= 0xffffu;
+                  }
+                  *piece(r) = make_uint4(y[0], y[1], y[2], y[3]);
+                  const int e = static_cast<int>(t0 - ctx) + r;
+                  atomicOr(&odd[j % kOddBufs][e >> 5], 1u << (e & 31));
                 }
-                *piece(r) = make_uint4(y[0], y[1], y[2], y[3]);
-                const int e = static_cast<int>(t0 - ctx) + r;
-                atomicOr(&odd[j % kOddBufs][e >> 5], 1u << (e & 31));
               }
+              __syncwarp();
             }
           }
           fence_proxy_async_smem();
@@ -414,20 +430,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
       for (int t = pair ? 0 : x; t < nt; t += t_step, ++cnt) {
         const int key0 = (w.b0 + t) * kTreeTcKeys;
         const bool allv = key0 + kTreeTcKeys <= ctx;
-        // what the row sees of these keys: cached tokens, its ancestors
-        uint64_t km[2] = {~0ull, ~0ull};
-        if (!allv) {
-#pragma unroll
-          for (int q = 0; q < 2; ++q) {
-            const int e0 = key0 + 64 * q - ctx;
-            if (dead) {
-              km[q] = 0ull;
-            } else if (e0 > -64) {
-              km[q] = sees_window(par, node, e0, p.status);
-              if (e0 < 0) km[q] |= (1ull << -e0) - 1ull;
-            }
-          }
-        }
+        uint64_t km[2] = {0ull, 0ull};  // what the row sees of these keys, where not all
+        if (!allv && !dead) sees_window(par, node, key0 - ctx, p.status, km);
         // every wait's outcome is made warp-uniform: a lane whose wait ran out
         // takes its whole warp along
         if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[x]), cnt & 1, abort_flag, p.status, kWaitLimitNs,
@@ -588,7 +592,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
           for (int i = 0; i <= node; ++i) {
             const int tok = ctx + i;
             if (!(odd[j % kOddBufs][i >> 5] >> (i & 31) & 1u)) continue;
-            if (!(sees_window(par, node, i, p.status) & 1ull)) continue;
+            uint64_t seen[2];
+            sees_window(par, node, i, p.status, seen);
+            if (!(seen[0] & 1ull)) continue;
             const int at = tree_pool_token(p, w.s, tok);
             if (at < 0) continue;
             const __nv_bfloat16* v = static_cast<const __nv_bfloat16*>(p.cache.v) + at * p.cache.v_token_stride +
