@@ -347,39 +347,56 @@ class PagedCache:
         self.ref = ctypes.byref(self.struct)
 
 
-def _head_rows(t: torch.Tensor, heads: int, hd: int, like: torch.Tensor, what: str) -> specfold_head_rows:
-    if t.dim() != 3 or t.shape[1] != heads or t.shape[2] != hd or t.stride(2) != 1:
-        raise ValueError(f"{what} must be [rows, {heads}, {hd}] with unit last stride")
-    if t.dtype != like.dtype or t.device != like.device:
+# These calls are short next to a Python call's own cost, so their checks read
+# each property of a tensor once and the stream comes as its raw handle.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_NO_ROWS = specfold_head_rows(None, 0, 0)
+
+
+def _head_rows(t: torch.Tensor, rows: int, heads: int, hd: int, dtype, dev: int, what: str) -> specfold_head_rows:
+    s0, s1, s2 = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if s2 != 1 or t.shape != (rows, heads, hd):
+        raise ValueError(f"{what} must be [{rows}, {heads}, {hd}], the same rows as its peers, with unit last stride")
+    if t.dtype is not dtype or t.get_device() != dev:
         raise ValueError(f"{what} must have the dtype and device of the other tensors")
-    return specfold_head_rows(t.data_ptr(), t.stride(0), t.stride(1))
+    return specfold_head_rows(t.data_ptr(), s0, s1)
 
 
-def _vec(t: Optional[torch.Tensor], n: int, dtype: torch.dtype, like: torch.Tensor, what: str):
+def _vec(t: Optional[torch.Tensor], n: int, dtype, dev: int, what: str):
     """Pointer of a contiguous vector of at least n entries (None: NULL)."""
     if t is None:
         return None
-    if t.dim() != 1 or t.dtype != dtype or t.device != like.device or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
+    if t.dim() != 1 or t.dtype is not dtype or t.get_device() != dev or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
         raise ValueError(f"{what} must be a contiguous {dtype} vector of {n} entries on the same device")
     return t.data_ptr()
 
 
-class _on_device:
-    """Makes the tensors' device current for a call (a no-op where it is)."""
+def _device_of(t: torch.Tensor) -> int:
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError("the operators take CUDA tensors")
+    return dev
 
-    def __init__(self, t: torch.Tensor):
-        if not t.is_cuda:
-            raise ValueError("the operators take CUDA tensors")
-        self.dev = t.device.index
 
-    def __enter__(self):
-        self.prev = torch.cuda.current_device()
-        if self.prev != self.dev:
-            torch.cuda.set_device(self.dev)
-
-    def __exit__(self, *exc):
-        if self.prev != self.dev:
-            torch.cuda.set_device(self.prev)
+def _call(fn, what: str, dev: int, stream, *args):
+    """fn(*args, stream) with the tensors' device current: on `stream`, or on
+    that device's current stream."""
+    here = torch.cuda.current_device()
+    if here != dev:
+        torch.cuda.set_device(dev)
+    try:
+        if stream is not None:
+            raw = stream.cuda_stream
+        elif _raw_stream is not None:
+            raw = _raw_stream(dev)
+        else:
+            raw = torch.cuda.current_stream(dev).cuda_stream
+        rc = fn(*args, raw)
+    finally:
+        if here != dev:
+            torch.cuda.set_device(here)
+    if rc != OK:
+        raise SpecfoldError(rc, what)
 
 
 def specfold_qk_norm_rope(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], Q_out: Optional[torch.Tensor],
@@ -393,26 +410,25 @@ def specfold_qk_norm_rope(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], 
     like = Q if Q is not None else K
     if like is None:
         raise ValueError("Q or K must be given")
-    T, _, hd = like.shape
-    none = specfold_head_rows(None, 0, 0)
-    n_q = n_kv = 0
-    q = qo = k = ko = none
+    T, n_q, hd = like.shape
+    n_kv = 0
+    dtype, dev = like.dtype, like.get_device()
+    q = qo = k = ko = _NO_ROWS
     if Q is not None:
-        n_q = Q.shape[1]
-        q, qo = _head_rows(Q, n_q, hd, like, "Q"), _head_rows(Q_out, n_q, hd, like, "Q_out")
+        q = _head_rows(Q, T, n_q, hd, dtype, dev, "Q")
+        qo = _head_rows(Q_out, T, n_q, hd, dtype, dev, "Q_out")
+    else:
+        n_q = 0
     if K is not None:
         n_kv = K.shape[1]
-        k, ko = _head_rows(K, n_kv, hd, like, "K"), _head_rows(K_out, n_kv, hd, like, "K_out")
-    for t in (Q, K, Q_out, K_out):
-        if t is not None and t.shape[0] != T:
-            raise ValueError("Q, K and their outputs have the same rows")
+        k = _head_rows(K, T, n_kv, hd, dtype, dev, "K")
+        ko = _head_rows(K_out, T, n_kv, hd, dtype, dev, "K_out")
     if rope_theta and positions is None:
         raise ValueError("a rotation needs positions")
-    with _on_device(like):
-        _check(lib().specfold_qk_norm_rope(dtype_code(like.dtype), T, n_q, n_kv, hd, q, k, qo, ko,
-                                           _vec(gq, hd, like.dtype, like, "gq"), _vec(gk, hd, like.dtype, like, "gk"),
-                                           eps, _vec(positions, T, torch.int32, like, "positions"), rope_theta,
-                                           _stream(stream)), "specfold_qk_norm_rope")
+    _device_of(like)
+    _call(lib().specfold_qk_norm_rope, "specfold_qk_norm_rope", dev, stream, dtype_code(dtype), T, n_q, n_kv, hd, q, k,
+          qo, ko, _vec(gq, hd, dtype, dev, "gq"), _vec(gk, hd, dtype, dev, "gk"), eps,
+          _vec(positions, T, torch.int32, dev, "positions"), rope_theta)
 
 
 def specfold_kv_append(K: torch.Tensor, V: torch.Tensor, cache: PagedCache, row_start: torch.Tensor,
@@ -425,23 +441,19 @@ def specfold_kv_append(K: torch.Tensor, V: torch.Tensor, cache: PagedCache, row_
     rows, one per batch row; `positions` (int32, per batch row) defaults to
     the tokens' own indices.  `status`: an optional int32/uint32 word for the
     device status bits (read it with specfold_get_status)."""
-    n_seqs = ctx_len.shape[0]
-    T = K.shape[0] if rows is None else rows.shape[0]
-    if V.shape[0] != K.shape[0] or n_seqs > cache.n_seqs:
-        raise ValueError("K and V have the same rows, the cache a table for every sequence")
-    if status is not None and (status.element_size() != 4 or status.device != K.device):
+    n_seqs, n_src = ctx_len.shape[0], K.shape[0]
+    T = n_src if rows is None else rows.shape[0]
+    if n_seqs > cache.n_seqs:
+        raise ValueError("the cache has a table for every sequence")
+    dtype, dev, n_kv, hd = cache.dtype, cache.device.index, cache.n_kv, cache.head_dim
+    if status is not None and (status.element_size() != 4 or status.get_device() != dev):
         raise ValueError("status is one 32-bit word on the same device")
-    k = _head_rows(K, cache.n_kv, cache.head_dim, cache.k_pool, "K")
-    v = _head_rows(V, cache.n_kv, cache.head_dim, cache.k_pool, "V")
-    with _on_device(K):
-        _check(lib().specfold_kv_append(dtype_code(K.dtype), T, cache.n_kv, cache.head_dim, k, v, K.shape[0],
-                                        _vec(rows, T, torch.int32, K, "rows"),
-                                        _vec(gk, cache.head_dim, K.dtype, K, "gk"), eps,
-                                        _vec(positions, T, torch.int32, K, "positions"), rope_theta, cache.ref,
-                                        _vec(row_start, n_seqs + 1, torch.int32, K, "row_start"),
-                                        _vec(ctx_len, n_seqs, torch.int32, K, "ctx_len"), n_seqs,
-                                        None if status is None else status.data_ptr(), _stream(stream)),
-               "specfold_kv_append")
+    _call(lib().specfold_kv_append, "specfold_kv_append", dev, stream, dtype_code(dtype), T, n_kv, hd,
+          _head_rows(K, n_src, n_kv, hd, dtype, dev, "K"), _head_rows(V, n_src, n_kv, hd, dtype, dev, "V"), n_src,
+          _vec(rows, T, torch.int32, dev, "rows"), _vec(gk, hd, dtype, dev, "gk"), eps,
+          _vec(positions, T, torch.int32, dev, "positions"), rope_theta, cache.ref,
+          _vec(row_start, n_seqs + 1, torch.int32, dev, "row_start"), _vec(ctx_len, n_seqs, torch.int32, dev, "ctx_len"),
+          n_seqs, None if status is None else status.data_ptr())
 
 
 def tree_attention_workspace_size(dtype: int, n_q: int, n_kv: int, hd: int, max_nodes: int) -> int:
@@ -458,18 +470,16 @@ def specfold_tree_attention(Q: torch.Tensor, cache: PagedCache, parent: Optional
     least every sequence's rows; ws: tree_attention_workspace_size bytes."""
     T, n_q, hd = Q.shape
     n_seqs = ctx_len.shape[0]
-    if hd != cache.head_dim or O.shape[0] != T or n_seqs > cache.n_seqs:
-        raise ValueError("Q and O have the same rows and the cache's head size, the cache a table for every sequence")
-    if ws.device != Q.device or ws.element_size() != 1 or ws.stride(0) != 1:
+    if hd != cache.head_dim or n_seqs > cache.n_seqs:
+        raise ValueError("Q has the cache's head size, the cache a table for every sequence")
+    dtype, dev = cache.dtype, cache.device.index
+    if ws.get_device() != dev or ws.element_size() != 1 or ws.stride(0) != 1:
         raise ValueError("ws is a byte workspace on the same device")
-    q = _head_rows(Q, n_q, hd, cache.k_pool, "Q")
-    o = _head_rows(O, n_q, hd, cache.k_pool, "O")
-    with _on_device(Q):
-        _check(lib().specfold_tree_attention(dtype_code(Q.dtype), T, max_nodes, n_q, cache.n_kv, hd, q, cache.ref,
-                                             _vec(parent, T, torch.int32, Q, "parent"),
-                                             _vec(row_start, n_seqs + 1, torch.int32, Q, "row_start"),
-                                             _vec(ctx_len, n_seqs, torch.int32, Q, "ctx_len"), n_seqs, scale, o,
-                                             ws.data_ptr(), ws.numel(), _stream(stream)), "specfold_tree_attention")
+    _call(lib().specfold_tree_attention, "specfold_tree_attention", dev, stream, dtype_code(dtype), T, max_nodes, n_q,
+          cache.n_kv, hd, _head_rows(Q, T, n_q, hd, dtype, dev, "Q"), cache.ref,
+          _vec(parent, T, torch.int32, dev, "parent"), _vec(row_start, n_seqs + 1, torch.int32, dev, "row_start"),
+          _vec(ctx_len, n_seqs, torch.int32, dev, "ctx_len"), n_seqs, scale,
+          _head_rows(O, T, n_q, hd, dtype, dev, "O"), ws.data_ptr(), ws.numel())
 
 
 def stack_workspace_size(dims: specfold_dims, B: int, L: int) -> int:
