@@ -26,15 +26,36 @@ namespace {
 
 constexpr int kThreads = 256;
 
-SF_DEV void load8(const __nv_bfloat16* p, float (&x)[8]) {
-  const uint4 u = *reinterpret_cast<const uint4*>(p);
-  x[0] = bf16lo(u.x); x[1] = bf16hi(u.x); x[2] = bf16lo(u.y); x[3] = bf16hi(u.y);
-  x[4] = bf16lo(u.z); x[5] = bf16hi(u.z); x[6] = bf16lo(u.w); x[7] = bf16hi(u.w);
-}
-SF_DEV void load8(const float* p, float (&x)[8]) {
-  const float4 a = reinterpret_cast<const float4*>(p)[0], b = reinterpret_cast<const float4*>(p)[1];
-  x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
-}
+// A lane's two runs of eight elements as they lie in memory: what a warp has in
+// flight while it works on the group of heads before.
+template <typename T>
+struct Raw;
+template <>
+struct Raw<__nv_bfloat16> {
+  uint4 u[2];
+  SF_DEV void read(const __nv_bfloat16* p, int half) {
+    u[0] = *reinterpret_cast<const uint4*>(p);
+    u[1] = *reinterpret_cast<const uint4*>(p + half);
+  }
+  SF_DEV void unpack(int i, float (&x)[8]) const {
+    x[0] = bf16lo(u[i].x); x[1] = bf16hi(u[i].x); x[2] = bf16lo(u[i].y); x[3] = bf16hi(u[i].y);
+    x[4] = bf16lo(u[i].z); x[5] = bf16hi(u[i].z); x[6] = bf16lo(u[i].w); x[7] = bf16hi(u[i].w);
+  }
+};
+template <>
+struct Raw<float> {
+  float4 u[4];
+  SF_DEV void read(const float* p, int half) {
+    u[0] = reinterpret_cast<const float4*>(p)[0];
+    u[1] = reinterpret_cast<const float4*>(p)[1];
+    u[2] = reinterpret_cast<const float4*>(p + half)[0];
+    u[3] = reinterpret_cast<const float4*>(p + half)[1];
+  }
+  SF_DEV void unpack(int i, float (&x)[8]) const {
+    const float4 a = u[2 * i], b = u[2 * i + 1];
+    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  }
+};
 SF_DEV void store8(__nv_bfloat16* p, const float (&y)[8]) {
   *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
                                             pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
@@ -77,23 +98,26 @@ SF_DEV void lane_angles(const uint64_t* s_f, long long pos, int lane, int c, flo
   }
 }
 
-// One head's row in registers: norm with the gain (two runs of eight at g,
-// g + HD/2; null: none), then the rotation.
+// One head's row in registers (two runs of eight, from 8c and HD/2 + 8c on): the
+// norm with the gain g where `normed`, then the rotation.  Every lane of the
+// warp takes part in the sum.
 template <int HD>
-SF_DEV void norm_rotate(float (&a)[8], float (&b)[8], const float* g, float eps, bool rope, const float (&cs)[8],
-                        const float (&sn)[8]) {
-  if (g) {
+SF_DEV void norm_rotate(float (&a)[8], float (&b)[8], bool any_norm, bool normed, const float* g, float eps, bool rope,
+                        const float (&cs)[8], const float (&sn)[8]) {
+  if (any_norm) {
     float ss = 0.f;
 #pragma unroll
     for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
 #pragma unroll
     for (int o = HD / 32; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    // a square root and a division, as the formula has them: one per row and lane
-    const float inv = 1.f / sqrtf(ss * (1.f / HD) + eps);
+    if (normed) {
+      // a square root and a division, as the formula has them: one per row and lane
+      const float inv = 1.f / sqrtf(ss * (1.f / HD) + eps);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      a[e] = a[e] * inv * g[e];
-      b[e] = b[e] * inv * g[HD / 2 + e];
+      for (int e = 0; e < 8; ++e) {
+        a[e] = a[e] * inv * g[e];
+        b[e] = b[e] * inv * g[HD / 2 + e];
+      }
     }
   }
   if (rope) {
@@ -131,7 +155,7 @@ struct QkArgs {
 // Work item: row t, one of `parts` shares of its heads (a few rows alone
 // would leave most SMs idle), one warp each.
 template <typename T, int HD>
-__global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_constant__ QkArgs<T> p) {
+__global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const __grid_constant__ QkArgs<T> p) {
   constexpr int LPR = HD / 16, RPW = 32 / LPR;
   __shared__ uint64_t s_f[HD / 2];
   __shared__ float s_g[2][HD];
@@ -149,42 +173,32 @@ __global__ void __launch_bounds__(kThreads) qk_norm_rope_kernel(const __grid_con
   const long long step = static_cast<long long>(gridDim.x) * (kThreads / 32);
   for (long long it = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
     const int t = static_cast<int>(it / p.parts);
+    const int first = static_cast<int>(it - static_cast<long long>(t) * p.parts);
+    auto read = [&](int u, Raw<T>& x) {
+      const int hh = u * RPW + sub;
+      if (u < units && hh < heads) {
+        const Rows<T>& in = hh < p.n_q ? p.q_in : p.k_in;
+        x.read(in.p + t * in.rs + (hh < p.n_q ? hh : hh - p.n_q) * in.hs + 8 * c, HD / 2);
+      }
+    };
+    Raw<T> next = {};
+    read(first, next);
     float cs[8], sn[8];
     if (p.rope) lane_angles<HD>(s_f, p.positions[t], lane, c, cs, sn);
-    for (int u = static_cast<int>(it - static_cast<long long>(t) * p.parts); u < units; u += p.parts) {
+    for (int u = first; u < units; u += p.parts) {
       const int hh = u * RPW + sub;
-      const bool live = hh < heads, is_q = hh < p.n_q;
-      const int h = is_q ? hh : hh - p.n_q;
-      float a[8] = {}, b[8] = {};
-      if (live) {
-        const Rows<T>& in = is_q ? p.q_in : p.k_in;
-        const T* x = in.p + t * in.rs + h * in.hs + 8 * c;
-        load8(x, a);
-        load8(x + HD / 2, b);
-      }
-      // a warp may hold query and key heads at once, of which one side alone
-      // is normed: the norm's shuffles stay within a head's lanes
-      const bool normed = is_q ? p.gq != nullptr : p.gk != nullptr;
-      if (p.gq || p.gk) {
-        float ss = 0.f;
-#pragma unroll
-        for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
-#pragma unroll
-        for (int o = LPR / 2; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-        if (normed) {
-          const float inv = 1.f / sqrtf(ss * (1.f / HD) + p.eps);
-          const float* g = &s_g[is_q ? 0 : 1][8 * c];
-#pragma unroll
-          for (int e = 0; e < 8; ++e) {
-            a[e] = a[e] * inv * g[e];
-            b[e] = b[e] * inv * g[HD / 2 + e];
-          }
-        }
-      }
-      norm_rotate<HD>(a, b, nullptr, 0.f, p.rope != 0, cs, sn);
-      if (live) {
+      const bool is_q = hh < p.n_q;
+      float a[8], b[8];
+      next.unpack(0, a);
+      next.unpack(1, b);
+      read(u + p.parts, next);
+      // a warp may hold query and key heads at once, of which one side alone is
+      // normed (and, behind the last head, lanes with leftovers, not stored)
+      norm_rotate<HD>(a, b, p.gq || p.gk, is_q ? p.gq != nullptr : p.gk != nullptr, &s_g[is_q ? 0 : 1][8 * c], p.eps,
+                      p.rope != 0, cs, sn);
+      if (hh < heads) {
         const Rows<T>& out = is_q ? p.q_out : p.k_out;
-        T* y = out.p + t * out.rs + h * out.hs + 8 * c;
+        T* y = out.p + t * out.rs + (is_q ? hh : hh - p.n_q) * out.hs + 8 * c;
         store8(y, a);
         store8(y + HD / 2, b);
       }
@@ -213,29 +227,13 @@ int qk_go(const QkNormRopeCall& c, cudaStream_t st) {
   const long long want = 2LL * num_sms() * (kThreads / 32);
   a.parts = static_cast<int>(std::min<long long>(units, std::max<long long>(1, want / c.T)));
   const long long blocks = (static_cast<long long>(c.T) * a.parts + kThreads / 32 - 1) / (kThreads / 32);
-  launch_k(qk_norm_rope_kernel<T, HD>, dim3(static_cast<unsigned>(std::min<long long>(blocks, 8LL * num_sms()))),
+  launch_k(qk_norm_rope_kernel<T, HD>, dim3(static_cast<unsigned>(std::min<long long>(blocks, 4LL * num_sms()))),
            dim3(kThreads), 0, st, a);
   count_launch();
   return check_launch();
 }
 
 // ---------------------------------------------------------------- append --
-// The sequence that owns row t: the last s with row_start[s] <= t, found by the
-// whole warp (32 probes a round, two rounds for up to 1024 sequences), or -1.
-SF_DEV int seq_of_row(const int32_t* row_start, int n_seqs, int t, int lane) {
-  int lo = 0, n = n_seqs;
-  while (true) {
-    const int step = (n + 31) / 32;
-    const int at = lane * step;
-    const unsigned below = __ballot_sync(0xffffffffu, at < n && row_start[lo + min(at, n - 1)] <= t);
-    if (below == 0) return -1;
-    const int k = 31 - __clz(below);
-    lo += k * step;
-    n = min(step, n - k * step);
-    if (step == 1) return lo;
-  }
-}
-
 template <typename T>
 struct AppendArgs {
   Rows<T> k, v;
@@ -245,16 +243,22 @@ struct AppendArgs {
   specfold_paged_cache cache;
   SeqBatch batch;
   uint32_t* status;
-  int n_kv, n_src, rope;
+  int n_kv, n_src, rope, chunk;
   float eps;
   Turns turns;
 };
 
+// Work item: the keys, or the values, of a chunk of consecutive rows, one warp.
+// A row's place takes a search for its sequence (over the batch's entries in
+// shared memory) and its table's entry: lane r has row r's, so a chunk waits
+// for them once.  The rows' groups of heads then stream through with the next
+// one in flight.
 template <typename T, int HD>
-__global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_constant__ AppendArgs<T> p) {
+__global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const __grid_constant__ AppendArgs<T> p) {
   constexpr int LPR = HD / 16, RPW = 32 / LPR;
   __shared__ uint64_t s_f[HD / 2];
   __shared__ float s_g[HD];
+  __shared__ int s_start[SPECFOLD_MAX_SEQS + 1], s_ctx[SPECFOLD_MAX_SEQS];
   if (p.rope && threadIdx.x < HD / 2) s_f[threadIdx.x] = p.turns.f[threadIdx.x];
   // No early release of dependents: a dependent may read the cache (a prefix
   // view) before its own wait.
@@ -262,58 +266,85 @@ __global__ void __launch_bounds__(kThreads) kv_append_kernel(const __grid_consta
   if (p.gk)
     for (int i = threadIdx.x; i < HD; i += kThreads) s_g[i] = static_cast<float>(p.gk[i]);
   const SeqBatch& bt = p.batch;
-  if (p.status && blockIdx.x == 0) {  // the batch's own validity, whether or not it has rows
-    bool bad = false;
-    for (int s = threadIdx.x; s < bt.n_seqs; s += kThreads)
-      bad = bad || bt.row_start[s] < 0 || bt.row_start[s + 1] < bt.row_start[s] || bt.row_start[s + 1] > bt.T ||
-            bt.ctx_len[s] < 0;
-    if (bad) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
+  for (int s = threadIdx.x; s <= bt.n_seqs; s += kThreads) {
+    s_start[s] = bt.row_start[s];
+    if (s < bt.n_seqs) s_ctx[s] = bt.ctx_len[s];
   }
   __syncthreads();
+  auto bad_seq = [&](int s) {
+    return s_start[s] < 0 || s_start[s + 1] < s_start[s] || s_start[s + 1] > bt.T || s_ctx[s] < 0;
+  };
+  if (p.status && blockIdx.x == 0) {  // the batch's own validity, whether or not it has rows
+    bool bad = false;
+    for (int s = threadIdx.x; s < bt.n_seqs; s += kThreads) bad = bad || bad_seq(s);
+    if (bad) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
+  }
   const int lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
   const specfold_paged_cache& ch = p.cache;
-  for (int t = blockIdx.x * (kThreads / 32) + (threadIdx.x >> 5); t < bt.T; t += gridDim.x * (kThreads / 32)) {
-    const int src = p.rows ? p.rows[t] : t;
-    const int s = seq_of_row(bt.row_start, bt.n_seqs, t, lane);
-    if (s < 0) continue;
-    const int beg = bt.row_start[s], end = bt.row_start[s + 1], ctx = bt.ctx_len[s];
-    if (t >= end) continue;                             // behind the last sequence
-    if (beg < 0 || end > bt.T || ctx < 0) continue;      // reported above
-    if (src < 0 || src >= p.n_src) {
-      if (p.status && lane == 0) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
-      continue;
-    }
-    const long long tok = static_cast<long long>(ctx) + (t - beg);
-    const long long pg = tok / ch.page_size;
-    int page = -1;
-    if (pg < ch.table_pages) page = ch.block_table[s * ch.table_stride + pg];
-    if (page < 0 || page >= ch.num_pages) {
-      if (p.status && lane == 0) atomicOr(p.status, SPECFOLD_DEV_BAD_PAGE);
-      continue;
-    }
-    const long long slot = static_cast<long long>(page) * ch.page_size + (tok - pg * ch.page_size);
-    float cs[8], sn[8];
-    if (p.rope) lane_angles<HD>(s_f, p.positions ? p.positions[t] : tok, lane, c, cs, sn);
-    for (int h0 = 0; h0 < p.n_kv; h0 += RPW) {
-      const int h = h0 + sub;
-      const bool live = h < p.n_kv;
-      float a[8] = {}, b[8] = {}, va[8], vb[8];
-      if (live) {
-        const T* x = p.k.p + src * p.k.rs + h * p.k.hs + 8 * c;
-        const T* z = p.v.p + src * p.v.rs + h * p.v.hs + 8 * c;
-        load8(x, a);
-        load8(x + HD / 2, b);
-        load8(z, va);
-        load8(z + HD / 2, vb);
+  const int units = (p.n_kv + RPW - 1) / RPW;
+  const int chunks = (bt.T + p.chunk - 1) / p.chunk;
+  const long long items = 2LL * chunks, step = static_cast<long long>(gridDim.x) * (kThreads / 32);
+  for (long long it = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
+    const bool is_v = it & 1;
+    const int t0 = static_cast<int>(it >> 1) * p.chunk, n = min(p.chunk, bt.T - t0);
+    int src = -1, slot = -1;
+    unsigned tok = 0;
+    if (lane < n) {
+      const int t = t0 + lane;
+      src = p.rows ? p.rows[t] : t;
+      int lo = -1, hi = bt.n_seqs;  // the last sequence that starts at t or before it
+      while (hi - lo > 1) {
+        const int mid = (lo + hi) >> 1;
+        if (s_start[mid] <= t)
+          lo = mid;
+        else
+          hi = mid;
       }
-      norm_rotate<HD>(a, b, p.gk ? s_g + 8 * c : nullptr, p.eps, p.rope != 0, cs, sn);
-      if (live) {
-        T* y = static_cast<T*>(ch.k) + slot * ch.k_token_stride + h * ch.k_head_stride + 8 * c;
-        T* w = static_cast<T*>(ch.v) + slot * ch.v_token_stride + h * ch.v_head_stride + 8 * c;
-        store8(y, a);
-        store8(y + HD / 2, b);
-        store8(w, va);
-        store8(w + HD / 2, vb);
+      if (lo >= 0 && t < s_start[lo + 1] && !bad_seq(lo)) {
+        uint32_t wrong = 0u;
+        tok = static_cast<unsigned>(s_ctx[lo]) + static_cast<unsigned>(t - s_start[lo]);  // < 2^32
+        const unsigned pg = tok / static_cast<unsigned>(ch.page_size);
+        int page = -1;
+        if (pg < static_cast<unsigned>(ch.table_pages)) page = ch.block_table[lo * ch.table_stride + pg];
+        if (src < 0 || src >= p.n_src)
+          wrong = SPECFOLD_DEV_BAD_SEQ;
+        else if (page < 0 || page >= ch.num_pages)
+          wrong = SPECFOLD_DEV_BAD_PAGE;
+        else
+          slot = page * ch.page_size + static_cast<int>(tok - pg * ch.page_size);
+        if (wrong && p.status) atomicOr(p.status, wrong);
+      }
+    }
+    const Rows<T>& in = is_v ? p.v : p.k;
+    T* pool = static_cast<T*>(is_v ? ch.v : ch.k) + 8 * c;
+    const long long ts = is_v ? ch.v_token_stride : ch.k_token_stride, hs = is_v ? ch.v_head_stride : ch.k_head_stride;
+    const bool rope = p.rope && !is_v, norm = p.gk && !is_v;
+    auto read = [&](int r, int u, Raw<T>& x) {  // the whole warp: row r's group u
+      const int from = __shfl_sync(0xffffffffu, src, r), to = __shfl_sync(0xffffffffu, slot, r), h = u * RPW + sub;
+      if (to >= 0 && h < p.n_kv) x.read(in.p + from * in.rs + h * in.hs + 8 * c, HD / 2);
+    };
+    Raw<T> next = {};
+    read(0, 0, next);
+    float cs[8], sn[8];
+    for (int r = 0; r < n; ++r) {
+      const int to = __shfl_sync(0xffffffffu, slot, r);
+      if (rope) {
+        const long long at = __shfl_sync(0xffffffffu, tok, r);
+        lane_angles<HD>(s_f, p.positions ? p.positions[t0 + r] : at, lane, c, cs, sn);
+      }
+      for (int u = 0; u < units; ++u) {
+        const int h = u * RPW + sub;
+        float a[8], b[8];
+        next.unpack(0, a);
+        next.unpack(1, b);
+        const bool last = u == units - 1;
+        if (!last || r + 1 < n) read(last ? r + 1 : r, last ? 0 : u + 1, next);
+        norm_rotate<HD>(a, b, norm, norm, s_g + 8 * c, p.eps, rope, cs, sn);
+        if (to >= 0 && h < p.n_kv) {
+          T* y = pool + to * ts + h * hs;
+          store8(y, a);
+          store8(y + HD / 2, b);
+        }
       }
     }
   }
@@ -335,8 +366,11 @@ int append_go(const KvAppendCall& c, cudaStream_t st) {
   a.eps = c.eps;
   a.rope = c.theta > 0.f;
   if (a.rope) rope_turns(c.theta, HD, &a.turns);
-  const int blocks = (c.batch.T + kThreads / 32 - 1) / (kThreads / 32);
-  launch_k(kv_append_kernel<T, HD>, dim3(std::min(blocks, 8 * num_sms())), dim3(kThreads), 0, st, a);
+  // chunks that give every SM the 32 warps it holds, and no more than a warp's rows
+  a.chunk = std::min(32, std::max(1, static_cast<int>(2LL * c.batch.T / (32LL * num_sms()))));
+  const long long blocks = (2LL * ((c.batch.T + a.chunk - 1) / a.chunk) + kThreads / 32 - 1) / (kThreads / 32);
+  launch_k(kv_append_kernel<T, HD>, dim3(static_cast<unsigned>(std::min<long long>(blocks, 4LL * num_sms()))),
+           dim3(kThreads), 0, st, a);
   count_launch();
   return check_launch();
 }
