@@ -25,6 +25,11 @@ namespace sf {
 namespace {
 
 constexpr int kThreads = 256;
+// Resident blocks an SM, which cap the registers.  Measured (16381 rows of 24 + 8
+// heads; 16331 rows of 8 heads appended): 2, 3, 4, 5 blocks 56.5, 48.3, 46.3,
+// 68.5 us and 24.0, 21.0, 23.8, 27.5 us: fewer hold too few bytes in flight, more
+// spill.
+constexpr int kQkBlocks = 4, kAppendBlocks = 3;
 
 // A lane's two runs of eight elements as they lie in memory: what a warp has in
 // flight while it works on the group of heads before.
@@ -37,9 +42,10 @@ struct Raw<__nv_bfloat16> {
     u[0] = *reinterpret_cast<const uint4*>(p);
     u[1] = *reinterpret_cast<const uint4*>(p + half);
   }
-  SF_DEV void unpack(int i, float (&x)[8]) const {
-    x[0] = bf16lo(u[i].x); x[1] = bf16hi(u[i].x); x[2] = bf16lo(u[i].y); x[3] = bf16hi(u[i].y);
-    x[4] = bf16lo(u[i].z); x[5] = bf16hi(u[i].z); x[6] = bf16lo(u[i].w); x[7] = bf16hi(u[i].w);
+  SF_DEV void unpack(int i, float2 (&x)[4]) const {
+    const uint32_t v[4] = {u[i].x, u[i].y, u[i].z, u[i].w};
+#pragma unroll
+    for (int e = 0; e < 4; ++e) x[e] = make_float2(bf16lo(v[e]), bf16hi(v[e]));
   }
 };
 template <>
@@ -51,18 +57,21 @@ struct Raw<float> {
     u[2] = reinterpret_cast<const float4*>(p + half)[0];
     u[3] = reinterpret_cast<const float4*>(p + half)[1];
   }
-  SF_DEV void unpack(int i, float (&x)[8]) const {
-    const float4 a = u[2 * i], b = u[2 * i + 1];
-    x[0] = a.x; x[1] = a.y; x[2] = a.z; x[3] = a.w; x[4] = b.x; x[5] = b.y; x[6] = b.z; x[7] = b.w;
+  SF_DEV void unpack(int i, float2 (&x)[4]) const {
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      x[2 * e] = make_float2(u[2 * i + e].x, u[2 * i + e].y);
+      x[2 * e + 1] = make_float2(u[2 * i + e].z, u[2 * i + e].w);
+    }
   }
 };
-SF_DEV void store8(__nv_bfloat16* p, const float (&y)[8]) {
-  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]),
-                                            pack_bf16x2(y[4], y[5]), pack_bf16x2(y[6], y[7]));
+SF_DEV void store8(__nv_bfloat16* p, const float2 (&y)[4]) {
+  *reinterpret_cast<uint4*>(p) = make_uint4(pack_bf16x2(y[0].x, y[0].y), pack_bf16x2(y[1].x, y[1].y),
+                                            pack_bf16x2(y[2].x, y[2].y), pack_bf16x2(y[3].x, y[3].y));
 }
-SF_DEV void store8(float* p, const float (&y)[8]) {
-  reinterpret_cast<float4*>(p)[0] = make_float4(y[0], y[1], y[2], y[3]);
-  reinterpret_cast<float4*>(p)[1] = make_float4(y[4], y[5], y[6], y[7]);
+SF_DEV void store8(float* p, const float2 (&y)[4]) {
+  reinterpret_cast<float4*>(p)[0] = make_float4(y[0].x, y[0].y, y[1].x, y[1].y);
+  reinterpret_cast<float4*>(p)[1] = make_float4(y[2].x, y[2].y, y[3].x, y[3].y);
 }
 
 // Turn fractions F_j of the rotation frequencies (see the file comment).
@@ -78,54 +87,60 @@ void rope_turns(float theta, int hd, Turns* t) {
 
 // cos and sin of this lane's eight pairs (j = 8c .. 8c + 7) at position pos.
 // Lane l computes the pairs HD/64*l .. of the warp's HD/2 frequencies and the
-// eight come by shuffles: every angle once per warp.
-template <int HD>
-SF_DEV void lane_angles(const uint64_t* s_f, long long pos, int lane, int c, float (&cs)[8], float (&sn)[8]) {
+// eight come by shuffles: every angle once per warp.  For bf16 results the
+// special function unit's sine and cosine do (off by at most 2^-20 on one turn,
+// against a rounding of 2^-8).
+template <typename T, int HD>
+SF_DEV void lane_angles(const uint64_t* s_f, long long pos, int lane, int c, float2 (&cs)[4], float2 (&sn)[4]) {
   constexpr int PER = HD / 64;  // angles a lane computes: 2 or 1
   float myc[PER], mys[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
     const uint64_t turn = static_cast<uint64_t>(pos) * s_f[lane * PER + e];
     // the fraction's upper 32 bits as a signed number: half turns in [-1, 1)
-    const float half = static_cast<float>(static_cast<int32_t>(turn >> 32)) * (1.f / 2147483648.f);
-    sincospif(half, &mys[e], &myc[e]);
+    const float half = static_cast<float>(static_cast<int32_t>(turn >> 32));
+    if constexpr (sizeof(T) == 2)
+      __sincosf(half * (3.14159265358979f / 2147483648.f), &mys[e], &myc[e]);
+    else
+      sincospif(half * (1.f / 2147483648.f), &mys[e], &myc[e]);
   }
+  auto from = [&](const float (&mine)[PER], int e) {
+    return __shfl_sync(0xffffffffu, mine[e % PER], (8 * c + e) / PER);
+  };
 #pragma unroll
-  for (int e = 0; e < 8; ++e) {
-    const int from = (8 * c + e) / PER;
-    cs[e] = __shfl_sync(0xffffffffu, myc[e % PER], from);
-    sn[e] = __shfl_sync(0xffffffffu, mys[e % PER], from);
+  for (int e = 0; e < 4; ++e) {
+    cs[e] = make_float2(from(myc, 2 * e), from(myc, 2 * e + 1));
+    sn[e] = make_float2(from(mys, 2 * e), from(mys, 2 * e + 1));
   }
 }
 
 // One head's row in registers (two runs of eight, from 8c and HD/2 + 8c on): the
-// norm with the gain g where `normed`, then the rotation.  Every lane of the
-// warp takes part in the sum.
+// norm with the gain g (null: none), then the rotation.  The whole warp takes
+// part; g is at the lane's first element.
 template <int HD>
-SF_DEV void norm_rotate(float (&a)[8], float (&b)[8], bool any_norm, bool normed, const float* g, float eps, bool rope,
-                        const float (&cs)[8], const float (&sn)[8]) {
-  if (any_norm) {
-    float ss = 0.f;
+SF_DEV void norm_rotate(float2 (&a)[4], float2 (&b)[4], const float* g, float eps, bool rope, const float2 (&cs)[4],
+                        const float2 (&sn)[4]) {
+  if (g) {
+    float2 ss = make_float2(0.f, 0.f);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) ss = fmaf(a[e], a[e], fmaf(b[e], b[e], ss));
+    for (int e = 0; e < 4; ++e) ss = fma2(a[e], a[e], fma2(b[e], b[e], ss));
+    float sum = ss.x + ss.y;
 #pragma unroll
-    for (int o = HD / 32; o > 0; o >>= 1) ss += __shfl_xor_sync(0xffffffffu, ss, o);
-    if (normed) {
-      // a square root and a division, as the formula has them: one per row and lane
-      const float inv = 1.f / sqrtf(ss * (1.f / HD) + eps);
+    for (int o = HD / 32; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    const float inv = rsqrtf(sum * (1.f / HD) + eps);  // off by at most 2^-22
+    const float2 inv2 = make_float2(inv, inv);
 #pragma unroll
-      for (int e = 0; e < 8; ++e) {
-        a[e] = a[e] * inv * g[e];
-        b[e] = b[e] * inv * g[HD / 2 + e];
-      }
+    for (int e = 0; e < 4; ++e) {
+      a[e] = mul2(mul2(a[e], inv2), reinterpret_cast<const float2*>(g)[e]);
+      b[e] = mul2(mul2(b[e], inv2), reinterpret_cast<const float2*>(g + HD / 2)[e]);
     }
   }
   if (rope) {
 #pragma unroll
-    for (int e = 0; e < 8; ++e) {
-      const float x = a[e], y = b[e];
-      a[e] = x * cs[e] - y * sn[e];
-      b[e] = y * cs[e] + x * sn[e];
+    for (int e = 0; e < 4; ++e) {
+      const float2 x = a[e], y = b[e], minus = make_float2(-sn[e].x, -sn[e].y);
+      a[e] = fma2(x, cs[e], mul2(y, minus));
+      b[e] = fma2(y, cs[e], mul2(x, sn[e]));
     }
   }
 }
@@ -155,10 +170,10 @@ struct QkArgs {
 // Work item: row t, one of `parts` shares of its heads (a few rows alone
 // would leave most SMs idle), one warp each.
 template <typename T, int HD>
-__global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const __grid_constant__ QkArgs<T> p) {
+__global__ void __launch_bounds__(kThreads, kQkBlocks) qk_norm_rope_kernel(const __grid_constant__ QkArgs<T> p) {
   constexpr int LPR = HD / 16, RPW = 32 / LPR;
   __shared__ uint64_t s_f[HD / 2];
-  __shared__ float s_g[2][HD];
+  __shared__ __align__(16) float s_g[2][HD];
   if (p.rope && threadIdx.x < HD / 2) s_f[threadIdx.x] = p.turns.f[threadIdx.x];
   pdl_wait();
   pdl_trigger();
@@ -168,37 +183,35 @@ __global__ void __launch_bounds__(kThreads, 4) qk_norm_rope_kernel(const __grid_
   }
   __syncthreads();
   const int lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
-  const int heads = p.n_q + p.n_kv, units = (heads + RPW - 1) / RPW;
+  // a unit is a group of heads that a warp holds at once, queries' before keys'
+  const int units_q = (p.n_q + RPW - 1) / RPW, units = units_q + (p.n_kv + RPW - 1) / RPW;
   const long long items = static_cast<long long>(p.T_rows) * p.parts;
   const long long step = static_cast<long long>(gridDim.x) * (kThreads / 32);
   for (long long it = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
     const int t = static_cast<int>(it / p.parts);
     const int first = static_cast<int>(it - static_cast<long long>(t) * p.parts);
     auto read = [&](int u, Raw<T>& x) {
-      const int hh = u * RPW + sub;
-      if (u < units && hh < heads) {
-        const Rows<T>& in = hh < p.n_q ? p.q_in : p.k_in;
-        x.read(in.p + t * in.rs + (hh < p.n_q ? hh : hh - p.n_q) * in.hs + 8 * c, HD / 2);
-      }
+      const bool is_q = u < units_q;
+      const int h = (is_q ? u : u - units_q) * RPW + sub;
+      const Rows<T>& in = is_q ? p.q_in : p.k_in;
+      if (u < units && h < (is_q ? p.n_q : p.n_kv)) x.read(in.p + t * in.rs + h * in.hs + 8 * c, HD / 2);
     };
     Raw<T> next = {};
     read(first, next);
-    float cs[8], sn[8];
-    if (p.rope) lane_angles<HD>(s_f, p.positions[t], lane, c, cs, sn);
+    float2 cs[4], sn[4];
+    if (p.rope) lane_angles<T, HD>(s_f, p.positions[t], lane, c, cs, sn);
     for (int u = first; u < units; u += p.parts) {
-      const int hh = u * RPW + sub;
-      const bool is_q = hh < p.n_q;
-      float a[8], b[8];
+      float2 a[4], b[4];
       next.unpack(0, a);
       next.unpack(1, b);
       read(u + p.parts, next);
-      // a warp may hold query and key heads at once, of which one side alone is
-      // normed (and, behind the last head, lanes with leftovers, not stored)
-      norm_rotate<HD>(a, b, p.gq || p.gk, is_q ? p.gq != nullptr : p.gk != nullptr, &s_g[is_q ? 0 : 1][8 * c], p.eps,
-                      p.rope != 0, cs, sn);
-      if (hh < heads) {
-        const Rows<T>& out = is_q ? p.q_out : p.k_out;
-        T* y = out.p + t * out.rs + (is_q ? hh : hh - p.n_q) * out.hs + 8 * c;
+      const bool is_q = u < units_q;
+      const int h = (is_q ? u : u - units_q) * RPW + sub;
+      const float* g = is_q ? (p.gq ? &s_g[0][8 * c] : nullptr) : (p.gk ? &s_g[1][8 * c] : nullptr);
+      norm_rotate<HD>(a, b, g, p.eps, p.rope != 0, cs, sn);
+      const Rows<T>& out = is_q ? p.q_out : p.k_out;
+      if (h < (is_q ? p.n_q : p.n_kv)) {  // lanes behind the last head hold leftovers
+        T* y = out.p + t * out.rs + h * out.hs + 8 * c;
         store8(y, a);
         store8(y + HD / 2, b);
       }
@@ -222,12 +235,12 @@ int qk_go(const QkNormRopeCall& c, cudaStream_t st) {
   a.eps = c.eps;
   a.rope = c.theta > 0.f;
   if (a.rope) rope_turns(c.theta, HD, &a.turns);
-  const int units = (c.n_q + c.n_kv + 512 / HD - 1) / (512 / HD);
-  // shares of a row's heads: as many as give every SM two blocks
-  const long long want = 2LL * num_sms() * (kThreads / 32);
-  a.parts = static_cast<int>(std::min<long long>(units, std::max<long long>(1, want / c.T)));
+  const int units = (c.n_q + 512 / HD - 1) / (512 / HD) + (c.n_kv + 512 / HD - 1) / (512 / HD);
+  // shares of a row's heads: enough that the last round of the grid's warps weighs little
+  const long long want = 6LL * kQkBlocks * num_sms() * (kThreads / 32);
+  a.parts = static_cast<int>(std::min<long long>(units, std::max<long long>(1, (want + c.T - 1) / c.T)));
   const long long blocks = (static_cast<long long>(c.T) * a.parts + kThreads / 32 - 1) / (kThreads / 32);
-  launch_k(qk_norm_rope_kernel<T, HD>, dim3(static_cast<unsigned>(std::min<long long>(blocks, 4LL * num_sms()))),
+  launch_k(qk_norm_rope_kernel<T, HD>, dim3(static_cast<unsigned>(std::min<long long>(blocks, static_cast<long long>(kQkBlocks) * num_sms()))),
            dim3(kThreads), 0, st, a);
   count_launch();
   return check_launch();
@@ -254,10 +267,10 @@ struct AppendArgs {
 // for them once.  The rows' groups of heads then stream through with the next
 // one in flight.
 template <typename T, int HD>
-__global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const __grid_constant__ AppendArgs<T> p) {
+__global__ void __launch_bounds__(kThreads, kAppendBlocks) kv_append_kernel(const __grid_constant__ AppendArgs<T> p) {
   constexpr int LPR = HD / 16, RPW = 32 / LPR;
   __shared__ uint64_t s_f[HD / 2];
-  __shared__ float s_g[HD];
+  __shared__ __align__(16) float s_g[HD];
   __shared__ int s_start[SPECFOLD_MAX_SEQS + 1], s_ctx[SPECFOLD_MAX_SEQS];
   if (p.rope && threadIdx.x < HD / 2) s_f[threadIdx.x] = p.turns.f[threadIdx.x];
   // No early release of dependents: a dependent may read the cache (a prefix
@@ -325,21 +338,21 @@ __global__ void __launch_bounds__(kThreads, 4) kv_append_kernel(const __grid_con
     };
     Raw<T> next = {};
     read(0, 0, next);
-    float cs[8], sn[8];
+    float2 cs[4], sn[4];
     for (int r = 0; r < n; ++r) {
       const int to = __shfl_sync(0xffffffffu, slot, r);
       if (rope) {
         const long long at = __shfl_sync(0xffffffffu, tok, r);
-        lane_angles<HD>(s_f, p.positions ? p.positions[t0 + r] : at, lane, c, cs, sn);
+        lane_angles<T, HD>(s_f, p.positions ? p.positions[t0 + r] : at, lane, c, cs, sn);
       }
       for (int u = 0; u < units; ++u) {
         const int h = u * RPW + sub;
-        float a[8], b[8];
+        float2 a[4], b[4];
         next.unpack(0, a);
         next.unpack(1, b);
         const bool last = u == units - 1;
         if (!last || r + 1 < n) read(last ? r + 1 : r, last ? 0 : u + 1, next);
-        norm_rotate<HD>(a, b, norm, norm, s_g + 8 * c, p.eps, rope, cs, sn);
+        norm_rotate<HD>(a, b, norm ? s_g + 8 * c : nullptr, p.eps, rope, cs, sn);
         if (to >= 0 && h < p.n_kv) {
           T* y = pool + to * ts + h * hs;
           store8(y, a);
@@ -366,10 +379,11 @@ int append_go(const KvAppendCall& c, cudaStream_t st) {
   a.eps = c.eps;
   a.rope = c.theta > 0.f;
   if (a.rope) rope_turns(c.theta, HD, &a.turns);
-  // chunks that give every SM the 32 warps it holds, and no more than a warp's rows
-  a.chunk = std::min(32, std::max(1, static_cast<int>(2LL * c.batch.T / (32LL * num_sms()))));
+  // chunks of rows such that the grid's warps take one each, and no more than a warp's lanes
+  const long long warps = static_cast<long long>(kAppendBlocks) * num_sms() * (kThreads / 32);
+  a.chunk = static_cast<int>(std::min<long long>(32, (2LL * c.batch.T + warps - 1) / warps));
   const long long blocks = (2LL * ((c.batch.T + a.chunk - 1) / a.chunk) + kThreads / 32 - 1) / (kThreads / 32);
-  launch_k(kv_append_kernel<T, HD>, dim3(static_cast<unsigned>(std::min<long long>(blocks, 4LL * num_sms()))),
+  launch_k(kv_append_kernel<T, HD>, dim3(static_cast<unsigned>(std::min<long long>(blocks, static_cast<long long>(kAppendBlocks) * num_sms()))),
            dim3(kThreads), 0, st, a);
   count_launch();
   return check_launch();
