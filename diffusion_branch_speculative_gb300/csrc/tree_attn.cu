@@ -30,7 +30,7 @@ SF_DEV void store4(__nv_bfloat16* p, float4 v) {
 // output of the current piece's rows, or into its partial slot.
 template <typename T, int HD, int RT>
 SF_DEV void merge_warps(const TreeArgs& p, const TreeWalk& w, bool first, const uint8_t* smem, int stride) {
-  const int h = w.head(), m0 = tree_m0(p, w), rows = tree_tile_rows(p, w);
+  const int h = w.head, m0 = tree_m0(p, w), rows = tree_tile_rows(p, w);
   const bool whole = w.whole();
   const size_t ps = static_cast<size_t>(tree_slot(first)) * p.tile_rows;
   const float* mw = reinterpret_cast<const float*>(smem);
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const __grid_c
   pdl_wait();
   pdl_trigger();
   TreeWalk w;
-  long long lo, per;
+  unsigned lo, per;
   const bool work = tree_locate(p, w, lo, per);
   if (threadIdx.x == 0) tree_describe(p, w, work, lo, per);
   if (!work) return;
@@ -114,10 +114,10 @@ __global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const __grid_c
   float* s_p = reinterpret_cast<float*>(smem + C::OFF_P) + warp * kChunk * RT;
   const T* qp = static_cast<const T*>(p.q);
 
-  for (bool first = true; w.left > 0; first = false, w.next(p)) {
-    const int h = w.head(), m0 = tree_m0(p, w), rows = tree_tile_rows(p, w);
+  for (bool first = true; w.n > 0; first = false, w.next(p)) {
+    const int h = w.head, m0 = tree_m0(p, w), rows = tree_tile_rows(p, w);
     const int len = w.q.ctx + w.q.n, key_lo = w.b0 * p.kb;
-    const int key_hi = min(static_cast<long long>(len), static_cast<long long>(w.b0 + w.blocks()) * p.kb);
+    const int key_hi = min(static_cast<long long>(len), static_cast<long long>(w.b0 + w.n) * p.kb);
     __syncthreads();  // the previous piece's shared memory is free
     for (int i = threadIdx.x; i < RT * (HD / 4); i += kThreads) {
       const int r = i / (HD / 4), d = (i % (HD / 4)) * 4, m = m0 + r;
@@ -338,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_ker
   pdl_wait();
   pdl_trigger();
   TreeWalk w;
-  long long lo, per;
+  unsigned lo, per;
   const bool work = tree_locate(p, w, lo, per);
   if (threadIdx.x == 0) tree_describe(p, w, work, lo, per);
   if (!work) return;
@@ -352,10 +352,10 @@ __global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_ker
     return smem_u32(s_q + r * C::ROW + (((ks * 2 + (lane >> 4)) ^ (r & 7)) << 4));
   };
 
-  for (bool first = true; w.left > 0; first = false, w.next(p)) {
-    const int h = w.head(), rows = w.q.n * p.g;
+  for (bool first = true; w.n > 0; first = false, w.next(p)) {
+    const int h = w.head, rows = w.q.n * p.g;
     const int len = w.q.ctx + w.q.n, key_lo = w.b0 * p.kb;
-    const int key_hi = min(static_cast<long long>(len), static_cast<long long>(w.b0 + w.blocks()) * p.kb);
+    const int key_hi = min(static_cast<long long>(len), static_cast<long long>(w.b0 + w.n) * p.kb);
     __syncthreads();  // the previous piece's shared memory is free
 
     // this warp's chunks: key_lo + 16 * (warp + 4 i)
@@ -703,17 +703,17 @@ __global__ void __launch_bounds__(kCombineQuads * 32) tree_combine_quads_kernel(
 // --------------------------------------------------------------- launches --
 // A kernel's geometry: CTAs per SM, rows of a tile, keys of a block.
 struct Plan {
-  int ctas_per_sm, tile_rows, kb, unit_cost;
+  int ctas_per_sm, tile_rows, kb, unit_cost, w_full, w_half;
 };
 
 Plan plan_of(int dtype, int g, int hd, int max_nodes) {
   const int rows = max_nodes * g;
   if (dtype == SPECFOLD_BF16) {
-    if (rows > 32) return {1, kTreeTcRows, kTreeTcKeys, 3};
+    if (rows > 32) return {1, kTreeTcRows, kTreeTcKeys, 4, 5, 3};
     const int rt = rows <= 16 ? 16 : 32;
-    return {hd == 128 ? Few<128, 1>::CTAS : Few<64, 1>::CTAS, rt, 4 * kChunk, 2};
+    return {hd == 128 ? Few<128, 1>::CTAS : Few<64, 1>::CTAS, rt, 4 * kChunk, 2, 1, 1};
   }
-  return {1, 8, 4 * kChunk, 1};
+  return {1, 8, 4 * kChunk, 1, 1, 1};
 }
 
 int tree_start(void (*kernel)(TreeArgs), int smem, const TreeArgs& a, int grid, cudaStream_t st) {
@@ -742,6 +742,8 @@ int tree_go(const TreeAttnCall& c, const Plan& pl, cudaStream_t st) {
   a.tile_rows = pl.tile_rows;
   a.kb = pl.kb;
   a.unit_cost = pl.unit_cost;
+  a.w_full = pl.w_full;
+  a.w_half = pl.w_half;
   a.sl2 = static_cast<float>(1.4426950408889634 * (c.scale > 0.f ? c.scale : 1.0 / std::sqrt(static_cast<double>(HD))));
   uint8_t* ws = static_cast<uint8_t*>(c.ws);
   a.status = reinterpret_cast<uint32_t*>(ws);

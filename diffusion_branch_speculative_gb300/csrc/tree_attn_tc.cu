@@ -153,7 +153,7 @@ SF_DEV void gather_queries(const TreeArgs& p, const TreeWalk& w, uint8_t* smem, 
   int hd = m % g;
   const long long d_node = p.q_rs - g * p.q_hs, d_step = dn * p.q_rs + dh * p.q_hs;
   const __nv_bfloat16* src = static_cast<const __nv_bfloat16*>(p.q) + (w.q.row0 + m / g) * p.q_rs +
-                             (w.head() * g + hd) * p.q_hs + c * 8;
+                             (w.head * g + hd) * p.q_hs + c * 8;
   const uint32_t q0 = smem_u32(smem) + (c >> 3) * kAtom;
 #pragma unroll 4
   for (int r = tid / (HD / 8); r < most; r += RSTEP) {
@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
   pdl_wait();
   pdl_trigger();
   TreeWalk w;
-  long long lo, per;
+  unsigned lo, per;
   const bool work = tree_locate(p, w, lo, per);
   if (threadIdx.x == 0) tree_describe(p, w, work, lo, per);
   tc_fence_before();
@@ -251,9 +251,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
     const int pool = p.cache.num_pages * ps;
     const int box = lane & 15, atom = lane >> 4;  // what this thread issues of a tile
     const bool issues = box < boxes && atom < C::NATOM;
-    for (; w.left > 0 && ok; w.next(p), ++j) {
-      const int h = w.head(), rows = tree_tile_rows(p, w), ctx = w.q.ctx, len = ctx + w.q.n;
-      const int nt = w.blocks(), lead = rows > 128 ? 1 : 2;
+    for (; w.n > 0 && ok; w.next(p), ++j) {
+      const int h = w.head, rows = tree_tile_rows(p, w), ctx = w.q.ctx, len = ctx + w.q.n;
+      const int nt = w.n, lead = rows > 128 ? 1 : 2;
       // queries, by both warps: the previous unit's S products must be done with
       // their place (the first unit's come from the softmax warps, idle then)
       auto load_queries = [&]() {
@@ -399,8 +399,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
     named_bar_sync(1, 256);
     if (leader) mbar_arrive(smem_u32(q_full));
     bool ok = true;
-    for (bool first = true; w.left > 0 && ok; first = false, w.next(p), ++j) {
-      const int h = w.head(), ctx = w.q.ctx, nt = w.blocks(), rows = tree_tile_rows(p, w);
+    for (bool first = true; w.n > 0 && ok; first = false, w.next(p), ++j) {
+      const int h = w.head, ctx = w.q.ctx, nt = w.n, rows = tree_tile_rows(p, w);
       const bool pair = rows > 128;
       const int r = pair ? x * 128 + row : row;  // row of the tile
       const bool valid = r < rows;
@@ -654,8 +654,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
                  sdesc_sw128(aK + (kk >> 2) * kAtom + (kk & 3) * 32, 16, 1024), idS, kk > 0 ? 1u : 0u);
       warp_commit(me, smem_u32(&s_full[x]));
     };
-    for (; uniform(w.left > 0) && ok; w.next(p), ++j) {
-      const int nt = uniform(w.blocks());
+    for (; uniform(w.n > 0) && ok; w.next(p), ++j) {
+      const int nt = uniform(w.n);
       const bool pair = uniform(tree_tile_rows(p, w) > 128);
       const int lead = pair ? 1 : 2;
       const uint32_t aQ1 = base + (pair ? C::Q_BYTES : 0);

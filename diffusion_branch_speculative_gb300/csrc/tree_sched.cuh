@@ -6,8 +6,10 @@
 // the lengths are known on the device only, and one rule serves a single long
 // sequence and a ragged batch of short ones.  Starting a unit costs a CTA as
 // much as some blocks (its queries, an output to write): a unit counts unit_cost
-// places more than its blocks, in front of them, so that a CTA that starts more
-// units gets fewer blocks.  A cut inside these places is one at the unit's start.  A run's piece that covers its
+// blocks more than it has, in front of them, so that a CTA that starts more
+// units gets fewer blocks.  A block counts as many places as its tile weighs: one
+// with at most half its rows may cost less.  A cut inside a block's places is one
+// before it, a cut inside a unit's start one before the unit.  A run's piece that covers its
 // whole unit writes the output; any other writes an unnormalised partial (o,
 // running max m in log2 units, sum l), at most the run's first and last piece
 // (slots 2c and 2c + 1 of CTA c), which the combine kernel merges in order, so
@@ -30,6 +32,7 @@ struct TreeArgs {
   int tile_rows;  // query rows of a tile: row m is node m / g, head m % g of the group
   int kb;         // keys per block
   int unit_cost;  // a unit's start, in blocks
+  int w_full, w_half;  // places of a block: of a tile with more, with at most half its rows
   float sl2;               // scale * log2(e)
   uint32_t* status;
   int4* desc;              // [2 * grid]: the unit cut at CTA c's start, see tree_describe
@@ -38,12 +41,15 @@ struct TreeArgs {
 };
 
 // One sequence: rows n behind ctx cached tokens, nb blocks of keys, tiles of
-// query rows.  An invalid one has none.
+// query rows (the last one's rows may be at most half a tile's).  An invalid one
+// has none.
 struct TreeSeq {
   int row0, n, ctx, nb, tiles;
-  bool bad;
-  SF_DEV long long items(const TreeArgs& p) const {  // its places in the line
-    return static_cast<long long>(nb + (n > 0 ? p.unit_cost : 0)) * tiles * p.n_kv;
+  bool half, bad;
+  SF_DEV unsigned weight(const TreeArgs& p, int tile) const { return half && tile == tiles - 1 ? p.w_half : p.w_full; }
+  // places in the line of all its tiles of one head
+  SF_DEV unsigned head_places(const TreeArgs& p) const {
+    return static_cast<unsigned>(nb + p.unit_cost) * (tiles * p.w_full - (half ? p.w_full - p.w_half : 0));
   }
 };
 
@@ -64,123 +70,136 @@ SF_DEV TreeSeq tree_seq(const TreeArgs& p, int s) {
   q.n = q.bad ? 0 : end - q.row0;
   q.nb = q.n > 0 ? (q.ctx + q.n - 1) / p.kb + 1 : 0;
   q.tiles = (q.n * p.g + p.tile_rows - 1) / p.tile_rows;
+  q.half = 2 * (q.n * p.g - (q.tiles - 1) * p.tile_rows) <= p.tile_rows;
   return q;
 }
 
-// A CTA's walk along its run: the current unit u (head u / tiles, tile u %
-// tiles) of sequence s from block b0 on, `left` places to go (the unit's start
-// not counted when b0 > 0).
+// A CTA's walk along its run: the current piece, blocks b0 .. b0 + n - 1 of
+// (sequence s, head, tile), and the places left from there on.  All of this is
+// executed once or twice a launch, mostly on cold instruction caches: it is kept
+// short (32-bit places, few divisions).
 struct TreeWalk {
-  int s, u, b0;
-  long long left;
+  int s, head, tile, b0, n;
+  unsigned left;
+  unsigned past;  // places of block b0 before the run's first, where the run starts in it
   TreeSeq q;
-  SF_DEV int head() const { return u / q.tiles; }
-  SF_DEV int tile() const { return u % q.tiles; }
-  SF_DEV int blocks() const {  // of the current piece
-    const long long rest = q.nb - b0;
-    return static_cast<int>(rest < left ? rest : left);
+  SF_DEV bool whole() const { return n == q.nb; }
+  SF_DEV void cut(unsigned wt) {  // n, from b0 and left
+    n = q.nb - b0;
+    if (left < n * wt) n = left / wt;
   }
-  SF_DEV bool whole() const { return b0 == 0 && blocks() == q.nb; }
-  // Enter the current unit at its start: its places are paid for, or, where the
-  // run ends among them, it is left to the next CTA.
+  // The current unit from its start on, whose start is paid for, or, where the
+  // run ends before its first block does, is left to the next CTA.
   SF_DEV void enter(const TreeArgs& p) {
-    b0 = 0;
-    left = left > p.unit_cost ? left - p.unit_cost : 0;
+    const unsigned wt = q.weight(p, tile), start = p.unit_cost * wt;
+    b0 = n = 0;
+    if (left < start + wt) return;
+    left -= start;
+    cut(wt);
   }
   SF_DEV void next(const TreeArgs& p) {
-    left -= blocks();
-    if (++u >= q.tiles * p.n_kv) {
-      u = 0;
-      while (left > 0) {
-        if (++s >= p.batch.n_seqs) {  // lengths that changed under the call
-          left = 0;
-          break;
-        }
-        q = tree_seq(p, s);
-        if (q.n > 0) break;
+    const bool ends = b0 + n < q.nb;  // the run does
+    left -= n * q.weight(p, tile);
+    b0 = n = 0;
+    if (ends || left == 0) return;
+    if (++tile == q.tiles) {
+      tile = 0;
+      if (++head == p.n_kv) {
+        head = 0;
+        do {
+          if (++s >= p.batch.n_seqs) return;  // lengths that changed under the call
+          q = tree_seq(p, s);
+        } while (q.n == 0);
       }
     }
     enter(p);
   }
 };
 
-// Quotient of numbers that hardly ever need more than 32 bits.
-SF_DEV long long div_ll(long long a, unsigned b) {
-  return a >> 32 ? a / b : static_cast<long long>(static_cast<unsigned>(a) / b);
-}
-
-SF_DEV TreeSeq tree_seq_or_none(const TreeArgs& p, int s) {
-  if (s < p.batch.n_seqs) return tree_seq(p, s);
-  TreeSeq q;
-  q.row0 = q.n = q.ctx = q.nb = q.tiles = 0;
-  q.bad = false;
-  return q;
-}
-
-SF_DEV long long warp_prefix(long long v, int lane) {
-#pragma unroll
-  for (int o = 1; o < 32; o <<= 1) {
-    const long long u = __shfl_up_sync(0xffffffffu, v, o);
-    if (lane >= o) v += u;
-  }
-  return v;
-}
-
 // This CTA's run, found by every warp on its own (a lane a sequence, 32 at a
-// time: no block-wide barrier, one round trip for up to 32 sequences).  lo: the
-// run's first block, per: the blocks of a run.  Returns false for a CTA without
+// time: no block-wide barrier, one round trip for up to 32 sequences).  lo: where
+// the run starts in the line, per: the places of a run.  False for a CTA without
 // work; the walk is the same in all threads.
-SF_DEV bool tree_locate(const TreeArgs& p, TreeWalk& w, long long& lo, long long& per) {
-  const int lane = threadIdx.x & 31, n = p.batch.n_seqs;
-  TreeSeq q = tree_seq_or_none(p, lane);
-  bool bad = q.bad;
-  long long inc = warp_prefix(q.items(p), lane);
-  long long total = __shfl_sync(0xffffffffu, inc, 31);
-  for (int c = 32; c < n; c += 32) {
-    const TreeSeq r = tree_seq_or_none(p, c + lane);
-    bad = bad || r.bad;
-    total += __shfl_sync(0xffffffffu, warp_prefix(r.items(p), lane), 31);
+SF_DEV bool tree_locate(const TreeArgs& p, TreeWalk& w, unsigned& lo, unsigned& per) {
+  const int lane = threadIdx.x & 31, n_seqs = p.batch.n_seqs;
+  TreeSeq q;
+  unsigned inc = 0;
+  float size = 0.f;  // the total again, which cannot wrap
+  // 32 sequences from c on: q this lane's, inc the places up to and with its own
+  auto take = [&](int c) {
+    q = tree_seq(p, min(c + lane, n_seqs - 1));
+    const bool mine = c + lane < n_seqs && q.n > 0;
+    const unsigned places = mine ? q.head_places(p) * p.n_kv : 0;
+    size += mine ? static_cast<float>(q.nb + p.unit_cost) * q.tiles * p.w_full * p.n_kv : 0.f;
+    inc = places;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+      const unsigned u = __shfl_up_sync(0xffffffffu, inc, o);
+      if (lane >= o) inc += u;
+    }
+    return places;
+  };
+  unsigned total = 0, places = 0;
+  bool bad = false;
+#pragma unroll 1
+  for (int c = (n_seqs - 1) & ~31; c >= 0; c -= 32) {  // the first 32 last: they stay
+    places = take(c);
+    total += __shfl_sync(0xffffffffu, inc, 31);
+    bad = bad || q.bad;
   }
-  if (bad && blockIdx.x == 0 && threadIdx.x < 32) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
-  per = div_ll(total + gridDim.x - 1, gridDim.x);
+  // a line of 10^8 places a lane and more (hours of work) could wrap: refused
+  const bool wraps = __any_sync(0xffffffffu, size > 1.2e8f);
+  if ((bad || wraps) && blockIdx.x == 0 && threadIdx.x < 32) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
+  per = max((total + gridDim.x - 1) / gridDim.x, static_cast<unsigned>(p.w_full));  // a block at least
   lo = per * blockIdx.x;
-  const long long hi = min(lo + per, total);
-  if (lo >= hi) return false;
-  long long base = 0;
+  if (wraps || lo >= total) return false;
+  unsigned before = 0;
   int c = 0;
-  while (lo >= base + __shfl_sync(0xffffffffu, inc, 31)) {
-    base += __shfl_sync(0xffffffffu, inc, 31);
+#pragma unroll 1
+  while (true) {
+    const unsigned sum = __shfl_sync(0xffffffffu, inc, 31);
+    if (lo < before + sum) break;
+    before += sum;
     c += 32;
-    q = tree_seq_or_none(p, c + lane);
-    inc = warp_prefix(q.items(p), lane);
+    if (c >= n_seqs) return false;  // lengths that changed under the call
+    places = take(c);
   }
-  const int src = __ffs(__ballot_sync(0xffffffffu, lo < base + inc)) - 1;
-  const long long off = lo - base - __shfl_sync(0xffffffffu, inc - q.items(p), src);
+  const int src = __ffs(__ballot_sync(0xffffffffu, lo < before + inc)) - 1;
+  const unsigned off = lo - before - __shfl_sync(0xffffffffu, inc - places, src);
   w.s = c + src;
   w.q.row0 = __shfl_sync(0xffffffffu, q.row0, src);
   w.q.n = __shfl_sync(0xffffffffu, q.n, src);
   w.q.ctx = __shfl_sync(0xffffffffu, q.ctx, src);
   w.q.nb = __shfl_sync(0xffffffffu, q.nb, src);
   w.q.tiles = __shfl_sync(0xffffffffu, q.tiles, src);
-  w.q.bad = false;
-  const int places = w.q.nb + p.unit_cost;
-  w.u = static_cast<int>(div_ll(off, places));
-  const int at = static_cast<int>(off - static_cast<long long>(w.u) * places);
-  w.left = hi - lo;
-  if (at <= p.unit_cost) {  // at the unit's start
+  w.q.half = __shfl_sync(0xffffffffu, q.half, src);
+  const unsigned hp = w.q.head_places(p), tp = static_cast<unsigned>(w.q.nb + p.unit_cost) * p.w_full;
+  w.head = off / hp;
+  unsigned at = off - w.head * hp;
+  w.tile = 0;
+  while (w.tile < w.q.tiles - 1 && at >= tp) {  // a division's worth for most
+    at -= tp;
+    ++w.tile;
+  }
+  const unsigned wt = w.q.weight(p, w.tile), v = at / wt;  // blocks, the start's among them, before the cut
+  w.left = min(per, total - lo);
+  if (static_cast<int>(v) <= p.unit_cost) {  // before the unit
     w.left += at;
     w.enter(p);
   } else {
-    w.b0 = at - p.unit_cost;
+    w.past = at - v * wt;
+    w.left += w.past;
+    w.b0 = v - p.unit_cost;
+    w.cut(wt);
   }
-  return w.left > 0;
+  return w.n > 0;
 }
 
 // The partial slot of a run's piece.
 SF_DEV int tree_slot(bool first) { return 2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1); }
 
 // Rows of the current unit's tile: the first one and how many.
-SF_DEV int tree_m0(const TreeArgs& p, const TreeWalk& w) { return w.tile() * p.tile_rows; }
+SF_DEV int tree_m0(const TreeArgs& p, const TreeWalk& w) { return w.tile * p.tile_rows; }
 SF_DEV int tree_tile_rows(const TreeArgs& p, const TreeWalk& w) {
   return min(p.tile_rows, w.q.n * p.g - tree_m0(p, w));
 }
@@ -188,17 +207,17 @@ SF_DEV int tree_tile_rows(const TreeArgs& p, const TreeWalk& w) {
 // By one thread of every CTA: the unit that this CTA's start cuts, if this is
 // the first cut in it, for the combine kernel: {rows, row0, m0, head},
 // {first CTA, last CTA, the first CTA's slot, 0}; rows 0: nothing to merge.
-SF_DEV void tree_describe(const TreeArgs& p, const TreeWalk& w, bool work, long long lo, long long per) {
+SF_DEV void tree_describe(const TreeArgs& p, const TreeWalk& w, bool work, unsigned lo, unsigned per) {
   const int c = blockIdx.x;
   int4 a = make_int4(0, 0, 0, 0);
   if (work && w.b0 > 0) {
-    // the unit's places are [beg, end), its first block's place beg + unit_cost
-    const long long beg = lo - w.b0 - p.unit_cost, end = beg + p.unit_cost + w.q.nb, before = lo - per;
-    if (beg + p.unit_cost >= before) {  // CTA c - 1 has the first block
-      a = make_int4(tree_tile_rows(p, w), w.q.row0, tree_m0(p, w), w.head());
-      // per < 2^32: a run of more 64-key blocks than that is no cache's
-      p.desc[2 * c + 1] = make_int4(c - 1, static_cast<int>(div_ll(end - 1, static_cast<unsigned>(per))),
-                                    2 * (c - 1) + (beg <= before ? 0 : 1), 0);
+    // Where the unit begins and ends, from where its block b0 does; a block is its last place's owner's.
+    const unsigned wt = w.q.weight(p, w.tile), before = lo - per;
+    const unsigned b0_at = lo - w.past;
+    const unsigned beg = b0_at - (w.b0 + p.unit_cost) * wt, end = b0_at + (w.q.nb - w.b0) * wt;
+    if (beg + (p.unit_cost + 1) * wt > before) {  // CTA c - 1 has the first block
+      a = make_int4(tree_tile_rows(p, w), w.q.row0, tree_m0(p, w), w.head);
+      p.desc[2 * c + 1] = make_int4(c - 1, (end - 1) / per, 2 * (c - 1) + (beg <= before ? 0 : 1), 0);
     }
   }
   p.desc[2 * c] = a;
