@@ -90,10 +90,11 @@ struct Simt {
   static constexpr int OFF_Q = kWarps * (RING > MERGE ? RING : MERGE);
   static constexpr int OFF_P = OFF_Q + RT * HD * 4;
   static constexpr int SMEM = OFF_P + kWarps * kChunk * RT * 4;
+  static constexpr int CTAS = HD == 64 ? 3 : 1;  // per SM: 68 or 135 KB each
 };
 
 template <int HD>
-__global__ void __launch_bounds__(kThreads) tree_attn_simt_kernel(const __grid_constant__ TreeArgs p) {
+__global__ void __launch_bounds__(kThreads, Simt<HD>::CTAS) tree_attn_simt_kernel(const __grid_constant__ TreeArgs p) {
   using C = Simt<HD>;
   using T = float;
   constexpr int RT = C::RT, DPL = HD / 32;  // dimensions of the output a lane holds
@@ -709,11 +710,11 @@ struct Plan {
 Plan plan_of(int dtype, int g, int hd, int max_nodes) {
   const int rows = max_nodes * g;
   if (dtype == SPECFOLD_BF16) {
-    if (rows > 32) return {1, kTreeTcRows, kTreeTcKeys, 4, 5, 3};
+    if (rows > 32) return {1, kTreeTcRows, kTreeTcKeys, 5, 5, 3};
     const int rt = rows <= 16 ? 16 : 32;
     return {hd == 128 ? Few<128, 1>::CTAS : Few<64, 1>::CTAS, rt, 4 * kChunk, 2, 1, 1};
   }
-  return {1, 8, 4 * kChunk, 1, 1, 1};
+  return {hd == 128 ? Simt<128>::CTAS : Simt<64>::CTAS, 8, 4 * kChunk, 1, 1, 1};
 }
 
 int tree_start(void (*kernel)(TreeArgs), int smem, const TreeArgs& a, int grid, cudaStream_t st) {

@@ -176,11 +176,8 @@ SF_DEV bool tree_locate(const TreeArgs& p, TreeWalk& w, unsigned& lo, unsigned& 
   const unsigned hp = w.q.head_places(p), tp = static_cast<unsigned>(w.q.nb + p.unit_cost) * p.w_full;
   w.head = off / hp;
   unsigned at = off - w.head * hp;
-  w.tile = 0;
-  while (w.tile < w.q.tiles - 1 && at >= tp) {  // a division's worth for most
-    at -= tp;
-    ++w.tile;
-  }
+  w.tile = min(static_cast<int>(at / tp), w.q.tiles - 1);
+  at -= w.tile * tp;
   const unsigned wt = w.q.weight(p, w.tile), v = at / wt;  // blocks, the start's among them, before the cut
   w.left = min(per, total - lo);
   if (static_cast<int>(v) <= p.unit_cost) {  // before the unit

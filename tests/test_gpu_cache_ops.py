@@ -529,6 +529,86 @@ def test_guards_intact(B, dt, nodes):
     check_tree(B, c, o, dt)
 
 
+def far_cache(B, rng, n_kv, hd, page, need, tokens):
+    """A cache whose sequences' pages lie at the end of a pool of `tokens`
+    tokens; the rest of the pool is never touched."""
+    kp, vp = (torch.empty((tokens, n_kv, hd), dtype=torch.bfloat16, device="cuda") for _ in range(2))
+    pages = [-(-int(n) // page) for n in need]
+    table = np.zeros((len(need), max(pages)), np.int32)
+    at = tokens // page
+    for s, n in enumerate(pages):
+        for i in range(n):
+            at -= 1
+            table[s, i] = at
+            kp[at * page:(at + 1) * page] = randn(rng, (page, n_kv, hd), "bf16")
+            vp[at * page:(at + 1) * page] = randn(rng, (page, n_kv, hd), "bf16")
+    return B.PagedCache(kp, vp, ints(table), page), table
+
+
+@pytest.mark.parametrize("nodes,n_q", [(3, 8), (40, 16)])
+def test_pools_past_two_to_the_31_elements(B, nodes, n_q):
+    """Append and attention at element offsets that 32 bits do not hold."""
+    rng = np.random.default_rng(22)
+    n_kv, hd, page, tokens = 4, 128, 16, 4_300_000 // 16 * 16   # 2.2e9 elements a pool
+    counts, ctx = np.array([nodes, 2]), np.array([100, 33])
+    start = np.concatenate([[0], np.cumsum(counts)])
+    cache, table = far_cache(B, rng, n_kv, hd, page, ctx + counts, tokens)
+    T = int(start[-1])
+    K, V, q = randn(rng, (T, n_kv, hd), "bf16"), randn(rng, (T, n_kv, hd), "bf16"), randn(rng, (T, n_q, hd), "bf16")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.specfold_kv_append(K, V, cache, ints(start), ints(ctx), status=status)
+    # the oracle on the used pages alone
+    used = table[table > 0]
+    slots = torch.from_numpy((used[:, None].astype(np.int64) * page + np.arange(page)).reshape(-1)).cuda()
+    small = np.zeros_like(table)
+    small[table > 0] = np.arange(len(used))
+    kp, vp = cache.k_pool[slots], cache.v_pool[slots]
+    for s in range(2):
+        for i in range(int(counts[s])):
+            t = int(ctx[s]) + i
+            at = int(small[s, t // page]) * page + t % page
+            assert torch.equal(kp[at], K[int(start[s]) + i]) and torch.equal(vp[at], V[int(start[s]) + i])
+    assert int(status) == 0
+    c = dict(cache=cache, table=table, start=start, ctx=ctx, parent=None, q=q, T=T, nodes=nodes)
+    o, ws = run_tree(B, c)
+    torch.cuda.synchronize()
+    assert B.specfold_get_status(ws) == 0
+
+    class Small:
+        k_pool, v_pool, page_size = kp, vp, page
+    check_tree(B, dict(c, cache=Small, table=small), o, "bf16")
+
+
+def test_a_batch_too_long_for_one_call_is_refused(B):
+    """Sequences whose blocks no 32-bit count holds (tables that name one page
+    over and over): nothing is computed, and the status says so."""
+    rng = np.random.default_rng(23)
+    page = 1 << 19
+    kp = torch.zeros((page, 4, 64), dtype=torch.bfloat16, device="cuda")
+    table = torch.zeros((2, 4096), dtype=torch.int32, device="cuda")
+    cache = B.PagedCache(kp, kp, table, page)
+    c = dict(cache=cache, start=[0, 1, 2], ctx=[2 ** 31 - 600, 2 ** 31 - 600], parent=None, q=randn(rng, (2, 8, 64), "bf16"),
+             nodes=1)
+    o, ws = run_tree(B, c)
+    torch.cuda.synchronize()
+    assert B.specfold_get_status(ws) == B.DEV_BAD_SEQ
+    assert (o == 7.0).all()
+
+
+@pytest.mark.parametrize("dt,nodes", [("bf16", 1), ("bf16", 4), ("bf16", 60), ("f32", 9)])
+def test_tree_grows_like_a_sequence(B, dt, nodes):
+    """Rows one by one, each appended and attended alone, give what the chain
+    gives at once (another split of the keys: rounding apart)."""
+    rng = np.random.default_rng(24)
+    c = tree_case(B, rng, dt, 64, 4, 2, 8, "fused", [nodes], [45], "none", extra=0)
+    whole, _ = run_tree(B, c)
+    for i in range(nodes):
+        one = dict(c, q=c["q"][i:i + 1], start=[0, 1], ctx=[45 + i], nodes=1)
+        o, _ = run_tree(B, one)
+        torch.cuda.synchronize()
+        assert torch.allclose(o[0].float(), whole[i].float(), rtol=0.03, atol=0.03 if dt == "bf16" else 1e-4)
+
+
 # ------------------------------------------------------------- a whole step --
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
