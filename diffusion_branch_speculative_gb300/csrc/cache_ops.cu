@@ -336,28 +336,49 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) kv_append_kernel(cons
       const int from = __shfl_sync(0xffffffffu, src, r), to = __shfl_sync(0xffffffffu, slot, r), h = u * RPW + sub;
       if (to >= 0 && h < p.n_kv) x.read(in.p + from * in.rs + h * in.hs + 8 * c, HD / 2);
     };
-    Raw<T> next = {};
-    read(0, 0, next);
-    float2 cs[4], sn[4];
-    for (int r = 0; r < n; ++r) {
-      const int to = __shfl_sync(0xffffffffu, slot, r);
-      if (rope) {
-        const long long at = __shfl_sync(0xffffffffu, tok, r);
-        lane_angles<T, HD>(s_f, p.positions ? p.positions[t0 + r] : at, lane, c, cs, sn);
+    // the chunk's groups in one sequence, kDepth of them in flight
+    struct At {
+      int r, u;
+      SF_DEV void next(int units) {
+        if (++u == units) {
+          u = 0;
+          ++r;
+        }
       }
-      for (int u = 0; u < units; ++u) {
-        const int h = u * RPW + sub;
+    };
+    // (16331 rows of 8 heads: 21.0 us with one, 19.9 with two, 21.3 with three)
+    constexpr int kDepth = sizeof(T) == 2 ? 2 : 1;
+    Raw<T> flight[kDepth] = {};
+    At ahead = {0, 0}, now = {0, 0};
+#pragma unroll
+    for (int d = 0; d < kDepth; ++d) {
+      if (ahead.r < n) read(ahead.r, ahead.u, flight[d]);
+      ahead.next(units);
+    }
+    float2 cs[4], sn[4];
+    int to = -1;
+    while (now.r < n) {
+#pragma unroll
+      for (int d = 0; d < kDepth; ++d) {
+        if (now.r >= n) break;
+        if (now.u == 0) {
+          to = __shfl_sync(0xffffffffu, slot, now.r);
+          const long long at = __shfl_sync(0xffffffffu, tok, now.r);
+          if (rope) lane_angles<T, HD>(s_f, p.positions ? p.positions[t0 + now.r] : at, lane, c, cs, sn);
+        }
+        const int h = now.u * RPW + sub;
         float2 a[4], b[4];
-        next.unpack(0, a);
-        next.unpack(1, b);
-        const bool last = u == units - 1;
-        if (!last || r + 1 < n) read(last ? r + 1 : r, last ? 0 : u + 1, next);
+        flight[d].unpack(0, a);
+        flight[d].unpack(1, b);
+        if (ahead.r < n) read(ahead.r, ahead.u, flight[d]);
+        ahead.next(units);
         norm_rotate<HD>(a, b, norm ? s_g + 8 * c : nullptr, p.eps, rope, cs, sn);
         if (to >= 0 && h < p.n_kv) {
           T* y = pool + to * ts + h * hs;
           store8(y, a);
           store8(y + HD / 2, b);
         }
+        now.next(units);
       }
     }
   }
