@@ -90,7 +90,7 @@ struct Simt {
   static constexpr int OFF_Q = kWarps * (RING > MERGE ? RING : MERGE);
   static constexpr int OFF_P = OFF_Q + RT * HD * 4;
   static constexpr int SMEM = OFF_P + kWarps * kChunk * RT * 4;
-  static constexpr int CTAS = HD == 64 ? 3 : 1;  // per SM: 68 or 135 KB each
+  static constexpr int CTAS = HD == 64 ? 3 : 1;  // per SM: 68 or 135 KB each (head size 64 with two: 50.8, not 43.4 us)
 };
 
 template <int HD>
@@ -280,30 +280,35 @@ __global__ void __launch_bounds__(kThreads, Simt<HD>::CTAS) tree_attn_simt_kerne
 
 // ---------------------------------------------------- few rows, bf16: mma --
 // Up to RT = 16 MT rows of a head group (a whole sequence's nodes times the
-// group): decoding and small trees.  Such a unit does at most 32 operations a
+// group; MT 2 for head size 64 alone): decoding and small trees.  Such a unit does at most 32 operations a
 // byte of cache, so the memory bounds it and warp-level matrix instructions,
 // whose rows fit, are enough; what counts is bytes in flight and no barrier
-// between them.  So, as above, each of the four warps streams its own 16-key
-// chunks through a private ring of asynchronous copies:
-//   S [rows x 16 keys] = Q K^T, keys as the B operand straight from their rows;
+// between them.  So, as above, each of the four warps streams its own 4 KB
+// chunks of keys through a private ring of asynchronous copies:
+//   S [rows x chunk] = Q K^T, keys as the B operand straight from their rows;
 //   O [rows x HD] += P V, P from S's registers (rounded to bf16, the tensor
 //   cores' operand: off by half a step of each weight), V's rows transposed
 //   by the load.
 // 64 KB in flight an SM would cover the latency at full bandwidth; two CTAs of
-// 96 KB keep it covered while one of them merges.
+// 96 KB keep it covered while one of them merges.  Measured (32 sequences of 8000
+// tokens, 8 key/value heads, 4 rows; copy peak 6690 GB/s): head size 128
+// 1.05 GB in 166.5 us (6300 GB/s; one CTA an SM 232.7), head size 64 0.52 GB in
+// 99.6 us (5260 GB/s; chunks of 16 keys with two or four CTAs 107.4 and 116.5).
+// 8 sequences of 500 tokens: 11.5 and 8.8 us, the latency of the two launches.
 template <int HD, int MT>
 struct Few {
   static constexpr int RT = 16 * MT;
+  static constexpr int CH = 2048 / HD;  // keys of a warp's step: 4 KB, and as much of values
   static constexpr int STAGES = 3;
   static constexpr int ROW = HD * 2;
   static constexpr int CPR = ROW / 16;
-  static constexpr int STAGE = 2 * kChunk * ROW;
+  static constexpr int STAGE = 2 * CH * ROW;
   static constexpr int RING = STAGES * STAGE;
   static constexpr int MERGE = RT * (HD + 2) * 4;
   static_assert(MERGE <= RING, "the merge goes over the ring");
   static constexpr int OFF_Q = kWarps * RING;
   static constexpr int SMEM = OFF_Q + RT * ROW;
-  static constexpr int CTAS = HD == 128 ? 2 : 4;  // per SM
+  static constexpr int CTAS = 2;  // per SM
   static constexpr bool Q_IN_REGS = MT == 1;      // two row tiles' queries would not fit beside their outputs
 };
 
@@ -334,7 +339,7 @@ template <int HD, int MT>
 __global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_kernel(const __grid_constant__ TreeArgs p) {
   using C = Few<HD, MT>;
   using T = __nv_bfloat16;
-  constexpr int RT = C::RT, KS = HD / 16;
+  constexpr int RT = C::RT, KS = HD / 16, CH = C::CH, KH = CH / 16;
   extern __shared__ __align__(128) uint8_t smem[];
   pdl_wait();
   pdl_trigger();
@@ -359,12 +364,12 @@ __global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_ker
     const int key_hi = min(static_cast<long long>(len), static_cast<long long>(w.b0 + w.n) * p.kb);
     __syncthreads();  // the previous piece's shared memory is free
 
-    // this warp's chunks: key_lo + 16 * (warp + 4 i)
-    const int chunks = (key_hi - key_lo + kChunk - 1) / kChunk;
+    // this warp's chunks: key_lo + CH * (warp + 4 i)
+    const int chunks = (key_hi - key_lo + CH - 1) / CH;
     const int mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
-    auto key_of = [&](int i) { return key_lo + kChunk * (warp + kWarps * i); };
-    auto slot_of = [&](int i) {  // lanes 0..15: pool tokens of chunk i's keys
-      const int tok = key_of(i) + (lane & (kChunk - 1));
+    auto key_of = [&](int i) { return key_lo + CH * (warp + kWarps * i); };
+    auto slot_of = [&](int i) {  // lanes 0..CH-1: pool tokens of chunk i's keys
+      const int tok = key_of(i) + (lane & (CH - 1));
       return i < mine && tok < key_hi ? tree_pool_token(p, w.s, tok) : -1;
     };
     const T* kbase = static_cast<const T*>(p.cache.k) + h * p.cache.k_head_stride;
@@ -375,13 +380,13 @@ __global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_ker
         constexpr int KEYS = 32 / C::CPR;  // keys of one step of the warp's lanes
         const int c = lane % C::CPR;
 #pragma unroll
-        for (int it = 0; it < kChunk / KEYS; ++it) {
+        for (int it = 0; it < CH / KEYS; ++it) {
           const int key = it * KEYS + lane / C::CPR;
           const int tk = __shfl_sync(0xffffffffu, slot, key);
           const uint32_t n = tk < 0 ? 0u : 16u, at = st + key * C::ROW + ((c ^ (key & 7)) << 4);
           const long long tz = tk < 0 ? 0 : tk;  // any valid address when nothing is read
           cp_async16(at, kbase + tz * p.cache.k_token_stride + c * 8, n);
-          cp_async16(at + kChunk * C::ROW, vbase + tz * p.cache.v_token_stride + c * 8, n);
+          cp_async16(at + CH * C::ROW, vbase + tz * p.cache.v_token_stride + c * 8, n);
         }
       }
       cp_async_commit();
@@ -434,7 +439,7 @@ __global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_ker
       vis[q >> 1][q & 1] = r < rows ? v : 0u;
     }
     __syncthreads();
-    uint32_t qf[C::Q_IN_REGS ? KS : 1][4];
+    uint32_t qf[KS][4];
     if constexpr (C::Q_IN_REGS) {
 #pragma unroll
       for (int ks = 0; ks < KS; ++ks) ldsm4(q_addr(0, ks), qf[ks]);
@@ -454,49 +459,53 @@ __global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_ker
       cp_async_wait<C::STAGES - 1>();
       __syncwarp();
       uint8_t* stg = ring + (i % C::STAGES) * C::STAGE;
-      uint8_t* sv = stg + kChunk * C::ROW;
-      float s[MT][2][4] = {};
+      uint8_t* sv = stg + CH * C::ROW;
+      float s[MT][2 * KH][4] = {};
       {
         const int key = (lane & 7) + ((lane >> 4) << 3);
         const uint32_t base = smem_u32(stg + key * C::ROW);
 #pragma unroll
         for (int ks = 0; ks < KS; ++ks) {
-          uint32_t b[4];
-          ldsm4(base + (((ks * 2 + ((lane >> 3) & 1)) ^ (key & 7)) << 4), b);
+          uint32_t a[MT][4];
+          if constexpr (!C::Q_IN_REGS) {
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            if constexpr (C::Q_IN_REGS) {
-              mma16816(s[mt][0], qf[ks], b[0], b[1]);
-              mma16816(s[mt][1], qf[ks], b[2], b[3]);
-            } else {
-              uint32_t a[4];
-              ldsm4(q_addr(mt, ks), a);
-              mma16816(s[mt][0], a, b[0], b[1]);
-              mma16816(s[mt][1], a, b[2], b[3]);
+            for (int mt = 0; mt < MT; ++mt) ldsm4(q_addr(mt, ks), a[mt]);
+          }
+#pragma unroll
+          for (int kh = 0; kh < KH; ++kh) {
+            uint32_t b[4];
+            ldsm4(base + kh * 16 * C::ROW + (((ks * 2 + ((lane >> 3) & 1)) ^ (key & 7)) << 4), b);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              const uint32_t(&q)[4] = C::Q_IN_REGS ? qf[ks] : a[mt];
+              mma16816(s[mt][2 * kh], q, b[0], b[1]);
+              mma16816(s[mt][2 * kh + 1], q, b[2], b[3]);
             }
           }
         }
       }
       const int e0 = key_of(i) - w.q.ctx;
-      const bool tail = e0 + kChunk > 0;  // holds tokens that not every row sees
+      const bool tail = e0 + CH > 0;  // holds tokens that not every row sees
       if (tail) {
 #pragma unroll
         for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
-          for (int x = 0; x < 8; ++x) {
+          for (int x = 0; x < 8 * KH; ++x) {
             const int e = e0 + (x >> 2) * 8 + (lane & 3) * 2 + (x & 1);
             const bool see = e < 0 || (e < 32 && (vis[mt][(x >> 1) & 1] >> (e & 31) & 1u));
             if (!see) s[mt][x >> 2][x & 3] = -INFINITY;
           }
       }
-      uint32_t pf[MT][4];
+      uint32_t pf[MT][KH][4];
       bool grew = false;
       float alpha[MT][2];
 #pragma unroll
       for (int mt = 0; mt < MT; ++mt)
 #pragma unroll
         for (int hr = 0; hr < 2; ++hr) {
-          float m = fmaxf(fmaxf(s[mt][0][2 * hr], s[mt][0][2 * hr + 1]), fmaxf(s[mt][1][2 * hr], s[mt][1][2 * hr + 1]));
+          float m = fmaxf(s[mt][0][2 * hr], s[mt][0][2 * hr + 1]);
+#pragma unroll
+          for (int j = 1; j < 2 * KH; ++j) m = fmaxf(m, fmaxf(s[mt][j][2 * hr], s[mt][j][2 * hr + 1]));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 1));
           m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, 2));
           m = fmaxf(m * p.sl2, mx[mt][hr]);
@@ -504,12 +513,16 @@ __global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_ker
           alpha[mt][hr] = mx[mt][hr] == m ? 1.f : ex2(mx[mt][hr] - base);
           grew = grew || mx[mt][hr] != m;
           mx[mt][hr] = m;
-          float pr[4];
+          l[mt][hr] *= alpha[mt][hr];
 #pragma unroll
-          for (int x = 0; x < 4; ++x) pr[x] = ex2(fmaf(s[mt][x >> 1][2 * hr + (x & 1)], p.sl2, -base));
-          l[mt][hr] = l[mt][hr] * alpha[mt][hr] + ((pr[0] + pr[1]) + (pr[2] + pr[3]));
-          pf[mt][hr] = pack_bf16x2(pr[0], pr[1]);
-          pf[mt][2 + hr] = pack_bf16x2(pr[2], pr[3]);
+          for (int kh = 0; kh < KH; ++kh) {
+            float pr[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) pr[x] = ex2(fmaf(s[mt][2 * kh + (x >> 1)][2 * hr + (x & 1)], p.sl2, -base));
+            l[mt][hr] += (pr[0] + pr[1]) + (pr[2] + pr[3]);
+            pf[mt][kh][hr] = pack_bf16x2(pr[0], pr[1]);
+            pf[mt][kh][2 + hr] = pack_bf16x2(pr[2], pr[3]);
+          }
         }
       if (__any_sync(0xffffffffu, grew)) {
 #pragma unroll
@@ -527,12 +540,12 @@ __global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_ker
         // product, so such values of the tree's rows are added by hand to the
         // rows that see them and then taken out
         bool odd = false;
-        for (int x = lane; x < kChunk * C::CPR; x += 32) {
+        for (int x = lane; x < CH * C::CPR; x += 32) {
           const uint4 u = *reinterpret_cast<const uint4*>(sv + x * 16);
           odd = odd || bf16_not_finite(u.x) || bf16_not_finite(u.y) || bf16_not_finite(u.z) || bf16_not_finite(u.w);
         }
         if (__any_sync(0xffffffffu, odd)) {
-          for (int k = 0; k < kChunk; ++k) {
+          for (int k = 0; k < CH; ++k) {
             const int e = e0 + k;
 #pragma unroll
             for (int j = 0; j < HD / 8; ++j) {
@@ -548,7 +561,7 @@ __global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_ker
             }
           }
           __syncwarp();
-          for (int x = lane; x < kChunk * C::CPR * 8; x += 32) {
+          for (int x = lane; x < CH * C::CPR * 8; x += 32) {
             uint16_t* v = reinterpret_cast<uint16_t*>(sv) + x;
             if ((*v & 0x7f80u) == 0x7f80u) *v = 0;
           }
@@ -559,15 +572,17 @@ __global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_ker
         const int key = (lane & 7) + ((lane >> 3) & 1) * 8;
         const uint32_t base = smem_u32(sv + key * C::ROW);
 #pragma unroll
-        for (int j = 0; j < HD / 16; ++j) {
-          uint32_t b[4];
-          ldsm4t(base + (((j * 2 + (lane >> 4)) ^ (key & 7)) << 4), b);
+        for (int kh = 0; kh < KH; ++kh)
 #pragma unroll
-          for (int mt = 0; mt < MT; ++mt) {
-            mma16816(o[mt][2 * j], pf[mt], b[0], b[1]);
-            mma16816(o[mt][2 * j + 1], pf[mt], b[2], b[3]);
+          for (int j = 0; j < HD / 16; ++j) {
+            uint32_t b[4];
+            ldsm4t(base + kh * 16 * C::ROW + (((j * 2 + (lane >> 4)) ^ (key & 7)) << 4), b);
+#pragma unroll
+            for (int mt = 0; mt < MT; ++mt) {
+              mma16816(o[mt][2 * j], pf[mt][kh], b[0], b[1]);
+              mma16816(o[mt][2 * j + 1], pf[mt][kh], b[2], b[3]);
+            }
           }
-        }
       }
       __syncwarp();  // the stage may be overwritten
     }
@@ -707,12 +722,23 @@ struct Plan {
   int ctas_per_sm, tile_rows, kb, unit_cost, w_full, w_half;
 };
 
+// bf16 rows that fit one or, for head size 64, two row tiles of the warps' matrix
+// instructions take the few-rows kernel, more the tcgen05 one.  Both sides
+// (few-rows, tcgen05; us; 8 key/value heads, groups of 4):
+//   sequences x tokens       32 x 8000      1 x 40000     8 x 500
+//   head size 128, 16 rows   171.1  173.8   42.8  43.8    12.4  16.4
+//                  32 rows   184.4  175.0   49.0  44.3    16.4  16.4
+//   head size 64,  16 rows   101.3  143.5   22.8  29.1     9.6  13.5
+//                  32 rows   107.9  143.2   28.5  29.3    12.0  13.6
+//                  64 rows   201.0  147.9   46.2  29.6    17.0  15.1  (chunks of 16 keys)
+// Two row tiles for head size 64 and 16 rows: 105.1, 33.8, 11.7 (chunks of 16).
+// A unit's start is worth 2 to 8 blocks without a difference above 2 %, and so are
+// weights of 3:2 to 2:1 of a block's full and half tiles.
 Plan plan_of(int dtype, int g, int hd, int max_nodes) {
   const int rows = max_nodes * g;
   if (dtype == SPECFOLD_BF16) {
-    if (rows > 32) return {1, kTreeTcRows, kTreeTcKeys, 5, 5, 3};
-    const int rt = rows <= 16 ? 16 : 32;
-    return {hd == 128 ? Few<128, 1>::CTAS : Few<64, 1>::CTAS, rt, 4 * kChunk, 2, 1, 1};
+    if (rows > (hd == 128 ? 16 : 32)) return {1, kTreeTcRows, kTreeTcKeys, 5, 5, 3};
+    return {Few<128, 1>::CTAS, rows <= 16 ? 16 : 32, 64, 2, 1, 1};
   }
   return {hd == 128 ? Simt<128>::CTAS : Simt<64>::CTAS, 8, 4 * kChunk, 1, 1, 1};
 }
@@ -755,9 +781,12 @@ int tree_go(const TreeAttnCall& c, const Plan& pl, cudaStream_t st) {
   const int grid = std::min(num_sms(), kSmBudget) * pl.ctas_per_sm;
   int rc;
   if constexpr (sizeof(T) == 2) {
-    rc = pl.tile_rows == 16   ? tree_start(tree_attn_few_kernel<HD, 1>, Few<HD, 1>::SMEM, a, grid, st)
-         : pl.tile_rows == 32 ? tree_start(tree_attn_few_kernel<HD, 2>, Few<HD, 2>::SMEM, a, grid, st)
-                              : launch_tree_tc(a, HD, grid, st);
+    if (pl.tile_rows == 16)
+      rc = tree_start(tree_attn_few_kernel<HD, 1>, Few<HD, 1>::SMEM, a, grid, st);
+    else if (HD == 64 && pl.tile_rows == 32)
+      rc = tree_start(tree_attn_few_kernel<64, 2>, Few<64, 2>::SMEM, a, grid, st);
+    else
+      rc = launch_tree_tc(a, HD, grid, st);
   } else {
     rc = tree_start(tree_attn_simt_kernel<HD>, Simt<HD>::SMEM, a, grid, st);
   }
