@@ -17,10 +17,6 @@ constexpr int kChunk = 16;     // keys of a warp's step
 constexpr int kSmBudget = 160; // SMs the workspace is sized for (>= one GB300)
 
 SF_DEV float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
-SF_DEV float4 load4(const __nv_bfloat16* p) {
-  const uint2 u = *reinterpret_cast<const uint2*>(p);
-  return make_float4(bf16lo(u.x), bf16hi(u.x), bf16lo(u.y), bf16hi(u.y));
-}
 SF_DEV void store4(float* p, float4 v) { *reinterpret_cast<float4*>(p) = v; }
 SF_DEV void store4(__nv_bfloat16* p, float4 v) {
   *reinterpret_cast<uint2*>(p) = make_uint2(pack_bf16x2(v.x, v.y), pack_bf16x2(v.z, v.w));
