@@ -295,7 +295,7 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) kv_append_kernel(cons
   const int lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
   const specfold_paged_cache& ch = p.cache;
   const int units = (p.n_kv + RPW - 1) / RPW;
-  const int chunks = (bt.T + p.chunk - 1) / p.chunk;
+  const int chunks = (bt.T - 1) / p.chunk + 1;
   const long long items = 2LL * chunks, step = static_cast<long long>(gridDim.x) * (kThreads / 32);
   for (long long it = static_cast<long long>(blockIdx.x) * (kThreads / 32) + (threadIdx.x >> 5); it < items; it += step) {
     const bool is_v = it & 1;
@@ -403,7 +403,7 @@ int append_go(const KvAppendCall& c, cudaStream_t st) {
   // chunks of rows such that the grid's warps take one each, and no more than a warp's lanes
   const long long warps = static_cast<long long>(kAppendBlocks) * num_sms() * (kThreads / 32);
   a.chunk = static_cast<int>(std::min<long long>(32, (2LL * c.batch.T + warps - 1) / warps));
-  const long long blocks = (2LL * ((c.batch.T + a.chunk - 1) / a.chunk) + kThreads / 32 - 1) / (kThreads / 32);
+  const long long blocks = (2LL * ((c.batch.T - 1) / a.chunk + 1) + kThreads / 32 - 1) / (kThreads / 32);
   launch_k(kv_append_kernel<T, HD>, dim3(static_cast<unsigned>(std::min<long long>(blocks, static_cast<long long>(kAppendBlocks) * num_sms()))),
            dim3(kThreads), 0, st, a);
   count_launch();

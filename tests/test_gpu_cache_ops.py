@@ -689,3 +689,124 @@ def test_decoding_steps_together(B, dt, captured):
     # what the steps left is what the framework's own paged prefix view reads
     pk = B.PagedPrefix(cache.k_pool, cache.block_table[2], page, int(length[2]))
     assert pk.view().num_pages == cache.k_pool.shape[0] // page
+
+
+# ------------------------------------------------------------------- edges --
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("n_q,n_kv,hd", [(128, 1, 128), (127, 1, 64), (218, 2, 128), (96, 1, 64)])
+@pytest.mark.parametrize("counts,ctx", [([1], [300]), ([3, 1, 2], [129, 0, 40])])
+def test_tree_widest_groups(B, dt, n_q, n_kv, hd, counts, ctx):
+    rng = np.random.default_rng(31)
+    c = tree_case(B, rng, dt, hd, n_q, n_kv, 40, "fused", counts, ctx, "tree")
+    o, ws = run_tree(B, c)
+    torch.cuda.synchronize()
+    assert B.specfold_get_status(ws) == 0
+    check_tree(B, c, o, dt)
+
+
+@pytest.mark.parametrize("nodes,hd", [(4, 128), (5, 128), (8, 128), (9, 128), (4, 64), (5, 64), (8, 64), (9, 64)])
+@pytest.mark.parametrize("page", [8, 1000])
+def test_tree_on_both_sides_of_the_rules(B, nodes, hd, page):
+    """Rows of a head group just within and just past 16 and 32."""
+    rng = np.random.default_rng(32)
+    c = tree_case(B, rng, "bf16", hd, 8, 2, page, "heads", [nodes, 1, nodes], [999, 2000, 31], "padded")
+    o, ws = run_tree(B, c)
+    torch.cuda.synchronize()
+    assert B.specfold_get_status(ws) == 0
+    check_tree(B, c, o, "bf16")
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("nodes", [2, 40])
+def test_sequences_that_share_one_table(B, dt, nodes):
+    """One table row for all sequences (stride 0): the same cache, read by each
+    to its own length."""
+    rng = np.random.default_rng(33)
+    c = tree_case(B, rng, dt, 64, 4, 2, 16, "split", [nodes] * 5, [400, 3, 17, 128, 64], "tree")
+    one = c["cache"].block_table[:1].expand(5, -1)
+    c["cache"] = B.PagedCache(c["cache"].k_pool, c["cache"].v_pool, one, 16)
+    c["table"] = np.repeat(c["table"][:1], 5, axis=0)
+    o, ws = run_tree(B, c)
+    torch.cuda.synchronize()
+    assert B.specfold_get_status(ws) == 0
+    check_tree(B, c, o, dt)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_append_takes_a_row_many_times(B, dt):
+    rng = np.random.default_rng(34)
+    T = 70
+    x = randn(rng, (9, 3, 64), dt)
+    cache, table = make_cache(B, rng, dt, 64, 3, 8, [100, 20], "fused")
+    rows, start, ctx = np.repeat([8, 0, 8, 3, 3], 14), [0, 55, 70], [45, 5]
+    before = host(cache.k_pool), host(cache.v_pool)
+    B.specfold_kv_append(x, x, cache, ints(start), ints(ctx), rope_theta=1e4, rows=ints(rows))
+    torch.cuda.synchronize()
+    assert len(check_append(B, cache, table, before, (x, x, start, ctx, None, None, 1e4, rows), dt, T)) == T
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_calls_on_a_stream_of_their_own(B, dt):
+    """stream= takes the work off the current stream, and the order on that
+    stream is the calls'."""
+    rng = np.random.default_rng(35)
+    c = tree_case(B, rng, dt, 64, 4, 2, 16, "fused", [6, 2], [500, 90], "tree", extra=0)
+    cache, T = c["cache"], c["T"]
+    k = randn(rng, (T, 2, 64), dt)
+    g = randn(rng, (64,), dt)
+    pos, start, ctx, par = (ints(v) for v in (np.arange(T), c["start"], c["ctx"], c["parent"]))
+    keep = cache.k_pool.clone(), cache.v_pool.clone()
+    ws = B.alloc_workspace(B.tree_attention_workspace_size(B.dtype_code(DT[dt]), 4, 2, 64, 6))
+
+    def step(stream):
+        cache.k_pool.copy_(keep[0]), cache.v_pool.copy_(keep[1])
+        qr, o = torch.zeros(T, 4, 64, device="cuda", dtype=DT[dt]), torch.zeros(T, 4, 64, device="cuda", dtype=DT[dt])
+        torch.cuda.synchronize()
+        for _ in range(3):
+            B.specfold_qk_norm_rope(c["q"], None, qr, None, g, None, 1e-6, pos, 1e4, stream=stream)
+            B.specfold_kv_append(k, k, cache, start, ctx, gk=g, rope_theta=1e4, stream=stream)
+            B.specfold_tree_attention(qr, cache, par, start, ctx, 6, o, ws, stream=stream)
+        torch.cuda.synchronize()
+        return qr, o, cache.k_pool.clone(), cache.v_pool.clone()
+
+    here, there = step(None), step(torch.cuda.Stream())
+    assert all(torch.equal(a, b) for a, b in zip(here, there))
+
+
+def test_append_then_a_layer_that_reads_the_prefix(B):
+    """The verification layer right behind the append that writes its paged
+    prefix, no wait between: the same result as with one."""
+    from diffusion_branch_speculative_gb300 import synth
+    from tests.gpu_cases import DeviceInputs
+    inp = synth.make_layer_inputs(synth.small_workload(d=512, n_q=8, n_kv=2, hd=128, F=384, P=500, L=12,
+                                                       levels=(1, 3, 4)), seed=8)
+    dev = DeviceInputs(inp)
+    nb, L, _ = inp.H.shape
+    P, page = 500, 16
+    pages = -(-P // page)
+    pk, pv = (torch.zeros(pages * page, 2, 128, device="cuda", dtype=torch.bfloat16) for _ in range(2))
+    table = ints(np.random.default_rng(36).permutation(pages)[None])
+    cache = B.PagedCache(pk, pv, table, page)
+    start, ctx = ints([0, P]), ints([0])
+    ws = B.alloc_workspace(B.workspace_size(dev.dims, nb, L))
+    cw = B.make_weights(dev.W)
+
+    def layer(wait):
+        pk.zero_(), pv.zero_()
+        out = torch.empty_like(dev.H)
+        B.specfold_kv_append(dev.pk, dev.pv, cache, start, ctx)
+        if wait:
+            torch.cuda.synchronize()
+        B.specfold_layer_forward(dev.dims, cw, dev.H, dev.parent, B.PagedPrefix(pk, table[0], page, P),
+                                 B.PagedPrefix(pv, table[0], page, P), P, 0.05, out, ws)
+        return out
+
+    ref = layer(True)
+    plain = torch.empty_like(dev.H)
+    B.specfold_layer_forward(dev.dims, cw, dev.H, dev.parent, dev.pk, dev.pv, P, 0.05, plain, ws)
+    outs = [layer(False) for _ in range(20)]
+    torch.cuda.synchronize()
+    assert B.specfold_get_status(ws) == 0
+    assert torch.equal(ref, plain)
+    assert all(torch.equal(o, ref) for o in outs)
