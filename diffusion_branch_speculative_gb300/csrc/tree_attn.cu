@@ -7,13 +7,14 @@
 #include <algorithm>
 #include <cmath>
 #include <cstring>
+#include <type_traits>
 
 namespace sf {
 namespace {
 
 constexpr int kThreads = 128;  // 4 warps, each with its own chunks of keys
 constexpr int kWarps = kThreads / 32;
-constexpr int kChunk = 16;     // keys of a warp's step
+constexpr int kFewKeys = 64;   // keys of a block of these kernels: a chunk or two of each warp's
 constexpr int kSmBudget = 160; // SMs the workspace is sized for (>= one GB300)
 
 SF_DEV float4 load4(const float* p) { return *reinterpret_cast<const float4*>(p); }
@@ -65,35 +66,43 @@ SF_DEV void merge_warps(const TreeArgs& p, const TreeWalk& w, bool first, const 
 
 // ------------------------------------------------------ fp32: CUDA cores --
 // Tiles of RT rows (row m = node m / g, head m % g of the group).  Every warp
-// streams its own chunks of 16 keys through a private ring of asynchronous
+// streams its own 4 KB chunks of keys through a private ring of asynchronous
 // copies, with its own running maximum and sum, so the loop has no block-wide
 // barrier; the four warps merge once per piece.
-//   scores: lane = (key, half of the dimensions), the row's query broadcast
-//           from shared memory, the halves joined by one shuffle;
+//   scores: lane = (key, 32 of the dimensions), the row's query broadcast
+//           from shared memory, a key's lanes joined by shuffles;
 //   output: lane = dimensions, the probabilities broadcast.
 // A chunk's 16-byte pieces are stored with their index xored with the row's low
-// three bits, so that eight rows read at one place never share a bank.
+// three bits, so that eight rows read at one place never share a bank.  A piece
+// of at most RT / 2 rows does no other rows' arithmetic.
+// Few rows are bound by the memory, more by the reads of shared memory (nine of
+// 16 bytes for 32 multiply-adds a lane).  Measured (16 sequences of 4000 tokens,
+// 4 key/value heads; copy peak 6690 GB/s): head size 128, 2 rows 0.26 GB in
+// 52.6 us (4980 GB/s; all eight rows' arithmetic 75.9; with one CTA an SM for
+// 16-key chunks 90.8), 16 rows in two tiles 145.5 us; head size 64 32.1 and
+// 76.1 us (two CTAs an SM instead of three: 50.8 and 90.7 with eight rows each).
 template <int HD>
 struct Simt {
   using T = float;
   static constexpr int RT = 8;
+  static constexpr int CH = 1024 / HD;              // keys of a warp's step: 4 KB, and as much of values
   static constexpr int STAGES = 2;
   static constexpr int ROW = HD * sizeof(T);        // bytes of a key
   static constexpr int CPR = ROW / 16;              // 16-byte pieces of a key
-  static constexpr int STAGE = 2 * kChunk * ROW;    // keys, then values
+  static constexpr int STAGE = 2 * CH * ROW;        // keys, then values
   static constexpr int RING = STAGES * STAGE;       // of one warp
   static constexpr int MERGE = RT * (HD + 2) * 4;   // of one warp, over its ring
   static constexpr int OFF_Q = kWarps * (RING > MERGE ? RING : MERGE);
   static constexpr int OFF_P = OFF_Q + RT * HD * 4;
-  static constexpr int SMEM = OFF_P + kWarps * kChunk * RT * 4;
-  static constexpr int CTAS = HD == 64 ? 3 : 1;  // per SM: 68 or 135 KB each (head size 64 with two: 50.8, not 43.4 us)
+  static constexpr int SMEM = OFF_P + kWarps * CH * RT * 4;
+  static constexpr int CTAS = 3;  // per SM: 68 to 71 KB each
 };
 
 template <int HD>
 __global__ void __launch_bounds__(kThreads, Simt<HD>::CTAS) tree_attn_simt_kernel(const __grid_constant__ TreeArgs p) {
   using C = Simt<HD>;
   using T = float;
-  constexpr int RT = C::RT, DPL = HD / 32;  // dimensions of the output a lane holds
+  constexpr int RT = C::RT, CH = C::CH, DPL = HD / 32;  // dimensions of the output a lane holds
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ int16_t s_parent[SPECFOLD_MAX_TREE];
   __shared__ uint32_t s_sees[RT][SPECFOLD_MAX_TREE / 32];  // a tile row's ancestors and itself
@@ -108,7 +117,7 @@ __global__ void __launch_bounds__(kThreads, Simt<HD>::CTAS) tree_attn_simt_kerne
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = smem + warp * (C::RING > C::MERGE ? C::RING : C::MERGE);
   float* s_q = reinterpret_cast<float*>(smem + C::OFF_Q);
-  float* s_p = reinterpret_cast<float*>(smem + C::OFF_P) + warp * kChunk * RT;
+  float* s_p = reinterpret_cast<float*>(smem + C::OFF_P) + warp * CH * RT;
   const T* qp = static_cast<const T*>(p.q);
 
   for (bool first = true; w.n > 0; first = false, w.next(p)) {
@@ -141,26 +150,26 @@ __global__ void __launch_bounds__(kThreads, Simt<HD>::CTAS) tree_attn_simt_kerne
     }
     __syncthreads();
 
-    // this warp's chunks: key_lo + 16 * (warp + 4 i)
-    const int chunks = (key_hi - key_lo + kChunk - 1) / kChunk;
+    // this warp's chunks: key_lo + CH * (warp + 4 i)
+    const int chunks = (key_hi - key_lo + CH - 1) / CH;
     const int mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
-    auto key_of = [&](int i) { return key_lo + kChunk * (warp + kWarps * i); };
-    auto slot_of = [&](int i) {  // lanes 0..15: pool tokens of chunk i's keys
-      const int tok = key_of(i) + (lane & (kChunk - 1));
+    auto key_of = [&](int i) { return key_lo + CH * (warp + kWarps * i); };
+    auto slot_of = [&](int i) {  // lanes 0..CH-1: pool tokens of chunk i's keys
+      const int tok = key_of(i) + (lane & (CH - 1));
       return i < mine && tok < key_hi ? tree_pool_token(p, w.s, tok) : -1;
     };
     auto load = [&](int i, int slot) {
       if (i < mine) {
         uint8_t* st = ring + (i % C::STAGES) * C::STAGE;
 #pragma unroll
-        for (int it = 0; it < 2 * kChunk * C::CPR / 32; ++it) {
+        for (int it = 0; it < 2 * CH * C::CPR / 32; ++it) {
           const int idx = it * 32 + lane;
-          const int c = idx % C::CPR, key = (idx / C::CPR) % kChunk, is_v = idx / (C::CPR * kChunk);
+          const int c = idx % C::CPR, key = (idx / C::CPR) % CH, is_v = idx / (C::CPR * CH);
           const int tk = __shfl_sync(0xffffffffu, slot, key);
           const T* src = is_v ? static_cast<const T*>(p.cache.v) + tk * p.cache.v_token_stride + h * p.cache.v_head_stride
                               : static_cast<const T*>(p.cache.k) + tk * p.cache.k_token_stride + h * p.cache.k_head_stride;
           if (tk < 0) src = static_cast<const T*>(p.cache.k);  // any valid address: nothing is read
-          cp_async16(smem_u32(st + is_v * kChunk * C::ROW + key * C::ROW + ((c ^ (key & 7)) << 4)),
+          cp_async16(smem_u32(st + is_v * CH * C::ROW + key * C::ROW + ((c ^ (key & 7)) << 4)),
                      reinterpret_cast<const uint8_t*>(src) + (tk < 0 ? 0 : c * 16), tk < 0 ? 0u : 16u);
         }
       }
@@ -185,73 +194,84 @@ __global__ void __launch_bounds__(kThreads, Simt<HD>::CTAS) tree_attn_simt_kerne
       load(i, slot);
       slot = slot_of(i + 1);
     }
-    for (int i = 0; i < mine; ++i) {
-      load(i + C::STAGES - 1, slot);
-      slot = slot_of(i + C::STAGES);
-      cp_async_wait<C::STAGES - 1>();
-      __syncwarp();
-      const uint8_t* sk = ring + (i % C::STAGES) * C::STAGE;
-      const uint8_t* sv = sk + kChunk * C::ROW;
-      const int key = lane & (kChunk - 1), half = lane / kChunk;
-      float s[RT];
+    auto stream = [&](auto nr) {
+      constexpr int NR = decltype(nr)::value;  // rows worked on
+      for (int i = 0; i < mine; ++i) {
+        load(i + C::STAGES - 1, slot);
+        slot = slot_of(i + C::STAGES);
+        cp_async_wait<C::STAGES - 1>();
+        __syncwarp();
+        const uint8_t* sk = ring + (i % C::STAGES) * C::STAGE;
+        const uint8_t* sv = sk + CH * C::ROW;
+        const int key = lane & (CH - 1), part = lane / CH;
+        float s[NR];
 #pragma unroll
-      for (int r = 0; r < RT; ++r) s[r] = 0.f;
-#pragma unroll 4
-      for (int d = 0; d < HD / 2; d += 4) {
-        const float4 k4 = load4(at(sk, key, half * (HD / 2) + d));
+        for (int r = 0; r < NR; ++r) s[r] = 0.f;
 #pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          const float4 q4 = load4(s_q + r * HD + half * (HD / 2) + d);
-          s[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[r]))));
-        }
-      }
-      const int tok = key_of(i) + key, e = tok - w.q.ctx;
-      const bool tail = key_of(i) + kChunk > w.q.ctx;  // holds tokens that not every row sees
-      float pr[RT];
+        for (int d = 0; d < 32; d += 4) {
+          const float4 k4 = load4(at(sk, key, part * 32 + d));
 #pragma unroll
-      for (int r = 0; r < RT; ++r) {
-        s[r] += __shfl_xor_sync(0xffffffffu, s[r], kChunk);
-        bool see = !s_dead[r];
-        if (tail) see = see && tok < key_hi && (e < 0 || (s_sees[r][(e >> 5) & 7] >> (e & 31) & 1u));
-        s[r] = see ? s[r] * p.sl2 : -INFINITY;
-        float m = s[r];
-#pragma unroll
-        for (int o = kChunk / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        m = fmaxf(m, mx[r]);
-        const float base = m == -INFINITY ? 0.f : m;
-        const float alpha = mx[r] == m ? 1.f : ex2(mx[r] - base);
-        pr[r] = see ? ex2(s[r] - base) : 0.f;
-        mx[r] = m;
-        l[r] = l[r] * alpha + pr[r];
-        if (alpha != 1.f) {
-#pragma unroll
-          for (int d = 0; d < DPL; ++d) acc[r][d] *= alpha;
-        }
-      }
-      if (half == 0) {
-        store4(s_p + key * RT, make_float4(pr[0], pr[1], pr[2], pr[3]));
-        store4(s_p + key * RT + 4, make_float4(pr[4], pr[5], pr[6], pr[7]));
-      }
-      __syncwarp();
-#pragma unroll 4
-      for (int k = 0; k < kChunk; ++k) {
-        float v[DPL];
-        const T* vp = at(sv, k, lane * DPL);
-#pragma unroll
-        for (int d = 0; d < DPL; ++d) v[d] = static_cast<float>(vp[d]);
-        const float4 pa = load4(s_p + k * RT), pb = load4(s_p + k * RT + 4);
-        const float pk[RT] = {pa.x, pa.y, pa.z, pa.w, pb.x, pb.y, pb.z, pb.w};
-#pragma unroll
-        for (int r = 0; r < RT; ++r) {
-          // a token the row does not see adds nothing, whatever its value
-          if (!tail || pk[r] != 0.f) {
-#pragma unroll
-            for (int d = 0; d < DPL; ++d) acc[r][d] = fmaf(pk[r], v[d], acc[r][d]);
+          for (int r = 0; r < NR; ++r) {
+            const float4 q4 = load4(s_q + r * HD + part * 32 + d);
+            s[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[r]))));
           }
         }
+        const int tok = key_of(i) + key, e = tok - w.q.ctx;
+        const bool tail = key_of(i) + CH > w.q.ctx;  // holds tokens that not every row sees
+        float pr[NR];
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+#pragma unroll
+          for (int o = CH; o < 32; o <<= 1) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+          bool see = !s_dead[r];
+          if (tail) see = see && tok < key_hi && (e < 0 || (s_sees[r][(e >> 5) & 7] >> (e & 31) & 1u));
+          s[r] = see ? s[r] * p.sl2 : -INFINITY;
+          float m = s[r];
+#pragma unroll
+          for (int o = CH / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+          m = fmaxf(m, mx[r]);
+          const float base = m == -INFINITY ? 0.f : m;
+          const float alpha = mx[r] == m ? 1.f : ex2(mx[r] - base);
+          pr[r] = see ? ex2(s[r] - base) : 0.f;
+          mx[r] = m;
+          l[r] = l[r] * alpha + pr[r];
+          if (alpha != 1.f) {
+#pragma unroll
+            for (int d = 0; d < DPL; ++d) acc[r][d] *= alpha;
+          }
+        }
+        if (part == 0) {
+#pragma unroll
+          for (int r = 0; r < NR; r += 4) store4(s_p + key * RT + r, make_float4(pr[r], pr[r + 1], pr[r + 2], pr[r + 3]));
+        }
+        __syncwarp();
+#pragma unroll 4
+        for (int k = 0; k < CH; ++k) {
+          float v[DPL];
+          const T* vp = at(sv, k, lane * DPL);
+#pragma unroll
+          for (int d = 0; d < DPL; ++d) v[d] = static_cast<float>(vp[d]);
+#pragma unroll
+          for (int r0 = 0; r0 < NR; r0 += 4) {
+            const float4 p4 = load4(s_p + k * RT + r0);
+            const float pk[4] = {p4.x, p4.y, p4.z, p4.w};
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+              // a token the row does not see adds nothing, whatever its value
+              if (!tail || pk[r] != 0.f) {
+#pragma unroll
+                for (int d = 0; d < DPL; ++d) acc[r0 + r][d] = fmaf(pk[r], v[d], acc[r0 + r][d]);
+              }
+            }
+          }
+        }
+        __syncwarp();  // the stage and the probabilities may be overwritten
       }
-      __syncwarp();  // the stage and the probabilities may be overwritten
-    }
+    };
+    if (rows <= RT / 2)
+      stream(std::integral_constant<int, RT / 2>{});
+    else
+      stream(std::integral_constant<int, RT>{});
     cp_async_wait<0>();
     __syncwarp();
 
@@ -261,7 +281,7 @@ __global__ void __launch_bounds__(kThreads, Simt<HD>::CTAS) tree_attn_simt_kerne
     for (int r = 0; r < RT; ++r) {
       float ls = l[r];
 #pragma unroll
-      for (int o = kChunk / 2; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
+      for (int o = CH / 2; o > 0; o >>= 1) ls += __shfl_xor_sync(0xffffffffu, ls, o);
 #pragma unroll
       for (int d = 0; d < DPL; ++d) mo[r * HD + lane * DPL + d] = acc[r][d];
       if (lane == 0) {
@@ -276,10 +296,10 @@ __global__ void __launch_bounds__(kThreads, Simt<HD>::CTAS) tree_attn_simt_kerne
 
 // ---------------------------------------------------- few rows, bf16: mma --
 // Up to RT = 16 MT rows of a head group (a whole sequence's nodes times the
-// group; MT 2 for head size 64 alone): decoding and small trees.  Such a unit does at most 32 operations a
-// byte of cache, so the memory bounds it and warp-level matrix instructions,
-// whose rows fit, are enough; what counts is bytes in flight and no barrier
-// between them.  So, as above, each of the four warps streams its own 4 KB
+// group; MT 2 for head size 64 alone): decoding and small trees.  Such a unit
+// does at most 32 operations a byte of cache, so the memory bounds it and
+// warp-level matrix instructions, whose rows fit, are enough; what counts is
+// bytes in flight and no barrier between them.  So, as above, each of the four warps streams its own 4 KB
 // chunks of keys through a private ring of asynchronous copies:
 //   S [rows x chunk] = Q K^T, keys as the B operand straight from their rows;
 //   O [rows x HD] += P V, P from S's registers (rounded to bf16, the tensor
@@ -734,9 +754,9 @@ Plan plan_of(int dtype, int g, int hd, int max_nodes) {
   const int rows = max_nodes * g;
   if (dtype == SPECFOLD_BF16) {
     if (rows > (hd == 128 ? 16 : 32)) return {1, kTreeTcRows, kTreeTcKeys, 5, 5, 3};
-    return {Few<128, 1>::CTAS, rows <= 16 ? 16 : 32, 64, 2, 1, 1};
+    return {Few<128, 1>::CTAS, rows <= 16 ? 16 : 32, kFewKeys, 2, 1, 1};
   }
-  return {hd == 128 ? Simt<128>::CTAS : Simt<64>::CTAS, 8, 4 * kChunk, 1, 1, 1};
+  return {Simt<128>::CTAS, Simt<128>::RT, kFewKeys, 1, 1, 1};
 }
 
 int tree_start(void (*kernel)(TreeArgs), int smem, const TreeArgs& a, int grid, cudaStream_t st) {
