@@ -27,8 +27,9 @@ namespace {
 constexpr int kThreads = 256;
 // Resident blocks an SM, which cap the registers.  Measured (16381 rows of 24 + 8
 // heads; 16331 rows of 8 heads appended): 2, 3, 4, 5 blocks 56.5, 48.3, 46.3,
-// 68.5 us and 24.0, 21.0, 23.8, 27.5 us: fewer hold too few bytes in flight, more
-// spill.
+// 68.5 us and 24.0, 21.0, 23.8, 27.5 us (one group in flight): fewer hold too few
+// bytes in flight, more spill.  That is 5800 GB/s of the rows' 268 MB (copy peak
+// 6690); head size 64 5740, fp32 5450 to 5590.
 constexpr int kQkBlocks = 4, kAppendBlocks = 3;
 
 // A lane's two runs of eight elements as they lie in memory: what a warp has in
@@ -346,7 +347,8 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) kv_append_kernel(cons
         }
       }
     };
-    // (16331 rows of 8 heads: 21.0 us with one, 19.9 with two, 21.3 with three)
+    // (16331 rows of 8 heads, 134 MB of which L2 keeps a part: 21.0 us with one,
+    // 19.9 with two, 21.3 with three; fp32 has as many bytes in one)
     constexpr int kDepth = sizeof(T) == 2 ? 2 : 1;
     Raw<T> flight[kDepth] = {};
     At ahead = {0, 0}, now = {0, 0};
