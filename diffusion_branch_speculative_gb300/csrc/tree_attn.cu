@@ -630,61 +630,109 @@ __global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_ker
 }
 
 // ---------------------------------------------------------------- combine --
-// Merges the partials of cut units: block (c, y) has the unit that CTA c's
-// start cuts first, one warp per row.  The partials of one unit lie at its
-// first CTA's slot and at the first slots of the CTAs after it.
-constexpr int kCombineRows = 8;
+// Merges the partials of cut units: block (c, y) has eight rows of the unit that
+// CTA c's start cuts first.  The partials of one unit lie at its first CTA's slot
+// and at the first slots of the CTAs after it; each of the block's warps takes
+// every eighth of them, all rows at once, with a running maximum and sum of its
+// own, and the warps merge at the end.  One sequence of 40000 tokens (76 partials
+// a unit of 7 rows) takes 22.2 us in all, 28.5 with a warp a row that goes through
+// its partials alone; 64 sequences of 8000 (2 a unit) take 168 us either way.
+// More loads at once (22.6 and 172) cost registers, and with them blocks.  Merging
+// by the last CTA of a unit to arrive, without a launch: 26.5 and 184, and 12.4
+// instead of 11.3 for 8 sequences of 500.
+constexpr int kCombineRows = 8, kCombineWarps = 8;
 
 template <typename T, int HD>
-__global__ void __launch_bounds__(kCombineRows * 32) tree_combine_kernel(const __grid_constant__ TreeArgs p) {
+__global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const __grid_constant__ TreeArgs p) {
+  constexpr int R = kCombineRows, DPL = HD / 32;
+  __shared__ __align__(16) float s_o[kCombineWarps][R][HD];
+  __shared__ float s_m[kCombineWarps][R], s_l[kCombineWarps][R];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x + 1;
+  const int c = blockIdx.x + 1, warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const int4 a = p.desc[2 * c], b = p.desc[2 * c + 1];
-  const int r = blockIdx.y * kCombineRows + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (r >= a.x) return;
-  constexpr int DPL = HD / 32;
+  const int r0 = blockIdx.y * R, rows = min(R, a.x - r0);
+  if (rows <= 0) return;
   const int n = b.y - b.x + 1;
-  auto slot = [&](int z) { return static_cast<size_t>(z == 0 ? b.z : 2 * (b.x + z)) * p.tile_rows + r; };
-  float M = -INFINITY;
-  for (int z = lane; z < n; z += 32) M = fmaxf(M, p.part_ml[slot(z) * 2]);
+  auto slot = [&](int z) { return static_cast<size_t>(z == 0 ? b.z : 2 * (b.x + z)) * p.tile_rows + r0; };
+  // statistics: a lane has row lane & 7 of the (lane >> 3)-th of four partials
+  const int row = lane & (R - 1), zi = lane / R;
+  float m = -INFINITY, l = 0.f, acc[R][DPL] = {};
+  auto stats = [&](int k) {  // of this warp's partials 4 k .. 4 k + 3
+    const int z = warp + kCombineWarps * (4 * k + zi);
+    return z < n && row < rows ? *reinterpret_cast<const float2*>(p.part_ml + (slot(z) + row) * 2)
+                               : make_float2(-INFINITY, 0.f);
+  };
+  float2 next = stats(0);
+#pragma unroll 1
+  for (int k = 0; warp + kCombineWarps * 4 * k < n; ++k) {
+    const float2 ml = next;
+    next = stats(k + 1);
+    float top = fmaxf(ml.x, __shfl_xor_sync(0xffffffffu, ml.x, 8));
+    top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)), m);
+    const float alpha = merge_weight(m, top), wz = merge_weight(ml.x, top);
+    m = top;
+    float add = wz * ml.y;
+    add += __shfl_xor_sync(0xffffffffu, add, 8);
+    add += __shfl_xor_sync(0xffffffffu, add, 16);
+    l = l * alpha + add;
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-  float L = 0.f, acc[DPL] = {};
-  for (int z0 = 0; z0 < n; z0 += 32) {
-    float wz = 0.f, lz = 0.f;
-    if (z0 + lane < n) {
-      const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + slot(z0 + lane) * 2);
-      wz = merge_weight(ml.x, M);
-      lz = ml.y * wz;
+    for (int r = 0; r < R; ++r) {
+      const float f = __shfl_sync(0xffffffffu, alpha, r);
+#pragma unroll
+      for (int d = 0; d < DPL; ++d) acc[r][d] *= f;
     }
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) lz += __shfl_xor_sync(0xffffffffu, lz, o);
-    L += lz;
-    const int m = min(32, n - z0);
-#pragma unroll 4
-    for (int z = 0; z < m; ++z) {
-      const float wv = __shfl_sync(0xffffffffu, wz, z);
-      const float* v = p.part_o + slot(z0 + z) * HD + lane * DPL;
-      if constexpr (DPL == 4) {
-        const float4 x = load4(v);
-        acc[0] = fmaf(wv, x.x, acc[0]);
-        acc[1] = fmaf(wv, x.y, acc[1]);
-        acc[2] = fmaf(wv, x.z, acc[2]);
-        acc[3] = fmaf(wv, x.w, acc[3]);
-      } else {
-        const float2 x = *reinterpret_cast<const float2*>(v);
-        acc[0] = fmaf(wv, x.x, acc[0]);
-        acc[1] = fmaf(wv, x.y, acc[1]);
+    for (int i = 0; i < 4; ++i) {
+      const int z = warp + kCombineWarps * (4 * k + i);
+      const float* from = p.part_o + slot(z) * HD + lane * DPL;
+      float v[R][DPL];
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const bool there = z < n && r < rows;
+        if constexpr (DPL == 4) {
+          const float4 x = there ? load4(from + r * HD) : make_float4(0.f, 0.f, 0.f, 0.f);
+          v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
+        } else {
+          const float2 x = there ? *reinterpret_cast<const float2*>(from + r * HD) : make_float2(0.f, 0.f);
+          v[r][0] = x.x, v[r][1] = x.y;
+        }
+      }
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+        const float f = __shfl_sync(0xffffffffu, wz, i * R + r);
+#pragma unroll
+        for (int d = 0; d < DPL; ++d) acc[r][d] = fmaf(f, v[r][d], acc[r][d]);
       }
     }
   }
+#pragma unroll
+  for (int r = 0; r < R; ++r)
+#pragma unroll
+    for (int d = 0; d < DPL; ++d) s_o[warp][r][lane * DPL + d] = acc[r][d];
+  if (lane < R) {
+    s_m[warp][lane] = m;
+    s_l[warp][lane] = l;
+  }
+  __syncthreads();
+  const int r = warp;  // a warp a row
+  if (r >= rows) return;
+  float M = -INFINITY, L = 0.f, out[DPL] = {};
+#pragma unroll
+  for (int k = 0; k < kCombineWarps; ++k) M = fmaxf(M, s_m[k][r]);
+#pragma unroll
+  for (int k = 0; k < kCombineWarps; ++k) {
+    const float f = merge_weight(s_m[k][r], M);
+    L = fmaf(f, s_l[k][r], L);
+#pragma unroll
+    for (int d = 0; d < DPL; ++d) out[d] = fmaf(f, s_o[k][r][lane * DPL + d], out[d]);
+  }
   const float sc = merge_scale(L);
-  const int m = a.z + r;
-  T* dst = static_cast<T*>(p.o) + (a.y + m / p.g) * p.o_rs + (a.w * p.g + m % p.g) * p.o_hs + lane * DPL;
+  const int at = a.z + r0 + r;
+  T* dst = static_cast<T*>(p.o) + (a.y + at / p.g) * p.o_rs + (a.w * p.g + at % p.g) * p.o_hs + lane * DPL;
 #pragma unroll
   for (int d = 0; d < DPL; d += 2) {
-    const float x = L == 0.f ? 0.f : acc[d] * sc, y = L == 0.f ? 0.f : acc[d + 1] * sc;
+    const float x = L == 0.f ? 0.f : out[d] * sc, y = L == 0.f ? 0.f : out[d + 1] * sc;
     if constexpr (sizeof(T) == 2)
       *reinterpret_cast<uint32_t*>(dst + d) = pack_bf16x2(x, y);
     else
@@ -814,8 +862,8 @@ int tree_go(const TreeAttnCall& c, const Plan& pl, cudaStream_t st) {
     launch_k(tree_combine_quads_kernel<HD>, dim3(grid - 1, kTreeTcRows / 32, HD / 4 / kCombineQuads),
              dim3(kCombineQuads * 32), 0, st, a);
   else
-    launch_k(tree_combine_kernel<T, HD>, dim3(grid - 1, (pl.tile_rows + kCombineRows - 1) / kCombineRows),
-             dim3(kCombineRows * 32), 0, st, a);
+    launch_k(tree_combine_kernel<T, HD>, dim3(grid - 1, (std::min(pl.tile_rows, a.max_nodes * a.g) + kCombineRows - 1) / kCombineRows),
+             dim3(kCombineWarps * 32), 0, st, a);
   count_launch();
   return check_launch();
 }
