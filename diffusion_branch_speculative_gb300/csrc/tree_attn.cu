@@ -740,46 +740,96 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
   }
 }
 
-// The same for partials stored [quad of columns][row]: a warp has 32 rows and
-// one quad, so that every load is 512 bytes side by side; block (c, rows, quads).
-// Latency bounds both: some 4 us behind the attention, for 14 MB of partials of
-// one long sequence as for a few rows.
-constexpr int kCombineQuads = 8;
+// The same for the tcgen05 kernel's partials, up to 256 rows each, stored [quad of
+// columns][row]: an item is 32 rows and eight quads of a cut unit, a warp a quad,
+// so that every load is 512 bytes side by side.  Every block counts all units'
+// items (one round trip) and takes its share.  The case of one sequence of 40000
+// tokens, 19 partials of 183 rows a unit, takes 51.5 us with this merge; with a
+// block a possible item (four rounds of blocks, most of them empty), which read
+// the maxima first, 58.5.  Batches of 2, 4, 8 partials: 55.5, 51.5, 50.0, and for
+// padded batches (2 or 3 a unit) 64.4, 64.3, 67.1.
+constexpr int kCombineQuads = 8, kCombineThreads = kCombineQuads * 32;
+constexpr int kCombineBlocks = 8;  // per SM
+constexpr int kCombineBatch = 4;   // partials read at once
+static_assert(kSmBudget <= kCombineThreads, "a thread a run");
 
 template <int HD>
-__global__ void __launch_bounds__(kCombineQuads * 32) tree_combine_quads_kernel(const __grid_constant__ TreeArgs p) {
+__global__ void __launch_bounds__(kCombineThreads) tree_combine_quads_kernel(const __grid_constant__ TreeArgs p, int runs) {
+  constexpr int GROUPS = HD / 4 / kCombineQuads;  // of quads
+  __shared__ int s_warp[kCombineThreads / 32], s_end[kCombineThreads];
   pdl_wait();
   pdl_trigger();
-  const int c = blockIdx.x + 1;
-  const int4 a = p.desc[2 * c], b = p.desc[2 * c + 1];
-  const int lane = threadIdx.x & 31;
-  if (static_cast<int>(blockIdx.y) * 32 >= a.x) return;
-  const int r = min(static_cast<int>(blockIdx.y) * 32 + lane, a.x - 1);
-  const int quad = blockIdx.z * kCombineQuads + (threadIdx.x >> 5);
-  const int n = b.y - b.x + 1;
-  auto slot = [&](int z) { return static_cast<size_t>(z == 0 ? b.z : 2 * (b.x + z)) * p.tile_rows; };
-  float M = -INFINITY;
-#pragma unroll 8
-  for (int z = 0; z < n; ++z) M = fmaxf(M, p.part_ml[(slot(z) + r) * 2]);
-  float L = 0.f;
-  float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-  for (int z = 0; z < n; ++z) {
-    const float2 ml = *reinterpret_cast<const float2*>(p.part_ml + (slot(z) + r) * 2);
-    const float4 v = *reinterpret_cast<const float4*>(p.part_o + slot(z) * HD + (quad * p.tile_rows + r) * 4);
-    const float wz = merge_weight(ml.x, M);
-    L = fmaf(wz, ml.y, L);
-    acc.x = fmaf(wz, v.x, acc.x);
-    acc.y = fmaf(wz, v.y, acc.y);
-    acc.z = fmaf(wz, v.z, acc.z);
-    acc.w = fmaf(wz, v.w, acc.w);
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // thread t: the items of the unit that CTA t + 1's start cuts first, and of those before
+  int end = static_cast<int>(threadIdx.x) + 1 < runs ? (p.desc[2 * (threadIdx.x + 1)].x + 31) / 32 * GROUPS : 0;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, end, o);
+    if (lane >= o) end += u;
   }
-  if (static_cast<int>(blockIdx.y) * 32 + lane >= a.x) return;
-  const float sc = merge_scale(L);
-  if (L == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
-  const int m = a.z + r;
-  store4(static_cast<__nv_bfloat16*>(p.o) + (a.y + m / p.g) * p.o_rs + (a.w * p.g + m % p.g) * p.o_hs + quad * 4,
-         make_float4(acc.x * sc, acc.y * sc, acc.z * sc, acc.w * sc));
+  if (lane == 31) s_warp[warp] = end;
+  __syncthreads();
+  int total = 0;
+#pragma unroll
+  for (int k = 0; k < kCombineThreads / 32; ++k) {
+    if (k == warp) end += total;
+    total += s_warp[k];
+  }
+  s_end[threadIdx.x] = end;
+  __syncthreads();
+  for (int item = blockIdx.x; item < total; item += gridDim.x) {
+    int lo = -1, hi = kCombineThreads - 1;  // the first unit that ends past the item
+    while (hi - lo > 1) {
+      const int mid = (lo + hi) >> 1;
+      if (s_end[mid] > item)
+        hi = mid;
+      else
+        lo = mid;
+    }
+    const int4 a = p.desc[2 * (hi + 1)], b = p.desc[2 * (hi + 1) + 1];
+    const int at = item - (hi > 0 ? s_end[hi - 1] : 0);
+    const int row = at / GROUPS * 32 + lane, r = min(row, a.x - 1);
+    const int quad = at % GROUPS * kCombineQuads + warp;
+    const int n = b.y - b.x + 1;
+    auto slot = [&](int z) { return static_cast<size_t>(z == 0 ? b.z : 2 * (b.x + z)) * p.tile_rows; };
+    float M = -INFINITY, L = 0.f;
+    float4 acc = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 1
+    for (int z0 = 0; z0 < n; z0 += kCombineBatch) {
+      float2 ml[kCombineBatch];
+      float4 v[kCombineBatch];
+#pragma unroll
+      for (int z = 0; z < kCombineBatch; ++z) {
+        const size_t at_z = slot(min(z0 + z, n - 1));  // (no branch between the loads)
+        ml[z] = *reinterpret_cast<const float2*>(p.part_ml + (at_z + r) * 2);
+        v[z] = load4(p.part_o + at_z * HD + (quad * p.tile_rows + r) * 4);
+        if (z0 + z >= n) ml[z] = make_float2(-INFINITY, 0.f);
+      }
+      float top = M;
+#pragma unroll
+      for (int z = 0; z < kCombineBatch; ++z) top = fmaxf(top, ml[z].x);
+      const float alpha = merge_weight(M, top);
+      M = top;
+      L *= alpha;
+      acc = make_float4(acc.x * alpha, acc.y * alpha, acc.z * alpha, acc.w * alpha);
+#pragma unroll
+      for (int z = 0; z < kCombineBatch; ++z) {
+        const bool there = z0 + z < n;
+        const float wz = there ? merge_weight(ml[z].x, top) : 0.f;
+        L = fmaf(wz, ml[z].y, L);
+        acc.x = fmaf(wz, there ? v[z].x : 0.f, acc.x);
+        acc.y = fmaf(wz, there ? v[z].y : 0.f, acc.y);
+        acc.z = fmaf(wz, there ? v[z].z : 0.f, acc.z);
+        acc.w = fmaf(wz, there ? v[z].w : 0.f, acc.w);
+      }
+    }
+    if (row >= a.x) continue;
+    const float sc = merge_scale(L);
+    if (L == 0.f) acc = make_float4(0.f, 0.f, 0.f, 0.f);
+    const int m = a.z + r;
+    store4(static_cast<__nv_bfloat16*>(p.o) + (a.y + m / p.g) * p.o_rs + (a.w * p.g + m % p.g) * p.o_hs + quad * 4,
+           make_float4(acc.x * sc, acc.y * sc, acc.z * sc, acc.w * sc));
+  }
 }
 
 // --------------------------------------------------------------- launches --
@@ -859,8 +909,7 @@ int tree_go(const TreeAttnCall& c, const Plan& pl, cudaStream_t st) {
   if (rc) return rc;
   if (grid == 1) return SPECFOLD_OK;
   if (sizeof(T) == 2 && pl.tile_rows == kTreeTcRows)
-    launch_k(tree_combine_quads_kernel<HD>, dim3(grid - 1, kTreeTcRows / 32, HD / 4 / kCombineQuads),
-             dim3(kCombineQuads * 32), 0, st, a);
+    launch_k(tree_combine_quads_kernel<HD>, dim3(kCombineBlocks * num_sms()), dim3(kCombineThreads), 0, st, a, grid);
   else
     launch_k(tree_combine_kernel<T, HD>, dim3(grid - 1, (std::min(pl.tile_rows, a.max_nodes * a.g) + kCombineRows - 1) / kCombineRows),
              dim3(kCombineWarps * 32), 0, st, a);
