@@ -308,9 +308,9 @@ __global__ void __launch_bounds__(kThreads, Simt<HD>::CTAS) tree_attn_simt_kerne
 // 64 KB in flight an SM would cover the latency at full bandwidth; two CTAs of
 // 96 KB keep it covered while one of them merges.  Measured (32 sequences of 8000
 // tokens, 8 key/value heads, 4 rows; copy peak 6690 GB/s): head size 128
-// 1.05 GB in 166.5 us (6300 GB/s; one CTA an SM 232.7), head size 64 0.52 GB in
-// 99.6 us (5260 GB/s; chunks of 16 keys with two or four CTAs 107.4 and 116.5).
-// 8 sequences of 500 tokens: 11.5 and 8.8 us, the latency of the two launches.
+// 1.05 GB in 162 us (6470 GB/s; one CTA an SM 233), head size 64 0.52 GB in
+// 90 us (5820 GB/s; chunks of 16 keys with two or four CTAs 107 and 117).
+// 8 sequences of 500 tokens: 10.9 and 8.6 us, the latency of the two launches.
 template <int HD, int MT>
 struct Few {
   static constexpr int RT = 16 * MT;
@@ -630,21 +630,22 @@ __global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_ker
 }
 
 // ---------------------------------------------------------------- combine --
-// Merges the partials of cut units: block (c, y) has eight rows of the unit that
+// Merges the partials of cut units: block (c, y) has four rows of the unit that
 // CTA c's start cuts first.  The partials of one unit lie at its first CTA's slot
 // and at the first slots of the CTAs after it; each of the block's warps takes
 // every eighth of them, all rows at once, with a running maximum and sum of its
 // own, and the warps merge at the end.  One sequence of 40000 tokens (76 partials
-// a unit of 7 rows) takes 22.2 us in all, 28.5 with a warp a row that goes through
-// its partials alone; 64 sequences of 8000 (2 a unit) take 168 us either way.
-// More loads at once (22.6 and 172) cost registers, and with them blocks.  Merging
-// by the last CTA of a unit to arrive, without a launch: 26.5 and 184, and 12.4
-// instead of 11.3 for 8 sequences of 500.
-constexpr int kCombineRows = 8, kCombineWarps = 8;
+// a unit of 7 rows) takes 19.9 us in all, 28.5 with a warp a row that goes through
+// its partials alone; 64 sequences of 8000 (2 a unit) 168 us either way.  Eight
+// rows a block: 20.9, two 19.6 but 14.5 instead of 12.4 for 8 sequences of 500
+// tokens and 32 rows; four warps a block 23.4.  Merging by the last CTA of a unit
+// to arrive, without a launch: 26.5 and 184, and 12.4 instead of 10.9 for 8
+// sequences of 500 and 4 rows.
+constexpr int kCombineRows = 4, kCombineWarps = 8;
 
 template <typename T, int HD>
 __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const __grid_constant__ TreeArgs p) {
-  constexpr int R = kCombineRows, DPL = HD / 32;
+  constexpr int R = kCombineRows, ZS = 32 / R, DPL = HD / 32;
   __shared__ __align__(16) float s_o[kCombineWarps][R][HD];
   __shared__ float s_m[kCombineWarps][R], s_l[kCombineWarps][R];
   pdl_wait();
@@ -655,26 +656,27 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
   if (rows <= 0) return;
   const int n = b.y - b.x + 1;
   auto slot = [&](int z) { return static_cast<size_t>(z == 0 ? b.z : 2 * (b.x + z)) * p.tile_rows + r0; };
-  // statistics: a lane has row lane & 7 of the (lane >> 3)-th of four partials
+  // statistics: a lane has row lane % R of the (lane / R)-th of ZS partials
   const int row = lane & (R - 1), zi = lane / R;
   float m = -INFINITY, l = 0.f, acc[R][DPL] = {};
-  auto stats = [&](int k) {  // of this warp's partials 4 k .. 4 k + 3
-    const int z = warp + kCombineWarps * (4 * k + zi);
+  auto stats = [&](int k) {  // of this warp's partials from the (ZS k)-th on
+    const int z = warp + kCombineWarps * (ZS * k + zi);
     return z < n && row < rows ? *reinterpret_cast<const float2*>(p.part_ml + (slot(z) + row) * 2)
                                : make_float2(-INFINITY, 0.f);
   };
   float2 next = stats(0);
 #pragma unroll 1
-  for (int k = 0; warp + kCombineWarps * 4 * k < n; ++k) {
+  for (int k = 0; warp + kCombineWarps * ZS * k < n; ++k) {
     const float2 ml = next;
     next = stats(k + 1);
-    float top = fmaxf(ml.x, __shfl_xor_sync(0xffffffffu, ml.x, 8));
-    top = fmaxf(fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16)), m);
+    float top = fmaxf(ml.x, m);
+#pragma unroll
+    for (int o = R; o < 32; o <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
     const float alpha = merge_weight(m, top), wz = merge_weight(ml.x, top);
     m = top;
     float add = wz * ml.y;
-    add += __shfl_xor_sync(0xffffffffu, add, 8);
-    add += __shfl_xor_sync(0xffffffffu, add, 16);
+#pragma unroll
+    for (int o = R; o < 32; o <<= 1) add += __shfl_xor_sync(0xffffffffu, add, o);
     l = l * alpha + add;
 #pragma unroll
     for (int r = 0; r < R; ++r) {
@@ -683,13 +685,14 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
       for (int d = 0; d < DPL; ++d) acc[r][d] *= f;
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int z = warp + kCombineWarps * (4 * k + i);
+    for (int i = 0; i < ZS; ++i) {
+      const int z = warp + kCombineWarps * (ZS * k + i);
+      if (z >= n) break;
       const float* from = p.part_o + slot(z) * HD + lane * DPL;
       float v[R][DPL];
 #pragma unroll
       for (int r = 0; r < R; ++r) {
-        const bool there = z < n && r < rows;
+        const bool there = r < rows;
         if constexpr (DPL == 4) {
           const float4 x = there ? load4(from + r * HD) : make_float4(0.f, 0.f, 0.f, 0.f);
           v[r][0] = x.x, v[r][1] = x.y, v[r][2] = x.z, v[r][3] = x.w;
@@ -715,7 +718,8 @@ __global__ void __launch_bounds__(kCombineWarps * 32) tree_combine_kernel(const 
     s_l[warp][lane] = l;
   }
   __syncthreads();
-  const int r = warp;  // a warp a row
+  static_assert(kCombineWarps >= R, "a warp a row");
+  const int r = warp;
   if (r >= rows) return;
   float M = -INFINITY, L = 0.f, out[DPL] = {};
 #pragma unroll
@@ -842,11 +846,12 @@ struct Plan {
 // instructions take the few-rows kernel, more the tcgen05 one.  Both sides
 // (few-rows, tcgen05; us; 8 key/value heads, groups of 4):
 //   sequences x tokens       32 x 8000      1 x 40000     8 x 500
-//   head size 128, 16 rows   171.1  173.8   42.8  43.8    12.4  16.4
-//                  32 rows   184.4  175.0   49.0  44.3    16.4  16.4
-//   head size 64,  16 rows   101.3  143.5   22.8  29.1     9.6  13.5
-//                  32 rows   107.9  143.2   28.5  29.3    12.0  13.6
-//                  64 rows   201.0  147.9   46.2  29.6    17.0  15.1  (chunks of 16 keys)
+//   head size 128, 16 rows   167.9  167.3   36.8  39.8    12.1  14.8
+//                  20 rows   180.2  168.1   42.3  41.2    15.1  15.0
+//                  32 rows   186.5  169.0   44.5  40.7    17.0  15.3
+//   head size 64,  16 rows    94.2  137.4   19.1  26.9     9.4  13.8
+//                  32 rows   107.3  139.0   25.5  27.3    12.5  14.1
+//                  64 rows   199.5  141.1   37.2  27.9    16.8  15.4
 // Two row tiles for head size 64 and 16 rows: 105.1, 33.8, 11.7 (chunks of 16).
 // A unit's start is worth 2 to 8 blocks without a difference above 2 %, and so are
 // weights of 3:2 to 2:1 of a block's full and half tiles.
