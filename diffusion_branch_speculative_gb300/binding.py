@@ -350,6 +350,7 @@ class PagedCache:
 # These calls are short next to a Python call's own cost, so their checks read
 # each property of a tensor once and the stream comes as its raw handle.
 _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+_current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
 _NO_ROWS = specfold_head_rows(None, 0, 0)
 
 
@@ -366,7 +367,8 @@ def _vec(t: Optional[torch.Tensor], n: int, dtype, dev: int, what: str):
     """Pointer of a contiguous vector of at least n entries (None: NULL)."""
     if t is None:
         return None
-    if t.dim() != 1 or t.dtype is not dtype or t.get_device() != dev or t.shape[0] < n or (n > 1 and t.stride(0) != 1):
+    if (t.dtype is not dtype or t.get_device() != dev or t.numel() < n
+            or t.stride() != (1,) and (t.dim() != 1 or n > 1)):
         raise ValueError(f"{what} must be a contiguous {dtype} vector of {n} entries on the same device")
     return t.data_ptr()
 
@@ -381,7 +383,7 @@ def _device_of(t: torch.Tensor) -> int:
 def _call(fn, what: str, dev: int, stream, *args):
     """fn(*args, stream) with the tensors' device current: on `stream`, or on
     that device's current stream."""
-    here = torch.cuda.current_device()
+    here = _current_device()
     if here != dev:
         torch.cuda.set_device(dev)
     try:
