@@ -78,9 +78,9 @@ SF_DEV void merge_warps(const TreeArgs& p, const TreeWalk& w, bool first, const 
 // Few rows are bound by the memory, more by the reads of shared memory (nine of
 // 16 bytes for 32 multiply-adds a lane).  Measured (16 sequences of 4000 tokens,
 // 4 key/value heads; copy peak 6690 GB/s): head size 128, 2 rows 0.26 GB in
-// 52.6 us (4980 GB/s; all eight rows' arithmetic 75.9; with one CTA an SM for
-// 16-key chunks 90.8), 16 rows in two tiles 145.5 us; head size 64 32.1 and
-// 76.1 us (two CTAs an SM instead of three: 50.8 and 90.7 with eight rows each).
+// 51.4 us (5100 GB/s; all eight rows' arithmetic 75.9; with one CTA an SM for
+// 16-key chunks 90.8), 16 rows in two tiles 144.5 us; head size 64 31.2 and
+// 75.3 us (two CTAs an SM instead of three: 50.8 and 90.7 with eight rows each).
 template <int HD>
 struct Simt {
   using T = float;
