@@ -101,7 +101,7 @@ int make_map_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols
 }
 
 int make_map_3d(CUtensorMap* map, const void* base, uint64_t dim, uint64_t heads, uint64_t tokens,
-                uint64_t head_stride, uint64_t token_stride, uint32_t box_tokens) {
+                uint64_t head_stride, uint64_t token_stride, uint32_t box_tokens, int l2_bytes) {
   EncodeTiledFn fn = encode_fn();
   if (!fn) return SPECFOLD_ECUDA;
   const cuuint64_t dims[3] = {dim, heads, tokens};
@@ -110,7 +110,8 @@ int make_map_3d(CUtensorMap* map, const void* base, uint64_t dim, uint64_t heads
   const cuuint32_t es[3] = {1, 1, 1};
   const CUresult r = fn(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, es,
                         CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B,
-                        CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+                        l2_bytes == 128 ? CU_TENSOR_MAP_L2_PROMOTION_L2_128B : CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                        CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
   return r == CUDA_SUCCESS ? SPECFOLD_OK : SPECFOLD_ECUDA;
 }
 

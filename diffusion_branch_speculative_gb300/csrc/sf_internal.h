@@ -214,8 +214,9 @@ int launch_tree_attention(const TreeAttnCall& c, cudaStream_t st);
 int make_map_2d(CUtensorMap* map, const void* base, uint64_t rows, uint64_t cols,
                 uint64_t row_stride_elems, uint32_t box_rows);
 // 3-D bf16 map {dim, heads, tokens} with strides in elements and a
-// {64, 1, box_tokens} box, 128-byte swizzle.
+// {64, 1, box_tokens} box, 128-byte swizzle.  l2_bytes: what L2 fetches around a
+// read, 128 or 256.
 int make_map_3d(CUtensorMap* map, const void* base, uint64_t dim, uint64_t heads, uint64_t tokens,
-                uint64_t head_stride, uint64_t token_stride, uint32_t box_tokens);
+                uint64_t head_stride, uint64_t token_stride, uint32_t box_tokens, int l2_bytes = 256);
 
 }  // namespace sf

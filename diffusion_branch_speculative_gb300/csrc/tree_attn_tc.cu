@@ -736,8 +736,14 @@ int tc_go(const TreeArgs& a, int grid, cudaStream_t st) {
   const specfold_paged_cache& c = a.cache;
   ta.box = c.page_size % 64 == 0 ? 64 : c.page_size % 32 == 0 ? 32 : c.page_size % 16 == 0 ? 16 : 8;
   const uint64_t tokens = static_cast<uint64_t>(c.num_pages) * c.page_size;
-  if (const int rc = make_map_3d(&ta.mapK, c.k, HD, a.n_kv, tokens, c.k_head_stride, c.k_token_stride, ta.box)) return rc;
-  if (const int rc = make_map_3d(&ta.mapV, c.v, HD, a.n_kv, tokens, c.v_head_stride, c.v_token_stride, ta.box)) return rc;
+  // L2 fetches a row: with 256 bytes for rows of 128 the other half would be another
+  // head's (32 sequences of 8000 tokens, 64 rows, head size 64: 105 us, not 140; the
+  // same 104 where a head's rows lie side by side)
+  constexpr int kRow = HD * 2;
+  if (const int rc = make_map_3d(&ta.mapK, c.k, HD, a.n_kv, tokens, c.k_head_stride, c.k_token_stride, ta.box, kRow))
+    return rc;
+  if (const int rc = make_map_3d(&ta.mapV, c.v, HD, a.n_kv, tokens, c.v_head_stride, c.v_token_stride, ta.box, kRow))
+    return rc;
   if (const int rc = smem_limit_once(tree_attn_tc_kernel<HD>, C::SMEM)) return rc;
   launch_k(tree_attn_tc_kernel<HD>, dim3(grid), dim3(kTcThreads), C::SMEM, st, ta);
   count_launch();
