@@ -849,9 +849,9 @@ struct Plan {
 //   head size 128, 16 rows   167.9  167.3   36.8  39.8    12.1  14.8
 //                  20 rows   180.2  168.1   42.3  41.2    15.1  15.0
 //                  32 rows   186.5  169.0   44.5  40.7    17.0  15.3
-//   head size 64,  16 rows    94.2  137.4   19.1  26.9     9.4  13.8
-//                  32 rows   107.3  139.0   25.5  27.3    12.5  14.1
-//                  64 rows   199.5  141.1   37.2  27.9    16.8  15.4
+//   head size 64,  16 rows    93.5  100.2   19.1  26.7     9.2  13.4
+//                  32 rows   107.3  101.0   25.6  27.1    12.5  13.8
+//                  64 rows   199.5  101.8   37.2  27.6    16.8  14.8
 // Two row tiles for head size 64 and 16 rows: 105.1, 33.8, 11.7 (chunks of 16).
 // A unit's start is worth 2 to 8 blocks without a difference above 2 %, and so are
 // weights of 3:2 to 2:1 of a block's full and half tiles.
