@@ -221,7 +221,7 @@ static int check_tree_shape(int dtype, int n_q, int n_kv, int hd, int max_nodes)
   if (!dtype_ok(dtype) || n_q <= 0 || n_kv <= 0 || max_nodes <= 0) return SPECFOLD_EINVAL;
   if (hd != 64 && hd != 128) return SPECFOLD_EUNSUPPORTED;
   if (n_q % n_kv || n_q / n_kv > 128) return SPECFOLD_EUNSUPPORTED;
-  return max_nodes <= SPECFOLD_MAX_TREE ? SPECFOLD_OK : SPECFOLD_ECAPACITY;
+  return max_nodes <= SPECFOLD_MAX_TREE && n_q <= SPECFOLD_MAX_HEADS ? SPECFOLD_OK : SPECFOLD_ECAPACITY;
 }
 
 // ------------------------------------------------------ workspace layout --
@@ -673,6 +673,7 @@ int specfold_qk_norm_rope(int dtype, int T, int n_q, int n_kv, int head_dim, spe
                           void* stream) {
   SF_TRY(check_norm_rope(dtype, T, head_dim, eps, rope_theta));
   if (n_q < 0 || n_kv < 0) return SPECFOLD_EINVAL;
+  if (n_q > SPECFOLD_MAX_HEADS || n_kv > SPECFOLD_MAX_HEADS) return SPECFOLD_ECAPACITY;
   if (T == 0 || n_q + n_kv == 0) return SPECFOLD_OK;
   if (rope_theta > 0.f && !positions) return SPECFOLD_EINVAL;
   if (n_q > 0) {
@@ -693,6 +694,7 @@ int specfold_kv_append(int dtype, int T, int n_kv, int head_dim, specfold_head_r
                        uint32_t* status, void* stream) {
   SF_TRY(check_norm_rope(dtype, T, head_dim, eps, rope_theta));
   if (n_kv <= 0 || n_src < 0) return SPECFOLD_EINVAL;
+  if (n_kv > SPECFOLD_MAX_HEADS) return SPECFOLD_ECAPACITY;
   SF_TRY(check_paged_cache(cache));
   SF_TRY(check_batch(row_start, ctx_len, n_seqs));
   if (!rows && n_src < T) return SPECFOLD_EINVAL;

@@ -92,6 +92,7 @@ extern "C" {
 #define SPECFOLD_MAX_ROWS 16384     /* largest B*L */
 #define SPECFOLD_MAX_SEQS 1024      /* sequences of one batch (specfold_kv_append, specfold_tree_attention) */
 #define SPECFOLD_MAX_TREE 256       /* drafted rows of one sequence (specfold_tree_attention) */
+#define SPECFOLD_MAX_HEADS 65536    /* heads of one kind (the three calls on a decoder's cache) */
 #define SPECFOLD_TREE_PAD -2        /* parent of a padding row (specfold_tree_attention) */
 
 typedef enum { SPECFOLD_BF16 = 0, SPECFOLD_F32 = 1 } specfold_dtype;
@@ -455,7 +456,8 @@ typedef struct {
  *   q_in, q_out [T, n_q, hd], k_in, k_out [T, n_kv, hd]; n_q or n_kv may be 0
  * (that side's views are not read).  An output may be its input (the same
  * pointer and strides), and may not overlap it in any other way.
- * head_dim 64 or 128; eps >= 0; T >= 0. */
+ * head_dim 64 or 128; eps >= 0; T >= 0; n_q, n_kv <= SPECFOLD_MAX_HEADS
+ * (SPECFOLD_ECAPACITY). */
 int specfold_qk_norm_rope(int dtype, int T, int n_q, int n_kv, int head_dim, specfold_head_rows q_in,
                           specfold_head_rows k_in, specfold_head_rows q_out, specfold_head_rows k_out,
                           const void* gq, const void* gk, float eps, const int32_t* positions,

@@ -241,3 +241,13 @@ def test_binding_refuses_bad_caches(B):
         B.PagedCache(pool, pool, table.long(), 16)
     with pytest.raises(ValueError, match="one shape"):
         B.PagedCache(pool, pool[:, :1], table, 16)
+
+
+def test_too_many_heads_are_refused(B):
+    assert B.MAX_HEADS == 65536
+    for n in (B.MAX_HEADS + 1, 2 ** 31 - 1):
+        assert _qk(B, n_q=n) == B.ECAPACITY
+        assert _qk(B, n_kv=n) == B.ECAPACITY
+        assert _append(B, n_kv=n) == B.ECAPACITY
+        assert _tree(B, n_q=n, n_kv=n) == B.ECAPACITY
+        assert B.tree_attention_workspace_size(B.BF16, n, n, 128, 4) == 0
