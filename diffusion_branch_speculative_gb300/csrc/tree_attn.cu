@@ -110,9 +110,9 @@ __global__ void __launch_bounds__(kThreads, Simt<HD>::CTAS) tree_attn_simt_kerne
   pdl_wait();
   pdl_trigger();
   TreeWalk w;
-  unsigned lo, per;
-  const bool work = tree_locate(p, w, lo, per);
-  if (threadIdx.x == 0) tree_describe(p, w, work, lo, per);
+  unsigned per;
+  const bool work = tree_locate(p, w, per);
+  if (threadIdx.x == 0) tree_describe(p, w, work, per);
   if (!work) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = smem + warp * (C::RING > C::MERGE ? C::RING : C::MERGE);
@@ -360,9 +360,9 @@ __global__ void __launch_bounds__(kThreads, Few<HD, MT>::CTAS) tree_attn_few_ker
   pdl_wait();
   pdl_trigger();
   TreeWalk w;
-  unsigned lo, per;
-  const bool work = tree_locate(p, w, lo, per);
-  if (threadIdx.x == 0) tree_describe(p, w, work, lo, per);
+  unsigned per;
+  const bool work = tree_locate(p, w, per);
+  if (threadIdx.x == 0) tree_describe(p, w, work, per);
   if (!work) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   uint8_t* ring = smem + warp * C::RING;

@@ -241,9 +241,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
   pdl_wait();
   pdl_trigger();
   TreeWalk w;
-  unsigned lo, per;
-  const bool work = tree_locate(p, w, lo, per);
-  if (threadIdx.x == 0) tree_describe(p, w, work, lo, per);
+  unsigned per;
+  const bool work = tree_locate(p, w, per);
+  if (threadIdx.x == 0) tree_describe(p, w, work, per);
   tc_fence_before();
   __syncthreads();
   tc_fence_after();

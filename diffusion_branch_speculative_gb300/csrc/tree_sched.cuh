@@ -21,6 +21,12 @@
 
 namespace sf {
 
+// Blocks that a call may count, head by head: what the header states.  Nothing here
+// needs the bound (at 10^8 blocks a call reads 1.6 TB and more, a quarter of a second
+// at the copy rate, once for every tile of rows); it turns lengths that cannot be meant
+// into an error.
+constexpr unsigned kTreeMaxBlocks = 100000000u;
+
 struct TreeArgs {
   const void* q;
   void* o;
@@ -48,8 +54,9 @@ struct TreeSeq {
   bool half, bad;
   SF_DEV unsigned weight(const TreeArgs& p, int tile) const { return half && tile == tiles - 1 ? p.w_half : p.w_full; }
   // places in the line of all its tiles of one head
-  SF_DEV unsigned head_places(const TreeArgs& p) const {
-    return static_cast<unsigned>(nb + p.unit_cost) * (tiles * p.w_full - (half ? p.w_full - p.w_half : 0));
+  template <typename Places>
+  SF_DEV Places head_places(const TreeArgs& p) const {
+    return static_cast<Places>(nb + p.unit_cost) * static_cast<unsigned>(tiles * p.w_full - (half ? p.w_full - p.w_half : 0));
   }
 };
 
@@ -77,7 +84,7 @@ SF_DEV TreeSeq tree_seq(const TreeArgs& p, int s) {
 // A CTA's walk along its run: the current piece, blocks b0 .. b0 + n - 1 of
 // (sequence s, head, tile), and the places left from there on.  All of this is
 // executed once or twice a launch, mostly on cold instruction caches: it is kept
-// short (32-bit places, few divisions).
+// short (few divisions; 32 bits within a run).
 struct TreeWalk {
   int s, head, tile, b0, n;
   unsigned left;
@@ -117,29 +124,39 @@ struct TreeWalk {
 };
 
 // This CTA's run, found by every warp on its own (a lane a sequence, 32 at a
-// time: no block-wide barrier, one round trip for up to 32 sequences).  lo: where
-// the run starts in the line, per: the places of a run.  False for a CTA without
-// work; the walk is the same in all threads.
-SF_DEV bool tree_locate(const TreeArgs& p, TreeWalk& w, unsigned& lo, unsigned& per) {
+// time: no block-wide barrier, one round trip for up to 32 sequences).  per: the
+// places of a run.  False for a CTA without work; the walk is the same in all threads.
+//
+// Places is 64 bits where the line may be longer than 32 bits hold (10^8 blocks times
+// up to 4096 tiles of a head group's rows; a run's places fit always: 4.1 10^11 over
+// the fp32 kernel's 456 CTAs, 6.4 10^10 over the tcgen05 kernel's 152), and that form
+// alone asks for the limit.  With it for every call the tcgen05 kernel took 2 us more.
+template <typename Places>
+SF_DEV bool tree_locate_in(const TreeArgs& p, TreeWalk& w, unsigned& per) {
+  constexpr bool kLong = sizeof(Places) == 8;
   const int lane = threadIdx.x & 31, n_seqs = p.batch.n_seqs;
   TreeSeq q;
-  unsigned inc = 0;
-  float size = 0.f;  // the total again, which cannot wrap
+  Places inc = 0;
+  float size = 0.f;  // this lane's part of the line, in places, which cannot wrap
+  Places blocks = 0;
   // 32 sequences from c on: q this lane's, inc the places up to and with its own
   auto take = [&](int c) {
     q = tree_seq(p, min(c + lane, n_seqs - 1));
     const bool mine = c + lane < n_seqs && q.n > 0;
-    const unsigned places = mine ? q.head_places(p) * p.n_kv : 0;
-    size += mine ? static_cast<float>(q.nb + p.unit_cost) * q.tiles * p.w_full * p.n_kv : 0.f;
+    const Places places = mine ? q.head_places<Places>(p) * p.n_kv : 0;
+    if constexpr (kLong)
+      blocks += mine ? static_cast<Places>(q.nb) * p.n_kv : 0;
+    else
+      size += mine ? static_cast<float>(q.nb + p.unit_cost) * q.tiles * p.w_full * p.n_kv : 0.f;
     inc = places;
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
-      const unsigned u = __shfl_up_sync(0xffffffffu, inc, o);
+      const Places u = __shfl_up_sync(0xffffffffu, inc, o);
       if (lane >= o) inc += u;
     }
     return places;
   };
-  unsigned total = 0, places = 0;
+  Places total = 0, places = 0;
   bool bad = false;
 #pragma unroll 1
   for (int c = (n_seqs - 1) & ~31; c >= 0; c -= 32) {  // the first 32 last: they stay
@@ -147,17 +164,25 @@ SF_DEV bool tree_locate(const TreeArgs& p, TreeWalk& w, unsigned& lo, unsigned& 
     total += __shfl_sync(0xffffffffu, inc, 31);
     bad = bad || q.bad;
   }
-  // a line of 10^8 places a lane and more (hours of work) could wrap: refused
-  const bool wraps = __any_sync(0xffffffffu, size > 1.2e8f);
-  if ((bad || wraps) && blockIdx.x == 0 && threadIdx.x < 32) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
-  per = max((total + gridDim.x - 1) / gridDim.x, static_cast<unsigned>(p.w_full));  // a block at least
-  lo = per * blockIdx.x;
-  if (wraps || lo >= total) return false;
-  unsigned before = 0;
+  bool too_long = false;
+  if constexpr (kLong) {
+    // (a lane's count is cut where it is too much by itself, so that 32 of them fit)
+    const unsigned cut = static_cast<unsigned>(min(blocks, static_cast<Places>(kTreeMaxBlocks) + 1));
+    too_long = __reduce_add_sync(0xffffffffu, cut) > kTreeMaxBlocks;
+  } else if (__any_sync(0xffffffffu, size > kTreeMaxBlocks / 32)) {  // else no more than that in all
+    return tree_locate_in<unsigned long long>(p, w, per);
+  }
+  const Places run = max((total + gridDim.x - 1) / gridDim.x, static_cast<Places>(p.w_full));  // a block at least
+  if (kLong && run > 0x7fffffffu) too_long = true;  // (not on a grid of a hundred CTAs)
+  if ((bad || too_long) && blockIdx.x == 0 && threadIdx.x < 32) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
+  per = static_cast<unsigned>(run);
+  const Places lo = run * blockIdx.x;  // where the run starts in the line
+  if (too_long || lo >= total) return false;
+  Places before = 0;
   int c = 0;
 #pragma unroll 1
   while (true) {
-    const unsigned sum = __shfl_sync(0xffffffffu, inc, 31);
+    const Places sum = __shfl_sync(0xffffffffu, inc, 31);
     if (lo < before + sum) break;
     before += sum;
     c += 32;
@@ -165,7 +190,7 @@ SF_DEV bool tree_locate(const TreeArgs& p, TreeWalk& w, unsigned& lo, unsigned& 
     places = take(c);
   }
   const int src = __ffs(__ballot_sync(0xffffffffu, lo < before + inc)) - 1;
-  const unsigned off = lo - before - __shfl_sync(0xffffffffu, inc - places, src);
+  const Places off = lo - before - __shfl_sync(0xffffffffu, inc - places, src);
   w.s = c + src;
   w.q.row0 = __shfl_sync(0xffffffffu, q.row0, src);
   w.q.n = __shfl_sync(0xffffffffu, q.n, src);
@@ -173,13 +198,14 @@ SF_DEV bool tree_locate(const TreeArgs& p, TreeWalk& w, unsigned& lo, unsigned& 
   w.q.nb = __shfl_sync(0xffffffffu, q.nb, src);
   w.q.tiles = __shfl_sync(0xffffffffu, q.tiles, src);
   w.q.half = __shfl_sync(0xffffffffu, q.half, src);
-  const unsigned hp = w.q.head_places(p), tp = static_cast<unsigned>(w.q.nb + p.unit_cost) * p.w_full;
-  w.head = off / hp;
-  unsigned at = off - w.head * hp;
-  w.tile = min(static_cast<int>(at / tp), w.q.tiles - 1);
-  at -= w.tile * tp;
+  const Places hp = w.q.head_places<Places>(p);
+  const unsigned tp = static_cast<unsigned>(w.q.nb + p.unit_cost) * p.w_full;
+  w.head = static_cast<int>(off / hp);
+  const Places in_head = off - w.head * hp;
+  w.tile = min(static_cast<int>(in_head / tp), w.q.tiles - 1);
+  const unsigned at = static_cast<unsigned>(in_head - static_cast<Places>(w.tile) * tp);
   const unsigned wt = w.q.weight(p, w.tile), v = at / wt;  // blocks, the start's among them, before the cut
-  w.left = min(per, total - lo);
+  w.left = static_cast<unsigned>(min(run, total - lo));
   if (static_cast<int>(v) <= p.unit_cost) {  // before the unit
     w.left += at;
     w.enter(p);
@@ -191,6 +217,7 @@ SF_DEV bool tree_locate(const TreeArgs& p, TreeWalk& w, unsigned& lo, unsigned& 
   }
   return w.n > 0;
 }
+SF_DEV bool tree_locate(const TreeArgs& p, TreeWalk& w, unsigned& per) { return tree_locate_in<unsigned>(p, w, per); }
 
 // The partial slot of a run's piece.
 SF_DEV int tree_slot(bool first) { return 2 * static_cast<int>(blockIdx.x) + (first ? 0 : 1); }
@@ -204,17 +231,17 @@ SF_DEV int tree_tile_rows(const TreeArgs& p, const TreeWalk& w) {
 // By one thread of every CTA: the unit that this CTA's start cuts, if this is
 // the first cut in it, for the combine kernel: {rows, row0, m0, head},
 // {first CTA, last CTA, the first CTA's slot, 0}; rows 0: nothing to merge.
-SF_DEV void tree_describe(const TreeArgs& p, const TreeWalk& w, bool work, unsigned lo, unsigned per) {
+SF_DEV void tree_describe(const TreeArgs& p, const TreeWalk& w, bool work, unsigned per) {
   const int c = blockIdx.x;
   int4 a = make_int4(0, 0, 0, 0);
   if (work && w.b0 > 0) {
-    // Where the unit begins and ends, from where its block b0 does; a block is its last place's owner's.
-    const unsigned wt = w.q.weight(p, w.tile), before = lo - per;
-    const unsigned b0_at = lo - w.past;
-    const unsigned beg = b0_at - (w.b0 + p.unit_cost) * wt, end = b0_at + (w.q.nb - w.b0) * wt;
-    if (beg + (p.unit_cost + 1) * wt > before) {  // CTA c - 1 has the first block
+    // Where the unit begins and ends, from where its block b0 does, in places from the cut
+    // on; a block is its last place's owner's.
+    const unsigned wt = w.q.weight(p, w.tile);
+    const unsigned begins = w.past + (w.b0 + p.unit_cost) * wt, ends = (w.q.nb - w.b0) * wt - w.past;  // before, behind the cut
+    if (begins - (p.unit_cost + 1) * wt < per) {  // CTA c - 1 has the first block
       a = make_int4(tree_tile_rows(p, w), w.q.row0, tree_m0(p, w), w.head);
-      p.desc[2 * c + 1] = make_int4(c - 1, (end - 1) / per, 2 * (c - 1) + (beg <= before ? 0 : 1), 0);
+      p.desc[2 * c + 1] = make_int4(c - 1, c + (ends - 1) / per, 2 * (c - 1) + (begins >= per ? 0 : 1), 0);
     }
   }
   p.desc[2 * c] = a;

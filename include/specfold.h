@@ -509,9 +509,11 @@ int specfold_kv_append(int dtype, int T, int n_kv, int head_dim, specfold_head_r
  * their pages hold (infinities and NaN included).  Rows of o that belong to
  * no sequence stay as they were, as do those of a sequence whose row_start,
  * ctx_len or row count is invalid (SPECFOLD_DEV_BAD_SEQ), or every row where
- * the batch as a whole counts more than 10^8 blocks of keys, head by head; a
- * page outside the pool or a token past the table reads as zeros
- * (SPECFOLD_DEV_BAD_PAGE).
+ * the batch as a whole counts more than 10^8 blocks of keys (the same bit): a
+ * sequence with rows has ceil((ctx_len + rows) / 64) of them for every
+ * key/value head, or / 128 for bf16 with max_nodes * n_q / n_kv above 16 (head
+ * size 64: above 32).  A page outside the pool or a token past the table reads
+ * as zeros (SPECFOLD_DEV_BAD_PAGE).
  * bf16 runs on the tensor cores: products of bf16 values summed in 32 bits,
  * softmax in 32 bits, the probabilities rounded to bf16 for their product
  * with the values.  fp32 keeps 32 bits throughout.
