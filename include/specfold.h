@@ -452,6 +452,7 @@ typedef struct {
  *   out[j + hd/2] = y[j + hd/2] cos a_j + y[j] sin a_j
  * with a_j = positions[t] * rope_theta^(-2j/hd) reduced exactly to one turn
  * (rope_theta 0: no rotation, positions may be NULL), rounded once to dtype.
+ * A head that is neither normed nor rotated is copied bit for bit.
  * gq and gk [head_dim] are the queries' and the keys' gains.
  *   q_in, q_out [T, n_q, hd], k_in, k_out [T, n_kv, hd]; n_q or n_kv may be 0
  * (that side's views are not read).  An output may be its input (the same
@@ -469,7 +470,7 @@ int specfold_qk_norm_rope(int dtype, int T, int n_q, int n_kv, int head_dim, spe
  * tokens (device int32).  Its row i goes to the cache's token
  * ctx_len[s] + i: the key normed with gk (NULL: not normed) and rotated to
  * positions[t] (NULL: to the token's own index; rope_theta 0: not rotated)
- * as in specfold_qk_norm_rope, the value as it is.
+ * as in specfold_qk_norm_rope, the value as it is, bit for bit.
  *   k, v     views of n_src rows of n_kv heads, 0 <= n_src
  *            (outside the pools: rows are read while others are written)
  *   rows     device int32 [T] or NULL: the row of k and v that row t of the

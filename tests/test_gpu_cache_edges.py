@@ -1,0 +1,63 @@
+"""Norm with rotation, append and tree attention at the calls that their
+documentation allows beside the ordinary ones."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_cache_ops import B, DT, ints, make_cache
+
+pytestmark = pytest.mark.gpu
+BITS = {"bf16": torch.int16, "f32": torch.int32}
+
+
+def patterns(rng, shape, dt):
+    """Every kind of bit pattern: a fifth of the elements are NaN of either sign
+    and any payload, infinities, subnormals or zeros of either sign."""
+    info = np.iinfo(np.int16 if dt == "bf16" else np.int32)
+    x = rng.integers(info.min, info.max, shape, endpoint=True)
+    ones = {"bf16": 0x7F80, "f32": 0x7F800000}[dt]
+    kind = rng.integers(0, 20, shape)
+    x = np.where(kind < 2, x | ones, np.where(kind == 2, x & ~ones, np.where(kind == 3, x & info.min, x)))
+    return torch.from_numpy(x.astype(info.dtype)).cuda().view(DT[dt])
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("hd,n_kv", [(64, 3), (128, 2), (128, 9)])
+@pytest.mark.parametrize("picked", [False, True])
+def test_append_copies_bit_for_bit(B, dt, hd, n_kv, picked):
+    """Values always, keys where they are neither normed nor rotated."""
+    rng = np.random.default_rng(61)
+    counts, ctx = [70, 0, 1, 300], [5, 0, 63, 17]
+    start = np.concatenate([[0], np.cumsum(counts)])
+    T = int(start[-1])
+    x = patterns(rng, (2 * T, 2, n_kv, hd), dt)
+    rows = rng.integers(0, 2 * T, T) if picked else np.arange(T)
+    for theta in (0.0, 1e4):
+        cache, table = make_cache(B, rng, dt, hd, n_kv, 16, np.array(ctx) + counts, "fused")
+        B.specfold_kv_append(x[:, 0], x[:, 1], cache, ints(start), ints(ctx), rope_theta=theta,
+                             rows=ints(rows) if picked else None)
+        torch.cuda.synchronize()
+        tok = np.concatenate([c + np.arange(n) for c, n in zip(ctx, counts)])
+        seq = np.repeat(np.arange(4), counts)
+        at = torch.from_numpy(table[seq, tok // 16].astype(np.int64) * 16 + tok % 16).cuda()
+        src = torch.from_numpy(rows[:T]).cuda()
+        assert torch.equal(cache.v_pool[at].view(BITS[dt]), x[src, 1].contiguous().view(BITS[dt]))
+        if theta == 0.0:
+            assert torch.equal(cache.k_pool[at].view(BITS[dt]), x[src, 0].contiguous().view(BITS[dt]))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("T", [1, 9, 3000])
+def test_heads_neither_normed_nor_rotated_are_copies(B, dt, T):
+    rng = np.random.default_rng(62)
+    x = patterns(rng, (T, 9, 128), dt)
+    q, k = x[:, :7], x[:, 7:]
+    qo, ko = torch.empty_like(q), torch.empty((2, T, 128), device="cuda", dtype=DT[dt]).transpose(0, 1)
+    B.specfold_qk_norm_rope(q, k, qo, ko)
+    torch.cuda.synchronize()
+    assert torch.equal(qo.contiguous().view(BITS[dt]), q.contiguous().view(BITS[dt]))
+    assert torch.equal(ko.contiguous().view(BITS[dt]), k.contiguous().view(BITS[dt]))
+    # one side normed, the other still a copy
+    B.specfold_qk_norm_rope(q, k, qo, ko, gk=torch.ones(128, device="cuda", dtype=DT[dt]))
+    torch.cuda.synchronize()
+    assert torch.equal(qo.contiguous().view(BITS[dt]), q.contiguous().view(BITS[dt]))
