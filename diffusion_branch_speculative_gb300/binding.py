@@ -354,7 +354,10 @@ _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device
 _NO_ROWS = specfold_head_rows(None, 0, 0)
 
 
-def _head_rows(t: torch.Tensor, rows: int, heads: int, hd: int, dtype, dev: int, what: str) -> specfold_head_rows:
+def _head_rows(t: Optional[torch.Tensor], rows: int, heads: int, hd: int, dtype, dev: int,
+               what: str) -> specfold_head_rows:
+    if t is None:
+        raise ValueError(f"{what} must be given")
     s0, s1, s2 = t.stride() if t.dim() == 3 else (0, 0, 0)
     if s2 != 1 or t.shape != (rows, heads, hd):
         raise ValueError(f"{what} must be [{rows}, {heads}, {hd}], the same rows as its peers, with unit last stride")
@@ -408,7 +411,7 @@ def specfold_qk_norm_rope(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], 
     """Norm of every query and key head (gains gq, gk [hd]; None: not normed)
     and the rotation by positions (int32 [T]; rope_theta 0: none).  Q, Q_out
     [T, n_q, hd] and K, K_out [T, n_kv, hd], strided views allowed, an output
-    may be its input; Q or K may be None."""
+    may be its input; Q or K may be None, with its output."""
     like = Q if Q is not None else K
     if like is None:
         raise ValueError("Q or K must be given")
@@ -422,7 +425,7 @@ def specfold_qk_norm_rope(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], 
     else:
         n_q = 0
     if K is not None:
-        n_kv = K.shape[1]
+        n_kv = K.shape[1] if K.dim() == 3 else 0
         k = _head_rows(K, T, n_kv, hd, dtype, dev, "K")
         ko = _head_rows(K_out, T, n_kv, hd, dtype, dev, "K_out")
     if rope_theta and positions is None:

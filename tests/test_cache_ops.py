@@ -251,3 +251,12 @@ def test_too_many_heads_are_refused(B):
         assert _append(B, n_kv=n) == B.ECAPACITY
         assert _tree(B, n_q=n, n_kv=n) == B.ECAPACITY
         assert B.tree_attention_workspace_size(B.BF16, n, n, 128, 4) == 0
+
+
+def test_binding_refuses_missing_outputs(B):
+    q, k = torch.zeros(3, 4, 64), torch.zeros(3, 2, 64)
+    for args, what in (((q, k, None, k), "Q_out"), ((q, k, q, None), "K_out"), ((q, None, None, None), "Q_out"),
+                       ((None, k, None, None), "K_out"), ((q, k[:, 0], q, k), "K must be"),
+                       ((q, k[0, 0], q, k), "K must be")):
+        with pytest.raises(ValueError, match=what):
+            B.specfold_qk_norm_rope(*args)
