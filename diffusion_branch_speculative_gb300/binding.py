@@ -442,7 +442,7 @@ def specfold_kv_append(K: torch.Tensor, V: torch.Tensor, cache: PagedCache, row_
                        rows: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
     """Appends the batch's keys and values to the cache: row i of sequence s
     (batch rows row_start[s] .. row_start[s+1]-1, int32 [n_seqs + 1]) becomes
-    token ctx_len[s] + i.  K, V [n_src, n_kv, hd], not views of the pools; `rows`
+    token ctx_len[s] + i.  K, V [n_src, n_kv, hd], not rows of the pools (refused); `rows`
     (int32) picks their rows, one per batch row; `positions` (int32, per batch row) defaults to
     the tokens' own indices.  `status`: an optional int32/uint32 word for the
     device status bits (read it with specfold_get_status)."""

@@ -212,6 +212,26 @@ static int check_paged_cache(const specfold_paged_cache* c) {
   return SPECFOLD_OK;
 }
 
+// Whether rows of heads of one view lie among another's: exact where the views' strides
+// are the same (slices of one buffer), else by their ranges.  Strides in elements of
+// `bytes`, positive.
+struct HeadView {
+  const void* ptr;
+  long long rows, row_stride, head_stride;
+};
+static bool views_meet(const HeadView& a, const HeadView& b, int heads, int hd, int bytes) {
+  auto span = [&](const HeadView& v) { return (v.rows - 1) * v.row_stride + (heads - 1) * v.head_stride + hd; };
+  const long long d = (reinterpret_cast<intptr_t>(b.ptr) - reinterpret_cast<intptr_t>(a.ptr)) / bytes;
+  if (d >= span(a) || -d >= span(b)) return false;
+  if (a.row_stride != b.row_stride || a.head_stride != b.head_stride) return true;
+  for (long long h = 1 - heads; h < heads; ++h) {  // b's head less a's; then b's row less a's, around what brings them together
+    const long long x = d + h * a.head_stride, near = -x / a.row_stride;
+    for (long long t = near - 1; t <= near + 1; ++t)
+      if (t > -a.rows && t < b.rows && std::llabs(x + t * a.row_stride) < hd) return true;
+  }
+  return false;
+}
+
 static int check_batch(const int32_t* row_start, const int32_t* ctx_len, int n_seqs) {
   if (!row_start || !ctx_len || n_seqs < 1) return SPECFOLD_EINVAL;
   return n_seqs <= SPECFOLD_MAX_SEQS ? SPECFOLD_OK : SPECFOLD_ECAPACITY;
@@ -702,6 +722,15 @@ int specfold_kv_append(int dtype, int T, int n_kv, int head_dim, specfold_head_r
   if (n_src > 0) {
     SF_TRY(check_head_rows(k));
     SF_TRY(check_head_rows(v));
+    // rows are read while others are written
+    const long long tokens = static_cast<long long>(cache->num_pages) * cache->page_size;
+    const HeadView pools[2] = {{cache->k, tokens, cache->k_token_stride, cache->k_head_stride},
+                               {cache->v, tokens, cache->v_token_stride, cache->v_head_stride}};
+    for (const specfold_head_rows* src : {&k, &v})
+      for (const HeadView& pool : pools)
+        if (views_meet({src->ptr, n_src, src->row_stride, src->head_stride}, pool, n_kv, head_dim,
+                       dtype == SPECFOLD_BF16 ? 2 : 4))
+          return SPECFOLD_EINVAL;
   }
   KvAppendCall c{dtype, n_kv, head_dim, k, v, n_src, rows, gk, eps, positions, rope_theta, *cache,
                  {row_start, ctx_len, n_seqs, T}, status};

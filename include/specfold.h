@@ -472,7 +472,9 @@ int specfold_qk_norm_rope(int dtype, int T, int n_q, int n_kv, int head_dim, spe
  * positions[t] (NULL: to the token's own index; rope_theta 0: not rotated)
  * as in specfold_qk_norm_rope, the value as it is, bit for bit.
  *   k, v     views of n_src rows of n_kv heads, 0 <= n_src
- *            (outside the pools: rows are read while others are written)
+ *            (outside the pools, for rows are read while others are written:
+ *            a view whose rows lie among a pool's is SPECFOLD_EINVAL; one in
+ *            a pool's range with other strides counts as such)
  *   rows     device int32 [T] or NULL: the row of k and v that row t of the
  *            batch takes (a step's accepted rows are committed this way:
  *            appended again, at their final places).  NULL: row t itself,

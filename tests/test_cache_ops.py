@@ -260,3 +260,17 @@ def test_binding_refuses_missing_outputs(B):
                        ((q, k[0, 0], q, k), "K must be")):
         with pytest.raises(ValueError, match=what):
             B.specfold_qk_norm_rope(*args)
+
+
+def test_append_refuses_sources_in_the_pools(B):
+    """Pools of 128 tokens of 1024 bytes, keys at A, values behind them; sources of four rows."""
+    size = 128 * 1024
+    v = A + size
+    cache = _cache(B, v=v)
+    far = _hr(B, ptr=A + 4 * size)
+    for src in (_hr(B, ptr=A), _hr(B, ptr=v), _hr(B, ptr=A + 4 * 1024), _hr(B, ptr=v + size - 1024),
+                _hr(B, ptr=A - 3 * 1024),                               # the last of them the pool's first
+                _hr(B, ptr=A + 256), _hr(B, ptr=A + 1024 - 256),        # a head on; a head back, of the next token
+                _hr(B, ptr=A + 4096, rs=256), _hr(B, ptr=A + 4096, hs=256)):    # other strides, in the range
+        assert _append(B, k=src, v=far, cache=cache) == B.EINVAL
+        assert _append(B, k=far, v=src, cache=cache) == B.EINVAL

@@ -61,3 +61,32 @@ def test_heads_neither_normed_nor_rotated_are_copies(B, dt, T):
     B.specfold_qk_norm_rope(q, k, qo, ko, gk=torch.ones(128, device="cuda", dtype=DT[dt]))
     torch.cuda.synchronize()
     assert torch.equal(qo.contiguous().view(BITS[dt]), q.contiguous().view(BITS[dt]))
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("layout", ["beside", "between heads", "behind", "head-major"])
+def test_append_from_the_pools_own_buffer(B, dt, layout):
+    """Sources and pools are slices of one buffer that share no element."""
+    rng = np.random.default_rng(63)
+    tokens, n, n_kv, hd = 96, 40, 3, 64
+    if layout == "beside":                              # a token: the pools' heads, then the sources'
+        x = patterns(rng, (tokens, 4, n_kv, hd), dt)
+        kp, vp, K, V = x[:, 0], x[:, 1], x[:n, 2], x[:n, 3]
+    elif layout == "between heads":                     # a head of each in turn
+        x = patterns(rng, (tokens, n_kv, 4, hd), dt)
+        kp, vp, K, V = x[:, :, 0], x[:, :, 1], x[5:5 + n, :, 2], x[5:5 + n, :, 3]
+    elif layout == "behind":
+        x = patterns(rng, (2, tokens + n, n_kv, hd), dt)
+        kp, vp, K, V = x[0, :tokens], x[1, :tokens], x[0, tokens:], x[1, tokens:]
+    else:                                               # head by head, the sources behind each head's pool
+        x = patterns(rng, (2, n_kv, tokens + n, hd), dt).transpose(1, 2)
+        kp, vp, K, V = x[0, :tokens], x[1, :tokens], x[0, tokens:], x[1, tokens:]
+    cache = B.PagedCache(kp, vp, ints(np.arange(12)[None]), 8)
+    keep = K.clone(), V.clone()
+    B.specfold_kv_append(K, V, cache, ints([0, n]), ints([30]))
+    torch.cuda.synchronize()
+    for pool, src in ((kp, keep[0]), (vp, keep[1])):
+        assert torch.equal(pool[30:30 + n].contiguous().view(BITS[dt]), src.contiguous().view(BITS[dt]))
+    with pytest.raises(B.SpecfoldError) as e:           # and from the pool itself
+        B.specfold_kv_append(kp[:n], V, cache, ints([0, n]), ints([30]))
+    assert e.value.code == B.EINVAL
