@@ -15,6 +15,12 @@
 // every 32-bit position: no large floating product and no 64-bit floating
 // arithmetic on the device.  f_j itself is computed on the host in 64 bits, which
 // leaves the angle off by at most p * 2^-49 turns.
+//
+// Both may release their dependents early, although what they write may be the prefix of
+// the layer's attention, which reads it before its wait: no call of this library starts
+// with that kernel in that form.  It comes behind one of the same call that has waited
+// for its predecessor, by when these are complete.  Norm with rotation does (a captured
+// step of norm, append and attention takes 12.0 us, 12.5 without).
 #include "sf_device.cuh"
 #include "sf_internal.h"
 
@@ -285,8 +291,8 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) kv_append_kernel(cons
   __shared__ __align__(16) float s_g[HD];
   __shared__ int s_start[SPECFOLD_MAX_SEQS + 1], s_ctx[SPECFOLD_MAX_SEQS];
   if (p.rope && threadIdx.x < HD / 2) s_f[threadIdx.x] = p.turns.f[threadIdx.x];
-  // No early release of dependents: a dependent may read the cache (a prefix
-  // view) before its own wait.
+  // Dependents are not released early: it would be sound (see above), but takes appended
+  // prompts 20.3 us, not 19.9, and a captured step of norm, append and attention gains nothing.
   pdl_wait();
   if (p.gk)
     for (int i = threadIdx.x; i < HD; i += kThreads) s_g[i] = static_cast<float>(p.gk[i]);

@@ -43,7 +43,10 @@
  *     before the call.  A caller's kernel that runs just before a call and
  *     releases its dependents early (griddepcontrol.launch_dependents) must
  *     not write those inputs after doing so.  Ordinary kernels, copies and
- *     memsets are complete before the call's first kernel starts.
+ *     memsets are complete before the call's first kernel starts.  Calls of
+ *     this library may follow one another directly whatever they write: of
+ *     what a call reads, its first kernel reads nothing but norm gains before
+ *     it has waited, and a later one starts only when the first's wait is over.
  *   - Matrices are row-major.  Weights use the [out, in] layout.
  *   - Alignment: every pointer is 16-byte aligned; the prefix view strides are
  *     multiples of 8 elements (SPECFOLD_EALIGN otherwise).

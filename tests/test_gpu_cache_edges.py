@@ -90,3 +90,55 @@ def test_append_from_the_pools_own_buffer(B, dt, layout):
     with pytest.raises(B.SpecfoldError) as e:           # and from the pool itself
         B.specfold_kv_append(kp[:n], V, cache, ints([0, n]), ints([30]))
     assert e.value.code == B.EINVAL
+
+
+@pytest.mark.parametrize("writer", ["append", "norm"])
+@pytest.mark.parametrize("P", [500, 3000])
+def test_prefix_read_right_behind_the_call_that_writes_it(B, writer, P):
+    """A contiguous prefix (head-major, which the layer's attention may read before
+    it waits), written by append or by norm with rotation, and directly behind it
+    the attention alone or the whole layer: the same bits as with a wait between."""
+    from diffusion_branch_speculative_gb300 import synth
+    from tests.gpu_cases import DeviceInputs
+    n_q, n_kv, hd, L = 8, 2, 128, 12
+    inp = synth.make_layer_inputs(synth.small_workload(d=512, n_q=n_q, n_kv=n_kv, hd=hd, F=384, P=P, L=L,
+                                                       levels=(1, 3, 4)), seed=8)
+    dev = DeviceInputs(inp)
+    nb = dev.B
+    R = nb * L
+    bf, i32 = dict(dtype=torch.bfloat16, device="cuda"), dict(dtype=torch.int32, device="cuda")
+    page = -(-P // 8) * 8
+    pk, pv = (torch.zeros(n_kv, page, hd, **bf).transpose(0, 1) for _ in range(2))
+    cache = B.PagedCache(pk, pv, torch.zeros(1, 1, **i32), page)
+    start, ctx = ints([0, P]), ints([0])
+    ws, cw = B.alloc_workspace(B.workspace_size(dev.dims, nb, L)), B.make_weights(dev.W)
+    Q = torch.randn(n_kv, R * (n_q // n_kv), hd, **bf)
+    bK, bV = torch.randn(R, n_kv, hd, **bf), torch.randn(R, n_kv, hd, **bf)
+    src, packed, n = torch.arange(R, **i32), torch.arange(R, **i32), torch.full((1,), R, **i32)
+    gain = torch.ones(hd, **bf)
+
+    def step(whole, wait):
+        pk.zero_()
+        if writer == "append":
+            pv.zero_()
+            B.specfold_kv_append(dev.pk, dev.pv, cache, start, ctx, gk=gain)
+        else:
+            pv[:P] = dev.pv
+            torch.cuda.synchronize()
+            B.specfold_qk_norm_rope(None, dev.pk, None, pk[:P], gk=gain)
+        if wait:
+            torch.cuda.synchronize()
+        if whole:
+            out = torch.empty_like(dev.H)
+            B.specfold_layer_forward(dev.dims, cw, dev.H, dev.parent, pk[:P], pv[:P], P, 0.05, out, ws)
+        else:
+            out = torch.empty(R, n_q * hd, **bf)
+            B.specfold_attention(dev.dims, Q, pk[:P], pv[:P], P, bK, bV, src, packed, n, nb, L, out, ws)
+        return out
+
+    for whole in (False, True):
+        ref = step(whole, True)
+        outs = [step(whole, False) for _ in range(20)]
+        torch.cuda.synchronize()
+        assert B.specfold_get_status(ws) == 0
+        assert torch.isfinite(ref).all() and all(torch.equal(o, ref) for o in outs)
