@@ -485,8 +485,9 @@ int specfold_qk_norm_rope(int dtype, int T, int n_q, int n_kv, int head_dim, spe
  *   status   device uint32 or NULL
  * T is the capacity of the row lists (T >= row_start[n_seqs]); positions has
  * T entries.  Nothing but the rows' own tokens is written; rows behind
- * row_start[n_seqs] are not touched.  Two rows that name the same pool token
- * (tables that share a page there) leave either one's values.  A page
+ * row_start[n_seqs] are not touched.  Rows that name the same pool token
+ * (tables that share a page there) leave a mixture of themselves in it: each
+ * element is one of theirs, keys and values apart.  A page
  * outside the pool or a token past the table drops the row and sets
  * SPECFOLD_DEV_BAD_PAGE; a row_start entry that descends, is negative or
  * above T, a negative ctx_len or a `rows` entry outside [0, n_src) drops that
@@ -514,7 +515,7 @@ int specfold_kv_append(int dtype, int T, int n_kv, int head_dim, specfold_head_r
  * Tokens that a row does not see change nothing in its output, whatever
  * their pages hold (infinities and NaN included).  Rows of o that belong to
  * no sequence stay as they were, as do those of a sequence whose row_start,
- * ctx_len or row count is invalid (SPECFOLD_DEV_BAD_SEQ), or every row where
+ * ctx_len (at most 2^31 - 513) or row count is invalid (SPECFOLD_DEV_BAD_SEQ), or every row where
  * the batch as a whole counts more than 10^8 blocks of keys (the same bit): a
  * sequence with rows has ceil((ctx_len + rows) / 64) of them for every
  * key/value head, or / 128 for bf16 with max_nodes * n_q / n_kv above 16 (head

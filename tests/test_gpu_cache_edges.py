@@ -142,3 +142,20 @@ def test_prefix_read_right_behind_the_call_that_writes_it(B, writer, P):
         torch.cuda.synchronize()
         assert B.specfold_get_status(ws) == 0
         assert torch.isfinite(ref).all() and all(torch.equal(o, ref) for o in outs)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_rows_that_name_one_token_leave_elements_of_theirs(B, dt):
+    """Forty sequences whose tables share a page write the same eight tokens."""
+    n_seqs, n_kv, hd = 40, 5, 128
+    gen = torch.Generator(device="cuda").manual_seed(65)
+    x = torch.randn(n_seqs * 8, 2, n_kv, hd, device="cuda", generator=gen).to(DT[dt])
+    kp, vp = torch.zeros(2, 32, n_kv, hd, device="cuda", dtype=DT[dt])
+    cache = B.PagedCache(kp, vp, torch.full((n_seqs, 1), 2, dtype=torch.int32, device="cuda"), 8)
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    B.specfold_kv_append(x[:, 0], x[:, 1], cache, ints(np.arange(n_seqs + 1) * 8), ints(np.zeros(n_seqs)), status=status)
+    torch.cuda.synchronize()
+    assert int(status) == 0
+    for pool, src in ((kp, x[:, 0]), (vp, x[:, 1])):
+        assert (pool[16:24][None] == src.reshape(n_seqs, 8, n_kv, hd)).any(0).all()
+        assert (pool[:16] == 0).all() and (pool[24:] == 0).all()
