@@ -14,7 +14,8 @@
 // that the wrapping 64-bit product p * F_j is the angle reduced to one turn, for
 // every 32-bit position: no large floating product and no 64-bit floating
 // arithmetic on the device.  f_j itself is computed on the host in 64 bits, which
-// leaves the angle off by at most p * 2^-49 turns.
+// leaves the angle off by at most p * 2^-49 turns (a base below one, whose
+// frequencies rise: p * 2^-49 / theta).
 //
 // Both may release their dependents early, although what they write may be the prefix of
 // the layer's attention, which reads it before its wait: no call of this library starts
@@ -32,10 +33,14 @@ namespace {
 
 constexpr int kThreads = 256;
 // Resident blocks an SM, which cap the registers.  Measured (16381 rows of 24 + 8
-// heads; 16331 rows of 8 heads appended): 2, 3, 4, 5 blocks 56.5, 48.3, 46.3,
+// heads; 12233 rows of 8 heads appended): 2, 3, 4, 5 blocks 56.5, 48.3, 46.3,
 // 68.5 us and 24.0, 21.0, 23.8, 27.5 us (one group in flight): fewer hold too few
-// bytes in flight, more spill.  That is 5800 GB/s of the rows' 268 MB (copy peak
-// 6690); head size 64 5740, fp32 5450 to 5590.
+// bytes in flight, more spill (four spill a little of the norm: 32 or 36 bytes a
+// thread, fp32 104).  That is 5820 GB/s of the rows' 268 MB (copy peak 6690); the same
+// rows of head size 64 4850 (134 MB), fp32 5430 (half the rows) and 5570.  The append
+// moves its 100 MB at 5030 GB/s, 50 MB of head size 64 at 4050, fp32 at 5710 (201 MB)
+// and 5160: the grid is one round of chunks of seven rows, DRAM is busy 36 % of it, and
+// the warps that have values only are done early.
 constexpr int kQkBlocks = 4, kAppendBlocks = 3;
 
 // A lane's two runs of eight elements as they lie in memory: what a warp has in
@@ -364,8 +369,8 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) kv_append_kernel(cons
         }
       }
     };
-    // (16331 rows of 8 heads, 134 MB of which L2 keeps a part: 21.0 us with one,
-    // 19.9 with two, 21.3 with three; fp32 has as many bytes in one)
+    // (12233 rows of 8 heads: 21.0 us with one, 19.9 with two, 21.3 with three; fp32
+    // has as many bytes in one)
     constexpr int kDepth = sizeof(T) == 2 ? 2 : 1;
     Raw<T> flight[kDepth] = {};
     At ahead = {0, 0}, now = {0, 0};

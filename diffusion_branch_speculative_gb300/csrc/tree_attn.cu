@@ -95,7 +95,7 @@ struct Simt {
   static constexpr int OFF_Q = kWarps * (RING > MERGE ? RING : MERGE);
   static constexpr int OFF_P = OFF_Q + RT * HD * 4;
   static constexpr int SMEM = OFF_P + kWarps * CH * RT * 4;
-  static constexpr int CTAS = 3;  // per SM: 68 to 71 KB each
+  static constexpr int CTAS = 3;  // per SM: 68 to 71 KB each (168 registers; head size 128 spills 8 bytes)
 };
 
 template <int HD>

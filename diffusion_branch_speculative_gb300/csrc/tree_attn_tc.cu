@@ -18,9 +18,9 @@
 // a block: the products alone take 2050 cycles for both lanes, 2700 beside the
 // loads and the softmax's TMEM traffic, the chain 3900.  Measured (us, with the
 // merge; floors by 6690 GB/s and 1925 TFLOP/s; 8, 4 and 8 key/value heads):
-//   1 sequence of 40000 tokens, 61 rows of 3 heads a group     50.4  (floor 24.6)
+//   1 sequence of 40000 tokens, 61 rows of 3 heads a group     51.2  (floor 24.6)
 //   16 padded sequences of 8192, 33 rows of 7                  63.8  (29.3)
-//   32 sequences of 8192, 128 rows of 3                       251    (120.9)
+//   32 sequences of 8192, 128 rows of 3                       248 to 260 by the box (120.9)
 // The tensor cores are busy 35, 33 and 44 % of the kernel's time; start, first
 // loads and merge are some 12 us of each.  No faster, beside 58.7, 65.5 and 246
 // before the merge was: two threads a row (640 threads; 67, 72, 271), P handed
@@ -28,7 +28,7 @@
 // 66.1, 250), the first keys ahead of all other loads (61.5, 70.4, 268: CTAs in
 // step ask the memory in bursts), 64 keys a step.
 //
-// Roles (384 threads): warp 0 loads keys, warp 1 values, both the queries; warp 2
+// Roles (384 threads of 168 registers, which spill 40 bytes, 84 for head size 64): warp 0 loads keys, warp 1 values, both the queries; warp 2
 // issues all products (warp 3 owns the TMEM allocation), warps 4-7 and 8-11 are
 // the lanes' softmax.  One issuer, so that a lane's P V and next Q K^T go out in
 // one run and the lanes fall into alternation (with an issuer each, both lanes'

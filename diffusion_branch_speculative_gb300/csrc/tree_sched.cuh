@@ -130,7 +130,7 @@ struct TreeWalk {
 // Places is 64 bits where the line may be longer than 32 bits hold (10^8 blocks times
 // up to 4096 tiles of a head group's rows; a run's places fit always: 4.1 10^11 over
 // the fp32 kernel's 456 CTAs, 6.4 10^10 over the tcgen05 kernel's 152), and that form
-// alone asks for the limit.  With it for every call the tcgen05 kernel took 2 us more.
+// alone asks for the limit.  With it for every call the tcgen05 kernel took 1 to 2 us more.
 template <typename Places>
 SF_DEV bool tree_locate_in(const TreeArgs& p, TreeWalk& w, unsigned& per) {
   constexpr bool kLong = sizeof(Places) == 8;
