@@ -21,6 +21,7 @@ HEADER = os.path.join(os.path.dirname(PKG), "include", "specfold.h")
 OK, EINVAL, EALIGN, ECAPACITY, EUNSUPPORTED, ECUDA, EDEVICE = 0, -1, -2, -3, -4, -5, -6
 DEV_TIMEOUT, DEV_BAD_PARENT, DEV_BAD_PAGE, DEV_BAD_SEQ = 1, 2, 4, 8
 MAX_SEQS, MAX_TREE, MAX_HEADS, TREE_PAD = 1024, 256, 65536, -2
+MAX_AXES, AXES_BLOCKS, AXES_IN_TURN = 4, 0, 1
 DEV_SITE_SHIFT = 8  # with DEV_TIMEOUT: bit DEV_SITE_SHIFT + site names the wait that ran out
 DEV_SITES = ("attention loader: Q buffer free", "attention loader: K/V stage free", "attention softmax: S ready",
              "attention softmax: P V before a rescale", "attention softmax: P V before the last P",
@@ -76,6 +77,25 @@ class specfold_paged_cache(ctypes.Structure):
                 ("table_pages", ctypes.c_int32), ("page_size", ctypes.c_int32), ("num_pages", ctypes.c_int32)]
 
 
+class specfold_rope_axes(ctypes.Structure):
+    _fields_ = [("theta", ctypes.c_float), ("n_axes", ctypes.c_int), ("pairs", ctypes.c_int * MAX_AXES),
+                ("order", ctypes.c_int), ("own_frequencies", ctypes.c_int)]
+
+
+class specfold_axis_positions(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("axis_stride", ctypes.c_int64)]
+
+
+class specfold_token_weights(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("seq_stride", ctypes.c_int64), ("head_stride", ctypes.c_int64),
+                ("tokens", ctypes.c_int32)]
+
+
+class specfold_kept_tokens(ctypes.Structure):
+    _fields_ = [("ptr", ctypes.c_void_p), ("seq_stride", ctypes.c_int64), ("set_stride", ctypes.c_int64),
+                ("n_sets", ctypes.c_int32), ("cap", ctypes.c_int32)]
+
+
 class specfold_ws_layout(ctypes.Structure):
     _fields_ = [(k, ctypes.c_size_t) for k in
                 ("status", "n_packed", "fold", "rel", "src", "packed_idx", "slot_of_row", "dep_rng", "dep_rows", "sync", "x1", "q",
@@ -110,6 +130,15 @@ _SIG = {
     "specfold_tree_attention": (_I, [_I, _I, _I, _I, _I, _I, specfold_head_rows, _P, _P, _P, _P, _I, ctypes.c_float,
                                      specfold_head_rows, _P, ctypes.c_size_t, _P]),
     "specfold_tree_attention_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I]),
+    "specfold_qk_norm_rope_axes": (_I, [_I, _I, _I, _I, _I, specfold_head_rows, specfold_head_rows, specfold_head_rows,
+                                        specfold_head_rows, _P, _P, ctypes.c_float, _P, specfold_axis_positions, _P]),
+    "specfold_kv_append_axes": (_I, [_I, _I, _I, _I, specfold_head_rows, specfold_head_rows, _I, _P, _P, ctypes.c_float,
+                                     _P, specfold_axis_positions, _P, _P, _P, _I, _P, _P]),
+    "specfold_kv_weigh": (_I, [_I, _I, _I, _I, _I, _I, specfold_head_rows, _I, _P, _P, _P, _P, _I, ctypes.c_float,
+                               ctypes.c_float, specfold_token_weights, _P, ctypes.c_size_t, _P]),
+    "specfold_kv_weigh_workspace_size": (ctypes.c_size_t, [_I, _I, _I, _I, _I, _I, _I, _I]),
+    "specfold_kv_select": (_I, [specfold_token_weights, _P, _I, _I, _I, _I, specfold_kept_tokens, _P, _P, _P]),
+    "specfold_kv_compact": (_I, [_I, _I, _I, _P, specfold_kept_tokens, _P, _P, _I, _P, _P, _P]),
     "specfold_linear": (_I, [_I, _P, _P, _I, _I, _I, _P, _P, ctypes.c_size_t, _P]),
     "specfold_linear_noalloc": (_I, [_I, _P, _P, _I, _I, _I, _P, _P]),
     "specfold_workspace_size": (ctypes.c_size_t, [_P, _I, _I]),
@@ -485,6 +514,171 @@ def specfold_tree_attention(Q: torch.Tensor, cache: PagedCache, parent: Optional
           _vec(parent, T, torch.int32, dev, "parent"), _vec(row_start, n_seqs + 1, torch.int32, dev, "row_start"),
           _vec(ctx_len, n_seqs, torch.int32, dev, "ctx_len"), n_seqs, scale,
           _head_rows(O, T, n_q, hd, dtype, dev, "O"), ws.data_ptr(), ws.numel())
+
+
+# ---- positions with several axes ----
+
+class RopeAxes:
+    """A rotation by several axes (specfold_rope_axes): `pairs` has every
+    axis's share of the hd/2 rotation pairs, in blocks one after the other or
+    in turn; own_frequencies: an axis's frequencies go by the place among its
+    own pairs."""
+
+    def __init__(self, theta: float, pairs: Sequence[int], in_turn: bool = False, own_frequencies: bool = False):
+        self.pairs = tuple(int(n) for n in pairs)
+        if not 1 <= len(self.pairs) <= MAX_AXES:
+            raise ValueError(f"1 to {MAX_AXES} axes")
+        self.theta, self.in_turn, self.own_frequencies = float(theta), bool(in_turn), bool(own_frequencies)
+        self.struct = specfold_rope_axes(self.theta, len(self.pairs), (ctypes.c_int * MAX_AXES)(*self.pairs),
+                                         AXES_IN_TURN if in_turn else AXES_BLOCKS, int(self.own_frequencies))
+        self.ref = ctypes.byref(self.struct)
+
+
+def _axis_positions(t: Optional[torch.Tensor], axes: RopeAxes, rows: int, dev: int) -> specfold_axis_positions:
+    if t is None:
+        raise ValueError("a rotation needs positions")
+    if t.dim() != 2 or t.dtype is not torch.int32 or t.get_device() != dev:
+        raise ValueError("positions are int32 [axes, rows] on the device of the other tensors")
+    n, have = t.shape
+    if n != len(axes.pairs) or have < rows:
+        raise ValueError(f"positions must be [{len(axes.pairs)}, {rows}]")
+    by_axis, by_row = t.stride()
+    return specfold_axis_positions(t.data_ptr(), by_row, by_axis)
+
+
+def specfold_qk_norm_rope_axes(Q: Optional[torch.Tensor], K: Optional[torch.Tensor], Q_out: Optional[torch.Tensor],
+                               K_out: Optional[torch.Tensor], axes: RopeAxes, positions: torch.Tensor,
+                               gq: Optional[torch.Tensor] = None, gk: Optional[torch.Tensor] = None, eps: float = 1e-6,
+                               stream=None):
+    """specfold_qk_norm_rope with a rotation by several axes: positions int32
+    [axes, T], any strides."""
+    like = Q if Q is not None else K
+    if like is None:
+        raise ValueError("Q or K must be given")
+    T, n_q, hd = like.shape
+    n_kv = 0
+    dtype, dev = like.dtype, like.get_device()
+    q = qo = k = ko = _NO_ROWS
+    if Q is not None:
+        q = _head_rows(Q, T, n_q, hd, dtype, dev, "Q")
+        qo = _head_rows(Q_out, T, n_q, hd, dtype, dev, "Q_out")
+    else:
+        n_q = 0
+    if K is not None:
+        n_kv = K.shape[1] if K.dim() == 3 else 0
+        k = _head_rows(K, T, n_kv, hd, dtype, dev, "K")
+        ko = _head_rows(K_out, T, n_kv, hd, dtype, dev, "K_out")
+    _device_of(like)
+    _call(lib().specfold_qk_norm_rope_axes, "specfold_qk_norm_rope_axes", dev, stream, dtype_code(dtype), T, n_q, n_kv,
+          hd, q, k, qo, ko, _vec(gq, hd, dtype, dev, "gq"), _vec(gk, hd, dtype, dev, "gk"), eps, axes.ref,
+          _axis_positions(positions, axes, T, dev))
+
+
+def specfold_kv_append_axes(K: torch.Tensor, V: torch.Tensor, cache: PagedCache, row_start: torch.Tensor,
+                            ctx_len: torch.Tensor, axes: RopeAxes, positions: torch.Tensor,
+                            gk: Optional[torch.Tensor] = None, eps: float = 1e-6, rows: Optional[torch.Tensor] = None,
+                            status: Optional[torch.Tensor] = None, stream=None):
+    """specfold_kv_append with the keys rotated by several axes: positions
+    int32 [axes, T], any strides, one column for every row of the batch."""
+    n_seqs, n_src = ctx_len.shape[0], K.shape[0]
+    T = n_src if rows is None else rows.shape[0]
+    dtype, dev, n_kv, hd = cache.dtype, cache.device.index, cache.n_kv, cache.head_dim
+    _check_batch(cache, n_seqs, status, dev)
+    _call(lib().specfold_kv_append_axes, "specfold_kv_append_axes", dev, stream, dtype_code(dtype), T, n_kv, hd,
+          _head_rows(K, n_src, n_kv, hd, dtype, dev, "K"), _head_rows(V, n_src, n_kv, hd, dtype, dev, "V"), n_src,
+          _vec(rows, T, torch.int32, dev, "rows"), _vec(gk, hd, dtype, dev, "gk"), eps, axes.ref,
+          _axis_positions(positions, axes, T, dev), cache.ref, _vec(row_start, n_seqs + 1, torch.int32, dev, "row_start"),
+          _vec(ctx_len, n_seqs, torch.int32, dev, "ctx_len"), n_seqs, None if status is None else status.data_ptr())
+
+
+# ---- thinning out a paged cache ----
+
+def _check_batch(cache: PagedCache, n_seqs: int, status: Optional[torch.Tensor], dev: int):
+    if n_seqs > cache.n_seqs:
+        raise ValueError("the cache has a table for every sequence")
+    _check_status(status, dev)
+
+
+def _check_status(status: Optional[torch.Tensor], dev: int):
+    if status is not None and (status.element_size() != 4 or status.get_device() != dev):
+        raise ValueError("status is one 32-bit word on the same device")
+
+
+def _per_token(t: torch.Tensor, n_seqs: int, heads: int, dtype, dev: int, what: str):
+    """Pointer, the two outer strides and the length of a [n_seqs, heads, n]
+    tensor with unit last stride."""
+    s0, s1, s2 = t.stride() if t.dim() == 3 else (0, 0, 0)
+    if s2 != 1 and not (t.dim() == 3 and t.shape[2] == 1) or t.shape[0] < n_seqs or t.shape[1] != heads:
+        raise ValueError(f"{what} must be [{n_seqs}, {heads}, n] with unit last stride")
+    if t.dtype is not dtype or t.get_device() != dev:
+        raise ValueError(f"{what} must be {dtype} on the device of the other tensors")
+    return t.data_ptr(), s0, s1, t.shape[2]
+
+
+def kv_weigh_workspace_size(dtype: int, T: int, max_rows: int, n_q: int, n_kv: int, hd: int, n_seqs: int,
+                            tokens: int) -> int:
+    return int(lib().specfold_kv_weigh_workspace_size(dtype, T, max_rows, n_q, n_kv, hd, n_seqs, tokens))
+
+
+def specfold_kv_weigh(Q: torch.Tensor, cache: PagedCache, row_start: torch.Tensor, ctx_len: torch.Tensor, max_rows: int,
+                      weights: torch.Tensor, ws: torch.Tensor, decay: float = 1.0, rows: Optional[torch.Tensor] = None,
+                      scale: float = 0.0, stream=None):
+    """Adds the attention weights of the batch's rows (their keys already
+    appended; a row sees its sequence's tokens up to its own) to `weights`,
+    float32 [n_seqs, n_kv, tokens]: cached tokens' old weights times `decay`
+    plus the sum over rows and the group's heads, the batch's own tokens that
+    sum alone.  Q [n_src, n_q, hd]; `rows` (int32) picks its rows, one per
+    batch row; ws: kv_weigh_workspace_size bytes."""
+    n_src, n_q, hd = Q.shape
+    n_seqs = ctx_len.shape[0]
+    T = n_src if rows is None else rows.shape[0]
+    if hd != cache.head_dim or n_seqs > cache.n_seqs:
+        raise ValueError("Q has the cache's head size, the cache a table for every sequence")
+    dtype, dev, n_kv = cache.dtype, cache.device.index, cache.n_kv
+    if ws.get_device() != dev or ws.element_size() != 1 or ws.stride(0) != 1:
+        raise ValueError("ws is a byte workspace on the same device")
+    _call(lib().specfold_kv_weigh, "specfold_kv_weigh", dev, stream, dtype_code(dtype), T, max_rows, n_q, n_kv, hd,
+          _head_rows(Q, n_src, n_q, hd, dtype, dev, "Q"), n_src, _vec(rows, T, torch.int32, dev, "rows"), cache.ref,
+          _vec(row_start, n_seqs + 1, torch.int32, dev, "row_start"), _vec(ctx_len, n_seqs, torch.int32, dev, "ctx_len"),
+          n_seqs, scale, decay, specfold_token_weights(*_per_token(weights, n_seqs, n_kv, torch.float32, dev, "weights")),
+          ws.data_ptr(), ws.numel())
+
+
+def specfold_kv_select(weights: torch.Tensor, lengths: torch.Tensor, keep: int, kept: torch.Tensor,
+                       new_len: torch.Tensor, sinks: int = 0, recent: int = 0, status: Optional[torch.Tensor] = None,
+                       stream=None):
+    """Writes to `kept` (int32 [n_seqs, sets, >= keep]) the tokens that stay of
+    every sequence's lengths[s], ascending: all, or the first `sinks`, the last
+    `recent` and the largest of `weights` (float32 [n_seqs, sets, tokens])
+    between them, `keep` in all; their number to new_len (int32 [n_seqs])."""
+    n_seqs, dev = lengths.shape[0], _device_of(lengths)
+    n_sets = weights.shape[1]
+    _check_status(status, dev)
+    k, k0, k1, cap = _per_token(kept, n_seqs, n_sets, torch.int32, dev, "kept")
+    _call(lib().specfold_kv_select, "specfold_kv_select", dev, stream,
+          specfold_token_weights(*_per_token(weights, n_seqs, n_sets, torch.float32, dev, "weights")),
+          _vec(lengths, n_seqs, torch.int32, dev, "lengths"), n_seqs, keep, sinks, recent,
+          specfold_kept_tokens(k, k0, k1, n_sets, cap), _vec(new_len, n_seqs, torch.int32, dev, "new_len"),
+          None if status is None else status.data_ptr())
+
+
+def specfold_kv_compact(cache: PagedCache, kept: torch.Tensor, lengths: torch.Tensor, new_len: torch.Tensor,
+                        weights: Optional[torch.Tensor] = None, status: Optional[torch.Tensor] = None, stream=None):
+    """Moves the kept tokens of every sequence (kept int32 [n_seqs, n_kv or 1,
+    n], new_len[s] of lengths[s], ascending) to the front of its pages, keys
+    and values in place, and with them their `weights` (float32 [n_seqs, n_kv
+    or 1, tokens])."""
+    n_seqs, n_sets = lengths.shape[0], kept.shape[1]
+    dev = cache.device.index
+    _check_batch(cache, n_seqs, status, dev)
+    k, k0, k1, cap = _per_token(kept, n_seqs, n_sets, torch.int32, dev, "kept")
+    w = None
+    if weights is not None:
+        w = ctypes.byref(specfold_token_weights(*_per_token(weights, n_seqs, n_sets, torch.float32, dev, "weights")))
+    _call(lib().specfold_kv_compact, "specfold_kv_compact", dev, stream, dtype_code(cache.dtype), cache.n_kv,
+          cache.head_dim, cache.ref, specfold_kept_tokens(k, k0, k1, n_sets, cap),
+          _vec(lengths, n_seqs, torch.int32, dev, "lengths"), _vec(new_len, n_seqs, torch.int32, dev, "new_len"), n_seqs,
+          w, None if status is None else status.data_ptr())
 
 
 def stack_workspace_size(dims: specfold_dims, B: int, L: int) -> int:

@@ -244,6 +244,55 @@ static int check_tree_shape(int dtype, int n_q, int n_kv, int hd, int max_nodes)
   return max_nodes <= SPECFOLD_MAX_TREE && n_q <= SPECFOLD_MAX_HEADS ? SPECFOLD_OK : SPECFOLD_ECAPACITY;
 }
 
+// ---- positions with several axes, thinning out a cache ----
+static int check_axes(const specfold_rope_axes* x, int hd) {
+  if (!x || !(x->theta > 0.f) || x->n_axes < 1 || x->n_axes > SPECFOLD_MAX_AXES) return SPECFOLD_EINVAL;
+  if (x->order != SPECFOLD_AXES_BLOCKS && x->order != SPECFOLD_AXES_IN_TURN) return SPECFOLD_EINVAL;
+  if (x->own_frequencies != 0 && x->own_frequencies != 1) return SPECFOLD_EINVAL;
+  if (hd != 64 && hd != 128) return SPECFOLD_EUNSUPPORTED;
+  int left = hd / 2;
+  for (int a = 0; a < x->n_axes; ++a) {
+    if (x->pairs[a] < 0 || x->pairs[a] > left) return SPECFOLD_EINVAL;
+    left -= x->pairs[a];
+  }
+  return left == 0 ? SPECFOLD_OK : SPECFOLD_EINVAL;
+}
+
+// Entries [a][b][n] with strides sa, sb and 1, the smaller of the two within the larger,
+// lie apart.
+static bool nested(long long na, long long sa, long long nb, long long sb, long long n) {
+  if (na > 1 && nb > 1 && sa < sb) return nested(nb, sb, na, sa, n);
+  if (nb > 1) {
+    if (sb < n) return false;
+    // (what would pass 64 bits lies apart from anything)
+    if (sb > (0x7fffffffffffffffLL - n) / (nb - 1)) return na <= 1;
+    n += (nb - 1) * sb;
+  }
+  return na <= 1 || sa >= n;
+}
+
+// n_seqs sequences of `heads` heads; written: entries have to lie apart.
+static int check_token_weights(const specfold_token_weights& w, int n_seqs, int heads, bool written) {
+  if (!w.ptr || w.seq_stride < 0 || w.head_stride < 0 || w.tokens < 1) return SPECFOLD_EINVAL;
+  if (reinterpret_cast<uintptr_t>(w.ptr) % sizeof(float)) return SPECFOLD_EALIGN;
+  return !written || nested(n_seqs, w.seq_stride, heads, w.head_stride, w.tokens) ? SPECFOLD_OK : SPECFOLD_EINVAL;
+}
+
+static int check_kept(const specfold_kept_tokens& k, int n_seqs, bool written) {
+  if (!k.ptr || k.seq_stride < 0 || k.set_stride < 0 || k.n_sets < 1 || k.cap < 1) return SPECFOLD_EINVAL;
+  if (k.n_sets > SPECFOLD_MAX_HEADS) return SPECFOLD_ECAPACITY;
+  if (reinterpret_cast<uintptr_t>(k.ptr) % sizeof(int32_t)) return SPECFOLD_EALIGN;
+  return !written || nested(n_seqs, k.seq_stride, k.n_sets, k.set_stride, k.cap) ? SPECFOLD_OK : SPECFOLD_EINVAL;
+}
+
+// lengths are read by blocks while others write new_len
+static int check_lengths(const int32_t* lengths, const int32_t* new_len, int n_seqs) {
+  if (!lengths || !new_len || n_seqs < 1) return SPECFOLD_EINVAL;
+  if (n_seqs > SPECFOLD_MAX_SEQS) return SPECFOLD_ECAPACITY;
+  const intptr_t d = reinterpret_cast<intptr_t>(new_len) - reinterpret_cast<intptr_t>(lengths);
+  return std::llabs(d) < 4LL * n_seqs ? SPECFOLD_EINVAL : SPECFOLD_OK;
+}
+
 // ------------------------------------------------------ workspace layout --
 static size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
@@ -687,15 +736,14 @@ int specfold_workspace_layout(const specfold_dims* dims, int B, int L, specfold_
   return SPECFOLD_OK;
 }
 
-int specfold_qk_norm_rope(int dtype, int T, int n_q, int n_kv, int head_dim, specfold_head_rows q_in,
-                          specfold_head_rows k_in, specfold_head_rows q_out, specfold_head_rows k_out,
-                          const void* gq, const void* gk, float eps, const int32_t* positions, float rope_theta,
-                          void* stream) {
-  SF_TRY(check_norm_rope(dtype, T, head_dim, eps, rope_theta));
+static int qk_norm_rope(int dtype, int T, int n_q, int n_kv, int head_dim, const specfold_head_rows& q_in,
+                        const specfold_head_rows& k_in, const specfold_head_rows& q_out, const specfold_head_rows& k_out,
+                        const void* gq, const void* gk, float eps, const RopePlan& rope, void* stream) {
+  SF_TRY(check_norm_rope(dtype, T, head_dim, eps, rope.theta));
   if (n_q < 0 || n_kv < 0) return SPECFOLD_EINVAL;
   if (n_q > SPECFOLD_MAX_HEADS || n_kv > SPECFOLD_MAX_HEADS) return SPECFOLD_ECAPACITY;
   if (T == 0 || n_q + n_kv == 0) return SPECFOLD_OK;
-  if (rope_theta > 0.f && !positions) return SPECFOLD_EINVAL;
+  if (rope.theta > 0.f && !rope.positions) return SPECFOLD_EINVAL;
   if (n_q > 0) {
     SF_TRY(check_head_rows(q_in));
     SF_TRY(check_head_rows(q_out));
@@ -704,21 +752,39 @@ int specfold_qk_norm_rope(int dtype, int T, int n_q, int n_kv, int head_dim, spe
     SF_TRY(check_head_rows(k_in));
     SF_TRY(check_head_rows(k_out));
   }
-  QkNormRopeCall c{dtype, T, n_q, n_kv, head_dim, q_in, k_in, q_out, k_out, gq, gk, eps, positions, rope_theta};
+  QkNormRopeCall c{dtype, T, n_q, n_kv, head_dim, q_in, k_in, q_out, k_out, gq, gk, eps, rope};
   return launch_qk_norm_rope(c, static_cast<cudaStream_t>(stream));
 }
 
-int specfold_kv_append(int dtype, int T, int n_kv, int head_dim, specfold_head_rows k, specfold_head_rows v, int n_src,
-                       const int32_t* rows, const void* gk, float eps, const int32_t* positions, float rope_theta,
-                       const specfold_paged_cache* cache, const int32_t* row_start, const int32_t* ctx_len, int n_seqs,
-                       uint32_t* status, void* stream) {
-  SF_TRY(check_norm_rope(dtype, T, head_dim, eps, rope_theta));
+int specfold_qk_norm_rope(int dtype, int T, int n_q, int n_kv, int head_dim, specfold_head_rows q_in,
+                          specfold_head_rows k_in, specfold_head_rows q_out, specfold_head_rows k_out,
+                          const void* gq, const void* gk, float eps, const int32_t* positions, float rope_theta,
+                          void* stream) {
+  return qk_norm_rope(dtype, T, n_q, n_kv, head_dim, q_in, k_in, q_out, k_out, gq, gk, eps, {positions, rope_theta},
+                      stream);
+}
+
+int specfold_qk_norm_rope_axes(int dtype, int T, int n_q, int n_kv, int head_dim, specfold_head_rows q_in,
+                               specfold_head_rows k_in, specfold_head_rows q_out, specfold_head_rows k_out,
+                               const void* gq, const void* gk, float eps, const specfold_rope_axes* axes,
+                               specfold_axis_positions positions, void* stream) {
+  SF_TRY(check_axes(axes, head_dim));
+  return qk_norm_rope(dtype, T, n_q, n_kv, head_dim, q_in, k_in, q_out, k_out, gq, gk, eps,
+                      {positions.ptr, axes->theta, axes, positions.row_stride, positions.axis_stride}, stream);
+}
+
+static int kv_append(int dtype, int T, int n_kv, int head_dim, const specfold_head_rows& k, const specfold_head_rows& v,
+                     int n_src, const int32_t* rows, const void* gk, float eps, const RopePlan& rope,
+                     const specfold_paged_cache* cache, const int32_t* row_start, const int32_t* ctx_len, int n_seqs,
+                     uint32_t* status, void* stream) {
+  SF_TRY(check_norm_rope(dtype, T, head_dim, eps, rope.theta));
   if (n_kv <= 0 || n_src < 0) return SPECFOLD_EINVAL;
   if (n_kv > SPECFOLD_MAX_HEADS) return SPECFOLD_ECAPACITY;
   SF_TRY(check_paged_cache(cache));
   SF_TRY(check_batch(row_start, ctx_len, n_seqs));
   if (!rows && n_src < T) return SPECFOLD_EINVAL;
   if (T == 0) return SPECFOLD_OK;
+  if (rope.axes && !rope.positions) return SPECFOLD_EINVAL;
   if (n_src > 0) {
     SF_TRY(check_head_rows(k));
     SF_TRY(check_head_rows(v));
@@ -732,9 +798,27 @@ int specfold_kv_append(int dtype, int T, int n_kv, int head_dim, specfold_head_r
                        dtype == SPECFOLD_BF16 ? 2 : 4))
           return SPECFOLD_EINVAL;
   }
-  KvAppendCall c{dtype, n_kv, head_dim, k, v, n_src, rows, gk, eps, positions, rope_theta, *cache,
-                 {row_start, ctx_len, n_seqs, T}, status};
+  KvAppendCall c{dtype, n_kv, head_dim, k, v, n_src, rows, gk, eps, rope, *cache, {row_start, ctx_len, n_seqs, T}, status};
   return launch_kv_append(c, static_cast<cudaStream_t>(stream));
+}
+
+int specfold_kv_append(int dtype, int T, int n_kv, int head_dim, specfold_head_rows k, specfold_head_rows v, int n_src,
+                       const int32_t* rows, const void* gk, float eps, const int32_t* positions, float rope_theta,
+                       const specfold_paged_cache* cache, const int32_t* row_start, const int32_t* ctx_len, int n_seqs,
+                       uint32_t* status, void* stream) {
+  return kv_append(dtype, T, n_kv, head_dim, k, v, n_src, rows, gk, eps, {positions, rope_theta}, cache, row_start, ctx_len,
+                   n_seqs, status, stream);
+}
+
+int specfold_kv_append_axes(int dtype, int T, int n_kv, int head_dim, specfold_head_rows k, specfold_head_rows v,
+                            int n_src, const int32_t* rows, const void* gk, float eps, const specfold_rope_axes* axes,
+                            specfold_axis_positions positions, const specfold_paged_cache* cache,
+                            const int32_t* row_start, const int32_t* ctx_len, int n_seqs, uint32_t* status,
+                            void* stream) {
+  SF_TRY(check_axes(axes, head_dim));
+  return kv_append(dtype, T, n_kv, head_dim, k, v, n_src, rows, gk, eps,
+                   {positions.ptr, axes->theta, axes, positions.row_stride, positions.axis_stride}, cache, row_start,
+                   ctx_len, n_seqs, status, stream);
 }
 
 size_t specfold_tree_attention_workspace_size(int dtype, int n_q, int n_kv, int head_dim, int max_nodes) {
@@ -758,6 +842,60 @@ int specfold_tree_attention(int dtype, int T, int max_nodes, int n_q, int n_kv, 
   SF_TRY(check_head_rows(o));
   TreeAttnCall c{dtype, n_q, n_kv, head_dim, max_nodes, q, o, *cache, parent, {row_start, ctx_len, n_seqs, T}, scale, ws};
   return launch_tree_attention(c, static_cast<cudaStream_t>(stream));
+}
+
+size_t specfold_kv_weigh_workspace_size(int dtype, int T, int max_rows, int n_q, int n_kv, int head_dim, int n_seqs,
+                                        int tokens) {
+  if (check_tree_shape(dtype, n_q, n_kv, head_dim, max_rows) || T < 0 || n_seqs < 1 || n_seqs > SPECFOLD_MAX_SEQS ||
+      tokens < 1)
+    return 0;
+  return kv_weigh_ws_bytes(dtype, T, max_rows, n_q, n_kv, head_dim, n_seqs, tokens);
+}
+
+int specfold_kv_weigh(int dtype, int T, int max_rows, int n_q, int n_kv, int head_dim, specfold_head_rows q, int n_src,
+                      const int32_t* rows, const specfold_paged_cache* cache, const int32_t* row_start,
+                      const int32_t* ctx_len, int n_seqs, float scale, float decay, specfold_token_weights w, void* ws,
+                      size_t ws_bytes, void* stream) {
+  SF_TRY(check_tree_shape(dtype, n_q, n_kv, head_dim, max_rows));
+  if (T < 0 || !(scale >= 0.f) || std::isinf(scale) || !(decay >= 0.f) || std::isinf(decay)) return SPECFOLD_EINVAL;
+  SF_TRY(check_paged_cache(cache));
+  SF_TRY(check_batch(row_start, ctx_len, n_seqs));
+  SF_TRY(check_token_weights(w, n_seqs, n_kv, true));
+  if (!ws) return SPECFOLD_EINVAL;
+  if (!a16(ws)) return SPECFOLD_EALIGN;
+  if (ws_bytes < kv_weigh_ws_bytes(dtype, T, max_rows, n_q, n_kv, head_dim, n_seqs, w.tokens)) return SPECFOLD_ECAPACITY;
+  if (n_src < 0 || (!rows && n_src < T)) return SPECFOLD_EINVAL;
+  if (T == 0) return SPECFOLD_OK;
+  if (n_src == 0) return SPECFOLD_EINVAL;
+  SF_TRY(check_head_rows(q));
+  KvWeighCall c{dtype, n_q, n_kv, head_dim, max_rows, q, n_src, rows, *cache, {row_start, ctx_len, n_seqs, T}, scale, decay, w, ws};
+  return launch_kv_weigh(c, static_cast<cudaStream_t>(stream));
+}
+
+int specfold_kv_select(specfold_token_weights w, const int32_t* lengths, int n_seqs, int keep, int sinks, int recent,
+                       specfold_kept_tokens kept, int32_t* new_len, uint32_t* status, void* stream) {
+  SF_TRY(check_lengths(lengths, new_len, n_seqs));
+  SF_TRY(check_kept(kept, n_seqs, true));
+  SF_TRY(check_token_weights(w, n_seqs, kept.n_sets, false));
+  if (keep < 1 || sinks < 0 || recent < 0 || sinks > keep || recent > keep - sinks || keep > kept.cap)
+    return SPECFOLD_EINVAL;
+  KvSelectCall c{w, lengths, n_seqs, keep, sinks, recent, kept, new_len, status};
+  return launch_kv_select(c, static_cast<cudaStream_t>(stream));
+}
+
+int specfold_kv_compact(int dtype, int n_kv, int head_dim, const specfold_paged_cache* cache,
+                        specfold_kept_tokens kept, const int32_t* lengths, const int32_t* new_len, int n_seqs,
+                        const specfold_token_weights* w, uint32_t* status, void* stream) {
+  if (!dtype_ok(dtype) || n_kv <= 0) return SPECFOLD_EINVAL;
+  if (n_kv > SPECFOLD_MAX_HEADS) return SPECFOLD_ECAPACITY;
+  if (head_dim != 64 && head_dim != 128) return SPECFOLD_EUNSUPPORTED;
+  SF_TRY(check_paged_cache(cache));
+  SF_TRY(check_lengths(lengths, new_len, n_seqs));
+  SF_TRY(check_kept(kept, n_seqs, false));
+  if (kept.n_sets != n_kv && kept.n_sets != 1) return SPECFOLD_EINVAL;
+  if (w) SF_TRY(check_token_weights(*w, n_seqs, kept.n_sets, true));
+  KvCompactCall c{dtype, n_kv, head_dim, *cache, kept, lengths, new_len, n_seqs, w ? *w : specfold_token_weights{}, status};
+  return launch_kv_compact(c, static_cast<cudaStream_t>(stream));
 }
 
 size_t specfold_linear_workspace_size(int M, int N) {

@@ -107,18 +107,35 @@ void rope_turns(float theta, int hd, Turns* t) {
     t->f[j] = static_cast<uint64_t>((f - std::floor(f)) * 18446744073709551616.0);
 }
 
-// cos and sin of this lane's eight pairs (j = 8c .. 8c + 7) at position pos.
-// Lane l computes the pairs HD/64*l .. of the warp's HD/2 frequencies and the
-// eight come by shuffles: every angle once per warp.  For bf16 results the
-// special function unit's sine and cosine do (off by at most 2^-20 on one turn,
-// against a rounding of 2^-8).
+// The same for several axes, whose pairs come in blocks or in turn, by the pair's
+// place among all or among its axis's own; and the axis of every pair.
+void rope_turns(const specfold_rope_axes& x, int hd, Turns* t, uint8_t* axis) {
+  int done[SPECFOLD_MAX_AXES] = {};
+  int a = 0;
+  for (int j = 0; j < hd / 2; ++j) {
+    while (done[a] == x.pairs[a]) a = (a + 1) % x.n_axes;  // the pairs add up to hd / 2
+    const double at = x.own_frequencies ? static_cast<double>(done[a]) / x.pairs[a] : 2.0 * j / hd;
+    const double f = 0.15915494309189535 * std::pow(static_cast<double>(x.theta), -at);  // 1 / (2 pi)
+    t->f[j] = static_cast<uint64_t>((f - std::floor(f)) * 18446744073709551616.0);
+    axis[j] = static_cast<uint8_t>(a);
+    ++done[a];
+    if (x.order == SPECFOLD_AXES_IN_TURN) a = (a + 1) % x.n_axes;
+  }
+}
+
+// cos and sin of this lane's eight pairs (j = 8c .. 8c + 7), pair j at position
+// pos[j % PER] of the lane that computes it.  Lane l computes the pairs HD/64*l ..
+// of the warp's HD/2 frequencies and the eight come by shuffles: every angle once per
+// warp.  For bf16 results the special function unit's sine and cosine do (off by at
+// most 2^-20 on one turn, against a rounding of 2^-8).
 template <typename T, int HD>
-SF_DEV void lane_angles(const uint64_t* s_f, long long pos, int lane, int c, float2 (&cs)[4], float2 (&sn)[4]) {
+SF_DEV void lane_angles(const uint64_t* s_f, const long long (&pos)[HD / 64], int lane, int c, float2 (&cs)[4],
+                        float2 (&sn)[4]) {
   constexpr int PER = HD / 64;  // angles a lane computes: 2 or 1
   float myc[PER], mys[PER];
 #pragma unroll
   for (int e = 0; e < PER; ++e) {
-    const uint64_t turn = static_cast<uint64_t>(pos) * s_f[lane * PER + e];
+    const uint64_t turn = static_cast<uint64_t>(pos[e]) * s_f[lane * PER + e];
     // the fraction's upper 32 bits as a signed number: half turns in [-1, 1)
     const float half = static_cast<float>(static_cast<int32_t>(turn >> 32));
     if constexpr (sizeof(T) == 2)
@@ -135,6 +152,36 @@ SF_DEV void lane_angles(const uint64_t* s_f, long long pos, int lane, int c, flo
     sn[e] = make_float2(from(mys, 2 * e), from(mys, 2 * e + 1));
   }
 }
+
+// The rows' positions: one a row, or one a row and axis (AXES), of which a lane
+// reads those of its own pairs.
+struct Places {
+  const int32_t* p;  // null, for one a row: the token's own index
+  long long rs, as;  // from row to row, from axis to axis (AXES)
+  uint8_t axis[64];  // of every pair (AXES)
+};
+template <int HD, bool AXES>
+struct LanePlaces {
+  static constexpr int PER = HD / 64;
+  long long off[PER];
+  SF_DEV explicit LanePlaces(const Places& at, int lane) {
+    if constexpr (AXES) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) off[e] = at.axis[lane * PER + e] * at.as;
+    }
+  }
+  // row t's; own: the token's index
+  SF_DEV void read(const Places& at, long long t, long long own, long long (&pos)[PER]) const {
+    if constexpr (AXES) {
+#pragma unroll
+      for (int e = 0; e < PER; ++e) pos[e] = at.p[t * at.rs + off[e]];
+    } else {
+      const long long x = at.p ? at.p[t] : own;
+#pragma unroll
+      for (int e = 0; e < PER; ++e) pos[e] = x;
+    }
+  }
+};
 
 // One head's row in registers (two runs of eight, from 8c and HD/2 + 8c on): the
 // norm with the gain g (null: none), then the rotation.  The whole warp takes
@@ -183,15 +230,15 @@ struct QkArgs {
   Rows<T> q_in, k_in, q_out, k_out;
   const T* gq;
   const T* gk;
-  const int32_t* positions;
   int T_rows, n_q, n_kv, parts, rope;
   float eps;
   Turns turns;
+  Places places;
 };
 
 // Work item: row t, one of `parts` shares of its heads (a few rows alone
 // would leave most SMs idle), one warp each.
-template <typename T, int HD>
+template <typename T, int HD, bool AXES>
 __global__ void __launch_bounds__(kThreads, kQkBlocks) qk_norm_rope_kernel(const __grid_constant__ QkArgs<T> p) {
   constexpr int LPR = HD / 16, RPW = 32 / LPR;
   __shared__ uint64_t s_f[HD / 2];
@@ -205,6 +252,7 @@ __global__ void __launch_bounds__(kThreads, kQkBlocks) qk_norm_rope_kernel(const
   }
   __syncthreads();
   const int lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
+  const LanePlaces<HD, AXES> places(p.places, lane);
   // a unit is a group of heads that a warp holds at once, queries' before keys'
   const int units_q = (p.n_q + RPW - 1) / RPW, units = units_q + (p.n_kv + RPW - 1) / RPW;
   const long long items = static_cast<long long>(p.T_rows) * p.parts;
@@ -221,7 +269,11 @@ __global__ void __launch_bounds__(kThreads, kQkBlocks) qk_norm_rope_kernel(const
     Raw<T> next = {};
     read(first, next);
     float2 cs[4], sn[4];
-    if (p.rope) lane_angles<T, HD>(s_f, p.positions[t], lane, c, cs, sn);
+    if (p.rope) {
+      long long pos[HD / 64];
+      places.read(p.places, t, 0, pos);
+      lane_angles<T, HD>(s_f, pos, lane, c, cs, sn);
+    }
     for (int u = first; u < units; u += p.parts) {
       float2 a[4], b[4];
       next.unpack(0, a);
@@ -242,7 +294,20 @@ __global__ void __launch_bounds__(kThreads, kQkBlocks) qk_norm_rope_kernel(const
   }
 }
 
-template <typename T, int HD>
+// Frequencies and positions of a call; false: it does not rotate.
+bool rotation(const RopePlan& r, int hd, Turns* turns, Places* at) {
+  at->p = r.positions;
+  at->rs = r.row_stride;
+  at->as = r.axis_stride;
+  if (!r.axes) {
+    if (r.theta > 0.f) rope_turns(r.theta, hd, turns);
+    return r.theta > 0.f;
+  }
+  rope_turns(*r.axes, hd, turns, at->axis);
+  return true;
+}
+
+template <typename T, int HD, bool AXES>
 int qk_go(const QkNormRopeCall& c, cudaStream_t st) {
   QkArgs<T> a;
   a.q_in = rows_of<T>(c.q_in);
@@ -251,19 +316,17 @@ int qk_go(const QkNormRopeCall& c, cudaStream_t st) {
   a.k_out = rows_of<T>(c.k_out);
   a.gq = static_cast<const T*>(c.gq);
   a.gk = static_cast<const T*>(c.gk);
-  a.positions = c.positions;
   a.T_rows = c.T;
   a.n_q = c.n_q;
   a.n_kv = c.n_kv;
   a.eps = c.eps;
-  a.rope = c.theta > 0.f;
-  if (a.rope) rope_turns(c.theta, HD, &a.turns);
+  a.rope = rotation(c.rope, HD, &a.turns, &a.places);
   const int units = (c.n_q + 512 / HD - 1) / (512 / HD) + (c.n_kv + 512 / HD - 1) / (512 / HD);
   // shares of a row's heads: enough that the last round of the grid's warps weighs little
   const long long want = 6LL * kQkBlocks * num_sms() * (kThreads / 32);
   a.parts = static_cast<int>(std::min<long long>(units, std::max<long long>(1, (want + c.T - 1) / c.T)));
   const long long blocks = (static_cast<long long>(c.T) * a.parts + kThreads / 32 - 1) / (kThreads / 32);
-  launch_k(qk_norm_rope_kernel<T, HD>, dim3(static_cast<unsigned>(std::min<long long>(blocks, static_cast<long long>(kQkBlocks) * num_sms()))),
+  launch_k(qk_norm_rope_kernel<T, HD, AXES>, dim3(static_cast<unsigned>(std::min<long long>(blocks, static_cast<long long>(kQkBlocks) * num_sms()))),
            dim3(kThreads), 0, st, a);
   count_launch();
   return check_launch();
@@ -275,13 +338,13 @@ struct AppendArgs {
   Rows<T> k, v;
   const int32_t* rows;
   const T* gk;
-  const int32_t* positions;
   specfold_paged_cache cache;
   SeqBatch batch;
   uint32_t* status;
   int n_kv, n_src, rope, chunk;
   float eps;
   Turns turns;
+  Places places;
 };
 
 // Work item: the keys, or the values, of a chunk of consecutive rows, one warp.
@@ -289,7 +352,7 @@ struct AppendArgs {
 // shared memory) and its table's entry: lane r has row r's, so a chunk waits
 // for them once.  The rows' groups of heads then stream through with the next
 // one in flight.
-template <typename T, int HD>
+template <typename T, int HD, bool AXES>
 __global__ void __launch_bounds__(kThreads, kAppendBlocks) kv_append_kernel(const __grid_constant__ AppendArgs<T> p) {
   constexpr int LPR = HD / 16, RPW = 32 / LPR;
   __shared__ uint64_t s_f[HD / 2];
@@ -316,6 +379,7 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) kv_append_kernel(cons
     if (bad) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
   }
   const int lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
+  const LanePlaces<HD, AXES> places(p.places, lane);
   const specfold_paged_cache& ch = p.cache;
   const int units = (p.n_kv + RPW - 1) / RPW;
   const int chunks = (bt.T - 1) / p.chunk + 1;
@@ -388,7 +452,11 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) kv_append_kernel(cons
         if (now.u == 0) {
           to = __shfl_sync(0xffffffffu, slot, now.r);
           const long long at = __shfl_sync(0xffffffffu, tok, now.r);
-          if (rope) lane_angles<T, HD>(s_f, p.positions ? p.positions[t0 + now.r] : at, lane, c, cs, sn);
+          if (rope) {
+            long long pos[HD / 64];
+            places.read(p.places, t0 + now.r, at, pos);
+            lane_angles<T, HD>(s_f, pos, lane, c, cs, sn);
+          }
         }
         const int h = now.u * RPW + sub;
         float2 a[4], b[4];
@@ -409,27 +477,25 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) kv_append_kernel(cons
   }
 }
 
-template <typename T, int HD>
+template <typename T, int HD, bool AXES>
 int append_go(const KvAppendCall& c, cudaStream_t st) {
   AppendArgs<T> a;
   a.k = rows_of<T>(c.k);
   a.v = rows_of<T>(c.v);
   a.rows = c.rows;
   a.gk = static_cast<const T*>(c.gk);
-  a.positions = c.positions;
   a.cache = c.cache;
   a.batch = c.batch;
   a.status = c.status;
   a.n_kv = c.n_kv;
   a.n_src = c.n_src;
   a.eps = c.eps;
-  a.rope = c.theta > 0.f;
-  if (a.rope) rope_turns(c.theta, HD, &a.turns);
+  a.rope = rotation(c.rope, HD, &a.turns, &a.places);
   // chunks of rows such that the grid's warps take one each, and no more than a warp's lanes
   const long long warps = static_cast<long long>(kAppendBlocks) * num_sms() * (kThreads / 32);
   a.chunk = static_cast<int>(std::min<long long>(32, (2LL * c.batch.T + warps - 1) / warps));
   const long long blocks = (2LL * ((c.batch.T - 1) / a.chunk + 1) + kThreads / 32 - 1) / (kThreads / 32);
-  launch_k(kv_append_kernel<T, HD>, dim3(static_cast<unsigned>(std::min<long long>(blocks, static_cast<long long>(kAppendBlocks) * num_sms()))),
+  launch_k(kv_append_kernel<T, HD, AXES>, dim3(static_cast<unsigned>(std::min<long long>(blocks, static_cast<long long>(kAppendBlocks) * num_sms()))),
            dim3(kThreads), 0, st, a);
   count_launch();
   return check_launch();
@@ -437,15 +503,17 @@ int append_go(const KvAppendCall& c, cudaStream_t st) {
 
 }  // namespace
 
-int launch_qk_norm_rope(const QkNormRopeCall& c, cudaStream_t st) {
-  if (c.dtype == SPECFOLD_BF16) return c.hd == 128 ? qk_go<__nv_bfloat16, 128>(c, st) : qk_go<__nv_bfloat16, 64>(c, st);
-  return c.hd == 128 ? qk_go<float, 128>(c, st) : qk_go<float, 64>(c, st);
-}
+// Element type, head size and kind of positions of a call to its instance.
+#define SF_ROPE_DISPATCH(go)                                                                        \
+  const bool axes = c.rope.axes != nullptr;                                                         \
+  if (c.dtype == SPECFOLD_BF16) {                                                                   \
+    if (c.hd == 128) return axes ? go<__nv_bfloat16, 128, true>(c, st) : go<__nv_bfloat16, 128, false>(c, st); \
+    return axes ? go<__nv_bfloat16, 64, true>(c, st) : go<__nv_bfloat16, 64, false>(c, st);         \
+  }                                                                                                 \
+  if (c.hd == 128) return axes ? go<float, 128, true>(c, st) : go<float, 128, false>(c, st);        \
+  return axes ? go<float, 64, true>(c, st) : go<float, 64, false>(c, st)
 
-int launch_kv_append(const KvAppendCall& c, cudaStream_t st) {
-  if (c.dtype == SPECFOLD_BF16)
-    return c.hd == 128 ? append_go<__nv_bfloat16, 128>(c, st) : append_go<__nv_bfloat16, 64>(c, st);
-  return c.hd == 128 ? append_go<float, 128>(c, st) : append_go<float, 64>(c, st);
-}
+int launch_qk_norm_rope(const QkNormRopeCall& c, cudaStream_t st) { SF_ROPE_DISPATCH(qk_go); }
+int launch_kv_append(const KvAppendCall& c, cudaStream_t st) { SF_ROPE_DISPATCH(append_go); }
 
 }  // namespace sf

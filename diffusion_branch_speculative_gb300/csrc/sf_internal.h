@@ -162,14 +162,20 @@ int launch_attention(const AttnCall& c, cudaStream_t st);
 int launch_attention_f32(const AttnCall& c, cudaStream_t st);  // fp32 Q/K/V/O (simt_f32.cu)
 
 // ---- a decoder's paged cache (cache_ops.cu, tree_attn.cu) ----
+// A rotation: by one position a row (axes null; theta 0: none), or by several.
+struct RopePlan {
+  const int32_t* positions;  // one a row; null: the token's own index (append)
+  float theta;
+  const specfold_rope_axes* axes = nullptr;
+  long long row_stride = 1, axis_stride = 0;
+};
 struct QkNormRopeCall {
   int dtype, T, n_q, n_kv, hd;
   specfold_head_rows q_in, k_in, q_out, k_out;
   const void* gq;  // gains, null: not normed
   const void* gk;
   float eps;
-  const int32_t* positions;
-  float theta;  // 0: not rotated
+  RopePlan rope;
 };
 int launch_qk_norm_rope(const QkNormRopeCall& c, cudaStream_t st);
 
@@ -188,8 +194,7 @@ struct KvAppendCall {
   const int32_t* rows;  // null: row t takes k and v row t
   const void* gk;
   float eps;
-  const int32_t* positions;  // null: the token's own index
-  float theta;
+  RopePlan rope;
   specfold_paged_cache cache;
   SeqBatch batch;
   uint32_t* status;  // may be null
@@ -207,6 +212,43 @@ struct TreeAttnCall {
 };
 size_t tree_attn_ws_bytes(int dtype, int n_q, int n_kv, int hd, int max_nodes);
 int launch_tree_attention(const TreeAttnCall& c, cudaStream_t st);
+
+// ---- what thins out a paged cache (kv_weigh.cu, kv_evict.cu) ----
+struct KvWeighCall {
+  int dtype, n_q, n_kv, hd, max_rows;
+  specfold_head_rows q;
+  int n_src;
+  const int32_t* rows;  // null: row t takes q's row t
+  specfold_paged_cache cache;
+  SeqBatch batch;
+  float scale, decay;
+  specfold_token_weights w;
+  void* ws;  // kv_weigh_ws_bytes
+};
+size_t kv_weigh_ws_bytes(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int n_seqs, int tokens);
+int launch_kv_weigh(const KvWeighCall& c, cudaStream_t st);
+
+struct KvSelectCall {
+  specfold_token_weights w;
+  const int32_t* lengths;
+  int n_seqs, keep, sinks, recent;
+  specfold_kept_tokens kept;
+  int32_t* new_len;
+  uint32_t* status;  // may be null
+};
+int launch_kv_select(const KvSelectCall& c, cudaStream_t st);
+
+struct KvCompactCall {
+  int dtype, n_kv, hd;
+  specfold_paged_cache cache;
+  specfold_kept_tokens kept;
+  const int32_t* lengths;
+  const int32_t* new_len;
+  int n_seqs;
+  specfold_token_weights w;  // ptr null: none
+  uint32_t* status;          // may be null
+};
+int launch_kv_compact(const KvCompactCall& c, cudaStream_t st);
 
 // ---- TMA descriptors (api.cu) ----
 // 2-D bf16 map over a row-major [rows, cols] matrix with a {64, box_rows}

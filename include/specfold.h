@@ -95,8 +95,9 @@ extern "C" {
 #define SPECFOLD_MAX_ROWS 16384     /* largest B*L */
 #define SPECFOLD_MAX_SEQS 1024      /* sequences of one batch (specfold_kv_append, specfold_tree_attention) */
 #define SPECFOLD_MAX_TREE 256       /* drafted rows of one sequence (specfold_tree_attention) */
-#define SPECFOLD_MAX_HEADS 65536    /* heads of one kind (the three calls on a decoder's cache) */
+#define SPECFOLD_MAX_HEADS 65536    /* heads of one kind (the calls on a decoder's cache) */
 #define SPECFOLD_TREE_PAD -2        /* parent of a padding row (specfold_tree_attention) */
+#define SPECFOLD_MAX_AXES 4         /* axes of a position (specfold_rope_axes) */
 
 typedef enum { SPECFOLD_BF16 = 0, SPECFOLD_F32 = 1 } specfold_dtype;
 
@@ -536,6 +537,152 @@ int specfold_tree_attention(int dtype, int T, int max_nodes, int n_q, int n_kv, 
 /* Workspace bytes of specfold_tree_attention (host only, no GPU needed).  0
  * if the shape is invalid. */
 size_t specfold_tree_attention_workspace_size(int dtype, int n_q, int n_kv, int head_dim, int max_nodes);
+
+/* ---- positions with several axes ---------------------------------- */
+/* Tokens of images and video sit at several coordinates (time, height,
+ * width) and every rotation pair turns by one of them.  Axis a has pairs[a] of
+ * the hd/2 pairs (they add up to it; none is allowed), in one of two orders:
+ *   SPECFOLD_AXES_BLOCKS   axis 0's pairs, then axis 1's, ...
+ *   SPECFOLD_AXES_IN_TURN  one pair an axis by turns, an axis that has had all
+ *                          of its own left out from then on
+ * Pair j (of axis a, its i-th) turns by position(a) * f_j,
+ *   f_j = theta^(-2j/hd), or theta^(-i/pairs[a]) with own_frequencies. */
+#define SPECFOLD_AXES_BLOCKS 0
+#define SPECFOLD_AXES_IN_TURN 1
+typedef struct {
+  float theta;                    /* > 0 */
+  int n_axes;                     /* 1 .. SPECFOLD_MAX_AXES */
+  int pairs[SPECFOLD_MAX_AXES];   /* >= 0; entries past n_axes are not read */
+  int order;                      /* SPECFOLD_AXES_BLOCKS or _IN_TURN */
+  int own_frequencies;            /* 0 or 1 */
+} specfold_rope_axes;
+
+/* Positions of rows: row t's on axis a is ptr[t*row_stride + a*axis_stride]
+ * (device int32; any strides). */
+typedef struct {
+  const int32_t* ptr;
+  int64_t row_stride;
+  int64_t axis_stride;
+} specfold_axis_positions;
+
+/* specfold_qk_norm_rope with the rotation by several axes: out[j] and
+ * out[j + hd/2] as there, a_j = position(axis of j) * f_j. */
+int specfold_qk_norm_rope_axes(int dtype, int T, int n_q, int n_kv, int head_dim, specfold_head_rows q_in,
+                               specfold_head_rows k_in, specfold_head_rows q_out, specfold_head_rows k_out,
+                               const void* gq, const void* gk, float eps, const specfold_rope_axes* axes,
+                               specfold_axis_positions positions, void* stream);
+
+/* specfold_kv_append with the keys rotated by several axes; positions has T
+ * rows, one for every row of the batch (whatever `rows` picks). */
+int specfold_kv_append_axes(int dtype, int T, int n_kv, int head_dim, specfold_head_rows k, specfold_head_rows v,
+                            int n_src, const int32_t* rows, const void* gk, float eps,
+                            const specfold_rope_axes* axes, specfold_axis_positions positions,
+                            const specfold_paged_cache* cache, const int32_t* row_start, const int32_t* ctx_len,
+                            int n_seqs, uint32_t* status, void* stream);
+
+/* ---- thinning out a paged cache ----------------------------------- */
+/* A cache that is to hold the tokens that matter: specfold_kv_weigh adds up
+ * the attention that every cached token gets, head by head,
+ * specfold_kv_select chooses the tokens that stay, specfold_kv_compact moves
+ * them to the front of their sequence's pages.  The cache's length is then
+ * new_len; keys keep the rotation of the positions they were appended at, so
+ * rows appended from then on are given their positions (a token's index is no
+ * longer its position). */
+
+/* A weight for every token: sequence s, head (or set) h, token t at
+ * ptr[s*seq_stride + h*head_stride + t], t < tokens (device float).  Where a
+ * call writes them, and the tokens kept, rows lie within the larger stride's
+ * steps: the smaller stride is no less than a row, the larger no less than all
+ * the rows of the smaller (SPECFOLD_EINVAL); a stride that no step uses does
+ * not count. */
+typedef struct {
+  float* ptr;
+  int64_t seq_stride;
+  int64_t head_stride;
+  int32_t tokens;
+} specfold_token_weights;
+
+/* The tokens kept, ascending: sequence s, set u, the i-th at
+ * ptr[s*seq_stride + u*set_stride + i], i < cap (device int32).  A set is a
+ * key/value head, or all of them together (n_sets 1). */
+typedef struct {
+  int32_t* ptr;
+  int64_t seq_stride;
+  int64_t set_stride;
+  int32_t n_sets;
+  int32_t cap;
+} specfold_kept_tokens;
+
+/* Attention weights of a batch's rows, added up per token and key/value head.
+ * The batch is specfold_kv_append's, its rows' keys already appended: row i of
+ * sequence s sees the cache's tokens 0 .. ctx_len[s] + i.  With p[i, h, t] the
+ * softmax over them of q[i, h] . k[t, h / g] * scale, g = n_q / n_kv (scale 0:
+ * 1/sqrt(head_dim)), and the sums over the sequence's rows and the group's
+ * heads:
+ *   t < ctx_len[s]:        w[s, u, t] = decay * w[s, u, t] + sum p[i, h, t]
+ *   the batch's own rows:  w[s, u, t] = sum p[i, h, t]
+ * A decay of 0 does not read the old weights.  Nothing else of w is written;
+ * a sequence without rows keeps its weights as they are.
+ *   q      view of n_src rows of n_q heads, n_src >= 1
+ *   rows   device int32 [T] or NULL: the row of q that row t of the batch takes
+ *          (the accepted rows of a step, as committed by specfold_kv_append).
+ *          NULL: row t itself, n_src >= T
+ *   max_rows  1 .. SPECFOLD_MAX_TREE, no less than any sequence's rows
+ * Rows of one sequence only are a chain: a tree's rows are weighed once they
+ * are accepted.  Tokens that a row does not see change nothing, whatever their
+ * pages hold.  A `rows` entry outside [0, n_src) weighs nothing
+ * (SPECFOLD_DEV_BAD_SEQ); a sequence whose row_start, ctx_len or row count is
+ * invalid or that has more than w.tokens tokens keeps its weights (the same
+ * bit); a page outside the pool or a token past the table reads as a key of
+ * zeros (SPECFOLD_DEV_BAD_PAGE).
+ * Products of bf16 values are summed in 32 bits, softmax and weights are 32
+ * bits; results do not depend on timing.
+ * head_dim 64 or 128; n_q / n_kv at most 128.  ws: as
+ * specfold_tree_attention's, of specfold_kv_weigh_workspace_size bytes for
+ * the same T (or a larger one), max_rows, n_seqs and w.tokens. */
+int specfold_kv_weigh(int dtype, int T, int max_rows, int n_q, int n_kv, int head_dim, specfold_head_rows q, int n_src,
+                      const int32_t* rows, const specfold_paged_cache* cache, const int32_t* row_start,
+                      const int32_t* ctx_len, int n_seqs, float scale, float decay, specfold_token_weights w, void* ws,
+                      size_t ws_bytes, void* stream);
+
+/* Workspace bytes of specfold_kv_weigh (host only, no GPU needed).  0 if the
+ * shape is invalid. */
+size_t specfold_kv_weigh_workspace_size(int dtype, int T, int max_rows, int n_q, int n_kv, int head_dim, int n_seqs,
+                                        int tokens);
+
+/* The tokens that stay, for every sequence s and set u of lengths[s] tokens: all
+ * where there are no more than `keep`, else the first `sinks`, the last
+ * `recent`, and of those between the keep - sinks - recent of largest weight,
+ * of equal ones the first.  A NaN is the smallest weight; zeros of either sign
+ * are equal.
+ *   w.ptr heads: kept.n_sets;  lengths  device int32 [n_seqs]
+ *   kept        min(lengths[s], keep) entries are written, ascending
+ *   new_len     device int32 [n_seqs] (not lengths): min(lengths[s], keep)
+ *   status      device uint32 or NULL
+ * A length that is negative or above w.tokens gives new_len -1, no tokens and
+ * SPECFOLD_DEV_BAD_SEQ.  keep >= 1, sinks, recent >= 0, sinks + recent <= keep
+ * <= kept.cap; n_seqs <= SPECFOLD_MAX_SEQS, kept.n_sets <= SPECFOLD_MAX_HEADS
+ * (SPECFOLD_ECAPACITY). */
+int specfold_kv_select(specfold_token_weights w, const int32_t* lengths, int n_seqs, int keep, int sinks, int recent,
+                       specfold_kept_tokens kept, int32_t* new_len, uint32_t* status, void* stream);
+
+/* Closes a cache's gaps in place: for every sequence s and key/value head h,
+ * token i becomes token kept[s, u, i], i < new_len[s] (u = h, or 0 with one set),
+ * keys and values bit for bit, and where w is given the weights of every set
+ * alike (w has kept.n_sets heads).  What lies behind new_len stays as it was.
+ * A sequence with new_len[s] == lengths[s] is left alone and its list is not read.
+ * The list must ascend strictly within [0, lengths[s]): a wrong entry ends that
+ * head's move there (SPECFOLD_DEV_BAD_SEQ).  new_len[s] outside 0 ..
+ * lengths[s] or above kept.cap, or lengths[s] above w.tokens, leaves the
+ * sequence as it is (the same bit).  A token whose page, or whose
+ * destination's, is outside the pool or past the table is not moved
+ * (SPECFOLD_DEV_BAD_PAGE).
+ * Pages that a moved token leaves or enters belong to one sequence: where two
+ * share them, what they hold afterwards is unspecified.
+ * kept.n_sets is n_kv or 1; head_dim 64 or 128. */
+int specfold_kv_compact(int dtype, int n_kv, int head_dim, const specfold_paged_cache* cache,
+                        specfold_kept_tokens kept, const int32_t* lengths, const int32_t* new_len, int n_seqs,
+                        const specfold_token_weights* w, uint32_t* status, void* stream);
 
 /* Enqueue one replay on `stream`. */
 int specfold_graph_launch(specfold_graph graph, void* stream);
