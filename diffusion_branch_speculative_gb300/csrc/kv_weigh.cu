@@ -1,9 +1,9 @@
 // The attention weight that cached tokens get from a batch of rows, added up per
 // key/value head (specfold_kv_weigh): what an eviction goes by.  Keys alone are
-// read.  Two passes over the scores: every row's maximum and sum, then each
-// token's weights over the rows.
-#include "sf_device.cuh"
-#include "sf_internal.h"
+// read.  kv_weigh.cuh has the two launches' division of work; here are the forms
+// whose first launch keeps the scores (few rows a head group) and the fp32 form
+// that does not.  kv_weigh_tc.cu has many rows.
+#include "kv_weigh.cuh"
 
 #include <algorithm>
 #include <cmath>
@@ -11,173 +11,585 @@
 namespace sf {
 namespace {
 
-struct WeighArgs {
-  const void* q;
-  long long q_rs, q_hs;
-  const int32_t* rows;
-  int n_src;
-  specfold_paged_cache cache;
-  SeqBatch batch;
-  int max_rows, n_kv, g;
-  float sl2, decay;  // scale * log2(e)
-  specfold_token_weights w;
-  uint32_t* status;
-  float2* stats;  // [T][n_kv * g]: a row's maximum in log2 units, and one over its sum
+constexpr int kThreads = 128;  // 4 warps, each with its own chunks of keys
+constexpr int kWarps = kThreads / 32;
+constexpr int kKeys = 64;        // keys of a block of the line
+constexpr int kSmBudget = 160;   // SMs the workspace is sized for (>= one GB300)
+
+// The warps' (m, l) of R rows, warp k's at s_ml[k * R], to their place.
+template <int R>
+SF_DEV void weigh_write_part(const WeighArgs& p, const TreeWalk& w, bool first, const float2* s_ml) {
+  const int r = threadIdx.x;
+  if (r >= R) return;
+  float2 a = s_ml[r];
+#pragma unroll
+  for (int k = 1; k < kWarps; ++k) a = weigh_merge(a, s_ml[k * R + r]);
+  weigh_leave(p, w, first, r, a);
+}
+
+// ------------------------------------------------------ few rows, bf16 --
+// Up to 8 NT rows of a head group, so at most 4 NT operations a byte of the
+// keys: the memory bounds it.  Each of the four warps streams its own 4 KB
+// chunks of keys through a private ring of asynchronous copies.  Keys are the
+// 16 rows of the warps' matrix instructions and the queries their 8 columns, so
+// that one token with a group of seven heads wastes one column in eight; the
+// scores go to the workspace, 32 bytes a token and eight rows, where the second
+// launch finds them in L2 rather than the keys in DRAM.
+template <int HD, int NT>
+struct WFew {
+  static constexpr int R = 8 * NT;
+  static constexpr int CH = 2048 / HD;  // keys of a warp's step: 4 KB
+  static constexpr int STAGES = 6;
+  static constexpr int ROW = HD * 2;
+  static constexpr int CPR = ROW / 16;
+  static constexpr int STAGE = CH * ROW;
+  static constexpr int RING = STAGES * STAGE;
+  static constexpr int OFF_Q = kWarps * RING;
+  static constexpr int SMEM = OFF_Q + R * ROW;
+  static constexpr int CTAS = 2;  // per SM
 };
 
-// One sequence of the batch: n rows behind ctx tokens; n 0 where it is invalid.
-struct WeighSeq {
-  int row0, n, ctx;
-};
-SF_DEV WeighSeq weigh_seq(const WeighArgs& p, int s, bool report) {
-  WeighSeq q;
-  q.row0 = p.batch.row_start[s];
-  const int end = p.batch.row_start[s + 1];
-  q.ctx = p.batch.ctx_len[s];
-  const bool bad = q.row0 < 0 || end < q.row0 || end > p.batch.T || end - q.row0 > p.max_rows || q.ctx < 0 ||
-                   static_cast<long long>(q.ctx) + (end - q.row0) > p.w.tokens;
-  if (bad && report) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
-  q.n = bad ? 0 : end - q.row0;
-  return q;
-}
-SF_DEV int weigh_slot(const WeighArgs& p, int s, int tok) {
-  const specfold_paged_cache& c = p.cache;
-  const unsigned pg = static_cast<unsigned>(tok) / static_cast<unsigned>(c.page_size);
-  if (pg < static_cast<unsigned>(c.table_pages)) {
-    const int page = c.block_table[s * c.table_stride + pg];
-    if (page >= 0 && page < c.num_pages) return page * c.page_size + (tok - static_cast<int>(pg) * c.page_size);
+template <int HD, int NT>
+__global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel(const __grid_constant__ WeighArgs a) {
+  using C = WFew<HD, NT>;
+  using T = __nv_bfloat16;
+  constexpr int R = C::R, KS = HD / 16, CH = C::CH, KH = CH / 16;
+  const TreeArgs& p = a.t;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 s_ml[kWarps * R];
+  pdl_wait();
+  pdl_trigger();
+  TreeWalk w;
+  unsigned per;
+  if (!tree_locate(p, w, per)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* ring = smem + warp * C::RING;
+  uint8_t* s_q = smem + C::OFF_Q;
+
+  for (bool first = true; w.n > 0; first = false, w.next(p)) {
+    const int h = w.head, rows = w.q.n * p.g;
+    const int len = w.q.ctx + w.q.n, key_lo = w.b0 * p.kb;
+    const int key_hi = min(static_cast<long long>(len), static_cast<long long>(w.b0 + w.n) * p.kb);
+    if (threadIdx.x == 0 && w.b0 == 0) weigh_note_span(a, w, first, per);
+    __syncthreads();  // the previous piece's shared memory is free
+
+    // this warp's chunks: key_lo + CH * (warp + 4 i)
+    const int chunks = (key_hi - key_lo + CH - 1) / CH;
+    const int mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
+    auto key_of = [&](int i) { return key_lo + CH * (warp + kWarps * i); };
+    auto slot_of = [&](int i) {  // lanes 0..CH-1: pool tokens of chunk i's keys
+      const int tok = key_of(i) + (lane & (CH - 1));
+      return i < mine && tok < key_hi ? tree_pool_token(p, w.s, tok) : -1;
+    };
+    const T* kbase = static_cast<const T*>(p.cache.k) + h * p.cache.k_head_stride;
+    auto load = [&](int i, int slot) {
+      if (i < mine) {
+        const uint32_t st = smem_u32(ring + (i % C::STAGES) * C::STAGE);
+        constexpr int KEYS = 32 / C::CPR;  // keys of one step of the warp's lanes
+        const int c = lane % C::CPR;
+#pragma unroll
+        for (int it = 0; it < CH / KEYS; ++it) {
+          const int key = it * KEYS + lane / C::CPR;
+          const int tk = __shfl_sync(0xffffffffu, slot, key);
+          const long long tz = tk < 0 ? 0 : tk;  // any valid address when nothing is read
+          cp_async16(st + key * C::ROW + ((c ^ (key & 7)) << 4), kbase + tz * p.cache.k_token_stride + c * 8,
+                     tk < 0 ? 0u : 16u);
+        }
+      }
+      cp_async_commit();
+    };
+    int slot = slot_of(0);
+#pragma unroll
+    for (int i = 0; i < C::STAGES - 1; ++i) {
+      load(i, slot);
+      slot = slot_of(i + 1);
+    }
+    // queries: row m = row m / g of the sequence, head m % g of the group; the rows
+    // past the last are its copies (zeros times an infinite key would be NaN)
+    for (int i = threadIdx.x; i < R * C::CPR; i += kThreads) {
+      const int r = i / C::CPR, c = i % C::CPR, m = min(r, rows - 1);
+      const int src = max(weigh_src(a, w.q.row0 + m / p.g), 0);
+      *reinterpret_cast<uint4*>(s_q + r * C::ROW + ((c ^ (r & 7)) << 4)) =
+          *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + src * p.q_rs + (h * p.g + m % p.g) * p.q_hs + c * 8);
+    }
+    __syncthreads();
+    uint32_t qf[NT][KS][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int ks = 0; ks < KS; ks += 2) {
+        uint32_t b[4];
+        const int r = nt * 8 + (lane & 7);
+        ldsm4(smem_u32(s_q + r * C::ROW + (((ks * 2 + (lane >> 3)) ^ (r & 7)) << 4)), b);
+        qf[nt][ks][0] = b[0], qf[nt][ks][1] = b[1], qf[nt][ks + 1][0] = b[2], qf[nt][ks + 1][1] = b[3];
+      }
+    // this thread's rows: 8 nt + 2 (lane % 4) and the next one; the last token each sees
+    int seen[NT][2];
+    float m[NT][2], l[NT][2];
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        seen[nt][e] = w.q.ctx + min(nt * 8 + (lane & 3) * 2 + e, rows - 1) / p.g;
+        m[nt][e] = -INFINITY;
+        l[nt][e] = 0.f;
+      }
+    float* out = a.scores + ((static_cast<size_t>(w.s) * p.n_kv + h) * a.w.tokens) * R + (lane & 3) * 2;
+    for (int i = 0; i < mine; ++i) {
+      load(i + C::STAGES - 1, slot);
+      slot = slot_of(i + C::STAGES);
+      cp_async_wait<C::STAGES - 1>();
+      __syncwarp();
+      const uint8_t* stg = ring + (i % C::STAGES) * C::STAGE;
+      const bool tail = key_of(i) + CH > w.q.ctx;  // holds tokens that not every row sees
+#pragma unroll
+      for (int kh = 0; kh < KH; ++kh) {
+        float s[NT][4] = {};
+        const int key = kh * 16 + (lane & 15);
+        const uint32_t base = smem_u32(stg + key * C::ROW);
+#pragma unroll
+        for (int ks = 0; ks < KS; ++ks) {
+          uint32_t k[4];
+          ldsm4(base + (((ks * 2 + (lane >> 4)) ^ (key & 7)) << 4), k);
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], k, qf[nt][ks][0], qf[nt][ks][1]);
+        }
+        const int t0 = key_of(i) + kh * 16 + (lane >> 2);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+          for (int x = 0; x < 4; ++x) {
+            s[nt][x] *= p.sl2;
+            if (tail && t0 + (x >> 1) * 8 > seen[nt][x & 1]) s[nt][x] = -INFINITY;
+          }
+#pragma unroll
+          for (int half = 0; half < 2; ++half)
+            if (!tail || t0 + half * 8 < len)
+              *reinterpret_cast<float2*>(out + static_cast<size_t>(t0 + half * 8) * R + nt * 8) =
+                  make_float2(s[nt][2 * half], s[nt][2 * half + 1]);
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            const float top = fmaxf(m[nt][e], fmaxf(s[nt][e], s[nt][2 + e]));
+            const float b = top == -INFINITY ? 0.f : top;
+            l[nt][e] = fmaf(l[nt][e], m[nt][e] == top ? 1.f : ex2(m[nt][e] - b), ex2(s[nt][e] - b) + ex2(s[nt][2 + e] - b));
+            m[nt][e] = top;
+          }
+        }
+      }
+      __syncwarp();  // the stage may be overwritten
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        float2 v = make_float2(m[nt][e], l[nt][e]);
+#pragma unroll
+        for (int o = 4; o < 32; o <<= 1)
+          v = weigh_merge(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+        if (lane < 4) s_ml[warp * R + nt * 8 + lane * 2 + e] = v;
+      }
+    __syncthreads();
+    weigh_write_part<R>(a, w, first, s_ml);
   }
-  atomicOr(p.status, SPECFOLD_DEV_BAD_PAGE);
-  return -1;
-}
-// The row of q that row t of the batch takes, or -1 (reported).
-SF_DEV int weigh_row(const WeighArgs& p, int t) {
-  const int r = p.rows ? p.rows[t] : t;
-  if (r >= 0 && r < p.n_src) return r;
-  atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
-  return -1;
 }
 
-constexpr int kThreads = 128;
+// ------------------------------------------------------------ fp32: few --
+// The same for fp32 by multiply-adds, a tile of eight rows at a time: a warp's
+// step is 4 KB of keys, a lane (key, 32 of the dimensions), the queries
+// broadcast from shared memory, a key's lanes joined by shuffles.
+template <int HD>
+struct WSimt {
+  static constexpr int R = 8;
+  static constexpr int CH = 1024 / HD;
+  static constexpr int STAGES = 4;
+  static constexpr int ROW = HD * 4;
+  static constexpr int CPR = ROW / 16;
+  static constexpr int STAGE = CH * ROW;
+  static constexpr int RING = STAGES * STAGE;
+  static constexpr int OFF_Q = kWarps * RING;
+  static constexpr int SMEM = OFF_Q + R * ROW;
+  static constexpr int CTAS = 3;
+};
 
-template <typename T, int HD>
-SF_DEV float dot_row(const T* k, const float* q) {
+template <int HD>
+__global__ void __launch_bounds__(kThreads, WSimt<HD>::CTAS) weigh_simt_kernel(const __grid_constant__ WeighArgs a) {
+  using C = WSimt<HD>;
+  constexpr int R = C::R, CH = C::CH;
+  const TreeArgs& p = a.t;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 s_ml[kWarps * R];
+  pdl_wait();
+  pdl_trigger();
+  TreeWalk w;
+  unsigned per;
+  if (!tree_locate(p, w, per)) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  uint8_t* ring = smem + warp * C::RING;
+  float* s_q = reinterpret_cast<float*>(smem + C::OFF_Q);
+
+  for (bool first = true; w.n > 0; first = false, w.next(p)) {
+    const int h = w.head, m0 = tree_m0(p, w), rows = tree_tile_rows(p, w);
+    const int len = w.q.ctx + w.q.n, key_lo = w.b0 * p.kb;
+    const int key_hi = min(static_cast<long long>(len), static_cast<long long>(w.b0 + w.n) * p.kb);
+    if (threadIdx.x == 0 && w.b0 == 0) weigh_note_span(a, w, first, per);
+    __syncthreads();
+    const int chunks = (key_hi - key_lo + CH - 1) / CH;
+    const int mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
+    auto key_of = [&](int i) { return key_lo + CH * (warp + kWarps * i); };
+    auto slot_of = [&](int i) {
+      const int tok = key_of(i) + (lane & (CH - 1));
+      return i < mine && tok < key_hi ? tree_pool_token(p, w.s, tok) : -1;
+    };
+    const float* kbase = static_cast<const float*>(p.cache.k) + h * p.cache.k_head_stride;
+    auto load = [&](int i, int slot) {
+      if (i < mine) {
+        uint8_t* st = ring + (i % C::STAGES) * C::STAGE;
+#pragma unroll
+        for (int it = 0; it < CH * C::CPR / 32; ++it) {
+          const int idx = it * 32 + lane, c = idx % C::CPR, key = idx / C::CPR;
+          const int tk = __shfl_sync(0xffffffffu, slot, key);
+          const long long tz = tk < 0 ? 0 : tk;
+          cp_async16(smem_u32(st + key * C::ROW + ((c ^ (key & 7)) << 4)), kbase + tz * p.cache.k_token_stride + c * 4,
+                     tk < 0 ? 0u : 16u);
+        }
+      }
+      cp_async_commit();
+    };
+    int slot = slot_of(0);
+#pragma unroll
+    for (int i = 0; i < C::STAGES - 1; ++i) {
+      load(i, slot);
+      slot = slot_of(i + 1);
+    }
+    for (int i = threadIdx.x; i < R * (HD / 4); i += kThreads) {
+      const int r = i / (HD / 4), d = (i % (HD / 4)) * 4, m = m0 + min(r, rows - 1);
+      const int src = max(weigh_src(a, w.q.row0 + m / p.g), 0);
+      *reinterpret_cast<float4*>(s_q + r * HD + d) = *reinterpret_cast<const float4*>(
+          static_cast<const float*>(p.q) + src * p.q_rs + (h * p.g + m % p.g) * p.q_hs + d);
+    }
+    int seen[R];
+    float m[R], l[R];
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      seen[r] = w.q.ctx + (m0 + min(r, rows - 1)) / p.g;
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+    __syncthreads();
+    const int key = lane & (CH - 1), part = lane / CH;
+    float* out = a.scores + ((static_cast<size_t>(w.s) * p.n_kv + h) * a.w.tokens) * a.score_rows + m0;
+    for (int i = 0; i < mine; ++i) {
+      load(i + C::STAGES - 1, slot);
+      slot = slot_of(i + C::STAGES);
+      cp_async_wait<C::STAGES - 1>();
+      __syncwarp();
+      const uint8_t* sk = ring + (i % C::STAGES) * C::STAGE + key * C::ROW;
+      float s[R] = {};
+#pragma unroll
+      for (int d = 0; d < 32; d += 4) {
+        const int b = part * 128 + d * 4;
+        const float4 k4 = *reinterpret_cast<const float4*>(sk + (((b >> 4) ^ (key & 7)) << 4));
+#pragma unroll
+        for (int r = 0; r < R; ++r) {
+          const float4 q4 = *reinterpret_cast<const float4*>(s_q + r * HD + part * 32 + d);
+          s[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[r]))));
+        }
+      }
+      const int tok = key_of(i) + key;
+      const bool tail = key_of(i) + CH > w.q.ctx;
+#pragma unroll
+      for (int r = 0; r < R; ++r) {
+#pragma unroll
+        for (int o = CH; o < 32; o <<= 1) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
+        s[r] = tail && tok > seen[r] ? -INFINITY : s[r] * p.sl2;
+        const float top = fmaxf(m[r], s[r]);
+        const float b = top == -INFINITY ? 0.f : top;
+        l[r] = fmaf(l[r], m[r] == top ? 1.f : ex2(m[r] - b), ex2(s[r] - b));
+        m[r] = top;
+      }
+      if (part < 2 && tok < len) {  // a key's eight scores by two of its lanes
+        const bool up = part == 1;
+        *reinterpret_cast<float4*>(out + static_cast<size_t>(tok) * a.score_rows + 4 * part) =
+            make_float4(up ? s[4] : s[0], up ? s[5] : s[1], up ? s[6] : s[2], up ? s[7] : s[3]);
+      }
+      __syncwarp();
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int r = 0; r < R; ++r) {
+      float2 v = make_float2(m[r], l[r]);
+#pragma unroll
+      for (int o = 1; o < CH; o <<= 1)
+        v = weigh_merge(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+      if (lane == 0) s_ml[warp * R + r] = v;
+    }
+    __syncthreads();
+    weigh_write_part<R>(a, w, first, s_ml);
+  }
+}
+
+// ------------------------------------------------- weights from the scores --
+// A thread a token: its scores' 2^(x - m) / l, eight rows at a time.
+constexpr int kSumThreads = 256;
+constexpr int kSumRows = 64;  // of a head group, at most
+
+__global__ void __launch_bounds__(kSumThreads) weigh_sum_kernel(const __grid_constant__ WeighArgs a) {
+  const TreeArgs& p = a.t;
+  __shared__ float2 s_part[kSumThreads];
+  __shared__ __align__(16) float s_m[kSumRows], s_rl[kSumRows];
+  pdl_wait();
+  pdl_trigger();
+  TreeWalk w;
+  unsigned per;
+  if (!tree_locate(p, w, per)) return;
+  const int SR = a.stat_rows, R = a.score_rows;
+  for (; w.n > 0; w.next(p)) {
+    const int h = w.head, rows = w.q.n * p.g;
+    const int len = w.q.ctx + w.q.n, key_lo = w.b0 * p.kb;
+    const int key_hi = min(static_cast<long long>(len), static_cast<long long>(w.b0 + w.n) * p.kb);
+    // the rows' statistics: thread (lane of partials, row)
+    for (int tile = 0; tile * SR < R; ++tile) {
+      const int r = threadIdx.x % SR, z0 = threadIdx.x / SR, zs = kSumThreads / SR;
+      const bool there = tile * SR + r < rows;
+      float2 v = there ? weigh_gather(a, w, tile, r, z0, zs) : make_float2(-INFINITY, 0.f);
+      __syncthreads();  // (the piece before has read m and 1 / l)
+      if (z0 < zs) s_part[z0 * SR + r] = v;
+      __syncthreads();
+      if (threadIdx.x < SR) {
+        for (int z = 1; z < zs; ++z) v = weigh_merge(v, s_part[z * SR + r]);
+        s_m[tile * SR + r] = there ? v.x : INFINITY;
+        s_rl[tile * SR + r] = there ? merge_scale(v.y) : 0.f;
+      }
+    }
+    __syncthreads();
+    const float* x = a.scores + (static_cast<size_t>(w.s) * p.n_kv + h) * a.w.tokens * R;
+    float* wt = a.w.ptr + w.s * a.w.seq_stride + h * a.w.head_stride;
+#pragma unroll 4
+    for (int t = key_lo + threadIdx.x; t < key_hi; t += kSumThreads) {
+      float sum = 0.f;
+      for (int r = 0; r < rows; r += 8) {
+        const float4 u = *reinterpret_cast<const float4*>(x + static_cast<size_t>(t) * R + r);
+        const float4 v = *reinterpret_cast<const float4*>(x + static_cast<size_t>(t) * R + r + 4);
+        sum = fmaf(ex2(u.x - s_m[r]), s_rl[r], sum);
+        sum = fmaf(ex2(u.y - s_m[r + 1]), s_rl[r + 1], sum);
+        sum = fmaf(ex2(u.z - s_m[r + 2]), s_rl[r + 2], sum);
+        sum = fmaf(ex2(u.w - s_m[r + 3]), s_rl[r + 3], sum);
+        sum = fmaf(ex2(v.x - s_m[r + 4]), s_rl[r + 4], sum);
+        sum = fmaf(ex2(v.y - s_m[r + 5]), s_rl[r + 5], sum);
+        sum = fmaf(ex2(v.z - s_m[r + 6]), s_rl[r + 6], sum);
+        sum = fmaf(ex2(v.w - s_m[r + 7]), s_rl[r + 7], sum);
+      }
+      if (t < w.q.ctx && a.decay != 0.f) sum = fmaf(a.decay, wt[t], sum);
+      wt[t] = sum;
+    }
+  }
+}
+
+// ------------------------------------------- fp32, more rows: no scores kept --
+// One block a row and query head, then one thread a token: right for any number of
+// rows, and bound by the products on the CUDA cores.
+template <int HD>
+SF_DEV float dot_row(const float* k, const float* q) {
   float a = 0.f;
 #pragma unroll 8
-  for (int d = 0; d < HD; ++d) a = fmaf(static_cast<float>(k[d]), q[d], a);
+  for (int d = 0; d < HD; d += 4) {
+    const float4 x = *reinterpret_cast<const float4*>(k + d), y = *reinterpret_cast<const float4*>(q + d);
+    a = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, a))));
+  }
   return a;
 }
 
-// One block a row and query head.
-template <typename T, int HD>
-__global__ void __launch_bounds__(kThreads) weigh_stats_kernel(const __grid_constant__ WeighArgs p) {
-  __shared__ float s_q[HD], s_m[kThreads], s_l[kThreads];
+template <int HD>
+__global__ void __launch_bounds__(kThreads) weigh_rows_kernel(const __grid_constant__ WeighArgs a) {
+  const TreeArgs& p = a.t;
+  __shared__ __align__(16) float s_q[HD];
+  __shared__ float2 s_ml[kThreads];
   pdl_wait();
   pdl_trigger();
-  const int t = blockIdx.x, hq = blockIdx.y, h = hq / p.g;
+  const int t = blockIdx.x;
   int s = 0;
   while (s < p.batch.n_seqs && !(p.batch.row_start[s] <= t && t < p.batch.row_start[s + 1])) ++s;
   if (s == p.batch.n_seqs) return;
-  const WeighSeq q = weigh_seq(p, s, false);
+  const TreeSeq q = tree_seq(p, s);
   if (q.n == 0) return;
-  float2* out = p.stats + static_cast<size_t>(t) * p.n_kv * p.g + hq;
-  const int src = weigh_row(p, t);
-  if (src < 0) {  // weighs nothing
-    if (threadIdx.x == 0) *out = make_float2(INFINITY, 0.f);
-    return;
-  }
-  for (int d = threadIdx.x; d < HD; d += kThreads)
-    s_q[d] = static_cast<float>(static_cast<const T*>(p.q)[src * p.q_rs + hq * p.q_hs + d]);
-  __syncthreads();
+  const int src = weigh_src(a, t);
   const int len = q.ctx + (t - q.row0) + 1;
+  for (int hq = blockIdx.y; hq < p.n_kv * p.g; hq += gridDim.y) {
+  const int h = hq / p.g;
+  __syncthreads();
+  for (int d = threadIdx.x; d < HD; d += kThreads)
+    s_q[d] = static_cast<const float*>(p.q)[max(src, 0) * p.q_rs + hq * p.q_hs + d];
+  __syncthreads();
   float m = -INFINITY, l = 0.f;
   for (int k = threadIdx.x; k < len; k += kThreads) {
-    const int slot = weigh_slot(p, s, k);
+    const int slot = tree_pool_token(p, s, k);
     float x = 0.f;
     if (slot >= 0)
-      x = dot_row<T, HD>(static_cast<const T*>(p.cache.k) + slot * p.cache.k_token_stride + h * p.cache.k_head_stride, s_q) *
+      x = dot_row<HD>(static_cast<const float*>(p.cache.k) + slot * p.cache.k_token_stride + h * p.cache.k_head_stride, s_q) *
           p.sl2;
-    const float top = fmaxf(m, x);
-    const float base = top == -INFINITY ? 0.f : top;
-    l = l * (m == top ? 1.f : ex2(m - base)) + ex2(x - base);
+    const float top = fmaxf(m, x), b = top == -INFINITY ? 0.f : top;
+    l = fmaf(l, m == top ? 1.f : ex2(m - b), ex2(x - b));
     m = top;
   }
-  s_m[threadIdx.x] = m;
-  s_l[threadIdx.x] = l;
+  s_ml[threadIdx.x] = make_float2(m, l);
   __syncthreads();
   if (threadIdx.x == 0) {
-    float M = -INFINITY, L = 0.f;
-    for (int i = 0; i < kThreads; ++i) M = fmaxf(M, s_m[i]);
-    for (int i = 0; i < kThreads; ++i) L += s_m[i] == M ? s_l[i] : ex2(s_m[i] - M) * s_l[i];
-    *out = make_float2(M, 1.f / L);
+    float2 v = s_ml[0];
+    for (int i = 1; i < kThreads; ++i) v = weigh_merge(v, s_ml[i]);
+    a.row_ml[static_cast<size_t>(t) * p.n_kv * p.g + hq] = src < 0 ? make_float2(INFINITY, 0.f) : make_float2(v.x, merge_scale(v.y));
+  }
   }
 }
 
-// One thread a token and key/value head.
-template <typename T, int HD>
-__global__ void __launch_bounds__(kThreads) weigh_tokens_kernel(const __grid_constant__ WeighArgs p) {
+template <int HD>
+__global__ void __launch_bounds__(kThreads) weigh_tokens_kernel(const __grid_constant__ WeighArgs a) {
+  const TreeArgs& p = a.t;
   pdl_wait();
   pdl_trigger();
-  const int s = blockIdx.y, h = blockIdx.z;
-  const WeighSeq q = weigh_seq(p, s, blockIdx.x == 0 && h == 0 && threadIdx.x == 0);
+  const int s = blockIdx.y;
+  const TreeSeq q = tree_seq(p, s);
+  if (q.bad && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
   const int len = q.n > 0 ? q.ctx + q.n : 0;
-  for (int k = blockIdx.x * kThreads + threadIdx.x; k < len; k += gridDim.x * kThreads) {
-    const int slot = weigh_slot(p, s, k);
-    const T* kp = static_cast<const T*>(p.cache.k) + max(slot, 0) * p.cache.k_token_stride + h * p.cache.k_head_stride;
-    float kv[HD], sum = 0.f;
-    for (int d = 0; d < HD; ++d) kv[d] = slot < 0 ? 0.f : static_cast<float>(kp[d]);
-    for (int i = max(0, k - q.ctx); i < q.n; ++i) {
-      const int src = weigh_row(p, q.row0 + i);
-      if (src < 0) continue;
-      for (int j = 0; j < p.g; ++j) {
-        const int hq = h * p.g + j;
-        const T* qp = static_cast<const T*>(p.q) + src * p.q_rs + hq * p.q_hs;
-        const float2 ml = p.stats[static_cast<size_t>(q.row0 + i) * p.n_kv * p.g + hq];
-        const float x = dot_row<T, HD>(qp, kv) * p.sl2;
-        sum += (x == ml.x ? 1.f : ex2(x - ml.x)) * ml.y;
+  for (int h = blockIdx.z; h < p.n_kv; h += gridDim.z)
+    for (int k = blockIdx.x * kThreads + threadIdx.x; k < len; k += gridDim.x * kThreads) {
+      const int slot = tree_pool_token(p, s, k);
+      const float* kp = static_cast<const float*>(p.cache.k) + max(slot, 0) * p.cache.k_token_stride + h * p.cache.k_head_stride;
+      float sum = 0.f;
+      for (int i = max(0, k - q.ctx); i < q.n; ++i) {
+        const int src = max(weigh_src(a, q.row0 + i), 0);
+        for (int j = 0; j < p.g; ++j) {
+          const int hq = h * p.g + j;
+          const float2 ml = a.row_ml[static_cast<size_t>(q.row0 + i) * p.n_kv * p.g + hq];
+          const float x = slot < 0 ? 0.f : dot_row<HD>(static_cast<const float*>(p.q) + src * p.q_rs + hq * p.q_hs, kp) * p.sl2;
+          sum = fmaf(ex2(x - ml.x), ml.y, sum);
+        }
       }
+      float* wt = a.w.ptr + s * a.w.seq_stride + h * a.w.head_stride + k;
+      *wt = k < q.ctx && a.decay != 0.f ? fmaf(a.decay, *wt, sum) : sum;
     }
-    float* w = p.w.ptr + s * p.w.seq_stride + h * p.w.head_stride + k;
-    *w = k < q.ctx && p.decay != 0.f ? fmaf(p.decay, *w, sum) : sum;
-  }
 }
 
-template <typename T, int HD>
-int weigh_go(const KvWeighCall& c, cudaStream_t st) {
-  WeighArgs a{};
-  a.q = c.q.ptr;
-  a.q_rs = c.q.row_stride;
-  a.q_hs = c.q.head_stride;
-  a.rows = c.rows;
-  a.n_src = c.n_src;
-  a.cache = c.cache;
-  a.batch = c.batch;
-  a.max_rows = c.max_rows;
-  a.n_kv = c.n_kv;
-  a.g = c.n_q / c.n_kv;
-  a.sl2 = static_cast<float>(1.4426950408889634 * (c.scale > 0.f ? c.scale : 1.0 / std::sqrt(static_cast<double>(HD))));
-  a.decay = c.decay;
-  a.w = c.w;
-  a.status = static_cast<uint32_t*>(c.ws);
-  a.stats = reinterpret_cast<float2*>(static_cast<uint8_t*>(c.ws) + 256);
-  launch_k(weigh_stats_kernel<T, HD>, dim3(c.batch.T, c.n_q), dim3(kThreads), 0, st, a);
-  count_launch();
-  if (const int rc = check_launch()) return rc;
-  launch_k(weigh_tokens_kernel<T, HD>, dim3(std::min((c.w.tokens - 1) / kThreads + 1, 64), c.batch.n_seqs, c.n_kv), dim3(kThreads), 0,
-           st, a);
+// --------------------------------------------------------------- launches --
+enum WeighForm { kFew, kSimt, kRows, kTc };
+struct WeighPlan {
+  WeighForm form;
+  int stat_rows, stat_tiles;  // of the first launch
+  int ctas_per_sm;
+  int score_rows;
+  size_t row_ml, part, span, scores;  // bytes
+};
+size_t up256(size_t x) { return (x + 255) / 256 * 256; }
+
+// Few rows keep their scores, as long as these take a workspace of at most 1 GB.
+WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int n_seqs, int tokens) {
+  const int rows = max_rows * (n_q / n_kv), r8 = (rows + 7) / 8 * 8;
+  WeighPlan pl{};
+  pl.score_rows = r8;
+  const size_t scores = static_cast<size_t>(n_seqs) * n_kv * tokens * r8 * sizeof(float);
+  const bool keeps = scores <= (size_t{1} << 30);
+  if (dtype == SPECFOLD_BF16) {
+    if (keeps && rows <= 32) {
+      pl.form = kFew;
+      pl.stat_rows = r8;
+      pl.ctas_per_sm = WFew<128, 1>::CTAS;
+    } else {
+      pl.form = kTc;
+      pl.stat_rows = kWeighTcRows;
+      pl.ctas_per_sm = 1;
+    }
+  } else if (keeps && rows <= kSumRows) {
+    pl.form = kSimt;
+    pl.stat_rows = 8;
+    pl.ctas_per_sm = WSimt<128>::CTAS;
+  } else {
+    pl.form = kRows;
+  }
+  pl.row_ml = up256(static_cast<size_t>(T) * n_q * sizeof(float2));
+  if (pl.form == kRows) return pl;
+  pl.stat_tiles = (rows + pl.stat_rows - 1) / pl.stat_rows;
+  pl.part = up256(2 * static_cast<size_t>(kSmBudget) * pl.ctas_per_sm * pl.stat_rows * sizeof(float2));
+  pl.span = up256(static_cast<size_t>(n_seqs) * n_kv * pl.stat_tiles * sizeof(int4));
+  pl.scores = pl.form == kTc ? 0 : up256(scores);
+  return pl;
+}
+
+int start(void (*kernel)(WeighArgs), const WeighArgs& a, int grid, int threads, int smem, cudaStream_t st) {
+  if (smem > 0)
+    if (const int rc = smem_limit_once(kernel, smem)) return rc;
+  launch_k(kernel, dim3(grid), dim3(threads), smem, st, a);
   count_launch();
   return check_launch();
 }
 
+template <int HD>
+int few_go(const WeighArgs& a, int grid, cudaStream_t st) {
+  switch (a.stat_rows / 8) {
+    case 1: return start(weigh_few_kernel<HD, 1>, a, grid, kThreads, WFew<HD, 1>::SMEM, st);
+    case 2: return start(weigh_few_kernel<HD, 2>, a, grid, kThreads, WFew<HD, 2>::SMEM, st);
+    case 3: return start(weigh_few_kernel<HD, 3>, a, grid, kThreads, WFew<HD, 3>::SMEM, st);
+    default: return start(weigh_few_kernel<HD, 4>, a, grid, kThreads, WFew<HD, 4>::SMEM, st);
+  }
+}
+
+template <int HD>
+int weigh_go(const KvWeighCall& c, cudaStream_t st) {
+  const WeighPlan pl = plan_of(c.dtype, c.batch.T, c.max_rows, c.n_q, c.n_kv, HD, c.batch.n_seqs, c.w.tokens);
+  WeighArgs a{};
+  TreeArgs& t = a.t;
+  t.q = c.q.ptr;
+  t.q_rs = c.q.row_stride;
+  t.q_hs = c.q.head_stride;
+  t.cache = c.cache;
+  t.batch = c.batch;
+  t.max_nodes = c.max_rows;
+  t.n_kv = c.n_kv;
+  t.g = c.n_q / c.n_kv;
+  t.most_tokens = c.w.tokens;
+  t.sl2 = static_cast<float>(1.4426950408889634 * (c.scale > 0.f ? c.scale : 1.0 / std::sqrt(static_cast<double>(HD))));
+  t.status = static_cast<uint32_t*>(c.ws);
+  a.rows = c.rows;
+  a.n_src = c.n_src;
+  a.decay = c.decay;
+  a.w = c.w;
+  a.stat_rows = pl.stat_rows;
+  a.stat_tiles = pl.stat_tiles;
+  uint8_t* ws = static_cast<uint8_t*>(c.ws) + 256;
+  a.row_ml = reinterpret_cast<float2*>(ws);
+  a.part = reinterpret_cast<float2*>(ws + pl.row_ml);
+  a.span = reinterpret_cast<int4*>(ws + pl.row_ml + pl.part);
+  a.scores = reinterpret_cast<float*>(ws + pl.row_ml + pl.part + pl.span);
+  a.score_rows = pl.score_rows;
+  const int grid = std::min(num_sms(), kSmBudget) * pl.ctas_per_sm;
+  t.w_full = t.w_half = 1;
+  if (pl.form == kTc) return launch_weigh_tc(a, HD, grid, st);
+  t.tile_rows = pl.stat_rows;
+  t.kb = kKeys;
+  t.unit_cost = 2;
+  if (pl.form == kRows) {
+    t.tile_rows = SPECFOLD_MAX_TREE * 128;
+    launch_k(weigh_rows_kernel<HD>, dim3(c.batch.T, std::min(c.n_q, 65535)), dim3(kThreads), 0, st, a);
+    count_launch();
+    if (const int rc = check_launch()) return rc;
+    launch_k(weigh_tokens_kernel<HD>, dim3(std::min((c.w.tokens - 1) / kThreads + 1, 64), c.batch.n_seqs, std::min(c.n_kv, 65535)),
+             dim3(kThreads), 0, st, a);
+    count_launch();
+    return check_launch();
+  }
+  if (const int rc = pl.form == kFew ? few_go<HD>(a, grid, st)
+                                     : start(weigh_simt_kernel<HD>, a, grid, kThreads, WSimt<HD>::SMEM, st))
+    return rc;
+  t.tile_rows = SPECFOLD_MAX_TREE * 128;  // all of a head group's rows
+  return start(weigh_sum_kernel, a, std::min(num_sms(), kSmBudget) * 4, kSumThreads, 0, st);
+}
+
 }  // namespace
 
-size_t kv_weigh_ws_bytes(int, int T, int, int n_q, int, int, int, int) {
-  return 256 + static_cast<size_t>(T) * n_q * sizeof(float2);
+size_t kv_weigh_ws_bytes(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int n_seqs, int tokens) {
+  const WeighPlan pl = plan_of(dtype, T, max_rows, n_q, n_kv, hd, n_seqs, tokens);
+  return 256 + pl.row_ml + pl.part + pl.span + pl.scores;
 }
 
-int launch_kv_weigh(const KvWeighCall& c, cudaStream_t st) {
-  if (c.dtype == SPECFOLD_BF16) return c.hd == 128 ? weigh_go<__nv_bfloat16, 128>(c, st) : weigh_go<__nv_bfloat16, 64>(c, st);
-  return c.hd == 128 ? weigh_go<float, 128>(c, st) : weigh_go<float, 64>(c, st);
-}
+int launch_kv_weigh(const KvWeighCall& c, cudaStream_t st) { return c.hd == 128 ? weigh_go<128>(c, st) : weigh_go<64>(c, st); }
 
 }  // namespace sf

@@ -1,0 +1,603 @@
+// Attention weights of many rows a head group, bf16, on the 5th-generation tensor
+// cores (specfold_kv_weigh; kv_weigh.cuh has the two launches' division).  The
+// scores are too many to keep, so both launches compute them, each with the
+// operand order that leaves its reduction inside a thread:
+//   statistics  S = Q K^T, a thread a query row: its maximum and sum over the keys
+//   weights     S = K Q^T, a thread a key: the sum of 2^(x - m) / l over the rows
+// A row-major tile is either operand as it lies, so both read the same K and Q
+// tiles.  Keys come by TMA through a ring, as in tree_attn_tc.cu, whose roles these
+// are (384 threads): warp 0 loads keys, warps 1 and 3 gather queries, warp 2 issues
+// the products, warps 4 to 11 reduce.  A score costs one product and one
+// exponential a launch.
+#include "kv_weigh.cuh"
+
+namespace sf {
+namespace {
+
+constexpr int kTcThreads = 384;
+constexpr int kAtom = 128 * 128;  // one 128-row x 128-byte swizzle block
+constexpr int kBlock = kWeighTcKeys;
+
+struct WTcArgs {
+  CUtensorMap mapK;  // {dim, heads, pool tokens}, box {64, 1, box}
+  WeighArgs a;
+  int box;
+};
+
+template <int HD>
+struct WTc {
+  static constexpr int NATOM = HD / 64;
+  static constexpr int Q_ATOM = 2 * kAtom;      // 64 dimensions of 256 query rows
+  static constexpr int TILE = kAtom * NATOM;    // 128 keys
+  static constexpr int RING = HD == 128 ? 4 : 8;
+  static constexpr int OFF_RING = Q_ATOM * NATOM;
+  static constexpr int SMEM = OFF_RING + RING * TILE + 1024;  // and the base's alignment
+};
+
+// Keys of a run's blocks, one TMA box per run of tokens inside a page: warp 0.
+// Returns false if a wait ran out.
+template <int HD>
+struct KeyLoader {
+  using C = WTc<HD>;
+  int it = 0;
+  SF_DEV bool piece(const WTcArgs& ta, const TreeWalk& w, uint8_t* smem, uint64_t* full, uint64_t* empty,
+                    volatile int* abort_flag) {
+    const TreeArgs& p = ta.a.t;
+    const int lane = threadIdx.x & 31;
+    const int ps = p.cache.page_size, pool = p.cache.num_pages * ps, len = w.q.ctx + w.q.n;
+    const int box = lane & 15, atom = lane >> 4;  // what this thread issues of a tile
+    const bool issues = box < kBlock / ta.box && atom < C::NATOM;
+    // the table's entry is read a tile ahead of its use and looked at only then
+    const unsigned tok0 = static_cast<unsigned>(w.b0) * kBlock + box * ta.box;
+    int pg = tok0 / static_cast<unsigned>(ps), off = tok0 - pg * ps;
+    const int dpg = kBlock / ps, doff = kBlock - dpg * ps;
+    const int32_t* table = p.cache.block_table + w.s * p.cache.table_stride;
+    long long left = static_cast<long long>(len) - tok0;
+    auto entry = [&](int t) { return issues && t < w.n && left > 0 && pg < p.cache.table_pages ? table[pg] : -1; };
+    int page = entry(0);
+    for (int t = 0; t < w.n; ++t, ++it) {
+      const int st = it % C::RING;
+      const uint32_t fb = smem_u32(&full[st]);
+      bool ok = true;
+      if (lane == 0) {
+        ok = mbar_wait(smem_u32(&empty[st]), ((it / C::RING) & 1) ^ 1, abort_flag, p.status, kWaitLimitNs, kSiteAttnKvEmpty);
+        if (ok) mbar_arrive_expect_tx(fb, C::TILE);
+      }
+      if (!__shfl_sync(0xffffffffu, ok, 0)) return false;
+      if (issues) {
+        const bool there = page >= 0 && page < p.cache.num_pages;
+        if (!there && left > 0) atomicOr(p.status, SPECFOLD_DEV_BAD_PAGE);
+        // a box without a page lies wholly past the pool: it reads zeros
+        tma_load_3d(smem_u32(smem + C::OFF_RING + st * C::TILE + atom * kAtom + box * ta.box * 128), &ta.mapK, fb, atom * 64,
+                    w.head, there && left > 0 ? page * ps + off : pool);
+      }
+      left -= kBlock;
+      pg += dpg;
+      off += doff;
+      if (off >= ps) {
+        off -= ps;
+        ++pg;
+      }
+      page = entry(t + 1);
+    }
+    return true;
+  }
+  // let the copies already issued land before the CTA exits
+  SF_DEV void drain(uint64_t* full, volatile int* abort_flag) {
+    if ((threadIdx.x & 31) == 0 && *abort_flag && it > 0) {
+      int never = 0;
+      mbar_wait(smem_u32(&full[(it - 1) % C::RING]), ((it - 1) / C::RING) & 1, &never, nullptr, 10000000ull);
+    }
+    __syncwarp();
+  }
+};
+
+// A tile's queries by 64 threads (tid 0 .. 63): `most` rows from m0 on, those past
+// the last the copies of it.
+template <int HD>
+SF_DEV void gather_rows(const WeighArgs& a, const TreeWalk& w, int m0, int rows, int most, uint8_t* smem, int tid) {
+  constexpr int CPR = HD / 8, RSTEP = 64 / CPR;
+  const TreeArgs& p = a.t;
+  const int c = tid % CPR, g = p.g;
+  const uint32_t q0 = smem_u32(smem) + (c >> 3) * WTc<HD>::Q_ATOM;
+#pragma unroll 4
+  for (int r = tid / CPR; r < most; r += RSTEP) {
+    const int m = m0 + min(r, rows - 1), node = m / g, j = m - node * g;
+    const int src = max(weigh_src(a, w.q.row0 + node), 0);
+    cp_async16(q0 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
+               static_cast<const __nv_bfloat16*>(p.q) + src * p.q_rs + (w.head * g + j) * p.q_hs + c * 8, 16u);
+  }
+  cp_async_commit();
+  cp_async_wait<0>();
+  fence_proxy_async_smem();
+}
+
+// D[128 x n] = A B^T over the HD dimensions of two tiles in shared memory.
+template <int HD>
+SF_DEV void tile_product(bool me, uint32_t d, uint32_t at_a, uint32_t a_atom, uint32_t at_b, uint32_t b_atom, uint32_t idesc) {
+#pragma unroll
+  for (int kk = 0; kk < HD / 16; ++kk)
+    warp_mma(me, d, sdesc_sw128(at_a + (kk >> 2) * a_atom + (kk & 3) * 32, 16, 1024),
+             sdesc_sw128(at_b + (kk >> 2) * b_atom + (kk & 3) * 32, 16, 1024), idesc, kk > 0 ? 1u : 0u);
+}
+
+// ------------------------------------------------------------- statistics --
+// Two lanes of 128 rows as in tree_attn_tc.cu: their own rows and every block, or,
+// of a tile of at most 128 rows, the same rows and alternate blocks.  A lane has
+// two score buffers, so the products run ahead.
+template <int HD>
+__global__ void __launch_bounds__(kTcThreads, 1) weigh_stats_tc_kernel(const __grid_constant__ WTcArgs ta) {
+  using C = WTc<HD>;
+  const WeighArgs& a = ta.a;
+  const TreeArgs& p = a.t;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ __align__(8) uint64_t bars[2 * C::RING + 11];
+  __shared__ uint32_t tmem_slot_s;
+  __shared__ volatile int abort_s;
+  __shared__ float2 xch[2][128];
+  uint64_t* full = bars;
+  uint64_t* empty = bars + C::RING;    // the lanes' two arrivals
+  uint64_t* q_full = bars + 2 * C::RING;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* s_full = q_full + 2;       // [lane * 2 + buffer]
+  uint64_t* s_free = q_full + 6;       // [lane * 2 + buffer], a warp an arrival
+  uint64_t* drain = q_full + 10;
+  volatile int* abort_flag = &abort_s;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::RING; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), 2);
+    }
+    mbar_init(smem_u32(q_full), 2);   // the gathering warps
+    mbar_init(smem_u32(q_empty), 2);  // the lanes
+    for (int i = 0; i < 4; ++i) {
+      mbar_init(smem_u32(&s_full[i]), 1);
+      mbar_init(smem_u32(&s_free[i]), 4);
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&ta.mapK);
+  }
+  if (warp == 3) {
+    tmem_alloc(smem_u32(&tmem_slot_s), 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_trigger();
+  TreeWalk w;
+  unsigned per;
+  const bool work = tree_locate(p, w, per);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot_s;
+  if (!work) {
+    if (warp == 3) tmem_dealloc(tmem, 512);
+    return;
+  }
+  if (warp == 0) {
+    KeyLoader<HD> keys;
+    for (; w.n > 0 && keys.piece(ta, w, smem, full, empty, abort_flag); w.next(p)) {
+    }
+    keys.drain(full, abort_flag);
+  } else if (warp == 1 || warp == 3) {
+    for (int j = 0; w.n > 0; w.next(p), ++j) {
+      bool ok = true;
+      if (lane == 0 && j > 0)
+        ok = mbar_wait(smem_u32(q_empty), (j - 1) & 1, abort_flag, p.status, kWaitLimitNs, kSiteAttnQEmpty);
+      if (!__shfl_sync(0xffffffffu, ok, 0)) break;
+      const int rows = tree_tile_rows(p, w);
+      gather_rows<HD>(a, w, tree_m0(p, w), rows, rows > 128 ? 256 : 128, smem, (warp >> 1) * 32 + lane);
+      __syncwarp();
+      if (lane == 0) mbar_arrive(smem_u32(q_full));
+    }
+  } else if (warp == 2) {
+    constexpr uint32_t idS = idesc_bf16_f32(128, 128, false);
+    const bool me = lane == 0;
+    auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int parity, int site) {
+      ok = __all_sync(0xffffffffu,
+                      ok && mbar_wait(smem_u32(bar), parity & 1, abort_flag, p.status, kWaitLimitNs, site));
+      return ok;
+    };
+    const uint32_t base = uniform(smem_u32(smem)), tm = uniform(tmem);
+    int it = 0, cnt0 = 0, cnt1 = 0;
+    for (int j = 0; uniform(w.n > 0) && ok; w.next(p), ++j) {
+      const int nt = uniform(w.n);
+      const bool pair = uniform(tree_tile_rows(p, w) > 128);
+      if (!wait(q_full, j, kSiteAttnQFull)) break;
+      for (int t = 0; t < nt && ok; ++t, ++it) {
+        if (!wait(&full[it % C::RING], it / C::RING, kSiteAttnKvFull)) break;
+        for (int x = pair ? 0 : t & 1; x < (pair ? 2 : (t & 1) + 1); ++x) {
+          int& cnt = x ? cnt1 : cnt0;
+          const int buf = x * 2 + (cnt & 1);
+          if (cnt >= 2 && !wait(&s_free[buf], (cnt >> 1) - 1, kSiteAttnSFree)) break;
+          tc_fence_after();
+          tile_product<HD>(me, tm + buf * 128, base + (pair && x ? kAtom : 0), C::Q_ATOM,
+                           base + C::OFF_RING + (it % C::RING) * C::TILE, kAtom, idS);
+          warp_commit(me, smem_u32(&s_full[buf]));
+          ++cnt;
+        }
+      }
+    }
+    warp_commit(me, smem_u32(drain));
+    int never = 0;
+    mbar_wait(smem_u32(drain), 0, &never, nullptr, 10000000ull);
+    __syncwarp();
+  } else {
+    const int x = (warp - 4) >> 2, row = (warp & 3) * 32 + lane;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const int pair_bar = 2 + (warp & 3);
+    const bool leader = (warp & 3) == 0 && lane == 0;
+    int cnt = 0, it = 0, j = 0;
+    bool ok = true;
+    for (bool first = true; w.n > 0 && ok; first = false, w.next(p), ++j) {
+      if (warp == 4 && lane == 0 && w.b0 == 0) weigh_note_span(a, w, first, per);
+      const int nt = w.n, rows = tree_tile_rows(p, w), ctx = w.q.ctx;
+      const bool pair = rows > 128;
+      const int r = pair ? x * 128 + row : row, m = tree_m0(p, w) + min(r, rows - 1);
+      const int seen = ctx + m / p.g;  // the last token that the row sees
+      const int t_step = pair ? 1 : 2;
+      float top = -INFINITY, l = 0.f;
+      if (leader && !pair && x >= nt) mbar_arrive(smem_u32(q_empty));  // no block of this unit
+      for (int t = pair ? 0 : x; t < nt; t += t_step, ++cnt) {
+        const int buf = x * 2 + (cnt & 1);
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&s_full[buf]), (cnt >> 1) & 1, abort_flag, p.status, kWaitLimitNs,
+                                               kSiteAttnSFull))) {
+          ok = false;
+          break;
+        }
+        tc_fence_after();
+        if (leader) {  // the products are done: with the keys, and after the last one the queries
+          const uint32_t eb = smem_u32(&empty[(it + t) % C::RING]);
+          mbar_arrive(eb);
+          if (!pair) mbar_arrive(eb);
+          if (t + t_step >= nt) mbar_arrive(smem_u32(q_empty));
+        }
+        uint32_t s[4][32];
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld32(tmem + lane_off + buf * 128 + c * 32, s[c]);
+#pragma unroll
+        for (int c = 0; c < 4; ++c) tmem_ld_wait(s[c]);
+        tc_fence_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(smem_u32(&s_free[buf]));
+        const long long key0 = static_cast<long long>(w.b0 + t) * kBlock;
+        if (key0 + kBlock > ctx + 1) {
+          const int lim = static_cast<int>(seen - key0);
+#pragma unroll
+          for (int c = 0; c < 4; ++c)
+#pragma unroll
+            for (int e = 0; e < 32; ++e)
+              if (c * 32 + e > lim) s[c][e] = 0xff800000u;  // -inf
+        }
+        float mx[4] = {-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2)
+            mx[(e >> 1) & 3] = max3(mx[(e >> 1) & 3], __uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1]));
+        const float now = fmaxf(top, fmaxf(max3(mx[0], mx[1], mx[2]), mx[3]) * p.sl2);
+        const float b = now == -INFINITY ? 0.f : now;
+        l *= top == now ? 1.f : ex2(top - b);
+        top = now;
+        const float2 scale2 = make_float2(p.sl2, p.sl2), b2 = make_float2(-b, -b);
+        float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+        for (int c = 0; c < 4; ++c)
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 y = fma2(make_float2(__uint_as_float(s[c][e]), __uint_as_float(s[c][e + 1])), scale2, b2);
+            sum[(e >> 1) & 1] = add2(sum[(e >> 1) & 1], make_float2(ex2(y.x), ex2(y.y)));
+          }
+        l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+      }
+      it += nt;
+      // where the lanes share rows, lane 1 hands its own to lane 0
+      if (x == 1) xch[j & 1][row] = make_float2(top, l);
+      if (!named_bar_and(pair_bar, 64, ok)) {
+        ok = false;
+        break;
+      }
+      float2 v = make_float2(top, l);
+      if (!pair && x == 0) v = weigh_merge(v, xch[j & 1][row]);
+      if (pair || x == 0) weigh_leave(a, w, first, r, v);
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+// ---------------------------------------------------------------- weights --
+// A unit is a (sequence, head); its rows are tiles of 256.  One tile stays in
+// place while the blocks stream by; with more, a group of RING blocks stays and the
+// tiles pass, back and forth, so that a tile is gathered once for a group.  A
+// product's 128 keys are TMEM's lanes, its rows the columns of one of two buffers;
+// the two halves of the reducing warps take alternate 32 columns.
+struct WItems {  // the order of a unit's products, the same in every role
+  int n, tiles, group;
+  int g0 = 0, tile_at = 0, dir = 1, done = 0;  // group's first block, tile now, its step, tiles of the group so far
+  SF_DEV WItems(int blocks, int tiles_, int ring) : n(blocks), tiles(tiles_), group(tiles_ > 1 ? ring : blocks) {}
+  SF_DEV int blocks() const { return min(group, n - g0); }
+  SF_DEV bool last() const { return done == tiles - 1; }
+  // to the next tile or group; true: another tile's queries are needed
+  SF_DEV bool next() {
+    if (++done < tiles) {
+      tile_at += dir;
+      return true;
+    }
+    done = 0;
+    dir = -dir;
+    g0 += group;
+    return false;
+  }
+};
+
+template <int HD>
+__global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __grid_constant__ WTcArgs ta) {
+  using C = WTc<HD>;
+  const WeighArgs& a = ta.a;
+  const TreeArgs& p = a.t;
+  extern __shared__ uint8_t smem_raw[];
+  uint8_t* smem = smem_raw + ((1024u - (smem_u32(smem_raw) & 1023u)) & 1023u);
+  __shared__ __align__(8) uint64_t bars[2 * C::RING + 7];
+  __shared__ uint32_t tmem_slot_s;
+  __shared__ volatile int abort_s;
+  __shared__ __align__(16) float s_m[2][kWeighTcRows], s_rl[2][kWeighTcRows];
+  __shared__ float s_sum[C::RING][256];  // of a group's blocks over the tiles so far, a thread's own
+  __shared__ float xch[2][128];
+  uint64_t* full = bars;
+  uint64_t* empty = bars + C::RING;
+  uint64_t* q_full = bars + 2 * C::RING;
+  uint64_t* q_empty = q_full + 1;
+  uint64_t* d_full = q_full + 2;  // [buffer]
+  uint64_t* d_free = q_full + 4;  // [buffer], a warp an arrival
+  uint64_t* drain = q_full + 6;
+  volatile int* abort_flag = &abort_s;
+  const int warp = __shfl_sync(0xffffffffu, static_cast<int>(threadIdx.x >> 5), 0), lane = threadIdx.x & 31;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < C::RING; ++i) {
+      mbar_init(smem_u32(&full[i]), 1);
+      mbar_init(smem_u32(&empty[i]), 1);
+    }
+    mbar_init(smem_u32(q_full), 2);
+    mbar_init(smem_u32(q_empty), 1);
+    for (int i = 0; i < 2; ++i) {
+      mbar_init(smem_u32(&d_full[i]), 1);
+      mbar_init(smem_u32(&d_free[i]), 8);
+    }
+    mbar_init(smem_u32(drain), 1);
+    *abort_flag = 0;
+    fence_mbar_init();
+    prefetch_tmap(&ta.mapK);
+  }
+  if (warp == 3) {
+    tmem_alloc(smem_u32(&tmem_slot_s), 512);
+    tmem_relinquish();
+  }
+  pdl_wait();
+  pdl_trigger();
+  TreeWalk w;
+  unsigned per;
+  const bool work = tree_locate(p, w, per);
+  tc_fence_before();
+  __syncthreads();
+  tc_fence_after();
+  const uint32_t tmem = tmem_slot_s;
+  if (!work) {
+    if (warp == 3) tmem_dealloc(tmem, 512);
+    return;
+  }
+  auto all_rows = [&]() { return w.q.n * p.g; };
+  auto tiles_of = [&]() { return (all_rows() + kWeighTcRows - 1) / kWeighTcRows; };
+  auto rows_of = [&](int tile) { return min(kWeighTcRows, all_rows() - tile * kWeighTcRows); };
+
+  if (warp == 0) {
+    KeyLoader<HD> keys;
+    for (; w.n > 0 && keys.piece(ta, w, smem, full, empty, abort_flag); w.next(p)) {
+    }
+    keys.drain(full, abort_flag);
+  } else if (warp == 1 || warp == 3) {
+    bool ok = true;
+    int ql = 0;  // tiles gathered so far
+    for (; w.n > 0 && ok; w.next(p)) {
+      WItems q(w.n, tiles_of(), C::RING);
+      bool fresh = true;
+      while (q.g0 < q.n) {
+        if (fresh) {
+          if (lane == 0 && ql > 0)
+            ok = mbar_wait(smem_u32(q_empty), (ql - 1) & 1, abort_flag, p.status, kWaitLimitNs, kSiteAttnQEmpty);
+          ok = __shfl_sync(0xffffffffu, ok, 0);
+          if (!ok) break;
+          const int rows = rows_of(q.tile_at);
+          gather_rows<HD>(a, w, q.tile_at * kWeighTcRows, rows, (rows + 31) & ~31, smem, (warp >> 1) * 32 + lane);
+          __syncwarp();
+          if (lane == 0) mbar_arrive(smem_u32(q_full));
+          ++ql;
+        }
+        fresh = q.next();
+      }
+    }
+  } else if (warp == 2) {
+    const bool me = lane == 0;
+    auto uniform = [](int v) { return __shfl_sync(0xffffffffu, v, 0); };
+    bool ok = true;
+    auto wait = [&](uint64_t* bar, int parity, int site) {
+      ok = __all_sync(0xffffffffu,
+                      ok && mbar_wait(smem_u32(bar), parity & 1, abort_flag, p.status, kWaitLimitNs, site));
+      return ok;
+    };
+    const uint32_t base = uniform(smem_u32(smem)), tm = uniform(tmem);
+    int it = 0, cnt = 0, ql = 0;
+    for (; uniform(w.n > 0) && ok; w.next(p)) {
+      WItems q(uniform(w.n), uniform(tiles_of()), C::RING);
+      bool fresh = true;
+      while (q.g0 < q.n && ok) {
+        if (fresh) {
+          if (!wait(q_full, ql, kSiteAttnQFull)) break;
+          ++ql;
+        }
+        const int cols = uniform((rows_of(q.tile_at) + 31) & ~31);
+        const uint32_t id = idesc_bf16_f32(128, cols, false);
+        const int nb = q.blocks();
+        for (int b = 0; b < nb; ++b, ++cnt) {
+          const int i = it + q.g0 + b, buf = cnt & 1;
+          if (q.done == 0 && !wait(&full[i % C::RING], i / C::RING, kSiteAttnKvFull)) break;
+          if (cnt >= 2 && !wait(&d_free[buf], (cnt >> 1) - 1, kSiteAttnSFree)) break;
+          tc_fence_after();
+          tile_product<HD>(me, tm + buf * 256, base + C::OFF_RING + (i % C::RING) * C::TILE, kAtom, base, C::Q_ATOM, id);
+          warp_commit(me, smem_u32(&d_full[buf]));
+        }
+        fresh = q.next();
+        // another tile follows, or another unit's: the queries are done with once these products are
+        if (ok && (fresh || q.g0 >= q.n)) warp_commit(me, smem_u32(q_empty));
+      }
+      it += q.n;
+    }
+    warp_commit(me, smem_u32(drain));
+    int never = 0;
+    mbar_wait(smem_u32(drain), 0, &never, nullptr, 10000000ull);
+    __syncwarp();
+  } else {
+    const int x = (warp - 4) >> 2, key = (warp & 3) * 32 + lane, tid = threadIdx.x - 128;
+    const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
+    const bool leader = warp == 4 && lane == 0;
+    int it = 0, cnt = 0, ql = 0, outs = 0;
+    bool ok = true;
+    for (; w.n > 0 && ok; w.next(p)) {
+      const int ctx = w.q.ctx, len = ctx + w.q.n;
+      float* wt = a.w.ptr + w.s * a.w.seq_stride + w.head * a.w.head_stride;
+      WItems q(w.n, tiles_of(), C::RING);
+      bool fresh = true;
+      while (q.g0 < q.n && ok) {
+        if (fresh) {  // the tile's statistics, a thread a row
+          const bool there = tid < rows_of(q.tile_at);
+          float2 v = make_float2(0.f, 0.f);
+          if (there) v = weigh_gather(a, w, q.tile_at, tid, 0, 1);
+          s_m[ql & 1][tid] = there ? -v.x : -INFINITY;
+          s_rl[ql & 1][tid] = there ? merge_scale(v.y) : 0.f;
+          if (!named_bar_and(1, 256, ok)) {
+            ok = false;
+            break;
+          }
+          ++ql;
+        }
+        const float *tm_ = s_m[(ql - 1) & 1], *tr = s_rl[(ql - 1) & 1];
+        const int chunks = (rows_of(q.tile_at) + 31) / 32, m0 = q.tile_at * kWeighTcRows;
+        const bool single = q.tiles == 1, last = q.last();
+        const int nb = q.blocks();
+        for (int b = 0; b < nb; ++b, ++cnt) {
+          const int buf = cnt & 1;
+          const long long t0 = static_cast<long long>(w.b0 + q.g0 + b) * kBlock;
+          const bool tail = t0 + kBlock > ctx;
+          const bool mine = last && x == 0 && t0 + key < len;  // this thread writes a weight
+          const float old = mine && t0 + key < ctx && a.decay != 0.f ? wt[t0 + key] : 0.f;
+          ok = __all_sync(0xffffffffu, ok && mbar_wait(smem_u32(&d_full[buf]), (cnt >> 1) & 1, abort_flag, p.status,
+                                                       kWaitLimitNs, kSiteAttnSFull));
+          float sum = 0.f;
+          if (ok) {
+            tc_fence_after();
+            if (leader && last) mbar_arrive(smem_u32(&empty[(it + q.g0 + b) % C::RING]));
+            // the first row that sees this key
+            const int from = tail ? static_cast<int>(min(max(t0 + key - ctx, 0ll) * p.g - m0, 1ll << 20)) : 0;
+            const float2 scale2 = make_float2(p.sl2, p.sl2);
+            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll 1
+            for (int c = x; c < chunks; c += 2) {
+              uint32_t s[32];
+              tmem_ld32(tmem + lane_off + buf * 256 + c * 32, s);
+              tmem_ld_wait(s);
+#pragma unroll
+              for (int e = 0; e < 32; e += 4) {
+                const float4 m4 = *reinterpret_cast<const float4*>(tm_ + c * 32 + e);
+                const float4 r4 = *reinterpret_cast<const float4*>(tr + c * 32 + e);
+                float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, make_float2(m4.x, m4.y));
+                float2 z = fma2(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), scale2, make_float2(m4.z, m4.w));
+                if (tail) {
+                  if (c * 32 + e < from) y.x = -INFINITY;
+                  if (c * 32 + e + 1 < from) y.y = -INFINITY;
+                  if (c * 32 + e + 2 < from) z.x = -INFINITY;
+                  if (c * 32 + e + 3 < from) z.y = -INFINITY;
+                }
+                // (a row that weighs nothing has -inf and 0)
+                acc[0] = fma2(make_float2(ex2(y.x), ex2(y.y)), make_float2(r4.x, r4.y), acc[0]);
+                acc[1] = fma2(make_float2(ex2(z.x), ex2(z.y)), make_float2(r4.z, r4.w), acc[1]);
+              }
+            }
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&d_free[buf]));
+            sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+            if (!single) {
+              if (q.done > 0) sum += s_sum[b][tid];
+              s_sum[b][tid] = sum;
+            }
+          }
+          if (last) {  // the halves of the rows together
+            if (x == 1) xch[outs & 1][key] = sum;
+            if (!named_bar_and(1, 256, ok)) {
+              ok = false;
+              break;
+            }
+            if (mine) {
+              sum += xch[outs & 1][key];
+              wt[t0 + key] = fmaf(a.decay, old, sum);
+            }
+            ++outs;
+          }
+        }
+        fresh = q.next();
+      }
+      it += q.n;
+    }
+  }
+  tc_fence_before();
+  __syncthreads();
+  if (warp == 3) {
+    tc_fence_after();
+    tmem_dealloc(tmem, 512);
+  }
+}
+
+template <int HD>
+int tc_go(WeighArgs& a, int grid, cudaStream_t st) {
+  using C = WTc<HD>;
+  WTcArgs ta;
+  const specfold_paged_cache& c = a.t.cache;
+  ta.box = c.page_size % 64 == 0 ? 64 : c.page_size % 32 == 0 ? 32 : c.page_size % 16 == 0 ? 16 : 8;
+  const uint64_t tokens = static_cast<uint64_t>(c.num_pages) * c.page_size;
+  if (const int rc = make_map_3d(&ta.mapK, c.k, HD, a.t.n_kv, tokens, c.k_head_stride, c.k_token_stride, ta.box, HD * 2))
+    return rc;
+  a.t.kb = kBlock;
+  a.t.tile_rows = kWeighTcRows;
+  a.t.unit_cost = 5;
+  a.t.w_full = 5;
+  a.t.w_half = 3;
+  ta.a = a;
+  if (const int rc = smem_limit_once(weigh_stats_tc_kernel<HD>, C::SMEM)) return rc;
+  launch_k(weigh_stats_tc_kernel<HD>, dim3(grid), dim3(kTcThreads), C::SMEM, st, ta);
+  count_launch();
+  if (const int rc = check_launch()) return rc;
+  ta.a.t.tile_rows = SPECFOLD_MAX_TREE * 128;  // all of a head group's rows
+  ta.a.t.w_full = ta.a.t.w_half = 1;
+  if (const int rc = smem_limit_once(weigh_tokens_tc_kernel<HD>, C::SMEM)) return rc;
+  launch_k(weigh_tokens_tc_kernel<HD>, dim3(grid), dim3(kTcThreads), C::SMEM, st, ta);
+  count_launch();
+  return check_launch();
+}
+
+}  // namespace
+
+int launch_weigh_tc(WeighArgs& a, int hd, int grid, cudaStream_t st) {
+  return hd == 128 ? tc_go<128>(a, grid, st) : tc_go<64>(a, grid, st);
+}
+
+}  // namespace sf

@@ -328,25 +328,6 @@ struct Few {
   static constexpr bool Q_IN_REGS = MT == 1;      // two row tiles' queries would not fit beside their outputs
 };
 
-SF_DEV void ldsm4(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-SF_DEV void ldsm4t(uint32_t addr, uint32_t (&r)[4]) {
-  asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
-               : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-               : "r"(addr)
-               : "memory");
-}
-// c [16 x 8] += a [16 x 16] b [16 x 8], bf16 in, fp32 accumulate.
-SF_DEV void mma16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-  asm volatile(
-      "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, {%0, %1, %2, %3};"
-      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
-      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
-}
 SF_DEV bool bf16_not_finite(uint32_t x) {  // either half
   return (x & 0x7f80u) == 0x7f80u || (x & 0x7f800000u) == 0x7f800000u;
 }
@@ -885,6 +866,7 @@ int tree_go(const TreeAttnCall& c, const Plan& pl, cudaStream_t st) {
   a.parent = c.parent;
   a.batch = c.batch;
   a.max_nodes = c.max_nodes;
+  a.most_tokens = 0xffffffffu;
   a.n_kv = c.n_kv;
   a.g = c.n_q / c.n_kv;
   a.tile_rows = pl.tile_rows;

@@ -76,39 +76,6 @@ struct Tc {
   static constexpr uint32_t col_p(int x) { return APART ? 384 + x * 64 : x * 128 + 64; }
 };
 
-// The products and commits of a warp that runs as one, issued by the thread with
-// `me` set: with the whole warp converged the descriptors stay in uniform
-// registers (a single thread's branch moves each there first: 80 cycles a
-// product, above its 64 of execution).
-// D[tmem] (+)= A[smem] * B[smem]^T
-SF_DEV void warp_mma(bool me, uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(me))
-      : "memory");
-}
-// D[tmem] (+)= A[tmem] * B[smem]^T: A's row r in TMEM lane r, two bf16 of
-// consecutive k a column.
-SF_DEV void warp_mma_ta(bool me, uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-  asm volatile(
-      "{\n\t.reg .pred p, q;\n\t"
-      "setp.ne.b32 p, %4, 0;\n\t"
-      "setp.ne.b32 q, %5, 0;\n\t"
-      "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}\n" ::"r"(d_tmem),
-      "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate), "r"(static_cast<uint32_t>(me))
-      : "memory");
-}
-SF_DEV void warp_commit(bool me, uint32_t bar) {
-  asm volatile(
-      "{\n\t.reg .pred q;\n\t"
-      "setp.ne.b32 q, %1, 0;\n\t"
-      "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}\n" ::"r"(bar),
-      "r"(static_cast<uint32_t>(me))
-      : "memory");
-}
 // Store 16 consecutive 32-bit columns of this thread's TMEM lane.
 SF_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
   asm volatile(
@@ -117,13 +84,6 @@ SF_DEV void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
       "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
       "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
       : "memory");
-}
-
-// The maximum of three in one instruction.
-SF_DEV float max3(float a, float b, float c) {
-  float d;
-  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
-  return d;
 }
 
 // Which of the 128 tokens e0, e0 + 1, ... behind the cached ones (negative: still

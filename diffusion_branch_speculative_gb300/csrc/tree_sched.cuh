@@ -18,6 +18,7 @@
 
 #include "sf_device.cuh"
 #include "sf_internal.h"
+#include "warp_ops.cuh"
 
 namespace sf {
 
@@ -35,6 +36,7 @@ struct TreeArgs {
   const int32_t* parent;
   SeqBatch batch;
   int max_nodes, n_kv, g;
+  unsigned most_tokens;  // a sequence's tokens, its rows among them, at most
   int tile_rows;  // query rows of a tile: row m is node m / g, head m % g of the group
   int kb;         // keys per block
   int unit_cost;  // a unit's start, in blocks
@@ -73,7 +75,8 @@ SF_DEV TreeSeq tree_seq(const TreeArgs& p, int s) {
   const int end = p.batch.row_start[s + 1];
   q.ctx = p.batch.ctx_len[s];
   q.bad = q.row0 < 0 || end < q.row0 || end > p.batch.T || end - q.row0 > p.max_nodes || q.ctx < 0 ||
-          q.ctx > 0x7fffffff - 2 * SPECFOLD_MAX_TREE;
+          q.ctx > 0x7fffffff - 2 * SPECFOLD_MAX_TREE ||
+          static_cast<unsigned>(q.ctx) + static_cast<unsigned>(end - q.row0) > p.most_tokens;
   q.n = q.bad ? 0 : end - q.row0;
   q.nb = q.n > 0 ? (q.ctx + q.n - 1) / p.kb + 1 : 0;
   q.tiles = (q.n * p.g + p.tile_rows - 1) / p.tile_rows;
@@ -257,17 +260,6 @@ SF_DEV int tree_pool_token(const TreeArgs& p, int s, int tok) {
   }
   atomicOr(p.status, SPECFOLD_DEV_BAD_PAGE);
   return -1;
-}
-
-// 16-byte asynchronous copy global -> shared of `bytes` (16 or 0, the rest
-// zero-filled), and the group waits.
-SF_DEV void cp_async16(uint32_t dst, const void* src, uint32_t bytes) {
-  asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(bytes) : "memory");
-}
-SF_DEV void cp_async_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
-template <int N>
-SF_DEV void cp_async_wait() {
-  asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
 }
 
 // ---- host ----
