@@ -671,8 +671,8 @@ int specfold_kv_select(specfold_token_weights w, const int32_t* lengths, int n_s
  * keys and values bit for bit, and where w is given the weights of every set
  * alike (w has kept.n_sets heads).  What lies behind new_len stays as it was.
  * A sequence with new_len[s] == lengths[s] is left alone and its list is not read.
- * The list must ascend strictly within [0, lengths[s]): a wrong entry ends that
- * head's move there (SPECFOLD_DEV_BAD_SEQ).  new_len[s] outside 0 ..
+ * An entry lies in [i, lengths[s]), as ascending ones do; another one moves
+ * nothing (SPECFOLD_DEV_BAD_SEQ).  new_len[s] outside 0 ..
  * lengths[s] or above kept.cap, or lengths[s] above w.tokens, leaves the
  * sequence as it is (the same bit).  A token whose page, or whose
  * destination's, is outside the pool or past the table is not moved
