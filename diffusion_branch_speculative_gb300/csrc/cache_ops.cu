@@ -160,28 +160,20 @@ struct Places {
   long long rs, as;  // from row to row, from axis to axis (AXES)
   uint8_t axis[64];  // of every pair (AXES)
 };
+// Row t's for this lane's pairs; s_off (AXES): where a pair's axis begins; own: the token's index.
 template <int HD, bool AXES>
-struct LanePlaces {
-  static constexpr int PER = HD / 64;
-  long long off[PER];
-  SF_DEV explicit LanePlaces(const Places& at, int lane) {
-    if constexpr (AXES) {
+SF_DEV void read_places(const Places& at, const long long* s_off, int lane, long long t, long long own,
+                        long long (&pos)[HD / 64]) {
+  if constexpr (AXES) {
+    const int32_t* row = at.p + t * at.rs;
 #pragma unroll
-      for (int e = 0; e < PER; ++e) off[e] = at.axis[lane * PER + e] * at.as;
-    }
+    for (int e = 0; e < HD / 64; ++e) pos[e] = row[s_off[lane * (HD / 64) + e]];
+  } else {
+    const long long x = at.p ? at.p[t] : own;
+#pragma unroll
+    for (int e = 0; e < HD / 64; ++e) pos[e] = x;
   }
-  // row t's; own: the token's index
-  SF_DEV void read(const Places& at, long long t, long long own, long long (&pos)[PER]) const {
-    if constexpr (AXES) {
-#pragma unroll
-      for (int e = 0; e < PER; ++e) pos[e] = at.p[t * at.rs + off[e]];
-    } else {
-      const long long x = at.p ? at.p[t] : own;
-#pragma unroll
-      for (int e = 0; e < PER; ++e) pos[e] = x;
-    }
-  }
-};
+}
 
 // One head's row in registers (two runs of eight, from 8c and HD/2 + 8c on): the
 // norm with the gain g (null: none), then the rotation.  The whole warp takes
@@ -243,7 +235,9 @@ __global__ void __launch_bounds__(kThreads, kQkBlocks) qk_norm_rope_kernel(const
   constexpr int LPR = HD / 16, RPW = 32 / LPR;
   __shared__ uint64_t s_f[HD / 2];
   __shared__ __align__(16) float s_g[2][HD];
+  __shared__ long long s_off[AXES ? HD / 2 : 1];
   if (p.rope && threadIdx.x < HD / 2) s_f[threadIdx.x] = p.turns.f[threadIdx.x];
+  if (AXES && threadIdx.x < HD / 2) s_off[threadIdx.x] = p.places.axis[threadIdx.x] * p.places.as;
   pdl_wait();
   pdl_trigger();
   for (int i = threadIdx.x; i < HD; i += kThreads) {
@@ -252,7 +246,6 @@ __global__ void __launch_bounds__(kThreads, kQkBlocks) qk_norm_rope_kernel(const
   }
   __syncthreads();
   const int lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
-  const LanePlaces<HD, AXES> places(p.places, lane);
   // a unit is a group of heads that a warp holds at once, queries' before keys'
   const int units_q = (p.n_q + RPW - 1) / RPW, units = units_q + (p.n_kv + RPW - 1) / RPW;
   const long long items = static_cast<long long>(p.T_rows) * p.parts;
@@ -271,7 +264,7 @@ __global__ void __launch_bounds__(kThreads, kQkBlocks) qk_norm_rope_kernel(const
     float2 cs[4], sn[4];
     if (p.rope) {
       long long pos[HD / 64];
-      places.read(p.places, t, 0, pos);
+      read_places<HD, AXES>(p.places, s_off, lane, t, 0, pos);
       lane_angles<T, HD>(s_f, pos, lane, c, cs, sn);
     }
     for (int u = first; u < units; u += p.parts) {
@@ -358,7 +351,9 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) kv_append_kernel(cons
   __shared__ uint64_t s_f[HD / 2];
   __shared__ __align__(16) float s_g[HD];
   __shared__ int s_start[SPECFOLD_MAX_SEQS + 1], s_ctx[SPECFOLD_MAX_SEQS];
+  __shared__ long long s_off[AXES ? HD / 2 : 1];
   if (p.rope && threadIdx.x < HD / 2) s_f[threadIdx.x] = p.turns.f[threadIdx.x];
+  if (AXES && threadIdx.x < HD / 2) s_off[threadIdx.x] = p.places.axis[threadIdx.x] * p.places.as;
   // Dependents are not released early: it would be sound (see above), but takes appended
   // prompts 20.3 us, not 19.9, and a captured step of norm, append and attention gains nothing.
   pdl_wait();
@@ -379,7 +374,6 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) kv_append_kernel(cons
     if (bad) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
   }
   const int lane = threadIdx.x & 31, c = lane % LPR, sub = lane / LPR;
-  const LanePlaces<HD, AXES> places(p.places, lane);
   const specfold_paged_cache& ch = p.cache;
   const int units = (p.n_kv + RPW - 1) / RPW;
   const int chunks = (bt.T - 1) / p.chunk + 1;
@@ -454,7 +448,7 @@ __global__ void __launch_bounds__(kThreads, kAppendBlocks) kv_append_kernel(cons
           const long long at = __shfl_sync(0xffffffffu, tok, now.r);
           if (rope) {
             long long pos[HD / 64];
-            places.read(p.places, t0 + now.r, at, pos);
+            read_places<HD, AXES>(p.places, s_off, lane, t0 + now.r, at, pos);
             lane_angles<T, HD>(s_f, pos, lane, c, cs, sn);
           }
         }

@@ -29,19 +29,20 @@ SF_DEV uint32_t weight_key(float x) {
   return u >> 31 ? ~u : u | 0x80000000u;
 }
 
-constexpr int kSelThreads = 1024, kSelWarps = kSelThreads / 32;
+constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;           // of a pass over 11, 11 and 10 bits of the keys
 constexpr int kSelCap = 48 * 1024;       // keys of a block's slice that shared memory holds
 constexpr int kSelMaxCluster = 8;
+constexpr int kSelSlice = 4096;          // tokens that are worth a block more
 
 SF_DEV int ld_dsmem_s32(uint32_t addr) {
   int v;
   asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
   return v;
 }
-SF_DEV int2 ld_dsmem_s32x2(uint32_t addr) {
-  int2 v;
-  asm volatile("ld.shared::cluster.v2.s32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(addr));
+SF_DEV int4 ld_dsmem_s32x4(uint32_t addr) {
+  int4 v;
+  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
   return v;
 }
 
@@ -52,7 +53,7 @@ SF_DEV int2 ld_dsmem_s32x2(uint32_t addr) {
 template <bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_constant__ SelectArgs p) {
   extern __shared__ uint32_t s_key[];
-  __shared__ __align__(8) int s_hist[3][kSelBins];  // a pass each: read by the cluster while the next is filled
+  __shared__ __align__(16) int s_hist[3][kSelBins];  // a pass each: read by the cluster while the next is filled
   __shared__ int s_warp[2][kSelWarps], s_found[3], s_total[2];
   pdl_wait();
   pdl_trigger();
@@ -94,7 +95,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   for (int i = threadIdx.x; i < 3 * kSelBins; i += kSelThreads) (&s_hist[0][0])[i] = 0;
   __syncthreads();
   // the keys, and the first pass
-#pragma unroll 4
+#pragma unroll 8
   for (int i = threadIdx.x; i < n; i += kSelThreads) {
     const uint32_t k = weight_key(w[i]);
     if (held) s_key[i] = k;
@@ -106,20 +107,25 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
 #pragma unroll 1
   for (int pass = 0;; ++pass) {
     all_sync();
-    // bins from the largest down, two a thread: the one with the rest-th key
-    const int bin = kSelBins - 2 - 2 * static_cast<int>(threadIdx.x);
-    int2 h = make_int2(0, 0);
+    // bins from the largest down, four a thread: the one with the rest-th key
+    static_assert(kSelBins == 4 * kSelThreads, "four bins a thread");
+    const int bin = kSelBins - 4 - 4 * static_cast<int>(threadIdx.x);
+    int4 h;
     if constexpr (CLUSTER) {
       const uint32_t at = smem_u32(&s_hist[pass][bin]);
-      for (int k = 0; k < blocks; ++k) {
-        const int2 x = ld_dsmem_s32x2(dsmem_addr(at, k));
-        h.x += x.x;
-        h.y += x.y;
+      h = make_int4(0, 0, 0, 0);
+#pragma unroll
+      for (int k0 = 0; k0 < kSelMaxCluster; k0 += 4) {
+        int4 x[4];  // four asked for before any is added
+#pragma unroll
+        for (int k = 0; k < 4; ++k) x[k] = k0 + k < blocks ? ld_dsmem_s32x4(dsmem_addr(at, k0 + k)) : make_int4(0, 0, 0, 0);
+#pragma unroll
+        for (int k = 0; k < 4; ++k) h = make_int4(h.x + x[k].x, h.y + x[k].y, h.z + x[k].z, h.w + x[k].w);
       }
     } else {
-      h = *reinterpret_cast<const int2*>(&s_hist[pass][bin]);
+      h = *reinterpret_cast<const int4*>(&s_hist[pass][bin]);
     }
-    int upto = h.x + h.y;
+    int upto = (h.x + h.y) + (h.z + h.w);
 #pragma unroll
     for (int o = 1; o < 32; o <<= 1) {
       const int u = __shfl_up_sync(0xffffffffu, upto, o);
@@ -130,12 +136,18 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     int before = lane < warp ? s_warp[0][lane] : 0;
     before = __reduce_add_sync(0xffffffffu, before);
     upto += before;
-    const int past = upto - h.x - h.y;  // keys above both bins
-    if (past < rest && rest <= upto) {
-      const bool upper = rest <= past + h.y;
-      s_found[0] = upper ? bin + 1 : bin;
-      s_found[1] = upper ? rest - past : rest - past - h.y;
-      s_found[2] = upper ? h.y : h.x;
+    int left = rest - (upto - (h.x + h.y) - (h.z + h.w));  // less the keys above these bins
+    if (left > 0 && rest <= upto) {
+      const int have[4] = {h.w, h.z, h.y, h.x};
+#pragma unroll
+      for (int k = 0; k < 4; ++k) {
+        if (left > 0 && left <= have[k]) {
+          s_found[0] = bin + 3 - k;
+          s_found[1] = left;
+          s_found[2] = have[k];
+        }
+        left -= have[k];
+      }
     }
     __syncthreads();
     const int digit = s_found[0], count = s_found[2];
@@ -165,7 +177,7 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     s_warp[1][warp] = equal;
   }
   __syncthreads();
-  int b0 = s_warp[0][lane], b1 = s_warp[1][lane];
+  int b0 = lane < kSelWarps ? s_warp[0][lane] : 0, b1 = lane < kSelWarps ? s_warp[1][lane] : 0;
   if constexpr (CLUSTER) {
     const int t0 = __reduce_add_sync(0xffffffffu, b0), t1 = __reduce_add_sync(0xffffffffu, b1);
     if (threadIdx.x == 0) {
@@ -210,17 +222,19 @@ struct CompactArgs {
   int n_kv, slices, blocks;  // 128-byte slices of a row, blocks of a cluster
 };
 
-constexpr int kMoveThreads = 256, kMovePieces = 4;
-constexpr int kMoveRow = 8;                                            // 16-byte pieces of a slice
-constexpr int kMoveTokens = kMoveThreads * kMovePieces / kMoveRow;     // of a block's round
-static_assert(2 * kMoveTokens <= kMoveThreads, "a thread a source and a destination");
+constexpr int kMovePieces = 4;  // of 16 bytes, a thread and round
+constexpr int kMoveRow = 8;     // of a slice
+constexpr int move_tokens(int threads) { return threads * kMovePieces / kMoveRow; }  // of a block's round
+constexpr int kMoveAlone = 128, kMoveCluster = 256;  // threads of a block
 
 // One cluster a (sequence, head, keys or values, slice of the row).  In a round each
 // block has a run of destinations: all sources of a round are read before any of its
 // destinations is written.  An entry is no less than its own index, so a later round
 // reads nothing that an earlier one has written.
-template <bool CLUSTER>
+template <int kMoveThreads, bool CLUSTER>
 __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const __grid_constant__ CompactArgs p) {
+  constexpr int kMoveTokens = move_tokens(kMoveThreads);
+  static_assert(2 * kMoveTokens <= kMoveThreads, "a thread a source and a destination");
   __shared__ int s_from[2][kMoveTokens], s_to[2][kMoveTokens];
   pdl_wait();
   pdl_trigger();
@@ -309,7 +323,7 @@ int launch_kv_select(const KvSelectCall& c, cudaStream_t st) {
   SelectArgs a{c.w, c.kept, c.lengths, c.new_len, c.status, c.keep, c.sinks, c.recent, 1, 0};
   // Blocks a cluster: more while that leaves two a SM, and slices of some length.
   const long long units = static_cast<long long>(c.n_seqs) * c.kept.n_sets;
-  while (a.blocks < kSelMaxCluster && c.w.tokens / a.blocks > 2048 && units * a.blocks * 2 <= 2LL * num_sms()) a.blocks *= 2;
+  while (a.blocks < kSelMaxCluster && c.w.tokens / a.blocks > kSelSlice && units * a.blocks * 2 <= 2LL * num_sms()) a.blocks *= 2;
   const int slice = ((c.w.tokens - 1) / a.blocks + 1 + 31) / 32 * 32;
   a.held = slice < kSelCap ? slice : kSelCap;
   const int smem = a.held * 4;
@@ -333,13 +347,13 @@ int launch_kv_compact(const KvCompactCall& c, cudaStream_t st) {
   for (int64_t* x : {&a.cache.k_token_stride, &a.cache.k_head_stride, &a.cache.v_token_stride, &a.cache.v_head_stride})
     *x = *x * e / 16;
   const long long units = 2LL * c.n_seqs * c.n_kv * a.slices;
-  while (a.blocks < 8 && a.blocks * kMoveTokens < c.kept.cap && units * a.blocks < 5LL * num_sms()) a.blocks *= 2;
+  while (a.blocks < 8 && a.blocks * move_tokens(kMoveCluster) < c.kept.cap && units * a.blocks < 5LL * num_sms()) a.blocks *= 2;
   if (units * a.blocks > 0x7fffffffLL) return SPECFOLD_ECAPACITY;
   const dim3 grid(static_cast<unsigned>(units * a.blocks));
   if (a.blocks > 1)
-    launch_kc(kv_compact_kernel<true>, grid, dim3(kMoveThreads), 0, st, a.blocks, a);
+    launch_kc(kv_compact_kernel<kMoveCluster, true>, grid, dim3(kMoveCluster), 0, st, a.blocks, a);
   else
-    launch_k(kv_compact_kernel<false>, grid, dim3(kMoveThreads), 0, st, a);
+    launch_k(kv_compact_kernel<kMoveAlone, false>, grid, dim3(kMoveAlone), 0, st, a);
   count_launch();
   return check_launch();
 }

@@ -39,14 +39,14 @@ template <int HD, int NT>
 struct WFew {
   static constexpr int R = 8 * NT;
   static constexpr int CH = 2048 / HD;  // keys of a warp's step: 4 KB
-  static constexpr int STAGES = 6;
+  static constexpr int STAGES = 3;
   static constexpr int ROW = HD * 2;
   static constexpr int CPR = ROW / 16;
   static constexpr int STAGE = CH * ROW;
   static constexpr int RING = STAGES * STAGE;
   static constexpr int OFF_Q = kWarps * RING;
   static constexpr int SMEM = OFF_Q + R * ROW;
-  static constexpr int CTAS = 2;  // per SM
+  static constexpr int CTAS = 4;  // per SM
 };
 
 template <int HD, int NT>
@@ -63,6 +63,7 @@ __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel
   unsigned per;
   if (!tree_locate(p, w, per)) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t once = policy_evict_first();  // the keys: L2 is for the scores
   uint8_t* ring = smem + warp * C::RING;
   uint8_t* s_q = smem + C::OFF_Q;
 
@@ -77,9 +78,18 @@ __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel
     const int chunks = (key_hi - key_lo + CH - 1) / CH;
     const int mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
     auto key_of = [&](int i) { return key_lo + CH * (warp + kWarps * i); };
-    auto slot_of = [&](int i) {  // lanes 0..CH-1: pool tokens of chunk i's keys
-      const int tok = key_of(i) + (lane & (CH - 1));
-      return i < mine && tok < key_hi ? tree_pool_token(p, w.s, tok) : -1;
+    // lanes 0..CH-1 have a chunk's keys: their pages are read two chunks ahead of use
+    const int32_t* table = p.cache.block_table + w.s * p.cache.table_stride;
+    const unsigned ps = p.cache.page_size;
+    auto page_of = [&](int i) {
+      const unsigned tok = key_of(i) + (lane & (CH - 1)), pg = tok / ps;
+      return i < mine && static_cast<int>(tok) < key_hi && pg < static_cast<unsigned>(p.cache.table_pages) ? table[pg] : -1;
+    };
+    auto slot_of = [&](int i, int page) {
+      const unsigned tok = key_of(i) + (lane & (CH - 1));
+      if (page >= 0 && page < p.cache.num_pages) return page * static_cast<int>(ps) + static_cast<int>(tok % ps);
+      if (i < mine && static_cast<int>(tok) < key_hi) atomicOr(p.status, SPECFOLD_DEV_BAD_PAGE);
+      return -1;
     };
     const T* kbase = static_cast<const T*>(p.cache.k) + h * p.cache.k_head_stride;
     auto load = [&](int i, int slot) {
@@ -92,17 +102,18 @@ __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel
           const int key = it * KEYS + lane / C::CPR;
           const int tk = __shfl_sync(0xffffffffu, slot, key);
           const long long tz = tk < 0 ? 0 : tk;  // any valid address when nothing is read
-          cp_async16(st + key * C::ROW + ((c ^ (key & 7)) << 4), kbase + tz * p.cache.k_token_stride + c * 8,
-                     tk < 0 ? 0u : 16u);
+          cp_async16_hint(st + key * C::ROW + ((c ^ (key & 7)) << 4), kbase + tz * p.cache.k_token_stride + c * 8,
+                          tk < 0 ? 0u : 16u, once);
         }
       }
       cp_async_commit();
     };
-    int slot = slot_of(0);
+    int page = page_of(0), next = page_of(1);
 #pragma unroll
     for (int i = 0; i < C::STAGES - 1; ++i) {
-      load(i, slot);
-      slot = slot_of(i + 1);
+      load(i, slot_of(i, page));
+      page = next;
+      next = page_of(i + 2);
     }
     // queries: row m = row m / g of the sequence, head m % g of the group; the rows
     // past the last are its copies (zeros times an infinite key would be NaN)
@@ -136,8 +147,9 @@ __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel
       }
     float* out = a.scores + ((static_cast<size_t>(w.s) * p.n_kv + h) * a.w.tokens) * R + (lane & 3) * 2;
     for (int i = 0; i < mine; ++i) {
-      load(i + C::STAGES - 1, slot);
-      slot = slot_of(i + C::STAGES);
+      load(i + C::STAGES - 1, slot_of(i + C::STAGES - 1, page));
+      page = next;
+      next = page_of(i + C::STAGES + 1);
       cp_async_wait<C::STAGES - 1>();
       __syncwarp();
       const uint8_t* stg = ring + (i % C::STAGES) * C::STAGE;
@@ -330,19 +342,23 @@ __global__ void __launch_bounds__(kThreads, WSimt<HD>::CTAS) weigh_simt_kernel(c
 }
 
 // ------------------------------------------------- weights from the scores --
-// A thread a token: its scores' 2^(x - m) / l, eight rows at a time.
-constexpr int kSumThreads = 256;
+// A thread a token, kSumTokens of them at once: the scores' 2^(x - m) / l, eight rows
+// at a time.  The run is found before the wait for the first launch: that one
+// waited for all before it, and reads the same lengths.
+constexpr int kSumThreads = 256, kSumTokens = 4;
+constexpr int kSumCtas = 3;   // per SM
 constexpr int kSumRows = 64;  // of a head group, at most
 
 __global__ void __launch_bounds__(kSumThreads) weigh_sum_kernel(const __grid_constant__ WeighArgs a) {
   const TreeArgs& p = a.t;
   __shared__ float2 s_part[kSumThreads];
   __shared__ __align__(16) float s_m[kSumRows], s_rl[kSumRows];
-  pdl_wait();
-  pdl_trigger();
   TreeWalk w;
   unsigned per;
-  if (!tree_locate(p, w, per)) return;
+  const bool work = tree_locate(p, w, per);
+  pdl_wait();
+  pdl_trigger();
+  if (!work) return;
   const int SR = a.stat_rows, R = a.score_rows;
   for (; w.n > 0; w.next(p)) {
     const int h = w.head, rows = w.q.n * p.g;
@@ -365,23 +381,40 @@ __global__ void __launch_bounds__(kSumThreads) weigh_sum_kernel(const __grid_con
     __syncthreads();
     const float* x = a.scores + (static_cast<size_t>(w.s) * p.n_kv + h) * a.w.tokens * R;
     float* wt = a.w.ptr + w.s * a.w.seq_stride + h * a.w.head_stride;
-#pragma unroll 4
-    for (int t = key_lo + threadIdx.x; t < key_hi; t += kSumThreads) {
-      float sum = 0.f;
-      for (int r = 0; r < rows; r += 8) {
-        const float4 u = *reinterpret_cast<const float4*>(x + static_cast<size_t>(t) * R + r);
-        const float4 v = *reinterpret_cast<const float4*>(x + static_cast<size_t>(t) * R + r + 4);
-        sum = fmaf(ex2(u.x - s_m[r]), s_rl[r], sum);
-        sum = fmaf(ex2(u.y - s_m[r + 1]), s_rl[r + 1], sum);
-        sum = fmaf(ex2(u.z - s_m[r + 2]), s_rl[r + 2], sum);
-        sum = fmaf(ex2(u.w - s_m[r + 3]), s_rl[r + 3], sum);
-        sum = fmaf(ex2(v.x - s_m[r + 4]), s_rl[r + 4], sum);
-        sum = fmaf(ex2(v.y - s_m[r + 5]), s_rl[r + 5], sum);
-        sum = fmaf(ex2(v.z - s_m[r + 6]), s_rl[r + 6], sum);
-        sum = fmaf(ex2(v.w - s_m[r + 7]), s_rl[r + 7], sum);
+    for (int t0 = key_lo + threadIdx.x; t0 < key_hi; t0 += kSumThreads * kSumTokens) {
+      float sum[kSumTokens] = {}, old[kSumTokens];
+#pragma unroll
+      for (int k = 0; k < kSumTokens; ++k) {
+        const int t = t0 + k * kSumThreads;
+        old[k] = t < key_hi && t < w.q.ctx && a.decay != 0.f ? wt[t] : 0.f;
       }
-      if (t < w.q.ctx && a.decay != 0.f) sum = fmaf(a.decay, wt[t], sum);
-      wt[t] = sum;
+      for (int r = 0; r < rows; r += 8) {
+        float4 u[kSumTokens], v[kSumTokens];
+#pragma unroll
+        for (int k = 0; k < kSumTokens; ++k) {
+          const float4* at = reinterpret_cast<const float4*>(x + static_cast<size_t>(min(t0 + k * kSumThreads, key_hi - 1)) * R + r);
+          u[k] = at[0];
+          v[k] = at[1];
+        }
+        const float4 m0 = *reinterpret_cast<const float4*>(s_m + r), m1 = *reinterpret_cast<const float4*>(s_m + r + 4);
+        const float4 l0 = *reinterpret_cast<const float4*>(s_rl + r), l1 = *reinterpret_cast<const float4*>(s_rl + r + 4);
+#pragma unroll
+        for (int k = 0; k < kSumTokens; ++k) {
+          sum[k] = fmaf(ex2(u[k].x - m0.x), l0.x, sum[k]);
+          sum[k] = fmaf(ex2(u[k].y - m0.y), l0.y, sum[k]);
+          sum[k] = fmaf(ex2(u[k].z - m0.z), l0.z, sum[k]);
+          sum[k] = fmaf(ex2(u[k].w - m0.w), l0.w, sum[k]);
+          sum[k] = fmaf(ex2(v[k].x - m1.x), l1.x, sum[k]);
+          sum[k] = fmaf(ex2(v[k].y - m1.y), l1.y, sum[k]);
+          sum[k] = fmaf(ex2(v[k].z - m1.z), l1.z, sum[k]);
+          sum[k] = fmaf(ex2(v[k].w - m1.w), l1.w, sum[k]);
+        }
+      }
+#pragma unroll
+      for (int k = 0; k < kSumTokens; ++k) {
+        const int t = t0 + k * kSumThreads;
+        if (t < key_hi) wt[t] = fmaf(a.decay, old[k], sum[k]);
+      }
     }
   }
 }
@@ -580,7 +613,7 @@ int weigh_go(const KvWeighCall& c, cudaStream_t st) {
                                      : start(weigh_simt_kernel<HD>, a, grid, kThreads, WSimt<HD>::SMEM, st))
     return rc;
   t.tile_rows = SPECFOLD_MAX_TREE * 128;  // all of a head group's rows
-  return start(weigh_sum_kernel, a, std::min(num_sms(), kSmBudget) * 4, kSumThreads, 0, st);
+  return start(weigh_sum_kernel, a, num_sms() * kSumCtas, kSumThreads, 0, st);
 }
 
 }  // namespace

@@ -35,8 +35,9 @@ struct WTc {
 };
 
 // Keys of a run's blocks, one TMA box per run of tokens inside a page: warp 0.
-// Returns false if a wait ran out.
-template <int HD>
+// Returns false if a wait ran out.  BACK: the last block first (see the weights'
+// kernel).
+template <int HD, bool BACK>
 struct KeyLoader {
   using C = WTc<HD>;
   int it = 0;
@@ -48,13 +49,14 @@ struct KeyLoader {
     const int box = lane & 15, atom = lane >> 4;  // what this thread issues of a tile
     const bool issues = box < kBlock / ta.box && atom < C::NATOM;
     // the table's entry is read a tile ahead of its use and looked at only then
-    const unsigned tok0 = static_cast<unsigned>(w.b0) * kBlock + box * ta.box;
+    const unsigned tok0 = static_cast<unsigned>(w.b0 + (BACK ? w.n - 1 : 0)) * kBlock + box * ta.box;
     int pg = tok0 / static_cast<unsigned>(ps), off = tok0 - pg * ps;
     const int dpg = kBlock / ps, doff = kBlock - dpg * ps;
     const int32_t* table = p.cache.block_table + w.s * p.cache.table_stride;
     long long left = static_cast<long long>(len) - tok0;
     auto entry = [&](int t) { return issues && t < w.n && left > 0 && pg < p.cache.table_pages ? table[pg] : -1; };
     int page = entry(0);
+    const uint64_t once = policy_evict_first();
     for (int t = 0; t < w.n; ++t, ++it) {
       const int st = it % C::RING;
       const uint32_t fb = smem_u32(&full[st]);
@@ -68,15 +70,25 @@ struct KeyLoader {
         const bool there = page >= 0 && page < p.cache.num_pages;
         if (!there && left > 0) atomicOr(p.status, SPECFOLD_DEV_BAD_PAGE);
         // a box without a page lies wholly past the pool: it reads zeros
-        tma_load_3d(smem_u32(smem + C::OFF_RING + st * C::TILE + atom * kAtom + box * ta.box * 128), &ta.mapK, fb, atom * 64,
-                    w.head, there && left > 0 ? page * ps + off : pool);
+        tma_load_3d_hint(smem_u32(smem + C::OFF_RING + st * C::TILE + atom * kAtom + box * ta.box * 128), &ta.mapK, fb,
+                         atom * 64, w.head, there && left > 0 ? page * ps + off : pool, once);
       }
-      left -= kBlock;
-      pg += dpg;
-      off += doff;
-      if (off >= ps) {
-        off -= ps;
-        ++pg;
+      if constexpr (BACK) {
+        left += kBlock;
+        pg -= dpg;
+        off -= doff;
+        if (off < 0) {
+          off += ps;
+          --pg;
+        }
+      } else {
+        left -= kBlock;
+        pg += dpg;
+        off += doff;
+        if (off >= ps) {
+          off -= ps;
+          ++pg;
+        }
       }
       page = entry(t + 1);
     }
@@ -110,6 +122,18 @@ SF_DEV void gather_rows(const WeighArgs& a, const TreeWalk& w, int m0, int rows,
   cp_async_commit();
   cp_async_wait<0>();
   fence_proxy_async_smem();
+}
+
+// 32 lanes x 16 columns, complete: thread t of the warp gets lane t's.
+SF_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(taddr)
+      : "memory");
 }
 
 // D[128 x n] = A B^T over the HD dimensions of two tiles in shared memory.
@@ -179,7 +203,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_stats_tc_kernel(const __g
     return;
   }
   if (warp == 0) {
-    KeyLoader<HD> keys;
+    KeyLoader<HD, false> keys;
     for (; w.n > 0 && keys.piece(ta, w, smem, full, empty, abort_flag); w.next(p)) {
     }
     keys.drain(full, abort_flag);
@@ -321,7 +345,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_stats_tc_kernel(const __g
 // place while the blocks stream by; with more, a group of RING blocks stays and the
 // tiles pass, back and forth, so that a tile is gathered once for a group.  A
 // product's 128 keys are TMEM's lanes, its rows the columns of one of two buffers;
-// the two halves of the reducing warps take alternate 32 columns.
+// the two halves of the reducing warps have half of the columns each.  Blocks go from
+// a run's last to its first: what the statistics read last is still in L2.
 struct WItems {  // the order of a unit's products, the same in every role
   int n, tiles, group;
   int g0 = 0, tile_at = 0, dir = 1, done = 0;  // group's first block, tile now, its step, tiles of the group so far
@@ -383,11 +408,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
     tmem_alloc(smem_u32(&tmem_slot_s), 512);
     tmem_relinquish();
   }
-  pdl_wait();
-  pdl_trigger();
   TreeWalk w;
   unsigned per;
-  const bool work = tree_locate(p, w, per);
+  const bool work = tree_locate(p, w, per);  // before the wait: the first launch has waited for all before it
+  pdl_wait();
+  pdl_trigger();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
@@ -401,7 +426,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
   auto rows_of = [&](int tile) { return min(kWeighTcRows, all_rows() - tile * kWeighTcRows); };
 
   if (warp == 0) {
-    KeyLoader<HD> keys;
+    KeyLoader<HD, true> keys;
     for (; w.n > 0 && keys.piece(ta, w, smem, full, empty, abort_flag); w.next(p)) {
     }
     keys.drain(full, abort_flag);
@@ -491,12 +516,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
           ++ql;
         }
         const float *tm_ = s_m[(ql - 1) & 1], *tr = s_rl[(ql - 1) & 1];
-        const int chunks = (rows_of(q.tile_at) + 31) / 32, m0 = q.tile_at * kWeighTcRows;
+        const int half = (rows_of(q.tile_at) + 31) / 32 * 16, m0 = q.tile_at * kWeighTcRows;
         const bool single = q.tiles == 1, last = q.last();
         const int nb = q.blocks();
         for (int b = 0; b < nb; ++b, ++cnt) {
           const int buf = cnt & 1;
-          const long long t0 = static_cast<long long>(w.b0 + q.g0 + b) * kBlock;
+          const long long t0 = static_cast<long long>(w.b0 + q.n - 1 - (q.g0 + b)) * kBlock;
           const bool tail = t0 + kBlock > ctx;
           const bool mine = last && x == 0 && t0 + key < len;  // this thread writes a weight
           const float old = mine && t0 + key < ctx && a.decay != 0.f ? wt[t0 + key] : 0.f;
@@ -510,27 +535,39 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
             const int from = tail ? static_cast<int>(min(max(t0 + key - ctx, 0ll) * p.g - m0, 1ll << 20)) : 0;
             const float2 scale2 = make_float2(p.sl2, p.sl2);
             float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-#pragma unroll 1
-            for (int c = x; c < chunks; c += 2) {
-              uint32_t s[32];
-              tmem_ld32(tmem + lane_off + buf * 256 + c * 32, s);
-              tmem_ld_wait(s);
+            // N columns from c0 on, loaded into s
+            auto add = [&](const auto& s, int c0) {
+              constexpr int N = sizeof(s) / sizeof(s[0]);
 #pragma unroll
-              for (int e = 0; e < 32; e += 4) {
-                const float4 m4 = *reinterpret_cast<const float4*>(tm_ + c * 32 + e);
-                const float4 r4 = *reinterpret_cast<const float4*>(tr + c * 32 + e);
+              for (int e = 0; e < N; e += 4) {
+                const float4 m4 = *reinterpret_cast<const float4*>(tm_ + c0 + e);
+                const float4 r4 = *reinterpret_cast<const float4*>(tr + c0 + e);
                 float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, make_float2(m4.x, m4.y));
                 float2 z = fma2(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), scale2, make_float2(m4.z, m4.w));
                 if (tail) {
-                  if (c * 32 + e < from) y.x = -INFINITY;
-                  if (c * 32 + e + 1 < from) y.y = -INFINITY;
-                  if (c * 32 + e + 2 < from) z.x = -INFINITY;
-                  if (c * 32 + e + 3 < from) z.y = -INFINITY;
+                  if (c0 + e < from) y.x = -INFINITY;
+                  if (c0 + e + 1 < from) y.y = -INFINITY;
+                  if (c0 + e + 2 < from) z.x = -INFINITY;
+                  if (c0 + e + 3 < from) z.y = -INFINITY;
                 }
                 // (a row that weighs nothing has -inf and 0)
                 acc[0] = fma2(make_float2(ex2(y.x), ex2(y.y)), make_float2(r4.x, r4.y), acc[0]);
                 acc[1] = fma2(make_float2(ex2(z.x), ex2(z.y)), make_float2(r4.z, r4.w), acc[1]);
               }
+            };
+            const uint32_t at = tmem + lane_off + buf * 256;
+            int c = x * half;
+#pragma unroll 1
+            for (; c + 32 <= (x + 1) * half; c += 32) {
+              uint32_t s[32];
+              tmem_ld32(at + c, s);
+              tmem_ld_wait(s);
+              add(s, c);
+            }
+            if (c < (x + 1) * half) {
+              uint32_t s[16];
+              tmem_ld16(at + c, s);
+              add(s, c);
             }
             tc_fence_before();
             __syncwarp();

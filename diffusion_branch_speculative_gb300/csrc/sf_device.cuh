@@ -208,6 +208,13 @@ SF_DEV void tma_load_3d(uint32_t dst, const CUtensorMap* map, uint32_t bar, int 
       "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z)
       : "memory");
 }
+SF_DEV void tma_load_3d_hint(uint32_t dst, const CUtensorMap* map, uint32_t bar, int x, int y, int z, uint64_t policy) {
+  asm volatile(
+      "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes.L2::cache_hint"
+      " [%0], [%1, {%3, %4, %5}], [%2], %6;" ::"r"(dst),
+      "l"(reinterpret_cast<uint64_t>(map)), "r"(bar), "r"(x), "r"(y), "r"(z), "l"(policy)
+      : "memory");
+}
 // Untiled bulk copy global -> shared memory of `bytes` (a multiple of 16,
 // both addresses 16-byte aligned), completing on the mbarrier.
 SF_DEV void bulk_load(uint32_t dst, const void* src, uint32_t bytes, uint32_t bar) {
