@@ -5,7 +5,7 @@
 #include "sf_internal.h"
 
 #include <algorithm>
-#include <climits>
+#include <type_traits>
 
 namespace sf {
 namespace {
@@ -31,30 +31,46 @@ SF_DEV uint32_t weight_key(float x) {
 
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;           // of a pass over 11, 11 and 10 bits of the keys
+constexpr int kSelGroups = kSelBins / 32;
 constexpr int kSelCap = 48 * 1024;       // keys of a block's slice that shared memory holds
 constexpr int kSelMaxCluster = 8;
 constexpr int kSelSlice = 4096;          // tokens that are worth a block more
+constexpr int kSelStep = 1024;           // keys of a warp's step, 32 a lane
 
-SF_DEV int ld_dsmem_s32(uint32_t addr) {
-  int v;
-  asm volatile("ld.shared::cluster.s32 %0, [%1];" : "=r"(v) : "r"(addr));
-  return v;
+SF_DEV void st_dsmem_s32(uint32_t addr, int v) {
+  asm volatile("st.shared::cluster.s32 [%0], %1;" ::"r"(addr), "r"(v) : "memory");
 }
-SF_DEV int4 ld_dsmem_s32x4(uint32_t addr) {
-  int4 v;
-  asm volatile("ld.shared::cluster.v4.s32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(addr));
-  return v;
+
+// Two of 64 counts a lane (h.x, h.y: those at 62 - 2 lane and 63 - 2 lane): the place, from the
+// last down, of the one with the left-th; left: which of its own that is.
+SF_DEV int find_from_last(int2 h, int lane, int& left) {
+  int upto = h.x + h.y;
+#pragma unroll
+  for (int o = 1; o < 32; o <<= 1) {
+    const int u = __shfl_up_sync(0xffffffffu, upto, o);
+    if (lane >= o) upto += u;
+  }
+  const int src = __ffs(__ballot_sync(0xffffffffu, upto >= left)) - 1;
+  const int in = left - (upto - h.x - h.y);  // less those above these two
+  const bool upper = in <= h.y;
+  left = __shfl_sync(0xffffffffu, upper ? in : in - h.y, src);
+  return __shfl_sync(0xffffffffu, 62 - 2 * lane + (upper ? 1 : 0), src);
 }
 
 // One cluster a (sequence, set); its blocks have a slice each of the tokens between
 // the first and the latest ones, its keys in shared memory.  Three passes find the
-// smallest chosen key by its digits (a histogram a block, added up over the cluster),
-// then every warp writes what it has of its run of the slice, behind what lies before.
+// smallest chosen key by its digits: a histogram a block, added up over the cluster
+// in two steps, the groups of 32 bins and then the bins of one, which the blocks write
+// to each other (reading all bins of eight blocks took 2 to 5 us a pass, reading
+// groups and bins 4).  Then every warp writes what it has of its run of the slice, behind
+// what lies before.  Measured (3 sequences of 131071 tokens at most, 8 sets): see below.
 template <bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_constant__ SelectArgs p) {
-  extern __shared__ uint32_t s_key[];
-  __shared__ __align__(16) int s_hist[3][kSelBins];  // a pass each: read by the cluster while the next is filled
-  __shared__ int s_warp[2][kSelWarps], s_found[3], s_total[2];
+  extern __shared__ __align__(16) uint32_t s_key[];
+  __shared__ int s_hist[2][kSelBins];
+  __shared__ __align__(8) int s_group[2][kSelMaxCluster][kSelGroups];  // the blocks' sums of this pass
+  __shared__ int s_bin[2][kSelMaxCluster][32];                         // and their bins of the group found
+  __shared__ int s_warp[kSelWarps][2], s_found[3], s_total[kSelMaxCluster][2];
   pdl_wait();
   pdl_trigger();
   const int blocks = CLUSTER ? p.blocks : 1, rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
@@ -82,133 +98,187 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
   for (int i = tid; i < p.recent; i += threads) out[lo + need + i] = hi + i;
   if (need == 0) return;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int slice = ((hi - lo - 1) / blocks + 1 + 31) & ~31;
-  const int from = min(hi, lo + rank * slice), n = min(hi - from, slice);  // this block's
+  const int slice = (hi - lo - 1) / blocks / kSelStep * kSelStep + kSelStep;
+  const int from = min(static_cast<long long>(hi), lo + static_cast<long long>(rank) * slice);
+  const int n = min(hi - from, slice);  // this block's (none, for some, of a short sequence)
   const float* w = p.w.ptr + s * p.w.seq_stride + set * p.w.head_stride + from;
-  const bool held = n <= p.held;
   auto all_sync = [] {
     if constexpr (CLUSTER)
       cluster_sync_all();
     else
       __syncthreads();
   };
-  for (int i = threadIdx.x; i < 3 * kSelBins; i += kSelThreads) (&s_hist[0][0])[i] = 0;
-  __syncthreads();
-  // the keys, and the first pass
-#pragma unroll 8
-  for (int i = threadIdx.x; i < n; i += kSelThreads) {
-    const uint32_t k = weight_key(w[i]);
-    if (held) s_key[i] = k;
-    atomicAdd(&s_hist[0][k >> 21], 1);
-  }
-  auto key = [&](int i) { return held ? s_key[i] : weight_key(w[i]); };
-  uint32_t prefix = 0u;
-  int rest = need, shift = 21;
-#pragma unroll 1
-  for (int pass = 0;; ++pass) {
-    all_sync();
-    // bins from the largest down, four a thread: the one with the rest-th key
-    static_assert(kSelBins == 4 * kSelThreads, "four bins a thread");
-    const int bin = kSelBins - 4 - 4 * static_cast<int>(threadIdx.x);
-    int4 h;
+  // v to all blocks' copies of a place in shared memory, a lane a block
+  auto tell = [&](int* at, int v) {
     if constexpr (CLUSTER) {
-      const uint32_t at = smem_u32(&s_hist[pass][bin]);
-      h = make_int4(0, 0, 0, 0);
-#pragma unroll
-      for (int k0 = 0; k0 < kSelMaxCluster; k0 += 4) {
-        int4 x[4];  // four asked for before any is added
-#pragma unroll
-        for (int k = 0; k < 4; ++k) x[k] = k0 + k < blocks ? ld_dsmem_s32x4(dsmem_addr(at, k0 + k)) : make_int4(0, 0, 0, 0);
-#pragma unroll
-        for (int k = 0; k < 4; ++k) h = make_int4(h.x + x[k].x, h.y + x[k].y, h.z + x[k].z, h.w + x[k].w);
-      }
+      if (lane < blocks) st_dsmem_s32(dsmem_addr(smem_u32(at), lane), v);
     } else {
-      h = *reinterpret_cast<const int4*>(&s_hist[pass][bin]);
+      if (lane == 0) *at = v;
     }
-    int upto = (h.x + h.y) + (h.z + h.w);
+  };
+  for (int i = threadIdx.x; i < kSelBins; i += kSelThreads) s_hist[0][i] = s_hist[1][i] = 0;
+  all_sync();  // (and the cluster's blocks have all begun)
+  auto choose = [&](auto held) {
+    constexpr bool kHeld = decltype(held)::value;
+    // Keys in pieces of four, piece c of eight at c ^ (the eight's number mod 8): a warp reads
+    // 32 pieces side by side or eight apart without conflicts.  Zeros past the end.
+    auto place = [](int i) { return i ^ ((i >> 5 & 7) << 2); };
+    auto keys = [&](int i, uint32_t (&k)[4]) {  // i .. i + 3, i a multiple of four
+      if constexpr (kHeld) {
+        const uint4 u = *reinterpret_cast<const uint4*>(s_key + place(i));
+        k[0] = u.x, k[1] = u.y, k[2] = u.z, k[3] = u.w;
+      } else {
 #pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-      const int u = __shfl_up_sync(0xffffffffu, upto, o);
-      if (lane >= o) upto += u;
-    }
-    if (lane == 31) s_warp[0][warp] = upto;
-    __syncthreads();
-    int before = lane < warp ? s_warp[0][lane] : 0;
-    before = __reduce_add_sync(0xffffffffu, before);
-    upto += before;
-    int left = rest - (upto - (h.x + h.y) - (h.z + h.w));  // less the keys above these bins
-    if (left > 0 && rest <= upto) {
-      const int have[4] = {h.w, h.z, h.y, h.x};
-#pragma unroll
-      for (int k = 0; k < 4; ++k) {
-        if (left > 0 && left <= have[k]) {
-          s_found[0] = bin + 3 - k;
-          s_found[1] = left;
-          s_found[2] = have[k];
-        }
-        left -= have[k];
+        for (int j = 0; j < 4; ++j) k[j] = i + j < n ? weight_key(w[i + j]) : 0u;
       }
+    };
+    // the keys, and the first pass
+#pragma unroll 8
+    for (int i = threadIdx.x; i < n; i += kSelThreads) {
+      const uint32_t k = weight_key(w[i]);
+      if constexpr (kHeld) s_key[place(i)] = k;
+      atomicAdd(&s_hist[0][k >> 21], 1);
+    }
+    if constexpr (kHeld) {
+      for (int i = max(n, 0) + threadIdx.x; i < (max(n, 0) + kSelStep - 1) / kSelStep * kSelStep; i += kSelThreads) s_key[place(i)] = 0u;
+    }
+    uint32_t prefix = 0u;
+    int rest = need, shift = 21;
+#pragma unroll 1
+    for (int pass = 0;; ++pass) {
+      int* hist = s_hist[pass & 1];
+      __syncthreads();
+      for (int g = warp; g < kSelGroups; g += kSelWarps)
+        tell(&s_group[pass & 1][rank][g], __reduce_add_sync(0xffffffffu, hist[g * 32 + lane]));
+      all_sync();
+      int left = rest, group = 0;
+      if (warp == 0) {
+        int2 h = make_int2(0, 0);
+        for (int k = 0; k < blocks; ++k) {
+          const int2 x = *reinterpret_cast<const int2*>(&s_group[pass & 1][k][62 - 2 * lane]);
+          h = make_int2(h.x + x.x, h.y + x.y);
+        }
+        group = find_from_last(h, lane, left);
+        const int mine = hist[group * 32 + lane];
+        if constexpr (CLUSTER) {
+          for (int k = 0; k < blocks; ++k) st_dsmem_s32(dsmem_addr(smem_u32(&s_bin[pass & 1][rank][lane]), k), mine);
+        } else {
+          s_bin[pass & 1][0][lane] = mine;
+        }
+      }
+      all_sync();
+      if (warp == 0) {
+        // the group's bins as the upper 32 of 64, two a lane
+        int2 h = make_int2(0, 0);
+        if (lane < 16)
+          for (int k = 0; k < blocks; ++k) {
+            h.x += s_bin[pass & 1][k][30 - 2 * lane];
+            h.y += s_bin[pass & 1][k][31 - 2 * lane];
+          }
+        const int digit = find_from_last(h, lane, left) - 32;
+        const int count = __shfl_sync(0xffffffffu, digit & 1 ? h.y : h.x, (31 - digit) / 2);
+        if (lane == 0) {
+          s_found[0] = group * 32 + digit;
+          s_found[1] = left;
+          s_found[2] = count;
+        }
+      }
+      __syncthreads();
+      const int digit = s_found[0], count = s_found[2];
+      rest = s_found[1];
+      prefix = pass == 0 ? digit : prefix << (pass == 1 ? 11 : 10) | static_cast<uint32_t>(digit);
+      if (pass == 2 || count == rest) break;  // (all of that bin: no further digit counts)
+      const int next = pass == 0 ? 10 : 0;
+      const uint32_t mask = pass == 0 ? 2047u : 1023u;
+      int* to = s_hist[(pass + 1) & 1];
+      if (pass == 1) {  // the first pass's
+        for (int i = threadIdx.x; i < kSelBins; i += kSelThreads) to[i] = 0;
+        __syncthreads();
+      }
+#pragma unroll 2
+      for (int i = 4 * threadIdx.x; i < n; i += 4 * kSelThreads) {
+        uint32_t k[4];
+        keys(i, k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j)
+          if (k[j] >> shift == prefix && i + j < n) atomicAdd(&to[(k[j] >> next) & mask], 1);
+      }
+      shift = next;
+    }
+    // ascending: all above the digits found, and the first `rest` of those that have them.
+    // A warp has a run of steps of 1024 keys, a lane 32 of them side by side.
+    const int steps = max(0, n + kSelStep - 1) / kSelStep, run = (steps + kSelWarps - 1) / kSelWarps;
+    const int st0 = min(steps, warp * run), st1 = min(steps, st0 + run);
+    uint32_t gt = 0u, eq = 0u;  // of the lane's keys in a step
+    auto marks = [&](int st) {
+      gt = eq = 0u;
+      const int i = st * kSelStep + 32 * lane;
+#pragma unroll
+      for (int c = 0; c < 8; ++c) {
+        uint32_t k[4];
+        keys(i + 4 * c, k);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          gt |= (k[j] >> shift > prefix ? 1u : 0u) << (4 * c + j);
+          eq |= (k[j] >> shift == prefix ? 1u : 0u) << (4 * c + j);
+        }
+      }
+      const int there = n - i;  // (what lies past the end is a key of zero)
+      if (there < 32) eq &= there <= 0 ? 0u : (1u << there) - 1u;
+    };
+    int above = 0, equal = 0;
+    for (int st = st0; st < st1; ++st) {
+      marks(st);
+      above += __popc(gt);
+      equal += __popc(eq);
+    }
+    above = __reduce_add_sync(0xffffffffu, above);
+    equal = __reduce_add_sync(0xffffffffu, equal);
+    if (lane == 0) {
+      s_warp[warp][0] = above;
+      s_warp[warp][1] = equal;
     }
     __syncthreads();
-    const int digit = s_found[0], count = s_found[2];
-    rest = s_found[1];
-    prefix = pass == 0 ? digit : prefix << (pass == 1 ? 11 : 10) | static_cast<uint32_t>(digit);
-    if (pass == 2 || count == rest) break;  // (all of that bin: no further digit counts)
-    const int next = pass == 0 ? 10 : 0;
-#pragma unroll 4
-    for (int i = threadIdx.x; i < n; i += kSelThreads) {
-      const uint32_t k = key(i);
-      if (k >> shift == prefix) atomicAdd(&s_hist[pass + 1][(k >> next) & (pass == 0 ? 2047u : 1023u)], 1);
+    int b0 = lane < kSelWarps ? s_warp[lane][0] : 0, b1 = lane < kSelWarps ? s_warp[lane][1] : 0;
+    if constexpr (CLUSTER) {
+      const int t0 = __reduce_add_sync(0xffffffffu, b0), t1 = __reduce_add_sync(0xffffffffu, b1);
+      if (warp == 0) {
+        tell(&s_total[rank][0], t0);
+        tell(&s_total[rank][1], t1);
+      }
+      cluster_sync_all();  // the last exchange: a block may end from here on
     }
-    shift = next;
-  }
-  // ascending: all above the digits found, and the first `rest` of those that have them
-  const int run = (slice / 32 + kSelWarps - 1) / kSelWarps * 32, i0 = warp * run, i1 = min(n, i0 + run);
-  int above = 0, equal = 0;
-  for (int i = i0 + lane; i < i1; i += 32) {
-    const uint32_t k = key(i) >> shift;
-    above += k > prefix;
-    equal += k == prefix;
-  }
-  above = __reduce_add_sync(0xffffffffu, above);
-  equal = __reduce_add_sync(0xffffffffu, equal);
-  if (lane == 0) {
-    s_warp[0][warp] = above;  // (pass's own values have been read, see its last barrier)
-    s_warp[1][warp] = equal;
-  }
-  __syncthreads();
-  int b0 = lane < kSelWarps ? s_warp[0][lane] : 0, b1 = lane < kSelWarps ? s_warp[1][lane] : 0;
-  if constexpr (CLUSTER) {
-    const int t0 = __reduce_add_sync(0xffffffffu, b0), t1 = __reduce_add_sync(0xffffffffu, b1);
-    if (threadIdx.x == 0) {
-      s_total[0] = t0;
-      s_total[1] = t1;
+    b0 = __reduce_add_sync(0xffffffffu, lane < warp ? b0 : 0);
+    b1 = __reduce_add_sync(0xffffffffu, lane < warp ? b1 : 0);
+    if constexpr (CLUSTER) {  // the blocks before
+      b0 += __reduce_add_sync(0xffffffffu, lane < rank ? s_total[lane][0] : 0);
+      b1 += __reduce_add_sync(0xffffffffu, lane < rank ? s_total[lane][1] : 0);
     }
-    cluster_sync_all();
-  }
-  b0 = __reduce_add_sync(0xffffffffu, lane < warp ? b0 : 0);
-  b1 = __reduce_add_sync(0xffffffffu, lane < warp ? b1 : 0);
-  if constexpr (CLUSTER) {
-    int c0 = 0, c1 = 0;
-    if (lane < rank) {  // the blocks before
-      c0 = ld_dsmem_s32(dsmem_addr(smem_u32(&s_total[0]), lane));
-      c1 = ld_dsmem_s32(dsmem_addr(smem_u32(&s_total[1]), lane));
+    for (int st = st0; st < st1; ++st) {
+      if (run > 1) marks(st);
+      const int mine = __popc(gt) + (__popc(eq) << 16);
+      int upto = mine;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int u = __shfl_up_sync(0xffffffffu, upto, o);
+        if (lane >= o) upto += u;
+      }
+      const int g = b0 + ((upto - mine) & 0xffff), e = b1 + ((upto - mine) >> 16);
+      for (uint32_t m = gt | eq; m; m &= m - 1u) {
+        const int bit = __ffs(m) - 1;
+        const uint32_t below = (1u << bit) - 1u;
+        const int at_e = e + __popc(eq & below);
+        if ((gt >> bit & 1u) || at_e < rest) out[lo + g + __popc(gt & below) + min(at_e, rest)] = from + st * kSelStep + 32 * lane + bit;
+      }
+      upto = __shfl_sync(0xffffffffu, upto, 31);
+      b0 += upto & 0xffff;
+      b1 += upto >> 16;
     }
-    b0 += __reduce_add_sync(0xffffffffu, c0);
-    b1 += __reduce_add_sync(0xffffffffu, c1);
-  }
-  const uint32_t below = (1u << lane) - 1u;
-  for (int i = i0; i < i1; i += 32) {
-    const bool there = i + lane < i1;
-    const uint32_t k = there ? key(i + lane) >> shift : 0u;
-    const bool gt = there && k > prefix, eq = there && k == prefix;
-    const uint32_t mg = __ballot_sync(0xffffffffu, gt), me = __ballot_sync(0xffffffffu, eq);
-    const int at_e = b1 + __popc(me & below);
-    if (gt || (eq && at_e < rest)) out[lo + b0 + __popc(mg & below) + min(at_e, rest)] = from + i + lane;
-    b0 += __popc(mg);
-    b1 += __popc(me);
-  }
-  if constexpr (CLUSTER) cluster_sync_all();  // no block ends while another reads its shared memory
+  };
+  if (slice <= p.held)  // the same in all of the cluster
+    choose(std::true_type{});
+  else
+    choose(std::false_type{});
 }
 
 // --------------------------------------------------------------- compact --
@@ -324,7 +394,7 @@ int launch_kv_select(const KvSelectCall& c, cudaStream_t st) {
   // Blocks a cluster: more while that leaves two a SM, and slices of some length.
   const long long units = static_cast<long long>(c.n_seqs) * c.kept.n_sets;
   while (a.blocks < kSelMaxCluster && c.w.tokens / a.blocks > kSelSlice && units * a.blocks * 2 <= 2LL * num_sms()) a.blocks *= 2;
-  const int slice = ((c.w.tokens - 1) / a.blocks + 1 + 31) / 32 * 32;
+  const int slice = (c.w.tokens - 1) / a.blocks / kSelStep * kSelStep + kSelStep;
   a.held = slice < kSelCap ? slice : kSelCap;
   const int smem = a.held * 4;
   auto kernel = a.blocks > 1 ? kv_select_kernel<true> : kv_select_kernel<false>;
