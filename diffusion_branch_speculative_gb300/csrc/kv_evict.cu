@@ -292,20 +292,23 @@ struct CompactArgs {
   int n_kv, slices, blocks;  // 128-byte slices of a row, blocks of a cluster
 };
 
-constexpr int kMovePieces = 4;  // of 16 bytes, a thread and round
-constexpr int kMoveRow = 8;     // of a slice
-constexpr int move_tokens(int threads) { return threads * kMovePieces / kMoveRow; }  // of a block's round
-constexpr int kMoveAlone = 128, kMoveCluster = 256;  // threads of a block
+constexpr int kMoveRow = 8;  // 16-byte pieces of a slice
+template <bool CLUSTER>
+struct Move {
+  static constexpr int THREADS = CLUSTER ? 256 : 128;
+  static constexpr int PIECES = 4;                                   // a thread and round
+  static constexpr int TOKENS = THREADS * PIECES / kMoveRow;         // of a block's round
+};
 
 // One cluster a (sequence, head, keys or values, slice of the row).  In a round each
 // block has a run of destinations: all sources of a round are read before any of its
 // destinations is written.  An entry is no less than its own index, so a later round
 // reads nothing that an earlier one has written.
-template <int kMoveThreads, bool CLUSTER>
-__global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const __grid_constant__ CompactArgs p) {
-  constexpr int kMoveTokens = move_tokens(kMoveThreads);
-  static_assert(2 * kMoveTokens <= kMoveThreads, "a thread a source and a destination");
-  __shared__ int s_from[2][kMoveTokens], s_to[2][kMoveTokens];
+template <bool CLUSTER>
+__global__ void __launch_bounds__(Move<CLUSTER>::THREADS) kv_compact_kernel(const __grid_constant__ CompactArgs p) {
+  constexpr int THREADS = Move<CLUSTER>::THREADS, PIECES = Move<CLUSTER>::PIECES, TOKENS = Move<CLUSTER>::TOKENS;
+  constexpr int WEIGHTS = (TOKENS + THREADS - 1) / THREADS;  // a thread and round
+  __shared__ int s_at[2][2][TOKENS];  // [round][source, destination]
   pdl_wait();
   pdl_trigger();
   const int blocks = CLUSTER ? p.blocks : 1, rank = CLUSTER ? static_cast<int>(cluster_ctarank()) : 0;
@@ -330,50 +333,56 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const __grid_c
   uint4* pool = reinterpret_cast<uint4*>(is_v ? c.v : c.k) + h * (is_v ? c.v_head_stride : c.k_head_stride) +
                 slice * kMoveRow + threadIdx.x % kMoveRow;
   const long long ts = is_v ? c.v_token_stride : c.k_token_stride;
-  const int mine = threadIdx.x / kMoveRow;  // and every kMoveThreads / kMoveRow-th token behind it
-  const bool dest = threadIdx.x >= kMoveTokens;
-  const int token = threadIdx.x % kMoveTokens;
-  // a round's pool tokens: the sources by the first threads, the destinations by the others
+  const int mine = threadIdx.x / kMoveRow;  // and every THREADS / kMoveRow-th token behind it
+  // a round's pool tokens, -1 for a token that stays
   auto locate = [&](int first, int buf) {
-    if (threadIdx.x >= 2 * kMoveTokens) return;
-    const int i = first + token;
-    int at = -1;
-    if (i < n) {
-      const int src = kept[i];
-      const bool good = src >= i && src < len;
-      if (!good && tells) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
-      if (good && src != i) {
-        const int tok = dest ? i : src;
-        const unsigned pg = static_cast<unsigned>(tok) / static_cast<unsigned>(c.page_size);
-        int page = -1;
-        if (pg < static_cast<unsigned>(c.table_pages)) page = table[pg];
-        if (page >= 0 && page < c.num_pages)
-          at = page * c.page_size + (tok - static_cast<int>(pg) * c.page_size);
-        else if (tells)
-          atomicOr(p.status, SPECFOLD_DEV_BAD_PAGE);
+#pragma unroll
+    for (int x = threadIdx.x; x < 2 * TOKENS; x += THREADS) {
+      const bool dest = x >= TOKENS;
+      const int token = x % TOKENS, i = first + token;
+      int at = -1;
+      if (i < n) {
+        const int src = kept[i];
+        const bool good = src >= i && src < len;
+        if (!good && tells) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
+        if (good && src != i) {
+          const int tok = dest ? i : src;
+          const unsigned pg = static_cast<unsigned>(tok) / static_cast<unsigned>(c.page_size);
+          int page = -1;
+          if (pg < static_cast<unsigned>(c.table_pages)) page = table[pg];
+          if (page >= 0 && page < c.num_pages)
+            at = page * c.page_size + (tok - static_cast<int>(pg) * c.page_size);
+          else if (tells)
+            atomicOr(p.status, SPECFOLD_DEV_BAD_PAGE);
+        }
       }
+      s_at[buf][dest][token] = at;
     }
-    (dest ? s_to : s_from)[buf][token] = at;
   };
-  const int step = blocks * kMoveTokens;
-  locate(rank * kMoveTokens, 0);
+  const int step = blocks * TOKENS;
+  locate(rank * TOKENS, 0);
   __syncthreads();
   int buf = 0;
-  for (int first = rank * kMoveTokens, round0 = 0; round0 < n; round0 += step, first += step, buf ^= 1) {
-    uint4 v[kMovePieces];
-    int to[kMovePieces];
+  for (int first = rank * TOKENS, round0 = 0; round0 < n; round0 += step, first += step, buf ^= 1) {
+    uint4 v[PIECES];
+    int to[PIECES];
 #pragma unroll
-    for (int k = 0; k < kMovePieces; ++k) {
-      const int t = mine + k * (kMoveThreads / kMoveRow), from = s_from[buf][t];
-      to[k] = from < 0 ? -1 : s_to[buf][t];
+    for (int k = 0; k < PIECES; ++k) {
+      const int t = mine + k * (THREADS / kMoveRow), from = s_at[buf][0][t];
+      to[k] = from < 0 ? -1 : s_at[buf][1][t];
       if (to[k] >= 0) v[k] = pool[from * ts];
     }
-    float moved = 0.f;
-    bool moves = false;
-    if (w && threadIdx.x < kMoveTokens && first + token < n) {
-      const int src = kept[first + token];
-      moves = src > first + token && src < len;
-      if (moves) moved = w[src];
+    float moved[WEIGHTS];
+    bool moves[WEIGHTS];
+#pragma unroll
+    for (int k = 0; k < WEIGHTS; ++k) {
+      const int token = threadIdx.x + k * THREADS, i = first + token;
+      moves[k] = false;
+      if (w && token < TOKENS && i < n) {
+        const int src = kept[i];
+        moves[k] = src > i && src < len;
+        if (moves[k]) moved[k] = w[src];
+      }
     }
     if (round0 + step < n) locate(first + step, buf ^ 1);
     if constexpr (CLUSTER)
@@ -381,9 +390,11 @@ __global__ void __launch_bounds__(kMoveThreads) kv_compact_kernel(const __grid_c
     else
       __syncthreads();
 #pragma unroll
-    for (int k = 0; k < kMovePieces; ++k)
+    for (int k = 0; k < PIECES; ++k)
       if (to[k] >= 0) pool[to[k] * ts] = v[k];
-    if (moves) w[first + token] = moved;
+#pragma unroll
+    for (int k = 0; k < WEIGHTS; ++k)
+      if (moves[k]) w[first + threadIdx.x + k * THREADS] = moved[k];
   }
 }
 
@@ -417,13 +428,13 @@ int launch_kv_compact(const KvCompactCall& c, cudaStream_t st) {
   for (int64_t* x : {&a.cache.k_token_stride, &a.cache.k_head_stride, &a.cache.v_token_stride, &a.cache.v_head_stride})
     *x = *x * e / 16;
   const long long units = 2LL * c.n_seqs * c.n_kv * a.slices;
-  while (a.blocks < 8 && a.blocks * move_tokens(kMoveCluster) < c.kept.cap && units * a.blocks < 5LL * num_sms()) a.blocks *= 2;
+  while (a.blocks < 8 && a.blocks * Move<true>::TOKENS < c.kept.cap && units * a.blocks < 5LL * num_sms()) a.blocks *= 2;
   if (units * a.blocks > 0x7fffffffLL) return SPECFOLD_ECAPACITY;
   const dim3 grid(static_cast<unsigned>(units * a.blocks));
   if (a.blocks > 1)
-    launch_kc(kv_compact_kernel<kMoveCluster, true>, grid, dim3(kMoveCluster), 0, st, a.blocks, a);
+    launch_kc(kv_compact_kernel<true>, grid, dim3(Move<true>::THREADS), 0, st, a.blocks, a);
   else
-    launch_k(kv_compact_kernel<kMoveAlone, false>, grid, dim3(kMoveAlone), 0, st, a);
+    launch_k(kv_compact_kernel<false>, grid, dim3(Move<false>::THREADS), 0, st, a);
   count_launch();
   return check_launch();
 }

@@ -7,6 +7,7 @@
 
 #include <algorithm>
 #include <cmath>
+#include <type_traits>
 
 namespace sf {
 namespace {
@@ -207,9 +208,10 @@ __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel
 }
 
 // ------------------------------------------------------------ fp32: few --
-// The same for fp32 by multiply-adds, a tile of eight rows at a time: a warp's
-// step is 4 KB of keys, a lane (key, 32 of the dimensions), the queries
-// broadcast from shared memory, a key's lanes joined by shuffles.
+// The same for fp32 by multiply-adds, a tile of eight rows at a time (a piece of at
+// most four does no other rows' arithmetic): a warp's step is 4 KB of keys, a lane
+// (key, 32 of the dimensions), the queries broadcast from shared memory; a key's lanes
+// add up by halves, so that each ends with some rows' scores.
 template <int HD>
 struct WSimt {
   static constexpr int R = 8;
@@ -227,7 +229,7 @@ struct WSimt {
 template <int HD>
 __global__ void __launch_bounds__(kThreads, WSimt<HD>::CTAS) weigh_simt_kernel(const __grid_constant__ WeighArgs a) {
   using C = WSimt<HD>;
-  constexpr int R = C::R, CH = C::CH;
+  constexpr int R = C::R, CH = C::CH, PARTS = HD / 32;
   const TreeArgs& p = a.t;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[kWarps * R];
@@ -280,62 +282,83 @@ __global__ void __launch_bounds__(kThreads, WSimt<HD>::CTAS) weigh_simt_kernel(c
       *reinterpret_cast<float4*>(s_q + r * HD + d) = *reinterpret_cast<const float4*>(
           static_cast<const float*>(p.q) + src * p.q_rs + (h * p.g + m % p.g) * p.q_hs + d);
     }
-    int seen[R];
-    float m[R], l[R];
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      seen[r] = w.q.ctx + (m0 + min(r, rows - 1)) / p.g;
-      m[r] = -INFINITY;
-      l[r] = 0.f;
-    }
     __syncthreads();
     const int key = lane & (CH - 1), part = lane / CH;
-    float* out = a.scores + ((static_cast<size_t>(w.s) * p.n_kv + h) * a.w.tokens) * a.score_rows + m0;
-    for (int i = 0; i < mine; ++i) {
-      load(i + C::STAGES - 1, slot);
-      slot = slot_of(i + C::STAGES);
-      cp_async_wait<C::STAGES - 1>();
-      __syncwarp();
-      const uint8_t* sk = ring + (i % C::STAGES) * C::STAGE + key * C::ROW;
-      float s[R] = {};
+    auto stream = [&](auto nr) {
+      constexpr int NR = decltype(nr)::value;  // rows worked on
+      constexpr int RP = NR / PARTS;           // of which a lane has RP's sums, from row part * RP on
+      int seen[RP];
+      float m[RP], l[RP];
 #pragma unroll
-      for (int d = 0; d < 32; d += 4) {
-        const int b = part * 128 + d * 4;
-        const float4 k4 = *reinterpret_cast<const float4*>(sk + (((b >> 4) ^ (key & 7)) << 4));
+      for (int r = 0; r < RP; ++r) {
+        seen[r] = w.q.ctx + (m0 + min(part * RP + r, rows - 1)) / p.g;
+        m[r] = -INFINITY;
+        l[r] = 0.f;
+      }
+      float* out = a.scores + ((static_cast<size_t>(w.s) * p.n_kv + h) * a.w.tokens) * a.score_rows + m0 + part * RP;
+      for (int i = 0; i < mine; ++i) {
+        load(i + C::STAGES - 1, slot);
+        slot = slot_of(i + C::STAGES);
+        cp_async_wait<C::STAGES - 1>();
+        __syncwarp();
+        const uint8_t* sk = ring + (i % C::STAGES) * C::STAGE + key * C::ROW;
+        float s[NR] = {};
 #pragma unroll
-        for (int r = 0; r < R; ++r) {
-          const float4 q4 = *reinterpret_cast<const float4*>(s_q + r * HD + part * 32 + d);
-          s[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[r]))));
+        for (int d0 = 0; d0 < 32; d0 += 4) {
+          // the parts start apart, so that their reads of a query share no bank
+          const int d = part * 32 + ((d0 + part * CH) & 31);
+          const float4 k4 = *reinterpret_cast<const float4*>(sk + (((d >> 2) ^ (key & 7)) << 4));
+#pragma unroll
+          for (int r = 0; r < NR; ++r) {
+            const float4 q4 = *reinterpret_cast<const float4*>(s_q + r * HD + d);
+            s[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[r]))));
+          }
         }
+        // the parts' sums: each step halves the rows that a lane keeps
+#pragma unroll
+        for (int n = NR / 2, o = 16; o >= CH; n /= 2, o /= 2) {
+          const bool upper = lane & o;
+#pragma unroll
+          for (int r = 0; r < n; ++r) {
+            const float keep = upper ? s[n + r] : s[r], give = upper ? s[r] : s[n + r];
+            s[r] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
+        }
+        const int tok = key_of(i) + key;
+        const bool tail = key_of(i) + CH > w.q.ctx;
+#pragma unroll
+        for (int r = 0; r < RP; ++r) {
+          s[r] = tail && tok > seen[r] ? -INFINITY : s[r] * p.sl2;
+          const float top = fmaxf(m[r], s[r]);
+          const float b = top == -INFINITY ? 0.f : top;
+          l[r] = fmaf(l[r], m[r] == top ? 1.f : ex2(m[r] - b), ex2(s[r] - b));
+          m[r] = top;
+        }
+        if (!tail || tok < len) {
+          float* to = out + static_cast<size_t>(tok) * a.score_rows;
+          if constexpr (RP == 4)
+            *reinterpret_cast<float4*>(to) = make_float4(s[0], s[1], s[2], s[3]);
+          else if constexpr (RP == 2)
+            *reinterpret_cast<float2*>(to) = make_float2(s[0], s[1]);
+          else
+            *to = s[0];
+        }
+        __syncwarp();
       }
-      const int tok = key_of(i) + key;
-      const bool tail = key_of(i) + CH > w.q.ctx;
+      cp_async_wait<0>();
 #pragma unroll
-      for (int r = 0; r < R; ++r) {
+      for (int r = 0; r < RP; ++r) {
+        float2 v = make_float2(m[r], l[r]);
 #pragma unroll
-        for (int o = CH; o < 32; o <<= 1) s[r] += __shfl_xor_sync(0xffffffffu, s[r], o);
-        s[r] = tail && tok > seen[r] ? -INFINITY : s[r] * p.sl2;
-        const float top = fmaxf(m[r], s[r]);
-        const float b = top == -INFINITY ? 0.f : top;
-        l[r] = fmaf(l[r], m[r] == top ? 1.f : ex2(m[r] - b), ex2(s[r] - b));
-        m[r] = top;
+        for (int o = 1; o < CH; o <<= 1)
+          v = weigh_merge(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+        if (key == 0) s_ml[warp * R + part * RP + r] = v;
       }
-      if (part < 2 && tok < len) {  // a key's eight scores by two of its lanes
-        const bool up = part == 1;
-        *reinterpret_cast<float4*>(out + static_cast<size_t>(tok) * a.score_rows + 4 * part) =
-            make_float4(up ? s[4] : s[0], up ? s[5] : s[1], up ? s[6] : s[2], up ? s[7] : s[3]);
-      }
-      __syncwarp();
-    }
-    cp_async_wait<0>();
-#pragma unroll
-    for (int r = 0; r < R; ++r) {
-      float2 v = make_float2(m[r], l[r]);
-#pragma unroll
-      for (int o = 1; o < CH; o <<= 1)
-        v = weigh_merge(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
-      if (lane == 0) s_ml[warp * R + r] = v;
-    }
+    };
+    if (rows <= R / 2)
+      stream(std::integral_constant<int, R / 2>{});
+    else
+      stream(std::integral_constant<int, R>{});
     __syncthreads();
     weigh_write_part<R>(a, w, first, s_ml);
   }
@@ -347,7 +370,7 @@ __global__ void __launch_bounds__(kThreads, WSimt<HD>::CTAS) weigh_simt_kernel(c
 // waited for all before it, and reads the same lengths.
 constexpr int kSumThreads = 256, kSumTokens = 4;
 constexpr int kSumCtas = 3;   // per SM
-constexpr int kSumRows = 64;  // of a head group, at most
+constexpr int kSumRows = 512;  // of a head group, at most
 
 __global__ void __launch_bounds__(kSumThreads) weigh_sum_kernel(const __grid_constant__ WeighArgs a) {
   const TreeArgs& p = a.t;
@@ -365,17 +388,21 @@ __global__ void __launch_bounds__(kSumThreads) weigh_sum_kernel(const __grid_con
     const int len = w.q.ctx + w.q.n, key_lo = w.b0 * p.kb;
     const int key_hi = min(static_cast<long long>(len), static_cast<long long>(w.b0 + w.n) * p.kb);
     // the rows' statistics: thread (lane of partials, row)
-    for (int tile = 0; tile * SR < R; ++tile) {
-      const int r = threadIdx.x % SR, z0 = threadIdx.x / SR, zs = kSumThreads / SR;
-      const bool there = tile * SR + r < rows;
-      float2 v = there ? weigh_gather(a, w, tile, r, z0, zs) : make_float2(-INFINITY, 0.f);
-      __syncthreads();  // (the piece before has read m and 1 / l)
-      if (z0 < zs) s_part[z0 * SR + r] = v;
-      __syncthreads();
-      if (threadIdx.x < SR) {
-        for (int z = 1; z < zs; ++z) v = weigh_merge(v, s_part[z * SR + r]);
-        s_m[tile * SR + r] = there ? v.x : INFINITY;
-        s_rl[tile * SR + r] = there ? merge_scale(v.y) : 0.f;
+    const int zs = max(kSumThreads / R, 1);
+    __syncthreads();  // the piece before has read m and 1 / l
+    for (int r0 = 0; r0 < R; r0 += kSumThreads) {
+      const int r = r0 + (zs > 1 ? threadIdx.x % R : threadIdx.x), z0 = zs > 1 ? threadIdx.x / R : 0;
+      float2 v = make_float2(INFINITY, 0.f);  // a row past the last weighs nothing
+      if (r < rows && z0 < zs) v = weigh_gather(a, w, r / SR, r % SR, z0, zs);
+      if (zs > 1) {
+        s_part[threadIdx.x] = v;
+        __syncthreads();
+        if (z0 == 0 && r < rows)
+          for (int z = 1; z < zs; ++z) v = weigh_merge(v, s_part[z * R + r]);
+      }
+      if (r < R && z0 == 0) {
+        s_m[r] = v.x;
+        s_rl[r] = merge_scale(v.y);
       }
     }
     __syncthreads();
@@ -394,7 +421,8 @@ __global__ void __launch_bounds__(kSumThreads) weigh_sum_kernel(const __grid_con
         for (int k = 0; k < kSumTokens; ++k) {
           const float4* at = reinterpret_cast<const float4*>(x + static_cast<size_t>(min(t0 + k * kSumThreads, key_hi - 1)) * R + r);
           u[k] = at[0];
-          v[k] = at[1];
+          // (the scores of a tile of at most four rows are four: the others hold leftovers)
+          v[k] = r + 4 < rows ? at[1] : make_float4(0.f, 0.f, 0.f, 0.f);
         }
         const float4 m0 = *reinterpret_cast<const float4*>(s_m + r), m1 = *reinterpret_cast<const float4*>(s_m + r + 4);
         const float4 l0 = *reinterpret_cast<const float4*>(s_rl + r), l1 = *reinterpret_cast<const float4*>(s_rl + r + 4);

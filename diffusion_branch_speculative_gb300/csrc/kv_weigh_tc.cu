@@ -104,20 +104,31 @@ struct KeyLoader {
   }
 };
 
-// A tile's queries by 64 threads (tid 0 .. 63): `most` rows from m0 on, those past
-// the last the copies of it.
-template <int HD>
+// A tile's queries by THREADS threads (tid 0 ..): `most` rows from m0 on, those past
+// the last the copies of it (zeros times an infinite key would be NaN).  Returns with
+// this thread's part visible to the tensor cores.
+template <int HD, int THREADS>
 SF_DEV void gather_rows(const WeighArgs& a, const TreeWalk& w, int m0, int rows, int most, uint8_t* smem, int tid) {
-  constexpr int CPR = HD / 8, RSTEP = 64 / CPR;
+  constexpr int CPR = HD / 8, RSTEP = THREADS / CPR;  // rows of one step; a row's node and head follow by steps
   const TreeArgs& p = a.t;
-  const int c = tid % CPR, g = p.g;
-  const uint32_t q0 = smem_u32(smem) + (c >> 3) * WTc<HD>::Q_ATOM;
+  const int c = tid % CPR, g = p.g, dn = RSTEP / g, dj = RSTEP % g;
+  const uint32_t at = smem_u32(smem) + (c >> 3) * WTc<HD>::Q_ATOM;
+  const __nv_bfloat16* q = static_cast<const __nv_bfloat16*>(p.q) + w.head * g * p.q_hs + c * 8;
+  auto from = [&](int node, int j) {
+    const int t = w.q.row0 + node;
+    return q + (a.rows ? max(weigh_src(a, t), 0) : t) * p.q_rs + j * p.q_hs;
+  };
+  const __nv_bfloat16* last = from((m0 + rows - 1) / g, (m0 + rows - 1) % g);
+  int node = (m0 + tid / CPR) / g, j = (m0 + tid / CPR) - node * g;
 #pragma unroll 4
   for (int r = tid / CPR; r < most; r += RSTEP) {
-    const int m = m0 + min(r, rows - 1), node = m / g, j = m - node * g;
-    const int src = max(weigh_src(a, w.q.row0 + node), 0);
-    cp_async16(q0 + r * 128 + (((c & 7) ^ (r & 7)) << 4),
-               static_cast<const __nv_bfloat16*>(p.q) + src * p.q_rs + (w.head * g + j) * p.q_hs + c * 8, 16u);
+    cp_async16(at + r * 128 + (((c & 7) ^ (r & 7)) << 4), r < rows ? from(node, j) : last, 16u);
+    node += dn;
+    j += dj;
+    if (j >= g) {
+      j -= g;
+      ++node;
+    }
   }
   cp_async_commit();
   cp_async_wait<0>();
@@ -174,7 +185,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_stats_tc_kernel(const __g
       mbar_init(smem_u32(&full[i]), 1);
       mbar_init(smem_u32(&empty[i]), 2);
     }
-    mbar_init(smem_u32(q_full), 2);   // the gathering warps
+    mbar_init(smem_u32(q_full), 2);   // the gathering warps, or the lanes
     mbar_init(smem_u32(q_empty), 2);  // the lanes
     for (int i = 0; i < 4; ++i) {
       mbar_init(smem_u32(&s_full[i]), 1);
@@ -208,13 +219,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_stats_tc_kernel(const __g
     }
     keys.drain(full, abort_flag);
   } else if (warp == 1 || warp == 3) {
-    for (int j = 0; w.n > 0; w.next(p), ++j) {
+    w.next(p);  // the first unit's come from the reducing warps, idle then
+    for (int j = 1; w.n > 0; w.next(p), ++j) {
       bool ok = true;
-      if (lane == 0 && j > 0)
+      if (lane == 0)
         ok = mbar_wait(smem_u32(q_empty), (j - 1) & 1, abort_flag, p.status, kWaitLimitNs, kSiteAttnQEmpty);
       if (!__shfl_sync(0xffffffffu, ok, 0)) break;
       const int rows = tree_tile_rows(p, w);
-      gather_rows<HD>(a, w, tree_m0(p, w), rows, rows > 128 ? 256 : 128, smem, (warp >> 1) * 32 + lane);
+      gather_rows<HD, 64>(a, w, tree_m0(p, w), rows, rows > 128 ? 256 : 128, smem, (warp >> 1) * 32 + lane);
       __syncwarp();
       if (lane == 0) mbar_arrive(smem_u32(q_full));
     }
@@ -258,6 +270,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_stats_tc_kernel(const __g
     const int pair_bar = 2 + (warp & 3);
     const bool leader = (warp & 3) == 0 && lane == 0;
     int cnt = 0, it = 0, j = 0;
+    gather_rows<HD, 256>(a, w, tree_m0(p, w), tree_tile_rows(p, w), tree_tile_rows(p, w) > 128 ? 256 : 128, smem,
+                         threadIdx.x - 128);
+    named_bar_sync(1, 256);
+    if (leader) mbar_arrive(smem_u32(q_full));
     bool ok = true;
     for (bool first = true; w.n > 0 && ok; first = false, w.next(p), ++j) {
       if (warp == 4 && lane == 0 && w.b0 == 0) weigh_note_span(a, w, first, per);
@@ -410,14 +426,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
   }
   TreeWalk w;
   unsigned per;
-  const bool work = tree_locate(p, w, per);  // before the wait: the first launch has waited for all before it
-  pdl_wait();
+  // Of what this kernel reads the first launch, which has waited for all before it, writes the
+  // statistics alone: only the warps that read them wait for it.
+  const bool work = tree_locate(p, w, per);
   pdl_trigger();
   tc_fence_before();
   __syncthreads();
   tc_fence_after();
   const uint32_t tmem = tmem_slot_s;
   if (!work) {
+    pdl_wait();
     if (warp == 3) tmem_dealloc(tmem, 512);
     return;
   }
@@ -432,22 +450,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
     keys.drain(full, abort_flag);
   } else if (warp == 1 || warp == 3) {
     bool ok = true;
-    int ql = 0;  // tiles gathered so far
+    int ql = 0;  // tiles gathered so far; the first by the reducing warps
     for (; w.n > 0 && ok; w.next(p)) {
       WItems q(w.n, tiles_of(), C::RING);
       bool fresh = true;
       while (q.g0 < q.n) {
-        if (fresh) {
-          if (lane == 0 && ql > 0)
+        if (fresh && ql > 0) {
+          if (lane == 0)
             ok = mbar_wait(smem_u32(q_empty), (ql - 1) & 1, abort_flag, p.status, kWaitLimitNs, kSiteAttnQEmpty);
           ok = __shfl_sync(0xffffffffu, ok, 0);
           if (!ok) break;
           const int rows = rows_of(q.tile_at);
-          gather_rows<HD>(a, w, q.tile_at * kWeighTcRows, rows, (rows + 31) & ~31, smem, (warp >> 1) * 32 + lane);
+          gather_rows<HD, 64>(a, w, q.tile_at * kWeighTcRows, rows, (rows + 31) & ~31, smem, (warp >> 1) * 32 + lane);
           __syncwarp();
           if (lane == 0) mbar_arrive(smem_u32(q_full));
-          ++ql;
         }
+        if (fresh) ++ql;
         fresh = q.next();
       }
     }
@@ -496,6 +514,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
     const bool leader = warp == 4 && lane == 0;
     int it = 0, cnt = 0, ql = 0, outs = 0;
+    gather_rows<HD, 256>(a, w, 0, rows_of(0), (rows_of(0) + 31) & ~31, smem, tid);
+    named_bar_sync(1, 256);
+    if (lane == 0 && (warp & 3) == 0) mbar_arrive(smem_u32(q_full));
+    pdl_wait();
     bool ok = true;
     for (; w.n > 0 && ok; w.next(p)) {
       const int ctx = w.q.ctx, len = ctx + w.q.n;
