@@ -1,8 +1,8 @@
 // The attention weight that cached tokens get from a batch of rows, added up per
 // key/value head (specfold_kv_weigh): what an eviction goes by.  Keys alone are
 // read.  kv_weigh.cuh has the two launches' division of work; here are the forms
-// whose first launch keeps the scores (few rows a head group) and the fp32 form
-// that does not.  kv_weigh_tc.cu has many rows.
+// whose first launch keeps the scores: few rows a head group, and fp32.
+// kv_weigh_tc.cu has many rows in bf16.
 #include "kv_weigh.cuh"
 
 #include <algorithm>
@@ -79,17 +79,31 @@ __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel
     const int chunks = (key_hi - key_lo + CH - 1) / CH;
     const int mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
     auto key_of = [&](int i) { return key_lo + CH * (warp + kWarps * i); };
-    // lanes 0..CH-1 have a chunk's keys: their pages are read two chunks ahead of use
+    // lanes 0..CH-1 have a chunk's keys; a chunk's pages are read two chunks ahead of its
+    // loads, and followed by steps (no division a chunk)
     const int32_t* table = p.cache.block_table + w.s * p.cache.table_stride;
-    const unsigned ps = p.cache.page_size;
-    auto page_of = [&](int i) {
-      const unsigned tok = key_of(i) + (lane & (CH - 1)), pg = tok / ps;
-      return i < mine && static_cast<int>(tok) < key_hi && pg < static_cast<unsigned>(p.cache.table_pages) ? table[pg] : -1;
+    const int ps = p.cache.page_size, dpg = CH * kWarps / ps, doff = CH * kWarps - dpg * ps;
+    struct Page {
+      int id, off;  // in the table; a key's place in it, -1: no key
     };
-    auto slot_of = [&](int i, int page) {
-      const unsigned tok = key_of(i) + (lane & (CH - 1));
-      if (page >= 0 && page < p.cache.num_pages) return page * static_cast<int>(ps) + static_cast<int>(tok % ps);
-      if (i < mine && static_cast<int>(tok) < key_hi) atomicOr(p.status, SPECFOLD_DEV_BAD_PAGE);
+    const unsigned tok0 = static_cast<unsigned>(key_lo) + CH * warp + (lane & (CH - 1));
+    int pg = tok0 / static_cast<unsigned>(ps), off = tok0 - pg * ps;
+    int left = key_hi > static_cast<int>(tok0) ? (key_hi - static_cast<int>(tok0) + CH * kWarps - 1) / (CH * kWarps) : 0;  // this lane's keys
+    auto page_next = [&]() {
+      Page x = {-1, left > 0 ? off : -1};
+      if (left > 0 && pg < p.cache.table_pages) x.id = table[pg];
+      --left;
+      pg += dpg;
+      off += doff;
+      if (off >= ps) {
+        off -= ps;
+        ++pg;
+      }
+      return x;
+    };
+    auto slot_of = [&](Page x) {
+      if (x.id >= 0 && x.id < p.cache.num_pages) return x.id * ps + x.off;
+      if (x.off >= 0) atomicOr(p.status, SPECFOLD_DEV_BAD_PAGE);
       return -1;
     };
     const T* kbase = static_cast<const T*>(p.cache.k) + h * p.cache.k_head_stride;
@@ -109,12 +123,12 @@ __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel
       }
       cp_async_commit();
     };
-    int page = page_of(0), next = page_of(1);
+    Page page = page_next(), next = page_next();
 #pragma unroll
     for (int i = 0; i < C::STAGES - 1; ++i) {
-      load(i, slot_of(i, page));
+      load(i, slot_of(page));
       page = next;
-      next = page_of(i + 2);
+      next = page_next();
     }
     // queries: row m = row m / g of the sequence, head m % g of the group; the rows
     // past the last are its copies (zeros times an infinite key would be NaN)
@@ -148,9 +162,9 @@ __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel
       }
     float* out = a.scores + ((static_cast<size_t>(w.s) * p.n_kv + h) * a.w.tokens) * R + (lane & 3) * 2;
     for (int i = 0; i < mine; ++i) {
-      load(i + C::STAGES - 1, slot_of(i + C::STAGES - 1, page));
+      load(i + C::STAGES - 1, slot_of(page));
       page = next;
-      next = page_of(i + C::STAGES + 1);
+      next = page_next();
       cp_async_wait<C::STAGES - 1>();
       __syncwarp();
       const uint8_t* stg = ring + (i % C::STAGES) * C::STAGE;
@@ -365,14 +379,16 @@ __global__ void __launch_bounds__(kThreads, WSimt<HD>::CTAS) weigh_simt_kernel(c
 }
 
 // ------------------------------------------------- weights from the scores --
-// A thread a token, kSumTokens of them at once: the scores' 2^(x - m) / l, eight rows
-// at a time.  The run is found before the wait for the first launch: that one
-// waited for all before it, and reads the same lengths.
-constexpr int kSumThreads = 256, kSumTokens = 4;
-constexpr int kSumCtas = 3;   // per SM
-constexpr int kSumRows = 512;  // of a head group, at most
+// Two threads a token, kSumTokens of them at once: the scores' 2^(x - m) / l, eight rows
+// at a time, four a thread: a warp's read is 32 bytes a token.  The run is found
+// before the wait for the first launch: that one waited for all before it, and reads
+// the same lengths.  A piece's first scores are on their way while its rows' statistics
+// are merged.  More rows than kSumRows come in groups, which add to the weights in turn.
+constexpr int kSumThreads = 256, kSumTokens = 8;
+constexpr int kSumCtas = 3;    // per SM
+constexpr int kSumRows = 512;  // of a group
 
-__global__ void __launch_bounds__(kSumThreads) weigh_sum_kernel(const __grid_constant__ WeighArgs a) {
+__global__ void __launch_bounds__(kSumThreads, kSumCtas) weigh_sum_kernel(const __grid_constant__ WeighArgs a) {
   const TreeArgs& p = a.t;
   __shared__ float2 s_part[kSumThreads];
   __shared__ __align__(16) float s_m[kSumRows], s_rl[kSumRows];
@@ -382,157 +398,78 @@ __global__ void __launch_bounds__(kSumThreads) weigh_sum_kernel(const __grid_con
   pdl_wait();
   pdl_trigger();
   if (!work) return;
-  const int SR = a.stat_rows, R = a.score_rows;
+  const int SR = a.stat_rows, R = a.score_rows, half = threadIdx.x & 1;
   for (; w.n > 0; w.next(p)) {
-    const int h = w.head, rows = w.q.n * p.g;
-    const int len = w.q.ctx + w.q.n, key_lo = w.b0 * p.kb;
+    const int rows = w.q.n * p.g, len = w.q.ctx + w.q.n, key_lo = w.b0 * p.kb;
     const int key_hi = min(static_cast<long long>(len), static_cast<long long>(w.b0 + w.n) * p.kb);
-    // the rows' statistics: thread (lane of partials, row)
-    const int zs = max(kSumThreads / R, 1);
-    __syncthreads();  // the piece before has read m and 1 / l
-    for (int r0 = 0; r0 < R; r0 += kSumThreads) {
-      const int r = r0 + (zs > 1 ? threadIdx.x % R : threadIdx.x), z0 = zs > 1 ? threadIdx.x / R : 0;
-      float2 v = make_float2(INFINITY, 0.f);  // a row past the last weighs nothing
-      if (r < rows && z0 < zs) v = weigh_gather(a, w, r / SR, r % SR, z0, zs);
-      if (zs > 1) {
-        s_part[threadIdx.x] = v;
-        __syncthreads();
-        if (z0 == 0 && r < rows)
-          for (int z = 1; z < zs; ++z) v = weigh_merge(v, s_part[z * R + r]);
-      }
-      if (r < R && z0 == 0) {
-        s_m[r] = v.x;
-        s_rl[r] = merge_scale(v.y);
-      }
-    }
-    __syncthreads();
-    const float* x = a.scores + (static_cast<size_t>(w.s) * p.n_kv + h) * a.w.tokens * R;
-    float* wt = a.w.ptr + w.s * a.w.seq_stride + h * a.w.head_stride;
-    for (int t0 = key_lo + threadIdx.x; t0 < key_hi; t0 += kSumThreads * kSumTokens) {
-      float sum[kSumTokens] = {}, old[kSumTokens];
+    const size_t unit = static_cast<size_t>(w.s) * p.n_kv + w.head;
+    const float* x = a.scores + unit * a.w.tokens * R + 4 * half;
+    float* wt = a.w.ptr + w.s * a.w.seq_stride + w.head * a.w.head_stride;
+    auto token = [&](int t0, int k) { return t0 + static_cast<int>(threadIdx.x >> 1) + k * (kSumThreads / 2); };
+    auto load = [&](int t0, int r, float4 (&u)[kSumTokens]) {  // (a tile of at most four rows has four scores: the others are leftovers)
 #pragma unroll
-      for (int k = 0; k < kSumTokens; ++k) {
-        const int t = t0 + k * kSumThreads;
-        old[k] = t < key_hi && t < w.q.ctx && a.decay != 0.f ? wt[t] : 0.f;
+      for (int k = 0; k < kSumTokens; ++k)
+        u[k] = token(t0, k) < key_hi && r + 4 * half < rows
+                   ? *reinterpret_cast<const float4*>(x + static_cast<size_t>(token(t0, k)) * R + r)
+                   : make_float4(0.f, 0.f, 0.f, 0.f);
+    };
+    for (int lo = 0; lo < rows; lo += kSumRows) {  // rows lo .. hi - 1
+      const int hi = min(lo + kSumRows, rows), r8 = (hi - lo + 7) & ~7;
+      float4 u[kSumTokens];
+      load(key_lo, lo, u);
+      // their m and 1 / l: thread (lane of partials, row)
+      const int zs = max(kSumThreads / r8, 1);
+      __syncthreads();  // the group before has read them
+      for (int r0 = 0; r0 < r8; r0 += kSumThreads) {
+        const int i = r0 + (zs > 1 ? threadIdx.x % r8 : threadIdx.x), z0 = zs > 1 ? threadIdx.x / r8 : 0, r = lo + i;
+        float2 ml = make_float2(INFINITY, 0.f);  // a row past the last weighs nothing
+        if (r < hi && z0 < zs)
+          ml = weigh_gather(a, unit * a.stat_tiles + r / SR, weigh_row_ml(a, w.q.row0, w.head, r), r % SR, z0, zs);
+        if (zs > 1) {
+          s_part[threadIdx.x] = ml;
+          __syncthreads();
+          if (z0 == 0 && r < hi)
+            for (int z = 1; z < zs; ++z) ml = weigh_merge(ml, s_part[z * r8 + i]);
+        }
+        if (i < r8 && z0 == 0) {
+          s_m[i] = ml.x;
+          s_rl[i] = merge_scale(ml.y);
+        }
       }
-      for (int r = 0; r < rows; r += 8) {
-        float4 u[kSumTokens], v[kSumTokens];
+      __syncthreads();
+      // old weights count times decay, those of the groups before once, the batch's own tokens' not at all
+      const int olds = lo > 0 ? key_hi : a.decay != 0.f ? min(key_hi, w.q.ctx) : 0;
+      const float factor = lo > 0 ? 1.f : a.decay;
+      for (int t0 = key_lo; t0 < key_hi; t0 += kSumThreads / 2 * kSumTokens) {
+        float sum[kSumTokens] = {}, old[kSumTokens];
+        if (t0 > key_lo) load(t0, lo, u);
+#pragma unroll
+        for (int k = 0; k < kSumTokens; ++k)  // every second token's weight is this thread's
+          old[k] = (k & 1) == half && token(t0, k) < olds ? wt[token(t0, k)] : 0.f;
+        for (int i = 0;; load(t0, lo + i, u)) {
+          const float4 m = *reinterpret_cast<const float4*>(s_m + i + 4 * half);
+          const float4 rl = *reinterpret_cast<const float4*>(s_rl + i + 4 * half);
+#pragma unroll
+          for (int k = 0; k < kSumTokens; ++k) {
+            sum[k] = fmaf(ex2(u[k].x - m.x), rl.x, sum[k]);
+            sum[k] = fmaf(ex2(u[k].y - m.y), rl.y, sum[k]);
+            sum[k] = fmaf(ex2(u[k].z - m.z), rl.z, sum[k]);
+            sum[k] = fmaf(ex2(u[k].w - m.w), rl.w, sum[k]);
+          }
+          if ((i += 8) >= hi - lo) break;
+        }
 #pragma unroll
         for (int k = 0; k < kSumTokens; ++k) {
-          const float4* at = reinterpret_cast<const float4*>(x + static_cast<size_t>(min(t0 + k * kSumThreads, key_hi - 1)) * R + r);
-          u[k] = at[0];
-          // (the scores of a tile of at most four rows are four: the others hold leftovers)
-          v[k] = r + 4 < rows ? at[1] : make_float4(0.f, 0.f, 0.f, 0.f);
+          const float both = sum[k] + __shfl_xor_sync(0xffffffffu, sum[k], 1);
+          if ((k & 1) == half && token(t0, k) < key_hi) wt[token(t0, k)] = fmaf(factor, old[k], both);
         }
-        const float4 m0 = *reinterpret_cast<const float4*>(s_m + r), m1 = *reinterpret_cast<const float4*>(s_m + r + 4);
-        const float4 l0 = *reinterpret_cast<const float4*>(s_rl + r), l1 = *reinterpret_cast<const float4*>(s_rl + r + 4);
-#pragma unroll
-        for (int k = 0; k < kSumTokens; ++k) {
-          sum[k] = fmaf(ex2(u[k].x - m0.x), l0.x, sum[k]);
-          sum[k] = fmaf(ex2(u[k].y - m0.y), l0.y, sum[k]);
-          sum[k] = fmaf(ex2(u[k].z - m0.z), l0.z, sum[k]);
-          sum[k] = fmaf(ex2(u[k].w - m0.w), l0.w, sum[k]);
-          sum[k] = fmaf(ex2(v[k].x - m1.x), l1.x, sum[k]);
-          sum[k] = fmaf(ex2(v[k].y - m1.y), l1.y, sum[k]);
-          sum[k] = fmaf(ex2(v[k].z - m1.z), l1.z, sum[k]);
-          sum[k] = fmaf(ex2(v[k].w - m1.w), l1.w, sum[k]);
-        }
-      }
-#pragma unroll
-      for (int k = 0; k < kSumTokens; ++k) {
-        const int t = t0 + k * kSumThreads;
-        if (t < key_hi) wt[t] = fmaf(a.decay, old[k], sum[k]);
       }
     }
   }
-}
-
-// ------------------------------------------- fp32, more rows: no scores kept --
-// One block a row and query head, then one thread a token: right for any number of
-// rows, and bound by the products on the CUDA cores.
-template <int HD>
-SF_DEV float dot_row(const float* k, const float* q) {
-  float a = 0.f;
-#pragma unroll 8
-  for (int d = 0; d < HD; d += 4) {
-    const float4 x = *reinterpret_cast<const float4*>(k + d), y = *reinterpret_cast<const float4*>(q + d);
-    a = fmaf(x.x, y.x, fmaf(x.y, y.y, fmaf(x.z, y.z, fmaf(x.w, y.w, a))));
-  }
-  return a;
-}
-
-template <int HD>
-__global__ void __launch_bounds__(kThreads) weigh_rows_kernel(const __grid_constant__ WeighArgs a) {
-  const TreeArgs& p = a.t;
-  __shared__ __align__(16) float s_q[HD];
-  __shared__ float2 s_ml[kThreads];
-  pdl_wait();
-  pdl_trigger();
-  const int t = blockIdx.x;
-  int s = 0;
-  while (s < p.batch.n_seqs && !(p.batch.row_start[s] <= t && t < p.batch.row_start[s + 1])) ++s;
-  if (s == p.batch.n_seqs) return;
-  const TreeSeq q = tree_seq(p, s);
-  if (q.n == 0) return;
-  const int src = weigh_src(a, t);
-  const int len = q.ctx + (t - q.row0) + 1;
-  for (int hq = blockIdx.y; hq < p.n_kv * p.g; hq += gridDim.y) {
-  const int h = hq / p.g;
-  __syncthreads();
-  for (int d = threadIdx.x; d < HD; d += kThreads)
-    s_q[d] = static_cast<const float*>(p.q)[max(src, 0) * p.q_rs + hq * p.q_hs + d];
-  __syncthreads();
-  float m = -INFINITY, l = 0.f;
-  for (int k = threadIdx.x; k < len; k += kThreads) {
-    const int slot = tree_pool_token(p, s, k);
-    float x = 0.f;
-    if (slot >= 0)
-      x = dot_row<HD>(static_cast<const float*>(p.cache.k) + slot * p.cache.k_token_stride + h * p.cache.k_head_stride, s_q) *
-          p.sl2;
-    const float top = fmaxf(m, x), b = top == -INFINITY ? 0.f : top;
-    l = fmaf(l, m == top ? 1.f : ex2(m - b), ex2(x - b));
-    m = top;
-  }
-  s_ml[threadIdx.x] = make_float2(m, l);
-  __syncthreads();
-  if (threadIdx.x == 0) {
-    float2 v = s_ml[0];
-    for (int i = 1; i < kThreads; ++i) v = weigh_merge(v, s_ml[i]);
-    a.row_ml[static_cast<size_t>(t) * p.n_kv * p.g + hq] = src < 0 ? make_float2(INFINITY, 0.f) : make_float2(v.x, merge_scale(v.y));
-  }
-  }
-}
-
-template <int HD>
-__global__ void __launch_bounds__(kThreads) weigh_tokens_kernel(const __grid_constant__ WeighArgs a) {
-  const TreeArgs& p = a.t;
-  pdl_wait();
-  pdl_trigger();
-  const int s = blockIdx.y;
-  const TreeSeq q = tree_seq(p, s);
-  if (q.bad && blockIdx.x == 0 && blockIdx.z == 0 && threadIdx.x == 0) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
-  const int len = q.n > 0 ? q.ctx + q.n : 0;
-  for (int h = blockIdx.z; h < p.n_kv; h += gridDim.z)
-    for (int k = blockIdx.x * kThreads + threadIdx.x; k < len; k += gridDim.x * kThreads) {
-      const int slot = tree_pool_token(p, s, k);
-      const float* kp = static_cast<const float*>(p.cache.k) + max(slot, 0) * p.cache.k_token_stride + h * p.cache.k_head_stride;
-      float sum = 0.f;
-      for (int i = max(0, k - q.ctx); i < q.n; ++i) {
-        const int src = max(weigh_src(a, q.row0 + i), 0);
-        for (int j = 0; j < p.g; ++j) {
-          const int hq = h * p.g + j;
-          const float2 ml = a.row_ml[static_cast<size_t>(q.row0 + i) * p.n_kv * p.g + hq];
-          const float x = slot < 0 ? 0.f : dot_row<HD>(static_cast<const float*>(p.q) + src * p.q_rs + hq * p.q_hs, kp) * p.sl2;
-          sum = fmaf(ex2(x - ml.x), ml.y, sum);
-        }
-      }
-      float* wt = a.w.ptr + s * a.w.seq_stride + h * a.w.head_stride + k;
-      *wt = k < q.ctx && a.decay != 0.f ? fmaf(a.decay, *wt, sum) : sum;
-    }
 }
 
 // --------------------------------------------------------------- launches --
-enum WeighForm { kFew, kSimt, kRows, kTc };
+enum WeighForm { kFew, kSimt, kTc };
 struct WeighPlan {
   WeighForm form;
   int stat_rows, stat_tiles;  // of the first launch
@@ -542,7 +479,18 @@ struct WeighPlan {
 };
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Few rows keep their scores, as long as these take a workspace of at most 1 GB.
+// Few rows keep their scores, as long as these take a workspace of at most 1 GB: up to 16
+// of a head group in bf16, where keeping them and computing them twice on the tensor
+// cores measure (us; 8 key/value heads, groups of 4):
+//   sequences x tokens       32 x 8000       1 x 40000     8 x 500
+//   head size 128, 8 rows     86.5  121.1                  11.6  15.2
+//                  16 rows   104.5  121.1    29.5  35.9    12.0  15.2
+//                  24 rows   133.5  121.1
+//                  32 rows   167.8  121.2    50.2  36.0    14.8  15.2
+//   head size 64,  8 rows     58.5   85.2
+//                  16 rows    74.5   85.3
+//                  32 rows   131.7   85.4
+// fp32 keeps them always: it would be bound by computing them twice.
 WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int n_seqs, int tokens) {
   const int rows = max_rows * (n_q / n_kv), r8 = (rows + 7) / 8 * 8;
   WeighPlan pl{};
@@ -550,7 +498,7 @@ WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int
   const size_t scores = static_cast<size_t>(n_seqs) * n_kv * tokens * r8 * sizeof(float);
   const bool keeps = scores <= (size_t{1} << 30);
   if (dtype == SPECFOLD_BF16) {
-    if (keeps && rows <= 32) {
+    if (keeps && rows <= 16) {
       pl.form = kFew;
       pl.stat_rows = r8;
       pl.ctas_per_sm = WFew<128, 1>::CTAS;
@@ -559,15 +507,12 @@ WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int
       pl.stat_rows = kWeighTcRows;
       pl.ctas_per_sm = 1;
     }
-  } else if (keeps && rows <= kSumRows) {
+  } else {
     pl.form = kSimt;
     pl.stat_rows = 8;
     pl.ctas_per_sm = WSimt<128>::CTAS;
-  } else {
-    pl.form = kRows;
   }
   pl.row_ml = up256(static_cast<size_t>(T) * n_q * sizeof(float2));
-  if (pl.form == kRows) return pl;
   pl.stat_tiles = (rows + pl.stat_rows - 1) / pl.stat_rows;
   pl.part = up256(2 * static_cast<size_t>(kSmBudget) * pl.ctas_per_sm * pl.stat_rows * sizeof(float2));
   pl.span = up256(static_cast<size_t>(n_seqs) * n_kv * pl.stat_tiles * sizeof(int4));
@@ -581,16 +526,6 @@ int start(void (*kernel)(WeighArgs), const WeighArgs& a, int grid, int threads, 
   launch_k(kernel, dim3(grid), dim3(threads), smem, st, a);
   count_launch();
   return check_launch();
-}
-
-template <int HD>
-int few_go(const WeighArgs& a, int grid, cudaStream_t st) {
-  switch (a.stat_rows / 8) {
-    case 1: return start(weigh_few_kernel<HD, 1>, a, grid, kThreads, WFew<HD, 1>::SMEM, st);
-    case 2: return start(weigh_few_kernel<HD, 2>, a, grid, kThreads, WFew<HD, 2>::SMEM, st);
-    case 3: return start(weigh_few_kernel<HD, 3>, a, grid, kThreads, WFew<HD, 3>::SMEM, st);
-    default: return start(weigh_few_kernel<HD, 4>, a, grid, kThreads, WFew<HD, 4>::SMEM, st);
-  }
 }
 
 template <int HD>
@@ -626,20 +561,11 @@ int weigh_go(const KvWeighCall& c, cudaStream_t st) {
   if (pl.form == kTc) return launch_weigh_tc(a, HD, grid, st);
   t.tile_rows = pl.stat_rows;
   t.kb = kKeys;
-  t.unit_cost = 2;
-  if (pl.form == kRows) {
-    t.tile_rows = SPECFOLD_MAX_TREE * 128;
-    launch_k(weigh_rows_kernel<HD>, dim3(c.batch.T, std::min(c.n_q, 65535)), dim3(kThreads), 0, st, a);
-    count_launch();
-    if (const int rc = check_launch()) return rc;
-    launch_k(weigh_tokens_kernel<HD>, dim3(std::min((c.w.tokens - 1) / kThreads + 1, 64), c.batch.n_seqs, std::min(c.n_kv, 65535)),
-             dim3(kThreads), 0, st, a);
-    count_launch();
-    return check_launch();
-  }
-  if (const int rc = pl.form == kFew ? few_go<HD>(a, grid, st)
-                                     : start(weigh_simt_kernel<HD>, a, grid, kThreads, WSimt<HD>::SMEM, st))
-    return rc;
+  t.unit_cost = 4;
+  const int rc = pl.form == kSimt       ? start(weigh_simt_kernel<HD>, a, grid, kThreads, WSimt<HD>::SMEM, st)
+                 : pl.stat_rows == 8 ? start(weigh_few_kernel<HD, 1>, a, grid, kThreads, WFew<HD, 1>::SMEM, st)
+                                     : start(weigh_few_kernel<HD, 2>, a, grid, kThreads, WFew<HD, 2>::SMEM, st);
+  if (rc) return rc;
   t.tile_rows = SPECFOLD_MAX_TREE * 128;  // all of a head group's rows
   return start(weigh_sum_kernel, a, num_sms() * kSumCtas, kSumThreads, 0, st);
 }

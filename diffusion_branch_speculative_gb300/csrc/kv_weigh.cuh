@@ -52,9 +52,9 @@ SF_DEV void weigh_note_span(const WeighArgs& p, const TreeWalk& w, bool first, u
   p.span[weigh_unit(p, w, w.tile)] = make_int4(c, last, w.whole() ? -1 : tree_slot(first), 0);
 }
 
-// Where row m of the current head's group has its own.
-SF_DEV float2* weigh_row_ml(const WeighArgs& p, const TreeWalk& w, int m) {
-  return p.row_ml + static_cast<size_t>(w.q.row0 + m / p.t.g) * (p.t.n_kv * p.t.g) + w.head * p.t.g + m % p.t.g;
+// Where row m of a head's group has its own.
+SF_DEV float2* weigh_row_ml(const WeighArgs& p, int row0, int head, int m) {
+  return p.row_ml + static_cast<size_t>(row0 + m / p.t.g) * (p.t.n_kv * p.t.g) + head * p.t.g + m % p.t.g;
 }
 // Row r of the current piece's tile: whole or partial.
 SF_DEV void weigh_leave(const WeighArgs& p, const TreeWalk& w, bool first, int r, float2 v) {
@@ -62,7 +62,7 @@ SF_DEV void weigh_leave(const WeighArgs& p, const TreeWalk& w, bool first, int r
   if (r >= tree_tile_rows(p.t, w)) return;
   if (weigh_src(p, w.q.row0 + m / p.t.g) < 0) v = make_float2(INFINITY, 0.f);  // weighs nothing: 2^(x - inf) = 0
   if (w.whole())
-    *weigh_row_ml(p, w, m) = v;
+    *weigh_row_ml(p, w.q.row0, w.head, m) = v;
   else
     p.part[static_cast<size_t>(tree_slot(first)) * p.stat_rows + r] = v;
 }
@@ -73,12 +73,12 @@ SF_DEV float2 weigh_merge(float2 a, float2 b) {
   return make_float2(M, fmaf(merge_weight(a.x, M), a.y, merge_weight(b.x, M) * b.y));
 }
 
-// This thread's merge of row r of the current head's tile `tile` (< its rows): the
-// partials z0, z0 + zs, ... of them.
-SF_DEV float2 weigh_gather(const WeighArgs& p, const TreeWalk& w, int tile, int r, int z0, int zs) {
-  const int4 sp = p.span[weigh_unit(p, w, tile)];
+// This thread's merge of a row, the r-th of the unit's tile: the partials z0, z0 + zs, ...;
+// whole: where it has its own if the unit was not cut.
+SF_DEV float2 weigh_gather(const WeighArgs& p, size_t unit, const float2* whole, int r, int z0, int zs) {
+  const int4 sp = p.span[unit];
   float2 v = make_float2(-INFINITY, 0.f);
-  if (sp.z < 0) return z0 == 0 ? *weigh_row_ml(p, w, tile * p.stat_rows + r) : v;
+  if (sp.z < 0) return z0 == 0 ? *whole : v;
 #pragma unroll 4
   for (int z = sp.x + z0; z <= sp.y; z += zs)
     v = weigh_merge(v, p.part[static_cast<size_t>(z == sp.x ? sp.z : 2 * z) * p.stat_rows + r]);

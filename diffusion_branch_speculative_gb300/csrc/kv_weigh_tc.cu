@@ -528,7 +528,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
         if (fresh) {  // the tile's statistics, a thread a row
           const bool there = tid < rows_of(q.tile_at);
           float2 v = make_float2(0.f, 0.f);
-          if (there) v = weigh_gather(a, w, q.tile_at, tid, 0, 1);
+          if (there)
+            v = weigh_gather(a, weigh_unit(a, w, q.tile_at), weigh_row_ml(a, w.q.row0, w.head, q.tile_at * kWeighTcRows + tid), tid, 0, 1);
           s_m[ql & 1][tid] = there ? -v.x : -INFINITY;
           s_rl[ql & 1][tid] = there ? merge_scale(v.y) : 0.f;
           if (!named_bar_and(1, 256, ok)) {

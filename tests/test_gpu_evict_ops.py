@@ -158,12 +158,16 @@ class Weigh:
         self.B.specfold_kv_weigh(self.q, self.cache, start, ctx, self.max_rows, self.w if w is None else w, self.ws,
                                  decay=decay, scale=scale, rows=rows, stream=stream)
 
-    def check(self, before, got, decay, scale=0.0):
+    def bound(self, before, decay, scale=0.0):
+        """The oracle's weights and how far a call's may be off."""
         ref, new, score = orc.weigh(host(self.q), host(self.cache.k_pool), self.table, self.cache.page_size, self.start,
                                     self.ctx, before, decay, self.rows, scale)
         terms = int(self.counts.max()) * self.n_q // self.n_kv
         d = 2 * self.hd * E * score + 2.0 ** -21
-        bound = (2 * d + (min(int(self.ctx.max()) + 300, 4160) + terms + 4) * E) * new + 3 * E * np.abs(ref) + 1e-37
+        return ref, (2 * d + (min(int(self.ctx.max()) + 300, 4160) + terms + 4) * E) * new + 3 * E * np.abs(ref) + 1e-37
+
+    def check(self, before, got, decay, scale=0.0):
+        ref, bound = self.bound(before, decay, scale)
         err = np.abs(got - ref)
         assert (err <= bound).all(), (err.max(), (err / bound).max())
 
@@ -225,6 +229,31 @@ def test_kv_weigh_long_context(B, dt, rows, n_q):
     before = host(b.w)
     b.call(1.0)
     b.check(before, host(b.w), 1.0)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows,g,hd", [(64, 8, 64), (57, 9, 128), (256, 5, 64), (40, 40, 64)])
+def test_kv_weigh_groups_of_rows(B, dt, rows, g, hd):
+    b = Weigh(B, np.random.default_rng(rows), dt, hd, g, 1, 16, "split", [rows, 1, 7], [70, 3, 130])
+    before = host(b.w)
+    b.call(0.75)
+    b.check(before, host(b.w), 0.75)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_kv_weigh_rows_in_parts(B, dt):
+    """Rows weighed a part at a time, each behind the tokens of the parts before."""
+    b = Weigh(B, np.random.default_rng(3), dt, 64, 4, 2, 16, "fused", [30, 12], [100, 9])
+    before = host(b.w)
+    got = b.w.clone()
+    for lo, hi in ((0, 5), (5, 12), (12, 30)):
+        n = [min(hi, c) - min(lo, c) for c in b.counts]
+        rows = ints(np.concatenate([b.start[s] + np.arange(min(lo, b.counts[s]), min(hi, b.counts[s])) for s in range(2)]))
+        ctx = ints(b.ctx + np.minimum(lo, b.counts))
+        B.specfold_kv_weigh(b.q, b.cache, ints(np.concatenate([[0], np.cumsum(n)])), ctx, b.max_rows, got, b.ws,
+                            decay=0.5 if lo == 0 else 1.0, rows=rows)
+    ref, bound = b.bound(before, 0.5)
+    assert (np.abs(host(got) - ref) <= 2 * bound).all()     # two more roundings of the sums
 
 
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
@@ -306,10 +335,13 @@ def test_kv_weigh_reports_and_survives_bad_entries(B, dt, rows):
 
     ok, good = run()
     assert ok == 0
+    # without one of its sequences a batch is cut elsewhere, and sums come in another order: either
+    # result is within the bound of the exact one, so they differ by twice that at most
+    apart = 2 * b.bound(before, 1.0)[1]
     for ctx in ([70, -1, 90], [70, 2 ** 31 - 1, 90], [70, b.tokens - rows + 1, 90]):
         st, got = run(ctx=ctx)
         assert st == B.DEV_BAD_SEQ and np.array_equal(got[1], before[1])
-        assert np.array_equal(got[0], good[0]) and np.array_equal(got[2], good[2])
+        assert (np.abs(got - good)[[0, 2]] <= apart[[0, 2]]).all()
     for start in ([0, rows, 3 * rows, 2 * rows], [0, rows, 2 * rows, b.T + 1], [-1, rows, 2 * rows, 3 * rows]):
         st, got = run(start=start)
         assert st & B.DEV_BAD_SEQ
