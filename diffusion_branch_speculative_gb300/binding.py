@@ -22,6 +22,7 @@ OK, EINVAL, EALIGN, ECAPACITY, EUNSUPPORTED, ECUDA, EDEVICE = 0, -1, -2, -3, -4,
 DEV_TIMEOUT, DEV_BAD_PARENT, DEV_BAD_PAGE, DEV_BAD_SEQ = 1, 2, 4, 8
 MAX_SEQS, MAX_TREE, MAX_HEADS, TREE_PAD = 1024, 256, 65536, -2
 MAX_AXES, AXES_BLOCKS, AXES_IN_TURN = 4, 0, 1
+MAX_TOKENS = 1 << 30
 DEV_SITE_SHIFT = 8  # with DEV_TIMEOUT: bit DEV_SITE_SHIFT + site names the wait that ran out
 DEV_SITES = ("attention loader: Q buffer free", "attention loader: K/V stage free", "attention softmax: S ready",
              "attention softmax: P V before a rescale", "attention softmax: P V before the last P",

@@ -275,12 +275,13 @@ static bool nested(long long na, long long sa, long long nb, long long sb, long 
 static int check_token_weights(const specfold_token_weights& w, int n_seqs, int heads, bool written) {
   if (!w.ptr || w.seq_stride < 0 || w.head_stride < 0 || w.tokens < 1) return SPECFOLD_EINVAL;
   if (reinterpret_cast<uintptr_t>(w.ptr) % sizeof(float)) return SPECFOLD_EALIGN;
+  if (w.tokens > SPECFOLD_MAX_TOKENS) return SPECFOLD_ECAPACITY;
   return !written || nested(n_seqs, w.seq_stride, heads, w.head_stride, w.tokens) ? SPECFOLD_OK : SPECFOLD_EINVAL;
 }
 
 static int check_kept(const specfold_kept_tokens& k, int n_seqs, bool written) {
   if (!k.ptr || k.seq_stride < 0 || k.set_stride < 0 || k.n_sets < 1 || k.cap < 1) return SPECFOLD_EINVAL;
-  if (k.n_sets > SPECFOLD_MAX_HEADS) return SPECFOLD_ECAPACITY;
+  if (k.n_sets > SPECFOLD_MAX_HEADS || k.cap > SPECFOLD_MAX_TOKENS) return SPECFOLD_ECAPACITY;
   if (reinterpret_cast<uintptr_t>(k.ptr) % sizeof(int32_t)) return SPECFOLD_EALIGN;
   return !written || nested(n_seqs, k.seq_stride, k.n_sets, k.set_stride, k.cap) ? SPECFOLD_OK : SPECFOLD_EINVAL;
 }
@@ -847,7 +848,7 @@ int specfold_tree_attention(int dtype, int T, int max_nodes, int n_q, int n_kv, 
 size_t specfold_kv_weigh_workspace_size(int dtype, int T, int max_rows, int n_q, int n_kv, int head_dim, int n_seqs,
                                         int tokens) {
   if (check_tree_shape(dtype, n_q, n_kv, head_dim, max_rows) || T < 0 || n_seqs < 1 || n_seqs > SPECFOLD_MAX_SEQS ||
-      tokens < 1)
+      tokens < 1 || tokens > SPECFOLD_MAX_TOKENS)
     return 0;
   return kv_weigh_ws_bytes(dtype, T, max_rows, n_q, n_kv, head_dim, n_seqs, tokens);
 }

@@ -410,7 +410,6 @@ int launch_kv_select(const KvSelectCall& c, cudaStream_t st) {
   const int smem = a.held * 4;
   auto kernel = a.blocks > 1 ? kv_select_kernel<true> : kv_select_kernel<false>;
   if (const int rc = smem_limit_once(kernel, kSelCap * 4)) return rc;
-  if (units * a.blocks > 0x7fffffffLL) return SPECFOLD_ECAPACITY;
   const dim3 grid(static_cast<unsigned>(units * a.blocks));
   if (a.blocks > 1)
     launch_kc(kernel, grid, dim3(kSelThreads), smem, st, a.blocks, a);
@@ -429,7 +428,6 @@ int launch_kv_compact(const KvCompactCall& c, cudaStream_t st) {
     *x = *x * e / 16;
   const long long units = 2LL * c.n_seqs * c.n_kv * a.slices;
   while (a.blocks < 8 && a.blocks * Move<true>::TOKENS < c.kept.cap && units * a.blocks < 5LL * num_sms()) a.blocks *= 2;
-  if (units * a.blocks > 0x7fffffffLL) return SPECFOLD_ECAPACITY;
   const dim3 grid(static_cast<unsigned>(units * a.blocks));
   if (a.blocks > 1)
     launch_kc(kv_compact_kernel<true>, grid, dim3(Move<true>::THREADS), 0, st, a.blocks, a);

@@ -495,7 +495,9 @@ WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int
   const int rows = max_rows * (n_q / n_kv), r8 = (rows + 7) / 8 * 8;
   WeighPlan pl{};
   pl.score_rows = r8;
-  const size_t scores = static_cast<size_t>(n_seqs) * n_kv * tokens * r8 * sizeof(float);
+  // (what passes 64 bits, which only shapes that no memory holds do, stays the most there is)
+  const size_t rows_all = static_cast<size_t>(n_kv) * r8 * sizeof(float), most = ~size_t{0} / 4 / n_seqs / tokens;
+  const size_t scores = std::min(rows_all, most) * n_seqs * tokens;
   const bool keeps = scores <= (size_t{1} << 30);
   if (dtype == SPECFOLD_BF16) {
     if (keeps && rows <= 16) {

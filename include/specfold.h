@@ -79,7 +79,8 @@ extern "C" {
 /* With SPECFOLD_DEV_TIMEOUT, bit (SPECFOLD_DEV_SITE_SHIFT + site) names the
  * wait that ran out (the other waits of that kernel then give up without a
  * bit of their own), for a report:
- *   attention  0 loader: Q buffer free       1 loader: K/V stage free
+ *   attention (the layer's, a tree's and the weights' of a cache alike)
+ *              0 loader: Q buffer free       1 loader: K/V stage free
  *              2 softmax: S ready            3 softmax: P V before a rescale
  *              4 softmax: P V before the last P   5 softmax: last P V
  *              6 MMA: P ready                7 MMA: Q loaded
@@ -98,6 +99,7 @@ extern "C" {
 #define SPECFOLD_MAX_HEADS 65536    /* heads of one kind (the calls on a decoder's cache) */
 #define SPECFOLD_TREE_PAD -2        /* parent of a padding row (specfold_tree_attention) */
 #define SPECFOLD_MAX_AXES 4         /* axes of a position (specfold_rope_axes) */
+#define SPECFOLD_MAX_TOKENS (1 << 30) /* entries of a row of weights or kept tokens */
 
 typedef enum { SPECFOLD_BF16 = 0, SPECFOLD_F32 = 1 } specfold_dtype;
 
@@ -594,7 +596,8 @@ int specfold_kv_append_axes(int dtype, int T, int n_kv, int head_dim, specfold_h
  * call writes them, and the tokens kept, rows lie within the larger stride's
  * steps: the smaller stride is no less than a row, the larger no less than all
  * the rows of the smaller (SPECFOLD_EINVAL); a stride that no step uses does
- * not count. */
+ * not count.  tokens, and the tokens kept's cap, are at most
+ * SPECFOLD_MAX_TOKENS (SPECFOLD_ECAPACITY). */
 typedef struct {
   float* ptr;
   int64_t seq_stride;
@@ -633,7 +636,8 @@ typedef struct {
  * pages hold.  A `rows` entry outside [0, n_src) weighs nothing
  * (SPECFOLD_DEV_BAD_SEQ); a sequence whose row_start, ctx_len or row count is
  * invalid or that has more than w.tokens tokens keeps its weights (the same
- * bit); a page outside the pool or a token past the table reads as a key of
+ * bit), as do all where the batch counts more blocks of keys than
+ * specfold_tree_attention takes; a page outside the pool or a token past the table reads as a key of
  * zeros (SPECFOLD_DEV_BAD_PAGE).
  * Products of bf16 values are summed in 32 bits, softmax and weights are 32
  * bits; results do not depend on timing.

@@ -202,6 +202,7 @@ def test_kv_weigh_refusals(B):
     assert _weigh(B, w=_tw(B, ptr=A + 2)) == B.EALIGN
     assert _weigh(B, w=_tw(B, tokens=0)) == B.EINVAL
     assert _weigh(B, w=_tw(B, ss=-4000)) == B.EINVAL
+    assert _weigh(B, w=_tw(B, ss=1 << 40, hs=1 << 36, tokens=B.MAX_TOKENS + 1)) == B.ECAPACITY
     for ss, hs in OVERLAP:
         assert _weigh(B, w=_tw(B, ss=ss, hs=hs)) == B.EINVAL
     need = B.kv_weigh_workspace_size(B.BF16, 4, 4, 4, 2, 128, 2, 1000)
@@ -216,8 +217,15 @@ def test_kv_weigh_workspace_size(B):
                  (B.BF16, 64, 257, 28, 4, 128, 64, 8192), (B.BF16, 64, 1, 28, 3, 128, 64, 8192),
                  (B.BF16, 64, 1, 28, 4, 96, 64, 8192), (B.BF16, 64, 1, 28, 4, 128, 0, 8192),
                  (B.BF16, 64, 1, 28, 4, 128, 1025, 8192), (B.BF16, 64, 1, 28, 4, 128, 64, 0),
-                 (9, 64, 1, 28, 4, 128, 64, 8192)):
+                 (9, 64, 1, 28, 4, 128, 64, 8192), (B.BF16, 64, 1, 28, 4, 128, 64, B.MAX_TOKENS + 1)):
         assert size(*args) == 0
+    # shapes that no memory holds ask for more than there is, not for what 64 bits leave of it
+    assert size(B.F32, 64, 256, 65536, 512, 128, 1024, B.MAX_TOKENS) > 1 << 60
+    assert size(B.F32, 64, 256, 128, 1, 128, 1024, B.MAX_TOKENS) > 1 << 50
+    # few rows of bf16 and all of fp32 keep their scores: eight rows of a group, 16 bytes and more a token
+    small, large = size(B.BF16, 64, 1, 28, 4, 128, 64, 1024), size(B.BF16, 64, 1, 28, 4, 128, 64, 8192)
+    assert large - small == 64 * 4 * (8192 - 1024) * 8 * 4
+    assert size(B.BF16, 64, 1, 28, 4, 128, 1024, 1 << 20) < 1 << 28        # past 1 GB: computed twice
 
 
 def _select(B, w=None, lengths=A, n_seqs=2, keep=50, sinks=4, recent=8, kept=None, new_len=FAR):
@@ -228,6 +236,8 @@ def _select(B, w=None, lengths=A, n_seqs=2, keep=50, sinks=4, recent=8, kept=Non
 def test_kv_select_refusals(B):
     assert _select(B, w=_tw(B, ptr=None)) == B.EINVAL
     assert _select(B, w=_tw(B, tokens=0)) == B.EINVAL
+    assert _select(B, w=_tw(B, tokens=B.MAX_TOKENS + 1)) == B.ECAPACITY
+    assert _select(B, kept=_kt(B, ss=1 << 40, us=1 << 36, cap=B.MAX_TOKENS + 1)) == B.ECAPACITY
     assert _select(B, w=_tw(B, ptr=A + 1)) == B.EALIGN
     assert _select(B, lengths=None) == B.EINVAL
     assert _select(B, new_len=None) == B.EINVAL
@@ -267,6 +277,8 @@ def test_kv_compact_refusals(B):
     assert _compact(B, kept=_kt(B, sets=3)) == B.EINVAL
     assert _compact(B, kept=_kt(B, cap=0)) == B.EINVAL
     assert _compact(B, kept=_kt(B, us=-1)) == B.EINVAL
+    assert _compact(B, kept=_kt(B, cap=B.MAX_TOKENS + 1)) == B.ECAPACITY
+    assert _compact(B, w=_tw(B, ss=1 << 40, hs=1 << 36, tokens=B.MAX_TOKENS + 1)) == B.ECAPACITY
     assert _compact(B, w=_tw(B, ptr=None)) == B.EINVAL
     assert _compact(B, w=_tw(B, hs=-1)) == B.EINVAL
     for ss, hs in OVERLAP:

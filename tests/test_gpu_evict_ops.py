@@ -18,7 +18,7 @@ import pytest
 import torch
 
 from oracle import evict_oracle as orc
-from tests.test_gpu_cache_ops import DT, E, half_step, host, ints, make_cache, randn, rot_bound
+from tests.test_gpu_cache_ops import DT, E, far_cache, half_step, host, ints, make_cache, randn, rot_bound
 
 pytestmark = pytest.mark.gpu
 
@@ -570,6 +570,155 @@ def test_kv_compact_bad_entries(B):
     st, k, v = run(tab=tab)
     want_k, want_v, _ = orc.compact(host(k0), host(v0), tab, 8, good, [100] * 3, [60] * 3)
     assert st == B.DEV_BAD_PAGE and np.array_equal(k, want_k) and np.array_equal(v, want_v)
+
+
+# ------------------------------------------------ where calls can go wrong --
+
+@pytest.mark.parametrize("rows,n_q", [(1, 28), (30, 16)])
+def test_pools_past_two_to_the_31_elements(B, rows, n_q):
+    """Weights and moves at element offsets that 32 bits do not hold."""
+    rng = np.random.default_rng(22)
+    n_kv, hd, page, tokens = 4, 128, 16, 4_300_000 // 16 * 16   # 2.2e9 elements a pool
+    counts, ctx = np.array([rows, 2]), np.array([100, 33])
+    start, n = np.concatenate([[0], np.cumsum(counts)]), ctx + counts
+    cache, table = far_cache(B, rng, n_kv, hd, page, n, tokens)
+    q = randn(rng, (int(start[-1]), n_q, hd), "bf16", 1.5)
+    # the weights' heads far apart as well
+    big = torch.empty(3 << 30, dtype=torch.float32, device="cuda")
+    w = big.as_strided((2, n_kv, int(n.max())), (1 << 30, 1 << 28, 1))
+    w.copy_(torch.rand(w.shape))
+    before = host(w)
+    most = int(counts.max())
+    ws = B.alloc_workspace(B.kv_weigh_workspace_size(B.BF16, len(q), most, n_q, n_kv, hd, 2, w.shape[2]))
+    B.specfold_kv_weigh(q, cache, ints(start), ints(ctx), most, w, ws, decay=0.5)
+    # the oracle on the used pages alone
+    used = table[table > 0]
+    slots = torch.from_numpy((used[:, None].astype(np.int64) * page + np.arange(page)).reshape(-1)).cuda()
+    small = np.zeros_like(table)
+    small[table > 0] = np.arange(len(used))
+    kp, vp = host(cache.k_pool[slots]), host(cache.v_pool[slots])
+    ref, new, score = orc.weigh(host(q), kp, small, page, start, ctx, before, 0.5)
+    d = 2 * hd * E * score + 2.0 ** -21
+    assert (np.abs(host(w) - ref) <= (2 * d + (4160 + rows * n_q) * E) * new + 3 * E * np.abs(ref)).all()
+    assert B.specfold_get_status(ws) == 0
+    kept, new_len, status = torch.zeros(2, n_kv, 25, dtype=torch.int32, device="cuda"), ints([0, 0]), word()
+    B.specfold_kv_select(w, ints(n), 25, kept, new_len, 1, 3, status)
+    w1 = host(w)
+    B.specfold_kv_compact(cache, kept, ints(n), new_len, weights=w, status=status)
+    torch.cuda.synchronize()
+    got = kept.cpu().numpy()
+    for s, sets in enumerate(orc.select(w1, n, 25, 1, 3)):
+        assert np.array_equal(got[s], np.stack(sets))
+    k2, v2, w2 = orc.compact(kp, vp, small, page, got, n, [25, 25], w1)
+    assert np.array_equal(host(cache.k_pool[slots]), k2) and np.array_equal(host(cache.v_pool[slots]), v2)
+    assert np.array_equal(host(w), w2) and int(status) == 0
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("rows", [1, 40])
+def test_two_streams_at_once(B, dt, rows):
+    """Calls that overlap, each with a workspace of its own."""
+    rng = np.random.default_rng(rows)
+    b = [Weigh(B, rng, dt, 64, 8, 2, 16, "split", [rows, rows, 1], [2000 + 300 * i, 70, 900]) for i in range(2)]
+    ref = []
+    for x in b:
+        w = x.w.clone()
+        x.call(1.0, w=w)
+        ref.append(w)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in b]
+    got = [[x.w.clone() for _ in range(8)] for x in b]
+    torch.cuda.synchronize()
+    for k in range(8):
+        for i, x in enumerate(b):
+            x.call(1.0, w=got[i][k], stream=streams[i])
+    torch.cuda.synchronize()
+    for i, x in enumerate(b):
+        assert all(torch.equal(w, ref[i]) for w in got[i]) and B.specfold_get_status(x.ws) == 0
+
+
+@pytest.mark.parametrize("rows", [1, 40])
+def test_a_captured_call_follows_its_lengths(B, rows):
+    """A graph replayed with other lengths, tables and rows than it was captured with."""
+    rng = np.random.default_rng(rows)
+    b = Weigh(B, rng, "bf16", 128, 8, 2, 16, "fused", [rows, rows], [600, 90], tail=rows)
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        b.call(1.0, w=b.w.clone())
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    w = b.w.clone()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        b.call(0.5, w=w)
+    for counts, ctx in (([rows, rows], [600, 90]), ([0, rows], [5, 33]), ([rows, 0], [0, 7]), ([0, 0], [9, 9]),
+                        ([max(1, rows // 3), rows], [599, 0])):
+        b.counts, b.ctx, b.start = np.array(counts), np.array(ctx), np.concatenate([[0], np.cumsum(counts)])
+        b.at[0].copy_(ints(b.start))
+        b.at[1].copy_(ints(b.ctx))
+        w.copy_(b.w)
+        graph.replay()
+        torch.cuda.synchronize()
+        b.check(host(b.w), host(w), 0.5)
+    assert B.specfold_get_status(b.ws) == 0
+
+
+def test_select_and_compact_captured(B):
+    rng = np.random.default_rng(11)
+    cache, table = make_cache(B, rng, "bf16", 64, 2, 16, [9000, 400], "split")
+    w = torch.rand(2, 2, 9000, device="cuda")
+    n, new = ints([9000, 400]), ints([0, 0])
+    kept = torch.zeros(2, 2, 1000, dtype=torch.int32, device="cuda")
+
+    def cut():
+        B.specfold_kv_select(w, n, 1000, kept, new, 4, 100)
+        B.specfold_kv_compact(cache, kept, n, new, weights=w)
+    state = [t.clone() for t in (cache.k_pool, cache.v_pool, w)]
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        cut()
+    torch.cuda.current_stream().wait_stream(side)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cut()
+    for lengths in ([9000, 400], [1001, 0], [700, 399], [8999, 400]):
+        for t, old in zip((cache.k_pool, cache.v_pool, w), state):
+            t.copy_(old)
+        n.copy_(ints(lengths))
+        w0, k0, v0 = w.cpu().numpy(), host(cache.k_pool), host(cache.v_pool)
+        graph.replay()
+        torch.cuda.synchronize()
+        m = np.minimum(lengths, 1000)
+        assert np.array_equal(new.cpu().numpy(), m)
+        got = kept.cpu().numpy()
+        for s, sets in enumerate(orc.select(w0, lengths, 1000, 4, 100)):
+            for u in range(2):
+                assert np.array_equal(got[s, u, :m[s]], sets[u])
+        k2, v2, w2 = orc.compact(k0, v0, table, 16, got, lengths, m, w0)
+        assert np.array_equal(host(cache.k_pool), k2) and np.array_equal(host(cache.v_pool), v2)
+        assert np.array_equal(w.cpu().numpy(), w2)
+
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+def test_guards_intact(B, dt):
+    """Nothing outside of outputs and workspace is written."""
+    rng = np.random.default_rng(12)
+    for rows, hd in ((1, 128), (33, 64)):
+        b = Weigh(B, rng, dt, hd, 8, 2, 16, "heads", [rows, 3], [300, 45])
+        n = b.ws.numel()
+        buf = torch.full((n + 8192,), 0xA5, dtype=torch.uint8, device="cuda")
+        buf[4096:4096 + n] = 0
+        b.ws = buf[4096:4096 + n]
+        wide = torch.full((4, b.n_kv + 2, b.tokens + 64), 3.0, device="cuda")
+        w = wide[1:3, 1:-1, 32:-32]
+        b.call(0.0, w=w)
+        torch.cuda.synchronize()
+        assert (buf[:4096] == 0xA5).all() and (buf[4096 + n:] == 0xA5).all()
+        w.fill_(3.0)
+        assert (wide == 3.0).all()
 
 
 # ----------------------------------------------------- a run of them --
