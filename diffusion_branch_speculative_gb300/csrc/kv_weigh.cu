@@ -36,11 +36,11 @@ SF_DEV void weigh_write_part(const WeighArgs& p, const TreeWalk& w, bool first, 
 // that one token with a group of seven heads wastes one column in eight; the
 // scores go to the workspace, 32 bytes a token and eight rows, where the second
 // launch finds them in L2 rather than the keys in DRAM.
-template <int HD, int NT>
+template <int HD, int NT, int STAGES_ = 3>
 struct WFew {
   static constexpr int R = 8 * NT;
   static constexpr int CH = 2048 / HD;  // keys of a warp's step: 4 KB
-  static constexpr int STAGES = 3;
+  static constexpr int STAGES = STAGES_;
   static constexpr int ROW = HD * 2;
   static constexpr int CPR = ROW / 16;
   static constexpr int STAGE = CH * ROW;
@@ -50,11 +50,164 @@ struct WFew {
   static constexpr int CTAS = 4;  // per SM
 };
 
-template <int HD, int NT>
-__global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel(const __grid_constant__ WeighArgs a) {
-  using C = WFew<HD, NT>;
+// A block's keys key_lo .. key_hi - 1 of sequence s, head h: the scores to row_of(token)
+// [R], the warps' statistics to s_ml [kWarps][R].
+template <typename C, int HD, int NT, typename RowOf>
+SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int key_lo, int key_hi, uint8_t* smem, float2* s_ml,
+                       RowOf row_of) {
   using T = __nv_bfloat16;
   constexpr int R = C::R, KS = HD / 16, CH = C::CH, KH = CH / 16;
+  const TreeArgs& p = a.t;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const uint64_t once = policy_evict_first();  // the keys: L2 is for the scores
+  uint8_t* ring = smem + warp * C::RING;
+  uint8_t* s_q = smem + C::OFF_Q;
+  const int rows = q.n * p.g, len = q.ctx + q.n;
+  // this warp's chunks: key_lo + CH * (warp + 4 i)
+  const int chunks = (key_hi - key_lo + CH - 1) / CH;
+  const int mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
+  auto key_of = [&](int i) { return key_lo + CH * (warp + kWarps * i); };
+  // lanes 0..CH-1 have a chunk's keys; a chunk's pages are read two chunks ahead of its
+  // loads, and followed by steps (no division a chunk)
+  const int32_t* table = p.cache.block_table + s * p.cache.table_stride;
+  const int ps = p.cache.page_size, dpg = CH * kWarps / ps, doff = CH * kWarps - dpg * ps;
+  struct Page {
+    int id, off;  // in the table; a key's place in it, -1: no key
+  };
+  const unsigned tok0 = static_cast<unsigned>(key_lo) + CH * warp + (lane & (CH - 1));
+  int pg = tok0 / static_cast<unsigned>(ps), off = tok0 - pg * ps;
+  int left = key_hi > static_cast<int>(tok0) ? (key_hi - static_cast<int>(tok0) + CH * kWarps - 1) / (CH * kWarps) : 0;  // this lane's keys
+  auto page_next = [&]() {
+    Page x = {-1, left > 0 ? off : -1};
+    if (left > 0 && pg < p.cache.table_pages) x.id = table[pg];
+    --left;
+    pg += dpg;
+    off += doff;
+    if (off >= ps) {
+      off -= ps;
+      ++pg;
+    }
+    return x;
+  };
+  auto slot_of = [&](Page x) {
+    if (x.id >= 0 && x.id < p.cache.num_pages) return x.id * ps + x.off;
+    if (x.off >= 0) atomicOr(p.status, SPECFOLD_DEV_BAD_PAGE);
+    return -1;
+  };
+  const T* kbase = static_cast<const T*>(p.cache.k) + h * p.cache.k_head_stride;
+  auto load = [&](int i, int slot) {
+    if (i < mine) {
+      const uint32_t st = smem_u32(ring + (i % C::STAGES) * C::STAGE);
+      constexpr int KEYS = 32 / C::CPR;  // keys of one step of the warp's lanes
+      const int c = lane % C::CPR;
+#pragma unroll
+      for (int it = 0; it < CH / KEYS; ++it) {
+        const int key = it * KEYS + lane / C::CPR;
+        const int tk = __shfl_sync(0xffffffffu, slot, key);
+        const long long tz = tk < 0 ? 0 : tk;  // any valid address when nothing is read
+        cp_async16_hint(st + key * C::ROW + ((c ^ (key & 7)) << 4), kbase + tz * p.cache.k_token_stride + c * 8,
+                        tk < 0 ? 0u : 16u, once);
+      }
+    }
+    cp_async_commit();
+  };
+  Page page = page_next(), next = page_next();
+#pragma unroll
+  for (int i = 0; i < C::STAGES - 1; ++i) {
+    load(i, slot_of(page));
+    page = next;
+    next = page_next();
+  }
+  // queries: row m = row m / g of the sequence, head m % g of the group; the rows
+  // past the last are its copies (zeros times an infinite key would be NaN)
+  for (int i = threadIdx.x; i < R * C::CPR; i += kThreads) {
+    const int r = i / C::CPR, c = i % C::CPR, m = min(r, rows - 1);
+    const int src = max(weigh_src(a, q.row0 + m / p.g), 0);
+    *reinterpret_cast<uint4*>(s_q + r * C::ROW + ((c ^ (r & 7)) << 4)) =
+        *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + src * p.q_rs + (h * p.g + m % p.g) * p.q_hs + c * 8);
+  }
+  __syncthreads();
+  uint32_t qf[NT][KS][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int ks = 0; ks < KS; ks += 2) {
+      uint32_t b[4];
+      const int r = nt * 8 + (lane & 7);
+      ldsm4(smem_u32(s_q + r * C::ROW + (((ks * 2 + (lane >> 3)) ^ (r & 7)) << 4)), b);
+      qf[nt][ks][0] = b[0], qf[nt][ks][1] = b[1], qf[nt][ks + 1][0] = b[2], qf[nt][ks + 1][1] = b[3];
+    }
+  // this thread's rows: 8 nt + 2 (lane % 4) and the next one; the last token each sees
+  int seen[NT][2];
+  float m[NT][2], l[NT][2];
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      seen[nt][e] = q.ctx + min(nt * 8 + (lane & 3) * 2 + e, rows - 1) / p.g;
+      m[nt][e] = -INFINITY;
+      l[nt][e] = 0.f;
+    }
+  for (int i = 0; i < mine; ++i) {
+    load(i + C::STAGES - 1, slot_of(page));
+    page = next;
+    next = page_next();
+    cp_async_wait<C::STAGES - 1>();
+    __syncwarp();
+    const uint8_t* stg = ring + (i % C::STAGES) * C::STAGE;
+    const bool tail = key_of(i) + CH > q.ctx;  // holds tokens that not every row sees
+#pragma unroll
+    for (int kh = 0; kh < KH; ++kh) {
+      float sc[NT][4] = {};
+      const int key = kh * 16 + (lane & 15);
+      const uint32_t base = smem_u32(stg + key * C::ROW);
+#pragma unroll
+      for (int ks = 0; ks < KS; ++ks) {
+        uint32_t k[4];
+        ldsm4(base + (((ks * 2 + (lane >> 4)) ^ (key & 7)) << 4), k);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt], k, qf[nt][ks][0], qf[nt][ks][1]);
+      }
+      const int t0 = key_of(i) + kh * 16 + (lane >> 2);
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+#pragma unroll
+        for (int x = 0; x < 4; ++x) {
+          sc[nt][x] *= p.sl2;
+          if (tail && t0 + (x >> 1) * 8 > seen[nt][x & 1]) sc[nt][x] = -INFINITY;
+        }
+#pragma unroll
+        for (int half = 0; half < 2; ++half)
+          if (!tail || t0 + half * 8 < len)
+            *reinterpret_cast<float2*>(row_of(t0 + half * 8) + nt * 8 + (lane & 3) * 2) =
+                make_float2(sc[nt][2 * half], sc[nt][2 * half + 1]);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const float top = fmaxf(m[nt][e], fmaxf(sc[nt][e], sc[nt][2 + e]));
+          const float b = top == -INFINITY ? 0.f : top;
+          l[nt][e] = fmaf(l[nt][e], m[nt][e] == top ? 1.f : ex2(m[nt][e] - b), ex2(sc[nt][e] - b) + ex2(sc[nt][2 + e] - b));
+          m[nt][e] = top;
+        }
+      }
+    }
+    __syncwarp();  // the stage may be overwritten
+  }
+  cp_async_wait<0>();
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int e = 0; e < 2; ++e) {
+      float2 v = make_float2(m[nt][e], l[nt][e]);
+#pragma unroll
+      for (int o = 4; o < 32; o <<= 1)
+        v = weigh_merge(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+      if (lane < 4) s_ml[warp * R + nt * 8 + lane * 2 + e] = v;
+    }
+}
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel(const __grid_constant__ WeighArgs a) {
+  constexpr int R = WFew<HD, NT>::R;
   const TreeArgs& p = a.t;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[kWarps * R];
@@ -63,161 +216,108 @@ __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel
   TreeWalk w;
   unsigned per;
   if (!tree_locate(p, w, per)) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const uint64_t once = policy_evict_first();  // the keys: L2 is for the scores
-  uint8_t* ring = smem + warp * C::RING;
-  uint8_t* s_q = smem + C::OFF_Q;
-
   for (bool first = true; w.n > 0; first = false, w.next(p)) {
-    const int h = w.head, rows = w.q.n * p.g;
-    const int len = w.q.ctx + w.q.n, key_lo = w.b0 * p.kb;
-    const int key_hi = min(static_cast<long long>(len), static_cast<long long>(w.b0 + w.n) * p.kb);
+    const int key_lo = w.b0 * p.kb;
+    const int key_hi = min(static_cast<long long>(w.q.ctx + w.q.n), static_cast<long long>(w.b0 + w.n) * p.kb);
     if (threadIdx.x == 0 && w.b0 == 0) weigh_note_span(a, w, first, per);
     __syncthreads();  // the previous piece's shared memory is free
-
-    // this warp's chunks: key_lo + CH * (warp + 4 i)
-    const int chunks = (key_hi - key_lo + CH - 1) / CH;
-    const int mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
-    auto key_of = [&](int i) { return key_lo + CH * (warp + kWarps * i); };
-    // lanes 0..CH-1 have a chunk's keys; a chunk's pages are read two chunks ahead of its
-    // loads, and followed by steps (no division a chunk)
-    const int32_t* table = p.cache.block_table + w.s * p.cache.table_stride;
-    const int ps = p.cache.page_size, dpg = CH * kWarps / ps, doff = CH * kWarps - dpg * ps;
-    struct Page {
-      int id, off;  // in the table; a key's place in it, -1: no key
-    };
-    const unsigned tok0 = static_cast<unsigned>(key_lo) + CH * warp + (lane & (CH - 1));
-    int pg = tok0 / static_cast<unsigned>(ps), off = tok0 - pg * ps;
-    int left = key_hi > static_cast<int>(tok0) ? (key_hi - static_cast<int>(tok0) + CH * kWarps - 1) / (CH * kWarps) : 0;  // this lane's keys
-    auto page_next = [&]() {
-      Page x = {-1, left > 0 ? off : -1};
-      if (left > 0 && pg < p.cache.table_pages) x.id = table[pg];
-      --left;
-      pg += dpg;
-      off += doff;
-      if (off >= ps) {
-        off -= ps;
-        ++pg;
-      }
-      return x;
-    };
-    auto slot_of = [&](Page x) {
-      if (x.id >= 0 && x.id < p.cache.num_pages) return x.id * ps + x.off;
-      if (x.off >= 0) atomicOr(p.status, SPECFOLD_DEV_BAD_PAGE);
-      return -1;
-    };
-    const T* kbase = static_cast<const T*>(p.cache.k) + h * p.cache.k_head_stride;
-    auto load = [&](int i, int slot) {
-      if (i < mine) {
-        const uint32_t st = smem_u32(ring + (i % C::STAGES) * C::STAGE);
-        constexpr int KEYS = 32 / C::CPR;  // keys of one step of the warp's lanes
-        const int c = lane % C::CPR;
-#pragma unroll
-        for (int it = 0; it < CH / KEYS; ++it) {
-          const int key = it * KEYS + lane / C::CPR;
-          const int tk = __shfl_sync(0xffffffffu, slot, key);
-          const long long tz = tk < 0 ? 0 : tk;  // any valid address when nothing is read
-          cp_async16_hint(st + key * C::ROW + ((c ^ (key & 7)) << 4), kbase + tz * p.cache.k_token_stride + c * 8,
-                          tk < 0 ? 0u : 16u, once);
-        }
-      }
-      cp_async_commit();
-    };
-    Page page = page_next(), next = page_next();
-#pragma unroll
-    for (int i = 0; i < C::STAGES - 1; ++i) {
-      load(i, slot_of(page));
-      page = next;
-      next = page_next();
-    }
-    // queries: row m = row m / g of the sequence, head m % g of the group; the rows
-    // past the last are its copies (zeros times an infinite key would be NaN)
-    for (int i = threadIdx.x; i < R * C::CPR; i += kThreads) {
-      const int r = i / C::CPR, c = i % C::CPR, m = min(r, rows - 1);
-      const int src = max(weigh_src(a, w.q.row0 + m / p.g), 0);
-      *reinterpret_cast<uint4*>(s_q + r * C::ROW + ((c ^ (r & 7)) << 4)) =
-          *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + src * p.q_rs + (h * p.g + m % p.g) * p.q_hs + c * 8);
-    }
-    __syncthreads();
-    uint32_t qf[NT][KS][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int ks = 0; ks < KS; ks += 2) {
-        uint32_t b[4];
-        const int r = nt * 8 + (lane & 7);
-        ldsm4(smem_u32(s_q + r * C::ROW + (((ks * 2 + (lane >> 3)) ^ (r & 7)) << 4)), b);
-        qf[nt][ks][0] = b[0], qf[nt][ks][1] = b[1], qf[nt][ks + 1][0] = b[2], qf[nt][ks + 1][1] = b[3];
-      }
-    // this thread's rows: 8 nt + 2 (lane % 4) and the next one; the last token each sees
-    int seen[NT][2];
-    float m[NT][2], l[NT][2];
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        seen[nt][e] = w.q.ctx + min(nt * 8 + (lane & 3) * 2 + e, rows - 1) / p.g;
-        m[nt][e] = -INFINITY;
-        l[nt][e] = 0.f;
-      }
-    float* out = a.scores + ((static_cast<size_t>(w.s) * p.n_kv + h) * a.w.tokens) * R + (lane & 3) * 2;
-    for (int i = 0; i < mine; ++i) {
-      load(i + C::STAGES - 1, slot_of(page));
-      page = next;
-      next = page_next();
-      cp_async_wait<C::STAGES - 1>();
-      __syncwarp();
-      const uint8_t* stg = ring + (i % C::STAGES) * C::STAGE;
-      const bool tail = key_of(i) + CH > w.q.ctx;  // holds tokens that not every row sees
-#pragma unroll
-      for (int kh = 0; kh < KH; ++kh) {
-        float s[NT][4] = {};
-        const int key = kh * 16 + (lane & 15);
-        const uint32_t base = smem_u32(stg + key * C::ROW);
-#pragma unroll
-        for (int ks = 0; ks < KS; ++ks) {
-          uint32_t k[4];
-          ldsm4(base + (((ks * 2 + (lane >> 4)) ^ (key & 7)) << 4), k);
-#pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma16816(s[nt], k, qf[nt][ks][0], qf[nt][ks][1]);
-        }
-        const int t0 = key_of(i) + kh * 16 + (lane >> 2);
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-#pragma unroll
-          for (int x = 0; x < 4; ++x) {
-            s[nt][x] *= p.sl2;
-            if (tail && t0 + (x >> 1) * 8 > seen[nt][x & 1]) s[nt][x] = -INFINITY;
-          }
-#pragma unroll
-          for (int half = 0; half < 2; ++half)
-            if (!tail || t0 + half * 8 < len)
-              *reinterpret_cast<float2*>(out + static_cast<size_t>(t0 + half * 8) * R + nt * 8) =
-                  make_float2(s[nt][2 * half], s[nt][2 * half + 1]);
-#pragma unroll
-          for (int e = 0; e < 2; ++e) {
-            const float top = fmaxf(m[nt][e], fmaxf(s[nt][e], s[nt][2 + e]));
-            const float b = top == -INFINITY ? 0.f : top;
-            l[nt][e] = fmaf(l[nt][e], m[nt][e] == top ? 1.f : ex2(m[nt][e] - b), ex2(s[nt][e] - b) + ex2(s[nt][2 + e] - b));
-            m[nt][e] = top;
-          }
-        }
-      }
-      __syncwarp();  // the stage may be overwritten
-    }
-    cp_async_wait<0>();
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        float2 v = make_float2(m[nt][e], l[nt][e]);
-#pragma unroll
-        for (int o = 4; o < 32; o <<= 1)
-          v = weigh_merge(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
-        if (lane < 4) s_ml[warp * R + nt * 8 + lane * 2 + e] = v;
-      }
+    float* out = a.scores + (static_cast<size_t>(w.s) * p.n_kv + w.head) * a.w.tokens * R;
+    few_stream<WFew<HD, NT>, HD, NT>(a, w.s, w.head, w.q, key_lo, key_hi, smem, s_ml, [&](int t) { return out + static_cast<size_t>(t) * R; });
     __syncthreads();
     weigh_write_part<R>(a, w, first, s_ml);
+  }
+}
+
+// The same in one launch where a unit's scores fit the shared memory of a cluster: its
+// blocks have a slice of the tokens each and keep its scores, tell each other their
+// rows' statistics, and add up their tokens' weights.  No scores pass through memory,
+// and one launch less is waited for and paid for on the host.
+constexpr int kUnitMost = 100 * 1024;  // bytes of a slice's scores
+constexpr int kUnitFloats = 8 * 1024;  // scores of a slice that a block more is taken for
+template <int HD, int NT>
+struct WUnit : WFew<HD, NT, 2> {
+  static constexpr int OFF_S = WFew<HD, NT, 2>::SMEM;                 // [tokens of a slice][R]
+  static constexpr int MAX_CLUSTER = 8;
+};
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(kThreads) weigh_unit_kernel(const __grid_constant__ WeighArgs a) {
+  using C = WUnit<HD, NT>;
+  constexpr int R = C::R;
+  const TreeArgs& p = a.t;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 s_ml[kWarps * R];
+  __shared__ float2 s_all[C::MAX_CLUSTER][R];
+  __shared__ __align__(16) float s_m[R], s_rl[R];
+  float* s_x = reinterpret_cast<float*>(smem + C::OFF_S);
+  pdl_wait();
+  pdl_trigger();
+  const int blocks = a.blocks, rank = static_cast<int>(cluster_ctarank());
+  const int unit = static_cast<int>(blockIdx.x) / blocks, s = unit / p.n_kv, h = unit - s * p.n_kv;
+  const TreeSeq q = tree_seq(p, s);
+  if (q.bad && h == 0 && rank == 0 && threadIdx.x == 0) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
+  if (q.n == 0) return;  // the same in all of the cluster
+  cluster_arrive();
+  const int rows = q.n * p.g, len = q.ctx + q.n;
+  const int slice = ((len - 1) / blocks / kKeys + 1) * kKeys;
+  const int key_lo = min(static_cast<long long>(len), static_cast<long long>(rank) * slice), key_hi = min(len - key_lo, slice) + key_lo;
+  few_stream<C, HD, NT>(a, s, h, q, key_lo, key_hi, smem, s_ml, [&](int t) { return s_x + (t - key_lo) * R; });
+  __syncthreads();
+  cluster_wait();  // all of them have begun
+  if (threadIdx.x < R) {
+    const int r = threadIdx.x;
+    float2 v = s_ml[r];
+#pragma unroll
+    for (int k = 1; k < kWarps; ++k) v = weigh_merge(v, s_ml[k * R + r]);
+    if (r >= rows || weigh_src(a, q.row0 + r / p.g) < 0) v = make_float2(INFINITY, 0.f);  // weighs nothing: 2^(x - inf) = 0
+    for (int k = 0; k < blocks; ++k) {
+      const uint32_t at = dsmem_addr(smem_u32(&s_all[rank][r]), k);
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
+    }
+  }
+  cluster_sync_all();  // the only exchange: a block may end from here on
+  if (threadIdx.x < R) {
+    float2 v = s_all[0][threadIdx.x];
+    for (int k = 1; k < blocks; ++k) v = weigh_merge(v, s_all[k][threadIdx.x]);
+    s_m[threadIdx.x] = v.x;
+    s_rl[threadIdx.x] = merge_scale(v.y);
+  }
+  __syncthreads();
+  // two threads a token, each with four of eight rows
+  const int half = threadIdx.x & 1;
+  float* wt = a.w.ptr + s * a.w.seq_stride + h * a.w.head_stride;
+  float4 m[NT], rl[NT];
+#pragma unroll
+  for (int i = 0; i < NT; ++i) {
+    m[i] = *reinterpret_cast<const float4*>(s_m + 8 * i + 4 * half);
+    rl[i] = *reinterpret_cast<const float4*>(s_rl + 8 * i + 4 * half);
+  }
+  constexpr int K = 4;  // tokens at once
+  for (int first = key_lo; first < key_hi; first += K * (kThreads / 2)) {
+    const int t0 = first + static_cast<int>(threadIdx.x >> 1);
+    float old[K];
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int t = t0 + k * (kThreads / 2);
+      old[k] = half == 0 && t < min(key_hi, q.ctx) && a.decay != 0.f ? wt[t] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const int t = t0 + k * (kThreads / 2);
+      float sum = 0.f;
+      if (t < key_hi) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) {
+          const float4 u = *reinterpret_cast<const float4*>(s_x + (t - key_lo) * R + 8 * i + 4 * half);
+          sum = fmaf(ex2(u.x - m[i].x), rl[i].x, sum);
+          sum = fmaf(ex2(u.y - m[i].y), rl[i].y, sum);
+          sum = fmaf(ex2(u.z - m[i].z), rl[i].z, sum);
+          sum = fmaf(ex2(u.w - m[i].w), rl[i].w, sum);
+        }
+      }
+      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+      if (half == 0 && t < key_hi) wt[t] = fmaf(a.decay, old[k], sum);
+    }
   }
 }
 
@@ -469,11 +569,12 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) weigh_sum_kernel(const 
 }
 
 // --------------------------------------------------------------- launches --
-enum WeighForm { kFew, kSimt, kTc };
+enum WeighForm { kUnit, kFew, kSimt, kTc };
 struct WeighPlan {
   WeighForm form;
   int stat_rows, stat_tiles;  // of the first launch
   int ctas_per_sm;
+  int blocks, slice;          // of a cluster; tokens of a block's slice at most (kUnit)
   int score_rows;
   size_t row_ml, part, span, scores;  // bytes
 };
@@ -500,6 +601,16 @@ WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int
   const size_t scores = std::min(rows_all, most) * n_seqs * tokens;
   const bool keeps = scores <= (size_t{1} << 30);
   if (dtype == SPECFOLD_BF16) {
+    const long long units = static_cast<long long>(n_seqs) * n_kv;
+    auto slice = [&](int blocks) { return ((tokens - 1) / blocks / kKeys + 1) * kKeys; };
+    int blocks = 1;
+    while (blocks < 8 && slice(blocks) > 256 && (slice(blocks) * r8 > kUnitFloats || units * blocks < 2LL * kSmBudget)) blocks *= 2;
+    if (rows <= 16 && static_cast<long long>(slice(blocks)) * r8 <= kUnitMost / 4) {
+      pl.form = kUnit;
+      pl.blocks = blocks;
+      pl.slice = slice(blocks);
+      return pl;
+    }
     if (keeps && rows <= 16) {
       pl.form = kFew;
       pl.stat_rows = r8;
@@ -526,6 +637,17 @@ int start(void (*kernel)(WeighArgs), const WeighArgs& a, int grid, int threads, 
   if (smem > 0)
     if (const int rc = smem_limit_once(kernel, smem)) return rc;
   launch_k(kernel, dim3(grid), dim3(threads), smem, st, a);
+  count_launch();
+  return check_launch();
+}
+
+template <int HD, int NT>
+int unit_go(const WeighPlan& pl, WeighArgs& a, cudaStream_t st) {
+  using C = WUnit<HD, NT>;
+  if (const int rc = smem_limit_once(weigh_unit_kernel<HD, NT>, C::OFF_S + kUnitMost)) return rc;
+  a.blocks = pl.blocks;
+  launch_kc(weigh_unit_kernel<HD, NT>, dim3(a.t.batch.n_seqs * a.t.n_kv * pl.blocks), dim3(kThreads),
+            C::OFF_S + pl.slice * C::R * 4, st, pl.blocks, a);
   count_launch();
   return check_launch();
 }
@@ -561,6 +683,9 @@ int weigh_go(const KvWeighCall& c, cudaStream_t st) {
   const int grid = std::min(num_sms(), kSmBudget) * pl.ctas_per_sm;
   t.w_full = t.w_half = 1;
   if (pl.form == kTc) return launch_weigh_tc(a, HD, grid, st);
+  t.tile_rows = SPECFOLD_MAX_TREE * 128;
+  t.kb = kKeys;
+  if (pl.form == kUnit) return pl.score_rows == 8 ? unit_go<HD, 1>(pl, a, st) : unit_go<HD, 2>(pl, a, st);
   t.tile_rows = pl.stat_rows;
   t.kb = kKeys;
   t.unit_cost = 4;

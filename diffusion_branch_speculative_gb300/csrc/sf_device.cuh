@@ -171,6 +171,9 @@ SF_DEV uint32_t cluster_ctarank() {
 SF_DEV void cluster_sync_all() {
   asm volatile("barrier.cluster.arrive.release.aligned;\n\tbarrier.cluster.wait.acquire.aligned;" ::: "memory");
 }
+// Its two halves.
+SF_DEV void cluster_arrive() { asm volatile("barrier.cluster.arrive.release.aligned;" ::: "memory"); }
+SF_DEV void cluster_wait() { asm volatile("barrier.cluster.wait.acquire.aligned;" ::: "memory"); }
 // Address of the same shared-memory offset in CTA `rank` of the cluster.
 SF_DEV uint32_t dsmem_addr(uint32_t local, uint32_t rank) {
   uint32_t r;
