@@ -232,13 +232,82 @@ __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel
 // blocks have a slice of the tokens each and keep its scores, tell each other their
 // rows' statistics, and add up their tokens' weights.  No scores pass through memory,
 // and one launch less is waited for and paid for on the host.
-constexpr int kUnitMost = 100 * 1024;  // bytes of a slice's scores
-constexpr int kUnitFloats = 8 * 1024;  // scores of a slice that a block more is taken for
+constexpr int kUnitCluster = 8;        // blocks at most
+constexpr int kUnitScores = 8 * 1024;  // of a slice, at most
 template <int HD, int NT>
 struct WUnit : WFew<HD, NT, 2> {
   static constexpr int OFF_S = WFew<HD, NT, 2>::SMEM;                 // [tokens of a slice][R]
-  static constexpr int MAX_CLUSTER = 8;
 };
+
+// What a cluster's blocks share of a unit: every block's statistics of its rows.
+template <int R>
+struct UnitShared {
+  float2 all[kUnitCluster][R];
+  float m[R], rl[R];
+};
+// This block's slice of the unit's tokens.
+struct Slice {
+  int lo, hi;
+  SF_DEV Slice(int len, int blocks, int rank) {
+    const int n = ((len - 1) / blocks / kKeys + 1) * kKeys;
+    lo = min(static_cast<long long>(len), static_cast<long long>(rank) * n);
+    hi = lo + min(len - lo, n);
+  }
+};
+// The warps' (m, l), as this block's, to all of the cluster.
+template <int R>
+SF_DEV void unit_tell(const WeighArgs& a, const TreeSeq& q, const float2* s_ml, UnitShared<R>& u, int rank) {
+  if (threadIdx.x >= R) return;
+  const int r = threadIdx.x;
+  float2 v = s_ml[r];
+#pragma unroll
+  for (int k = 1; k < kWarps; ++k) v = weigh_merge(v, s_ml[k * R + r]);
+  if (r >= q.n * a.t.g || weigh_src(a, q.row0 + r / a.t.g) < 0) v = make_float2(INFINITY, 0.f);  // weighs nothing
+  for (int k = 0; k < a.blocks; ++k) {
+    const uint32_t at = dsmem_addr(smem_u32(&u.all[rank][r]), k);
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
+  }
+}
+// Once all have told: the slice's weights from its scores s_x [tokens][R], two threads a token,
+// each with four of eight rows.
+template <int R>
+SF_DEV void unit_weights(const WeighArgs& a, int s, int h, const TreeSeq& q, Slice t, const float* s_x, UnitShared<R>& u) {
+  if (threadIdx.x < R) {
+    const int r = threadIdx.x;
+    float2 v = u.all[0][r];
+    for (int k = 1; k < a.blocks; ++k) v = weigh_merge(v, u.all[k][r]);
+    u.m[r] = v.x;
+    u.rl[r] = merge_scale(v.y);
+  }
+  __syncthreads();
+  const int half = threadIdx.x & 1, rows = q.n * a.t.g;
+  float* wt = a.w.ptr + s * a.w.seq_stride + h * a.w.head_stride;
+  constexpr int K = 4;  // tokens at once
+  for (int first = t.lo; first < t.hi; first += K * (kThreads / 2)) {
+    auto token = [&](int k) { return first + static_cast<int>(threadIdx.x >> 1) + k * (kThreads / 2); };
+    float old[K], sum[K] = {};
+#pragma unroll
+    for (int k = 0; k < K; ++k) old[k] = half == 0 && token(k) < min(t.hi, q.ctx) && a.decay != 0.f ? wt[token(k)] : 0.f;
+    for (int r = 4 * half; r < rows; r += 8) {
+      const float4 m = *reinterpret_cast<const float4*>(u.m + r), rl = *reinterpret_cast<const float4*>(u.rl + r);
+#pragma unroll
+      for (int k = 0; k < K; ++k) {
+        if (token(k) >= t.hi) continue;
+        const float4 x = *reinterpret_cast<const float4*>(s_x + (token(k) - t.lo) * R + r);
+        sum[k] = fmaf(ex2(x.x - m.x), rl.x, sum[k]);
+        sum[k] = fmaf(ex2(x.y - m.y), rl.y, sum[k]);
+        sum[k] = fmaf(ex2(x.z - m.z), rl.z, sum[k]);
+        sum[k] = fmaf(ex2(x.w - m.w), rl.w, sum[k]);
+      }
+    }
+    __syncwarp();
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      const float both = sum[k] + __shfl_xor_sync(0xffffffffu, sum[k], 1);
+      if (half == 0 && token(k) < t.hi) wt[token(k)] = fmaf(a.decay, old[k], both);
+    }
+  }
+}
 
 template <int HD, int NT>
 __global__ void __launch_bounds__(kThreads) weigh_unit_kernel(const __grid_constant__ WeighArgs a) {
@@ -247,78 +316,23 @@ __global__ void __launch_bounds__(kThreads) weigh_unit_kernel(const __grid_const
   const TreeArgs& p = a.t;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[kWarps * R];
-  __shared__ float2 s_all[C::MAX_CLUSTER][R];
-  __shared__ __align__(16) float s_m[R], s_rl[R];
+  __shared__ __align__(16) UnitShared<R> u;
   float* s_x = reinterpret_cast<float*>(smem + C::OFF_S);
   pdl_wait();
   pdl_trigger();
-  const int blocks = a.blocks, rank = static_cast<int>(cluster_ctarank());
-  const int unit = static_cast<int>(blockIdx.x) / blocks, s = unit / p.n_kv, h = unit - s * p.n_kv;
+  const int rank = static_cast<int>(cluster_ctarank()), unit = static_cast<int>(blockIdx.x) / a.blocks;
+  const int s = unit / p.n_kv, h = unit - s * p.n_kv;
   const TreeSeq q = tree_seq(p, s);
   if (q.bad && h == 0 && rank == 0 && threadIdx.x == 0) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
   if (q.n == 0) return;  // the same in all of the cluster
   cluster_arrive();
-  const int rows = q.n * p.g, len = q.ctx + q.n;
-  const int slice = ((len - 1) / blocks / kKeys + 1) * kKeys;
-  const int key_lo = min(static_cast<long long>(len), static_cast<long long>(rank) * slice), key_hi = min(len - key_lo, slice) + key_lo;
-  few_stream<C, HD, NT>(a, s, h, q, key_lo, key_hi, smem, s_ml, [&](int t) { return s_x + (t - key_lo) * R; });
+  const Slice t(q.ctx + q.n, a.blocks, rank);
+  few_stream<C, HD, NT>(a, s, h, q, t.lo, t.hi, smem, s_ml, [&](int tok) { return s_x + (tok - t.lo) * R; });
   __syncthreads();
   cluster_wait();  // all of them have begun
-  if (threadIdx.x < R) {
-    const int r = threadIdx.x;
-    float2 v = s_ml[r];
-#pragma unroll
-    for (int k = 1; k < kWarps; ++k) v = weigh_merge(v, s_ml[k * R + r]);
-    if (r >= rows || weigh_src(a, q.row0 + r / p.g) < 0) v = make_float2(INFINITY, 0.f);  // weighs nothing: 2^(x - inf) = 0
-    for (int k = 0; k < blocks; ++k) {
-      const uint32_t at = dsmem_addr(smem_u32(&s_all[rank][r]), k);
-      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
-    }
-  }
+  unit_tell<R>(a, q, s_ml, u, rank);
   cluster_sync_all();  // the only exchange: a block may end from here on
-  if (threadIdx.x < R) {
-    float2 v = s_all[0][threadIdx.x];
-    for (int k = 1; k < blocks; ++k) v = weigh_merge(v, s_all[k][threadIdx.x]);
-    s_m[threadIdx.x] = v.x;
-    s_rl[threadIdx.x] = merge_scale(v.y);
-  }
-  __syncthreads();
-  // two threads a token, each with four of eight rows
-  const int half = threadIdx.x & 1;
-  float* wt = a.w.ptr + s * a.w.seq_stride + h * a.w.head_stride;
-  float4 m[NT], rl[NT];
-#pragma unroll
-  for (int i = 0; i < NT; ++i) {
-    m[i] = *reinterpret_cast<const float4*>(s_m + 8 * i + 4 * half);
-    rl[i] = *reinterpret_cast<const float4*>(s_rl + 8 * i + 4 * half);
-  }
-  constexpr int K = 4;  // tokens at once
-  for (int first = key_lo; first < key_hi; first += K * (kThreads / 2)) {
-    const int t0 = first + static_cast<int>(threadIdx.x >> 1);
-    float old[K];
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int t = t0 + k * (kThreads / 2);
-      old[k] = half == 0 && t < min(key_hi, q.ctx) && a.decay != 0.f ? wt[t] : 0.f;
-    }
-#pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const int t = t0 + k * (kThreads / 2);
-      float sum = 0.f;
-      if (t < key_hi) {
-#pragma unroll
-        for (int i = 0; i < NT; ++i) {
-          const float4 u = *reinterpret_cast<const float4*>(s_x + (t - key_lo) * R + 8 * i + 4 * half);
-          sum = fmaf(ex2(u.x - m[i].x), rl[i].x, sum);
-          sum = fmaf(ex2(u.y - m[i].y), rl[i].y, sum);
-          sum = fmaf(ex2(u.z - m[i].z), rl[i].z, sum);
-          sum = fmaf(ex2(u.w - m[i].w), rl[i].w, sum);
-        }
-      }
-      sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-      if (half == 0 && t < key_hi) wt[t] = fmaf(a.decay, old[k], sum);
-    }
-  }
+  unit_weights(a, s, h, q, t, s_x, u);
 }
 
 // ------------------------------------------------------------ fp32: few --
@@ -340,10 +354,132 @@ struct WSimt {
   static constexpr int CTAS = 3;
 };
 
+// Rows m0 .. m0 + rows - 1 (at most R) of a block's keys key_lo .. key_hi - 1 of sequence s,
+// head h: the scores to row_of(token) + m0, the warps' statistics to s_ml [kWarps][R].
+template <typename C, int HD, typename RowOf>
+SF_DEV void simt_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int m0, int rows, int key_lo, int key_hi,
+                        uint8_t* smem, float2* s_ml, RowOf row_of) {
+  constexpr int R = C::R, CH = C::CH, PARTS = HD / 32;
+  const TreeArgs& p = a.t;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, len = q.ctx + q.n;
+  uint8_t* ring = smem + warp * C::RING;
+  float* s_q = reinterpret_cast<float*>(smem + C::OFF_Q);
+  const int chunks = (key_hi - key_lo + CH - 1) / CH;
+  const int mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
+  auto key_of = [&](int i) { return key_lo + CH * (warp + kWarps * i); };
+  auto slot_of = [&](int i) {
+    const int tok = key_of(i) + (lane & (CH - 1));
+    return i < mine && tok < key_hi ? tree_pool_token(p, s, tok) : -1;
+  };
+  const float* kbase = static_cast<const float*>(p.cache.k) + h * p.cache.k_head_stride;
+  auto load = [&](int i, int slot) {
+    if (i < mine) {
+      uint8_t* st = ring + (i % C::STAGES) * C::STAGE;
+#pragma unroll
+      for (int it = 0; it < CH * C::CPR / 32; ++it) {
+        const int idx = it * 32 + lane, c = idx % C::CPR, key = idx / C::CPR;
+        const int tk = __shfl_sync(0xffffffffu, slot, key);
+        const long long tz = tk < 0 ? 0 : tk;
+        cp_async16(smem_u32(st + key * C::ROW + ((c ^ (key & 7)) << 4)), kbase + tz * p.cache.k_token_stride + c * 4,
+                   tk < 0 ? 0u : 16u);
+      }
+    }
+    cp_async_commit();
+  };
+  int slot = slot_of(0);
+#pragma unroll
+  for (int i = 0; i < C::STAGES - 1; ++i) {
+    load(i, slot);
+    slot = slot_of(i + 1);
+  }
+  for (int i = threadIdx.x; i < R * (HD / 4); i += kThreads) {
+    const int r = i / (HD / 4), d = (i % (HD / 4)) * 4, m = m0 + min(r, rows - 1);
+    const int src = max(weigh_src(a, q.row0 + m / p.g), 0);
+    *reinterpret_cast<float4*>(s_q + r * HD + d) = *reinterpret_cast<const float4*>(
+        static_cast<const float*>(p.q) + src * p.q_rs + (h * p.g + m % p.g) * p.q_hs + d);
+  }
+  __syncthreads();
+  const int key = lane & (CH - 1), part = lane / CH;
+  auto stream = [&](auto nr) {
+    constexpr int NR = decltype(nr)::value;  // rows worked on
+    constexpr int RP = NR / PARTS;           // of which a lane has RP's sums, from row part * RP on
+    int seen[RP];
+    float m[RP], l[RP];
+#pragma unroll
+    for (int r = 0; r < RP; ++r) {
+      seen[r] = q.ctx + (m0 + min(part * RP + r, rows - 1)) / p.g;
+      m[r] = -INFINITY;
+      l[r] = 0.f;
+    }
+    for (int i = 0; i < mine; ++i) {
+      load(i + C::STAGES - 1, slot);
+      slot = slot_of(i + C::STAGES);
+      cp_async_wait<C::STAGES - 1>();
+      __syncwarp();
+      const uint8_t* sk = ring + (i % C::STAGES) * C::STAGE + key * C::ROW;
+      float x[NR] = {};
+#pragma unroll
+      for (int d0 = 0; d0 < 32; d0 += 4) {
+        // the parts start apart, so that their reads of a query share no bank
+        const int d = part * 32 + ((d0 + part * CH) & 31);
+        const float4 k4 = *reinterpret_cast<const float4*>(sk + (((d >> 2) ^ (key & 7)) << 4));
+#pragma unroll
+        for (int r = 0; r < NR; ++r) {
+          const float4 q4 = *reinterpret_cast<const float4*>(s_q + r * HD + d);
+          x[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, x[r]))));
+        }
+      }
+      // the parts' sums: each step halves the rows that a lane keeps
+#pragma unroll
+      for (int n = NR / 2, o = 16; o >= CH; n /= 2, o /= 2) {
+        const bool upper = lane & o;
+#pragma unroll
+        for (int r = 0; r < n; ++r) {
+          const float keep = upper ? x[n + r] : x[r], give = upper ? x[r] : x[n + r];
+          x[r] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        }
+      }
+      const int tok = key_of(i) + key;
+      const bool tail = key_of(i) + CH > q.ctx;
+#pragma unroll
+      for (int r = 0; r < RP; ++r) {
+        x[r] = tail && tok > seen[r] ? -INFINITY : x[r] * p.sl2;
+        const float top = fmaxf(m[r], x[r]);
+        const float b = top == -INFINITY ? 0.f : top;
+        l[r] = fmaf(l[r], m[r] == top ? 1.f : ex2(m[r] - b), ex2(x[r] - b));
+        m[r] = top;
+      }
+      if (!tail || tok < len) {
+        float* to = row_of(tok) + m0 + part * RP;
+        if constexpr (RP == 4)
+          *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
+        else if constexpr (RP == 2)
+          *reinterpret_cast<float2*>(to) = make_float2(x[0], x[1]);
+        else
+          *to = x[0];
+      }
+      __syncwarp();
+    }
+    cp_async_wait<0>();
+#pragma unroll
+    for (int r = 0; r < RP; ++r) {
+      float2 v = make_float2(m[r], l[r]);
+#pragma unroll
+      for (int o = 1; o < CH; o <<= 1)
+        v = weigh_merge(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
+      if (key == 0) s_ml[warp * R + part * RP + r] = v;
+    }
+  };
+  if (rows <= R / 2)
+    stream(std::integral_constant<int, R / 2>{});
+  else
+    stream(std::integral_constant<int, R>{});
+}
+
 template <int HD>
 __global__ void __launch_bounds__(kThreads, WSimt<HD>::CTAS) weigh_simt_kernel(const __grid_constant__ WeighArgs a) {
   using C = WSimt<HD>;
-  constexpr int R = C::R, CH = C::CH, PARTS = HD / 32;
+  constexpr int R = C::R;
   const TreeArgs& p = a.t;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[kWarps * R];
@@ -352,127 +488,14 @@ __global__ void __launch_bounds__(kThreads, WSimt<HD>::CTAS) weigh_simt_kernel(c
   TreeWalk w;
   unsigned per;
   if (!tree_locate(p, w, per)) return;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  uint8_t* ring = smem + warp * C::RING;
-  float* s_q = reinterpret_cast<float*>(smem + C::OFF_Q);
-
   for (bool first = true; w.n > 0; first = false, w.next(p)) {
-    const int h = w.head, m0 = tree_m0(p, w), rows = tree_tile_rows(p, w);
-    const int len = w.q.ctx + w.q.n, key_lo = w.b0 * p.kb;
-    const int key_hi = min(static_cast<long long>(len), static_cast<long long>(w.b0 + w.n) * p.kb);
+    const int key_lo = w.b0 * p.kb;
+    const int key_hi = min(static_cast<long long>(w.q.ctx + w.q.n), static_cast<long long>(w.b0 + w.n) * p.kb);
     if (threadIdx.x == 0 && w.b0 == 0) weigh_note_span(a, w, first, per);
-    __syncthreads();
-    const int chunks = (key_hi - key_lo + CH - 1) / CH;
-    const int mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
-    auto key_of = [&](int i) { return key_lo + CH * (warp + kWarps * i); };
-    auto slot_of = [&](int i) {
-      const int tok = key_of(i) + (lane & (CH - 1));
-      return i < mine && tok < key_hi ? tree_pool_token(p, w.s, tok) : -1;
-    };
-    const float* kbase = static_cast<const float*>(p.cache.k) + h * p.cache.k_head_stride;
-    auto load = [&](int i, int slot) {
-      if (i < mine) {
-        uint8_t* st = ring + (i % C::STAGES) * C::STAGE;
-#pragma unroll
-        for (int it = 0; it < CH * C::CPR / 32; ++it) {
-          const int idx = it * 32 + lane, c = idx % C::CPR, key = idx / C::CPR;
-          const int tk = __shfl_sync(0xffffffffu, slot, key);
-          const long long tz = tk < 0 ? 0 : tk;
-          cp_async16(smem_u32(st + key * C::ROW + ((c ^ (key & 7)) << 4)), kbase + tz * p.cache.k_token_stride + c * 4,
-                     tk < 0 ? 0u : 16u);
-        }
-      }
-      cp_async_commit();
-    };
-    int slot = slot_of(0);
-#pragma unroll
-    for (int i = 0; i < C::STAGES - 1; ++i) {
-      load(i, slot);
-      slot = slot_of(i + 1);
-    }
-    for (int i = threadIdx.x; i < R * (HD / 4); i += kThreads) {
-      const int r = i / (HD / 4), d = (i % (HD / 4)) * 4, m = m0 + min(r, rows - 1);
-      const int src = max(weigh_src(a, w.q.row0 + m / p.g), 0);
-      *reinterpret_cast<float4*>(s_q + r * HD + d) = *reinterpret_cast<const float4*>(
-          static_cast<const float*>(p.q) + src * p.q_rs + (h * p.g + m % p.g) * p.q_hs + d);
-    }
-    __syncthreads();
-    const int key = lane & (CH - 1), part = lane / CH;
-    auto stream = [&](auto nr) {
-      constexpr int NR = decltype(nr)::value;  // rows worked on
-      constexpr int RP = NR / PARTS;           // of which a lane has RP's sums, from row part * RP on
-      int seen[RP];
-      float m[RP], l[RP];
-#pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        seen[r] = w.q.ctx + (m0 + min(part * RP + r, rows - 1)) / p.g;
-        m[r] = -INFINITY;
-        l[r] = 0.f;
-      }
-      float* out = a.scores + ((static_cast<size_t>(w.s) * p.n_kv + h) * a.w.tokens) * a.score_rows + m0 + part * RP;
-      for (int i = 0; i < mine; ++i) {
-        load(i + C::STAGES - 1, slot);
-        slot = slot_of(i + C::STAGES);
-        cp_async_wait<C::STAGES - 1>();
-        __syncwarp();
-        const uint8_t* sk = ring + (i % C::STAGES) * C::STAGE + key * C::ROW;
-        float s[NR] = {};
-#pragma unroll
-        for (int d0 = 0; d0 < 32; d0 += 4) {
-          // the parts start apart, so that their reads of a query share no bank
-          const int d = part * 32 + ((d0 + part * CH) & 31);
-          const float4 k4 = *reinterpret_cast<const float4*>(sk + (((d >> 2) ^ (key & 7)) << 4));
-#pragma unroll
-          for (int r = 0; r < NR; ++r) {
-            const float4 q4 = *reinterpret_cast<const float4*>(s_q + r * HD + d);
-            s[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, s[r]))));
-          }
-        }
-        // the parts' sums: each step halves the rows that a lane keeps
-#pragma unroll
-        for (int n = NR / 2, o = 16; o >= CH; n /= 2, o /= 2) {
-          const bool upper = lane & o;
-#pragma unroll
-          for (int r = 0; r < n; ++r) {
-            const float keep = upper ? s[n + r] : s[r], give = upper ? s[r] : s[n + r];
-            s[r] = keep + __shfl_xor_sync(0xffffffffu, give, o);
-          }
-        }
-        const int tok = key_of(i) + key;
-        const bool tail = key_of(i) + CH > w.q.ctx;
-#pragma unroll
-        for (int r = 0; r < RP; ++r) {
-          s[r] = tail && tok > seen[r] ? -INFINITY : s[r] * p.sl2;
-          const float top = fmaxf(m[r], s[r]);
-          const float b = top == -INFINITY ? 0.f : top;
-          l[r] = fmaf(l[r], m[r] == top ? 1.f : ex2(m[r] - b), ex2(s[r] - b));
-          m[r] = top;
-        }
-        if (!tail || tok < len) {
-          float* to = out + static_cast<size_t>(tok) * a.score_rows;
-          if constexpr (RP == 4)
-            *reinterpret_cast<float4*>(to) = make_float4(s[0], s[1], s[2], s[3]);
-          else if constexpr (RP == 2)
-            *reinterpret_cast<float2*>(to) = make_float2(s[0], s[1]);
-          else
-            *to = s[0];
-        }
-        __syncwarp();
-      }
-      cp_async_wait<0>();
-#pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        float2 v = make_float2(m[r], l[r]);
-#pragma unroll
-        for (int o = 1; o < CH; o <<= 1)
-          v = weigh_merge(v, make_float2(__shfl_xor_sync(0xffffffffu, v.x, o), __shfl_xor_sync(0xffffffffu, v.y, o)));
-        if (key == 0) s_ml[warp * R + part * RP + r] = v;
-      }
-    };
-    if (rows <= R / 2)
-      stream(std::integral_constant<int, R / 2>{});
-    else
-      stream(std::integral_constant<int, R>{});
+    __syncthreads();  // the previous piece's shared memory is free
+    float* out = a.scores + (static_cast<size_t>(w.s) * p.n_kv + w.head) * a.w.tokens * a.score_rows;
+    simt_stream<C, HD>(a, w.s, w.head, w.q, tree_m0(p, w), tree_tile_rows(p, w), key_lo, key_hi, smem, s_ml,
+                       [&](int t) { return out + static_cast<size_t>(t) * a.score_rows; });
     __syncthreads();
     weigh_write_part<R>(a, w, first, s_ml);
   }
@@ -601,11 +624,18 @@ WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int
   const size_t scores = std::min(rows_all, most) * n_seqs * tokens;
   const bool keeps = scores <= (size_t{1} << 30);
   if (dtype == SPECFOLD_BF16) {
+    // A cluster for a unit, where a slice's scores leave room for three blocks an SM and the
+    // blocks fill the SMs or are short.  Both sides (one launch, two; us; 28 / 4 heads of 128,
+    // one row): 64 x 8000 tokens 82.4 and 86.8, 8 x 500 9.5 and 11.7, 1 x 2047 9.1 and 11.2;
+    // 2 x 8189, 32 / 8 heads 15.9 and 14.7; with up to 100 KB a slice 8 x 20000 63.4 and 34.0.
     const long long units = static_cast<long long>(n_seqs) * n_kv;
     auto slice = [&](int blocks) { return ((tokens - 1) / blocks / kKeys + 1) * kKeys; };
     int blocks = 1;
-    while (blocks < 8 && slice(blocks) > 256 && (slice(blocks) * r8 > kUnitFloats || units * blocks < 2LL * kSmBudget)) blocks *= 2;
-    if (rows <= 16 && static_cast<long long>(slice(blocks)) * r8 <= kUnitMost / 4) {
+    while (blocks < kUnitCluster && slice(blocks) > 256 &&
+           (static_cast<long long>(slice(blocks)) * r8 > kUnitScores || units * blocks < 2LL * kSmBudget))
+      blocks *= 2;
+    if (rows <= 16 && static_cast<long long>(slice(blocks)) * r8 <= kUnitScores &&
+        (units * blocks >= 2LL * kSmBudget || slice(blocks) <= 512)) {
       pl.form = kUnit;
       pl.blocks = blocks;
       pl.slice = slice(blocks);
@@ -641,13 +671,11 @@ int start(void (*kernel)(WeighArgs), const WeighArgs& a, int grid, int threads, 
   return check_launch();
 }
 
-template <int HD, int NT>
-int unit_go(const WeighPlan& pl, WeighArgs& a, cudaStream_t st) {
-  using C = WUnit<HD, NT>;
-  if (const int rc = smem_limit_once(weigh_unit_kernel<HD, NT>, C::OFF_S + kUnitMost)) return rc;
+int unit_start(void (*kernel)(WeighArgs), int smem, const WeighPlan& pl, WeighArgs& a, cudaStream_t st) {
+  if (const int rc = smem_limit_once(kernel, smem + kUnitScores * 4)) return rc;
   a.blocks = pl.blocks;
-  launch_kc(weigh_unit_kernel<HD, NT>, dim3(a.t.batch.n_seqs * a.t.n_kv * pl.blocks), dim3(kThreads),
-            C::OFF_S + pl.slice * C::R * 4, st, pl.blocks, a);
+  launch_kc(kernel, dim3(a.t.batch.n_seqs * a.t.n_kv * pl.blocks), dim3(kThreads), smem + pl.slice * pl.score_rows * 4, st,
+            pl.blocks, a);
   count_launch();
   return check_launch();
 }
@@ -685,7 +713,9 @@ int weigh_go(const KvWeighCall& c, cudaStream_t st) {
   if (pl.form == kTc) return launch_weigh_tc(a, HD, grid, st);
   t.tile_rows = SPECFOLD_MAX_TREE * 128;
   t.kb = kKeys;
-  if (pl.form == kUnit) return pl.score_rows == 8 ? unit_go<HD, 1>(pl, a, st) : unit_go<HD, 2>(pl, a, st);
+  if (pl.form == kUnit)
+    return pl.score_rows == 8 ? unit_start(weigh_unit_kernel<HD, 1>, WUnit<HD, 1>::OFF_S, pl, a, st)
+                              : unit_start(weigh_unit_kernel<HD, 2>, WUnit<HD, 2>::OFF_S, pl, a, st);
   t.tile_rows = pl.stat_rows;
   t.kb = kKeys;
   t.unit_cost = 4;
