@@ -135,18 +135,6 @@ SF_DEV void gather_rows(const WeighArgs& a, const TreeWalk& w, int m0, int rows,
   fence_proxy_async_smem();
 }
 
-// 32 lanes x 16 columns, complete: thread t of the warp gets lane t's.
-SF_DEV void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
-  asm volatile(
-      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
-      "{%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, [%16];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
-      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
-        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
-      : "r"(taddr)
-      : "memory");
-}
-
 // D[128 x n] = A B^T over the HD dimensions of two tiles in shared memory.
 template <int HD>
 SF_DEV void tile_product(bool me, uint32_t d, uint32_t at_a, uint32_t a_atom, uint32_t at_b, uint32_t b_atom, uint32_t idesc) {
@@ -361,8 +349,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_stats_tc_kernel(const __g
 // place while the blocks stream by; with more, a group of RING blocks stays and the
 // tiles pass, back and forth, so that a tile is gathered once for a group.  A
 // product's 128 keys are TMEM's lanes, its rows the columns of one of two buffers;
-// the two halves of the reducing warps have half of the columns each.  Blocks go from
-// a run's last to its first: what the statistics read last is still in L2.
+// the two halves of the reducing warps take alternate blocks, a buffer each, so that
+// none waits for the other.  A row's weight is 2^(x - (m + log2 l)): the one number a
+// row that the sum needs is rounded once more than m alone, by 2^-24 of itself, which
+// is no more than the products' own rounding of the scores, and halves what a score
+// reads of shared memory.  Blocks go from a run's last to its first: what the
+// statistics read last is still in L2.
 struct WItems {  // the order of a unit's products, the same in every role
   int n, tiles, group;
   int g0 = 0, tile_at = 0, dir = 1, done = 0;  // group's first block, tile now, its step, tiles of the group so far
@@ -392,9 +384,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
   __shared__ __align__(8) uint64_t bars[2 * C::RING + 7];
   __shared__ uint32_t tmem_slot_s;
   __shared__ volatile int abort_s;
-  __shared__ __align__(16) float s_m[2][kWeighTcRows], s_rl[2][kWeighTcRows];
-  __shared__ float s_sum[C::RING][256];  // of a group's blocks over the tiles so far, a thread's own
-  __shared__ float xch[2][128];
+  __shared__ __align__(16) float s_off[2][kWeighTcRows];  // -(m + log2 l) of a tile's rows, by turns
+  __shared__ float s_sum[C::RING][kBlock];  // of a group's blocks over the tiles so far
   uint64_t* full = bars;
   uint64_t* empty = bars + C::RING;
   uint64_t* q_full = bars + 2 * C::RING;
@@ -413,7 +404,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
     mbar_init(smem_u32(q_empty), 1);
     for (int i = 0; i < 2; ++i) {
       mbar_init(smem_u32(&d_full[i]), 1);
-      mbar_init(smem_u32(&d_free[i]), 8);
+      mbar_init(smem_u32(&d_free[i]), 4);
     }
     mbar_init(smem_u32(drain), 1);
     *abort_flag = 0;
@@ -479,7 +470,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
       return ok;
     };
     const uint32_t base = uniform(smem_u32(smem)), tm = uniform(tmem);
-    int it = 0, cnt = 0, ql = 0;
+    int it = 0, cnt0 = 0, cnt1 = 0, ql = 0;
     for (; uniform(w.n > 0) && ok; w.next(p)) {
       WItems q(uniform(w.n), uniform(tiles_of()), C::RING);
       bool fresh = true;
@@ -491,13 +482,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
         const int cols = uniform((rows_of(q.tile_at) + 31) & ~31);
         const uint32_t id = idesc_bf16_f32(128, cols, false);
         const int nb = q.blocks();
-        for (int b = 0; b < nb; ++b, ++cnt) {
-          const int i = it + q.g0 + b, buf = cnt & 1;
+        for (int b = 0; b < nb; ++b) {
+          const int i = it + q.g0 + b, buf = i & 1;
+          int& cnt = buf ? cnt1 : cnt0;
           if (q.done == 0 && !wait(&full[i % C::RING], i / C::RING, kSiteAttnKvFull)) break;
-          if (cnt >= 2 && !wait(&d_free[buf], (cnt >> 1) - 1, kSiteAttnSFree)) break;
+          if (cnt > 0 && !wait(&d_free[buf], cnt - 1, kSiteAttnSFree)) break;
           tc_fence_after();
           tile_product<HD>(me, tm + buf * 256, base + C::OFF_RING + (i % C::RING) * C::TILE, kAtom, base, C::Q_ATOM, id);
           warp_commit(me, smem_u32(&d_full[buf]));
+          ++cnt;
         }
         fresh = q.next();
         // another tile follows, or another unit's: the queries are done with once these products are
@@ -512,107 +505,99 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
   } else {
     const int x = (warp - 4) >> 2, key = (warp & 3) * 32 + lane, tid = threadIdx.x - 128;
     const uint32_t lane_off = static_cast<uint32_t>((warp & 3) * 32) << 16;
-    const bool leader = warp == 4 && lane == 0;
-    int it = 0, cnt = 0, ql = 0, outs = 0;
+    const bool leader = (warp & 3) == 0 && lane == 0;
+    const float2 scale2 = make_float2(p.sl2, p.sl2);
+    int it = 0, cnt = 0, ql = 0;
     gather_rows<HD, 256>(a, w, 0, rows_of(0), (rows_of(0) + 31) & ~31, smem, tid);
     named_bar_sync(1, 256);
-    if (lane == 0 && (warp & 3) == 0) mbar_arrive(smem_u32(q_full));
+    if (leader) mbar_arrive(smem_u32(q_full));
     pdl_wait();
-    bool ok = true;
-    for (; w.n > 0 && ok; w.next(p)) {
+    bool ok = true, all_ok = true;  // both halves meet at every tile, also where a wait of one ran out
+    for (; w.n > 0 && all_ok; w.next(p)) {
       const int ctx = w.q.ctx, len = ctx + w.q.n;
       float* wt = a.w.ptr + w.s * a.w.seq_stride + w.head * a.w.head_stride;
       WItems q(w.n, tiles_of(), C::RING);
       bool fresh = true;
-      while (q.g0 < q.n && ok) {
+      while (q.g0 < q.n) {
         if (fresh) {  // the tile's statistics, a thread a row
-          const bool there = tid < rows_of(q.tile_at);
-          float2 v = make_float2(0.f, 0.f);
-          if (there)
-            v = weigh_gather(a, weigh_unit(a, w, q.tile_at), weigh_row_ml(a, w.q.row0, w.head, q.tile_at * kWeighTcRows + tid), tid, 0, 1);
-          s_m[ql & 1][tid] = there ? -v.x : -INFINITY;
-          s_rl[ql & 1][tid] = there ? merge_scale(v.y) : 0.f;
-          if (!named_bar_and(1, 256, ok)) {
-            ok = false;
-            break;
+          float off = -INFINITY;  // no such row, or one that weighs nothing
+          if (tid < rows_of(q.tile_at)) {
+            const float2 v = weigh_gather(a, weigh_unit(a, w, q.tile_at), weigh_row_ml(a, w.q.row0, w.head, q.tile_at * kWeighTcRows + tid), tid, 0, 1);
+            if (v.y != 0.f) off = -(v.x + log2f(v.y));
           }
+          s_off[ql & 1][tid] = off;
+          all_ok = ok = named_bar_and(1, 256, ok);
+          if (!ok) break;
           ++ql;
         }
-        const float *tm_ = s_m[(ql - 1) & 1], *tr = s_rl[(ql - 1) & 1];
-        const int half = (rows_of(q.tile_at) + 31) / 32 * 16, m0 = q.tile_at * kWeighTcRows;
-        const bool single = q.tiles == 1, last = q.last();
+        const float* so = s_off[(ql - 1) & 1];
+        const int cols = (rows_of(q.tile_at) + 31) & ~31, m0 = q.tile_at * kWeighTcRows;
+        const bool last = q.last();
         const int nb = q.blocks();
-        for (int b = 0; b < nb; ++b, ++cnt) {
-          const int buf = cnt & 1;
+        for (int b = (x ^ (it + q.g0)) & 1; b < nb; b += 2, ++cnt) {
           const long long t0 = static_cast<long long>(w.b0 + q.n - 1 - (q.g0 + b)) * kBlock;
           const bool tail = t0 + kBlock > ctx;
-          const bool mine = last && x == 0 && t0 + key < len;  // this thread writes a weight
+          const bool mine = last && t0 + key < len;  // this thread writes a weight
           const float old = mine && t0 + key < ctx && a.decay != 0.f ? wt[t0 + key] : 0.f;
-          ok = __all_sync(0xffffffffu, ok && mbar_wait(smem_u32(&d_full[buf]), (cnt >> 1) & 1, abort_flag, p.status,
-                                                       kWaitLimitNs, kSiteAttnSFull));
-          float sum = 0.f;
-          if (ok) {
-            tc_fence_after();
-            if (leader && last) mbar_arrive(smem_u32(&empty[(it + q.g0 + b) % C::RING]));
-            // the first row that sees this key
-            const int from = tail ? static_cast<int>(min(max(t0 + key - ctx, 0ll) * p.g - m0, 1ll << 20)) : 0;
-            const float2 scale2 = make_float2(p.sl2, p.sl2);
-            float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-            // N columns from c0 on, loaded into s
-            auto add = [&](const auto& s, int c0) {
-              constexpr int N = sizeof(s) / sizeof(s[0]);
+          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&d_full[x]), cnt & 1, abort_flag, p.status, kWaitLimitNs,
+                                                 kSiteAttnSFull));
+          if (!ok) break;
+          tc_fence_after();
+          if (leader && last) mbar_arrive(smem_u32(&empty[(it + q.g0 + b) % C::RING]));
+          // the first row that sees this key
+          const int from = tail ? static_cast<int>(min(max(t0 + key - ctx, 0ll) * p.g - m0, 1ll << 20)) : 0;
+          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+          auto add = [&](const uint32_t(&s)[32], int c0, auto is_tail) {
 #pragma unroll
-              for (int e = 0; e < N; e += 4) {
-                const float4 m4 = *reinterpret_cast<const float4*>(tm_ + c0 + e);
-                const float4 r4 = *reinterpret_cast<const float4*>(tr + c0 + e);
-                float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, make_float2(m4.x, m4.y));
-                float2 z = fma2(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), scale2, make_float2(m4.z, m4.w));
-                if (tail) {
-                  if (c0 + e < from) y.x = -INFINITY;
-                  if (c0 + e + 1 < from) y.y = -INFINITY;
-                  if (c0 + e + 2 < from) z.x = -INFINITY;
-                  if (c0 + e + 3 < from) z.y = -INFINITY;
-                }
-                // (a row that weighs nothing has -inf and 0)
-                acc[0] = fma2(make_float2(ex2(y.x), ex2(y.y)), make_float2(r4.x, r4.y), acc[0]);
-                acc[1] = fma2(make_float2(ex2(z.x), ex2(z.y)), make_float2(r4.z, r4.w), acc[1]);
+            for (int e = 0; e < 32; e += 4) {
+              const float4 o4 = *reinterpret_cast<const float4*>(so + c0 + e);
+              float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, make_float2(o4.x, o4.y));
+              float2 z = fma2(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), scale2, make_float2(o4.z, o4.w));
+              if constexpr (decltype(is_tail)::value) {
+                if (c0 + e < from) y.x = -INFINITY;
+                if (c0 + e + 1 < from) y.y = -INFINITY;
+                if (c0 + e + 2 < from) z.x = -INFINITY;
+                if (c0 + e + 3 < from) z.y = -INFINITY;
               }
-            };
-            const uint32_t at = tmem + lane_off + buf * 256;
-            int c = x * half;
+              acc[0] = add2(acc[0], make_float2(ex2(y.x), ex2(y.y)));
+              acc[1] = add2(acc[1], make_float2(ex2(z.x), ex2(z.y)));
+            }
+          };
+          // 32 columns at a time, the next ones on their way
+          const uint32_t at = tmem + lane_off + x * 256;
+          uint32_t s0[32], s1[32];
+          auto loaded = [&](uint32_t(&s)[32], uint32_t(&then)[32], int c) {
+            tmem_ld_wait(s);
+            if (c + 32 < cols) {
+              tmem_ld32(at + c + 32, then);
+            } else {
+              tc_fence_before();
+              __syncwarp();
+              if (lane == 0) mbar_arrive(smem_u32(&d_free[x]));
+            }
+          };
+          auto columns = [&](auto is_tail) {
+            tmem_ld32(at, s0);
 #pragma unroll 1
-            for (; c + 32 <= (x + 1) * half; c += 32) {
-              uint32_t s[32];
-              tmem_ld32(at + c, s);
-              tmem_ld_wait(s);
-              add(s, c);
+            for (int c = 0; c < cols; c += 64) {
+              loaded(s0, s1, c);
+              add(s0, c, is_tail);
+              if (c + 32 < cols) {
+                loaded(s1, s0, c + 32);
+                add(s1, c + 32, is_tail);
+              }
             }
-            if (c < (x + 1) * half) {
-              uint32_t s[16];
-              tmem_ld16(at + c, s);
-              add(s, c);
-            }
-            tc_fence_before();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(smem_u32(&d_free[buf]));
-            sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-            if (!single) {
-              if (q.done > 0) sum += s_sum[b][tid];
-              s_sum[b][tid] = sum;
-            }
+          };
+          if (tail)
+            columns(std::true_type{});
+          else
+            columns(std::false_type{});
+          float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+          if (q.tiles > 1) {
+            if (q.done > 0) sum += s_sum[b][key];
+            s_sum[b][key] = sum;
           }
-          if (last) {  // the halves of the rows together
-            if (x == 1) xch[outs & 1][key] = sum;
-            if (!named_bar_and(1, 256, ok)) {
-              ok = false;
-              break;
-            }
-            if (mine) {
-              sum += xch[outs & 1][key];
-              wt[t0 + key] = fmaf(a.decay, old, sum);
-            }
-            ++outs;
-          }
+          if (mine) wt[t0 + key] = fmaf(a.decay, old, sum);
         }
         fresh = q.next();
       }

@@ -240,6 +240,16 @@ def test_kv_weigh_groups_of_rows(B, dt, rows, g, hd):
     b.check(before, host(b.w), 0.75)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("counts", [[40, 17, 5, 90], [3, 200, 33, 16], [65, 64, 63, 32], [16, 8, 15, 7]])
+def test_kv_weigh_runs_of_many_blocks(B, hd, counts):
+    """Of one, two and more tiles of rows a head group, a run of blocks passing from one to the next."""
+    b = Weigh(B, np.random.default_rng(hd), "bf16", hd, 64, 8, 16, "split", counts, [9000, 7011, 6100, 10007])
+    before = host(b.w)
+    b.call(0.5)
+    b.check(before, host(b.w), 0.5)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 def test_kv_weigh_rows_in_parts(B, dt):
     """Rows weighed a part at a time, each behind the tokens of the parts before."""
