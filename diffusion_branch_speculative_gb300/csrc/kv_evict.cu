@@ -32,7 +32,7 @@ SF_DEV uint32_t weight_key(float x) {
 constexpr int kSelThreads = 512, kSelWarps = kSelThreads / 32;
 constexpr int kSelBins = 2048;           // of a pass over 11, 11 and 10 bits of the keys
 constexpr int kSelGroups = kSelBins / 32;
-constexpr int kSelCap = 48 * 1024;       // keys of a block's slice that shared memory holds
+constexpr int kSelCap = 48 * 1024;       // keys of a block's slice that shared memory holds (longer ones are read each pass)
 constexpr int kSelMaxCluster = 8;
 constexpr int kSelSlice = 4096;          // tokens that are worth a block more
 constexpr int kSelStep = 1024;           // keys of a warp's step, 32 a lane
@@ -65,7 +65,7 @@ SF_DEV int find_from_last(int2 h, int lane, int& left) {
 // groups and bins 4).  Then every warp writes what it has of its run of the slice, behind
 // what lies before.  Measured (3 sequences of 131071 tokens at most, 8 sets): see below.
 template <bool CLUSTER>
-__global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_constant__ SelectArgs p) {
+__global__ void __launch_bounds__(kSelThreads, 4) kv_select_kernel(const __grid_constant__ SelectArgs p) {
   extern __shared__ __align__(16) uint32_t s_key[];
   __shared__ int s_hist[2][kSelBins];
   __shared__ __align__(8) int s_group[2][kSelMaxCluster][kSelGroups];  // the blocks' sums of this pass
@@ -123,14 +123,9 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     // Keys in pieces of four, piece c of eight at c ^ (the eight's number mod 8): a warp reads
     // 32 pieces side by side or eight apart without conflicts.  Zeros past the end.
     auto place = [](int i) { return i ^ ((i >> 5 & 7) << 2); };
-    auto keys = [&](int i, uint32_t (&k)[4]) {  // i .. i + 3, i a multiple of four
-      if constexpr (kHeld) {
-        const uint4 u = *reinterpret_cast<const uint4*>(s_key + place(i));
-        k[0] = u.x, k[1] = u.y, k[2] = u.z, k[3] = u.w;
-      } else {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) k[j] = i + j < n ? weight_key(w[i + j]) : 0u;
-      }
+    auto keys = [&](int i, uint32_t (&k)[4]) {  // held: i .. i + 3, i a multiple of four
+      const uint4 u = *reinterpret_cast<const uint4*>(s_key + place(i));
+      k[0] = u.x, k[1] = u.y, k[2] = u.z, k[3] = u.w;
     };
     // the keys, and the first pass
 #pragma unroll 8
@@ -195,13 +190,21 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
         for (int i = threadIdx.x; i < kSelBins; i += kSelThreads) to[i] = 0;
         __syncthreads();
       }
+      if constexpr (kHeld) {
 #pragma unroll 2
-      for (int i = 4 * threadIdx.x; i < n; i += 4 * kSelThreads) {
-        uint32_t k[4];
-        keys(i, k);
+        for (int i = 4 * threadIdx.x; i < n; i += 4 * kSelThreads) {
+          uint32_t k[4];
+          keys(i, k);
 #pragma unroll
-        for (int j = 0; j < 4; ++j)
-          if (k[j] >> shift == prefix && i + j < n) atomicAdd(&to[(k[j] >> next) & mask], 1);
+          for (int j = 0; j < 4; ++j)
+            if (k[j] >> shift == prefix && i + j < n) atomicAdd(&to[(k[j] >> next) & mask], 1);
+        }
+      } else {
+#pragma unroll 8
+        for (int i = threadIdx.x; i < n; i += kSelThreads) {
+          const uint32_t k = weight_key(w[i]);
+          if (k >> shift == prefix) atomicAdd(&to[(k >> next) & mask], 1);
+        }
       }
       shift = next;
     }
@@ -213,14 +216,24 @@ __global__ void __launch_bounds__(kSelThreads) kv_select_kernel(const __grid_con
     auto marks = [&](int st) {
       gt = eq = 0u;
       const int i = st * kSelStep + 32 * lane;
+      if constexpr (kHeld) {
 #pragma unroll
-      for (int c = 0; c < 8; ++c) {
-        uint32_t k[4];
-        keys(i + 4 * c, k);
+        for (int c = 0; c < 8; ++c) {
+          uint32_t k[4];
+          keys(i + 4 * c, k);
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          gt |= (k[j] >> shift > prefix ? 1u : 0u) << (4 * c + j);
-          eq |= (k[j] >> shift == prefix ? 1u : 0u) << (4 * c + j);
+          for (int j = 0; j < 4; ++j) {
+            gt |= (k[j] >> shift > prefix ? 1u : 0u) << (4 * c + j);
+            eq |= (k[j] >> shift == prefix ? 1u : 0u) << (4 * c + j);
+          }
+        }
+      } else {  // read side by side, a word of marks a lane
+#pragma unroll 8
+        for (int c = 0; c < 32; ++c) {
+          const int at = st * kSelStep + 32 * c + lane;
+          const uint32_t k = at < n ? weight_key(w[at]) : 0u;
+          const uint32_t g = __ballot_sync(0xffffffffu, k >> shift > prefix), e = __ballot_sync(0xffffffffu, k >> shift == prefix);
+          if (lane == c) gt = g, eq = e;
         }
       }
       const int there = n - i;  // (what lies past the end is a key of zero)
@@ -402,9 +415,14 @@ __global__ void __launch_bounds__(Move<CLUSTER>::THREADS) kv_compact_kernel(cons
 
 int launch_kv_select(const KvSelectCall& c, cudaStream_t st) {
   SelectArgs a{c.w, c.kept, c.lengths, c.new_len, c.status, c.keep, c.sinks, c.recent, 1, 0};
-  // Blocks a cluster: more while that leaves two a SM, and slices of some length.
+  // Blocks a cluster: more while slices are of some length and either the blocks are no more
+  // than the SMs or a slice's keys leave an SM no second block (64 sequences of 60000 tokens and
+  // 8 sets: 109 us with slices of 15000, 123 with 7500, 127 with 30000, 184 with one block a unit,
+  // which cannot hold its keys; 32 of 120000: 116 with slices of 15000, 263 with one block).
   const long long units = static_cast<long long>(c.n_seqs) * c.kept.n_sets;
-  while (a.blocks < kSelMaxCluster && c.w.tokens / a.blocks > kSelSlice && units * a.blocks * 2 <= 2LL * num_sms()) a.blocks *= 2;
+  while (a.blocks < kSelMaxCluster && c.w.tokens / a.blocks > kSelSlice &&
+         (units * a.blocks * 2 <= 2LL * num_sms() || c.w.tokens / a.blocks > kSelCap / 2))
+    a.blocks *= 2;
   const int slice = (c.w.tokens - 1) / a.blocks / kSelStep * kSelStep + kSelStep;
   a.held = slice < kSelCap ? slice : kSelCap;
   const int smem = a.held * 4;

@@ -453,6 +453,16 @@ def test_kv_select_long(B, tokens, S, U):
                 assert np.array_equal(got, np.concatenate([np.arange(sinks), best, np.arange(n - recent, n)]))
 
 
+@pytest.mark.parametrize("tokens,S,U", [(26011, 40, 5), (60007, 40, 5), (110003, 26, 6)])
+def test_kv_select_many_long(B, tokens, S, U):
+    """More sets than SMs, of more keys than two blocks of an SM hold."""
+    rng = np.random.default_rng(tokens)
+    w = torch.from_numpy(rng.random((S, U, tokens), dtype=np.float32) ** 4).cuda()
+    lengths = rng.integers(1, tokens + 1, S)
+    lengths[:3] = [tokens, 2048, 2049]
+    check_select(B, w, lengths, 2048, 4, 64)
+
+
 def test_kv_select_many_and_strided(B):
     rng = np.random.default_rng(1)
     S, U = 1024, 3
