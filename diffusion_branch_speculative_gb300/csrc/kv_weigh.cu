@@ -36,8 +36,9 @@ SF_DEV void weigh_write_part(const WeighArgs& p, const TreeWalk& w, bool first, 
 // that one token with a group of seven heads wastes one column in eight; the
 // scores go to the workspace, 32 bytes a token and eight rows, where the second
 // launch finds them in L2 rather than the keys in DRAM.
-template <int HD, int NT, int STAGES_ = 3>
+template <int HD, int NT, int STAGES_ = 3, int WARPS_ = kWarps>
 struct WFew {
+  static constexpr int WARPS = WARPS_;
   static constexpr int R = 8 * NT;
   static constexpr int CH = 2048 / HD;  // keys of a warp's step: 4 KB
   static constexpr int STAGES = STAGES_;
@@ -45,7 +46,7 @@ struct WFew {
   static constexpr int CPR = ROW / 16;
   static constexpr int STAGE = CH * ROW;
   static constexpr int RING = STAGES * STAGE;
-  static constexpr int OFF_Q = kWarps * RING;
+  static constexpr int OFF_Q = WARPS * RING;
   static constexpr int SMEM = OFF_Q + R * ROW;
   static constexpr int CTAS = 4;  // per SM
 };
@@ -56,7 +57,7 @@ template <typename C, int HD, int NT, typename RowOf>
 SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int key_lo, int key_hi, uint8_t* smem, float2* s_ml,
                        RowOf row_of) {
   using T = __nv_bfloat16;
-  constexpr int R = C::R, KS = HD / 16, CH = C::CH, KH = CH / 16;
+  constexpr int R = C::R, KS = HD / 16, CH = C::CH, KH = CH / 16, WARPS = C::WARPS;
   const TreeArgs& p = a.t;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t once = policy_evict_first();  // the keys: L2 is for the scores
@@ -65,18 +66,18 @@ SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int k
   const int rows = q.n * p.g, len = q.ctx + q.n;
   // this warp's chunks: key_lo + CH * (warp + 4 i)
   const int chunks = (key_hi - key_lo + CH - 1) / CH;
-  const int mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
-  auto key_of = [&](int i) { return key_lo + CH * (warp + kWarps * i); };
+  const int mine = chunks > warp ? (chunks - warp + WARPS - 1) / WARPS : 0;
+  auto key_of = [&](int i) { return key_lo + CH * (warp + WARPS * i); };
   // lanes 0..CH-1 have a chunk's keys; a chunk's pages are read two chunks ahead of its
   // loads, and followed by steps (no division a chunk)
   const int32_t* table = p.cache.block_table + s * p.cache.table_stride;
-  const int ps = p.cache.page_size, dpg = CH * kWarps / ps, doff = CH * kWarps - dpg * ps;
+  const int ps = p.cache.page_size, dpg = CH * WARPS / ps, doff = CH * WARPS - dpg * ps;
   struct Page {
     int id, off;  // in the table; a key's place in it, -1: no key
   };
   const unsigned tok0 = static_cast<unsigned>(key_lo) + CH * warp + (lane & (CH - 1));
   int pg = tok0 / static_cast<unsigned>(ps), off = tok0 - pg * ps;
-  int left = key_hi > static_cast<int>(tok0) ? (key_hi - static_cast<int>(tok0) + CH * kWarps - 1) / (CH * kWarps) : 0;  // this lane's keys
+  int left = key_hi > static_cast<int>(tok0) ? (key_hi - static_cast<int>(tok0) + CH * WARPS - 1) / (CH * WARPS) : 0;  // this lane's keys
   auto page_next = [&]() {
     Page x = {-1, left > 0 ? off : -1};
     if (left > 0 && pg < p.cache.table_pages) x.id = table[pg];
@@ -120,7 +121,7 @@ SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int k
   }
   // queries: row m = row m / g of the sequence, head m % g of the group; the rows
   // past the last are its copies (zeros times an infinite key would be NaN)
-  for (int i = threadIdx.x; i < R * C::CPR; i += kThreads) {
+  for (int i = threadIdx.x; i < R * C::CPR; i += 32 * WARPS) {
     const int r = i / C::CPR, c = i % C::CPR, m = min(r, rows - 1);
     const int src = max(weigh_src(a, q.row0 + m / p.g), 0);
     *reinterpret_cast<uint4*>(s_q + r * C::ROW + ((c ^ (r & 7)) << 4)) =
@@ -235,8 +236,10 @@ __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel
 constexpr int kUnitCluster = 8;        // blocks at most
 constexpr int kUnitScores = 8 * 1024;  // of a slice, at most
 template <int HD, int NT>
-struct WUnit : WFew<HD, NT, 2> {
-  static constexpr int OFF_S = WFew<HD, NT, 2>::SMEM;                 // [tokens of a slice][R]
+struct WUnit : WFew<HD, NT, 2, NT == 1 ? 5 : 4> {
+  using Base = WFew<HD, NT, 2, NT == 1 ? 5 : 4>;  // as many warps as leave room for three blocks an SM
+  static constexpr int THREADS = 32 * Base::WARPS;
+  static constexpr int OFF_S = Base::SMEM;        // [tokens of a slice][R]
 };
 
 // What a cluster's blocks share of a unit: every block's statistics of its rows.
@@ -255,13 +258,13 @@ struct Slice {
   }
 };
 // The warps' (m, l), as this block's, to all of the cluster.
-template <int R>
+template <int R, int WARPS>
 SF_DEV void unit_tell(const WeighArgs& a, const TreeSeq& q, const float2* s_ml, UnitShared<R>& u, int rank) {
   if (threadIdx.x >= R) return;
   const int r = threadIdx.x;
   float2 v = s_ml[r];
 #pragma unroll
-  for (int k = 1; k < kWarps; ++k) v = weigh_merge(v, s_ml[k * R + r]);
+  for (int k = 1; k < WARPS; ++k) v = weigh_merge(v, s_ml[k * R + r]);
   if (r >= q.n * a.t.g || weigh_src(a, q.row0 + r / a.t.g) < 0) v = make_float2(INFINITY, 0.f);  // weighs nothing
   for (int k = 0; k < a.blocks; ++k) {
     const uint32_t at = dsmem_addr(smem_u32(&u.all[rank][r]), k);
@@ -270,7 +273,7 @@ SF_DEV void unit_tell(const WeighArgs& a, const TreeSeq& q, const float2* s_ml, 
 }
 // Once all have told: the slice's weights from its scores s_x [tokens][R], two threads a token,
 // each with four of eight rows.
-template <int R>
+template <int R, int THREADS>
 SF_DEV void unit_weights(const WeighArgs& a, int s, int h, const TreeSeq& q, Slice t, const float* s_x, UnitShared<R>& u) {
   if (threadIdx.x < R) {
     const int r = threadIdx.x;
@@ -283,8 +286,8 @@ SF_DEV void unit_weights(const WeighArgs& a, int s, int h, const TreeSeq& q, Sli
   const int half = threadIdx.x & 1, rows = q.n * a.t.g;
   float* wt = a.w.ptr + s * a.w.seq_stride + h * a.w.head_stride;
   constexpr int K = 4;  // tokens at once
-  for (int first = t.lo; first < t.hi; first += K * (kThreads / 2)) {
-    auto token = [&](int k) { return first + static_cast<int>(threadIdx.x >> 1) + k * (kThreads / 2); };
+  for (int first = t.lo; first < t.hi; first += K * (THREADS / 2)) {
+    auto token = [&](int k) { return first + static_cast<int>(threadIdx.x >> 1) + k * (THREADS / 2); };
     float old[K], sum[K] = {};
 #pragma unroll
     for (int k = 0; k < K; ++k) old[k] = half == 0 && token(k) < min(t.hi, q.ctx) && a.decay != 0.f ? wt[token(k)] : 0.f;
@@ -310,12 +313,12 @@ SF_DEV void unit_weights(const WeighArgs& a, int s, int h, const TreeSeq& q, Sli
 }
 
 template <int HD, int NT>
-__global__ void __launch_bounds__(kThreads) weigh_unit_kernel(const __grid_constant__ WeighArgs a) {
+__global__ void __launch_bounds__(WUnit<HD, NT>::THREADS) weigh_unit_kernel(const __grid_constant__ WeighArgs a) {
   using C = WUnit<HD, NT>;
   constexpr int R = C::R;
   const TreeArgs& p = a.t;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 s_ml[kWarps * R];
+  __shared__ float2 s_ml[C::WARPS * R];
   __shared__ __align__(16) UnitShared<R> u;
   float* s_x = reinterpret_cast<float*>(smem + C::OFF_S);
   pdl_wait();
@@ -330,9 +333,9 @@ __global__ void __launch_bounds__(kThreads) weigh_unit_kernel(const __grid_const
   few_stream<C, HD, NT>(a, s, h, q, t.lo, t.hi, smem, s_ml, [&](int tok) { return s_x + (tok - t.lo) * R; });
   __syncthreads();
   cluster_wait();  // all of them have begun
-  unit_tell<R>(a, q, s_ml, u, rank);
+  unit_tell<R, C::WARPS>(a, q, s_ml, u, rank);
   cluster_sync_all();  // the only exchange: a block may end from here on
-  unit_weights(a, s, h, q, t, s_x, u);
+  unit_weights<R, C::THREADS>(a, s, h, q, t, s_x, u);
 }
 
 // ------------------------------------------------------------ fp32: few --
@@ -671,10 +674,10 @@ int start(void (*kernel)(WeighArgs), const WeighArgs& a, int grid, int threads, 
   return check_launch();
 }
 
-int unit_start(void (*kernel)(WeighArgs), int smem, const WeighPlan& pl, WeighArgs& a, cudaStream_t st) {
+int unit_start(void (*kernel)(WeighArgs), int threads, int smem, const WeighPlan& pl, WeighArgs& a, cudaStream_t st) {
   if (const int rc = smem_limit_once(kernel, smem + kUnitScores * 4)) return rc;
   a.blocks = pl.blocks;
-  launch_kc(kernel, dim3(a.t.batch.n_seqs * a.t.n_kv * pl.blocks), dim3(kThreads), smem + pl.slice * pl.score_rows * 4, st,
+  launch_kc(kernel, dim3(a.t.batch.n_seqs * a.t.n_kv * pl.blocks), dim3(threads), smem + pl.slice * pl.score_rows * 4, st,
             pl.blocks, a);
   count_launch();
   return check_launch();
@@ -714,8 +717,8 @@ int weigh_go(const KvWeighCall& c, cudaStream_t st) {
   t.tile_rows = SPECFOLD_MAX_TREE * 128;
   t.kb = kKeys;
   if (pl.form == kUnit)
-    return pl.score_rows == 8 ? unit_start(weigh_unit_kernel<HD, 1>, WUnit<HD, 1>::OFF_S, pl, a, st)
-                              : unit_start(weigh_unit_kernel<HD, 2>, WUnit<HD, 2>::OFF_S, pl, a, st);
+    return pl.score_rows == 8 ? unit_start(weigh_unit_kernel<HD, 1>, WUnit<HD, 1>::THREADS, WUnit<HD, 1>::OFF_S, pl, a, st)
+                              : unit_start(weigh_unit_kernel<HD, 2>, WUnit<HD, 2>::THREADS, WUnit<HD, 2>::OFF_S, pl, a, st);
   t.tile_rows = pl.stat_rows;
   t.kb = kKeys;
   t.unit_cost = 4;

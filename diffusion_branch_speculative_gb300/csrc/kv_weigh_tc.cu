@@ -523,7 +523,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
           float off = -INFINITY;  // no such row, or one that weighs nothing
           if (tid < rows_of(q.tile_at)) {
             const float2 v = weigh_gather(a, weigh_unit(a, w, q.tile_at), weigh_row_ml(a, w.q.row0, w.head, q.tile_at * kWeighTcRows + tid), tid, 0, 1);
-            if (v.y != 0.f) off = -(v.x + log2f(v.y));
+            if (v.x != INFINITY || v.y != 0.f) off = -(v.x + log2f(v.y));
           }
           s_off[ql & 1][tid] = off;
           all_ok = ok = named_bar_and(1, 256, ok);

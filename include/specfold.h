@@ -94,8 +94,8 @@ extern "C" {
 #define SPECFOLD_DEV_SITE_SHIFT 8
 
 #define SPECFOLD_MAX_ROWS 16384     /* largest B*L */
-#define SPECFOLD_MAX_SEQS 1024      /* sequences of one batch (specfold_kv_append, specfold_tree_attention) */
-#define SPECFOLD_MAX_TREE 256       /* drafted rows of one sequence (specfold_tree_attention) */
+#define SPECFOLD_MAX_SEQS 1024      /* sequences of one batch (the calls on a decoder's cache) */
+#define SPECFOLD_MAX_TREE 256       /* rows of one sequence (specfold_tree_attention, specfold_kv_weigh) */
 #define SPECFOLD_MAX_HEADS 65536    /* heads of one kind (the calls on a decoder's cache) */
 #define SPECFOLD_TREE_PAD -2        /* parent of a padding row (specfold_tree_attention) */
 #define SPECFOLD_MAX_AXES 4         /* axes of a position (specfold_rope_axes) */
@@ -637,8 +637,10 @@ typedef struct {
  * (SPECFOLD_DEV_BAD_SEQ); a sequence whose row_start, ctx_len or row count is
  * invalid or that has more than w.tokens tokens keeps its weights (the same
  * bit), as do all where the batch counts more blocks of keys than
- * specfold_tree_attention takes; a page outside the pool or a token past the table reads as a key of
- * zeros (SPECFOLD_DEV_BAD_PAGE).
+ * specfold_tree_attention takes; the weights of sequences that share rows, as
+ * only a row_start that falls in between has them, are unspecified.  A page
+ * outside the pool or a token past the table reads as a key of zeros
+ * (SPECFOLD_DEV_BAD_PAGE).
  * Products of bf16 values are summed in 32 bits, softmax and weights are 32
  * bits; results do not depend on timing.
  * head_dim 64 or 128; n_q / n_kv at most 128.  ws: as
@@ -646,8 +648,9 @@ typedef struct {
  * the same T (or a larger one), max_rows, n_seqs and w.tokens.  With
  * max_rows * g up to 16 and, for fp32, always, it holds the scores: four bytes
  * for every token of n_seqs * n_kv times w.tokens and every row of a group, in
- * eights (bf16: none where they are few or 1 GB and more).  A batch's rows may also be weighed a part
- * at a time, each part behind the tokens of the parts before (decay 1). */
+ * eights (bf16: none where they are few or 1 GB and more).  A batch's rows may
+ * also be weighed a part at a time, each part behind the tokens of the parts
+ * before (decay 1). */
 int specfold_kv_weigh(int dtype, int T, int max_rows, int n_q, int n_kv, int head_dim, specfold_head_rows q, int n_src,
                       const int32_t* rows, const specfold_paged_cache* cache, const int32_t* row_start,
                       const int32_t* ctx_len, int n_seqs, float scale, float decay, specfold_token_weights w, void* ws,
