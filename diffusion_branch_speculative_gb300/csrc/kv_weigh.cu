@@ -36,48 +36,50 @@ SF_DEV void weigh_write_part(const WeighArgs& p, const TreeWalk& w, bool first, 
 // that one token with a group of seven heads wastes one column in eight; the
 // scores go to the workspace, 32 bytes a token and eight rows, where the second
 // launch finds them in L2 rather than the keys in DRAM.
-template <int HD, int NT, int STAGES_ = 3, int WARPS_ = kWarps>
+template <int HD, int NT>
 struct WFew {
-  static constexpr int WARPS = WARPS_;
   static constexpr int R = 8 * NT;
   static constexpr int CH = 2048 / HD;  // keys of a warp's step: 4 KB
-  static constexpr int STAGES = STAGES_;
+  static constexpr int STAGES = 3;
   static constexpr int ROW = HD * 2;
   static constexpr int CPR = ROW / 16;
   static constexpr int STAGE = CH * ROW;
   static constexpr int RING = STAGES * STAGE;
-  static constexpr int OFF_Q = WARPS * RING;
+  static constexpr int OFF_Q = kWarps * RING;
   static constexpr int SMEM = OFF_Q + R * ROW;
   static constexpr int CTAS = 4;  // per SM
 };
 
-// A block's keys key_lo .. key_hi - 1 of sequence s, head h: the scores to row_of(token)
-// [R], the warps' statistics to s_ml [kWarps][R].
-template <typename C, int HD, int NT, typename RowOf>
+// A block's keys key_lo .. key_hi - 1 of sequence s, head h: the warps' statistics to s_ml
+// [kWarps][R], the scores to keep(i, kh, x): this warp's step i, 16 of its keys, x[nt][2 e + f]
+// the score of the key lane / 4 + 8 e and the row 8 nt + 2 (lane % 4) + f.  STEPS: a warp's at
+// most, all of them unrolled; 0: any number.
+template <int HD, int NT, int STEPS, typename Keep>
 SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int key_lo, int key_hi, uint8_t* smem, float2* s_ml,
-                       RowOf row_of) {
+                       Keep keep) {
+  using C = WFew<HD, NT>;
   using T = __nv_bfloat16;
-  constexpr int R = C::R, KS = HD / 16, CH = C::CH, KH = CH / 16, WARPS = C::WARPS;
+  constexpr int R = C::R, KS = HD / 16, CH = C::CH, KH = CH / 16;
   const TreeArgs& p = a.t;
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   const uint64_t once = policy_evict_first();  // the keys: L2 is for the scores
   uint8_t* ring = smem + warp * C::RING;
   uint8_t* s_q = smem + C::OFF_Q;
-  const int rows = q.n * p.g, len = q.ctx + q.n;
+  const int rows = q.n * p.g;
   // this warp's chunks: key_lo + CH * (warp + 4 i)
   const int chunks = (key_hi - key_lo + CH - 1) / CH;
-  const int mine = chunks > warp ? (chunks - warp + WARPS - 1) / WARPS : 0;
-  auto key_of = [&](int i) { return key_lo + CH * (warp + WARPS * i); };
+  const int mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
+  auto key_of = [&](int i) { return key_lo + CH * (warp + kWarps * i); };
   // lanes 0..CH-1 have a chunk's keys; a chunk's pages are read two chunks ahead of its
   // loads, and followed by steps (no division a chunk)
   const int32_t* table = p.cache.block_table + s * p.cache.table_stride;
-  const int ps = p.cache.page_size, dpg = CH * WARPS / ps, doff = CH * WARPS - dpg * ps;
+  const int ps = p.cache.page_size, dpg = CH * kWarps / ps, doff = CH * kWarps - dpg * ps;
   struct Page {
     int id, off;  // in the table; a key's place in it, -1: no key
   };
   const unsigned tok0 = static_cast<unsigned>(key_lo) + CH * warp + (lane & (CH - 1));
   int pg = tok0 / static_cast<unsigned>(ps), off = tok0 - pg * ps;
-  int left = key_hi > static_cast<int>(tok0) ? (key_hi - static_cast<int>(tok0) + CH * WARPS - 1) / (CH * WARPS) : 0;  // this lane's keys
+  int left = key_hi > static_cast<int>(tok0) ? (key_hi - static_cast<int>(tok0) + CH * kWarps - 1) / (CH * kWarps) : 0;  // this lane's keys
   auto page_next = [&]() {
     Page x = {-1, left > 0 ? off : -1};
     if (left > 0 && pg < p.cache.table_pages) x.id = table[pg];
@@ -121,7 +123,7 @@ SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int k
   }
   // queries: row m = row m / g of the sequence, head m % g of the group; the rows
   // past the last are its copies (zeros times an infinite key would be NaN)
-  for (int i = threadIdx.x; i < R * C::CPR; i += 32 * WARPS) {
+  for (int i = threadIdx.x; i < R * C::CPR; i += kThreads) {
     const int r = i / C::CPR, c = i % C::CPR, m = min(r, rows - 1);
     const int src = max(weigh_src(a, q.row0 + m / p.g), 0);
     *reinterpret_cast<uint4*>(s_q + r * C::ROW + ((c ^ (r & 7)) << 4)) =
@@ -149,7 +151,7 @@ SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int k
       m[nt][e] = -INFINITY;
       l[nt][e] = 0.f;
     }
-  for (int i = 0; i < mine; ++i) {
+  auto step = [&](int i) {
     load(i + C::STAGES - 1, slot_of(page));
     page = next;
     next = page_next();
@@ -178,11 +180,6 @@ SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int k
           if (tail && t0 + (x >> 1) * 8 > seen[nt][x & 1]) sc[nt][x] = -INFINITY;
         }
 #pragma unroll
-        for (int half = 0; half < 2; ++half)
-          if (!tail || t0 + half * 8 < len)
-            *reinterpret_cast<float2*>(row_of(t0 + half * 8) + nt * 8 + (lane & 3) * 2) =
-                make_float2(sc[nt][2 * half], sc[nt][2 * half + 1]);
-#pragma unroll
         for (int e = 0; e < 2; ++e) {
           const float top = fmaxf(m[nt][e], fmaxf(sc[nt][e], sc[nt][2 + e]));
           const float b = top == -INFINITY ? 0.f : top;
@@ -190,8 +187,18 @@ SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int k
           m[nt][e] = top;
         }
       }
+      keep(i, kh, sc);
     }
     __syncwarp();  // the stage may be overwritten
+  };
+  if constexpr (STEPS > 0) {
+#pragma unroll
+    for (int i = 0; i < STEPS; ++i) {
+      if (i >= mine) break;
+      step(i);
+    }
+  } else {
+    for (int i = 0; i < mine; ++i) step(i);
   }
   cp_async_wait<0>();
 #pragma unroll
@@ -208,7 +215,8 @@ SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int k
 
 template <int HD, int NT>
 __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel(const __grid_constant__ WeighArgs a) {
-  constexpr int R = WFew<HD, NT>::R;
+  using C = WFew<HD, NT>;
+  constexpr int R = C::R;
   const TreeArgs& p = a.t;
   extern __shared__ __align__(128) uint8_t smem[];
   __shared__ float2 s_ml[kWarps * R];
@@ -223,24 +231,30 @@ __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel
     if (threadIdx.x == 0 && w.b0 == 0) weigh_note_span(a, w, first, per);
     __syncthreads();  // the previous piece's shared memory is free
     float* out = a.scores + (static_cast<size_t>(w.s) * p.n_kv + w.head) * a.w.tokens * R;
-    few_stream<WFew<HD, NT>, HD, NT>(a, w.s, w.head, w.q, key_lo, key_hi, smem, s_ml, [&](int t) { return out + static_cast<size_t>(t) * R; });
+    const int at = key_lo + C::CH * static_cast<int>(threadIdx.x >> 5) + ((threadIdx.x & 31) >> 2), len = w.q.ctx + w.q.n;
+    few_stream<HD, NT, 0>(a, w.s, w.head, w.q, key_lo, key_hi, smem, s_ml, [&](int i, int kh, const float(&x)[NT][4]) {
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int t = at + C::CH * kWarps * i + 16 * kh + 8 * e;
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+          if (t < len)
+            *reinterpret_cast<float2*>(out + static_cast<size_t>(t) * R + nt * 8 + (threadIdx.x & 3) * 2) = make_float2(x[nt][2 * e], x[nt][2 * e + 1]);
+      }
+    });
     __syncthreads();
     weigh_write_part<R>(a, w, first, s_ml);
   }
 }
 
-// The same in one launch where a unit's scores fit the shared memory of a cluster: its
+// The same in one launch where a unit's scores fit the registers of a cluster: its
 // blocks have a slice of the tokens each and keep its scores, tell each other their
 // rows' statistics, and add up their tokens' weights.  No scores pass through memory,
 // and one launch less is waited for and paid for on the host.
 constexpr int kUnitCluster = 8;        // blocks at most
-constexpr int kUnitScores = 8 * 1024;  // of a slice, at most
-template <int HD, int NT>
-struct WUnit : WFew<HD, NT, 2, NT == 1 ? 5 : 4> {
-  using Base = WFew<HD, NT, 2, NT == 1 ? 5 : 4>;  // as many warps as leave room for three blocks an SM
-  static constexpr int THREADS = 32 * Base::WARPS;
-  static constexpr int OFF_S = Base::SMEM;        // [tokens of a slice][R]
-};
+constexpr int kUnitScores = 8 * 1024;  // of a slice, at most: 64 a thread
+template <int NT>
+constexpr int kUnitCtas = NT == 1 ? 4 : 3;  // per SM
 
 // What a cluster's blocks share of a unit: every block's statistics of its rows.
 template <int R>
@@ -257,24 +271,56 @@ struct Slice {
     hi = lo + min(len - lo, n);
   }
 };
-// The warps' (m, l), as this block's, to all of the cluster.
-template <int R, int WARPS>
-SF_DEV void unit_tell(const WeighArgs& a, const TreeSeq& q, const float2* s_ml, UnitShared<R>& u, int rank) {
-  if (threadIdx.x >= R) return;
-  const int r = threadIdx.x;
-  float2 v = s_ml[r];
+
+template <int HD, int NT>
+__global__ void __launch_bounds__(kThreads, kUnitCtas<NT>) weigh_unit_kernel(const __grid_constant__ WeighArgs a) {
+  using C = WFew<HD, NT>;
+  constexpr int R = C::R, KH = C::CH / 16, STEPS = kUnitScores / R / (kWarps * C::CH);
+  const TreeArgs& p = a.t;
+  extern __shared__ __align__(128) uint8_t smem[];
+  __shared__ float2 s_ml[kWarps * R];
+  __shared__ UnitShared<R> u;
+  pdl_wait();
+  pdl_trigger();
+  const int rank = static_cast<int>(cluster_ctarank()), unit = static_cast<int>(blockIdx.x) / a.blocks;
+  const int s = unit / p.n_kv, h = unit - s * p.n_kv, lane = threadIdx.x & 31;
+  const TreeSeq q = tree_seq(p, s);
+  if (q.bad && h == 0 && rank == 0 && threadIdx.x == 0) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
+  if (q.n == 0) return;  // the same in all of the cluster
+  cluster_arrive();
+  const Slice t(q.ctx + q.n, a.blocks, rank);
+  float x[STEPS][KH][NT][4];
+  few_stream<HD, NT, STEPS>(a, s, h, q, t.lo, t.hi, smem, s_ml, [&](int i, int kh, const float(&sc)[NT][4]) {
 #pragma unroll
-  for (int k = 1; k < WARPS; ++k) v = weigh_merge(v, s_ml[k * R + r]);
-  if (r >= q.n * a.t.g || weigh_src(a, q.row0 + r / a.t.g) < 0) v = make_float2(INFINITY, 0.f);  // weighs nothing
-  for (int k = 0; k < a.blocks; ++k) {
-    const uint32_t at = dsmem_addr(smem_u32(&u.all[rank][r]), k);
-    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 4; ++e) x[i][kh][nt][e] = sc[nt][e];
+  });
+  // Lane 4 k of four has the token k of 16, lane 4 k + 1 the token k + 8.
+  const int first = t.lo + C::CH * static_cast<int>(threadIdx.x >> 5) + (lane >> 2) + 8 * (lane & 1);
+  auto token = [&](int i, int kh) { return first + C::CH * kWarps * i + 16 * kh; };
+  float* wt = a.w.ptr + s * a.w.seq_stride + h * a.w.head_stride;
+  const bool writes = (lane & 3) < 2;
+  const int olds = writes && a.decay != 0.f ? min(t.hi, q.ctx) : 0;
+  float old[STEPS][KH];
+#pragma unroll
+  for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+    for (int kh = 0; kh < KH; ++kh) old[i][kh] = token(i, kh) < olds ? wt[token(i, kh)] : 0.f;
+  __syncthreads();
+  cluster_wait();  // all of them have begun
+  if (threadIdx.x < R) {
+    const int r = threadIdx.x;
+    float2 v = s_ml[r];
+#pragma unroll
+    for (int k = 1; k < kWarps; ++k) v = weigh_merge(v, s_ml[k * R + r]);
+    if (r >= q.n * p.g || weigh_src(a, q.row0 + r / p.g) < 0) v = make_float2(INFINITY, 0.f);  // weighs nothing
+    for (int k = 0; k < a.blocks; ++k) {
+      const uint32_t at = dsmem_addr(smem_u32(&u.all[rank][r]), k);
+      asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
+    }
   }
-}
-// Once all have told: the slice's weights from its scores s_x [tokens][R], two threads a token,
-// each with four of eight rows.
-template <int R, int THREADS>
-SF_DEV void unit_weights(const WeighArgs& a, int s, int h, const TreeSeq& q, Slice t, const float* s_x, UnitShared<R>& u) {
+  cluster_sync_all();  // the only exchange: a block may end from here on
   if (threadIdx.x < R) {
     const int r = threadIdx.x;
     float2 v = u.all[0][r];
@@ -283,59 +329,31 @@ SF_DEV void unit_weights(const WeighArgs& a, int s, int h, const TreeSeq& q, Sli
     u.rl[r] = merge_scale(v.y);
   }
   __syncthreads();
-  const int half = threadIdx.x & 1, rows = q.n * a.t.g;
-  float* wt = a.w.ptr + s * a.w.seq_stride + h * a.w.head_stride;
-  constexpr int K = 4;  // tokens at once
-  for (int first = t.lo; first < t.hi; first += K * (THREADS / 2)) {
-    auto token = [&](int k) { return first + static_cast<int>(threadIdx.x >> 1) + k * (THREADS / 2); };
-    float old[K], sum[K] = {};
+  float m[NT][2], rl[NT][2];
 #pragma unroll
-    for (int k = 0; k < K; ++k) old[k] = half == 0 && token(k) < min(t.hi, q.ctx) && a.decay != 0.f ? wt[token(k)] : 0.f;
-    for (int r = 4 * half; r < rows; r += 8) {
-      const float4 m = *reinterpret_cast<const float4*>(u.m + r), rl = *reinterpret_cast<const float4*>(u.rl + r);
+  for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int k = 0; k < K; ++k) {
-        if (token(k) >= t.hi) continue;
-        const float4 x = *reinterpret_cast<const float4*>(s_x + (token(k) - t.lo) * R + r);
-        sum[k] = fmaf(ex2(x.x - m.x), rl.x, sum[k]);
-        sum[k] = fmaf(ex2(x.y - m.y), rl.y, sum[k]);
-        sum[k] = fmaf(ex2(x.z - m.z), rl.z, sum[k]);
-        sum[k] = fmaf(ex2(x.w - m.w), rl.w, sum[k]);
-      }
+    for (int f = 0; f < 2; ++f) {
+      m[nt][f] = u.m[nt * 8 + (lane & 3) * 2 + f];
+      rl[nt][f] = u.rl[nt * 8 + (lane & 3) * 2 + f];
     }
-    __syncwarp();
 #pragma unroll
-    for (int k = 0; k < K; ++k) {
-      const float both = sum[k] + __shfl_xor_sync(0xffffffffu, sum[k], 1);
-      if (half == 0 && token(k) < t.hi) wt[token(k)] = fmaf(a.decay, old[k], both);
+  for (int i = 0; i < STEPS; ++i) {
+    if (t.lo + C::CH * (static_cast<int>(threadIdx.x >> 5) + kWarps * i) >= t.hi) break;
+#pragma unroll
+    for (int kh = 0; kh < KH; ++kh) {
+      float sum[2] = {};  // of the tokens lane / 4 and 8 behind it
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sum[e >> 1] = fmaf(ex2(x[i][kh][nt][e] - m[nt][e & 1]), rl[nt][e & 1], sum[e >> 1]);
+      // lanes with an even place end with the first token's, the others with the second's
+      const bool odd = lane & 1;
+      float mine = (odd ? sum[1] : sum[0]) + __shfl_xor_sync(0xffffffffu, odd ? sum[0] : sum[1], 1);
+      mine += __shfl_xor_sync(0xffffffffu, mine, 2);
+      if (writes && token(i, kh) < t.hi) wt[token(i, kh)] = fmaf(a.decay, old[i][kh], mine);
     }
   }
-}
-
-template <int HD, int NT>
-__global__ void __launch_bounds__(WUnit<HD, NT>::THREADS) weigh_unit_kernel(const __grid_constant__ WeighArgs a) {
-  using C = WUnit<HD, NT>;
-  constexpr int R = C::R;
-  const TreeArgs& p = a.t;
-  extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 s_ml[C::WARPS * R];
-  __shared__ __align__(16) UnitShared<R> u;
-  float* s_x = reinterpret_cast<float*>(smem + C::OFF_S);
-  pdl_wait();
-  pdl_trigger();
-  const int rank = static_cast<int>(cluster_ctarank()), unit = static_cast<int>(blockIdx.x) / a.blocks;
-  const int s = unit / p.n_kv, h = unit - s * p.n_kv;
-  const TreeSeq q = tree_seq(p, s);
-  if (q.bad && h == 0 && rank == 0 && threadIdx.x == 0) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
-  if (q.n == 0) return;  // the same in all of the cluster
-  cluster_arrive();
-  const Slice t(q.ctx + q.n, a.blocks, rank);
-  few_stream<C, HD, NT>(a, s, h, q, t.lo, t.hi, smem, s_ml, [&](int tok) { return s_x + (tok - t.lo) * R; });
-  __syncthreads();
-  cluster_wait();  // all of them have begun
-  unit_tell<R, C::WARPS>(a, q, s_ml, u, rank);
-  cluster_sync_all();  // the only exchange: a block may end from here on
-  unit_weights<R, C::THREADS>(a, s, h, q, t, s_x, u);
 }
 
 // ------------------------------------------------------------ fp32: few --
@@ -600,7 +618,7 @@ struct WeighPlan {
   WeighForm form;
   int stat_rows, stat_tiles;  // of the first launch
   int ctas_per_sm;
-  int blocks, slice;          // of a cluster; tokens of a block's slice at most (kUnit)
+  int blocks;                 // of a cluster (kUnit)
   int score_rows;
   size_t row_ml, part, span, scores;  // bytes
 };
@@ -641,7 +659,6 @@ WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int
         (units * blocks >= 2LL * kSmBudget || slice(blocks) <= 512)) {
       pl.form = kUnit;
       pl.blocks = blocks;
-      pl.slice = slice(blocks);
       return pl;
     }
     if (keeps && rows <= 16) {
@@ -674,11 +691,10 @@ int start(void (*kernel)(WeighArgs), const WeighArgs& a, int grid, int threads, 
   return check_launch();
 }
 
-int unit_start(void (*kernel)(WeighArgs), int threads, int smem, const WeighPlan& pl, WeighArgs& a, cudaStream_t st) {
-  if (const int rc = smem_limit_once(kernel, smem + kUnitScores * 4)) return rc;
+int unit_start(void (*kernel)(WeighArgs), int smem, const WeighPlan& pl, WeighArgs& a, cudaStream_t st) {
+  if (const int rc = smem_limit_once(kernel, smem)) return rc;
   a.blocks = pl.blocks;
-  launch_kc(kernel, dim3(a.t.batch.n_seqs * a.t.n_kv * pl.blocks), dim3(threads), smem + pl.slice * pl.score_rows * 4, st,
-            pl.blocks, a);
+  launch_kc(kernel, dim3(a.t.batch.n_seqs * a.t.n_kv * pl.blocks), dim3(kThreads), smem, st, pl.blocks, a);
   count_launch();
   return check_launch();
 }
@@ -717,8 +733,8 @@ int weigh_go(const KvWeighCall& c, cudaStream_t st) {
   t.tile_rows = SPECFOLD_MAX_TREE * 128;
   t.kb = kKeys;
   if (pl.form == kUnit)
-    return pl.score_rows == 8 ? unit_start(weigh_unit_kernel<HD, 1>, WUnit<HD, 1>::THREADS, WUnit<HD, 1>::OFF_S, pl, a, st)
-                              : unit_start(weigh_unit_kernel<HD, 2>, WUnit<HD, 2>::THREADS, WUnit<HD, 2>::OFF_S, pl, a, st);
+    return pl.score_rows == 8 ? unit_start(weigh_unit_kernel<HD, 1>, WFew<HD, 1>::SMEM, pl, a, st)
+                              : unit_start(weigh_unit_kernel<HD, 2>, WFew<HD, 2>::SMEM, pl, a, st);
   t.tile_rows = pl.stat_rows;
   t.kb = kKeys;
   t.unit_cost = 4;
