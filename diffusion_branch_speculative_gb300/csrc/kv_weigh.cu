@@ -36,8 +36,9 @@ SF_DEV void weigh_write_part(const WeighArgs& p, const TreeWalk& w, bool first, 
 // that one token with a group of seven heads wastes one column in eight; the
 // scores go to the workspace, 32 bytes a token and eight rows, where the second
 // launch finds them in L2 rather than the keys in DRAM.
-template <int HD, int NT>
+template <int HD, int NT, int WARPS_ = kWarps>
 struct WFew {
+  static constexpr int WARPS = WARPS_;
   static constexpr int R = 8 * NT;
   static constexpr int CH = 2048 / HD;  // keys of a warp's step: 4 KB
   static constexpr int STAGES = 3;
@@ -45,19 +46,19 @@ struct WFew {
   static constexpr int CPR = ROW / 16;
   static constexpr int STAGE = CH * ROW;
   static constexpr int RING = STAGES * STAGE;
-  static constexpr int OFF_Q = kWarps * RING;
+  static constexpr int OFF_Q = WARPS * RING;
   static constexpr int SMEM = OFF_Q + R * ROW;
   static constexpr int CTAS = 4;  // per SM
 };
 
 // A block's keys key_lo .. key_hi - 1 of sequence s, head h: the warps' statistics to s_ml
-// [kWarps][R], the scores to keep(i, kh, x): this warp's step i, 16 of its keys, x[nt][2 e + f]
+// [WARPS][R], the scores to keep(i, kh, x): this warp's step i, 16 of its keys, x[nt][2 e + f]
 // the score of the key lane / 4 + 8 e and the row 8 nt + 2 (lane % 4) + f.  STEPS: a warp's at
 // most, all of them unrolled; 0: any number.
-template <int HD, int NT, int STEPS, typename Keep>
+template <int HD, int NT, int WARPS, int STEPS, typename Keep>
 SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int key_lo, int key_hi, uint8_t* smem, float2* s_ml,
                        Keep keep) {
-  using C = WFew<HD, NT>;
+  using C = WFew<HD, NT, WARPS>;
   using T = __nv_bfloat16;
   constexpr int R = C::R, KS = HD / 16, CH = C::CH, KH = CH / 16;
   const TreeArgs& p = a.t;
@@ -68,18 +69,18 @@ SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int k
   const int rows = q.n * p.g;
   // this warp's chunks: key_lo + CH * (warp + 4 i)
   const int chunks = (key_hi - key_lo + CH - 1) / CH;
-  const int mine = chunks > warp ? (chunks - warp + kWarps - 1) / kWarps : 0;
-  auto key_of = [&](int i) { return key_lo + CH * (warp + kWarps * i); };
+  const int mine = chunks > warp ? (chunks - warp + WARPS - 1) / WARPS : 0;
+  auto key_of = [&](int i) { return key_lo + CH * (warp + WARPS * i); };
   // lanes 0..CH-1 have a chunk's keys; a chunk's pages are read two chunks ahead of its
   // loads, and followed by steps (no division a chunk)
   const int32_t* table = p.cache.block_table + s * p.cache.table_stride;
-  const int ps = p.cache.page_size, dpg = CH * kWarps / ps, doff = CH * kWarps - dpg * ps;
+  const int ps = p.cache.page_size, dpg = CH * WARPS / ps, doff = CH * WARPS - dpg * ps;
   struct Page {
     int id, off;  // in the table; a key's place in it, -1: no key
   };
   const unsigned tok0 = static_cast<unsigned>(key_lo) + CH * warp + (lane & (CH - 1));
   int pg = tok0 / static_cast<unsigned>(ps), off = tok0 - pg * ps;
-  int left = key_hi > static_cast<int>(tok0) ? (key_hi - static_cast<int>(tok0) + CH * kWarps - 1) / (CH * kWarps) : 0;  // this lane's keys
+  int left = key_hi > static_cast<int>(tok0) ? (key_hi - static_cast<int>(tok0) + CH * WARPS - 1) / (CH * WARPS) : 0;  // this lane's keys
   auto page_next = [&]() {
     Page x = {-1, left > 0 ? off : -1};
     if (left > 0 && pg < p.cache.table_pages) x.id = table[pg];
@@ -123,7 +124,7 @@ SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int k
   }
   // queries: row m = row m / g of the sequence, head m % g of the group; the rows
   // past the last are its copies (zeros times an infinite key would be NaN)
-  for (int i = threadIdx.x; i < R * C::CPR; i += kThreads) {
+  for (int i = threadIdx.x; i < R * C::CPR; i += 32 * WARPS) {
     const int r = i / C::CPR, c = i % C::CPR, m = min(r, rows - 1);
     const int src = max(weigh_src(a, q.row0 + m / p.g), 0);
     *reinterpret_cast<uint4*>(s_q + r * C::ROW + ((c ^ (r & 7)) << 4)) =
@@ -232,7 +233,7 @@ __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel
     __syncthreads();  // the previous piece's shared memory is free
     float* out = a.scores + (static_cast<size_t>(w.s) * p.n_kv + w.head) * a.w.tokens * R;
     const int at = key_lo + C::CH * static_cast<int>(threadIdx.x >> 5) + ((threadIdx.x & 31) >> 2), len = w.q.ctx + w.q.n;
-    few_stream<HD, NT, 0>(a, w.s, w.head, w.q, key_lo, key_hi, smem, s_ml, [&](int i, int kh, const float(&x)[NT][4]) {
+    few_stream<HD, NT, kWarps, 0>(a, w.s, w.head, w.q, key_lo, key_hi, smem, s_ml, [&](int i, int kh, const float(&x)[NT][4]) {
 #pragma unroll
       for (int e = 0; e < 2; ++e) {
         const int t = at + C::CH * kWarps * i + 16 * kh + 8 * e;
@@ -252,9 +253,7 @@ __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel
 // rows' statistics, and add up their tokens' weights.  No scores pass through memory,
 // and one launch less is waited for and paid for on the host.
 constexpr int kUnitCluster = 8;        // blocks at most
-constexpr int kUnitScores = 8 * 1024;  // of a slice, at most: 64 a thread
-template <int NT>
-constexpr int kUnitCtas = NT == 1 ? 4 : 3;  // per SM
+constexpr int kUnitScores = 2 * 1024;  // of a warp, at most: 64 a thread
 
 // What a cluster's blocks share of a unit: every block's statistics of its rows.
 template <int R>
@@ -272,13 +271,13 @@ struct Slice {
   }
 };
 
-template <int HD, int NT>
-__global__ void __launch_bounds__(kThreads, kUnitCtas<NT>) weigh_unit_kernel(const __grid_constant__ WeighArgs a) {
-  using C = WFew<HD, NT>;
-  constexpr int R = C::R, KH = C::CH / 16, STEPS = kUnitScores / R / (kWarps * C::CH);
+template <int HD, int NT, int WARPS>
+__global__ void __launch_bounds__(32 * WARPS, (NT == 1 ? 16 / WARPS : 3)) weigh_unit_kernel(const __grid_constant__ WeighArgs a) {
+  using C = WFew<HD, NT, WARPS>;
+  constexpr int R = C::R, KH = C::CH / 16, STEPS = kUnitScores / R / C::CH;
   const TreeArgs& p = a.t;
   extern __shared__ __align__(128) uint8_t smem[];
-  __shared__ float2 s_ml[kWarps * R];
+  __shared__ float2 s_ml[WARPS * R];
   __shared__ UnitShared<R> u;
   pdl_wait();
   pdl_trigger();
@@ -290,7 +289,7 @@ __global__ void __launch_bounds__(kThreads, kUnitCtas<NT>) weigh_unit_kernel(con
   cluster_arrive();
   const Slice t(q.ctx + q.n, a.blocks, rank);
   float x[STEPS][KH][NT][4];
-  few_stream<HD, NT, STEPS>(a, s, h, q, t.lo, t.hi, smem, s_ml, [&](int i, int kh, const float(&sc)[NT][4]) {
+  few_stream<HD, NT, WARPS, STEPS>(a, s, h, q, t.lo, t.hi, smem, s_ml, [&](int i, int kh, const float(&sc)[NT][4]) {
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -298,7 +297,7 @@ __global__ void __launch_bounds__(kThreads, kUnitCtas<NT>) weigh_unit_kernel(con
   });
   // Lane 4 k of four has the token k of 16, lane 4 k + 1 the token k + 8.
   const int first = t.lo + C::CH * static_cast<int>(threadIdx.x >> 5) + (lane >> 2) + 8 * (lane & 1);
-  auto token = [&](int i, int kh) { return first + C::CH * kWarps * i + 16 * kh; };
+  auto token = [&](int i, int kh) { return first + C::CH * WARPS * i + 16 * kh; };
   float* wt = a.w.ptr + s * a.w.seq_stride + h * a.w.head_stride;
   const bool writes = (lane & 3) < 2;
   const int olds = writes && a.decay != 0.f ? min(t.hi, q.ctx) : 0;
@@ -313,7 +312,7 @@ __global__ void __launch_bounds__(kThreads, kUnitCtas<NT>) weigh_unit_kernel(con
     const int r = threadIdx.x;
     float2 v = s_ml[r];
 #pragma unroll
-    for (int k = 1; k < kWarps; ++k) v = weigh_merge(v, s_ml[k * R + r]);
+    for (int k = 1; k < WARPS; ++k) v = weigh_merge(v, s_ml[k * R + r]);
     if (r >= q.n * p.g || weigh_src(a, q.row0 + r / p.g) < 0) v = make_float2(INFINITY, 0.f);  // weighs nothing
     for (int k = 0; k < a.blocks; ++k) {
       const uint32_t at = dsmem_addr(smem_u32(&u.all[rank][r]), k);
@@ -339,7 +338,7 @@ __global__ void __launch_bounds__(kThreads, kUnitCtas<NT>) weigh_unit_kernel(con
     }
 #pragma unroll
   for (int i = 0; i < STEPS; ++i) {
-    if (t.lo + C::CH * (static_cast<int>(threadIdx.x >> 5) + kWarps * i) >= t.hi) break;
+    if (t.lo + C::CH * (static_cast<int>(threadIdx.x >> 5) + WARPS * i) >= t.hi) break;
 #pragma unroll
     for (int kh = 0; kh < KH; ++kh) {
       float sum[2] = {};  // of the tokens lane / 4 and 8 behind it
@@ -618,7 +617,7 @@ struct WeighPlan {
   WeighForm form;
   int stat_rows, stat_tiles;  // of the first launch
   int ctas_per_sm;
-  int blocks;                 // of a cluster (kUnit)
+  int blocks, warps;          // of a cluster, of a block (kUnit)
   int score_rows;
   size_t row_ml, part, span, scores;  // bytes
 };
@@ -645,20 +644,24 @@ WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int
   const size_t scores = std::min(rows_all, most) * n_seqs * tokens;
   const bool keeps = scores <= (size_t{1} << 30);
   if (dtype == SPECFOLD_BF16) {
-    // A cluster for a unit, where a slice's scores leave room for three blocks an SM and the
-    // blocks fill the SMs or are short.  Both sides (one launch, two; us; 28 / 4 heads of 128,
-    // one row): 64 x 8000 tokens 82.4 and 86.8, 8 x 500 9.5 and 11.7, 1 x 2047 9.1 and 11.2;
-    // 2 x 8189, 32 / 8 heads 15.9 and 14.7; with up to 100 KB a slice 8 x 20000 63.4 and 34.0.
+    // A cluster for a unit, where its warps hold the scores, four warps a block or, of up to
+    // eight rows, 8 or 16, and there are as many warps as four blocks an SM of half of the SMs
+    // have, or slices are short.  Both sides (one launch, two; us; 28 / 4 heads of 128, one row):
+    // 64 x 8000 tokens 68.7 and 86.8, 64 x 16000 127 and 171, 32 x 30000 135 and 157, 8 x 20000
+    // 33.8 and 34.1, 8 x 500 9.5 and 11.7, 1 x 2047 9.1 and 11.2; 2 x 8189, 32 / 8 heads 15.9 and
+    // 14.7; 16 rows by 12 warps, 32 x 8000 135 and 108.
     const long long units = static_cast<long long>(n_seqs) * n_kv;
     auto slice = [&](int blocks) { return ((tokens - 1) / blocks / kKeys + 1) * kKeys; };
     int blocks = 1;
     while (blocks < kUnitCluster && slice(blocks) > 256 &&
-           (static_cast<long long>(slice(blocks)) * r8 > kUnitScores || units * blocks < 2LL * kSmBudget))
+           (static_cast<long long>(slice(blocks)) * r8 > 4 * kUnitScores || units * blocks < 2LL * kSmBudget))
       blocks *= 2;
-    if (rows <= 16 && static_cast<long long>(slice(blocks)) * r8 <= kUnitScores &&
-        (units * blocks >= 2LL * kSmBudget || slice(blocks) <= 512)) {
+    const long long w = (static_cast<long long>(slice(blocks)) * r8 + kUnitScores - 1) / kUnitScores;
+    const int warps = w <= 4 || r8 > 8 ? 4 : w <= 8 ? 8 : 16;
+    if (rows <= 16 && w <= warps && (units * blocks * warps >= 8LL * kSmBudget || slice(blocks) <= 512)) {
       pl.form = kUnit;
       pl.blocks = blocks;
+      pl.warps = warps;
       return pl;
     }
     if (keeps && rows <= 16) {
@@ -691,10 +694,13 @@ int start(void (*kernel)(WeighArgs), const WeighArgs& a, int grid, int threads, 
   return check_launch();
 }
 
-int unit_start(void (*kernel)(WeighArgs), int smem, const WeighPlan& pl, WeighArgs& a, cudaStream_t st) {
+template <int HD, int NT, int WARPS>
+int unit_start(const WeighPlan& pl, WeighArgs& a, cudaStream_t st) {
+  auto kernel = weigh_unit_kernel<HD, NT, WARPS>;
+  constexpr int smem = WFew<HD, NT, WARPS>::SMEM;
   if (const int rc = smem_limit_once(kernel, smem)) return rc;
   a.blocks = pl.blocks;
-  launch_kc(kernel, dim3(a.t.batch.n_seqs * a.t.n_kv * pl.blocks), dim3(kThreads), smem, st, pl.blocks, a);
+  launch_kc(kernel, dim3(a.t.batch.n_seqs * a.t.n_kv * pl.blocks), dim3(32 * WARPS), smem, st, pl.blocks, a);
   count_launch();
   return check_launch();
 }
@@ -732,9 +738,11 @@ int weigh_go(const KvWeighCall& c, cudaStream_t st) {
   if (pl.form == kTc) return launch_weigh_tc(a, HD, grid, st);
   t.tile_rows = SPECFOLD_MAX_TREE * 128;
   t.kb = kKeys;
-  if (pl.form == kUnit)
-    return pl.score_rows == 8 ? unit_start(weigh_unit_kernel<HD, 1>, WFew<HD, 1>::SMEM, pl, a, st)
-                              : unit_start(weigh_unit_kernel<HD, 2>, WFew<HD, 2>::SMEM, pl, a, st);
+  if (pl.form == kUnit) {
+    if (pl.score_rows == 8)
+      return pl.warps == 4 ? unit_start<HD, 1, 4>(pl, a, st) : pl.warps == 8 ? unit_start<HD, 1, 8>(pl, a, st) : unit_start<HD, 1, 16>(pl, a, st);
+    return unit_start<HD, 2, 4>(pl, a, st);
+  }
   t.tile_rows = pl.stat_rows;
   t.kb = kKeys;
   t.unit_cost = 4;

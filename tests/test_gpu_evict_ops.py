@@ -231,6 +231,18 @@ def test_kv_weigh_long_context(B, dt, rows, n_q):
     b.check(before, host(b.w), 1.0)
 
 
+@pytest.mark.parametrize("hd", [64, 128])
+@pytest.mark.parametrize("longest", [7000, 12000, 16385, 26011, 32767])
+@pytest.mark.parametrize("rows,g", [(1, 7), (2, 4), (3, 5)])
+def test_kv_weigh_long_decoding(B, hd, longest, rows, g):
+    """Few rows of sequences whose slices take more and more warps of a cluster, most of them empty."""
+    b = Weigh(B, np.random.default_rng(longest), "bf16", hd, 4 * g, 4, 16, "split", [rows, 1, rows, 0, 1, rows],
+              [longest - rows, 100, longest // 2, 7, 0, 4095])
+    before = host(b.w)
+    b.call(0.5)
+    b.check(before, host(b.w), 0.5)
+
+
 @pytest.mark.parametrize("dt", ["bf16", "f32"])
 @pytest.mark.parametrize("rows,g,hd", [(64, 8, 64), (57, 9, 128), (256, 5, 64), (40, 40, 64)])
 def test_kv_weigh_groups_of_rows(B, dt, rows, g, hd):
