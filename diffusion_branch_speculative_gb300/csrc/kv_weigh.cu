@@ -29,13 +29,15 @@ SF_DEV void weigh_write_part(const WeighArgs& p, const TreeWalk& w, bool first, 
 }
 
 // ------------------------------------------------------ few rows, bf16 --
-// Up to 8 NT rows of a head group, so at most 4 NT operations a byte of the
-// keys: the memory bounds it.  Each of the four warps streams its own 4 KB
-// chunks of keys through a private ring of asynchronous copies.  Keys are the
-// 16 rows of the warps' matrix instructions and the queries their 8 columns, so
-// that one token with a group of seven heads wastes one column in eight; the
+// Up to 8 NT rows of a head group, so at most 16 NT operations a byte of the
+// keys: the memory bounds it.  Each warp streams its own 4 KB chunks of keys
+// through a private ring of asynchronous copies.  Keys are the 16 rows of the
+// warps' matrix instructions and the queries their 8 columns, so that one token
+// with a group of seven heads wastes one column in eight.  In two launches the
 // scores go to the workspace, 32 bytes a token and eight rows, where the second
-// launch finds them in L2 rather than the keys in DRAM.
+// finds them in L2 rather than the keys in DRAM: 8 sequences of 20000 tokens (28 / 4
+// heads of 128, 122 MB of keys) take 34 us, 26 of them the first launch, DRAM 59 %
+// busy, its start and uneven shares of the SMs the rest; one of 40000, 18.2.
 template <int HD, int NT, int WARPS_ = kWarps>
 struct WFew {
   static constexpr int WARPS = WARPS_;
@@ -131,16 +133,18 @@ SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int k
         *reinterpret_cast<const uint4*>(static_cast<const T*>(p.q) + src * p.q_rs + (h * p.g + m % p.g) * p.q_hs + c * 8);
   }
   __syncthreads();
-  uint32_t qf[NT][KS][2];
+  // two of their fragments, dimensions 16 ks .. 16 ks + 31
+  auto queries = [&](int nt, int ks, uint32_t (&b)[4]) {
+    const int r = nt * 8 + (lane & 7);
+    ldsm4(smem_u32(s_q + r * C::ROW + (((ks * 2 + (lane >> 3)) ^ (r & 7)) << 4)), b);
+  };
+  constexpr bool HELD = STEPS == 0 || NT == 1;  // beside the scores there is no room for two tiles'
+  uint32_t qf[HELD ? NT : 1][KS / 2][4];
+  if constexpr (HELD)
 #pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
+    for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int ks = 0; ks < KS; ks += 2) {
-      uint32_t b[4];
-      const int r = nt * 8 + (lane & 7);
-      ldsm4(smem_u32(s_q + r * C::ROW + (((ks * 2 + (lane >> 3)) ^ (r & 7)) << 4)), b);
-      qf[nt][ks][0] = b[0], qf[nt][ks][1] = b[1], qf[nt][ks + 1][0] = b[2], qf[nt][ks + 1][1] = b[3];
-    }
+      for (int ks = 0; ks < KS; ks += 2) queries(nt, ks, qf[nt][ks / 2]);
   // this thread's rows: 8 nt + 2 (lane % 4) and the next one; the last token each sees
   int seen[NT][2];
   float m[NT][2], l[NT][2];
@@ -166,11 +170,18 @@ SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int k
       const int key = kh * 16 + (lane & 15);
       const uint32_t base = smem_u32(stg + key * C::ROW);
 #pragma unroll
-      for (int ks = 0; ks < KS; ++ks) {
-        uint32_t k[4];
-        ldsm4(base + (((ks * 2 + (lane >> 4)) ^ (key & 7)) << 4), k);
+      for (int ks = 0; ks < KS; ks += 2) {
+        uint32_t k[2][4];
 #pragma unroll
-        for (int nt = 0; nt < NT; ++nt) mma16816(sc[nt], k, qf[nt][ks][0], qf[nt][ks][1]);
+        for (int x = 0; x < 2; ++x) ldsm4(base + ((((ks + x) * 2 + (lane >> 4)) ^ (key & 7)) << 4), k[x]);
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          uint32_t b[4];
+          if constexpr (!HELD) queries(nt, ks, b);
+          const uint32_t(&f)[4] = HELD ? qf[HELD ? nt : 0][ks / 2] : b;
+          mma16816(sc[nt], k[0], f[0], f[1]);
+          mma16816(sc[nt], k[1], f[2], f[3]);
+        }
       }
       const int t0 = key_of(i) + kh * 16 + (lane >> 2);
 #pragma unroll
@@ -249,9 +260,15 @@ __global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel
 }
 
 // The same in one launch where a unit's scores fit the registers of a cluster: its
-// blocks have a slice of the tokens each and keep its scores, tell each other their
-// rows' statistics, and add up their tokens' weights.  No scores pass through memory,
-// and one launch less is waited for and paid for on the host.
+// blocks have a slice of the tokens each and keep its scores, 64 a thread, tell each
+// other their rows' statistics, and add up their tokens' weights.  No scores pass
+// through memory, and one launch less is waited for and paid for on the host.  128
+// registers a thread and 12 KB of keys on the way a warp let an SM have 16 warps; the
+// unrolled steps are what lets registers hold the scores (in shared memory, beside
+// two stages and three blocks an SM, 80 us where this takes 68.7).  64 sequences of up
+// to 8000 tokens, one row of 28 / 4 heads of 128: 379 MB in 68.7 us, 5590 GB/s, 0.83 of
+// the copy rate; 32 of 8 heads and eight rows 0.90; head size 64 0.68.  What is left is
+// the blocks' own starts and exchanges.
 constexpr int kUnitCluster = 8;        // blocks at most
 constexpr int kUnitScores = 2 * 1024;  // of a warp, at most: 64 a thread
 
@@ -272,7 +289,7 @@ struct Slice {
 };
 
 template <int HD, int NT, int WARPS>
-__global__ void __launch_bounds__(32 * WARPS, (NT == 1 ? 16 / WARPS : 3)) weigh_unit_kernel(const __grid_constant__ WeighArgs a) {
+__global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) weigh_unit_kernel(const __grid_constant__ WeighArgs a) {
   using C = WFew<HD, NT, WARPS>;
   constexpr int R = C::R, KH = C::CH / 16, STEPS = kUnitScores / R / C::CH;
   const TreeArgs& p = a.t;
@@ -623,18 +640,19 @@ struct WeighPlan {
 };
 size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 
-// Few rows keep their scores, as long as these take a workspace of at most 1 GB: up to 16
-// of a head group in bf16, where keeping them and computing them twice on the tensor
-// cores measure (us; 8 key/value heads, groups of 4):
-//   sequences x tokens       32 x 8000       1 x 40000     8 x 500
-//   head size 128, 8 rows     86.5  121.1                  11.6  15.2
-//                  16 rows   104.5  121.1    29.5  35.9    12.0  15.2
-//                  24 rows   133.5  121.1
-//                  32 rows   167.8  121.2    50.2  36.0    14.8  15.2
-//   head size 64,  8 rows     58.5   85.2
-//                  16 rows    74.5   85.3
-//                  32 rows   131.7   85.4
-// fp32 keeps them always: it would be bound by computing them twice.
+// Up to 16 rows of a head group keep their scores in bf16: in the registers of one launch
+// where they fit, else, as long as they take a workspace of at most 1 GB, in memory.  More
+// rows, and what does not fit, have them computed twice on the tensor cores.  The three (us;
+// 8 key/value heads, groups of 4, sequences x tokens):
+//                           32 x 8000             1 x 40000       8 x 500
+//   head size 128,  8 rows   63.3   87.4  120.6   -  26.8  35.5    9.5  11.1  14.6
+//                  16 rows   80.5  108.1  120.8   -  31.3  35.7    9.3  12.4  14.7
+//                  24 rows      -  133.5  120.7                      -     -  14.6
+//                  32 rows      -  167.8  120.9   -  50.2  35.4      -  14.8  14.6
+//   head size 64,   8 rows   42.1   58.7   78.1
+//                  16 rows   63.9   77.6   77.5
+//                  32 rows      -  131.7   77.7
+// fp32 keeps them in memory always: it would be bound by computing them twice.
 WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int n_seqs, int tokens) {
   const int rows = max_rows * (n_q / n_kv), r8 = (rows + 7) / 8 * 8;
   WeighPlan pl{};
@@ -644,12 +662,13 @@ WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int
   const size_t scores = std::min(rows_all, most) * n_seqs * tokens;
   const bool keeps = scores <= (size_t{1} << 30);
   if (dtype == SPECFOLD_BF16) {
-    // A cluster for a unit, where its warps hold the scores, four warps a block or, of up to
-    // eight rows, 8 or 16, and there are as many warps as four blocks an SM of half of the SMs
-    // have, or slices are short.  Both sides (one launch, two; us; 28 / 4 heads of 128, one row):
-    // 64 x 8000 tokens 68.7 and 86.8, 64 x 16000 127 and 171, 32 x 30000 135 and 157, 8 x 20000
-    // 33.8 and 34.1, 8 x 500 9.5 and 11.7, 1 x 2047 9.1 and 11.2; 2 x 8189, 32 / 8 heads 15.9 and
-    // 14.7; 16 rows by 12 warps, 32 x 8000 135 and 108.
+    // A cluster for a unit, where 4, 8 or 16 warps a block hold its scores and there are enough
+    // of them: as many warps as fill half of the SMs, four rounds of the largest blocks, or
+    // slices are short.  Both sides (one launch, two; us; head size 128; one row of 28 / 4 heads):
+    //   64 x 8000 tokens 68.7 and 86.8, 64 x 16000 127 and 171, 32 x 30000 135 and 157,
+    //   8 x 20000 33.5 and 34.1, 8 x 500 9.4 and 11.7, 1 x 2047 9.1 and 11.2
+    // two rows of them: 32 x 16000 99.5 and 107, 4 x 16000 23.8 and 23.1; four of 32 / 8:
+    //   32 x 8000 81.3 and 106, 8 x 12000 49.3 and 45.0; one of them: 2 x 8189 15.9 and 14.7
     const long long units = static_cast<long long>(n_seqs) * n_kv;
     auto slice = [&](int blocks) { return ((tokens - 1) / blocks / kKeys + 1) * kKeys; };
     int blocks = 1;
@@ -657,8 +676,9 @@ WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int
            (static_cast<long long>(slice(blocks)) * r8 > 4 * kUnitScores || units * blocks < 2LL * kSmBudget))
       blocks *= 2;
     const long long w = (static_cast<long long>(slice(blocks)) * r8 + kUnitScores - 1) / kUnitScores;
-    const int warps = w <= 4 || r8 > 8 ? 4 : w <= 8 ? 8 : 16;
-    if (rows <= 16 && w <= warps && (units * blocks * warps >= 8LL * kSmBudget || slice(blocks) <= 512)) {
+    const int warps = w <= 4 ? 4 : w <= 8 ? 8 : 16;
+    if (rows <= 16 && w <= warps &&
+        (warps < 16 ? units * blocks * warps >= 8LL * kSmBudget || slice(blocks) <= 512 : units * blocks >= 4LL * kSmBudget)) {
       pl.form = kUnit;
       pl.blocks = blocks;
       pl.warps = warps;
@@ -740,8 +760,12 @@ int weigh_go(const KvWeighCall& c, cudaStream_t st) {
   t.kb = kKeys;
   if (pl.form == kUnit) {
     if (pl.score_rows == 8)
-      return pl.warps == 4 ? unit_start<HD, 1, 4>(pl, a, st) : pl.warps == 8 ? unit_start<HD, 1, 8>(pl, a, st) : unit_start<HD, 1, 16>(pl, a, st);
-    return unit_start<HD, 2, 4>(pl, a, st);
+      return pl.warps == 4   ? unit_start<HD, 1, 4>(pl, a, st)
+             : pl.warps == 8 ? unit_start<HD, 1, 8>(pl, a, st)
+                             : unit_start<HD, 1, 16>(pl, a, st);
+    return pl.warps == 4   ? unit_start<HD, 2, 4>(pl, a, st)
+           : pl.warps == 8 ? unit_start<HD, 2, 8>(pl, a, st)
+                           : unit_start<HD, 2, 16>(pl, a, st);
   }
   t.tile_rows = pl.stat_rows;
   t.kb = kKeys;
