@@ -1,8 +1,8 @@
 // The attention weight that cached tokens get from a batch of rows, added up per
 // key/value head (specfold_kv_weigh): what an eviction goes by.  Keys alone are
 // read.  kv_weigh.cuh has the two launches' division of work; here are the forms
-// whose first launch keeps the scores: few rows a head group, and fp32.
-// kv_weigh_tc.cu has many rows in bf16.
+// that keep the scores: few rows a head group, and fp32.  kv_weigh_tc.cu has many
+// rows in bf16.
 #include "kv_weigh.cuh"
 
 #include <algorithm>
@@ -29,7 +29,7 @@ SF_DEV void weigh_write_part(const WeighArgs& p, const TreeWalk& w, bool first, 
 }
 
 // ------------------------------------------------------ few rows, bf16 --
-// Up to 8 NT rows of a head group, so at most 16 NT operations a byte of the
+// Up to 8 NT rows of a head group, so at most 8 NT operations a byte of the
 // keys: the memory bounds it.  Each warp streams its own 4 KB chunks of keys
 // through a private ring of asynchronous copies.  Keys are the 16 rows of the
 // warps' matrix instructions and the queries their 8 columns, so that one token
@@ -50,8 +50,8 @@ struct WFew {
   static constexpr int RING = STAGES * STAGE;
   static constexpr int OFF_Q = WARPS * RING;
   static constexpr int SMEM = OFF_Q + R * ROW;
-  static constexpr int CTAS = 4;  // per SM
 };
+constexpr int kFewCtas = 4;  // per SM, of two launches
 
 // A block's keys key_lo .. key_hi - 1 of sequence s, head h: the warps' statistics to s_ml
 // [WARPS][R], the scores to keep(i, kh, x): this warp's step i, 16 of its keys, x[nt][2 e + f]
@@ -226,7 +226,7 @@ SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int k
 }
 
 template <int HD, int NT>
-__global__ void __launch_bounds__(kThreads, WFew<HD, NT>::CTAS) weigh_few_kernel(const __grid_constant__ WeighArgs a) {
+__global__ void __launch_bounds__(kThreads, kFewCtas) weigh_few_kernel(const __grid_constant__ WeighArgs a) {
   using C = WFew<HD, NT>;
   constexpr int R = C::R;
   const TreeArgs& p = a.t;
@@ -376,7 +376,12 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) weigh_unit_kernel(cons
 // The same for fp32 by multiply-adds, a tile of eight rows at a time (a piece of at
 // most four does no other rows' arithmetic): a warp's step is 4 KB of keys, a lane
 // (key, 32 of the dimensions), the queries broadcast from shared memory; a key's lanes
-// add up by halves, so that each ends with some rows' scores.
+// add up by halves, so that each ends with some rows' scores.  The reads of shared
+// memory bound it (a read feeds one row's products): 8 sequences of 8000 tokens, one row
+// of 24 / 8 heads of 128, 190 MB, take 49.8 us in all, 0.57 of the copy rate.  7 of 1111
+// tokens and five rows of 4 / 2 heads of 64 take 12.7 us, 9.2 and 9.9 the two launches
+// alone and cold: latency.  One launch by clusters, scores in shared memory, was slower
+// (70.6 us where two took 47.4, and 15.6 where they took 13.8).
 template <int HD>
 struct WSimt {
   static constexpr int R = 8;
@@ -544,6 +549,8 @@ __global__ void __launch_bounds__(kThreads, WSimt<HD>::CTAS) weigh_simt_kernel(c
 // before the wait for the first launch: that one waited for all before it, and reads
 // the same lengths.  A piece's first scores are on their way while its rows' statistics
 // are merged.  More rows than kSumRows come in groups, which add to the weights in turn.
+// The scores of 8 sequences of 20000 tokens, 17 MB, take it 14.7 us alone and cold, 8 behind
+// the first launch; four blocks an SM have too few registers (99.9 us where three take 87).
 constexpr int kSumThreads = 256, kSumTokens = 8;
 constexpr int kSumCtas = 3;    // per SM
 constexpr int kSumRows = 512;  // of a group
@@ -687,7 +694,7 @@ WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int
     if (keeps && rows <= 16) {
       pl.form = kFew;
       pl.stat_rows = r8;
-      pl.ctas_per_sm = WFew<128, 1>::CTAS;
+      pl.ctas_per_sm = kFewCtas;
     } else {
       pl.form = kTc;
       pl.stat_rows = kWeighTcRows;

@@ -1,6 +1,7 @@
 // What the kernels of specfold_kv_weigh share.
 //
-// Two launches, each over a line of work as tree_sched.cuh has it.  The first
+// Two launches (few rows often need but one: weigh_unit_kernel), each over a line of
+// work as tree_sched.cuh has it.  The first
 // finds every row's maximum m (in log2 units) and sum l over the keys it sees: a
 // piece that is its whole unit leaves its rows' own in row_ml, any other in its slot
 // (2c or 2c + 1 of CTA c: a run's first or last piece), and the CTA with a unit's

@@ -9,6 +9,15 @@
 // are (384 threads): warp 0 loads keys, warps 1 and 3 gather queries, warp 2 issues
 // the products, warps 4 to 11 reduce.  A score costs one product and one
 // exponential a launch.
+//
+// Up to about 100 rows a group the memory bounds it, which has to deliver the keys
+// twice: 32 rows of 24 / 8 heads over 4 x 32700 tokens, 2 x 217 MB, take 73.4 us, 5920
+// GB/s or 0.87 of the copy rate (44 us a launch alone and cold, DRAM 63 % and tensor
+// cores 26 and 18 % busy, 8 us of it the start; the two cannot share an SM).  Beyond, the
+// exponentials and the reads of the tensor memory do: 252 rows (36 of 28 / 4 heads) 64 us
+// for 2 x 107 MB, 896 rows 250 us, where a tile of 256 rows takes 0.95 us a block in the
+// first launch and 1.7 in the second.  Keeping a part of the keys in L2 from one launch to
+// the next by hints saves 1 to 2 us; the scores of 96 rows would be 1.5 times the keys.
 #include "kv_weigh.cuh"
 
 namespace sf {
@@ -354,7 +363,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_stats_tc_kernel(const __g
 // row that the sum needs is rounded once more than m alone, by 2^-24 of itself, which
 // is no more than the products' own rounding of the scores, and halves what a score
 // reads of shared memory.  Blocks go from a run's last to its first: what the
-// statistics read last is still in L2.
+// statistics read last is still in L2.  Tiles of 128 rows, two buffers a half and the
+// next tile gathered ahead were slower (36 rows of 28 / 4 heads 73.8 us where this takes
+// 63.7, 128 rows 256 where this takes 249): products half as wide read more of shared
+// memory for each score.
 struct WItems {  // the order of a unit's products, the same in every role
   int n, tiles, group;
   int g0 = 0, tile_at = 0, dir = 1, done = 0;  // group's first block, tile now, its step, tiles of the group so far
