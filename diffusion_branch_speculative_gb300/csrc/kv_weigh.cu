@@ -266,7 +266,7 @@ __global__ void __launch_bounds__(kThreads, kFewCtas) weigh_few_kernel(const __g
 // registers a thread and 12 KB of keys on the way a warp let an SM have 16 warps; the
 // unrolled steps are what lets registers hold the scores (in shared memory, beside
 // two stages and three blocks an SM, 80 us where this takes 68.7).  64 sequences of up
-// to 8000 tokens, one row of 28 / 4 heads of 128: 379 MB in 68.7 us, 5590 GB/s, 0.83 of
+// to 8000 tokens, one row of 28 / 4 heads of 128: 379 MB in 68.7 us, 5590 GB/s, 0.82 of
 // the copy rate; 32 of 8 heads and eight rows 0.90; head size 64 0.68.  What is left is
 // the blocks' own starts and exchanges.
 constexpr int kUnitCluster = 8;        // blocks at most
