@@ -648,9 +648,9 @@ typedef struct {
  * the same T (or a larger one), max_rows, n_seqs and w.tokens.  With
  * max_rows * g up to 16 and, for fp32, always, it holds the scores: four bytes
  * for every token of n_seqs * n_kv times w.tokens and every row of a group, in
- * eights (bf16: none where they are few or 1 GB and more).  A batch's rows may
- * also be weighed a part at a time, each part behind the tokens of the parts
- * before (decay 1). */
+ * eights (bf16: none where one launch holds them in registers, or 1 GB and
+ * more).  A batch's rows may also be weighed a part at a time, each part behind
+ * the tokens of the parts before (decay 1). */
 int specfold_kv_weigh(int dtype, int T, int max_rows, int n_q, int n_kv, int head_dim, specfold_head_rows q, int n_src,
                       const int32_t* rows, const specfold_paged_cache* cache, const int32_t* row_start,
                       const int32_t* ctx_len, int n_seqs, float scale, float decay, specfold_token_weights w, void* ws,
