@@ -400,6 +400,64 @@ def test_kv_weigh_repeats_bit_for_bit(B, dt, rows):
     assert all(torch.equal(x, got[0]) for x in got)
 
 
+@pytest.mark.parametrize("longest", [7000, 14000, 28000])
+@pytest.mark.parametrize("rows", [2, 4])
+@pytest.mark.parametrize("n_kv", [4, 16])
+def test_kv_weigh_long_decoding_edges(B, n_kv, longest, rows):
+    """Clusters of few and many warps: the same bits again, unseen keys, a bad page, a bad row, a bad length."""
+    b = Weigh(B, np.random.default_rng(longest), "bf16", 64, 4 * n_kv, n_kv, 16, "split", [rows] * 6,
+              [longest, 33, longest // 3, 0, 5000, longest - 700])
+    # One launch keeps nothing in the workspace and cuts no sequence by the others' lengths.  Two do:
+    # without one of its sequences the others' sums come in another order, and either result is
+    # within the bound of the exact one.
+    apart = None
+    if B.kv_weigh_workspace_size(B.BF16, b.T, rows, 4 * n_kv, n_kv, 64, 6, b.tokens) != 256:
+        apart = 2 * b.bound(host(b.w), 1.0)[1]
+    w0 = b.w.clone()
+
+    def run(ctx=None, picked=None):
+        b.w.copy_(w0)
+        B.specfold_kv_weigh(b.q, b.cache, b.at[0], b.at[1] if ctx is None else ints(ctx), rows, b.w, b.ws,
+                            rows=None if picked is None else ints(picked))
+        torch.cuda.synchronize()
+        return B.specfold_get_status(b.ws), b.w.clone()
+
+    ok, good = run()
+    assert ok == 0 and torch.equal(run()[1], good)
+    held = torch.zeros(b.cache.k_pool.shape[0], dtype=torch.bool)
+    for s in range(6):
+        t = np.arange(b.ctx[s] + rows)
+        held[b.table[s, t // 16] * 16 + t % 16] = True
+    b.cache.k_pool[~held.cuda()] = float("nan")
+    st, got = run()
+    assert st == 0 and torch.equal(got, good)
+    # sequence 2 is longer than its weights: no other one's change
+    st, got = run(ctx=[longest, 33, b.tokens, 0, 5000, longest - 700])
+    assert st == B.DEV_BAD_SEQ and torch.equal(got[2], w0[2])
+    others = [0, 1, 3, 4, 5]
+    if apart is None:
+        assert torch.equal(got[others], good[others])
+    else:
+        assert (np.abs(host(got) - host(good))[others] <= apart[others]).all()
+    # a picked row outside the source weighs nothing
+    pick = np.arange(b.T)
+    pick[0] = -1
+    st, got = run(picked=pick)
+    assert st == B.DEV_BAD_SEQ and torch.equal(got[1:], good[1:])
+    gain = (got[0] - w0[0])[:, :longest].double().sum() + got[0, :, longest:longest + rows].double().sum()
+    assert abs(float(gain) - 4 * n_kv * (rows - 1)) < 1e-2
+    # a page outside the pool reads as zeros
+    table = b.cache.block_table.clone()
+    b.cache.block_table[4, 100] = -3
+    st, got = run()
+    b.cache.block_table.copy_(table)
+    assert st == B.DEV_BAD_PAGE and torch.equal(got[[0, 1, 2, 3, 5]], good[[0, 1, 2, 3, 5]])
+    page = b.table[4, 100]
+    b.cache.k_pool[page * 16:page * 16 + 16] = 0
+    st, want = run()
+    assert st == 0 and torch.equal(got, want)
+
+
 # ------------------------------------------------------------- select --
 
 def run_select(B, w, lengths, keep, sinks=0, recent=0, cap=None):
