@@ -270,6 +270,8 @@ __global__ void __launch_bounds__(kThreads, kFewCtas) weigh_few_kernel(const __g
 // the copy rate; 32 of 8 heads and eight rows 0.90; head size 64 0.68.  What is left is
 // the blocks' own starts and exchanges.
 constexpr int kUnitCluster = 8;        // blocks at most
+constexpr int kUnitStep = 256;         // tokens that are worth a block more where SMs are idle,
+constexpr int kUnitLeast = 2;          // and where they are not: the share of what its warps can hold
 constexpr int kUnitScores = 2 * 1024;  // of a warp, at most: 64 a thread
 
 // What a cluster's blocks share of a unit: every block's statistics of its rows.
@@ -303,8 +305,12 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) weigh_unit_kernel(cons
   const TreeSeq q = tree_seq(p, s);
   if (q.bad && h == 0 && rank == 0 && threadIdx.x == 0) atomicOr(p.status, SPECFOLD_DEV_BAD_SEQ);
   if (q.n == 0) return;  // the same in all of the cluster
+  // no more blocks than this unit's length is worth
+  const int len = q.ctx + q.n, spread = min(a.spread, (len - 1) / kUnitStep + 1);
+  const int blocks = min(a.blocks, max((len - 1) / (kUnitScores / R * WARPS / kUnitLeast) + 1, spread));
+  if (rank >= blocks) return;  // (a cluster's barriers do not count those that have left)
   cluster_arrive();
-  const Slice t(q.ctx + q.n, a.blocks, rank);
+  const Slice t(len, blocks, rank);
   float x[STEPS][KH][NT][4];
   few_stream<HD, NT, WARPS, STEPS>(a, s, h, q, t.lo, t.hi, smem, s_ml, [&](int i, int kh, const float(&sc)[NT][4]) {
 #pragma unroll
@@ -331,7 +337,7 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) weigh_unit_kernel(cons
 #pragma unroll
     for (int k = 1; k < WARPS; ++k) v = weigh_merge(v, s_ml[k * R + r]);
     if (r >= q.n * p.g || weigh_src(a, q.row0 + r / p.g) < 0) v = make_float2(INFINITY, 0.f);  // weighs nothing
-    for (int k = 0; k < a.blocks; ++k) {
+    for (int k = 0; k < blocks; ++k) {
       const uint32_t at = dsmem_addr(smem_u32(&u.all[rank][r]), k);
       asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(at), "f"(v.x), "f"(v.y) : "memory");
     }
@@ -340,7 +346,7 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) weigh_unit_kernel(cons
   if (threadIdx.x < R) {
     const int r = threadIdx.x;
     float2 v = u.all[0][r];
-    for (int k = 1; k < a.blocks; ++k) v = weigh_merge(v, u.all[k][r]);
+    for (int k = 1; k < blocks; ++k) v = weigh_merge(v, u.all[k][r]);
     u.m[r] = v.x;
     u.rl[r] = merge_scale(v.y);
   }
@@ -669,13 +675,13 @@ WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int
   const size_t scores = std::min(rows_all, most) * n_seqs * tokens;
   const bool keeps = scores <= (size_t{1} << 30);
   if (dtype == SPECFOLD_BF16) {
-    // A cluster for a unit, where 4, 8 or 16 warps a block hold its scores and there are enough
-    // of them: as many warps as fill half of the SMs, four rounds of the largest blocks, or
-    // slices are short.  Both sides (one launch, two; us; head size 128; one row of 28 / 4 heads):
-    //   64 x 8000 tokens 68.7 and 86.8, 64 x 16000 127 and 171, 32 x 30000 135 and 157,
-    //   8 x 20000 33.5 and 34.1, 8 x 500 9.4 and 11.7, 1 x 2047 9.1 and 11.2
-    // two rows of them: 32 x 16000 99.5 and 107, 4 x 16000 23.8 and 23.1; four of 32 / 8:
-    //   32 x 8000 81.3 and 106, 8 x 12000 49.3 and 45.0; one of them: 2 x 8189 15.9 and 14.7
+    // A cluster for a unit wherever 4 or 8 warps a block hold its scores.  Both sides (one launch,
+    // two; us; sequences x tokens, head size 128), one row of 28 / 4 heads: 64 x 8000 68.7 and
+    // 87.4, 64 x 16000 127 and 171, 8 x 8000 14.9 and 20.4, 1 x 16000 14.0 and 13.5, 1 x 2047 9.1
+    // and 11.2; four of 32 / 8: 32 x 8000 81.3 and 106, 1 x 8000 10.5 and 15.0.  Where the weights
+    // have room for more tokens than there are: 64 x 8000 of 16384 86 and 87.7, 64 x 2000 of 16384
+    // 29 and 30, four rows of 32 x 4000 of 8192 63 and 57.  With 16 warps a block full lengths gain
+    // (32 x 30000 135 and 157), shorter ones lose (64 x 4000 of 32768 57 and 50).
     const long long units = static_cast<long long>(n_seqs) * n_kv;
     auto slice = [&](int blocks) { return ((tokens - 1) / blocks / kKeys + 1) * kKeys; };
     int blocks = 1;
@@ -683,9 +689,8 @@ WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int
            (static_cast<long long>(slice(blocks)) * r8 > 4 * kUnitScores || units * blocks < 2LL * kSmBudget))
       blocks *= 2;
     const long long w = (static_cast<long long>(slice(blocks)) * r8 + kUnitScores - 1) / kUnitScores;
-    const int warps = w <= 4 ? 4 : w <= 8 ? 8 : 16;
-    if (rows <= 16 && w <= warps &&
-        (warps < 16 ? units * blocks * warps >= 8LL * kSmBudget || slice(blocks) <= 512 : units * blocks >= 4LL * kSmBudget)) {
+    const int warps = w <= 4 ? 4 : 8;
+    if (rows <= 16 && w <= warps) {
       pl.form = kUnit;
       pl.blocks = blocks;
       pl.warps = warps;
@@ -727,6 +732,7 @@ int unit_start(const WeighPlan& pl, WeighArgs& a, cudaStream_t st) {
   constexpr int smem = WFew<HD, NT, WARPS>::SMEM;
   if (const int rc = smem_limit_once(kernel, smem)) return rc;
   a.blocks = pl.blocks;
+  a.spread = num_sms() * (16 / WARPS) / (a.t.batch.n_seqs * a.t.n_kv) + 1;
   launch_kc(kernel, dim3(a.t.batch.n_seqs * a.t.n_kv * pl.blocks), dim3(32 * WARPS), smem, st, pl.blocks, a);
   count_launch();
   return check_launch();
@@ -767,12 +773,8 @@ int weigh_go(const KvWeighCall& c, cudaStream_t st) {
   t.kb = kKeys;
   if (pl.form == kUnit) {
     if (pl.score_rows == 8)
-      return pl.warps == 4   ? unit_start<HD, 1, 4>(pl, a, st)
-             : pl.warps == 8 ? unit_start<HD, 1, 8>(pl, a, st)
-                             : unit_start<HD, 1, 16>(pl, a, st);
-    return pl.warps == 4   ? unit_start<HD, 2, 4>(pl, a, st)
-           : pl.warps == 8 ? unit_start<HD, 2, 8>(pl, a, st)
-                           : unit_start<HD, 2, 16>(pl, a, st);
+      return pl.warps == 4 ? unit_start<HD, 1, 4>(pl, a, st) : unit_start<HD, 1, 8>(pl, a, st);
+    return pl.warps == 4 ? unit_start<HD, 2, 4>(pl, a, st) : unit_start<HD, 2, 8>(pl, a, st);
   }
   t.tile_rows = pl.stat_rows;
   t.kb = kKeys;

@@ -26,7 +26,7 @@ struct WeighArgs {
   float2* row_ml;       // [T][n_kv * g]: m, l
   float* scores;        // [n_seqs][n_kv][w.tokens][score_rows] in log2 units, or null
   int score_rows;
-  int blocks;           // of a cluster, where one holds a unit
+  int blocks, spread;   // of a cluster, where one holds a unit; blocks a unit that fill the SMs
 };
 
 // q's row for row t of the batch; -1: there is none (reported).

@@ -225,9 +225,9 @@ def test_kv_weigh_workspace_size(B):
     # few rows of bf16 and all of fp32 keep their scores: eight rows of a group, 16 bytes and more a token
     small, large = size(B.BF16, 64, 1, 28, 4, 128, 64, 40000), size(B.BF16, 64, 1, 28, 4, 128, 64, 65536)
     assert large - small == 64 * 4 * (65536 - 40000) * 8 * 4
-    for tokens in (8192, 16384, 32768):
+    for tokens in (8192, 16384):
         assert size(B.BF16, 64, 1, 28, 4, 128, 64, tokens) == 256          # in registers
-    assert size(B.BF16, 64, 1, 28, 4, 128, 64, 32769) > 1 << 28
+    assert size(B.BF16, 64, 1, 28, 4, 128, 64, 16385) > 1 << 27
     assert size(B.F32, 64, 1, 28, 4, 128, 64, 8192) > 64 * 4 * 8192 * 8 * 4
     assert size(B.BF16, 64, 1, 28, 4, 128, 1024, 1 << 20) < 1 << 28        # past 1 GB: computed twice
 
