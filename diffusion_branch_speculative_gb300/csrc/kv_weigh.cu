@@ -265,9 +265,9 @@ __global__ void __launch_bounds__(kThreads, kFewCtas) weigh_few_kernel(const __g
 // through memory, and one launch less is waited for and paid for on the host.  128
 // registers a thread and 12 KB of keys on the way a warp let an SM have 16 warps; the
 // unrolled steps are what lets registers hold the scores (in shared memory, beside
-// two stages and three blocks an SM, 80 us where this takes 68.7).  64 sequences of up
-// to 8000 tokens, one row of 28 / 4 heads of 128: 379 MB in 68.7 us, 5590 GB/s, 0.82 of
-// the copy rate; 32 of 8 heads and eight rows 0.90; head size 64 0.68.  What is left is
+// two stages and three blocks an SM, 80 us where this takes 69.6).  64 sequences of up
+// to 8000 tokens, one row of 28 / 4 heads of 128: 384 MB in 69.6 us, 5510 GB/s, 0.81 of
+// the copy rate; 32 of 8 heads and eight rows 0.89; head size 64 0.67.  What is left is
 // the blocks' own starts and exchanges.
 constexpr int kUnitCluster = 8;        // blocks at most
 constexpr int kUnitStep = 256;         // tokens that are worth a block more where SMs are idle,
@@ -658,12 +658,12 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // rows, and what does not fit, have them computed twice on the tensor cores.  The three (us;
 // 8 key/value heads, groups of 4, sequences x tokens):
 //                           32 x 8000             1 x 40000       8 x 500
-//   head size 128,  8 rows   63.3   87.4  120.6   -  26.8  35.5    9.5  11.1  14.6
-//                  16 rows   80.5  108.1  120.8   -  31.3  35.7    9.3  12.4  14.7
+//   head size 128,  8 rows   63.7   87.4  120.6   -  26.8  35.5    9.6  11.1  14.6
+//                  16 rows   82.2  108.1  120.8   -  31.3  35.7    9.6  12.4  14.7
 //                  24 rows      -  133.5  120.7                      -     -  14.6
 //                  32 rows      -  167.8  120.9   -  50.2  35.4      -  14.8  14.6
-//   head size 64,   8 rows   42.1   58.7   78.1
-//                  16 rows   63.9   77.6   77.5
+//   head size 64,   8 rows   42.7   58.7   78.1
+//                  16 rows   64.1   77.6   77.5
 //                  32 rows      -  131.7   77.7
 // fp32 keeps them in memory always: it would be bound by computing them twice.
 WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int n_seqs, int tokens) {
@@ -676,9 +676,9 @@ WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int
   const bool keeps = scores <= (size_t{1} << 30);
   if (dtype == SPECFOLD_BF16) {
     // A cluster for a unit wherever 4 or 8 warps a block hold its scores.  Both sides (one launch,
-    // two; us; sequences x tokens, head size 128), one row of 28 / 4 heads: 64 x 8000 68.7 and
-    // 87.4, 64 x 16000 127 and 171, 8 x 8000 14.9 and 20.4, 1 x 16000 14.0 and 13.5, 1 x 2047 9.1
-    // and 11.2; four of 32 / 8: 32 x 8000 81.3 and 106, 1 x 8000 10.5 and 15.0.  Where the weights
+    // two; us; sequences x tokens, head size 128), one row of 28 / 4 heads: 64 x 8000 69.6 and
+    // 87.4, 64 x 16000 128 and 171, 8 x 8000 14.9 and 20.4, 1 x 16000 14.0 and 13.5, 1 x 2047 9.1
+    // and 11.2; four of 32 / 8: 32 x 8000 83 and 107, 1 x 8000 10.5 and 15.0.  Where the weights
     // have room for more tokens than there are: 64 x 8000 of 16384 86 and 87.7, 64 x 2000 of 16384
     // 29 and 30, four rows of 32 x 4000 of 8192 63 and 57.  With 16 warps a block full lengths gain
     // (32 x 30000 135 and 157), shorter ones lose (64 x 4000 of 32768 57 and 50).
