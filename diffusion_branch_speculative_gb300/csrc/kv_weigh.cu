@@ -382,9 +382,12 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) weigh_unit_kernel(cons
 // The same for fp32 by multiply-adds, a tile of eight rows at a time (a piece of at
 // most four does no other rows' arithmetic): a warp's step is 4 KB of keys, a lane
 // (key, 32 of the dimensions), the queries broadcast from shared memory; a key's lanes
-// add up by halves, so that each ends with some rows' scores.  The reads of shared
-// memory bound it (a read feeds one row's products): 8 sequences of 8000 tokens, one row
-// of 24 / 8 heads of 128, 190 MB, take 49.8 us in all, 0.57 of the copy rate.  7 of 1111
+// add up by halves, so that each ends with some rows' scores.  Two steps at a time, whose
+// keys share a query's read (alone, 16 sequences of 12239 tokens and twelve rows of 2 heads
+// took 57.3 us where this takes 51.3, 8 of 4000 and 48 rows of 8 heads 120 and 105; short
+// pieces wait 0.7 us longer for their first).  The reads of shared memory bound it all the
+// same: 8 sequences of 8000 tokens, one row of 24 / 8 heads of 128, 190 MB, take 48.7 us
+// in all, 0.58 of the copy rate.  7 of 1111
 // tokens and five rows of 4 / 2 heads of 64 take 12.7 us, 9.2 and 9.9 the two launches
 // alone and cold: latency.  One launch by clusters, scores in shared memory, was slower
 // (70.6 us where two took 47.4, and 15.6 where they took 13.8).
@@ -434,12 +437,15 @@ SF_DEV void simt_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int 
     }
     cp_async_commit();
   };
-  int slot = slot_of(0);
+  int slot[2] = {slot_of(0), slot_of(1)};  // of the next two steps to load
+  auto load_two = [&](int i) {
+    load(i, slot[0]);
+    load(i + 1, slot[1]);
+    slot[0] = slot_of(i + 2);
+    slot[1] = slot_of(i + 3);
+  };
 #pragma unroll
-  for (int i = 0; i < C::STAGES - 1; ++i) {
-    load(i, slot);
-    slot = slot_of(i + 1);
-  }
+  for (int i = 0; i < C::STAGES - 2; i += 2) load_two(i);
   for (int i = threadIdx.x; i < R * (HD / 4); i += kThreads) {
     const int r = i / (HD / 4), d = (i % (HD / 4)) * 4, m = m0 + min(r, rows - 1);
     const int src = max(weigh_src(a, q.row0 + m / p.g), 0);
@@ -459,52 +465,61 @@ SF_DEV void simt_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int 
       m[r] = -INFINITY;
       l[r] = 0.f;
     }
-    for (int i = 0; i < mine; ++i) {
-      load(i + C::STAGES - 1, slot);
-      slot = slot_of(i + C::STAGES);
-      cp_async_wait<C::STAGES - 1>();
+    for (int i = 0; i < mine; i += 2) {
+      load_two(i + C::STAGES - 2);
+      cp_async_wait<C::STAGES - 2>();
       __syncwarp();
-      const uint8_t* sk = ring + (i % C::STAGES) * C::STAGE + key * C::ROW;
-      float x[NR] = {};
+      const uint8_t* sk[2];
+      float x[2][NR] = {};
+#pragma unroll
+      for (int u = 0; u < 2; ++u) sk[u] = ring + ((i + u) % C::STAGES) * C::STAGE + key * C::ROW;
 #pragma unroll
       for (int d0 = 0; d0 < 32; d0 += 4) {
         // the parts start apart, so that their reads of a query share no bank
         const int d = part * 32 + ((d0 + part * CH) & 31);
-        const float4 k4 = *reinterpret_cast<const float4*>(sk + (((d >> 2) ^ (key & 7)) << 4));
+        float4 k4[2];
+#pragma unroll
+        for (int u = 0; u < 2; ++u) k4[u] = *reinterpret_cast<const float4*>(sk[u] + (((d >> 2) ^ (key & 7)) << 4));
 #pragma unroll
         for (int r = 0; r < NR; ++r) {
           const float4 q4 = *reinterpret_cast<const float4*>(s_q + r * HD + d);
-          x[r] = fmaf(q4.x, k4.x, fmaf(q4.y, k4.y, fmaf(q4.z, k4.z, fmaf(q4.w, k4.w, x[r]))));
+#pragma unroll
+          for (int u = 0; u < 2; ++u)
+            x[u][r] = fmaf(q4.x, k4[u].x, fmaf(q4.y, k4[u].y, fmaf(q4.z, k4[u].z, fmaf(q4.w, k4[u].w, x[u][r]))));
         }
       }
-      // the parts' sums: each step halves the rows that a lane keeps
 #pragma unroll
-      for (int n = NR / 2, o = 16; o >= CH; n /= 2, o /= 2) {
-        const bool upper = lane & o;
+      for (int u = 0; u < 2; ++u) {
+        if (i + u >= mine) break;  // (an odd number of steps: nothing was loaded)
+        // the parts' sums: each step halves the rows that a lane keeps
 #pragma unroll
-        for (int r = 0; r < n; ++r) {
-          const float keep = upper ? x[n + r] : x[r], give = upper ? x[r] : x[n + r];
-          x[r] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+        for (int n = NR / 2, o = 16; o >= CH; n /= 2, o /= 2) {
+          const bool upper = lane & o;
+#pragma unroll
+          for (int r = 0; r < n; ++r) {
+            const float keep = upper ? x[u][n + r] : x[u][r], give = upper ? x[u][r] : x[u][n + r];
+            x[u][r] = keep + __shfl_xor_sync(0xffffffffu, give, o);
+          }
         }
-      }
-      const int tok = key_of(i) + key;
-      const bool tail = key_of(i) + CH > q.ctx;
+        const int tok = key_of(i + u) + key;
+        const bool tail = key_of(i + u) + CH > q.ctx;
 #pragma unroll
-      for (int r = 0; r < RP; ++r) {
-        x[r] = tail && tok > seen[r] ? -INFINITY : x[r] * p.sl2;
-        const float top = fmaxf(m[r], x[r]);
-        const float b = top == -INFINITY ? 0.f : top;
-        l[r] = fmaf(l[r], m[r] == top ? 1.f : ex2(m[r] - b), ex2(x[r] - b));
-        m[r] = top;
-      }
-      if (!tail || tok < len) {
-        float* to = row_of(tok) + m0 + part * RP;
-        if constexpr (RP == 4)
-          *reinterpret_cast<float4*>(to) = make_float4(x[0], x[1], x[2], x[3]);
-        else if constexpr (RP == 2)
-          *reinterpret_cast<float2*>(to) = make_float2(x[0], x[1]);
-        else
-          *to = x[0];
+        for (int r = 0; r < RP; ++r) {
+          x[u][r] = tail && tok > seen[r] ? -INFINITY : x[u][r] * p.sl2;
+          const float top = fmaxf(m[r], x[u][r]);
+          const float b = top == -INFINITY ? 0.f : top;
+          l[r] = fmaf(l[r], m[r] == top ? 1.f : ex2(m[r] - b), ex2(x[u][r] - b));
+          m[r] = top;
+        }
+        if (!tail || tok < len) {
+          float* to = row_of(tok) + m0 + part * RP;
+          if constexpr (RP == 4)
+            *reinterpret_cast<float4*>(to) = make_float4(x[u][0], x[u][1], x[u][2], x[u][3]);
+          else if constexpr (RP == 2)
+            *reinterpret_cast<float2*>(to) = make_float2(x[u][0], x[u][1]);
+          else
+            *to = x[u][0];
+        }
       }
       __syncwarp();
     }
