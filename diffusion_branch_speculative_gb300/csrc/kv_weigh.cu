@@ -387,10 +387,10 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) weigh_unit_kernel(cons
 // took 57.3 us where this takes 51.3, 8 of 4000 and 48 rows of 8 heads 120 and 105; short
 // pieces wait 0.7 us longer for their first).  The reads of shared memory bound it all the
 // same: 8 sequences of 8000 tokens, one row of 24 / 8 heads of 128, 190 MB, take 48.7 us
-// in all, 0.58 of the copy rate.  7 of 1111
-// tokens and five rows of 4 / 2 heads of 64 take 12.7 us, 9.2 and 9.9 the two launches
-// alone and cold: latency.  One launch by clusters, scores in shared memory, was slower
-// (70.6 us where two took 47.4, and 15.6 where they took 13.8).
+// in all, 0.58 of the copy rate.  7 of 1111 tokens and five rows of 4 / 2 heads of 64 take
+// 12.7 us, 9.3 and 9.9 the two launches alone and cold: latency.  One launch by clusters,
+// scores in shared memory, was slower (70.6 us where two took 47.4, and 15.6 where they
+// took 13.8).
 template <int HD>
 struct WSimt {
   static constexpr int R = 8;
