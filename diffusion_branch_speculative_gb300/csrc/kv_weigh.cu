@@ -145,17 +145,21 @@ SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int k
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
       for (int ks = 0; ks < KS; ks += 2) queries(nt, ks, qf[nt][ks / 2]);
-  // this thread's rows: 8 nt + 2 (lane % 4) and the next one; the last token each sees
+  // this thread's rows: 8 nt + 2 (lane % 4) and the next one; the last token each sees (-1: none)
   int seen[NT][2];
   float m[NT][2], l[NT][2];
+  bool blind = false;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      seen[nt][e] = q.ctx + min(nt * 8 + (lane & 3) * 2 + e, rows - 1) / p.g;
+      const int r = min(nt * 8 + (lane & 3) * 2 + e, rows - 1) / p.g;
+      seen[nt][e] = weigh_has_src(a, q.row0 + r) ? q.ctx + r : -1;
+      blind = blind || seen[nt][e] < 0;
       m[nt][e] = -INFINITY;
       l[nt][e] = 0.f;
     }
+  const int all_see = __any_sync(0xffffffffu, blind) ? 0 : q.ctx;  // tokens before this one
   auto step = [&](int i) {
     load(i + C::STAGES - 1, slot_of(page));
     page = next;
@@ -163,7 +167,7 @@ SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int k
     cp_async_wait<C::STAGES - 1>();
     __syncwarp();
     const uint8_t* stg = ring + (i % C::STAGES) * C::STAGE;
-    const bool tail = key_of(i) + CH > q.ctx;  // holds tokens that not every row sees
+    const bool tail = key_of(i) + CH > all_see;  // holds tokens that not every row sees
 #pragma unroll
     for (int kh = 0; kh < KH; ++kh) {
       float sc[NT][4] = {};
@@ -459,12 +463,16 @@ SF_DEV void simt_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int 
     constexpr int RP = NR / PARTS;           // of which a lane has RP's sums, from row part * RP on
     int seen[RP];
     float m[RP], l[RP];
+    bool blind = false;
 #pragma unroll
     for (int r = 0; r < RP; ++r) {
-      seen[r] = q.ctx + (m0 + min(part * RP + r, rows - 1)) / p.g;
+      const int i = (m0 + min(part * RP + r, rows - 1)) / p.g;
+      seen[r] = weigh_has_src(a, q.row0 + i) ? q.ctx + i : -1;
+      blind = blind || seen[r] < 0;
       m[r] = -INFINITY;
       l[r] = 0.f;
     }
+    const int all_see = __any_sync(0xffffffffu, blind) ? 0 : q.ctx;  // tokens before this one
     for (int i = 0; i < mine; i += 2) {
       load_two(i + C::STAGES - 2);
       cp_async_wait<C::STAGES - 2>();
@@ -502,7 +510,7 @@ SF_DEV void simt_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int 
           }
         }
         const int tok = key_of(i + u) + key;
-        const bool tail = key_of(i + u) + CH > q.ctx;
+        const bool tail = key_of(i + u) + CH > all_see;
 #pragma unroll
         for (int r = 0; r < RP; ++r) {
           x[u][r] = tail && tok > seen[r] ? -INFINITY : x[u][r] * p.sl2;

@@ -397,6 +397,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
   __shared__ uint32_t tmem_slot_s;
   __shared__ volatile int abort_s;
   __shared__ __align__(16) float s_off[2][kWeighTcRows];  // -(m + log2 l) of a tile's rows, by turns
+  __shared__ __align__(16) int s_blind[2][8];  // whether a warp's of these rows are without a source
   __shared__ float s_sum[C::RING][kBlock];  // of a group's blocks over the tiles so far
   uint64_t* full = bars;
   uint64_t* empty = bars + C::RING;
@@ -529,17 +530,22 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
       const int ctx = w.q.ctx, len = ctx + w.q.n;
       float* wt = a.w.ptr + w.s * a.w.seq_stride + w.head * a.w.head_stride;
       WItems q(w.n, tiles_of(), C::RING);
-      bool fresh = true;
+      bool fresh = true, blind = false;
       while (q.g0 < q.n) {
         if (fresh) {  // the tile's statistics, a thread a row
           float off = -INFINITY;  // no such row, or one that weighs nothing
-          if (tid < rows_of(q.tile_at)) {
+          const bool there = tid < rows_of(q.tile_at);
+          if (there) {
             const float2 v = weigh_gather(a, weigh_unit(a, w, q.tile_at), weigh_row_ml(a, w.q.row0, w.head, q.tile_at * kWeighTcRows + tid), tid, 0, 1);
             if (v.x != INFINITY || v.y != 0.f) off = -(v.x + log2f(v.y));
           }
           s_off[ql & 1][tid] = off;
+          const bool none = __any_sync(0xffffffffu, there && off == -INFINITY);
+          if (lane == 0) s_blind[ql & 1][warp - 4] = none;
           all_ok = ok = named_bar_and(1, 256, ok);
           if (!ok) break;
+          const int4 u = reinterpret_cast<const int4*>(s_blind[ql & 1])[0], v = reinterpret_cast<const int4*>(s_blind[ql & 1])[1];
+          blind = u.x | u.y | u.z | u.w | v.x | v.y | v.z | v.w;
           ++ql;
         }
         const float* so = s_off[(ql - 1) & 1];
@@ -556,20 +562,20 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
           if (!ok) break;
           tc_fence_after();
           if (leader && last) mbar_arrive(smem_u32(&empty[(it + q.g0 + b) % C::RING]));
-          // the first row that sees this key
+          // the first row that sees this key; rows without a source see none
           const int from = tail ? static_cast<int>(min(max(t0 + key - ctx, 0ll) * p.g - m0, 1ll << 20)) : 0;
           float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          auto add = [&](const uint32_t(&s)[32], int c0, auto is_tail) {
+          auto add = [&](const uint32_t(&s)[32], int c0, auto hides) {
 #pragma unroll
             for (int e = 0; e < 32; e += 4) {
               const float4 o4 = *reinterpret_cast<const float4*>(so + c0 + e);
               float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, make_float2(o4.x, o4.y));
               float2 z = fma2(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), scale2, make_float2(o4.z, o4.w));
-              if constexpr (decltype(is_tail)::value) {
-                if (c0 + e < from) y.x = -INFINITY;
-                if (c0 + e + 1 < from) y.y = -INFINITY;
-                if (c0 + e + 2 < from) z.x = -INFINITY;
-                if (c0 + e + 3 < from) z.y = -INFINITY;
+              if constexpr (decltype(hides)::value) {
+                if (c0 + e < from || o4.x == -INFINITY) y.x = -INFINITY;
+                if (c0 + e + 1 < from || o4.y == -INFINITY) y.y = -INFINITY;
+                if (c0 + e + 2 < from || o4.z == -INFINITY) z.x = -INFINITY;
+                if (c0 + e + 3 < from || o4.w == -INFINITY) z.y = -INFINITY;
               }
               acc[0] = add2(acc[0], make_float2(ex2(y.x), ex2(y.y)));
               acc[1] = add2(acc[1], make_float2(ex2(z.x), ex2(z.y)));
@@ -588,19 +594,19 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
               if (lane == 0) mbar_arrive(smem_u32(&d_free[x]));
             }
           };
-          auto columns = [&](auto is_tail) {
+          auto columns = [&](auto hides) {
             tmem_ld32(at, s0);
 #pragma unroll 1
             for (int c = 0; c < cols; c += 64) {
               loaded(s0, s1, c);
-              add(s0, c, is_tail);
+              add(s0, c, hides);
               if (c + 32 < cols) {
                 loaded(s1, s0, c + 32);
-                add(s1, c + 32, is_tail);
+                add(s1, c + 32, hides);
               }
             }
           };
-          if (tail)
+          if (tail || blind)
             columns(std::true_type{});
           else
             columns(std::false_type{});

@@ -1,0 +1,51 @@
+"""Edges of the operators that thin out a paged cache, on the GPU against the
+float64 oracle: what is invalid or not finite reaches no further than the header
+says.  Bounds as in test_gpu_evict_ops.py."""
+import numpy as np
+import pytest
+import torch
+
+from tests.test_gpu_cache_ops import host, ints
+from tests.test_gpu_evict_ops import B, Weigh  # noqa: F401 (B is the fixture)
+
+pytestmark = pytest.mark.gpu
+
+# rows of a sequence, group, head size, the longest context: one launch of one and two tiles of rows, two launches
+# with the scores kept, products computed twice with one and several tiles of rows (fp32: one and several tiles)
+FORMS = [(3, 2, 128, 200), (3, 4, 64, 700), (3, 5, 128, 20000), (2, 2, 64, 40000), (30, 4, 128, 300), (70, 8, 64, 500)]
+
+
+def batch(B, dt, form):
+    rows, g, hd, longest = form
+    rng = np.random.default_rng(rows * g + hd)
+    return Weigh(B, rng, dt, hd, 2 * g, 2, 16, "split", [rows] * 3, [longest, 33, 130], pick=True)
+
+
+# ------------------------------------------------------------------ weigh --
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("what", ["nan query", "infinite query", "infinite key", "minus infinite key"])
+def test_rows_without_a_source_weigh_nothing_whatever_there_is(B, dt, form, what):
+    b = batch(B, dt, form)
+    rows = form[0]
+    pick = np.where(b.rows == 0, 1, b.rows)     # no row of the batch takes the source's first
+    pick[[0, rows - 1]] = -1, len(b.q)          # of sequence 0 the first and the last
+    pick[rows:2 * rows] = 2 ** 31 - 1           # of sequence 1 all
+    b.rows = pick
+    b.at = b.at[0], b.at[1], ints(pick)
+    if "query" in what:
+        b.q[0] = float("nan") if "nan" in what else float("inf")
+    else:                                       # a token that only rows without a source see
+        for s in (0, 1):
+            t = int(b.ctx[s]) + rows - 1
+            b.cache.k_pool[int(b.table[s, t // 16]) * 16 + t % 16] = float("inf") if what[0] == "i" else -float("inf")
+    before = host(b.w)
+    b.call(0.5)
+    torch.cuda.synchronize()
+    assert B.specfold_get_status(b.ws) == B.DEV_BAD_SEQ
+    got = host(b.w)
+    assert np.isfinite(got).all()
+    assert np.array_equal(got[1, :, :33], 0.5 * before[1, :, :33]) and (got[1, :, 33:33 + rows] == 0).all()
+    b.check(before, got, 0.5)
+
