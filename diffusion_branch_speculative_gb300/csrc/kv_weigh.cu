@@ -153,13 +153,22 @@ SF_DEV void few_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int k
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
     for (int e = 0; e < 2; ++e) {
-      const int r = min(nt * 8 + (lane & 3) * 2 + e, rows - 1) / p.g;
-      seen[nt][e] = weigh_has_src(a, q.row0 + r) ? q.ctx + r : -1;
-      blind = blind || seen[nt][e] < 0;
+      seen[nt][e] = q.ctx + min(nt * 8 + (lane & 3) * 2 + e, rows - 1) / p.g;
       m[nt][e] = -INFINITY;
       l[nt][e] = 0.f;
     }
-  const int all_see = __any_sync(0xffffffffu, blind) ? 0 : q.ctx;  // tokens before this one
+  if (a.rows) {
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e)
+        if (!weigh_has_src(a, q.row0 + seen[nt][e] - q.ctx)) {
+          seen[nt][e] = -1;
+          blind = true;
+        }
+    blind = __any_sync(0xffffffffu, blind);
+  }
+  const int all_see = blind ? 0 : q.ctx;  // tokens before this one
   auto step = [&](int i) {
     load(i + C::STAGES - 1, slot_of(page));
     page = next;
@@ -466,13 +475,20 @@ SF_DEV void simt_stream(const WeighArgs& a, int s, int h, const TreeSeq& q, int 
     bool blind = false;
 #pragma unroll
     for (int r = 0; r < RP; ++r) {
-      const int i = (m0 + min(part * RP + r, rows - 1)) / p.g;
-      seen[r] = weigh_has_src(a, q.row0 + i) ? q.ctx + i : -1;
-      blind = blind || seen[r] < 0;
+      seen[r] = q.ctx + (m0 + min(part * RP + r, rows - 1)) / p.g;
       m[r] = -INFINITY;
       l[r] = 0.f;
     }
-    const int all_see = __any_sync(0xffffffffu, blind) ? 0 : q.ctx;  // tokens before this one
+    if (a.rows) {
+#pragma unroll
+      for (int r = 0; r < RP; ++r)
+        if (!weigh_has_src(a, q.row0 + seen[r] - q.ctx)) {
+          seen[r] = -1;
+          blind = true;
+        }
+      blind = __any_sync(0xffffffffu, blind);
+    }
+    const int all_see = blind ? 0 : q.ctx;  // tokens before this one
     for (int i = 0; i < mine; i += 2) {
       load_two(i + C::STAGES - 2);
       cp_async_wait<C::STAGES - 2>();

@@ -37,11 +37,10 @@ SF_DEV int weigh_src(const WeighArgs& p, int t) {
   return -1;
 }
 
-// Whether row t has one (not reported).  A row without is given q's row 0 to work on, whose scores, and
-// those with an infinite key, may be anything: it sees no token, so that all its scores are -inf.
-SF_DEV bool weigh_has_src(const WeighArgs& p, int t) {
-  return !p.rows || (p.rows[t] >= 0 && p.rows[t] < p.n_src);
-}
+// Whether row t of a batch with `rows` has one (not reported).  A row without is given q's row 0 to work
+// on, whose scores, and those with an infinite key, may be anything: it sees no token, so that all its
+// scores are -inf.
+SF_DEV bool weigh_has_src(const WeighArgs& p, int t) { return p.rows[t] >= 0 && p.rows[t] < p.n_src; }
 
 SF_DEV size_t weigh_unit(const WeighArgs& p, const TreeWalk& w, int tile) {
   return (static_cast<size_t>(w.s) * p.t.n_kv + w.head) * p.stat_tiles + tile;
