@@ -292,6 +292,7 @@ template <int R>
 struct UnitShared {
   float2 all[kUnitCluster][R];
   float m[R], rl[R];
+  int spoilt;  // the last token that a row whose weights are no numbers sees
 };
 // This block's slice of the unit's tokens.
 struct Slice {
@@ -342,6 +343,7 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) weigh_unit_kernel(cons
   for (int i = 0; i < STEPS; ++i)
 #pragma unroll
     for (int kh = 0; kh < KH; ++kh) old[i][kh] = token(i, kh) < olds ? wt[token(i, kh)] : 0.f;
+  if (threadIdx.x == 0) u.spoilt = -1;
   __syncthreads();
   cluster_wait();  // all of them have begun
   if (threadIdx.x < R) {
@@ -360,10 +362,17 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) weigh_unit_kernel(cons
     const int r = threadIdx.x;
     float2 v = u.all[0][r];
     for (int k = 1; k < blocks; ++k) v = weigh_merge(v, u.all[k][r]);
+    // Such a row adds NaN to the tokens that it sees, and to no other (2^-inf times its NaN would be
+    // one): its sum stays out, and the tokens up to its last one are written so.
+    if (weigh_no_number(v)) {
+      atomicMax(&u.spoilt, q.ctx + r / p.g);
+      v = make_float2(INFINITY, 0.f);
+    }
     u.m[r] = v.x;
     u.rl[r] = merge_scale(v.y);
   }
   __syncthreads();
+  const int spoilt = u.spoilt;
   float m[NT][2], rl[NT][2];
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
@@ -386,6 +395,7 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) weigh_unit_kernel(cons
       const bool odd = lane & 1;
       float mine = (odd ? sum[1] : sum[0]) + __shfl_xor_sync(0xffffffffu, odd ? sum[0] : sum[1], 1);
       mine += __shfl_xor_sync(0xffffffffu, mine, 2);
+      if (token(i, kh) <= spoilt) mine = NAN;
       if (writes && token(i, kh) < t.hi) wt[token(i, kh)] = fmaf(a.decay, old[i][kh], mine);
     }
   }
@@ -672,8 +682,17 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) weigh_sum_kernel(const 
         }
 #pragma unroll
         for (int k = 0; k < kSumTokens; ++k) {
-          const float both = sum[k] + __shfl_xor_sync(0xffffffffu, sum[k], 1);
-          if ((k & 1) == half && token(t0, k) < key_hi) wt[token(t0, k)] = fmaf(factor, old[k], both);
+          float both = sum[k] + __shfl_xor_sync(0xffffffffu, sum[k], 1);
+          if ((k & 1) == half && token(t0, k) < key_hi) {
+            // a row whose weights are no numbers adds none to the tokens that it does not see, where the
+            // sum has 2^-inf times its NaN: the rows that see one of the batch's own
+            if (both != both && token(t0, k) > w.q.ctx) {
+              both = 0.f;
+              for (int i = max(lo, (token(t0, k) - w.q.ctx) * p.g); i < hi; ++i)
+                both = fmaf(ex2(x[static_cast<size_t>(token(t0, k)) * R - 4 * half + i] - s_m[i - lo]), s_rl[i - lo], both);
+            }
+            wt[token(t0, k)] = fmaf(factor, old[k], both);
+          }
         }
       }
     }

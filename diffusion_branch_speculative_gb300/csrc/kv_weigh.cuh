@@ -80,6 +80,10 @@ SF_DEV float2 weigh_merge(float2 a, float2 b) {
   return make_float2(M, fmaf(merge_weight(a.x, M), a.y, merge_weight(b.x, M) * b.y));
 }
 
+// Whether a row's weights are no numbers: a score of it is NaN or +inf, or all are -inf.  (One
+// that weighs nothing has m = +inf, l = 0.)
+SF_DEV bool weigh_no_number(float2 v) { return v.y != v.y || v.x == -INFINITY; }
+
 // This thread's merge of a row, the r-th of the unit's tile: the partials z0, z0 + zs, ...;
 // whole: where it has its own if the unit was not cut.
 SF_DEV float2 weigh_gather(const WeighArgs& p, size_t unit, const float2* whole, int r, int z0, int zs) {

@@ -1,10 +1,13 @@
 """Edges of the operators that thin out a paged cache, on the GPU against the
 float64 oracle: what is invalid or not finite reaches no further than the header
 says.  Bounds as in test_gpu_evict_ops.py."""
+import warnings
+
 import numpy as np
 import pytest
 import torch
 
+from oracle import evict_oracle as orc
 from tests.test_gpu_cache_ops import host, ints
 from tests.test_gpu_evict_ops import B, Weigh  # noqa: F401 (B is the fixture)
 
@@ -49,3 +52,31 @@ def test_rows_without_a_source_weigh_nothing_whatever_there_is(B, dt, form, what
     assert np.array_equal(got[1, :, :33], 0.5 * before[1, :, :33]) and (got[1, :, 33:33 + rows] == 0).all()
     b.check(before, got, 0.5)
 
+
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("form", FORMS)
+@pytest.mark.parametrize("what", [float("nan"), float("inf"), -float("inf")])
+@pytest.mark.parametrize("at", [0, 1])
+def test_a_row_without_a_softmax_spoils_what_it_sees_alone(B, dt, form, what, at):
+    """Scores that are NaN, or all of them infinite: the weights of the tokens that the row sees are NaN, those of the
+    rows behind it are not."""
+    b = batch(B, dt, form)
+    rows, g = form[:2]
+    b.q[:, :, 0].abs_()
+    b.cache.k_pool[:, :, 0].abs_().add_(0.5)    # an infinity keeps its sign, and comes with no zero
+    before = host(b.w)
+    _, bound = b.bound(before, 0.75)            # with finite queries: of at least the sums that are left
+    b.q[int(b.rows[at]), g - 1, 0] = what       # a row of sequence 0, the last of its first group's heads
+    with warnings.catch_warnings():
+        warnings.simplefilter("ignore")
+        ref = orc.weigh(host(b.q), host(b.cache.k_pool), b.table, 16, b.start, b.ctx, before, 0.75, b.rows)[0]
+    spoilt = np.isnan(ref)
+    n = int(b.ctx[0]) + at + 1
+    assert spoilt[0, 0, :n].all() and spoilt.sum() == n
+    b.call(0.75)
+    torch.cuda.synchronize()
+    got = host(b.w)
+    assert np.array_equal(np.isnan(got), spoilt)
+    err = np.abs(got - ref)[~spoilt]
+    assert (err <= bound[~spoilt]).all(), err.max()
+    assert B.specfold_get_status(b.ws) == 0
