@@ -688,6 +688,7 @@ __global__ void __launch_bounds__(kSumThreads, kSumCtas) weigh_sum_kernel(const 
             // sum has 2^-inf times its NaN: the rows that see one of the batch's own
             if (both != both && token(t0, k) > w.q.ctx) {
               both = 0.f;
+#pragma unroll 1
               for (int i = max(lo, (token(t0, k) - w.q.ctx) * p.g); i < hi; ++i)
                 both = fmaf(ex2(x[static_cast<size_t>(token(t0, k)) * R - 4 * half + i] - s_m[i - lo]), s_rl[i - lo], both);
             }
