@@ -400,13 +400,10 @@ __global__ void __launch_bounds__(Move<CLUSTER>::THREADS) kv_compact_kernel(cons
     bool moves[WEIGHTS];
 #pragma unroll
     for (int k = 0; k < WEIGHTS; ++k) {
-      const int token = threadIdx.x + k * THREADS, i = first + token;
-      moves[k] = false;
-      if (w && token < TOKENS && i < n) {
-        const int src = kept[i];
-        moves[k] = src > i && src < len;
-        if (moves[k]) moved[k] = w[src];
-      }
+      // a token's weight goes where its keys and values go: one that stays keeps its own
+      const int token = threadIdx.x + k * THREADS;
+      moves[k] = w && token < TOKENS && s_at[buf][0][token] >= 0 && s_at[buf][1][token] >= 0;
+      if (moves[k]) moved[k] = w[kept[first + token]];
     }
     if (round0 + step < n) locate(first + step, buf ^ 1);
     if constexpr (CLUSTER)

@@ -686,8 +686,8 @@ int specfold_kv_select(specfold_token_weights w, const int32_t* lengths, int n_s
  * nothing (SPECFOLD_DEV_BAD_SEQ).  new_len[s] outside 0 ..
  * lengths[s] or above kept.cap, or lengths[s] above w.tokens, leaves the
  * sequence as it is (the same bit).  A token whose page, or whose
- * destination's, is outside the pool or past the table is not moved
- * (SPECFOLD_DEV_BAD_PAGE).
+ * destination's, is outside the pool or past the table is not moved, nor is
+ * its weight (SPECFOLD_DEV_BAD_PAGE).
  * Pages that a moved token leaves or enters belong to one sequence: where two
  * share them, what they hold afterwards is unspecified.
  * kept.n_sets is n_kv or 1; head_dim 64 or 128. */

@@ -110,5 +110,7 @@ def compact(k_pool, v_pool, table, page, kept, lengths, new_len, weights=None):
                     kp[a, h], vp[a, h] = k_pool[b, h], v_pool[b, h]
         if w is not None:
             for u in range(len(kept[s])):
-                w[s, u, :n] = weights[s, u, np.asarray(kept[s][u][:n], np.int64)]
+                for i in range(n):
+                    if None not in [slot_of(table, page, num_pages, s, t) for t in (i, int(kept[s][u][i]))]:
+                        w[s, u, i] = weights[s, u, int(kept[s][u][i])]
     return kp, vp, w

@@ -78,6 +78,14 @@ def test_oracle_compact():
     assert one[8, 0, 0] == kp[9, 0, 0] and one[8, 1, 0] == kp[9, 1, 0]
 
 
+def test_oracle_compact_leaves_a_token_without_a_page():
+    kp = np.arange(32.0).reshape(16, 2, 1)
+    table = np.array([[1, 7]], np.int32)            # the second page lies outside the pool
+    k, v, w = orc.compact(kp, kp, table, 8, [[[1, 9]]], [12], [2], np.arange(12.0).reshape(1, 1, 12))
+    assert k[8, 0, 0] == kp[9, 0, 0] and k[9, 0, 0] == v[9, 0, 0] == kp[9, 0, 0]
+    assert list(w[0, 0, :3]) == [1, 1, 2]
+
+
 # ----------------------------------------------------------- C ABI refusals --
 # Aligned fake addresses: every call below is refused before a launch.
 

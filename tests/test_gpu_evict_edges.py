@@ -8,8 +8,8 @@ import pytest
 import torch
 
 from oracle import evict_oracle as orc
-from tests.test_gpu_cache_ops import host, ints
-from tests.test_gpu_evict_ops import B, Weigh  # noqa: F401 (B is the fixture)
+from tests.test_gpu_cache_ops import host, ints, make_cache
+from tests.test_gpu_evict_ops import B, Weigh, chosen, word  # noqa: F401 (B is the fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +80,44 @@ def test_a_row_without_a_softmax_spoils_what_it_sees_alone(B, dt, form, what, at
     err = np.abs(got - ref)[~spoilt]
     assert (err <= bound[~spoilt]).all(), err.max()
     assert B.specfold_get_status(b.ws) == 0
+
+
+# ---------------------------------------------------------------- compact --
+
+@pytest.mark.parametrize("sets", [1, 3])
+@pytest.mark.parametrize("lengths,keep", [([100, 100, 70], 60), ([9000, 300, 8000], 2000)])
+def test_a_token_that_stays_keeps_its_weight(B, sets, lengths, keep):
+    """A move from or to a page outside the pool, or past the table: neither keys and values nor the weight."""
+    rng = np.random.default_rng(keep + sets)
+    cache, table = make_cache(B, rng, "bf16", 64, 3, 8, lengths, "split")
+    kept = np.zeros((3, sets, keep), np.int64)
+    for s, n in enumerate(lengths):
+        for u in range(sets):
+            kept[s, u, :min(n, keep)] = chosen(rng, n, min(n, keep))
+    kept[2, 0, [20, 21]] = 5, -1                    # entries that move nothing
+    bad = table.copy()
+    bad[0, 2], bad[0, 9], bad[1, 1] = -3, 10 ** 6, cache.k_pool.shape[0] // 8
+    cache.block_table.copy_(ints(bad))
+    w = torch.rand(3, sets, max(lengths) + 2, device="cuda")
+    before = [host(cache.k_pool), host(cache.v_pool), host(w)]
+    n = [min(x, keep) for x in lengths]
+    status = word()
+    B.specfold_kv_compact(cache, ints(kept), ints(lengths), ints(n), weights=w, status=status)
+    torch.cuda.synchronize()
+    assert int(status) == B.DEV_BAD_PAGE | B.DEV_BAD_SEQ
+    # the definition, a token at a time
+    want = [x.copy() for x in before]
+    pages = cache.k_pool.shape[0] // 8
+    for s in range(3):
+        for h in range(3):
+            u = h if sets > 1 else 0
+            for i in range(n[s]):
+                t = int(kept[s, u, i])
+                if not i <= t < lengths[s] or not all(0 <= bad[s, x // 8] < pages for x in (i, t)):
+                    continue
+                to, of = (int(bad[s, x // 8]) * 8 + x % 8 for x in (i, t))
+                want[0][to, h], want[1][to, h] = before[0][of, h], before[1][of, h]
+                if h < sets:
+                    want[2][s, u, i] = before[2][s, u, t]
+    for got, ref in zip((cache.k_pool, cache.v_pool, w), want):
+        assert np.array_equal(host(got), ref)
