@@ -19,6 +19,7 @@
 // first launch and 1.7 in the second.  Keeping a part of the keys in L2 from one launch to
 // the next by hints saves 1 to 2 us; the scores of 96 rows would be 1.5 times the keys.
 #include "kv_weigh.cuh"
+#include "weigh_order.h"
 
 namespace sf {
 namespace {
@@ -367,25 +368,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_stats_tc_kernel(const __g
 // next tile gathered ahead were slower (36 rows of 28 / 4 heads 73.8 us where this takes
 // 63.7, 128 rows 256 where this takes 249): products half as wide read more of shared
 // memory for each score.
-struct WItems {  // the order of a unit's products, the same in every role
-  int n, tiles, group;
-  int g0 = 0, tile_at = 0, dir = 1, done = 0;  // group's first block, tile now, its step, tiles of the group so far
-  SF_DEV WItems(int blocks, int tiles_, int ring) : n(blocks), tiles(tiles_), group(tiles_ > 1 ? ring : blocks) {}
-  SF_DEV int blocks() const { return min(group, n - g0); }
-  SF_DEV bool last() const { return done == tiles - 1; }
-  // to the next tile or group; true: another tile's queries are needed
-  SF_DEV bool next() {
-    if (++done < tiles) {
-      tile_at += dir;
-      return true;
-    }
-    done = 0;
-    dir = -dir;
-    g0 += group;
-    return false;
-  }
-};
-
 template <int HD>
 __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __grid_constant__ WTcArgs ta) {
   using C = WTc<HD>;
@@ -525,101 +507,99 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
     named_bar_sync(1, 256);
     if (leader) mbar_arrive(smem_u32(q_full));
     pdl_wait();
-    bool ok = true, all_ok = true;  // both halves meet at every tile, also where a wait of one ran out
-    for (; w.n > 0 && all_ok; w.next(p)) {
+    bool ok = true;
+    for (; w.n > 0; w.next(p)) {
       const int ctx = w.q.ctx, len = ctx + w.q.n;
       float* wt = a.w.ptr + w.s * a.w.seq_stride + w.head * a.w.head_stride;
-      WItems q(w.n, tiles_of(), C::RING);
-      bool fresh = true, blind = false;
-      while (q.g0 < q.n) {
-        if (fresh) {  // the tile's statistics, a thread a row
-          float off = -INFINITY;  // no such row, or one that weighs nothing
-          const bool there = tid < rows_of(q.tile_at);
-          if (there) {
-            const float2 v = weigh_gather(a, weigh_unit(a, w, q.tile_at), weigh_row_ml(a, w.q.row0, w.head, q.tile_at * kWeighTcRows + tid), tid, 0, 1);
-            if (v.x != INFINITY || v.y != 0.f) off = -(v.x + log2f(v.y));
-          }
-          s_off[ql & 1][tid] = off;
-          const bool none = __any_sync(0xffffffffu, there && off == -INFINITY);
-          if (lane == 0) s_blind[ql & 1][warp - 4] = none;
-          all_ok = ok = named_bar_and(1, 256, ok);
-          if (!ok) break;
-          const int4 u = reinterpret_cast<const int4*>(s_blind[ql & 1])[0], v = reinterpret_cast<const int4*>(s_blind[ql & 1])[1];
-          blind = u.x | u.y | u.z | u.w | v.x | v.y | v.z | v.w;
-          ++ql;
+      bool blind = false;
+      auto tile = [&](const WItems& q, bool mine) {  // its statistics, a thread a row
+        float off = -INFINITY;  // no such row, or one that weighs nothing
+        const bool there = tid < rows_of(q.tile_at);
+        if (there) {
+          const float2 v = weigh_gather(a, weigh_unit(a, w, q.tile_at), weigh_row_ml(a, w.q.row0, w.head, q.tile_at * kWeighTcRows + tid), tid, 0, 1);
+          if (v.x != INFINITY || v.y != 0.f) off = -(v.x + log2f(v.y));
         }
+        s_off[ql & 1][tid] = off;
+        const bool none = __any_sync(0xffffffffu, there && off == -INFINITY);
+        if (lane == 0) s_blind[ql & 1][warp - 4] = none;
+        if (!named_bar_and(1, 256, mine)) return false;
+        const int4 u = reinterpret_cast<const int4*>(s_blind[ql & 1])[0], v = reinterpret_cast<const int4*>(s_blind[ql & 1])[1];
+        blind = u.x | u.y | u.z | u.w | v.x | v.y | v.z | v.w;
+        ++ql;
+        return true;
+      };
+      auto block = [&](const WItems& q, int b) {
         const float* so = s_off[(ql - 1) & 1];
         const int cols = (rows_of(q.tile_at) + 31) & ~31, m0 = q.tile_at * kWeighTcRows;
         const bool last = q.last();
-        const int nb = q.blocks();
-        for (int b = (x ^ (it + q.g0)) & 1; b < nb; b += 2, ++cnt) {
-          const long long t0 = static_cast<long long>(w.b0 + q.n - 1 - (q.g0 + b)) * kBlock;
-          const bool tail = t0 + kBlock > ctx;
-          const bool mine = last && t0 + key < len;  // this thread writes a weight
-          const float old = mine && t0 + key < ctx && a.decay != 0.f ? wt[t0 + key] : 0.f;
-          ok = __all_sync(0xffffffffu, mbar_wait(smem_u32(&d_full[x]), cnt & 1, abort_flag, p.status, kWaitLimitNs,
-                                                 kSiteAttnSFull));
-          if (!ok) break;
-          tc_fence_after();
-          if (leader && last) mbar_arrive(smem_u32(&empty[(it + q.g0 + b) % C::RING]));
-          // the first row that sees this key; rows without a source see none
-          const int from = tail ? static_cast<int>(min(max(t0 + key - ctx, 0ll) * p.g - m0, 1ll << 20)) : 0;
-          float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
-          auto add = [&](const uint32_t(&s)[32], int c0, auto hides) {
+        const long long t0 = static_cast<long long>(w.b0 + q.n - 1 - (q.g0 + b)) * kBlock;
+        const bool tail = t0 + kBlock > ctx;
+        const bool mine = last && t0 + key < len;  // this thread writes a weight
+        const float old = mine && t0 + key < ctx && a.decay != 0.f ? wt[t0 + key] : 0.f;
+        if (!__all_sync(0xffffffffu, mbar_wait(smem_u32(&d_full[x]), cnt & 1, abort_flag, p.status, kWaitLimitNs,
+                                               kSiteAttnSFull)))
+          return false;
+        ++cnt;
+        tc_fence_after();
+        if (leader && last) mbar_arrive(smem_u32(&empty[(it + q.g0 + b) % C::RING]));
+        // the first row that sees this key; rows without a source see none
+        const int from = tail ? static_cast<int>(min(max(t0 + key - ctx, 0ll) * p.g - m0, 1ll << 20)) : 0;
+        float2 acc[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+        auto add = [&](const uint32_t(&s)[32], int c0, auto hides) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 4) {
-              const float4 o4 = *reinterpret_cast<const float4*>(so + c0 + e);
-              float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, make_float2(o4.x, o4.y));
-              float2 z = fma2(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), scale2, make_float2(o4.z, o4.w));
-              if constexpr (decltype(hides)::value) {
-                if (c0 + e < from || o4.x == -INFINITY) y.x = -INFINITY;
-                if (c0 + e + 1 < from || o4.y == -INFINITY) y.y = -INFINITY;
-                if (c0 + e + 2 < from || o4.z == -INFINITY) z.x = -INFINITY;
-                if (c0 + e + 3 < from || o4.w == -INFINITY) z.y = -INFINITY;
-              }
-              acc[0] = add2(acc[0], make_float2(ex2(y.x), ex2(y.y)));
-              acc[1] = add2(acc[1], make_float2(ex2(z.x), ex2(z.y)));
+          for (int e = 0; e < 32; e += 4) {
+            const float4 o4 = *reinterpret_cast<const float4*>(so + c0 + e);
+            float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, make_float2(o4.x, o4.y));
+            float2 z = fma2(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), scale2, make_float2(o4.z, o4.w));
+            if constexpr (decltype(hides)::value) {
+              if (c0 + e < from || o4.x == -INFINITY) y.x = -INFINITY;
+              if (c0 + e + 1 < from || o4.y == -INFINITY) y.y = -INFINITY;
+              if (c0 + e + 2 < from || o4.z == -INFINITY) z.x = -INFINITY;
+              if (c0 + e + 3 < from || o4.w == -INFINITY) z.y = -INFINITY;
             }
-          };
-          // 32 columns at a time, the next ones on their way
-          const uint32_t at = tmem + lane_off + x * 256;
-          uint32_t s0[32], s1[32];
-          auto loaded = [&](uint32_t(&s)[32], uint32_t(&then)[32], int c) {
-            tmem_ld_wait(s);
-            if (c + 32 < cols) {
-              tmem_ld32(at + c + 32, then);
-            } else {
-              tc_fence_before();
-              __syncwarp();
-              if (lane == 0) mbar_arrive(smem_u32(&d_free[x]));
-            }
-          };
-          auto columns = [&](auto hides) {
-            tmem_ld32(at, s0);
-#pragma unroll 1
-            for (int c = 0; c < cols; c += 64) {
-              loaded(s0, s1, c);
-              add(s0, c, hides);
-              if (c + 32 < cols) {
-                loaded(s1, s0, c + 32);
-                add(s1, c + 32, hides);
-              }
-            }
-          };
-          if (tail || blind)
-            columns(std::true_type{});
-          else
-            columns(std::false_type{});
-          float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
-          if (q.tiles > 1) {
-            if (q.done > 0) sum += s_sum[b][key];
-            s_sum[b][key] = sum;
+            acc[0] = add2(acc[0], make_float2(ex2(y.x), ex2(y.y)));
+            acc[1] = add2(acc[1], make_float2(ex2(z.x), ex2(z.y)));
           }
-          if (mine) wt[t0 + key] = fmaf(a.decay, old, sum);
+        };
+        // 32 columns at a time, the next ones on their way
+        const uint32_t at = tmem + lane_off + x * 256;
+        uint32_t s0[32], s1[32];
+        auto loaded = [&](uint32_t(&s)[32], uint32_t(&then)[32], int c) {
+          tmem_ld_wait(s);
+          if (c + 32 < cols) {
+            tmem_ld32(at + c + 32, then);
+          } else {
+            tc_fence_before();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(smem_u32(&d_free[x]));
+          }
+        };
+        auto columns = [&](auto hides) {
+          tmem_ld32(at, s0);
+#pragma unroll 1
+          for (int c = 0; c < cols; c += 64) {
+            loaded(s0, s1, c);
+            add(s0, c, hides);
+            if (c + 32 < cols) {
+              loaded(s1, s0, c + 32);
+              add(s1, c + 32, hides);
+            }
+          }
+        };
+        if (tail || blind)
+          columns(std::true_type{});
+        else
+          columns(std::false_type{});
+        float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
+        if (q.tiles > 1) {
+          if (q.done > 0) sum += s_sum[b][key];
+          s_sum[b][key] = sum;
         }
-        fresh = q.next();
-      }
-      it += q.n;
+        if (mine) wt[t0 + key] = fmaf(a.decay, old, sum);
+        return true;
+      };
+      if (!half_pass(WItems(w.n, tiles_of(), C::RING), it, x, ok, tile, block)) break;
+      it += w.n;
     }
   }
   tc_fence_before();
