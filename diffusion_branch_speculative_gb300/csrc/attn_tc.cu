@@ -483,10 +483,8 @@ __global__ void __launch_bounds__(kAttnThreads, 1) attn_kernel(const __grid_cons
     }
     if (lt == 0 && *abort_flag) {
       // let the copies already issued land before the CTA exits
+      ring_land(kv_full, C::KV_STAGES, issued_tma);
       int never = 0;
-      if (issued_tma >= 0)
-        mbar_wait(smem_u32(&kv_full[issued_tma % C::KV_STAGES]), (issued_tma / C::KV_STAGES) & 1, &never, nullptr,
-                  10000000ull);
       if (issued_q >= 0) mbar_wait(smem_u32(q_full), issued_q & 1, &never, nullptr, 10000000ull);
     }
   } else if (warp >= 4) {

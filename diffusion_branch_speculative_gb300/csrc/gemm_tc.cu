@@ -593,13 +593,8 @@ __global__ void __launch_bounds__(kGemmThreads, 1) gemm_kernel(const __grid_cons
           tma_load_2d(smem_u32(sb + (BN / 2) * 128), mhi, fb, kb * kBK, yhi);
         }
       }
-      if (!ok && it > 0) {
-        // let the loads already issued land before the CTA exits
-        int never = 0;
-        const uint32_t last = it - 1;
-        mbar_wait(smem_u32(&full[last % C::STAGES]), (last / C::STAGES) & 1, &never, nullptr,
-                  10000000ull);
-      }
+      // let the loads already issued land before the CTA exits
+      if (!ok) ring_land(full, C::STAGES, static_cast<int>(it) - 1);
     }
     __syncwarp();
   } else if (warp == 1) {

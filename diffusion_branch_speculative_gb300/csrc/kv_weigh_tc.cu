@@ -106,10 +106,7 @@ struct KeyLoader {
   }
   // let the copies already issued land before the CTA exits
   SF_DEV void drain(uint64_t* full, volatile int* abort_flag) {
-    if ((threadIdx.x & 31) == 0 && *abort_flag && it > 0) {
-      int never = 0;
-      mbar_wait(smem_u32(&full[(it - 1) % C::RING]), ((it - 1) / C::RING) & 1, &never, nullptr, 10000000ull);
-    }
+    if ((threadIdx.x & 31) == 0 && *abort_flag) ring_land(full, C::RING, it - 1);
     __syncwarp();
   }
 };

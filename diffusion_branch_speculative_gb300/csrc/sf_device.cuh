@@ -9,6 +9,7 @@
 #include <cuda_runtime.h>
 #include <stdint.h>
 
+#include "ring_uses.h"
 #include "specfold.h"
 
 #define SF_DEV __device__ __forceinline__
@@ -83,6 +84,13 @@ SF_DEV bool mbar_wait(uint32_t bar, uint32_t parity, volatile int* abort, uint32
   }
 }
 
+// Before a CTA that gave up exits: the copies into a ring, whose uses 0 .. last have
+// begun, land.  They need not land in order, so every slot's last one is waited for (10 ms
+// at most: a use that was given up itself completes nothing).
+SF_DEV void ring_land(uint64_t* full, int ring, int last) {
+  int never = 0;
+  each_last_use(last, ring, [&](int slot, uint32_t parity) { mbar_wait(smem_u32(&full[slot]), parity, &never, nullptr, 10000000ull); });
+}
 
 // Programmatic dependent launch: every kernel of the library waits for the
 // grids it depends on before touching their outputs (griddepcontrol.wait is a

@@ -348,11 +348,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) tree_attn_tc_kernel(const __gri
     }
     if (lane == 0 && *abort_flag) {
       // let the copies already issued land before the CTA exits
+      ring_land(full + (is_v ? C::KRING : 0), is_v ? C::VRING : C::KRING, issued);
       int never = 0;
-      if (issued >= 0) {
-        const int ring = is_v ? C::VRING : C::KRING;
-        mbar_wait(smem_u32(&full[(is_v ? C::KRING : 0) + issued % ring]), (issued / ring) & 1, &never, nullptr, 10000000ull);
-      }
       if (fixes > 0) mbar_wait(smem_u32(landed), (fixes - 1) & 1, &never, nullptr, 10000000ull);
     }
     __syncwarp();
