@@ -82,6 +82,15 @@ def test_a_row_without_a_softmax_spoils_what_it_sees_alone(B, dt, form, what, at
     assert B.specfold_get_status(b.ws) == 0
 
 
+@pytest.mark.parametrize("rows,n_q,n_kv,ctx", [(48, 24, 2, 12011), (256, 4, 1, 5003)])
+def test_fp32_many_rows_over_a_long_context(B, rows, n_q, n_kv, ctx):
+    """Many tiles of rows, each cut over many blocks."""
+    b = Weigh(B, np.random.default_rng(rows), "f32", 64, n_q, n_kv, 64, "split", [rows, 1], [ctx, 700])
+    before = host(b.w)
+    b.call(0.5)
+    b.check(before, host(b.w), 0.5)
+
+
 # ---------------------------------------------------------------- compact --
 
 @pytest.mark.parametrize("sets", [1, 3])
