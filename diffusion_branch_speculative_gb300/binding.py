@@ -653,7 +653,7 @@ def specfold_kv_select(weights: torch.Tensor, lengths: torch.Tensor, keep: int, 
     `recent` and the largest of `weights` (float32 [n_seqs, sets, tokens])
     between them, `keep` in all; their number to new_len (int32 [n_seqs])."""
     n_seqs, dev = lengths.shape[0], _device_of(lengths)
-    n_sets = weights.shape[1]
+    n_sets = weights.shape[1] if weights.dim() == 3 else 0
     _check_status(status, dev)
     k, k0, k1, cap = _per_token(kept, n_seqs, n_sets, torch.int32, dev, "kept")
     _call(lib().specfold_kv_select, "specfold_kv_select", dev, stream,
@@ -669,7 +669,7 @@ def specfold_kv_compact(cache: PagedCache, kept: torch.Tensor, lengths: torch.Te
     n], new_len[s] of lengths[s], ascending) to the front of its pages, keys
     and values in place, and with them their `weights` (float32 [n_seqs, n_kv
     or 1, tokens])."""
-    n_seqs, n_sets = lengths.shape[0], kept.shape[1]
+    n_seqs, n_sets = lengths.shape[0], kept.shape[1] if kept.dim() == 3 else 0
     dev = cache.device.index
     _check_batch(cache, n_seqs, status, dev)
     k, k0, k1, cap = _per_token(kept, n_seqs, n_sets, torch.int32, dev, "kept")

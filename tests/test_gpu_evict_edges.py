@@ -130,3 +130,20 @@ def test_a_token_that_stays_keeps_its_weight(B, sets, lengths, keep):
                     want[2][s, u, i] = before[2][s, u, t]
     for got, ref in zip((cache.k_pool, cache.v_pool, w), want):
         assert np.array_equal(host(got), ref)
+
+
+# -------------------------------------------------------- binding refusals --
+
+def test_lists_and_weights_of_other_dimensions_are_refused(B):
+    cache, _ = make_cache(B, np.random.default_rng(0), "f32", 64, 2, 8, [16], "split")
+    n, new, kept, w = ints([16]), ints([4]), ints([[[1, 2, 3, 4]] * 2]), torch.rand(1, 2, 16, device="cuda")
+    for bad in (kept[0, 0], kept[0], kept[None]):
+        with pytest.raises(ValueError, match="kept"):
+            B.specfold_kv_compact(cache, bad, n, new)
+        with pytest.raises(ValueError, match="kept"):
+            B.specfold_kv_select(w, n, 4, bad, new)
+    for bad in (w[0, 0], w[0], w[None]):
+        with pytest.raises(ValueError):
+            B.specfold_kv_select(bad, n, 4, kept, new)
+        with pytest.raises(ValueError, match="weights"):
+            B.specfold_kv_compact(cache, kept, n, new, weights=bad)
