@@ -64,10 +64,13 @@ SF_DEV int find_from_last(int2 h, int lane, int& left) {
 // to each other (reading all bins of eight blocks took 2 to 5 us a pass, reading
 // groups and bins 4).  Then every warp writes what it has of its run of the slice, behind
 // what lies before.  Latency bounds it: the chain of reads, passes and exchanges.  3
-// sequences of up to 131071 tokens and 8 sets, 10 MB, take 17.4 us (21 cold), 64 of 8192
-// 16, 64 of 2080 9.4, one of 2080 8.3 with the call, where the bytes need 1.5, 2.4, 0.9
-// and 0.01.  1024 threads were slower with eight blocks a cluster; 32 registers a thread
-// let an SM have four blocks (64 x 8192: 16.0 us, 17.5 with three).
+// sequences of up to 131071 tokens and 8 sets, 10 MB, take 18.9 us (21 cold), 64 of 8192
+// 16.2, 64 of 2080 9.4, one of 2080 8.4 with the call, where the bytes need 1.5, 2.4, 0.9
+// and 0.01.  Those weights spread over some twenty octaves; where they meet in few bins
+// the counting waits: 64 of 8192 within three octaves 17.6, within one bin of the first
+// pass 18.1, all equal 20.5; 64 of 60000 102, 119, 122, 145.  1024 threads were slower
+// with eight blocks a cluster; 32 registers a thread (a block alone spills 4 bytes) let an
+// SM have four blocks (64 x 8192: 16.0 us, 17.5 with three).
 template <bool CLUSTER>
 __global__ void __launch_bounds__(kSelThreads, 4) kv_select_kernel(const __grid_constant__ SelectArgs p) {
   extern __shared__ __align__(16) uint32_t s_key[];
@@ -427,6 +430,9 @@ int launch_kv_select(const KvSelectCall& c, cudaStream_t st) {
   // than the SMs or a slice's keys leave an SM no second block (64 sequences of 60000 tokens and
   // 8 sets: 109 us with slices of 15000, 123 with 7500, 127 with 30000, 184 with one block a unit,
   // which cannot hold its keys; 32 of 120000: 116 with slices of 15000, 263 with one block).
+  // The rule knows the room of the weights, not the lengths: with room for four times as many
+  // tokens 64 of 8192 take 40 us, not 16.2, 64 of 60000 356, not 102, 3 of 131071 24.5, not 19.2,
+  // one of 2080 11.5, not 8.6.
   const long long units = static_cast<long long>(c.n_seqs) * c.kept.n_sets;
   while (a.blocks < kSelMaxCluster && c.w.tokens / a.blocks > kSelSlice &&
          (units * a.blocks * 2 <= 2LL * num_sms() || c.w.tokens / a.blocks > kSelCap / 2))

@@ -36,8 +36,8 @@ SF_DEV void weigh_write_part(const WeighArgs& p, const TreeWalk& w, bool first, 
 // with a group of seven heads wastes one column in eight.  In two launches the
 // scores go to the workspace, 32 bytes a token and eight rows, where the second
 // finds them in L2 rather than the keys in DRAM: 8 sequences of 20000 tokens (28 / 4
-// heads of 128, 122 MB of keys) take 34 us, 26 of them the first launch, DRAM 59 %
-// busy, its start and uneven shares of the SMs the rest; one of 40000, 18.2.
+// heads of 128, 122 MB of keys) take 33 us, 26 of them the first launch, DRAM 59 %
+// busy, its start and uneven shares of the SMs the rest; one of 40000, 17.6.
 template <int HD, int NT, int WARPS_ = kWarps>
 struct WFew {
   static constexpr int WARPS = WARPS_;
@@ -278,8 +278,9 @@ __global__ void __launch_bounds__(kThreads, kFewCtas) weigh_few_kernel(const __g
 // through memory, and one launch less is waited for and paid for on the host.  128
 // registers a thread and 12 KB of keys on the way a warp let an SM have 16 warps; the
 // unrolled steps are what lets registers hold the scores (in shared memory, beside
-// two stages and three blocks an SM, 80 us where this takes 69.6).  64 sequences of up
-// to 8000 tokens, one row of 28 / 4 heads of 128: 384 MB in 69.6 us, 5510 GB/s, 0.81 of
+// two stages and three blocks an SM, 80 us where this takes 70; of the eight instances
+// three, with two tiles of rows, spill 4 to 12 bytes).  64 sequences of up
+// to 8000 tokens, one row of 28 / 4 heads of 128: 384 MB in 70 us, 5480 GB/s, 0.81 of
 // the copy rate; 32 of 8 heads and eight rows 0.89; head size 64 0.67.  What is left is
 // the blocks' own starts and exchanges.
 constexpr int kUnitCluster = 8;        // blocks at most
@@ -408,10 +409,13 @@ __global__ void __launch_bounds__(32 * WARPS, 16 / WARPS) weigh_unit_kernel(cons
 // add up by halves, so that each ends with some rows' scores.  Two steps at a time, whose
 // keys share a query's read (alone, 16 sequences of 12239 tokens and twelve rows of 2 heads
 // took 57.3 us where this takes 51.3, 8 of 4000 and 48 rows of 8 heads 120 and 105; short
-// pieces wait 0.7 us longer for their first).  The reads of shared memory bound it all the
-// same: 8 sequences of 8000 tokens, one row of 24 / 8 heads of 128, 190 MB, take 48.7 us
-// in all, 0.58 of the copy rate.  7 of 1111 tokens and five rows of 4 / 2 heads of 64 take
-// 12.7 us, 9.3 and 9.9 the two launches alone and cold: latency.  One launch by clusters,
+// pieces wait 0.7 us longer for their first).  8 sequences of 8000 tokens, one row of 24 / 8
+// heads of 128, 190 MB, take 48 us in all, 0.59 of the copy rate: 39 the first launch (cold;
+// DRAM 66 % busy, shared memory's pipe 31 %, multiply-adds 19 %: warps wait for their
+// keys, 12 of them an SM), then the second with the 12 MB of scores that eight rows' room
+// for three comes to, 14 cold.  48 rows go over the keys six times, from L2: 105 us, where
+// their bytes need 14.  7 of 1111 tokens and five rows of 4 / 2 heads of 64 take
+// 12.2 us, 9.3 and 9.9 the two launches alone and cold: latency.  One launch by clusters,
 // scores in shared memory, was slower (70.6 us where two took 47.4, and 15.6 where they
 // took 13.8).
 template <int HD>
@@ -605,7 +609,8 @@ __global__ void __launch_bounds__(kThreads, WSimt<HD>::CTAS) weigh_simt_kernel(c
 // the same lengths.  A piece's first scores are on their way while its rows' statistics
 // are merged.  More rows than kSumRows come in groups, which add to the weights in turn.
 // The scores of 8 sequences of 20000 tokens, 17 MB, take it 14.7 us alone and cold, 8 behind
-// the first launch; four blocks an SM have too few registers (99.9 us where three take 87).
+// the first launch; four blocks an SM have too few registers (99.9 us where three, 80
+// registers without a spill, took 87).
 constexpr int kSumThreads = 256, kSumTokens = 8;
 constexpr int kSumCtas = 3;    // per SM
 constexpr int kSumRows = 512;  // of a group
@@ -717,13 +722,13 @@ size_t up256(size_t x) { return (x + 255) / 256 * 256; }
 // rows, and what does not fit, have them computed twice on the tensor cores.  The three (us;
 // 8 key/value heads, groups of 4, sequences x tokens):
 //                           32 x 8000             1 x 40000       8 x 500
-//   head size 128,  8 rows   63.7   87.4  120.6   -  26.8  35.5    9.6  11.1  14.6
-//                  16 rows   82.2  108.1  120.8   -  31.3  35.7    9.6  12.4  14.7
-//                  24 rows      -  133.5  120.7                      -     -  14.6
-//                  32 rows      -  167.8  120.9   -  50.2  35.4      -  14.8  14.6
-//   head size 64,   8 rows   42.7   58.7   78.1
-//                  16 rows   64.1   77.6   77.5
-//                  32 rows      -  131.7   77.7
+//   head size 128,  8 rows   63.8   86.9  117     -  26.2  35.3    9.4  12.4  14.8
+//                  16 rows   82.4  104.7  118     -  30.4  35.2    9.5  12.2  14.8
+//                  24 rows      -  133.5  120                        -     -  14.6
+//                  32 rows      -  167.8  120     -  50.2  35.4      -  14.8  14.6
+//   head size 64,   8 rows   42.6   57.5   78.5
+//                  16 rows   65.3   74.7   78.2
+//                  32 rows      -  131.7   77.9
 // fp32 keeps them in memory always: it would be bound by computing them twice.
 WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int n_seqs, int tokens) {
   const int rows = max_rows * (n_q / n_kv), r8 = (rows + 7) / 8 * 8;
@@ -735,12 +740,13 @@ WeighPlan plan_of(int dtype, int T, int max_rows, int n_q, int n_kv, int hd, int
   const bool keeps = scores <= (size_t{1} << 30);
   if (dtype == SPECFOLD_BF16) {
     // A cluster for a unit wherever 4 or 8 warps a block hold its scores.  Both sides (one launch,
-    // two; us; sequences x tokens, head size 128), one row of 28 / 4 heads: 64 x 8000 69.6 and
-    // 87.4, 64 x 16000 128 and 171, 8 x 8000 14.9 and 20.4, 1 x 16000 14.0 and 13.5, 1 x 2047 9.1
-    // and 11.2; four of 32 / 8: 32 x 8000 83 and 107, 1 x 8000 10.5 and 15.0.  Where the weights
-    // have room for more tokens than there are: 64 x 8000 of 16384 86 and 87.7, 64 x 2000 of 16384
-    // 29 and 30, four rows of 32 x 4000 of 8192 63 and 57.  With 16 warps a block full lengths gain
-    // (32 x 30000 135 and 157), shorter ones lose (64 x 4000 of 32768 57 and 50).
+    // two; us; sequences x tokens, head size 128), one row of 28 / 4 heads: 64 x 8000 69.3 and
+    // 88, 64 x 16000 127 and 165, 8 x 8000 14.9 and 20.2, 1 x 16000 13.9 and 12.8, 1 x 2047 9.2
+    // and 12; four of 32 / 8: 32 x 8000 82.4 and 105, 1 x 8000 10.6 and 14.4.  The rule knows the
+    // room of the weights, not the lengths; where there is room for more tokens: 64 x 8000 of
+    // 16384 85.3 and 87, of 32768 and more only the two launches, 87; 64 x 2000 of 16384 29.5 and 30.3;
+    // four rows of 32 x 4000 of 8192 63 and 57.  With 16 warps a block full lengths gained
+    // (32 x 30000 135 and 157), shorter ones lost (64 x 4000 of 32768 57 and 50).
     const long long units = static_cast<long long>(n_seqs) * n_kv;
     auto slice = [&](int blocks) { return ((tokens - 1) / blocks / kKeys + 1) * kKeys; };
     int blocks = 1;

@@ -11,12 +11,15 @@
 // exponential a launch.
 //
 // Up to about 100 rows a group the memory bounds it, which has to deliver the keys
-// twice: 32 rows of 24 / 8 heads over 4 x 32700 tokens, 2 x 217 MB, take 73.4 us, 5920
-// GB/s or 0.87 of the copy rate (44 us a launch alone and cold, DRAM 63 % and tensor
-// cores 26 and 18 % busy, 8 us of it the start; the two cannot share an SM).  Beyond, the
-// exponentials and the reads of the tensor memory do: 252 rows (36 of 28 / 4 heads) 64 us
+// twice: 32 rows of 24 / 8 heads over 4 x 32700 tokens, 2 x 217 MB, take 72 to 74 us, 5870 to
+// 6030 GB/s or 0.87 to 0.89 of the copy rate (44 us a launch alone and cold, DRAM 63 % and
+// tensor cores 26 and 18 % busy, 8 us of it the start; the two cannot share an SM).  Beyond,
+// neither memory nor a unit does: 252 rows (36 of 28 / 4 heads) take 64 us
 // for 2 x 107 MB, 896 rows 250 us, where a tile of 256 rows takes 0.95 us a block in the
-// first launch and 1.7 in the second.  Keeping a part of the keys in L2 from one launch to
+// first launch and 1.7 in the second.  Of 896 rows the first launch has the exponentials' unit
+// 48 % busy and the tensor cores 44 %; the second 25 % and 19 %, shared memory 17 %, DRAM 8 %, and
+// its warps wait: a half has one buffer of 128 keys by 256 rows, whose next product starts
+// when the reads of the one before are done.  Keeping a part of the keys in L2 from one launch to
 // the next by hints saves 1 to 2 us; the scores of 96 rows would be 1.5 times the keys.
 #include "kv_weigh.cuh"
 #include "weigh_order.h"

@@ -625,7 +625,9 @@ typedef struct {
  *   t < ctx_len[s]:        w[s, u, t] = decay * w[s, u, t] + sum p[i, h, t]
  *   the batch's own rows:  w[s, u, t] = sum p[i, h, t]
  * A decay of 0 does not read the old weights.  Nothing else of w is written;
- * a sequence without rows keeps its weights as they are.
+ * a sequence without rows keeps its weights as they are.  A row with a score
+ * that is NaN or +infinity, or with none above -infinity, makes the weights of the
+ * tokens that it sees NaN, and no others.
  *   q      view of n_src rows of n_q heads, n_src >= 1
  *   rows   device int32 [T] or NULL: the row of q that row t of the batch takes
  *          (the accepted rows of a step, as committed by specfold_kv_append).
@@ -633,11 +635,13 @@ typedef struct {
  *   max_rows  1 .. SPECFOLD_MAX_TREE, no less than any sequence's rows
  * Rows of one sequence only are a chain: a tree's rows are weighed once they
  * are accepted.  Tokens that a row does not see change nothing, whatever their
- * pages hold.  A `rows` entry outside [0, n_src) weighs nothing
- * (SPECFOLD_DEV_BAD_SEQ); a sequence whose row_start, ctx_len or row count is
- * invalid or that has more than w.tokens tokens keeps its weights (the same
- * bit), as do all where the batch counts more blocks of keys than
- * specfold_tree_attention takes; the weights of sequences that share rows, as
+ * pages hold.  A `rows` entry outside [0, n_src) weighs nothing, whatever q
+ * and the keys hold (SPECFOLD_DEV_BAD_SEQ); a sequence whose row_start, ctx_len
+ * or row count is invalid or that has more than w.tokens tokens keeps its
+ * weights (the same bit), as do all where two launches are taken and the batch
+ * counts more than 10^8 blocks of keys: ceil((ctx_len + rows) / 64) for every
+ * sequence with rows and key/value head, / 128 for bf16 where the scores are
+ * computed twice; the weights of sequences that share rows, as
  * only a row_start that falls in between has them, are unspecified.  A page
  * outside the pool or a token past the table reads as a key of zeros
  * (SPECFOLD_DEV_BAD_PAGE).
@@ -649,7 +653,11 @@ typedef struct {
  * max_rows * g up to 16 and, for fp32, always, it holds the scores: four bytes
  * for every token of n_seqs * n_kv times w.tokens and every row of a group, in
  * eights (bf16: none where one launch holds them in registers, or 1 GB and
- * more).  A batch's rows may also be weighed a part at a time, each part behind
+ * more; fp32: without a bound).  The form goes by these sizes, so fewer sequences
+ * or tokens may ask for more bytes: a workspace for several shapes has the
+ * largest of their sizes.  What the weights have room for counts, not what the
+ * sequences hold: room for more than 16384 tokens (8192 of 9 to 16 rows) takes
+ * the slower two launches.  A batch's rows may also be weighed a part at a time, each part behind
  * the tokens of the parts before (decay 1). */
 int specfold_kv_weigh(int dtype, int T, int max_rows, int n_q, int n_kv, int head_dim, specfold_head_rows q, int n_src,
                       const int32_t* rows, const specfold_paged_cache* cache, const int32_t* row_start,
