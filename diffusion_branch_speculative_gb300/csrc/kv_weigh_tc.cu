@@ -520,11 +520,15 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
           if (v.x != INFINITY || v.y != 0.f) off = -(v.x + log2f(v.y));
         }
         s_off[ql & 1][tid] = off;
-        const bool none = __any_sync(0xffffffffu, there && off == -INFINITY);
-        if (lane == 0) s_blind[ql & 1][warp - 4] = none;
+        if (a.rows) {
+          const bool none = __any_sync(0xffffffffu, there && off == -INFINITY);
+          if (lane == 0) s_blind[ql & 1][warp - 4] = none;
+        }
         if (!named_bar_and(1, 256, mine)) return false;
-        const int4 u = reinterpret_cast<const int4*>(s_blind[ql & 1])[0], v = reinterpret_cast<const int4*>(s_blind[ql & 1])[1];
-        blind = u.x | u.y | u.z | u.w | v.x | v.y | v.z | v.w;
+        if (a.rows) {
+          const int4 u = reinterpret_cast<const int4*>(s_blind[ql & 1])[0], v = reinterpret_cast<const int4*>(s_blind[ql & 1])[1];
+          blind = u.x | u.y | u.z | u.w | v.x | v.y | v.z | v.w;
+        }
         ++ql;
         return true;
       };
@@ -551,11 +555,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
             const float4 o4 = *reinterpret_cast<const float4*>(so + c0 + e);
             float2 y = fma2(make_float2(__uint_as_float(s[e]), __uint_as_float(s[e + 1])), scale2, make_float2(o4.x, o4.y));
             float2 z = fma2(make_float2(__uint_as_float(s[e + 2]), __uint_as_float(s[e + 3])), scale2, make_float2(o4.z, o4.w));
-            if constexpr (decltype(hides)::value) {
-              if (c0 + e < from || o4.x == -INFINITY) y.x = -INFINITY;
-              if (c0 + e + 1 < from || o4.y == -INFINITY) y.y = -INFINITY;
-              if (c0 + e + 2 < from || o4.z == -INFINITY) z.x = -INFINITY;
-              if (c0 + e + 3 < from || o4.w == -INFINITY) z.y = -INFINITY;
+            constexpr int kHides = decltype(hides)::value;  // nothing, tokens behind a row's own, rows without a source too
+            auto hidden = [&](int i, float off) { return c0 + e + i < from || (kHides == 2 && off == -INFINITY); };
+            if constexpr (kHides > 0) {
+              if (hidden(0, o4.x)) y.x = -INFINITY;
+              if (hidden(1, o4.y)) y.y = -INFINITY;
+              if (hidden(2, o4.z)) z.x = -INFINITY;
+              if (hidden(3, o4.w)) z.y = -INFINITY;
             }
             acc[0] = add2(acc[0], make_float2(ex2(y.x), ex2(y.y)));
             acc[1] = add2(acc[1], make_float2(ex2(z.x), ex2(z.y)));
@@ -586,10 +592,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) weigh_tokens_tc_kernel(const __
             }
           }
         };
-        if (tail || blind)
-          columns(std::true_type{});
+        if (blind)
+          columns(std::integral_constant<int, 2>{});
+        else if (tail)
+          columns(std::integral_constant<int, 1>{});
         else
-          columns(std::false_type{});
+          columns(std::integral_constant<int, 0>{});
         float sum = (acc[0].x + acc[0].y) + (acc[1].x + acc[1].y);
         if (q.tiles > 1) {
           if (q.done > 0) sum += s_sum[b][key];
